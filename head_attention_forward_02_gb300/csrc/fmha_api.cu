@@ -15,6 +15,9 @@ int gen_set_test_gate(int on);                   // fmha_gen.cu: its producer te
 int bwd_read_status(int reset);   // fmha_bwd.cu: the backward kernels' status word
 int bwd_set_wait_limit(unsigned long long ns);   // fmha_bwd.cu: its wait limit (0: 4 s)
 int bwd_set_test_gate(int on);                   // fmha_bwd.cu: its producer test gate
+int tree_read_status(int reset);   // fmha_tree.cu: the drafted-tree kernels' status word
+int tree_set_wait_limit(unsigned long long ns);  // fmha_tree.cu: its wait limit (0: 4 s)
+int tree_set_test_gate(int on);                  // fmha_tree.cu: its producer test gate
 }
 
 namespace fmha {
@@ -143,21 +146,24 @@ int fmha_set_wait_limit_ns(unsigned long long ns) {
     const int a = fmha::sm103_set_wait_limit(ns);
     const int b = fmha::gen_set_wait_limit(ns);
     const int c = fmha::bwd_set_wait_limit(ns);
-    return a != FMHA_OK ? a : b != FMHA_OK ? b : c;
+    const int d = fmha::tree_set_wait_limit(ns);
+    return a != FMHA_OK ? a : b != FMHA_OK ? b : c != FMHA_OK ? c : d;
 }
 
 int fmha_set_test_gate(int on) {
     const int a = fmha::sm103_set_test_gate(on);
     const int b = fmha::gen_set_test_gate(on);
     const int c = fmha::bwd_set_test_gate(on);
-    return a != FMHA_OK ? a : b != FMHA_OK ? b : c;
+    const int d = fmha::tree_set_test_gate(on);
+    return a != FMHA_OK ? a : b != FMHA_OK ? b : c != FMHA_OK ? c : d;
 }
 
 int fmha_device_status(int reset) {
     const int a = fmha::sm103_read_status(reset);
     const int b = fmha::gen_read_status(reset);
     const int c = fmha::bwd_read_status(reset);
-    return a != FMHA_OK ? a : (b != FMHA_OK ? b : c);
+    const int d = fmha::tree_read_status(reset);
+    return a != FMHA_OK ? a : b != FMHA_OK ? b : c != FMHA_OK ? c : d;
 }
 
 int fmha_kv_tile_range(int q_row0, int q_rows, int Sq, int Sk, int mask, int causal_type,

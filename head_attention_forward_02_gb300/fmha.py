@@ -76,6 +76,14 @@ def lib():
             ctypes.c_size_t, ctypes.c_void_p]
         L.fmha_gen_workspace_size.restype = ctypes.c_size_t
         L.fmha_gen_workspace_size.argtypes = [ctypes.c_int] * 5
+        L.fmha_tree_fwd.restype = ctypes.c_int
+        L.fmha_tree_fwd.argtypes = [fmha_tensor] * 6 + [ctypes.c_void_p] + [ctypes.c_int] * 7 + [
+            ctypes.c_void_p] * 4 + [ctypes.c_int64, ctypes.c_float, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t,
+                                    ctypes.c_void_p]
+        L.fmha_tree_workspace_size.restype = ctypes.c_size_t
+        L.fmha_tree_workspace_size.argtypes = [ctypes.c_int] * 6
+        L.fmha_tree_commit.restype = ctypes.c_int
+        L.fmha_tree_commit.argtypes = [fmha_tensor] * 4 + [ctypes.c_int] * 7 + [ctypes.c_void_p] * 5
         L.fmha_bwd.restype = ctypes.c_int
         L.fmha_bwd.argtypes = [fmha_tensor] * 5 + [ctypes.c_void_p] + [fmha_tensor] * 3 + [ctypes.c_int] * 5 + [
             ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
@@ -299,6 +307,130 @@ def gen_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, seqle
     if rc != OK:
         raise FmhaError(rc, status_string(rc))
     return out, lse
+
+
+def fmha_tree_fwd(q, k_cache, v_cache, k_new, v_new, o, lse, B, T, H, H_k, D, B_cache, S_max, seqlen, batch_idx,
+                  n_draft, tree_mask, mask_batch_stride, scale, out_scale, workspace, workspace_bytes,
+                  stream=None) -> int:
+    """Same arguments, order and status codes as the C function fmha_tree_fwd."""
+    return lib().fmha_tree_fwd(
+        _tensor(q), _tensor(k_cache), _tensor(v_cache), _tensor(k_new), _tensor(v_new), _tensor(o), _ptr(lse), int(B),
+        int(T), int(H), int(H_k), int(D), int(B_cache), int(S_max), _ptr(seqlen), _ptr(batch_idx), _ptr(n_draft),
+        _ptr(tree_mask), int(mask_batch_stride), float(scale), float(out_scale), _ptr(workspace),
+        int(workspace_bytes), _stream(stream))
+
+
+def fmha_tree_workspace_size(B, T, H, H_k, D, S_max) -> int:
+    return int(lib().fmha_tree_workspace_size(int(B), int(T), int(H), int(H_k), int(D), int(S_max)))
+
+
+def fmha_tree_commit(k_cache, v_cache, k_new, v_new, B, T, P, H_k, D, B_cache, S_max, seqlen, batch_idx, path,
+                     n_accept, stream=None) -> int:
+    """Same arguments, order and status codes as the C function fmha_tree_commit."""
+    return lib().fmha_tree_commit(_tensor(k_cache), _tensor(v_cache), _tensor(k_new), _tensor(v_new), int(B), int(T),
+                                  int(P), int(H_k), int(D), int(B_cache), int(S_max), _ptr(seqlen), _ptr(batch_idx),
+                                  _ptr(path), _ptr(n_accept), _stream(stream))
+
+
+def _check(name: str, t, shape, dtype, device) -> None:
+    """Refuse a tensor that the library would misread: it takes only an address."""
+    if t is None:
+        return
+    if t.device != device or t.device.type != "cuda":
+        raise ValueError(f"{name} is on {t.device}, not on the CUDA device of the call ({device})")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+
+
+def _stream_on(stream, device) -> int:
+    """The stream to launch on: torch's current one of the tensors' device."""
+    return _stream(torch.cuda.current_stream(device) if stream is None else stream)
+
+
+def _raise(rc: int) -> None:
+    if rc != OK:
+        raise FmhaError(rc, status_string(rc))
+
+
+def tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+             seqlen: torch.Tensor, *, tree_mask: Optional[torch.Tensor] = None,
+             n_draft: Optional[torch.Tensor] = None, batch_idx: Optional[torch.Tensor] = None,
+             scale: Optional[float] = None, out_scale: float = 1.0, out: Optional[torch.Tensor] = None,
+             lse: Optional[torch.Tensor] = None, return_lse: bool = True,
+             workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of drafted tokens over a K/V cache (see fmha_tree_fwd).
+
+    q [B, T, H, 128]; k_cache / v_cache [B_cache, S_max, H_k, 128]; k_new /
+    v_new [B, T, H_k, 128]; seqlen, n_draft, batch_idx int32 [B]; tree_mask
+    bool or uint8 [B, T, T], or [T, T] for every sequence, true where draft
+    row sees draft column (None: a chain).  Allocates O, LSE [B, H, T] and the
+    workspace with torch when not given; rows of drafts at or past n_draft[b]
+    are not written.  Returns (O, LSE)."""
+    if q.dim() != 4 or k_cache.dim() != 4:
+        raise ValueError("q is [B, T, H, 128] and the caches are [B_cache, S_max, H_k, 128]")
+    B, T, H, D = q.shape
+    B_cache, S_max, H_k = k_cache.shape[0], k_cache.shape[1], k_cache.shape[2]
+    dev = q.device
+    if q.dtype not in _TORCH_DTYPE:
+        raise FmhaError(ERR_UNSUPPORTED, status_string(ERR_UNSUPPORTED))
+    _check("q", q, q.shape, q.dtype, dev)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check(name, t, (B_cache, S_max, H_k, D), q.dtype, dev)
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        _check(name, t, (B, T, H_k, D), q.dtype, dev)
+    for name, t in (("seqlen", seqlen), ("n_draft", n_draft), ("batch_idx", batch_idx)):
+        _check(name, t, (B,), torch.int32, dev)
+    stride = 0
+    if tree_mask is not None:
+        _check("tree_mask", tree_mask, (T, T) if tree_mask.dim() == 2 else (B, T, T), (torch.bool, torch.uint8), dev)
+        stride = 0 if tree_mask.dim() == 2 else T * T
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None and return_lse:
+            lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
+        _check("out", out, q.shape, q.dtype, dev)
+        _check("lse", lse, (B, H, T), torch.float32, dev)
+        nbytes = fmha_tree_workspace_size(B, T, H, H_k, D, S_max)
+        if workspace is None:
+            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev:
+            raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
+        _raise(fmha_tree_fwd(q, k_cache, v_cache, k_new, v_new, out, lse, B, T, H, H_k, D, B_cache, S_max, seqlen,
+                             batch_idx, n_draft, tree_mask, stride, 1.0 / math.sqrt(D) if scale is None else scale,
+                             out_scale, workspace, workspace.numel() * workspace.element_size(),
+                             _stream_on(stream, dev)))
+    return out, lse
+
+
+def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                seqlen: torch.Tensor, path: torch.Tensor, n_accept: torch.Tensor, *,
+                batch_idx: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Write the accepted drafts into the cache (see fmha_tree_commit): rows
+    path[b, i], i < n_accept[b], of k_new / v_new [B, T, H_k, 128] become rows
+    seqlen[b] + i of sequence b's entry.  path int32 [B, P]; n_accept, seqlen,
+    batch_idx int32 [B].  seqlen is not changed."""
+    if k_cache.dim() != 4 or k_new.dim() != 4 or path.dim() != 2:
+        raise ValueError("the caches are [B_cache, S_max, H_k, 128], k_new is [B, T, H_k, 128] and path is [B, P]")
+    B_cache, S_max, H_k, D = k_cache.shape
+    B, T, P = k_new.shape[0], k_new.shape[1], path.shape[1]
+    dev = k_cache.device
+    if k_cache.dtype not in _TORCH_DTYPE:
+        raise FmhaError(ERR_UNSUPPORTED, status_string(ERR_UNSUPPORTED))
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check(name, t, (B_cache, S_max, H_k, D), k_cache.dtype, dev)
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        _check(name, t, (B, T, H_k, D), k_cache.dtype, dev)
+    _check("path", path, (B, P), torch.int32, dev)
+    for name, t in (("seqlen", seqlen), ("n_accept", n_accept), ("batch_idx", batch_idx)):
+        _check(name, t, (B,), torch.int32, dev)
+    with torch.cuda.device(dev):
+        _raise(fmha_tree_commit(k_cache, v_cache, k_new, v_new, B, T, P, H_k, D, B_cache, S_max, seqlen, batch_idx,
+                                path, n_accept, _stream_on(stream, dev)))
 
 
 def fmha_bwd(q, k, v, o, dout, lse, dq, dk, dv, B, H, Sq, Sk, D, scale, mask, causal_type, workspace,

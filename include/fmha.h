@@ -268,6 +268,90 @@ int fmha_gen_fwd(fmha_tensor q, fmha_tensor k_cache, fmha_tensor v_cache,
 size_t fmha_gen_workspace_size(int B, int H, int H_k, int D, int S_max);
 
 /*
+ * fmha_tree_fwd -- attention of drafted tokens over a key/value cache: T
+ * tokens a sequence that a cheap model proposed, as a tree (or a chain), are
+ * checked in one call.  It is fmha_gen_fwd with T query tokens, which see one
+ * another as their tree says.  The pages have no counterpart.
+ *
+ * For sequence b, with cache entry e = batch_idx ? batch_idx[b] : b,
+ * L = seqlen[b] cached tokens and n = n_draft ? n_draft[b] : T drafts, draft
+ * t < n and query head h of kv head g = h / (H / H_k) see the keys
+ *   K_cache[e, 0..L-1, g, :], and K_new[b, j, g, :] for those j < n with
+ *   tree_mask[b, t, j] != 0 (tree_mask NULL: j <= t, a chain)
+ * and the values alike, and
+ *   O[b, t, h, :] = out_scale * softmax(scale * q[b, t, h, :] . keys) values
+ *   lse[b, h, t]  = natural-log log-sum-exp of the scaled scores
+ * (no key at all: O = 0, lse = -inf).  The rows of drafts t >= n are left as
+ * they were.  The call writes neither the cache nor seqlen: fmha_tree_commit
+ * does that for the drafts that are accepted.
+ *
+ * Layouts (contiguous, device memory):
+ *   q, o               [B, T, H, 128]
+ *   k_cache, v_cache   [B_cache, S_max, H_k, 128]
+ *   k_new, v_new       [B, T, H_k, 128]
+ *   seqlen, batch_idx, n_draft   int32 [B] (the last two may be NULL)
+ *   tree_mask          uint8 [T, T] of sequence b at tree_mask + b *
+ *                      mask_batch_stride (0: one mask for all; else >= T * T),
+ *                      or NULL.  Any mask: it need not be a tree's, and a
+ *                      draft need not see itself.
+ *   lse                float [B, H, T], or NULL
+ * All tensors share one dtype, FMHA_F16, FMHA_BF16 or FMHA_E4M3; D must be
+ * 128 and H / H_k at most 128.  Device pointers must be 16-byte aligned
+ * (int32 and lse 4-byte).  P is rounded to the tensors' dtype before P.V (its
+ * row sum is not), and O with saturation for e4m3.
+ * Requirements the host cannot check: 0 <= seqlen[b] <= S_max, 0 <=
+ * batch_idx[b] < B_cache, 0 <= n_draft[b] <= T; a kernel that meets a
+ * violation clamps the length or the count, or reads zeros for the missing
+ * entry, and fmha_device_status then reports FMHA_ERR_INVALID_ARG.  Entries
+ * may be shared.  Rows at or past a sequence's lengths are never used, and may
+ * hold any bits, including NaN; a masked draft below n must be finite.
+ *
+ * workspace: caller-owned scratch of at least fmha_tree_workspace_size(...)
+ * bytes, 256-byte aligned; nothing in it needs initialising; it must not be
+ * shared with a call that may run concurrently.  The call allocates nothing
+ * and is asynchronous on `stream` (a kernel, then a merge kernel).
+ * Returns FMHA_OK, FMHA_ERR_INVALID_ARG (bad sizes or pointers, scale not
+ * finite and > 0, mask stride, workspace too small or misaligned),
+ * FMHA_ERR_UNSUPPORTED (dtype, alignment, device) or FMHA_ERR_CUDA.  B = 0 or
+ * T = 0 succeeds without a launch.
+ */
+int fmha_tree_fwd(fmha_tensor q, fmha_tensor k_cache, fmha_tensor v_cache,
+                  fmha_tensor k_new, fmha_tensor v_new, fmha_tensor o, float *lse,
+                  int B, int T, int H, int H_k, int D, int B_cache, int S_max,
+                  const int *seqlen, const int *batch_idx, const int *n_draft,
+                  const uint8_t *tree_mask, int64_t mask_batch_stride, float scale, float out_scale,
+                  void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Workspace bytes fmha_tree_fwd needs for these sizes: two sets of fp32
+ * partial rows per thread block of the attention kernel, at most 40 MB
+ * whatever the sizes.  0 for invalid sizes.
+ */
+size_t fmha_tree_workspace_size(int B, int T, int H, int H_k, int D, int S_max);
+
+/*
+ * fmha_tree_commit -- write the accepted drafts of fmha_tree_fwd into the
+ * cache: for i < n_accept[b],
+ *   K_cache[e, L + i, :, :] = K_new[b, path[b, i], :, :], V alike,
+ * with e and L = seqlen[b] as there.  seqlen is not changed (the caller adds
+ * n_accept to it).  Layouts as fmha_tree_fwd; path int32 [B, P], n_accept
+ * int32 [B].  A draft may appear more than once.  Entries of path at or past
+ * n_accept are not read.  Two sequences must not share an entry.
+ * In device memory, so checked there: 0 <= seqlen[b], 0 <= n_accept[b] <= P,
+ * seqlen[b] + n_accept[b] <= S_max, batch_idx[b] in [0, B_cache) and path in
+ * [0, T); a kernel that meets a violation clamps the count, or writes nothing
+ * for that entry or draft, and fmha_device_status then reports
+ * FMHA_ERR_INVALID_ARG.
+ * Returns FMHA_OK, FMHA_ERR_INVALID_ARG, FMHA_ERR_UNSUPPORTED (dtype,
+ * alignment, B > 65535, device) or FMHA_ERR_CUDA.  B = 0 or P = 0 succeeds
+ * without a launch.
+ */
+int fmha_tree_commit(fmha_tensor k_cache, fmha_tensor v_cache, fmha_tensor k_new, fmha_tensor v_new,
+                     int B, int T, int P, int H_k, int D, int B_cache, int S_max,
+                     const int *seqlen, const int *batch_idx, const int *path, const int *n_accept,
+                     cudaStream_t stream);
+
+/*
  * fmha_bwd -- backward pass of fmha_fwd: dQ, dK, dV from dO ("CUTLASS
  * Blackwell FMHA 示例完全解析", §FMHA for Blackwell 反向 (Backward): row sums
  * of O * dO, a dK/dV kernel and a dQ kernel, Q and K blocking 128, causal
