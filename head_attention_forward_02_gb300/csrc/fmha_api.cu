@@ -18,6 +18,10 @@ int bwd_set_test_gate(int on);                   // fmha_bwd.cu: its producer te
 int tree_read_status(int reset);   // fmha_tree.cu: the drafted-tree kernels' status word
 int tree_set_wait_limit(unsigned long long ns);  // fmha_tree.cu: its wait limit (0: 4 s)
 int tree_set_test_gate(int on);                  // fmha_tree.cu: its producer test gate
+int weights_read_status(int reset);              // fmha_weights.cu: likewise
+int weights_set_wait_limit(unsigned long long ns);
+int weights_set_test_gate(int on);
+int evict_read_status(int reset);                // fmha_evict.cu: its status word (it has no waits)
 }
 
 namespace fmha {
@@ -147,7 +151,8 @@ int fmha_set_wait_limit_ns(unsigned long long ns) {
     const int b = fmha::gen_set_wait_limit(ns);
     const int c = fmha::bwd_set_wait_limit(ns);
     const int d = fmha::tree_set_wait_limit(ns);
-    return a != FMHA_OK ? a : b != FMHA_OK ? b : c != FMHA_OK ? c : d;
+    const int e = fmha::weights_set_wait_limit(ns);
+    return a != FMHA_OK ? a : b != FMHA_OK ? b : c != FMHA_OK ? c : d != FMHA_OK ? d : e;
 }
 
 int fmha_set_test_gate(int on) {
@@ -155,7 +160,8 @@ int fmha_set_test_gate(int on) {
     const int b = fmha::gen_set_test_gate(on);
     const int c = fmha::bwd_set_test_gate(on);
     const int d = fmha::tree_set_test_gate(on);
-    return a != FMHA_OK ? a : b != FMHA_OK ? b : c != FMHA_OK ? c : d;
+    const int e = fmha::weights_set_test_gate(on);
+    return a != FMHA_OK ? a : b != FMHA_OK ? b : c != FMHA_OK ? c : d != FMHA_OK ? d : e;
 }
 
 int fmha_device_status(int reset) {
@@ -163,7 +169,11 @@ int fmha_device_status(int reset) {
     const int b = fmha::gen_read_status(reset);
     const int c = fmha::bwd_read_status(reset);
     const int d = fmha::tree_read_status(reset);
-    return a != FMHA_OK ? a : b != FMHA_OK ? b : c != FMHA_OK ? c : d;
+    const int e = fmha::weights_read_status(reset);
+    const int f = fmha::evict_read_status(reset);
+    for (int s : {a, b, c, d, e})
+        if (s != FMHA_OK) return s;
+    return f;
 }
 
 int fmha_kv_tile_range(int q_row0, int q_rows, int Sq, int Sk, int mask, int causal_type,

@@ -84,6 +84,14 @@ def lib():
         L.fmha_tree_workspace_size.argtypes = [ctypes.c_int] * 6
         L.fmha_tree_commit.restype = ctypes.c_int
         L.fmha_tree_commit.argtypes = [fmha_tensor] * 4 + [ctypes.c_int] * 7 + [ctypes.c_void_p] * 5
+        L.fmha_cache_weights.restype = ctypes.c_int
+        L.fmha_cache_weights.argtypes = [fmha_tensor] * 2 + [ctypes.c_void_p] * 3 + [ctypes.c_int] * 7 + [
+            ctypes.c_void_p] * 3 + [ctypes.c_float, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
+        L.fmha_cache_weights_workspace_size.restype = ctypes.c_size_t
+        L.fmha_cache_weights_workspace_size.argtypes = []
+        L.fmha_cache_evict.restype = ctypes.c_int
+        L.fmha_cache_evict.argtypes = [fmha_tensor] * 2 + [ctypes.c_void_p] + [fmha_tensor] * 2 + [
+            ctypes.c_void_p] + [ctypes.c_int] * 7 + [ctypes.c_void_p] * 3 + [ctypes.c_int] * 2 + [ctypes.c_void_p] * 3
         L.fmha_bwd.restype = ctypes.c_int
         L.fmha_bwd.argtypes = [fmha_tensor] * 5 + [ctypes.c_void_p] + [fmha_tensor] * 3 + [ctypes.c_int] * 5 + [
             ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
@@ -431,6 +439,118 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, k_new: torch.Tenso
     with torch.cuda.device(dev):
         _raise(fmha_tree_commit(k_cache, v_cache, k_new, v_new, B, T, P, H_k, D, B_cache, S_max, seqlen, batch_idx,
                                 path, n_accept, _stream_on(stream, dev)))
+
+
+def fmha_cache_weights(q, k_cache, lse, acc_in, acc_out, B, Sq, H, H_k, D, B_cache, S_max, seqlen, batch_idx, n_query,
+                       scale, mask, workspace, workspace_bytes, stream=None) -> int:
+    """Same arguments, order and status codes as the C function fmha_cache_weights."""
+    return lib().fmha_cache_weights(
+        _tensor(q), _tensor(k_cache), _ptr(lse), _ptr(acc_in), _ptr(acc_out), int(B), int(Sq), int(H), int(H_k), int(D),
+        int(B_cache), int(S_max), _ptr(seqlen), _ptr(batch_idx), _ptr(n_query), float(scale), int(mask),
+        _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+def fmha_cache_weights_workspace_size() -> int:
+    return int(lib().fmha_cache_weights_workspace_size())
+
+
+def fmha_cache_evict(k_cache, v_cache, acc, k_out, v_out, acc_out, B, H_k, D, B_cache, S_max, B_out, S_out, seqlen,
+                     batch_idx, out_idx, budget, recent, kept, new_seqlen, stream=None) -> int:
+    """Same arguments, order and status codes as the C function fmha_cache_evict."""
+    return lib().fmha_cache_evict(
+        _tensor(k_cache), _tensor(v_cache), _ptr(acc), _tensor(k_out), _tensor(v_out), _ptr(acc_out), int(B), int(H_k),
+        int(D), int(B_cache), int(S_max), int(B_out), int(S_out), _ptr(seqlen), _ptr(batch_idx), _ptr(out_idx),
+        int(budget), int(recent), _ptr(kept), _ptr(new_seqlen), _stream(stream))
+
+
+def cache_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor, seqlen: torch.Tensor, *,
+                  acc: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                  n_query: Optional[torch.Tensor] = None, batch_idx: Optional[torch.Tensor] = None,
+                  mask: str = "none", scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """Add the attention weight of every cached key to a running score (see
+    fmha_cache_weights).
+
+    q [B, Sq, H, 128], or [B, H, 128] of a generation step; k_cache [B_cache,
+    S_max, H_k, 128]; lse [B, H, Sq], or [B, H], as the attention call returned
+    it; acc float [B_cache, H_k, S_max], None: start from nothing; mask "none"
+    or "causal" (q-end).  Updates acc in place unless ``out`` is given; with
+    neither, returns a new array that is zero past every length."""
+    if q.dim() == 3:
+        q, lse = q.unsqueeze(1), lse.unsqueeze(-1)
+    if q.dim() != 4 or k_cache.dim() != 4:
+        raise ValueError("q is [B, Sq, H, 128] or [B, H, 128] and the cache is [B_cache, S_max, H_k, 128]")
+    if mask not in ("none", "causal"):
+        raise ValueError(f"mask is none or causal, not {mask!r}")
+    B, Sq, H, D = q.shape
+    B_cache, S_max, H_k = k_cache.shape[0], k_cache.shape[1], k_cache.shape[2]
+    dev = q.device
+    if q.dtype not in _TORCH_DTYPE:
+        raise FmhaError(ERR_UNSUPPORTED, status_string(ERR_UNSUPPORTED))
+    _check("q", q, q.shape, q.dtype, dev)
+    _check("k_cache", k_cache, (B_cache, S_max, H_k, D), q.dtype, dev)
+    _check("lse", lse, (B, H, Sq), torch.float32, dev)
+    for name, t in (("seqlen", seqlen), ("n_query", n_query), ("batch_idx", batch_idx)):
+        _check(name, t, (B,), torch.int32, dev)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.zeros((B_cache, H_k, S_max), dtype=torch.float32, device=dev) if acc is None else acc
+        for name, t in (("acc", acc), ("out", out)):
+            _check(name, t, (B_cache, H_k, S_max), torch.float32, dev)
+        nbytes = fmha_cache_weights_workspace_size()
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        elif workspace.device != dev:
+            raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
+        _raise(fmha_cache_weights(q, k_cache, lse, acc, out, B, Sq, H, H_k, D, B_cache, S_max, seqlen, batch_idx,
+                                  n_query, 1.0 / math.sqrt(D) if scale is None else scale, _MASKS[mask], workspace,
+                                  workspace.numel() * workspace.element_size(), _stream_on(stream, dev)))
+    return out
+
+
+def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor, seqlen: torch.Tensor, budget: int, *,
+                recent: int = 0, batch_idx: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                v_out: Optional[torch.Tensor] = None, acc_out: Optional[torch.Tensor] = None,
+                out_idx: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None,
+                new_seqlen: Optional[torch.Tensor] = None, stream=None):
+    """Shrink sequences to ``budget`` cached rows by score (see fmha_cache_evict).
+
+    k_cache / v_cache [B_cache, S_max, H_k, 128], acc float [B_cache, H_k,
+    S_max], seqlen int32 [B].  In place unless k_out / v_out [B_out, S_out,
+    H_k, 128] and acc_out [B_out, H_k, S_out] are given (out_idx: their
+    entries).  Returns (kept int32 [B, H_k, budget], new_seqlen int32 [B])."""
+    if k_cache.dim() != 4:
+        raise ValueError("the caches are [B_cache, S_max, H_k, 128]")
+    outs = (k_out, v_out, acc_out)
+    if any(t is None for t in outs) and any(t is not None for t in outs + (out_idx,)):
+        raise ValueError("k_out, v_out and acc_out come together, and out_idx only with them")
+    if k_out is None:
+        k_out, v_out, acc_out, out_idx = k_cache, v_cache, acc, batch_idx
+    B_cache, S_max, H_k, D = k_cache.shape
+    if k_out.dim() != 4:
+        raise ValueError("the output caches are [B_out, S_out, H_k, 128]")
+    B, B_out, S_out = seqlen.shape[0], k_out.shape[0], k_out.shape[1]
+    dev = k_cache.device
+    if k_cache.dtype not in _TORCH_DTYPE:
+        raise FmhaError(ERR_UNSUPPORTED, status_string(ERR_UNSUPPORTED))
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        _check(name, t, (B_cache, S_max, H_k, D), k_cache.dtype, dev)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _check(name, t, (B_out, S_out, H_k, D), k_cache.dtype, dev)
+    _check("acc", acc, (B_cache, H_k, S_max), torch.float32, dev)
+    _check("acc_out", acc_out, (B_out, H_k, S_out), torch.float32, dev)
+    for name, t in (("seqlen", seqlen), ("batch_idx", batch_idx), ("out_idx", out_idx), ("new_seqlen", new_seqlen)):
+        _check(name, t, (B,), torch.int32, dev)
+    _check("kept", kept, (B, H_k, budget), torch.int32, dev)
+    with torch.cuda.device(dev):
+        if kept is None:
+            kept = torch.empty((B, H_k, max(budget, 0)), dtype=torch.int32, device=dev)
+        if new_seqlen is None:
+            new_seqlen = torch.empty((B,), dtype=torch.int32, device=dev)
+        _raise(fmha_cache_evict(k_cache, v_cache, acc, k_out, v_out, acc_out, B, H_k, D, B_cache, S_max, B_out, S_out,
+                                seqlen, batch_idx, out_idx, budget, recent, kept, new_seqlen,
+                                _stream_on(stream, dev)))
+    return kept, new_seqlen
 
 
 def fmha_bwd(q, k, v, o, dout, lse, dq, dk, dv, B, H, Sq, Sk, D, scale, mask, causal_type, workspace,

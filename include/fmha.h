@@ -352,6 +352,81 @@ int fmha_tree_commit(fmha_tensor k_cache, fmha_tensor v_cache, fmha_tensor k_new
                      cudaStream_t stream);
 
 /*
+ * fmha_cache_weights -- the attention weight that every cached key received
+ * from a call's queries, added to a running score per key: what a cache that
+ * is to be shrunk is judged by.  It follows fmha_gen_fwd, fmha_tree_fwd or
+ * fmha_fwd and takes the LSE that they return.  The pages have no counterpart.
+ *
+ * For sequence b with cache entry e, L = seqlen[b] cached keys, n = n_query ?
+ * n_query[b] : Sq query tokens and kv head g, for j < L
+ *   acc_out[e, g, j] = (acc_in ? acc_in[e, g, j] : 0) + sum over t, h of
+ *     exp(scale * q[b, t, h, :] . K_cache[e, j, g, :] - lse[b, h, t])
+ * over the query heads h of group g and the tokens t < n that see key j: all
+ * (mask FMHA_MASK_NONE), or those with j <= t + L - n (FMHA_MASK_CAUSAL,
+ * q-end aligned: the last token sees every key).  A row with lse = -inf (it
+ * saw no key) adds nothing.  acc at or past L is left as it was.
+ *
+ * Layouts (contiguous): q [B, Sq, H, 128]; k_cache [B_cache, S_max, H_k, 128]
+ * of q's dtype (FMHA_F16, FMHA_BF16, FMHA_E4M3); lse float [B, H, Sq];
+ * acc_in, acc_out float [B_cache, H_k, S_max], the same array or apart; seqlen,
+ * batch_idx, n_query int32 [B] (the last two may be NULL).  H / H_k at most
+ * 128.  q and k_cache 16-byte, the others 4-byte aligned.  Sums are fp32 in an
+ * order that does not depend on timing.
+ * seqlen and batch_idx are treated as in fmha_tree_fwd, n_query as n_draft
+ * there; nothing is written for a missing entry.  Two sequences must not share
+ * an entry.  Cached rows at or past L are never used.
+ * workspace: fmha_cache_weights_workspace_size() bytes (whatever the sizes,
+ * 0.3 MB), 256-byte aligned, no initialisation, not shared with a concurrent
+ * call.  Asynchronous on `stream` (one kernel, a second one where a sequence's
+ * rows fill more than one chunk of 128).  Returns FMHA_OK,
+ * FMHA_ERR_INVALID_ARG, FMHA_ERR_UNSUPPORTED (dtype, alignment, device) or
+ * FMHA_ERR_CUDA.  B = 0 or Sq = 0 succeeds without a launch and writes nothing.
+ */
+int fmha_cache_weights(fmha_tensor q, fmha_tensor k_cache, const float *lse, const float *acc_in, float *acc_out,
+                       int B, int Sq, int H, int H_k, int D, int B_cache, int S_max,
+                       const int *seqlen, const int *batch_idx, const int *n_query, float scale, int mask,
+                       void *workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t fmha_cache_weights_workspace_size(void);
+
+/*
+ * fmha_cache_evict -- shrink sequences to a budget of cached rows by a score
+ * per key (fmha_cache_weights', or any other).
+ *
+ * For sequence b with entry e and L = seqlen[b] rows, per kv head g: with
+ * L <= budget every row stays.  Else the newest `recent` rows stay, and the
+ * budget - recent of the others with the largest acc[e, g, :] (equal scores:
+ * the lower row; NaN: below every number).  In ascending order they become
+ * rows 0, 1, ... of K, V and acc of entry d = out_idx ? out_idx[b] : b of the
+ * output.  new_seqlen[b] = min(L, budget), kept[b, g, i] = the row that row i
+ * was (-1 for i >= new_seqlen[b]), and acc_out[d, g, new_seqlen[b] ...] = 0,
+ * so that a row inserted later starts from no weight.  K and V rows behind
+ * new_seqlen[b] are left as they were.  Kv heads keep rows of their own, so
+ * a row's position is kept[b, g, i], not i.
+ *
+ * Layouts (contiguous): k_cache, v_cache [B_cache, S_max, H_k, 128], acc float
+ * [B_cache, H_k, S_max]; k_out, v_out [B_out, S_out, H_k, 128], acc_out float
+ * [B_out, H_k, S_out]; kept int32 [B, H_k, budget]; seqlen, new_seqlen,
+ * batch_idx, out_idx int32 [B] (the last two may be NULL: entry b).  The
+ * output is the input itself (k_out.data == k_cache.data, and then v_out,
+ * acc_out, B_out, S_out and out_idx are the input's too), or apart from it in
+ * memory.  1 <= budget <= S_out, 0 <= recent <= budget.  new_seqlen is another
+ * array than seqlen.  K, V 16-byte, the others 4-byte aligned; dtype FMHA_F16,
+ * FMHA_BF16 or FMHA_E4M3.
+ * seqlen, batch_idx and out_idx are treated as in fmha_tree_fwd; nothing is
+ * moved from or to a missing entry.  Two sequences must not share an entry of
+ * the output, nor, in place, of the input.
+ * No workspace; asynchronous on `stream` (a selection kernel, then a move
+ * kernel).  Returns FMHA_OK, FMHA_ERR_INVALID_ARG, FMHA_ERR_UNSUPPORTED
+ * (dtype, alignment, B > 65535, device) or FMHA_ERR_CUDA.  B = 0 succeeds
+ * without a launch.
+ */
+int fmha_cache_evict(fmha_tensor k_cache, fmha_tensor v_cache, const float *acc,
+                     fmha_tensor k_out, fmha_tensor v_out, float *acc_out,
+                     int B, int H_k, int D, int B_cache, int S_max, int B_out, int S_out,
+                     const int *seqlen, const int *batch_idx, const int *out_idx,
+                     int budget, int recent, int *kept, int *new_seqlen, cudaStream_t stream);
+
+/*
  * fmha_bwd -- backward pass of fmha_fwd: dQ, dK, dV from dO ("CUTLASS
  * Blackwell FMHA 示例完全解析", §FMHA for Blackwell 反向 (Backward): row sums
  * of O * dO, a dK/dV kernel and a dQ kernel, Q and K blocking 128, causal

@@ -37,6 +37,11 @@ def fill_nan(t, index):
     t.view(torch.uint8).view(*t.shape, t.element_size())[index] = 0xFF
 
 
+def take(t, rows):
+    """t[rows] of rows of any type (torch does not index e4m3 on the CPU)."""
+    return t.contiguous().view(torch.uint8)[rows].view(t.dtype)
+
+
 def random_tree(gen, B, T):
     """Ancestor masks of random trees over T drafts (draft i's parent is before it, or the cache)."""
     m = torch.zeros((B, T, T), dtype=torch.bool)
