@@ -109,6 +109,27 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, r);
 }
 
+// The same with its polling loop inlined, for places where many values are
+// live (around a call the compiler would save them all).
+__device__ __forceinline__ bool warp_wait_inline(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    bool r = mbar_try_wait(bar, parity);
+    if (!r) {
+        const unsigned long long t0 = globaltimer();
+        for (uint32_t it = 1;; ++it) {
+            if ((r = mbar_try_wait(bar, parity))) break;
+            if ((it & 63) == 0) {
+                if (*abort_flag) break;
+                if (globaltimer() - t0 > g_wait_ns) {
+                    *abort_flag = 1;
+                    atomicExch(&g_status, FMHA_ERR_TIMEOUT);
+                    break;
+                }
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, r);
+}
+
 // Bounded wait that ignores the abort flag (only while draining).
 __device__ __noinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity) {
     const unsigned long long t0 = globaltimer();
@@ -252,6 +273,23 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
                  : "memory");
 }
 
+// 16 columns
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -279,6 +317,31 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Pairs of fp32 values in one 64-bit register, and the instructions that work on both.
+__device__ __forceinline__ uint64_t pack_f2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -347,7 +410,7 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // A tensor map of `rank` dimensions (innermost first) over packed rows of 128
 // elements, 128-byte swizzle, zero fill outside; false if it cannot be made.
 inline bool make_map(CUtensorMap *m, int dtype, const void *data, int rank, const cuuint64_t *dims,
-                     const cuuint32_t *box) {
+                     const cuuint32_t *box, CUtensorMapL2promotion promo = CU_TENSOR_MAP_L2_PROMOTION_L2_256B) {
     auto fn = encode_fn();
     if (!fn) return false;
     const CUtensorMapDataType t = dtype == FMHA_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -358,8 +421,16 @@ inline bool make_map(CUtensorMap *m, int dtype, const void *data, int rank, cons
     for (int i = 0; i + 1 < rank; ++i) strides[i] = s *= dims[i];
     const cuuint32_t es[5] = {1, 1, 1, 1, 1};
     return fn(m, t, rank, const_cast<void *>(data), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_SWIZZLE_128B, promo,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// L2 fetch size for tiles of one head's rows of a cache: its row.  A fetch of
+// 256 bytes brings half of it for the next head when rows are 128 bytes
+// (e4m3), which is gone before it is used: 95 us against 81 for
+// fmha_tree_fwd at B=16 T=5 H=64 H_k=8 S=16384.
+inline CUtensorMapL2promotion row_promotion(int dtype) {
+    return dtype == FMHA_E4M3 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
 }
 
 inline int sm_count() {

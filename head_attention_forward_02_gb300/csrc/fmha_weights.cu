@@ -568,7 +568,7 @@ extern "C" int fmha_cache_weights(fmha_tensor q, fmha_tensor k_cache, const floa
     const cuuint32_t bq[3] = {box_d, (cuuint32_t)p.G, (cuuint32_t)p.TB};
     const cuuint64_t dk[4] = {kD, (cuuint64_t)H_k, (cuuint64_t)S_max, (cuuint64_t)B_cache};
     const cuuint32_t bk[4] = {box_d, 1, kRows, 1};
-    if (!make_map(&tq, dt, q.data, 3, dq, bq) || !make_map(&tk, dt, k_cache.data, 4, dk, bk)) return FMHA_ERR_CUDA;
+    if (!make_map(&tq, dt, q.data, 3, dq, bq) || !make_map(&tk, dt, k_cache.data, 4, dk, bk, row_promotion(dt))) return FMHA_ERR_CUDA;
 
     auto kern = dt == FMHA_BF16 ? fmha_weights_kernel<FMHA_BF16>
                 : dt == FMHA_F16 ? fmha_weights_kernel<FMHA_F16> : fmha_weights_kernel<FMHA_E4M3>;
