@@ -9,12 +9,16 @@
 // order, -1 past the end, and row i of the output entry is row kept[b, g, i]
 // of the input entry for K, V and acc; acc past the new length is zeroed.
 //
-// Selection (one CTA a kv head): the scores are mapped to 32-bit keys of the
-// same order and the threshold, the need-th largest key, is found digit by
-// digit (11, 11 and 10 bits) from histograms in shared memory; a last pass
-// over the scores writes the rows above it, and the first few equal to it, in
-// order by a block-wide prefix sum.  Whole numbers only, so the result does not
-// depend on the order of the atomics.
+// Selection (a cluster of 1, 2, 4 or 8 CTAs a kv head): the scores are mapped
+// to 32-bit keys of the same order and the threshold, the need-th largest key,
+// is found digit by digit (11, 11 and 10 bits) from histograms in shared
+// memory that the CTAs of a cluster add up through distributed shared memory.
+// Then every warp counts the keys above the threshold and equal to it in its
+// own run of consecutive rows, and, with the counts of the runs before, writes
+// its kept rows in order, the first few equal ones among them.  Whole numbers
+// only, so the result does not depend on the order of the atomics.  One CTA of
+// 512 threads a head took 125 us for 65536 rows where the bytes take 0.6; the
+// cluster takes TODO-FIGURES.
 //
 // The move is bound by memory: 4 * 128 * E bytes a kept row and head.  In
 // place, the rows of a head move down one after another: row i comes from a
@@ -26,7 +30,7 @@ namespace fmha {
 
 namespace {
 
-constexpr int kSelThreads = 512;
+constexpr int kSelKeys = 16;             // keys a thread holds
 constexpr int kBins = 2048;
 constexpr int kMoveThreads = 256;
 
@@ -54,14 +58,30 @@ __device__ __forceinline__ int evict_len(const EvictParams &p, int b, bool repor
     return clamped(p.seqlen[b], 0, p.S_max, report);
 }
 
-__global__ void __launch_bounds__(kSelThreads) fmha_evict_select_kernel(const EvictParams p) {
-    __shared__ uint32_t hist[kBins];
-    __shared__ uint32_t warp_sum[kSelThreads / 32][2];
-    __shared__ uint32_t s_digit, s_above;
+// A word of shared memory in CTA `rank` of the cluster, at the address that
+// `p` has in this one.
+__device__ __forceinline__ uint32_t cluster_word(const uint32_t *p, uint32_t rank) {
+    uint32_t a, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// grid (CS * H_k, B), clusters of CS CTAs of TH threads along x
+template <int CS, int TH>
+__global__ void __launch_bounds__(TH) fmha_evict_select_kernel(const EvictParams p) {
+    constexpr int kSelWarps = TH / 32;
+    __shared__ uint32_t hist[2][kBins];          // of alternate passes: one is read by the cluster while the next is filled
+    __shared__ uint32_t warp_sum[kSelWarps], warp_eq[kSelWarps];
+    __shared__ uint32_t s_digit, s_above, s_tot[2];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int g = blockIdx.x, b = blockIdx.y;
+    const int g = blockIdx.x / CS, rank = blockIdx.x % CS, b = blockIdx.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const bool first = g == 0 && tid == 0;
+    const bool first = blockIdx.x == 0 && tid == 0;
     const int L = evict_len(p, b, first);
     const int e = cache_entry(p.batch_idx, b, p.B_cache, first);
     if (first) {
@@ -69,105 +89,164 @@ __global__ void __launch_bounds__(kSelThreads) fmha_evict_select_kernel(const Ev
         p.new_seqlen[b] = imin(L, p.budget);
     }
     int *kept = p.kept + ((int64_t)b * p.H_k + g) * p.budget;
-    if (L <= p.budget || e < 0) {
-        for (int i = tid; i < p.budget; i += kSelThreads) kept[i] = i < L ? i : -1;
+    if (L <= p.budget || e < 0) {                // the same in every CTA of the cluster
+        for (int i = rank * TH + tid; i < p.budget; i += CS * TH) kept[i] = i < L ? i : -1;
         return;
     }
     const int cand = L - p.recent, need = p.budget - p.recent;   // cand > need >= 0
     const float *acc = p.acc + ((int64_t)e * p.H_k + g) * p.S_max;
-    for (int i = tid; i < p.recent; i += kSelThreads) kept[need + i] = cand + i;
+    for (int i = rank * TH + tid; i < p.recent; i += CS * TH) kept[need + i] = cand + i;
     if (need == 0) return;
+
+    // this warp's run of rows [lo, hi), in blocks of kSelKeys a lane; a run of
+    // one block is read once and stays in registers
+    const int run = ((cand + CS * kSelWarps - 1) / (CS * kSelWarps) + 31) / 32 * 32;
+    const int lo = imin(cand, (rank * kSelWarps + warp) * run), hi = imin(cand, lo + run);
+    constexpr int kBlock = 32 * kSelKeys;
+    const bool once = run <= kBlock;
+    uint32_t key[kSelKeys];
+    auto load = [&](int base) {
+        float x[kSelKeys];
+#pragma unroll
+        for (int k = 0; k < kSelKeys; ++k) {
+            const int i = base + 32 * k + lane;
+            x[k] = i < hi ? acc[i] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kSelKeys; ++k) key[k] = score_key(x[k]);
+    };
+    if (once) load(lo);
 
     // the need-th largest key: its digits, and how many keys equal to it stay
     uint32_t prefix = 0, want = need;
+    for (int i = tid; i < kBins; i += TH) hist[0][i] = 0;
+    __syncthreads();
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < cand; i += kSelThreads) {
-            const uint32_t k = score_key(acc[i]);
-            if (pass == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1u);
-        }
-        __syncthreads();
-        // bins from the top: the one in which the count passes `want`
-        constexpr int PER = kBins / kSelThreads;
-        uint32_t mine = 0;
+        uint32_t *h = hist[pass & 1], *other = hist[(pass & 1) ^ 1];
+        for (int base = lo; base < hi; base += kBlock) {
+            if (!once) load(base);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) mine += hist[kBins - 1 - (tid * PER + i)];
+            for (int k = 0; k < kSelKeys; ++k)
+                if (base + 32 * k + lane < hi && (pass == 0 || (key[k] >> (shift + bits)) == prefix))
+                    atomicAdd(&h[(key[k] >> shift) & ((1u << bits) - 1)], 1u);
+        }
+        // every CTA's histogram is complete, and nobody reads the other buffer any more
+        if (CS > 1) cluster_sync();
+        else __syncthreads();
+        // bins from the top, two a thread: the one in which the count passes `want`
+        constexpr int PER = kBins / TH;
+        uint32_t n[PER], mine = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int bin = kBins - 1 - (tid * PER + i);
+            n[i] = 0;
+#pragma unroll
+            for (int c = 0; c < CS; ++c) n[i] += CS > 1 ? cluster_word(&h[bin], c) : h[bin];
+            mine += n[i];
+        }
+        for (int i = tid; i < kBins; i += TH) other[i] = 0;
         uint32_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += y;
         }
-        if (lane == 31) warp_sum[warp][0] = incl;
+        if (lane == 31) warp_sum[warp] = incl;
         __syncthreads();
-        uint32_t above = incl - mine;
-        for (int w = 0; w < warp; ++w) above += warp_sum[w][0];
+        const uint32_t ws = lane < kSelWarps ? warp_sum[lane] : 0u;
+        const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? ws : 0u);
+        uint32_t above = before + incl - mine;
         if (above < want && above + mine >= want) {
+#pragma unroll
             for (int i = 0; i < PER; ++i) {
-                const int bin = kBins - 1 - (tid * PER + i);
-                if (above + hist[bin] >= want) {
-                    s_digit = bin;
+                if (above < want && above + n[i] >= want) {
+                    s_digit = kBins - 1 - (tid * PER + i);
                     s_above = above;
-                    break;
                 }
-                above += hist[bin];
+                above += n[i];
             }
         }
         __syncthreads();
         prefix = (prefix << bits) | s_digit;
         want -= s_above;
-        __syncthreads();
     }
 
-    // rows above the threshold, and the first `want` equal to it, in order
-    uint32_t base_gt = 0, base_eq = 0;
-    for (int i0 = 0; i0 < cand; i0 += kSelThreads) {
-        const int i = i0 + tid;
-        const uint32_t k = i < cand ? score_key(acc[i]) : 0u;
-        const bool gt = i < cand && k > prefix, eq = i < cand && k == prefix;
-        const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) {
-            warp_sum[warp][0] = __popc(mg);
-            warp_sum[warp][1] = __popc(me);
-        }
-        __syncthreads();
-        uint32_t rg = base_gt, re = base_eq;
+    // rows above the threshold, and those equal to it, of every warp's run
+    uint32_t gt = 0, eq = 0;
+    for (int base = lo; base < hi; base += kBlock) {
+        if (!once) load(base);
 #pragma unroll
-        for (int w = 0; w < kSelThreads / 32; ++w) {
-            const uint32_t a = warp_sum[w][0], c = warp_sum[w][1];
-            if (w < warp) {
-                rg += a;
-                re += c;
-            }
-            base_gt += a;
-            base_eq += c;
+        for (int k = 0; k < kSelKeys; ++k) {
+            const bool in = base + 32 * k + lane < hi;
+            gt += in && key[k] > prefix;
+            eq += in && key[k] == prefix;
         }
-        const uint32_t lt = (1u << lane) - 1u;
-        rg += __popc(mg & lt);
-        re += __popc(me & lt);
-        if (gt || (eq && re < want)) kept[rg + min(re, want)] = i;
-        __syncthreads();
     }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    __syncthreads();
+    if (lane == 0) {
+        warp_sum[warp] = gt;
+        warp_eq[warp] = eq;
+    }
+    __syncthreads();
+    const uint32_t wg = lane < kSelWarps ? warp_sum[lane] : 0u, we = lane < kSelWarps ? warp_eq[lane] : 0u;
+    uint32_t at_gt = __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0u);
+    uint32_t at_eq = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0u);
+    if (CS > 1) {
+        const uint32_t tg = __reduce_add_sync(0xffffffffu, wg), te = __reduce_add_sync(0xffffffffu, we);
+        if (tid == 0) {
+            s_tot[0] = tg;
+            s_tot[1] = te;
+        }
+        cluster_sync();
+        for (int c = 0; c < rank; ++c) {
+            at_gt += cluster_word(&s_tot[0], c);
+            at_eq += cluster_word(&s_tot[1], c);
+        }
+    }
+    const uint32_t lt = (1u << lane) - 1u;
+    for (int base = lo; base < hi; base += kBlock) {
+        if (!once) load(base);
+#pragma unroll
+        for (int k = 0; k < kSelKeys; ++k) {
+            if (base + 32 * k >= hi) break;
+            const int i = base + 32 * k + lane;
+            const bool is_gt = i < hi && key[k] > prefix, is_eq = i < hi && key[k] == prefix;
+            const uint32_t mg = __ballot_sync(0xffffffffu, is_gt), me = __ballot_sync(0xffffffffu, is_eq);
+            const uint32_t re = at_eq + __popc(me & lt);
+            if (is_gt || (is_eq && re < want)) kept[at_gt + __popc(mg & lt) + min(re, want)] = i;
+            at_gt += __popc(mg);
+            at_eq += __popc(me);
+        }
+    }
+    if (CS > 1) cluster_sync();                  // the others have read this CTA's shared memory
 }
 
-// 16-byte pieces of a row, and the rows of a block: a block is 16 KB
-template <int ROW>
+// A CTA moves slices of SL bytes of a head's rows: 16-byte pieces, a thread
+// holds four rows' of a block.
+template <int SL>
 struct MoveCfg {
-    static constexpr int PIECES = ROW / 16;
+    static constexpr int PIECES = SL / 16;
     static constexpr int ROWS_AT_ONCE = kMoveThreads / PIECES;
-    static constexpr int PER = 4;                               // rows a thread holds
+    static constexpr int PER = 4;
     static constexpr int BLOCK = ROWS_AT_ONCE * PER;
 };
 
-// K or V of one head: grid (H_k, B, 2 * chunks); a chunk is every `chunks`-th
-// block of rows.  In place there is one chunk, walked in order.
-template <int ROW>
+// K or V of one head: grid (H_k, B, chunks * 2 * ROW / SL).  Apart from the
+// input, a chunk is every `chunks`-th block of whole rows.  In place there is
+// one chunk, walked in order, and for few heads the rows are cut into slices
+// of 64 bytes, which move down independently: four times the CTAs, and four
+// times the rows in a block.
+template <int ROW, int SL>
 __global__ void __launch_bounds__(kMoveThreads) fmha_evict_move_kernel(const EvictParams p) {
-    using M = MoveCfg<ROW>;
-    const int g = blockIdx.x, b = blockIdx.y, kv = blockIdx.z & 1, chunk = blockIdx.z >> 1, chunks = gridDim.z >> 1;
+    using M = MoveCfg<SL>;
+    constexpr int kSlices = ROW / SL;
+    const int g = blockIdx.x, b = blockIdx.y;
+    const int slice = blockIdx.z % kSlices, kv = blockIdx.z / kSlices % 2;
+    const int chunk = blockIdx.z / (2 * kSlices), chunks = gridDim.z / (2 * kSlices);
     const int tid = threadIdx.x, piece = tid % M::PIECES, r0 = tid / M::PIECES;
     const int L = evict_len(p, b, false), n = imin(L, p.budget);
     const int e = cache_entry(p.batch_idx, b, p.B_cache, false), d = cache_entry(p.out_idx, b, p.B_out, false);
@@ -175,16 +254,28 @@ __global__ void __launch_bounds__(kMoveThreads) fmha_evict_move_kernel(const Evi
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (e < 0 || d < 0) return;
     const int64_t pitch = (int64_t)p.H_k * ROW;
-    const uint8_t *src = (kv ? p.v : p.k) + (int64_t)e * p.S_max * pitch + (int64_t)g * ROW + piece * 16;
-    uint8_t *dst = (kv ? p.v_out : p.k_out) + (int64_t)d * p.S_out * pitch + (int64_t)g * ROW + piece * 16;
-    if (!p.in_place || L > p.budget) {
-        for (int i0 = chunk * M::BLOCK; i0 < n; i0 += chunks * M::BLOCK) {
-            uint4 x[M::PER];
+    const int64_t col = (int64_t)g * ROW + slice * SL + piece * 16;
+    const uint8_t *src = (kv ? p.v : p.k) + (int64_t)e * p.S_max * pitch + col;
+    uint8_t *dst = (kv ? p.v_out : p.k_out) + (int64_t)d * p.S_out * pitch + col;
+    const bool moves = !p.in_place || L > p.budget;
+    if (moves) {
+        // the rows' numbers of a block are fetched while the block before moves
+        int from[M::PER];
+        auto fetch = [&](int i0) {
 #pragma unroll
             for (int k = 0; k < M::PER; ++k) {
                 const int i = i0 + k * M::ROWS_AT_ONCE + r0;
-                if (i < n) x[k] = *reinterpret_cast<const uint4 *>(src + kept[i] * pitch);
+                from[k] = i < n ? kept[i] : 0;
             }
+        };
+        const int step = chunks * M::BLOCK;
+        fetch(chunk * M::BLOCK);
+        for (int i0 = chunk * M::BLOCK; i0 < n; i0 += step) {
+            uint4 x[M::PER];
+#pragma unroll
+            for (int k = 0; k < M::PER; ++k)
+                if (i0 + k * M::ROWS_AT_ONCE + r0 < n) x[k] = *reinterpret_cast<const uint4 *>(src + from[k] * pitch);
+            fetch(i0 + step);
             if (p.in_place) __syncthreads();                    // the block is read: it may be overwritten
 #pragma unroll
             for (int k = 0; k < M::PER; ++k) {
@@ -193,19 +284,28 @@ __global__ void __launch_bounds__(kMoveThreads) fmha_evict_move_kernel(const Evi
             }
         }
     }
-    if (kv != 0 || chunk != 0) return;
-    // the scores of the head, and zeros behind them
+    if (kv != 0 || slice != 0) return;
+    // the scores of the head, and zeros behind them, by the same chunks
     const float *a = p.acc + ((int64_t)e * p.H_k + g) * p.S_max;
     float *o = p.acc_out + ((int64_t)d * p.H_k + g) * p.S_out;
-    if (!p.in_place || L > p.budget)
-        for (int i0 = 0; i0 < n; i0 += kMoveThreads) {
-            const int i = i0 + tid;
-            const float x = i < n ? a[kept[i]] : 0.f;
+    constexpr int kScores = 4;                                  // a thread
+    if (moves)
+        for (int i0 = chunk * kScores * kMoveThreads; i0 < n; i0 += chunks * kScores * kMoveThreads) {
+            float x[kScores];
+#pragma unroll
+            for (int k = 0; k < kScores; ++k) {
+                const int i = i0 + k * kMoveThreads + tid;
+                x[k] = i < n ? a[kept[i]] : 0.f;
+            }
             if (p.in_place) __syncthreads();
-            if (i < n) o[i] = x;
+#pragma unroll
+            for (int k = 0; k < kScores; ++k) {
+                const int i = i0 + k * kMoveThreads + tid;
+                if (i < n) o[i] = x[k];
+            }
         }
     __syncthreads();
-    for (int i = n + tid; i < p.S_out; i += kMoveThreads) o[i] = 0.f;
+    for (int i = n + chunk * kMoveThreads + tid; i < p.S_out; i += chunks * kMoveThreads) o[i] = 0.f;
 }
 
 }  // namespace
@@ -281,19 +381,41 @@ extern "C" int fmha_cache_evict(fmha_tensor k_cache, fmha_tensor v_cache, const 
     p.recent = recent;
     p.row = row;
     p.in_place = in_place ? 1 : 0;
-    fmha_evict_select_kernel<<<dim3(H_k, B), kSelThreads, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return FMHA_ERR_CUDA;
+    // CTAs of a head's selection: while all fit the SMs at once (clusters of
+    // eight do not pack: half) and each has 2048 rows; 1024 threads where 512
+    // would not hold a CTA's keys in registers
+    int cs = 8;
+    while (cs > 1 && ((int64_t)B * H_k * cs > (cs == 8 ? sms / 2 : sms) || S_max / cs < 2048)) cs /= 2;
+    const bool wide = S_max / cs > 512 * kSelKeys;
+    {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(cs * H_k, B);
+        cfg.blockDim = dim3(wide ? 1024 : 512);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = cs;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = cs > 1 ? 1 : 0;
+        auto select = wide ? (cs == 8 ? fmha_evict_select_kernel<8, 1024> : cs == 4 ? fmha_evict_select_kernel<4, 1024>
+                              : cs == 2 ? fmha_evict_select_kernel<2, 1024> : fmha_evict_select_kernel<1, 1024>)
+                           : (cs == 8 ? fmha_evict_select_kernel<8, 512> : cs == 4 ? fmha_evict_select_kernel<4, 512>
+                              : cs == 2 ? fmha_evict_select_kernel<2, 512> : fmha_evict_select_kernel<1, 512>);
+        if (cudaLaunchKernelEx(&cfg, select, p) != cudaSuccess) return cuda_failed();
+    }
 
     // apart from the input, the blocks of a head are spread over CTAs until
-    // the SMs hold eight each
+    // the SMs hold eight each; in place, few heads are cut into slices
+    const int64_t heads = (int64_t)2 * B * H_k;
+    const bool sliced = in_place && heads < 2 * sms;
     const int block = dt == FMHA_E4M3 ? MoveCfg<128>::BLOCK : MoveCfg<256>::BLOCK;
     const int blocks = (budget + block - 1) / block;
-    const int64_t heads = (int64_t)2 * B * H_k;
     int chunks = (int)((8 * (int64_t)sms + heads - 1) / heads);
     if (chunks > blocks) chunks = blocks;
     if (in_place) chunks = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(H_k, B, 2 * chunks);
+    cfg.gridDim = dim3(H_k, B, 2 * chunks * (sliced ? row / 64 : 1));
     cfg.blockDim = dim3(kMoveThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -301,7 +423,8 @@ extern "C" int fmha_cache_evict(fmha_tensor k_cache, fmha_tensor v_cache, const 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    auto move = dt == FMHA_E4M3 ? fmha_evict_move_kernel<128> : fmha_evict_move_kernel<256>;
+    auto move = dt == FMHA_E4M3 ? (sliced ? fmha_evict_move_kernel<128, 64> : fmha_evict_move_kernel<128, 128>)
+                                : (sliced ? fmha_evict_move_kernel<256, 64> : fmha_evict_move_kernel<256, 256>);
     if (cudaLaunchKernelEx(&cfg, move, p) != cudaSuccess) return cuda_failed();
     return FMHA_OK;
 }

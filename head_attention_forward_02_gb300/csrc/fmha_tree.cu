@@ -748,12 +748,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         tmem_alloc(smem_u32(&bars->tmem_base), 512);
         tmem_relinquish();
     }
-    if (threadIdx.x == kTreeProd * 32) {
-        prefetch_tmap(&tmQ);
-        prefetch_tmap(&tmK);
-        prefetch_tmap(&tmV);
-        prefetch_tmap(&tmKn);
-        prefetch_tmap(&tmVn);
+    TreeCursor cur;
+    int gate = 0;
+    if (warp == kTreeProd) {
+        if (lane == 0) {
+            prefetch_tmap(&tmQ);
+            prefetch_tmap(&tmK);
+            prefetch_tmap(&tmV);
+            prefetch_tmap(&tmKn);
+            prefetch_tmap(&tmVn);
+        }
+        gate = g_test_gate;             // read along with the lengths
+        tree_schedule(p, cur, lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -765,9 +771,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (warp < kTreeProd) {
         tree_softmax<C>(p, smem, bars, tmem, warp, lane);
     } else if (warp == kTreeProd) {
-        TreeCursor cur;
-        const int gate = g_test_gate;   // read along with the lengths
-        tree_schedule(p, cur, lane);
         if (lane == 0) tree_producer<C>(p, cur, gate, &tmQ, &tmK, &tmV, &tmKn, &tmVn, smem, bars);
     } else {
         tree_mma<C>(smem, bars, tmem, warp - kTreeMma, lane);

@@ -202,6 +202,7 @@ E_CASES = {
     "budget_1": dict(dtype="e4m3", H_k=1, S_max=50, S_out=5, seqlen=[50, 2, 1], budget=1, recent=0),
     "all_but_one": dict(dtype="e4m3", H_k=5, S_max=1025, S_out=1024, seqlen=[1025], budget=1024, recent=3),
     "long": dict(dtype="e4m3", H_k=2, S_max=70001, S_out=1000, seqlen=[70001, 40000], budget=999, recent=10),
+    "two_ctas": dict(dtype="bf16", H_k=3, S_max=4700, S_out=300, seqlen=[4700, 301], budget=300, recent=7),
     "many": dict(dtype="bf16", H_k=2, S_max=90, S_out=64, seqlen=[(i * 17) % 91 for i in range(80)], budget=33, recent=5),
 }
 

@@ -100,6 +100,9 @@ CASES = {
     "batch": dict(dtype="bf16", T=9, H=8, H_k=2, S_max=900, seqlen=[(i * 37) % 900 for i in range(70)],
                   n_draft=[1 + i % 9 for i in range(70)], batch_idx=[(i * 3) % 70 for i in range(70)]),
     "peaked": dict(dtype="bf16", T=12, H=8, H_k=2, S_max=3000, seqlen=[2999], q_scale=20.0),
+    "head_pairs": dict(dtype="e4m3", T=3, H=40, H_k=10, S_max=4500, seqlen=[4500, 130, 0, 4097, 128, 700], n_draft=[3, 1, 3, 0, 2, 3],
+                       batch_idx=[5, 0, 2, 1, 4, 3]),
+    "head_pairs_full": dict(dtype="e4m3", T=32, H=16, H_k=4, S_max=9000, seqlen=[9000, 20, 4097, 128, 333]),
     "wide_long": dict(dtype="e4m3", T=64, H=8, H_k=1, S_max=4100, seqlen=[4097]),
 }
 
