@@ -18,7 +18,9 @@
 //
 // A unit is 256 keys of one kv head (two MMA tiles that share the query
 // stream) and its query chunks (TB = 128 / G tokens each).  The chunks of all
-// units form one sequence, cut evenly over the CTAs; a unit that is cut
+// units form one sequence, kv heads fastest, so that a CTA reads the heads'
+// rows of the same keys one after another (they are adjacent in the cache);
+// the sequence is cut evenly over the CTAs; a unit that is cut
 // leaves partial sums (256 floats) in the workspace and a second kernel adds
 // them in CTA order, so results do not depend on timing.
 #include "fmha_cache.cuh"
@@ -29,20 +31,8 @@ namespace {
 
 constexpr int kWeightsMaxCtas = 152;     // CTAs at most (bounds the workspace)
 constexpr int kUnitKeys = 2 * kRows;
-constexpr int kWThreads = 320;           // 8 softmax warps, producer, MMA issuer
-constexpr int kWProd = 8, kWMma = 9;
-
-template <int ELEM>
-struct WCfg : ElemCfg<ELEM> {
-    using B = ElemCfg<ELEM>;
-    static constexpr int NK = 4 * 32768 / B::TILE_BYTES;      // K ring stages (one 128-key tile each): 128 KB
-    static constexpr int NQ = 2 * 32768 / B::TILE_BYTES;      // Q ring stages (one chunk each): 64 KB
-    static constexpr int OFF_K = 0;
-    static constexpr int OFF_Q = NK * B::TILE_BYTES;
-    static constexpr int OFF_BARS = OFF_Q + NQ * B::TILE_BYTES;
-    static constexpr int SMEM_BYTES = OFF_BARS + 4096 + 1024;
-    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-};
+constexpr int kWThreads = 352;           // 8 summing warps, producer, MMA issuer, LSE loader
+constexpr int kWProd = 8, kWMma = 9, kWLse = 10;
 
 struct WMeta {                           // one partial sum in the workspace
     int64_t row;                         // its unit's first element of acc
@@ -64,20 +54,42 @@ struct WParams {
     float c;                             // scale * log2(e)
 };
 
-struct WSched {
-    int64_t left;                        // chunks of this CTA
-    int b, g, tile, skip;                // its first unit, and chunks of that unit that are other CTAs'
+struct WItem {
+    int b, g, tile, entry, L, n;         // b < 0: no more items
+    int c0, c1;                          // query chunks [c0, c1) of the unit that are this CTA's
+    int nkt;                             // K tiles to load: 2, or 1 at the end of a sequence
+    bool begins, ends;                   // the unit's first / last chunk is among them
 };
 
+constexpr int kWItems = 4;               // work items published ahead
+constexpr int kWStages = 14;             // ring stages at most, K's and Q's together
+
 struct WBars {
-    uint64_t k_full[8], k_empty[8], q_full[4], q_empty[4];
-    uint64_t s_full[2][2], s_free[2][2], drain;
+    uint64_t full[kWStages], empty[kWStages];            // K ring, then Q ring
+    uint64_t s_full[2][2], s_free[2][2], drain;          // [key tile][buffer]
+    uint64_t item_full[kWItems], item_empty[kWItems];
+    WItem item[kWItems];
     uint32_t tmem_base;
     int abort;
-    WSched sched;
-    float lse[2][2][kRows];              // per group and buffer: a chunk's LSE in log2 units
+    alignas(16) float lse[2][kRows];     // by buffer: a chunk's -LSE in log2 units
 };
-static_assert(sizeof(WBars) <= 4096, "barrier block");
+
+// Ring stages of 128 rows, 224 KB in all.  Where a sequence's rows fill one
+// chunk (ONE) the stream is K's: 160 KB of it in flight; else it is Q's, 32 KB
+// a chunk from L2, with two stages of which a chunk's load latency was
+// exposed (TODO-FIGURES).
+template <int ELEM, bool ONE>
+struct WCfg : ElemCfg<ELEM> {
+    using B = ElemCfg<ELEM>;
+    static constexpr int NK = (ONE ? 5 : 3) * 32768 / B::TILE_BYTES;
+    static constexpr int NQ = (ONE ? 2 : 4) * 32768 / B::TILE_BYTES;
+    static_assert(NK + NQ <= kWStages, "ring barriers");
+    static constexpr int OFF_K = 0;
+    static constexpr int OFF_Q = NK * B::TILE_BYTES;
+    static constexpr int OFF_BARS = OFF_Q + NQ * B::TILE_BYTES;
+    static constexpr int SMEM_BYTES = OFF_BARS + sizeof(WBars) + 1024;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+};
 
 __device__ __forceinline__ int w_keys(const WParams &p, int b, bool report) {
     return clamped(p.seqlen[b], 0, p.S_max, report);
@@ -111,23 +123,37 @@ __device__ __forceinline__ int64_t w_head_cost(const WParams &p, int L, int n, i
     return cost;
 }
 
-// One warp: this CTA's share of the chunks and where it starts.
-__device__ void w_schedule(const WParams &p, WSched *sc, int lane) {
+// Where the producer is in this CTA's chunks.
+struct WCursor {
+    int64_t left;                        // chunks still to hand out
+    int b, g, tile, skip;                // next unit, and chunks of it that are other CTAs'
+    int L, n, entry;                     // of sequence b
+};
+
+__device__ __forceinline__ void w_load_seq(const WParams &p, WCursor &cur) {
+    cur.L = w_keys(p, cur.b, false);
+    cur.n = w_queries(p, cur.b, false);
+    cur.entry = cache_entry(p.batch_idx, cur.b, p.B_cache, false);
+}
+
+// One warp: this CTA's share of the chunks and where it starts (the same in every lane).
+__device__ void w_schedule(const WParams &p, WCursor &cur, int lane) {
     int64_t T = 0;
     int uni;
-    for (int b = lane; b < p.B; b += 32) {
-        const bool report = blockIdx.x == 0;                 // values outside their bounds, once a call
-        if (report) cache_entry(p.batch_idx, b, p.B_cache, true);
-        T += p.H_k * w_head_cost(p, w_keys(p, b, report), w_queries(p, b, report), &uni);
-    }
+    for (int b = lane; b < p.B; b += 32) T += p.H_k * w_head_cost(p, w_keys(p, b, false), w_queries(p, b, false), &uni);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) T += __shfl_xor_sync(0xffffffffu, T, o);
     const int64_t per = (T + gridDim.x - 1) / gridDim.x;
     const int64_t G0 = min((int64_t)blockIdx.x * per, T), G1 = min(G0 + per, T);
-    WSched s;
-    s.left = G1 - G0;
-    s.b = p.B;
-    s.g = s.tile = s.skip = 0;
+    if (blockIdx.x == gridDim.x - 1)     // reports values outside their bounds, once a call
+        for (int b = lane; b < p.B; b += 32) {
+            w_keys(p, b, true);
+            w_queries(p, b, true);
+            cache_entry(p.batch_idx, b, p.B_cache, true);
+        }
+    cur.left = G1 - G0;
+    cur.b = p.B;
+    cur.g = cur.tile = cur.skip = 0;
     int64_t base = 0;
     for (int bb = 0; bb < p.B && G0 < G1; bb += 32) {
         const int b = bb + lane;
@@ -142,94 +168,96 @@ __device__ void w_schedule(const WParams &p, WSched *sc, int lane) {
         const unsigned hit = __ballot_sync(0xffffffffu, head > 0 && base + incl > G0);
         if (hit) {
             const int l = __ffs(hit) - 1;
-            if (lane == l) {
-                int64_t r = G0 - (base + incl - p.H_k * head);
-                const int L = w_keys(p, b, false), n = w_queries(p, b, false);
-                s.b = b;
-                s.g = (int)(r / head);
-                r -= s.g * head;
-                const int64_t c0 = w_cost(p, L, n, 0);
-                s.tile = uni > 0 ? (int)min((int64_t)uni, r / c0) : 0;
-                r -= s.tile * c0;
-                while (r >= w_cost(p, L, n, s.tile)) r -= w_cost(p, L, n, s.tile++);
-                s.skip = (int)r;
-                *sc = s;
-            }
+            cur.b = bb + l;
+            w_load_seq(p, cur);
+            head = __shfl_sync(0xffffffffu, head, l);
+            uni = __shfl_sync(0xffffffffu, uni, l);
+            int64_t r = G0 - (__shfl_sync(0xffffffffu, base + incl, l) - p.H_k * head);
+            auto cost = [&](int tile) { return (int64_t)p.H_k * w_cost(p, cur.L, cur.n, tile); };
+            cur.tile = uni > 0 ? (int)min((int64_t)uni, r / cost(0)) : 0;
+            r -= cur.tile * cost(0);
+            while (r >= cost(cur.tile)) r -= cost(cur.tile++);
+            const int unit = w_cost(p, cur.L, cur.n, cur.tile);
+            cur.g = (int)(r / unit);
+            r -= (int64_t)cur.g * unit;
+            cur.skip = (int)r;
             return;
         }
         base += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) *sc = s;
 }
 
-struct WItem {
-    int b, g, tile, entry, L, n;
-    int c0, c1;                          // query chunks [c0, c1) of the unit that are this CTA's
-    int nkt;                             // key tiles of the unit: 2, or 1 at the end of a sequence
-    bool begins, ends;                   // the unit's first / last chunk is among them
-};
-
-struct WCursor {
-    int b = -1, g = 0, tile = 0, skip = 0;
-    int64_t left = 0;
-};
-
-__device__ bool w_next(const WParams &p, const WSched &sc, WCursor &cur, WItem &it) {
-    if (cur.b < 0) {
-        cur.b = sc.b;
-        cur.g = sc.g;
-        cur.tile = sc.tile;
-        cur.skip = sc.skip;
-        cur.left = sc.left;
-    }
+__device__ bool w_next(const WParams &p, WCursor &cur, WItem &it) {
+    it.b = -1;
     for (;;) {
         if (cur.b >= p.B || cur.left <= 0) return false;
-        const int L = w_keys(p, cur.b, false), n = w_queries(p, cur.b, false);
-        if (cur.tile * kUnitKeys < L) {
-            const int cost = w_cost(p, L, n, cur.tile), fc = w_first_chunk(p, L, n, cur.tile);
+        if (cur.tile * kUnitKeys < cur.L) {
+            const int cost = w_cost(p, cur.L, cur.n, cur.tile), fc = w_first_chunk(p, cur.L, cur.n, cur.tile);
             const int take = (int)min((int64_t)(cost - cur.skip), cur.left);
             it.b = cur.b;
             it.g = cur.g;
             it.tile = cur.tile;
-            it.entry = cache_entry(p.batch_idx, cur.b, p.B_cache, false);
-            it.L = L;
-            it.n = n;
-            it.nkt = L - cur.tile * kUnitKeys > kRows ? 2 : 1;
+            it.entry = cur.entry;
+            it.L = cur.L;
+            it.n = cur.n;
+            it.nkt = cur.L - cur.tile * kUnitKeys > kRows ? 2 : 1;
             it.begins = cur.skip == 0;
             it.ends = cur.skip + take == cost;
             it.c0 = fc + cur.skip;
-            it.c1 = imin(it.c0 + take, (n + p.TB - 1) / p.TB);   // none without queries
+            it.c1 = imin(it.c0 + take, (cur.n + p.TB - 1) / p.TB);   // none without queries
             cur.left -= take;
             cur.skip = 0;
-            ++cur.tile;
+            if (++cur.g == p.H_k) {
+                cur.g = 0;
+                ++cur.tile;
+            }
             return true;
         }
         cur.tile = 0;
-        if (++cur.g == p.H_k) {
-            cur.g = 0;
-            ++cur.b;
-        }
+        if (++cur.b < p.B) w_load_seq(p, cur);
     }
 }
 
+// Items: the producer publishes them ahead of its loads; the other warps take
+// a copy each and hand the slot back.
+__device__ __forceinline__ bool w_publish(WBars *bars, uint32_t i, const WItem &it, volatile int *abort_flag) {
+    const uint32_t st = i % kWItems;
+    if (i >= kWItems && !mbar_wait(smem_u32(&bars->item_empty[st]), (i / kWItems - 1) & 1, abort_flag)) return false;
+    bars->item[st] = it;
+    mbar_arrive(smem_u32(&bars->item_full[st]));
+    return true;
+}
+
+__device__ __forceinline__ bool w_take(WBars *bars, uint32_t i, WItem &it, volatile int *abort_flag, int lane) {
+    const uint32_t st = i % kWItems;
+    if (!warp_wait(smem_u32(&bars->item_full[st]), (i / kWItems) & 1, abort_flag)) return false;
+    it = bars->item[st];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[st]));
+    return it.b >= 0;
+}
+
 template <class C>
-__device__ void w_producer(const WParams &p, const WSched &sc, const CUtensorMap *tmQ, const CUtensorMap *tmK,
+__device__ void w_producer(const WParams &p, WCursor &cur, int gate, const CUtensorMap *tmQ, const CUtensorMap *tmK,
                            uint8_t *smem, WBars *bars) {
     volatile int *abort_flag = &bars->abort;
+    uint64_t *k_full = bars->full, *k_empty = bars->empty, *q_full = k_full + C::NK, *q_empty = k_empty + C::NK;
     uint32_t kf = 0, qf = 0;
-    bool ok = test_gate_open(abort_flag);
-    WCursor cur;
-    while (ok) {
-        WItem it;
-        if (!w_next(p, sc, cur, it)) break;
+    bool ok = !gate || test_gate_open(abort_flag);
+    WItem it, next;
+    if (ok) {
+        w_next(p, cur, it);
+        ok = w_publish(bars, 0, it, abort_flag);
+    }
+    for (uint32_t i = 1; ok && it.b >= 0; ++i, it = next) {
         const int e = it.entry >= 0 ? it.entry : p.B_cache;   // out of range: zero fill
-        for (int x = 0; ok && x < it.nkt; ++x, ++kf) {
+        for (int x = 0; x < it.nkt; ++x, ++kf) {
             const int st = kf % C::NK;
-            if (kf >= C::NK && !mbar_wait(smem_u32(&bars->k_empty[st]), (kf / C::NK - 1) & 1, abort_flag)) {
+            if (kf >= C::NK && !mbar_wait(smem_u32(&k_empty[st]), (kf / C::NK - 1) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
-            const uint32_t fb = smem_u32(&bars->k_full[st]);
+            const uint32_t fb = smem_u32(&k_full[st]);
             mbar_expect_tx(fb, C::TILE_BYTES);
 #pragma unroll
             for (int pn = 0; pn < C::PANELS; ++pn)
@@ -238,65 +266,69 @@ __device__ void w_producer(const WParams &p, const WSched &sc, const CUtensorMap
         }
         for (int c = it.c0; ok && c < it.c1; ++c, ++qf) {
             const int st = qf % C::NQ;
-            if (qf >= C::NQ && !mbar_wait(smem_u32(&bars->q_empty[st]), (qf / C::NQ - 1) & 1, abort_flag)) {
+            if (qf >= C::NQ && !mbar_wait(smem_u32(&q_empty[st]), (qf / C::NQ - 1) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
-            const uint32_t fb = smem_u32(&bars->q_full[st]);
+            const uint32_t fb = smem_u32(&q_full[st]);
             mbar_expect_tx(fb, C::PANELS * p.TB * p.G * 128);
 #pragma unroll
             for (int pn = 0; pn < C::PANELS; ++pn)
                 tma_load_3d(smem_u32(smem + C::OFF_Q + st * C::TILE_BYTES + pn * kPanelBytes), tmQ, fb, pn * C::BOX,
                             it.g * p.G, it.b * p.Sq + c * p.TB);
+            if (c == it.c0) {
+                w_next(p, cur, next);
+                ok = w_publish(bars, i, next, abort_flag);
+            }
+        }
+        if (ok && it.c0 >= it.c1) {
+            w_next(p, cur, next);
+            ok = w_publish(bars, i, next, abort_flag);
         }
     }
-    if (ok) {
-        // the last release of every stage must arrive before exit
-        for (uint32_t f = kf > C::NK ? kf - C::NK : 0; f < kf; ++f)
-            if (!mbar_wait(smem_u32(&bars->k_empty[f % C::NK]), (f / C::NK) & 1, abort_flag)) break;
-        for (uint32_t f = qf > C::NQ ? qf - C::NQ : 0; f < qf; ++f)
-            if (!mbar_wait(smem_u32(&bars->q_empty[f % C::NQ]), (f / C::NQ) & 1, abort_flag)) break;
-    } else {
-        // aborted: let the copies already issued land before the CTA exits
-        for (uint32_t f = kf > C::NK ? kf - C::NK : 0; f < kf; ++f)
-            mbar_wait_drain(smem_u32(&bars->k_full[f % C::NK]), (f / C::NK) & 1);
-        for (uint32_t f = qf > C::NQ ? qf - C::NQ : 0; f < qf; ++f)
-            mbar_wait_drain(smem_u32(&bars->q_full[f % C::NQ]), (f / C::NQ) & 1);
+    // the last release of every stage must arrive before exit; when the CTA
+    // gave up, only the copies already issued
+    for (uint32_t f = kf > C::NK ? kf - C::NK : 0; f < kf; ++f) {
+        if (ok) ok = mbar_wait(smem_u32(&k_empty[f % C::NK]), (f / C::NK) & 1, abort_flag);
+        if (!ok) mbar_wait_drain(smem_u32(&k_full[f % C::NK]), (f / C::NK) & 1);
+    }
+    for (uint32_t f = qf > C::NQ ? qf - C::NQ : 0; f < qf; ++f) {
+        if (ok) ok = mbar_wait(smem_u32(&q_empty[f % C::NQ]), (f / C::NQ) & 1, abort_flag);
+        if (!ok) mbar_wait_drain(smem_u32(&q_full[f % C::NQ]), (f / C::NQ) & 1);
     }
 }
 
-// S^T of every (chunk, key tile) into that tile's two alternating buffers.
+// S^T of every (chunk, key tile) into that tile's buffer chunk % 2.  A unit of
+// one key tile computes it twice; the second copy is not stored.
 template <class C>
-__device__ void w_mma(const WParams &p, const WSched &sc, uint8_t *smem, WBars *bars, uint32_t tmem_any) {
+__device__ void w_mma(const WParams &p, uint8_t *smem, WBars *bars, uint32_t tmem_any, int lane) {
     volatile int *abort_flag = &bars->abort;
+    uint64_t *k_full = bars->full, *k_empty = bars->empty, *q_full = k_full + C::NK, *q_empty = k_empty + C::NK;
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
     const uint32_t idesc = mma_idesc(C::FMT, p.NMMA, false);
-    uint32_t kf = 0, qf = 0, cnt[2] = {0, 0};
+    uint32_t kf = 0, qf = 0;             // K tiles and chunks so far
     bool ok = true;
-    WCursor cur;
-    while (ok) {
-        WItem it;
-        if (!w_next(p, sc, cur, it)) break;
+    WItem it;
+    for (uint32_t i = 0; ok && w_take(bars, i, it, abort_flag, lane); ++i) {
         for (int x = 0; ok && x < it.nkt; ++x)
-            ok = warp_wait(smem_u32(&bars->k_full[(kf + x) % C::NK]), ((kf + x) / C::NK) & 1, abort_flag);
+            ok = warp_wait(smem_u32(&k_full[(kf + x) % C::NK]), ((kf + x) / C::NK) & 1, abort_flag);
         for (int c = it.c0; ok && c < it.c1; ++c, ++qf) {
             const int qst = qf % C::NQ;
-            if (!warp_wait(smem_u32(&bars->q_full[qst]), (qf / C::NQ) & 1, abort_flag)) {
+            const uint32_t buf = qf & 1;
+            if (!warp_wait(smem_u32(&q_full[qst]), (qf / C::NQ) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
             const uint64_t q = smem_desc(smem_u32(smem + C::OFF_Q + qst * C::TILE_BYTES), 16, 1024);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                if (!ok || x >= it.nkt) continue;
-                const uint32_t i = cnt[x]++, buf = i & 1;
-                if (i >= 2 && !warp_wait(smem_u32(&bars->s_free[x][buf]), ((i - 2) >> 1) & 1, abort_flag)) {
+                if (!ok || (qf >= 2 && !warp_wait(smem_u32(&bars->s_free[x][buf]), ((qf - 2) >> 1) & 1, abort_flag))) {
                     ok = false;
                     continue;
                 }
                 tc_fence_after();
-                const uint64_t k =
-                    smem_desc(smem_u32(smem + C::OFF_K + ((kf + x) % C::NK) * C::TILE_BYTES), 16, 1024);
+                const uint64_t k = smem_desc(
+                    smem_u32(smem + C::OFF_K + ((kf + (x < it.nkt ? x : 0)) % C::NK) * C::TILE_BYTES), 16, 1024);
 #pragma unroll
                 for (int kk = 0; kk < kD / C::MMA_K; ++kk) {
                     const uint32_t off = (kk * 32 / 128) * kPanelBytes + (kk * 32) % 128;
@@ -304,10 +336,10 @@ __device__ void w_mma(const WParams &p, const WSched &sc, uint8_t *smem, WBars *
                 }
                 tc_commit(smem_u32(&bars->s_full[x][buf]));
             }
-            if (ok) tc_commit(smem_u32(&bars->q_empty[qst]));
+            if (ok) tc_commit(smem_u32(&q_empty[qst]));
         }
         if (!ok) break;
-        for (int x = 0; x < it.nkt; ++x) tc_commit(smem_u32(&bars->k_empty[(kf + x) % C::NK]));
+        for (int x = 0; x < it.nkt; ++x) tc_commit(smem_u32(&k_empty[(kf + x) % C::NK]));
         kf += it.nkt;
     }
     // no tensor-core operation may be in flight when TMEM is released
@@ -315,87 +347,116 @@ __device__ void w_mma(const WParams &p, const WSched &sc, uint8_t *smem, WBars *
     mbar_wait_drain(smem_u32(&bars->drain), 0);
 }
 
-// Barrier 1 + x over the 128 threads of key tile x, with a vote: all go on or all give up.
-__device__ __forceinline__ bool group_all(int x, bool v) {
-    uint32_t r;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.and.pred q, %2, 128, p;\nselp.u32 %0, 1, 0, q;\n}\n"
-                 : "=r"(r)
-                 : "r"((uint32_t)v), "r"(1 + x)
-                 : "memory");
-    return r != 0;
+// One warp: -LSE of every chunk's columns, in log2 units (-inf, weight 0,
+// where the row saw no key), into shared memory; its arrival and the MMA's
+// complete s_full together.  (With the summing threads loading it, a chunk had
+// two barriers of 128 threads: 2500 cycles against TODO-FIGURES.)
+__device__ void w_load_lse(const WParams &p, WBars *bars, int lane) {
+    volatile int *abort_flag = &bars->abort;
+    uint32_t n = 0;                      // chunks so far
+    WItem it;
+    for (uint32_t i = 0; w_take(bars, i, it, abort_flag, lane); ++i) {
+        const float *lse = p.lse + ((int64_t)it.b * p.H + it.g * p.G) * p.Sq;
+        for (int c = it.c0; c < it.c1; ++c, ++n) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = 32 * k + lane, rt = r / p.G, t = c * p.TB + rt;
+                v[k] = rt < p.TB && t < it.n ? lse[(int64_t)(r - rt * p.G) * p.Sq + t] : -INFINITY;
+            }
+            const uint32_t buf = n & 1;
+            if (n >= 2 && (!warp_wait(smem_u32(&bars->s_free[0][buf]), ((n - 2) >> 1) & 1, abort_flag) ||
+                           !warp_wait(smem_u32(&bars->s_free[1][buf]), ((n - 2) >> 1) & 1, abort_flag)))
+                return;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) bars->lse[buf][32 * k + lane] = v[k] == -INFINITY ? -INFINITY : v[k] * -kLog2e;
+            __syncwarp();
+            if (lane < 2) mbar_arrive(smem_u32(&bars->s_full[lane][buf]));
+        }
+    }
 }
 
 // Weights: warps 4x .. 4x + 3 own key tile x of every unit, a key a thread.
-__device__ void w_sum(const WParams &p, const WSched &sc, WBars *bars, uint32_t tmem, int warp, int lane) {
+__device__ void w_sum(const WParams &p, WBars *bars, uint32_t tmem, int warp, int lane) {
     volatile int *abort_flag = &bars->abort;
     const int x = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 2 * x * kRows;
-    const int rt = r / p.G, rh = r % p.G;                // as a chunk's column: its token and head
-    uint32_t cnt = 0;
+    uint32_t n = 0;                                      // chunks so far
     int parts = 0;                                       // bit s: slot s of this CTA holds a partial
-    WCursor cur;
-    for (;;) {
-        WItem it;
-        if (!w_next(p, sc, cur, it)) break;
+    WItem it;
+    for (uint32_t i = 0; w_take(bars, i, it, abort_flag, lane); ++i) {
         const int key = it.tile * kUnitKeys + x * kRows + r;
         const bool whole = it.begins && it.ends;
         const int64_t at = ((int64_t)(it.entry < 0 ? 0 : it.entry) * p.H_k + it.g) * p.S_max + key;
         float old = 0.f;
         if (whole && p.acc_in && key < it.L && it.entry >= 0) old = p.acc_in[at];
-        // LSE of this thread's column of chunk c, in log2 units; +inf (weight
-        // 0) where the row saw no key
-        auto load_lse = [&](int c) {
-            const int t = c * p.TB + rt;
-            if (rt >= p.TB || t >= it.n) return INFINITY;
-            const float v = p.lse[((int64_t)it.b * p.H + it.g * p.G + rh) * p.Sq + t];
-            return v == -INFINITY ? INFINITY : v * kLog2e;
-        };
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t sum[2] = {0, 0};        // two pairs of partial sums
         bool ok = true;
-        if (x < it.nkt) {
-            float next = it.c0 < it.c1 ? load_lse(it.c0) : 0.f;
-            for (int c = it.c0; c < it.c1; ++c, ++cnt) {
-                const uint32_t buf = cnt & 1;
-                float *lse = bars->lse[x][buf];
-                lse[r] = next;           // the threads that read it two chunks ago are past the last barrier
-                if (c + 1 < it.c1) next = load_lse(c + 1);
-                if (!group_all(x, warp_wait(smem_u32(&bars->s_full[x][buf]), (cnt >> 1) & 1, abort_flag))) {
-                    ok = false;
-                    break;
+        for (int c = it.c0; c < it.c1; ++c, ++n) {
+            const uint32_t buf = n & 1;
+            const float *lse = bars->lse[buf];
+            if (!warp_wait(smem_u32(&bars->s_full[x][buf]), (n >> 1) & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const int cols = imin(p.TB, it.n - c * p.TB) * p.G;      // valid columns
+            // columns below lo are queries that do not see this key
+            int lo = 0;
+            if (p.causal) {
+                const int t = key - (it.L - it.n) - c * p.TB;        // first token of the chunk that sees it
+                lo = t <= 0 ? 0 : t >= p.TB ? kRows : t * p.G;
+            }
+            const uint32_t s_tm = lane_base + buf * kRows;
+            const uint64_t c2 = pack_f2(p.c, p.c);
+            // 32 columns: weights of pairs, with a check of every column where some are not to be counted
+            auto add = [&](const uint32_t (&s)[32], int q, bool all) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    const ulonglong2 nl = *reinterpret_cast<const ulonglong2 *>(lse + q + i);
+                    float w[4];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const uint64_t s2 = pack_f2(__uint_as_float(s[i + 2 * y]), __uint_as_float(s[i + 2 * y + 1]));
+                        unpack_f2(fma_f2(s2, c2, y ? nl.y : nl.x), w[2 * y], w[2 * y + 1]);
+                    }
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        w[y] = ex2(w[y]);
+                        if (!all) w[y] = q + i + y >= lo && q + i + y < cols ? w[y] : 0.f;
+                    }
+                    sum[0] = add_f2(sum[0], pack_f2(w[0], w[1]));
+                    sum[1] = add_f2(sum[1], pack_f2(w[2], w[3]));
                 }
-                tc_fence_after();
-                const int cols = imin(p.TB, it.n - c * p.TB) * p.G;      // valid columns
-                // columns below lo are queries that do not see this key
-                int lo = 0;
-                if (p.causal) {
-                    const int t = key - (it.L - it.n) - c * p.TB;        // first token of the chunk that sees it
-                    lo = t <= 0 ? 0 : t >= p.TB ? kRows : t * p.G;
+            };
+            if (cols == kRows && __all_sync(0xffffffffu, lo == 0)) {
+                // the whole tile: all its loads in flight at once
+                uint32_t s[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_ld32(s_tm + 32 * q, s[q]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    tmem_wait_ld(s[q]);
+                    add(s[q], 32 * q, true);
                 }
-                const uint32_t s_tm = lane_base + buf * kRows;
+            } else {
 #pragma unroll 1
                 for (int q = 0; q < cols; q += 32) {
                     uint32_t s[32];
                     tmem_ld32(s_tm + q, s);
                     tmem_wait_ld(s);
-                    if (q + 32 <= cols && __all_sync(0xffffffffu, lo <= q)) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) sum[i & 3] += ex2(fmaf(__uint_as_float(s[i]), p.c, -lse[q + i]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const bool in = q + i >= lo && q + i < cols;
-                            const float w = ex2(fmaf(__uint_as_float(s[i]), p.c, -lse[q + i]));
-                            sum[i & 3] += in ? w : 0.f;
-                        }
-                    }
+                    add(s, q, q + 32 <= cols && __all_sync(0xffffffffu, lo <= q));
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[x][buf]));
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[x][buf]));
         }
         if (!ok) break;
-        const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float t0, t1, t2, t3;
+        unpack_f2(sum[0], t0, t1);
+        unpack_f2(sum[1], t2, t3);
+        const float total = (t0 + t1) + (t2 + t3);
         if (whole) {
             if (key < it.L && it.entry >= 0) p.acc_out[at] = old + total;
         } else {
@@ -418,29 +479,29 @@ __device__ void w_sum(const WParams &p, const WSched &sc, WBars *bars, uint32_t 
     }
 }
 
-template <int ELEM>
+template <int ELEM, bool ONE>
 __global__ void __launch_bounds__(kWThreads, 1)
     fmha_weights_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const WParams p) {
-    using C = WCfg<ELEM>;
+    using C = WCfg<ELEM, ONE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     WBars *bars = reinterpret_cast<WBars *>(smem + C::OFF_BARS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::NK; ++s) {
-            mbar_init(smem_u32(&bars->k_full[s]), 1);
-            mbar_init(smem_u32(&bars->k_empty[s]), 1);
-        }
-        for (int s = 0; s < C::NQ; ++s) {
-            mbar_init(smem_u32(&bars->q_full[s]), 1);
-            mbar_init(smem_u32(&bars->q_empty[s]), 1);
+        for (int s = 0; s < C::NK + C::NQ; ++s) {
+            mbar_init(smem_u32(&bars->full[s]), 1);
+            mbar_init(smem_u32(&bars->empty[s]), 1);
         }
         for (int x = 0; x < 2; ++x)
             for (int b = 0; b < 2; ++b) {
-                mbar_init(smem_u32(&bars->s_full[x][b]), 1);
+                mbar_init(smem_u32(&bars->s_full[x][b]), 2);     // the MMA and the LSE
                 mbar_init(smem_u32(&bars->s_free[x][b]), 4);
             }
+        for (int s = 0; s < kWItems; ++s) {
+            mbar_init(smem_u32(&bars->item_full[s]), 1);
+            mbar_init(smem_u32(&bars->item_empty[s]), 10);   // all warps but the producer
+        }
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -449,25 +510,29 @@ __global__ void __launch_bounds__(kWThreads, 1)
         tmem_alloc(smem_u32(&bars->tmem_base), 512);
         tmem_relinquish();
     }
+    WCursor cur;
+    int gate = 0;
     if (warp == kWProd) {
         if (lane == 0) {
             prefetch_tmap(&tmQ);
             prefetch_tmap(&tmK);
         }
-        w_schedule(p, &bars->sched, lane);
+        gate = g_test_gate;              // read along with the lengths
+        w_schedule(p, cur, lane);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const WSched sc = bars->sched;
     if (warp < 8) {
-        w_sum(p, sc, bars, tmem, warp, lane);
+        w_sum(p, bars, tmem, warp, lane);
     } else if (warp == kWProd) {
-        if (lane == 0) w_producer<C>(p, sc, &tmQ, &tmK, smem, bars);
-    } else {
-        w_mma<C>(p, sc, smem, bars, tmem);
+        if (lane == 0) w_producer<C>(p, cur, gate, &tmQ, &tmK, smem, bars);
+    } else if (warp == kWMma) {
+        w_mma<C>(p, smem, bars, tmem, lane);
+    } else if (warp == kWLse) {
+        w_load_lse(p, bars, lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -570,14 +635,18 @@ extern "C" int fmha_cache_weights(fmha_tensor q, fmha_tensor k_cache, const floa
     const cuuint32_t bk[4] = {box_d, 1, kRows, 1};
     if (!make_map(&tq, dt, q.data, 3, dq, bq) || !make_map(&tk, dt, k_cache.data, 4, dk, bk, row_promotion(dt))) return FMHA_ERR_CUDA;
 
-    auto kern = dt == FMHA_BF16 ? fmha_weights_kernel<FMHA_BF16>
-                : dt == FMHA_F16 ? fmha_weights_kernel<FMHA_F16> : fmha_weights_kernel<FMHA_E4M3>;
-    const int smem = dt == FMHA_E4M3 ? WCfg<FMHA_E4M3>::SMEM_BYTES : WCfg<FMHA_BF16>::SMEM_BYTES;
+    const bool one = chunks == 1;
+    auto kern = one ? (dt == FMHA_BF16 ? fmha_weights_kernel<FMHA_BF16, true>
+                       : dt == FMHA_F16 ? fmha_weights_kernel<FMHA_F16, true> : fmha_weights_kernel<FMHA_E4M3, true>)
+                    : (dt == FMHA_BF16 ? fmha_weights_kernel<FMHA_BF16, false>
+                       : dt == FMHA_F16 ? fmha_weights_kernel<FMHA_F16, false> : fmha_weights_kernel<FMHA_E4M3, false>);
+    constexpr int smem = WCfg<FMHA_BF16, true>::SMEM_BYTES;      // the same of every kind
+    static_assert(WCfg<FMHA_E4M3, true>::SMEM_BYTES == smem && WCfg<FMHA_E4M3, false>::SMEM_BYTES == smem, "");
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return cuda_failed();
     kern<<<grid, kWThreads, smem, stream>>>(tq, tk, p);
     if (cudaGetLastError() != cudaSuccess) return FMHA_ERR_CUDA;
-    if (chunks > 1) {                    // else no unit is ever cut
+    if (!one) {                          // else no unit is ever cut
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(grid);
         cfg.blockDim = dim3(kUnitKeys);
