@@ -16,12 +16,13 @@
 // more than a few dozen rows by the exponentials (two for each 128 * 2 flops
 // of the tensor core's 8192 a cycle).
 //
-// A unit is 256 keys of one kv head (two MMA tiles that share the query
-// stream) and its query chunks (TB = 128 / G tokens each).  The chunks of all
+// A unit is 512 keys of one kv head (four MMA tiles that share the query
+// stream: with two, a chunk took the 1950 cycles that the SMs together need to
+// fetch theirs from L2) and its query chunks (TB = 128 / G tokens each).  The chunks of all
 // units form one sequence, kv heads fastest, so that a CTA reads the heads'
 // rows of the same keys one after another (they are adjacent in the cache);
 // the sequence is cut evenly over the CTAs; a unit that is cut
-// leaves partial sums (256 floats) in the workspace and a second kernel adds
+// leaves partial sums (a float a key) in the workspace and a second kernel adds
 // them in CTA order, so results do not depend on timing.
 #include "fmha_cache.cuh"
 
@@ -30,9 +31,10 @@ namespace fmha {
 namespace {
 
 constexpr int kWeightsMaxCtas = 152;     // CTAs at most (bounds the workspace)
-constexpr int kUnitKeys = 2 * kRows;
-constexpr int kWThreads = 352;           // 8 summing warps, producer, MMA issuer, LSE loader
-constexpr int kWProd = 8, kWMma = 9, kWLse = 10;
+constexpr int kGroups = 4;               // groups of four summing warps, a key tile of the unit each
+constexpr int kUnitMax = kGroups * kRows;                    // keys of the largest unit
+constexpr int kWProd = 16, kWMma = 17, kWLse = 18;           // then the producer, MMA issuer and LSE loader
+constexpr int kWThreads = 608;
 
 struct WMeta {                           // one partial sum in the workspace
     int64_t row;                         // its unit's first element of acc
@@ -46,9 +48,10 @@ struct WParams {
     float *acc_out;
     const int *seqlen, *batch_idx, *n_query;
     WMeta *meta;                         // [2 * ncta]
-    float *part;                         // [2 * ncta][256]
+    float *part;                         // [2 * ncta][UK]
     int B, Sq, H, H_k, G, B_cache, S_max;
     int TB;                              // query tokens of a chunk
+    int UK;                              // keys of a unit: 512, or 256 where those are too few
     int NMMA;                            // MMA N: TB * G rounded up to 16
     int causal;
     float c;                             // scale * log2(e)
@@ -57,7 +60,7 @@ struct WParams {
 struct WItem {
     int b, g, tile, entry, L, n;         // b < 0: no more items
     int c0, c1;                          // query chunks [c0, c1) of the unit that are this CTA's
-    int nkt;                             // K tiles to load: 2, or 1 at the end of a sequence
+    int nkt;                             // K tiles to load: UK / 128, or fewer at the end of a sequence
     bool begins, ends;                   // the unit's first / last chunk is among them
 };
 
@@ -66,7 +69,8 @@ constexpr int kWStages = 14;             // ring stages at most, K's and Q's tog
 
 struct WBars {
     uint64_t full[kWStages], empty[kWStages];            // K ring, then Q ring
-    uint64_t s_full[2][2], s_free[2][2], drain;          // [key tile][buffer]
+    uint64_t s_full[kGroups], s_free[kGroups], drain;
+    uint64_t lse_full[2], lse_free[2];
     uint64_t item_full[kWItems], item_empty[kWItems];
     WItem item[kWItems];
     uint32_t tmem_base;
@@ -75,14 +79,13 @@ struct WBars {
 };
 
 // Ring stages of 128 rows, 224 KB in all.  Where a sequence's rows fill one
-// chunk (ONE) the stream is K's: 160 KB of it in flight; else it is Q's, 32 KB
-// a chunk from L2, with two stages of which a chunk's load latency was
-// exposed (TODO-FIGURES).
+// chunk (ONE) the stream is K's, 160 KB of it in flight; else it is Q's, 32 KB
+// a chunk (16-bit) from L2.
 template <int ELEM, bool ONE>
 struct WCfg : ElemCfg<ELEM> {
     using B = ElemCfg<ELEM>;
-    static constexpr int NK = (ONE ? 5 : 3) * 32768 / B::TILE_BYTES;
-    static constexpr int NQ = (ONE ? 2 : 4) * 32768 / B::TILE_BYTES;
+    static constexpr int NK = (ONE ? 5 : 4) * 32768 / B::TILE_BYTES;
+    static constexpr int NQ = (ONE ? 2 : 3) * 32768 / B::TILE_BYTES;
     static_assert(NK + NQ <= kWStages, "ring barriers");
     static constexpr int OFF_K = 0;
     static constexpr int OFF_Q = NK * B::TILE_BYTES;
@@ -98,24 +101,27 @@ __device__ __forceinline__ int w_queries(const WParams &p, int b, bool report) {
     return p.n_query ? clamped(p.n_query[b], 0, p.Sq, report) : p.Sq;
 }
 
+// Chunks of a sequence's n rows.
+__device__ __forceinline__ int w_chunks(const WParams &p, int n) { return (n + p.TB - 1) / p.TB; }
+
 // Query t of a sequence sees key j iff j <= t + L - n (causal): the first
 // chunk of unit `tile` that holds a query which sees one of its keys.
 __device__ __forceinline__ int w_first_chunk(const WParams &p, int L, int n, int tile) {
     if (!p.causal) return 0;
-    const int t = tile * kUnitKeys - (L - n);
+    const int t = tile * p.UK - (L - n);
     return t > 0 ? t / p.TB : 0;
 }
 // Chunks of a unit; a sequence without queries still copies acc: one empty chunk.
 __device__ __forceinline__ int w_cost(const WParams &p, int L, int n, int tile) {
-    return imax(1, (n + p.TB - 1) / p.TB - w_first_chunk(p, L, n, tile));
+    return imax(1, w_chunks(p, n) - w_first_chunk(p, L, n, tile));
 }
 // Units [0, *uniform) of one head cost the same; the sum over all of them.
 __device__ __forceinline__ int64_t w_head_cost(const WParams &p, int L, int n, int *uniform) {
-    const int nt = (L + kUnitKeys - 1) / kUnitKeys;
+    const int nt = (L + p.UK - 1) / p.UK;
     int u = nt;
     if (p.causal) {
-        const int64_t x = (int64_t)p.TB - 1 + L - n;         // last key whose tile still starts at chunk 0
-        u = x < 0 ? 0 : imin(nt, (int)(x / kUnitKeys) + 1);
+        const int64_t x = (int64_t)p.TB - 1 + L - n;         // last key whose unit still starts at chunk 0
+        u = x < 0 ? 0 : imin(nt, (int)(x / p.UK) + 1);
     }
     *uniform = u;
     int64_t cost = u > 0 ? (int64_t)u * w_cost(p, L, n, 0) : 0;
@@ -191,7 +197,7 @@ __device__ bool w_next(const WParams &p, WCursor &cur, WItem &it) {
     it.b = -1;
     for (;;) {
         if (cur.b >= p.B || cur.left <= 0) return false;
-        if (cur.tile * kUnitKeys < cur.L) {
+        if (cur.tile * p.UK < cur.L) {
             const int cost = w_cost(p, cur.L, cur.n, cur.tile), fc = w_first_chunk(p, cur.L, cur.n, cur.tile);
             const int take = (int)min((int64_t)(cost - cur.skip), cur.left);
             it.b = cur.b;
@@ -200,11 +206,11 @@ __device__ bool w_next(const WParams &p, WCursor &cur, WItem &it) {
             it.entry = cur.entry;
             it.L = cur.L;
             it.n = cur.n;
-            it.nkt = cur.L - cur.tile * kUnitKeys > kRows ? 2 : 1;
+            it.nkt = imin(p.UK / kRows, (cur.L - cur.tile * p.UK + kRows - 1) / kRows);
             it.begins = cur.skip == 0;
             it.ends = cur.skip + take == cost;
             it.c0 = fc + cur.skip;
-            it.c1 = imin(it.c0 + take, (cur.n + p.TB - 1) / p.TB);   // none without queries
+            it.c1 = imin(it.c0 + take, w_chunks(p, cur.n));          // none without queries
             cur.left -= take;
             cur.skip = 0;
             if (++cur.g == p.H_k) {
@@ -262,7 +268,7 @@ __device__ void w_producer(const WParams &p, WCursor &cur, int gate, const CUten
 #pragma unroll
             for (int pn = 0; pn < C::PANELS; ++pn)
                 tma_load_4d(smem_u32(smem + C::OFF_K + st * C::TILE_BYTES + pn * kPanelBytes), tmK, fb, pn * C::BOX,
-                            it.g, it.tile * kUnitKeys + x * kRows, e);
+                            it.g, it.tile * p.UK + x * kRows, e);
         }
         for (int c = it.c0; ok && c < it.c1; ++c, ++qf) {
             const int st = qf % C::NQ;
@@ -298,48 +304,57 @@ __device__ void w_producer(const WParams &p, WCursor &cur, int gate, const CUten
     }
 }
 
-// S^T of every (chunk, key tile) into that tile's buffer chunk % 2.  A unit of
-// one key tile computes it twice; the second copy is not stored.
+// S^T of every (chunk, key tile): tile x of a unit is group x's.  Tiles past the
+// end of a sequence compute its first one again, and nothing of them is
+// stored.
 template <class C>
 __device__ void w_mma(const WParams &p, uint8_t *smem, WBars *bars, uint32_t tmem_any, int lane) {
     volatile int *abort_flag = &bars->abort;
     uint64_t *k_full = bars->full, *k_empty = bars->empty, *q_full = k_full + C::NK, *q_empty = k_empty + C::NK;
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
     const uint32_t idesc = mma_idesc(C::FMT, p.NMMA, false);
+    const int groups = p.UK / kRows;
     uint32_t kf = 0, qf = 0;             // K tiles and chunks so far
     bool ok = true;
     WItem it;
     for (uint32_t i = 0; ok && w_take(bars, i, it, abort_flag, lane); ++i) {
-        for (int x = 0; ok && x < it.nkt; ++x)
-            ok = warp_wait(smem_u32(&k_full[(kf + x) % C::NK]), ((kf + x) / C::NK) & 1, abort_flag);
+        int landed = 0;                  // K tiles of the unit that are here
         for (int c = it.c0; ok && c < it.c1; ++c, ++qf) {
             const int qst = qf % C::NQ;
-            const uint32_t buf = qf & 1;
             if (!warp_wait(smem_u32(&q_full[qst]), (qf / C::NQ) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
             const uint64_t q = smem_desc(smem_u32(smem + C::OFF_Q + qst * C::TILE_BYTES), 16, 1024);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (!ok || (qf >= 2 && !warp_wait(smem_u32(&bars->s_free[x][buf]), ((qf - 2) >> 1) & 1, abort_flag))) {
-                    ok = false;
-                    continue;
+#pragma unroll 1
+            for (int x = 0; x < groups; ++x) {
+                const uint32_t kt = kf + (x < it.nkt ? x : 0);
+                if (x == landed && x < it.nkt) {
+                    ok = warp_wait(smem_u32(&k_full[kt % C::NK]), (kt / C::NK) & 1, abort_flag);
+                    ++landed;
                 }
+                if (ok && qf > 0) ok = warp_wait(smem_u32(&bars->s_free[x]), (qf - 1) & 1, abort_flag);
+                if (!ok) break;
                 tc_fence_after();
-                const uint64_t k = smem_desc(
-                    smem_u32(smem + C::OFF_K + ((kf + (x < it.nkt ? x : 0)) % C::NK) * C::TILE_BYTES), 16, 1024);
+                const uint64_t k = smem_desc(smem_u32(smem + C::OFF_K + (kt % C::NK) * C::TILE_BYTES), 16, 1024);
 #pragma unroll
                 for (int kk = 0; kk < kD / C::MMA_K; ++kk) {
                     const uint32_t off = (kk * 32 / 128) * kPanelBytes + (kk * 32) % 128;
-                    mma_ss<C::FP8>(tmem + (2 * x + buf) * kRows, k + (off >> 4), q + (off >> 4), idesc, kk > 0 ? 1u : 0u);
+                    mma_ss<C::FP8>(tmem + x * kRows, k + (off >> 4), q + (off >> 4), idesc, kk > 0 ? 1u : 0u);
                 }
-                tc_commit(smem_u32(&bars->s_full[x][buf]));
+                tc_commit(smem_u32(&bars->s_full[x]));
+                // the unit's last use of the tile (tile 0 also stands in for missing ones)
+                if (c == it.c1 - 1 && x < it.nkt && (x > 0 || it.nkt == groups)) tc_commit(smem_u32(&k_empty[kt % C::NK]));
             }
             if (ok) tc_commit(smem_u32(&q_empty[qst]));
         }
+        // without chunks the tiles are still waited for before they are given back
+        for (; ok && landed < it.nkt; ++landed) {
+            ok = warp_wait(smem_u32(&k_full[(kf + landed) % C::NK]), ((kf + landed) / C::NK) & 1, abort_flag);
+            if (ok && (landed > 0 || it.nkt == groups)) tc_commit(smem_u32(&k_empty[(kf + landed) % C::NK]));
+        }
         if (!ok) break;
-        for (int x = 0; x < it.nkt; ++x) tc_commit(smem_u32(&k_empty[(kf + x) % C::NK]));
+        if (it.nkt < groups) tc_commit(smem_u32(&k_empty[kf % C::NK]));
         kf += it.nkt;
     }
     // no tensor-core operation may be in flight when TMEM is released
@@ -348,109 +363,122 @@ __device__ void w_mma(const WParams &p, uint8_t *smem, WBars *bars, uint32_t tme
 }
 
 // One warp: -LSE of every chunk's columns, in log2 units (-inf, weight 0,
-// where the row saw no key), into shared memory; its arrival and the MMA's
-// complete s_full together.  (With the summing threads loading it, a chunk had
-// two barriers of 128 threads: 2500 cycles against TODO-FIGURES.)
+// where the row saw no key), into one of two buffers in shared memory.  (With
+// the summing threads loading it, a chunk had two barriers of 128 threads more.)
 __device__ void w_load_lse(const WParams &p, WBars *bars, int lane) {
     volatile int *abort_flag = &bars->abort;
     uint32_t n = 0;                      // chunks so far
     WItem it;
     for (uint32_t i = 0; w_take(bars, i, it, abort_flag, lane); ++i) {
         const float *lse = p.lse + ((int64_t)it.b * p.H + it.g * p.G) * p.Sq;
-        for (int c = it.c0; c < it.c1; ++c, ++n) {
-            float v[4];
+        float next[4];                   // a chunk's values are fetched before the buffer of the chunk before is free
+        auto fetch = [&](int c) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int r = 32 * k + lane, rt = r / p.G, t = c * p.TB + rt;
-                v[k] = rt < p.TB && t < it.n ? lse[(int64_t)(r - rt * p.G) * p.Sq + t] : -INFINITY;
+                next[k] = rt < p.TB && t < it.n ? lse[(int64_t)(r - rt * p.G) * p.Sq + t] : -INFINITY;
             }
+        };
+        fetch(it.c0);
+        for (int c = it.c0; c < it.c1; ++c, ++n) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = next[k];
+            if (c + 1 < it.c1) fetch(c + 1);
             const uint32_t buf = n & 1;
-            if (n >= 2 && (!warp_wait(smem_u32(&bars->s_free[0][buf]), ((n - 2) >> 1) & 1, abort_flag) ||
-                           !warp_wait(smem_u32(&bars->s_free[1][buf]), ((n - 2) >> 1) & 1, abort_flag)))
-                return;
+            if (n >= 2 && !warp_wait(smem_u32(&bars->lse_free[buf]), ((n - 2) >> 1) & 1, abort_flag)) return;
 #pragma unroll
             for (int k = 0; k < 4; ++k) bars->lse[buf][32 * k + lane] = v[k] == -INFINITY ? -INFINITY : v[k] * -kLog2e;
             __syncwarp();
-            if (lane < 2) mbar_arrive(smem_u32(&bars->s_full[lane][buf]));
+            if (lane == 0) mbar_arrive(smem_u32(&bars->lse_full[buf]));
         }
     }
 }
 
-// Weights: warps 4x .. 4x + 3 own key tile x of every unit, a key a thread.
+// Weights: warps 4 x .. 4 x + 3 own key tile x of every unit, a key a thread.
+// Four warps an SM sub-partition hide one another's latencies (two, with twice
+// the columns in registers, took 1500 cycles for 128 columns of a tile, of
+// which they issued 350).
 __device__ void w_sum(const WParams &p, WBars *bars, uint32_t tmem, int warp, int lane) {
     volatile int *abort_flag = &bars->abort;
-    const int x = warp >> 2, r = (warp & 3) * 32 + lane;
-    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 2 * x * kRows;
+    const int x = warp >> 2, r = warp * 32 + lane;       // key tile, key of the unit
+    const uint32_t s_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + x * kRows;
+    const uint64_t c2 = pack_f2(p.c, p.c);
     uint32_t n = 0;                                      // chunks so far
     int parts = 0;                                       // bit s: slot s of this CTA holds a partial
     WItem it;
     for (uint32_t i = 0; w_take(bars, i, it, abort_flag, lane); ++i) {
-        const int key = it.tile * kUnitKeys + x * kRows + r;
-        const bool whole = it.begins && it.ends;
+        const int key = it.tile * p.UK + r;
+        const bool whole = it.begins && it.ends, mine = key < it.L && it.entry >= 0;
         const int64_t at = ((int64_t)(it.entry < 0 ? 0 : it.entry) * p.H_k + it.g) * p.S_max + key;
-        float old = 0.f;
-        if (whole && p.acc_in && key < it.L && it.entry >= 0) old = p.acc_in[at];
+        const float old = whole && p.acc_in && mine ? p.acc_in[at] : 0.f;
         uint64_t sum[2] = {0, 0};        // two pairs of partial sums
         bool ok = true;
         for (int c = it.c0; c < it.c1; ++c, ++n) {
-            const uint32_t buf = n & 1;
-            const float *lse = bars->lse[buf];
-            if (!warp_wait(smem_u32(&bars->s_full[x][buf]), (n >> 1) & 1, abort_flag)) {
+            const float *lse = bars->lse[n & 1];
+            if (!warp_wait(smem_u32(&bars->lse_full[n & 1]), (n >> 1) & 1, abort_flag) ||
+                !warp_wait(smem_u32(&bars->s_full[x]), n & 1, abort_flag)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const int cols = imin(p.TB, it.n - c * p.TB) * p.G;      // valid columns
+            const int cols = imin(p.TB, it.n - c * p.TB) * p.G;        // valid columns
             // columns below lo are queries that do not see this key
             int lo = 0;
             if (p.causal) {
-                const int t = key - (it.L - it.n) - c * p.TB;        // first token of the chunk that sees it
+                const int t = key - (it.L - it.n) - c * p.TB;           // first token of the chunk that sees it
                 lo = t <= 0 ? 0 : t >= p.TB ? kRows : t * p.G;
             }
-            const uint32_t s_tm = lane_base + buf * kRows;
-            const uint64_t c2 = pack_f2(p.c, p.c);
-            // 32 columns: weights of pairs, with a check of every column where some are not to be counted
-            auto add = [&](const uint32_t (&s)[32], int q, bool all) {
+            // 32 columns: weights of pairs
+            auto add = [&](const uint32_t (&s)[32], int q) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const ulonglong2 nl = *reinterpret_cast<const ulonglong2 *>(lse + q + i);
-                    float w[4];
+                for (int k = 0; k < 32; k += 4) {
+                    const ulonglong2 nl = *reinterpret_cast<const ulonglong2 *>(lse + q + k);
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const uint64_t s2 = pack_f2(__uint_as_float(s[i + 2 * y]), __uint_as_float(s[i + 2 * y + 1]));
-                        unpack_f2(fma_f2(s2, c2, y ? nl.y : nl.x), w[2 * y], w[2 * y + 1]);
+                    for (int z = 0; z < 2; ++z) {
+                        const uint64_t s2 = pack_f2(__uint_as_float(s[k + 2 * z]), __uint_as_float(s[k + 2 * z + 1]));
+                        float a, b;
+                        unpack_f2(fma_f2(s2, c2, z ? nl.y : nl.x), a, b);
+                        sum[z] = add_f2(sum[z], pack_f2(ex2(a), ex2(b)));
                     }
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        w[y] = ex2(w[y]);
-                        if (!all) w[y] = q + i + y >= lo && q + i + y < cols ? w[y] : 0.f;
-                    }
-                    sum[0] = add_f2(sum[0], pack_f2(w[0], w[1]));
-                    sum[1] = add_f2(sum[1], pack_f2(w[2], w[3]));
                 }
             };
             if (cols == kRows && __all_sync(0xffffffffu, lo == 0)) {
-                // the whole tile: all its loads in flight at once
-                uint32_t s[4][32];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld32(s_tm + 32 * q, s[q]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    tmem_wait_ld(s[q]);
-                    add(s[q], 32 * q, true);
+#pragma unroll 1
+                for (int q = 0; q < kRows; q += 64) {
+                    uint32_t s[2][32];
+                    tmem_ld32(s_tm + q, s[0]);
+                    tmem_ld32(s_tm + q + 32, s[1]);
+                    tmem_wait_ld(s[0]);
+                    tmem_wait_ld(s[1]);
+                    add(s[0], q);
+                    add(s[1], q + 32);
                 }
             } else {
 #pragma unroll 1
                 for (int q = 0; q < cols; q += 32) {
+                    // a bit for every column that counts; the others' scores become -inf
+                    const int l = lo - q, h = cols - q;
+                    const uint32_t m = (l <= 0 ? 0xffffffffu : l >= 32 ? 0u : 0xffffffffu << l) &
+                                       (h >= 32 ? 0xffffffffu : (1u << h) - 1u);
+                    if (__all_sync(0xffffffffu, m == 0u)) continue;
                     uint32_t s[32];
                     tmem_ld32(s_tm + q, s);
                     tmem_wait_ld(s);
-                    add(s, q, q + 32 <= cols && __all_sync(0xffffffffu, lo <= q));
+                    if (!__all_sync(0xffffffffu, m == 0xffffffffu)) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (!((m >> k) & 1u)) s[k] = 0xff800000u;
+                    }
+                    add(s, q);
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[x][buf]));
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&bars->s_free[x]));
+                mbar_arrive(smem_u32(&bars->lse_free[n & 1]));
+            }
         }
         if (!ok) break;
         float t0, t1, t2, t3;
@@ -458,15 +486,15 @@ __device__ void w_sum(const WParams &p, WBars *bars, uint32_t tmem, int warp, in
         unpack_f2(sum[1], t2, t3);
         const float total = (t0 + t1) + (t2 + t3);
         if (whole) {
-            if (key < it.L && it.entry >= 0) p.acc_out[at] = old + total;
+            if (mine) p.acc_out[at] = old + total;
         } else {
             const int slot = it.begins ? 1 : 0;
             parts |= 1 << slot;
-            p.part[((int64_t)2 * blockIdx.x + slot) * kUnitKeys + x * kRows + r] = total;
+            p.part[((int64_t)2 * blockIdx.x + slot) * p.UK + r] = total;
             if (threadIdx.x == 0) {
                 WMeta m;
                 m.row = at;
-                m.keys = it.entry < 0 ? 0 : imin(kUnitKeys, it.L - it.tile * kUnitKeys);
+                m.keys = it.entry < 0 ? 0 : imin(p.UK, it.L - it.tile * p.UK);
                 m.last = it.ends;
                 p.meta[2 * blockIdx.x + slot] = m;
             }
@@ -493,14 +521,18 @@ __global__ void __launch_bounds__(kWThreads, 1)
             mbar_init(smem_u32(&bars->full[s]), 1);
             mbar_init(smem_u32(&bars->empty[s]), 1);
         }
-        for (int x = 0; x < 2; ++x)
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(smem_u32(&bars->s_full[x][b]), 2);     // the MMA and the LSE
-                mbar_init(smem_u32(&bars->s_free[x][b]), 4);
-            }
+        for (int x = 0; x < kGroups; ++x) {
+            mbar_init(smem_u32(&bars->s_full[x]), 1);
+            mbar_init(smem_u32(&bars->s_free[x]), 4);
+        }
+        const int summing = p.UK / 32;                       // warps that sum
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&bars->lse_full[b]), 1);
+            mbar_init(smem_u32(&bars->lse_free[b]), summing);
+        }
         for (int s = 0; s < kWItems; ++s) {
             mbar_init(smem_u32(&bars->item_full[s]), 1);
-            mbar_init(smem_u32(&bars->item_empty[s]), 10);   // all warps but the producer
+            mbar_init(smem_u32(&bars->item_empty[s]), summing + 2);
         }
         mbar_init(smem_u32(&bars->drain), 1);
         bars->abort = 0;
@@ -525,8 +557,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp < 8) {
-        w_sum(p, bars, tmem, warp, lane);
+    if (warp < kWProd) {
+        if (warp * 32 < p.UK) w_sum(p, bars, tmem, warp, lane);
     } else if (warp == kWProd) {
         if (lane == 0) w_producer<C>(p, cur, gate, &tmQ, &tmK, smem, bars);
     } else if (warp == kWMma) {
@@ -544,18 +576,23 @@ __global__ void __launch_bounds__(kWThreads, 1)
 }
 
 // CTA c joins the unit that CTA c of the kernel above began and did not end.
-__global__ void __launch_bounds__(kUnitKeys) fmha_weights_join_kernel(const WParams p) {
+__global__ void __launch_bounds__(kUnitMax) fmha_weights_join_kernel(const WParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const WMeta m = p.meta[2 * blockIdx.x + 1];
-    if (m.keys == 0 || (int)threadIdx.x >= m.keys) return;
-    float sum = p.part[((int64_t)2 * blockIdx.x + 1) * kUnitKeys + threadIdx.x];
+    if ((int)threadIdx.x >= m.keys) return;
+    float sum = p.part[((int64_t)2 * blockIdx.x + 1) * p.UK + threadIdx.x];
     for (unsigned c = blockIdx.x + 1, last = m.last; !last && c < gridDim.x; ++c) {
-        const WMeta x = p.meta[2 * c];
-        sum += p.part[(int64_t)2 * c * kUnitKeys + threadIdx.x];
-        last = x.last;
+        sum += p.part[(int64_t)2 * c * p.UK + threadIdx.x];
+        last = p.meta[2 * c].last;
     }
     const int64_t at = m.row + threadIdx.x;
     p.acc_out[at] = (p.acc_in ? p.acc_in[at] : 0.f) + sum;
+}
+
+using WKernel = void (*)(CUtensorMap, CUtensorMap, WParams);
+template <int ELEM>
+WKernel w_kernel(bool one) {
+    return one ? fmha_weights_kernel<ELEM, true> : fmha_weights_kernel<ELEM, false>;
 }
 
 int w_tokens(int Sq, int G) { return imin(kRows / G, Sq); }
@@ -571,7 +608,7 @@ int weights_read_status(int reset) { return cache_read_status(reset); }
 using namespace fmha;
 
 extern "C" size_t fmha_cache_weights_workspace_size(void) {
-    return (size_t)2 * kWeightsMaxCtas * (kUnitKeys * sizeof(float) + sizeof(WMeta));
+    return (size_t)2 * kWeightsMaxCtas * (kUnitMax * sizeof(float) + sizeof(WMeta));
 }
 
 extern "C" int fmha_cache_weights(fmha_tensor q, fmha_tensor k_cache, const float *lse, const float *acc_in,
@@ -622,10 +659,13 @@ extern "C" int fmha_cache_weights(fmha_tensor q, fmha_tensor k_cache, const floa
     p.causal = mask == FMHA_MASK_CAUSAL;
     p.c = scale * kLog2e;
     const int chunks = (Sq + p.TB - 1) / p.TB;
-    const int64_t work = (int64_t)B * H_k * (((int64_t)S_max + kUnitKeys - 1) / kUnitKeys) * chunks;
+    // units of 512 keys, or of half that where they would not fill the SMs
+    const bool one = chunks == 1;
+    p.UK = (int64_t)B * H_k * (((int64_t)S_max + kUnitMax - 1) / kUnitMax) * chunks >= sms ? kUnitMax : kUnitMax / 2;
+    const int64_t work = (int64_t)B * H_k * (((int64_t)S_max + p.UK - 1) / p.UK) * chunks;
     const int grid = (int)(work < imin(sms, kWeightsMaxCtas) ? work : imin(sms, kWeightsMaxCtas));
     p.part = static_cast<float *>(workspace);
-    p.meta = reinterpret_cast<WMeta *>(p.part + (size_t)2 * kWeightsMaxCtas * kUnitKeys);
+    p.meta = reinterpret_cast<WMeta *>(p.part + (size_t)2 * kWeightsMaxCtas * kUnitMax);
 
     CUtensorMap tq, tk;
     const cuuint32_t box_d = dt == FMHA_E4M3 ? 128 : 64;
@@ -635,13 +675,11 @@ extern "C" int fmha_cache_weights(fmha_tensor q, fmha_tensor k_cache, const floa
     const cuuint32_t bk[4] = {box_d, 1, kRows, 1};
     if (!make_map(&tq, dt, q.data, 3, dq, bq) || !make_map(&tk, dt, k_cache.data, 4, dk, bk, row_promotion(dt))) return FMHA_ERR_CUDA;
 
-    const bool one = chunks == 1;
-    auto kern = one ? (dt == FMHA_BF16 ? fmha_weights_kernel<FMHA_BF16, true>
-                       : dt == FMHA_F16 ? fmha_weights_kernel<FMHA_F16, true> : fmha_weights_kernel<FMHA_E4M3, true>)
-                    : (dt == FMHA_BF16 ? fmha_weights_kernel<FMHA_BF16, false>
-                       : dt == FMHA_F16 ? fmha_weights_kernel<FMHA_F16, false> : fmha_weights_kernel<FMHA_E4M3, false>);
-    constexpr int smem = WCfg<FMHA_BF16, true>::SMEM_BYTES;      // the same of every kind
-    static_assert(WCfg<FMHA_E4M3, true>::SMEM_BYTES == smem && WCfg<FMHA_E4M3, false>::SMEM_BYTES == smem, "");
+    auto kern = dt == FMHA_BF16  ? w_kernel<FMHA_BF16>(one)
+                : dt == FMHA_F16 ? w_kernel<FMHA_F16>(one) : w_kernel<FMHA_E4M3>(one);
+    constexpr int smem = WCfg<FMHA_BF16, true>::SMEM_BYTES;      // the same of every kernel
+    static_assert(WCfg<FMHA_BF16, false>::SMEM_BYTES == smem && WCfg<FMHA_E4M3, true>::SMEM_BYTES == smem &&
+                      WCfg<FMHA_E4M3, false>::SMEM_BYTES == smem, "");
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return cuda_failed();
     kern<<<grid, kWThreads, smem, stream>>>(tq, tk, p);
@@ -649,7 +687,7 @@ extern "C" int fmha_cache_weights(fmha_tensor q, fmha_tensor k_cache, const floa
     if (!one) {                          // else no unit is ever cut
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(grid);
-        cfg.blockDim = dim3(kUnitKeys);
+        cfg.blockDim = dim3(p.UK);
         cfg.stream = stream;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -91,6 +91,9 @@ W_CASES = {
     "no_queries": dict(dtype="bf16", Sq=5, H=4, H_k=2, S_max=600, seqlen=[600, 300], n_query=[0, 5]),
     "long": dict(dtype="bf16", Sq=150, H=8, H_k=1, S_max=9000, seqlen=[8999], mask="causal"),
     "odd_group": dict(dtype="bf16", Sq=50, H=21, H_k=3, S_max=400, seqlen=[400, 50], mask="causal"),
+    "many_odd": dict(dtype="e4m3", Sq=333, H=20, H_k=2, S_max=1400, seqlen=[1400, 333, 700, 129], n_query=[333, 331, 40, 0],
+                     mask="causal"),
+    "many_no_mask": dict(dtype="f16", Sq=260, H=8, H_k=2, S_max=700, seqlen=[641, 0, 513], n_query=[260, 7, 259]),
     "batch": dict(dtype="bf16", Sq=2, H=8, H_k=2, S_max=500, seqlen=[(i * 41) % 501 for i in range(70)]),
 }
 
