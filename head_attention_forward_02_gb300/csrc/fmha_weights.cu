@@ -33,8 +33,8 @@ namespace {
 constexpr int kWeightsMaxCtas = 152;     // CTAs at most (bounds the workspace)
 constexpr int kGroups = 4;               // groups of four summing warps, a key tile of the unit each
 constexpr int kUnitMax = kGroups * kRows;                    // keys of the largest unit
-constexpr int kWProd = 16, kWMma = 17, kWLse = 18;           // then the producer, MMA issuer and LSE loader
-constexpr int kWThreads = 608;
+constexpr int kWProd = 16, kWLse = 17, kWMma = 18;           // then the producer, LSE loader and two MMA issuers
+constexpr int kWThreads = 640;
 
 struct WMeta {                           // one partial sum in the workspace
     int64_t row;                         // its unit's first element of acc
@@ -69,7 +69,7 @@ constexpr int kWStages = 14;             // ring stages at most, K's and Q's tog
 
 struct WBars {
     uint64_t full[kWStages], empty[kWStages];            // K ring, then Q ring
-    uint64_t s_full[kGroups], s_free[kGroups], drain;
+    uint64_t s_full[kGroups], s_free[kGroups], drain[2];
     uint64_t lse_full[2], lse_free[2];
     uint64_t item_full[kWItems], item_empty[kWItems];
     WItem item[kWItems];
@@ -304,17 +304,18 @@ __device__ void w_producer(const WParams &p, WCursor &cur, int gate, const CUten
     }
 }
 
-// S^T of every (chunk, key tile): tile x of a unit is group x's.  Tiles past the
-// end of a sequence compute its first one again, and nothing of them is
-// stored.
+// S^T of every (chunk, key tile): tile x of a unit is group x's, and issuer x % 2
+// issues it, so that one issuer's waits pass under the other's MMAs (with one,
+// a tile took 900 cycles for 512 of MMAs).  Both wait for every K tile and
+// give it back, so that neither misses a phase of its barrier.
 template <class C>
-__device__ void w_mma(const WParams &p, uint8_t *smem, WBars *bars, uint32_t tmem_any, int lane) {
+__device__ void w_mma(const WParams &p, uint8_t *smem, WBars *bars, uint32_t tmem_any, int who, int lane) {
     volatile int *abort_flag = &bars->abort;
     uint64_t *k_full = bars->full, *k_empty = bars->empty, *q_full = k_full + C::NK, *q_empty = k_empty + C::NK;
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
     const uint32_t idesc = mma_idesc(C::FMT, p.NMMA, false);
-    const int groups = p.UK / kRows;
     uint32_t kf = 0, qf = 0;             // K tiles and chunks so far
+    uint32_t cnt[2] = {0, 0};            // of groups who and who + 2: their chunks
     bool ok = true;
     WItem it;
     for (uint32_t i = 0; ok && w_take(bars, i, it, abort_flag, lane); ++i) {
@@ -326,40 +327,39 @@ __device__ void w_mma(const WParams &p, uint8_t *smem, WBars *bars, uint32_t tme
                 break;
             }
             const uint64_t q = smem_desc(smem_u32(smem + C::OFF_Q + qst * C::TILE_BYTES), 16, 1024);
-#pragma unroll 1
-            for (int x = 0; x < groups; ++x) {
-                const uint32_t kt = kf + (x < it.nkt ? x : 0);
-                if (x == landed && x < it.nkt) {
-                    ok = warp_wait(smem_u32(&k_full[kt % C::NK]), (kt / C::NK) & 1, abort_flag);
-                    ++landed;
-                }
-                if (ok && qf > 0) ok = warp_wait(smem_u32(&bars->s_free[x]), (qf - 1) & 1, abort_flag);
-                if (!ok) break;
+#pragma unroll
+            for (int y = 0; y < kGroups / 2; ++y) {
+                const int x = who + 2 * y;
+                if (!ok || x >= it.nkt) continue;
+                for (; ok && landed <= x; ++landed)
+                    ok = warp_wait(smem_u32(&k_full[(kf + landed) % C::NK]), ((kf + landed) / C::NK) & 1, abort_flag);
+                if (ok && cnt[y] > 0) ok = warp_wait(smem_u32(&bars->s_free[x]), (cnt[y] - 1) & 1, abort_flag);
+                if (!ok) continue;
+                ++cnt[y];
                 tc_fence_after();
-                const uint64_t k = smem_desc(smem_u32(smem + C::OFF_K + (kt % C::NK) * C::TILE_BYTES), 16, 1024);
+                const int st = (kf + x) % C::NK;
+                const uint64_t k = smem_desc(smem_u32(smem + C::OFF_K + st * C::TILE_BYTES), 16, 1024);
 #pragma unroll
                 for (int kk = 0; kk < kD / C::MMA_K; ++kk) {
                     const uint32_t off = (kk * 32 / 128) * kPanelBytes + (kk * 32) % 128;
                     mma_ss<C::FP8>(tmem + x * kRows, k + (off >> 4), q + (off >> 4), idesc, kk > 0 ? 1u : 0u);
                 }
                 tc_commit(smem_u32(&bars->s_full[x]));
-                // the unit's last use of the tile (tile 0 also stands in for missing ones)
-                if (c == it.c1 - 1 && x < it.nkt && (x > 0 || it.nkt == groups)) tc_commit(smem_u32(&k_empty[kt % C::NK]));
+                if (c == it.c1 - 1) tc_commit(smem_u32(&k_empty[st]));       // the unit's last use of it
             }
             if (ok) tc_commit(smem_u32(&q_empty[qst]));
         }
-        // without chunks the tiles are still waited for before they are given back
-        for (; ok && landed < it.nkt; ++landed) {
+        for (; ok && landed < it.nkt; ++landed)
             ok = warp_wait(smem_u32(&k_full[(kf + landed) % C::NK]), ((kf + landed) / C::NK) & 1, abort_flag);
-            if (ok && (landed > 0 || it.nkt == groups)) tc_commit(smem_u32(&k_empty[(kf + landed) % C::NK]));
-        }
         if (!ok) break;
-        if (it.nkt < groups) tc_commit(smem_u32(&k_empty[kf % C::NK]));
+        // the other issuer's tiles, and all of them where there is no chunk
+        for (int x = 0; x < it.nkt; ++x)
+            if (lane == 0 && ((x & 1) != who || it.c0 >= it.c1)) mbar_arrive(smem_u32(&k_empty[(kf + x) % C::NK]));
         kf += it.nkt;
     }
     // no tensor-core operation may be in flight when TMEM is released
-    tc_commit(smem_u32(&bars->drain));
-    mbar_wait_drain(smem_u32(&bars->drain), 0);
+    tc_commit(smem_u32(&bars->drain[who]));
+    mbar_wait_drain(smem_u32(&bars->drain[who]), 0);
 }
 
 // One warp: -LSE of every chunk's columns, in log2 units (-inf, weight 0,
@@ -404,7 +404,7 @@ __device__ void w_sum(const WParams &p, WBars *bars, uint32_t tmem, int warp, in
     const int x = warp >> 2, r = warp * 32 + lane;       // key tile, key of the unit
     const uint32_t s_tm = tmem + ((uint32_t)((warp & 3) * 32) << 16) + x * kRows;
     const uint64_t c2 = pack_f2(p.c, p.c);
-    uint32_t n = 0;                                      // chunks so far
+    uint32_t n = 0, m = 0;                               // chunks so far, and those of this group's tiles
     int parts = 0;                                       // bit s: slot s of this CTA holds a partial
     WItem it;
     for (uint32_t i = 0; w_take(bars, i, it, abort_flag, lane); ++i) {
@@ -417,9 +417,13 @@ __device__ void w_sum(const WParams &p, WBars *bars, uint32_t tmem, int warp, in
         for (int c = it.c0; c < it.c1; ++c, ++n) {
             const float *lse = bars->lse[n & 1];
             if (!warp_wait(smem_u32(&bars->lse_full[n & 1]), (n >> 1) & 1, abort_flag) ||
-                !warp_wait(smem_u32(&bars->s_full[x]), n & 1, abort_flag)) {
+                (x < it.nkt && !warp_wait(smem_u32(&bars->s_full[x]), m++ & 1, abort_flag))) {
                 ok = false;
                 break;
+            }
+            if (x >= it.nkt) {           // no tile at the end of a sequence
+                if (lane == 0) mbar_arrive(smem_u32(&bars->lse_free[n & 1]));
+                continue;
             }
             tc_fence_after();
             const int cols = imin(p.TB, it.n - c * p.TB) * p.G;        // valid columns
@@ -443,6 +447,12 @@ __device__ void w_sum(const WParams &p, WBars *bars, uint32_t tmem, int warp, in
                     }
                 }
             };
+            // S^T is in registers: the next chunk's may come
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[x]));
+            };
             if (cols == kRows && __all_sync(0xffffffffu, lo == 0)) {
 #pragma unroll 1
                 for (int q = 0; q < kRows; q += 64) {
@@ -451,6 +461,7 @@ __device__ void w_sum(const WParams &p, WBars *bars, uint32_t tmem, int warp, in
                     tmem_ld32(s_tm + q + 32, s[1]);
                     tmem_wait_ld(s[0]);
                     tmem_wait_ld(s[1]);
+                    if (q > 0) release();
                     add(s[0], q);
                     add(s[1], q + 32);
                 }
@@ -472,13 +483,10 @@ __device__ void w_sum(const WParams &p, WBars *bars, uint32_t tmem, int warp, in
                     }
                     add(s, q);
                 }
+                release();
             }
-            tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_u32(&bars->s_free[x]));
-                mbar_arrive(smem_u32(&bars->lse_free[n & 1]));
-            }
+            if (lane == 0) mbar_arrive(smem_u32(&bars->lse_free[n & 1]));
         }
         if (!ok) break;
         float t0, t1, t2, t3;
@@ -519,7 +527,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::NK + C::NQ; ++s) {
             mbar_init(smem_u32(&bars->full[s]), 1);
-            mbar_init(smem_u32(&bars->empty[s]), 1);
+            mbar_init(smem_u32(&bars->empty[s]), 2);         // both issuers
         }
         for (int x = 0; x < kGroups; ++x) {
             mbar_init(smem_u32(&bars->s_full[x]), 1);
@@ -532,9 +540,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
         }
         for (int s = 0; s < kWItems; ++s) {
             mbar_init(smem_u32(&bars->item_full[s]), 1);
-            mbar_init(smem_u32(&bars->item_empty[s]), summing + 2);
+            mbar_init(smem_u32(&bars->item_empty[s]), summing + 3);
         }
-        mbar_init(smem_u32(&bars->drain), 1);
+        mbar_init(smem_u32(&bars->drain[0]), 1);
+        mbar_init(smem_u32(&bars->drain[1]), 1);
         bars->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -561,10 +570,10 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (warp * 32 < p.UK) w_sum(p, bars, tmem, warp, lane);
     } else if (warp == kWProd) {
         if (lane == 0) w_producer<C>(p, cur, gate, &tmQ, &tmK, smem, bars);
-    } else if (warp == kWMma) {
-        w_mma<C>(p, smem, bars, tmem, lane);
     } else if (warp == kWLse) {
         w_load_lse(p, bars, lane);
+    } else {
+        w_mma<C>(p, smem, bars, tmem, warp - kWMma, lane);
     }
     tc_fence_before();
     __syncthreads();
