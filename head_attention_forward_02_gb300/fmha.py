@@ -8,6 +8,7 @@ fallback of any kind.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -340,28 +341,54 @@ def fmha_tree_commit(k_cache, v_cache, k_new, v_new, B, T, P, H_k, D, B_cache, S
                                   _ptr(path), _ptr(n_accept), _stream(stream))
 
 
-def _check(name: str, t, shape, dtype, device) -> None:
+# The operators below are called once a layer and token, where a call's Python
+# steps outlast its kernels: every tensor is looked at once, and the C function
+# is called directly (tree_fwd: 41 -> TODO us to enqueue).
+
+def _check(name: str, t, shape: tuple, dtype, index: int) -> None:
     """Refuse a tensor that the library would misread: it takes only an address."""
-    if t is None:
+    if t is None or (t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
         return
-    if t.device != device or t.device.type != "cuda":
-        raise ValueError(f"{name} is on {t.device}, not on the CUDA device of the call ({device})")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on the call's device cuda:{index}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} is not contiguous")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    raise ValueError(f"{name} is not contiguous")
 
 
-def _stream_on(stream, device) -> int:
+def _device_and_code(t: torch.Tensor) -> Tuple[int, int]:
+    """CUDA device index and element type code of a call's first tensor."""
+    index, code = t.get_device(), _TORCH_DTYPE.get(t.dtype)
+    if index < 0:
+        raise ValueError(f"the tensors are on {t.device}, not on a CUDA device")
+    if code is None:
+        raise FmhaError(ERR_UNSUPPORTED, f"dtype {t.dtype}: {status_string(ERR_UNSUPPORTED)}")
+    return index, code
+
+
+def _raw_stream(stream, index: int) -> Optional[int]:
     """The stream to launch on: torch's current one of the tensors' device."""
-    return _stream(torch.cuda.current_stream(device) if stream is None else stream)
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+
+
+def _workspace(workspace, nbytes: int, device) -> Tuple[int, int]:
+    if workspace is None:
+        workspace = torch.empty(nbytes or 1, dtype=torch.uint8, device=device)
+    elif workspace.device != device:
+        raise ValueError(f"workspace is on {workspace.device}, not on {device}")
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace is not contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _raise(rc: int) -> None:
     if rc != OK:
         raise FmhaError(rc, status_string(rc))
+
+
+_tree_workspace_size = functools.lru_cache(maxsize=256)(fmha_tree_workspace_size)
 
 
 def tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -378,40 +405,43 @@ def tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_ne
     row sees draft column (None: a chain).  Allocates O, LSE [B, H, T] and the
     workspace with torch when not given; rows of drafts at or past n_draft[b]
     are not written.  Returns (O, LSE)."""
+    index, code = _device_and_code(q)
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return tree_fwd(q, k_cache, v_cache, k_new, v_new, seqlen, tree_mask=tree_mask, n_draft=n_draft,
+                            batch_idx=batch_idx, scale=scale, out_scale=out_scale, out=out, lse=lse,
+                            return_lse=return_lse, workspace=workspace, stream=stream)
     if q.dim() != 4 or k_cache.dim() != 4:
         raise ValueError("q is [B, T, H, 128] and the caches are [B_cache, S_max, H_k, 128]")
-    B, T, H, D = q.shape
-    B_cache, S_max, H_k = k_cache.shape[0], k_cache.shape[1], k_cache.shape[2]
-    dev = q.device
-    if q.dtype not in _TORCH_DTYPE:
-        raise FmhaError(ERR_UNSUPPORTED, status_string(ERR_UNSUPPORTED))
-    _check("q", q, q.shape, q.dtype, dev)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check(name, t, (B_cache, S_max, H_k, D), q.dtype, dev)
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        _check(name, t, (B, T, H_k, D), q.dtype, dev)
-    for name, t in (("seqlen", seqlen), ("n_draft", n_draft), ("batch_idx", batch_idx)):
-        _check(name, t, (B,), torch.int32, dev)
+    (B, T, H, D), (B_cache, S_max, H_k, _) = q.shape, k_cache.shape
+    dt, cache, new, per_seq = q.dtype, (B_cache, S_max, H_k, D), (B, T, H_k, D), (B,)
+    _check("q", q, (B, T, H, D), dt, index)
+    _check("k_cache", k_cache, cache, dt, index)
+    _check("v_cache", v_cache, cache, dt, index)
+    _check("k_new", k_new, new, dt, index)
+    _check("v_new", v_new, new, dt, index)
+    _check("seqlen", seqlen, per_seq, torch.int32, index)
+    _check("n_draft", n_draft, per_seq, torch.int32, index)
+    _check("batch_idx", batch_idx, per_seq, torch.int32, index)
     stride = 0
     if tree_mask is not None:
-        _check("tree_mask", tree_mask, (T, T) if tree_mask.dim() == 2 else (B, T, T), (torch.bool, torch.uint8), dev)
+        if tree_mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError(f"tree_mask has dtype {tree_mask.dtype}, not bool or uint8")
         stride = 0 if tree_mask.dim() == 2 else T * T
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and return_lse:
-            lse = torch.empty((B, H, T), dtype=torch.float32, device=dev)
-        _check("out", out, q.shape, q.dtype, dev)
-        _check("lse", lse, (B, H, T), torch.float32, dev)
-        nbytes = fmha_tree_workspace_size(B, T, H, H_k, D, S_max)
-        if workspace is None:
-            workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-        elif workspace.device != dev:
-            raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
-        _raise(fmha_tree_fwd(q, k_cache, v_cache, k_new, v_new, out, lse, B, T, H, H_k, D, B_cache, S_max, seqlen,
-                             batch_idx, n_draft, tree_mask, stride, 1.0 / math.sqrt(D) if scale is None else scale,
-                             out_scale, workspace, workspace.numel() * workspace.element_size(),
-                             _stream_on(stream, dev)))
+        _check("tree_mask", tree_mask, (T, T) if tree_mask.dim() == 2 else (B, T, T), tree_mask.dtype, index)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and return_lse:
+        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
+    _check("out", out, (B, T, H, D), dt, index)
+    _check("lse", lse, (B, H, T), torch.float32, index)
+    ws, nbytes = _workspace(workspace, _tree_workspace_size(B, T, H, H_k, D, S_max), q.device)
+    _raise(lib().fmha_tree_fwd(
+        fmha_tensor(q.data_ptr(), code), fmha_tensor(k_cache.data_ptr(), code), fmha_tensor(v_cache.data_ptr(), code),
+        fmha_tensor(k_new.data_ptr(), code), fmha_tensor(v_new.data_ptr(), code), fmha_tensor(out.data_ptr(), code),
+        _ptr(lse), B, T, H, H_k, D, B_cache, S_max, seqlen.data_ptr(), _ptr(batch_idx), _ptr(n_draft),
+        _ptr(tree_mask), stride, 1.0 / math.sqrt(D) if scale is None else scale, out_scale, ws.data_ptr(), nbytes,
+        _raw_stream(stream, index)))
     return out, lse
 
 
@@ -422,23 +452,27 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, k_new: torch.Tenso
     path[b, i], i < n_accept[b], of k_new / v_new [B, T, H_k, 128] become rows
     seqlen[b] + i of sequence b's entry.  path int32 [B, P]; n_accept, seqlen,
     batch_idx int32 [B].  seqlen is not changed."""
+    index, code = _device_and_code(k_cache)
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return tree_commit(k_cache, v_cache, k_new, v_new, seqlen, path, n_accept, batch_idx=batch_idx,
+                               stream=stream)
     if k_cache.dim() != 4 or k_new.dim() != 4 or path.dim() != 2:
         raise ValueError("the caches are [B_cache, S_max, H_k, 128], k_new is [B, T, H_k, 128] and path is [B, P]")
-    B_cache, S_max, H_k, D = k_cache.shape
-    B, T, P = k_new.shape[0], k_new.shape[1], path.shape[1]
-    dev = k_cache.device
-    if k_cache.dtype not in _TORCH_DTYPE:
-        raise FmhaError(ERR_UNSUPPORTED, status_string(ERR_UNSUPPORTED))
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check(name, t, (B_cache, S_max, H_k, D), k_cache.dtype, dev)
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        _check(name, t, (B, T, H_k, D), k_cache.dtype, dev)
-    _check("path", path, (B, P), torch.int32, dev)
-    for name, t in (("seqlen", seqlen), ("n_accept", n_accept), ("batch_idx", batch_idx)):
-        _check(name, t, (B,), torch.int32, dev)
-    with torch.cuda.device(dev):
-        _raise(fmha_tree_commit(k_cache, v_cache, k_new, v_new, B, T, P, H_k, D, B_cache, S_max, seqlen, batch_idx,
-                                path, n_accept, _stream_on(stream, dev)))
+    (B_cache, S_max, H_k, D), (B, T, _, _), P = k_cache.shape, k_new.shape, path.shape[1]
+    dt, cache, new, per_seq = k_cache.dtype, (B_cache, S_max, H_k, D), (B, T, H_k, D), (B,)
+    _check("k_cache", k_cache, cache, dt, index)
+    _check("v_cache", v_cache, cache, dt, index)
+    _check("k_new", k_new, new, dt, index)
+    _check("v_new", v_new, new, dt, index)
+    _check("path", path, (B, P), torch.int32, index)
+    _check("seqlen", seqlen, per_seq, torch.int32, index)
+    _check("n_accept", n_accept, per_seq, torch.int32, index)
+    _check("batch_idx", batch_idx, per_seq, torch.int32, index)
+    _raise(lib().fmha_tree_commit(
+        fmha_tensor(k_cache.data_ptr(), code), fmha_tensor(v_cache.data_ptr(), code),
+        fmha_tensor(k_new.data_ptr(), code), fmha_tensor(v_new.data_ptr(), code), B, T, P, H_k, D, B_cache, S_max,
+        seqlen.data_ptr(), _ptr(batch_idx), path.data_ptr(), n_accept.data_ptr(), _raw_stream(stream, index)))
 
 
 def fmha_cache_weights(q, k_cache, lse, acc_in, acc_out, B, Sq, H, H_k, D, B_cache, S_max, seqlen, batch_idx, n_query,
@@ -463,6 +497,9 @@ def fmha_cache_evict(k_cache, v_cache, acc, k_out, v_out, acc_out, B, H_k, D, B_
         int(budget), int(recent), _ptr(kept), _ptr(new_seqlen), _stream(stream))
 
 
+_weights_workspace_size = functools.lru_cache(maxsize=1)(fmha_cache_weights_workspace_size)
+
+
 def cache_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor, seqlen: torch.Tensor, *,
                   acc: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                   n_query: Optional[torch.Tensor] = None, batch_idx: Optional[torch.Tensor] = None,
@@ -476,35 +513,35 @@ def cache_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor, seq
     it; acc float [B_cache, H_k, S_max], None: start from nothing; mask "none"
     or "causal" (q-end).  Updates acc in place unless ``out`` is given; with
     neither, returns a new array that is zero past every length."""
+    index, code = _device_and_code(q)
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return cache_weights(q, k_cache, lse, seqlen, acc=acc, out=out, n_query=n_query, batch_idx=batch_idx,
+                                 mask=mask, scale=scale, workspace=workspace, stream=stream)
     if q.dim() == 3:
         q, lse = q.unsqueeze(1), lse.unsqueeze(-1)
     if q.dim() != 4 or k_cache.dim() != 4:
         raise ValueError("q is [B, Sq, H, 128] or [B, H, 128] and the cache is [B_cache, S_max, H_k, 128]")
     if mask not in ("none", "causal"):
         raise ValueError(f"mask is none or causal, not {mask!r}")
-    B, Sq, H, D = q.shape
-    B_cache, S_max, H_k = k_cache.shape[0], k_cache.shape[1], k_cache.shape[2]
-    dev = q.device
-    if q.dtype not in _TORCH_DTYPE:
-        raise FmhaError(ERR_UNSUPPORTED, status_string(ERR_UNSUPPORTED))
-    _check("q", q, q.shape, q.dtype, dev)
-    _check("k_cache", k_cache, (B_cache, S_max, H_k, D), q.dtype, dev)
-    _check("lse", lse, (B, H, Sq), torch.float32, dev)
-    for name, t in (("seqlen", seqlen), ("n_query", n_query), ("batch_idx", batch_idx)):
-        _check(name, t, (B,), torch.int32, dev)
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.zeros((B_cache, H_k, S_max), dtype=torch.float32, device=dev) if acc is None else acc
-        for name, t in (("acc", acc), ("out", out)):
-            _check(name, t, (B_cache, H_k, S_max), torch.float32, dev)
-        nbytes = fmha_cache_weights_workspace_size()
-        if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        elif workspace.device != dev:
-            raise ValueError(f"workspace is on {workspace.device}, not on {dev}")
-        _raise(fmha_cache_weights(q, k_cache, lse, acc, out, B, Sq, H, H_k, D, B_cache, S_max, seqlen, batch_idx,
-                                  n_query, 1.0 / math.sqrt(D) if scale is None else scale, _MASKS[mask], workspace,
-                                  workspace.numel() * workspace.element_size(), _stream_on(stream, dev)))
+    (B, Sq, H, D), (B_cache, S_max, H_k, _) = q.shape, k_cache.shape
+    dt, scores, per_seq = q.dtype, (B_cache, H_k, S_max), (B,)
+    _check("q", q, (B, Sq, H, D), dt, index)
+    _check("k_cache", k_cache, (B_cache, S_max, H_k, D), dt, index)
+    _check("lse", lse, (B, H, Sq), torch.float32, index)
+    _check("seqlen", seqlen, per_seq, torch.int32, index)
+    _check("n_query", n_query, per_seq, torch.int32, index)
+    _check("batch_idx", batch_idx, per_seq, torch.int32, index)
+    if out is None:
+        out = torch.zeros(scores, dtype=torch.float32, device=q.device) if acc is None else acc
+    _check("acc", acc, scores, torch.float32, index)
+    _check("out", out, scores, torch.float32, index)
+    ws, nbytes = _workspace(workspace, _weights_workspace_size(), q.device)
+    _raise(lib().fmha_cache_weights(
+        fmha_tensor(q.data_ptr(), code), fmha_tensor(k_cache.data_ptr(), code), lse.data_ptr(), _ptr(acc),
+        out.data_ptr(), B, Sq, H, H_k, D, B_cache, S_max, seqlen.data_ptr(), _ptr(batch_idx), _ptr(n_query),
+        1.0 / math.sqrt(D) if scale is None else scale, _MASKS[mask], ws.data_ptr(), nbytes,
+        _raw_stream(stream, index)))
     return out
 
 
@@ -519,37 +556,41 @@ def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor,
     S_max], seqlen int32 [B].  In place unless k_out / v_out [B_out, S_out,
     H_k, 128] and acc_out [B_out, H_k, S_out] are given (out_idx: their
     entries).  Returns (kept int32 [B, H_k, budget], new_seqlen int32 [B])."""
-    if k_cache.dim() != 4:
-        raise ValueError("the caches are [B_cache, S_max, H_k, 128]")
-    outs = (k_out, v_out, acc_out)
-    if any(t is None for t in outs) and any(t is not None for t in outs + (out_idx,)):
+    index, code = _device_and_code(k_cache)
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return cache_evict(k_cache, v_cache, acc, seqlen, budget, recent=recent, batch_idx=batch_idx, k_out=k_out,
+                               v_out=v_out, acc_out=acc_out, out_idx=out_idx, kept=kept, new_seqlen=new_seqlen,
+                               stream=stream)
+    given = (k_out is not None) + (v_out is not None) + (acc_out is not None)
+    if given not in (0, 3) or (given == 0 and out_idx is not None):
         raise ValueError("k_out, v_out and acc_out come together, and out_idx only with them")
-    if k_out is None:
+    if given == 0:
         k_out, v_out, acc_out, out_idx = k_cache, v_cache, acc, batch_idx
-    B_cache, S_max, H_k, D = k_cache.shape
-    if k_out.dim() != 4:
-        raise ValueError("the output caches are [B_out, S_out, H_k, 128]")
-    B, B_out, S_out = seqlen.shape[0], k_out.shape[0], k_out.shape[1]
-    dev = k_cache.device
-    if k_cache.dtype not in _TORCH_DTYPE:
-        raise FmhaError(ERR_UNSUPPORTED, status_string(ERR_UNSUPPORTED))
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _check(name, t, (B_cache, S_max, H_k, D), k_cache.dtype, dev)
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        _check(name, t, (B_out, S_out, H_k, D), k_cache.dtype, dev)
-    _check("acc", acc, (B_cache, H_k, S_max), torch.float32, dev)
-    _check("acc_out", acc_out, (B_out, H_k, S_out), torch.float32, dev)
-    for name, t in (("seqlen", seqlen), ("batch_idx", batch_idx), ("out_idx", out_idx), ("new_seqlen", new_seqlen)):
-        _check(name, t, (B,), torch.int32, dev)
-    _check("kept", kept, (B, H_k, budget), torch.int32, dev)
-    with torch.cuda.device(dev):
-        if kept is None:
-            kept = torch.empty((B, H_k, max(budget, 0)), dtype=torch.int32, device=dev)
-        if new_seqlen is None:
-            new_seqlen = torch.empty((B,), dtype=torch.int32, device=dev)
-        _raise(fmha_cache_evict(k_cache, v_cache, acc, k_out, v_out, acc_out, B, H_k, D, B_cache, S_max, B_out, S_out,
-                                seqlen, batch_idx, out_idx, budget, recent, kept, new_seqlen,
-                                _stream_on(stream, dev)))
+    if k_cache.dim() != 4 or k_out.dim() != 4 or seqlen.dim() != 1:
+        raise ValueError("the caches are [B_cache, S_max, H_k, 128] and seqlen is [B]")
+    (B_cache, S_max, H_k, D), (B_out, S_out), B = k_cache.shape, k_out.shape[:2], seqlen.shape[0]
+    dt, cache, moved, per_seq = k_cache.dtype, (B_cache, S_max, H_k, D), (B_out, S_out, H_k, D), (B,)
+    if kept is None:
+        kept = torch.empty((B, H_k, max(budget, 0)), dtype=torch.int32, device=k_cache.device)
+    if new_seqlen is None:
+        new_seqlen = torch.empty(per_seq, dtype=torch.int32, device=k_cache.device)
+    _check("k_cache", k_cache, cache, dt, index)
+    _check("v_cache", v_cache, cache, dt, index)
+    _check("acc", acc, (B_cache, H_k, S_max), torch.float32, index)
+    _check("k_out", k_out, moved, dt, index)
+    _check("v_out", v_out, moved, dt, index)
+    _check("acc_out", acc_out, (B_out, H_k, S_out), torch.float32, index)
+    _check("seqlen", seqlen, per_seq, torch.int32, index)
+    _check("batch_idx", batch_idx, per_seq, torch.int32, index)
+    _check("out_idx", out_idx, per_seq, torch.int32, index)
+    _check("new_seqlen", new_seqlen, per_seq, torch.int32, index)
+    _check("kept", kept, (B, H_k, max(budget, 0)), torch.int32, index)
+    _raise(lib().fmha_cache_evict(
+        fmha_tensor(k_cache.data_ptr(), code), fmha_tensor(v_cache.data_ptr(), code), acc.data_ptr(),
+        fmha_tensor(k_out.data_ptr(), code), fmha_tensor(v_out.data_ptr(), code), acc_out.data_ptr(), B, H_k, D,
+        B_cache, S_max, B_out, S_out, seqlen.data_ptr(), _ptr(batch_idx), _ptr(out_idx), budget, recent,
+        kept.data_ptr(), new_seqlen.data_ptr(), _raw_stream(stream, index)))
     return kept, new_seqlen
 
 
