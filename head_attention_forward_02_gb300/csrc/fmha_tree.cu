@@ -65,6 +65,9 @@ struct TreeCfg : ElemCfg<ELEM> {
     static constexpr int OFF_STAT = OFF_BARS + 1024;          // SPLIT: (m, l) of group 1's rows
     static constexpr int SMEM_BYTES = OFF_STAT + kRows * 8 + 1024;   // 1 KB alignment
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+    // log2 of the largest P right after the reference is set; up to 2^8 later.
+    // e4m3 underflows 2^9 below 1, so its weights start 2^4 up.
+    static constexpr float BIAS = B::FP8 ? 4.f : 0.f;
     // TMEM: S of each group, P over S, then O of each group
     static constexpr int O_COL = 2 * kRows;
 };
@@ -557,8 +560,9 @@ __device__ void tree_softmax(const TreeParams &p, uint8_t *smem, TreeBars *bars,
             if (__any_sync(0xffffffffu, need)) {
                 float alpha = 1.f;
                 if (need) {
-                    alpha = m == -INFINITY ? 0.f : ex2(m - tmax);
-                    m = tmax;
+                    const float ref = tmax - C::BIAS;
+                    alpha = m == -INFINITY ? 0.f : ex2(m - ref);
+                    m = ref;
                     l *= alpha;
                 }
                 if (t > tb) {
