@@ -536,12 +536,12 @@ __device__ void tree_softmax(const TreeParams &p, uint8_t *smem, TreeBars *bars,
             uint32_t s[4][32];
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_ld32(s_tm + 32 * q, s[q]);
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                tmem_wait_ld(s[q]);
-                if (drafts || nk < kRows) {
-                    // a bit per key: those below nk, of drafts the tree's
+            for (int q = 0; q < 4; ++q) tmem_wait_ld(s[q]);
+            if (drafts || nk < kRows) {
+                // a bit per key: those below nk, of drafts the tree's
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
                     const int cnt = nk - 32 * q;
                     uint32_t vis = cnt >= 32 ? 0xffffffffu : cnt > 0 ? (1u << cnt) - 1u : 0u;
                     if (drafts) vis &= bits[q];
@@ -549,12 +549,15 @@ __device__ void tree_softmax(const TreeParams &p, uint8_t *smem, TreeBars *bars,
                     for (int k = 0; k < 32; ++k)
                         if (!((vis >> k) & 1u)) s[q][k] = 0xff800000u;
                 }
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int k = 0; k < 32; k += 8)
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
                         mx[y] = max3(mx[y], __uint_as_float(s[q][k + 2 * y]), __uint_as_float(s[q][k + 2 * y + 1]));
-            }
             const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
             const bool need = tmax > m + kRescaleLog2;
             if (__any_sync(0xffffffffu, need)) {
