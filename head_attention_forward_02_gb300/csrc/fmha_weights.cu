@@ -257,7 +257,21 @@ __device__ void w_producer(const WParams &p, WCursor &cur, int gate, const CUten
     }
     for (uint32_t i = 1; ok && it.b >= 0; ++i, it = next) {
         const int e = it.entry >= 0 ? it.entry : p.B_cache;   // out of range: zero fill
-        for (int x = 0; x < it.nkt; ++x, ++kf) {
+        auto load_q = [&](int c) {
+            const int st = qf % C::NQ;
+            if (qf >= C::NQ && !mbar_wait(smem_u32(&q_empty[st]), (qf / C::NQ - 1) & 1, abort_flag)) return false;
+            const uint32_t fb = smem_u32(&q_full[st]);
+            mbar_expect_tx(fb, C::PANELS * p.TB * p.G * 128);
+#pragma unroll
+            for (int pn = 0; pn < C::PANELS; ++pn)
+                tma_load_3d(smem_u32(smem + C::OFF_Q + st * C::TILE_BYTES + pn * kPanelBytes), tmQ, fb, pn * C::BOX,
+                            it.g * p.G, it.b * p.Sq + c * p.TB);
+            ++qf;
+            return true;
+        };
+        // the first chunk's Q goes ahead of K, whose stages come free later
+        if (it.c0 < it.c1) ok = load_q(it.c0);
+        for (int x = 0; ok && x < it.nkt; ++x) {
             const int st = kf % C::NK;
             if (kf >= C::NK && !mbar_wait(smem_u32(&k_empty[st]), (kf / C::NK - 1) & 1, abort_flag)) {
                 ok = false;
@@ -269,28 +283,12 @@ __device__ void w_producer(const WParams &p, WCursor &cur, int gate, const CUten
             for (int pn = 0; pn < C::PANELS; ++pn)
                 tma_load_4d(smem_u32(smem + C::OFF_K + st * C::TILE_BYTES + pn * kPanelBytes), tmK, fb, pn * C::BOX,
                             it.g, it.tile * p.UK + x * kRows, e);
+            ++kf;
         }
-        for (int c = it.c0; ok && c < it.c1; ++c, ++qf) {
-            const int st = qf % C::NQ;
-            if (qf >= C::NQ && !mbar_wait(smem_u32(&q_empty[st]), (qf / C::NQ - 1) & 1, abort_flag)) {
-                ok = false;
-                break;
-            }
-            const uint32_t fb = smem_u32(&q_full[st]);
-            mbar_expect_tx(fb, C::PANELS * p.TB * p.G * 128);
-#pragma unroll
-            for (int pn = 0; pn < C::PANELS; ++pn)
-                tma_load_3d(smem_u32(smem + C::OFF_Q + st * C::TILE_BYTES + pn * kPanelBytes), tmQ, fb, pn * C::BOX,
-                            it.g * p.G, it.b * p.Sq + c * p.TB);
-            if (c == it.c0) {
-                w_next(p, cur, next);
-                ok = w_publish(bars, i, next, abort_flag);
-            }
-        }
-        if (ok && it.c0 >= it.c1) {
-            w_next(p, cur, next);
-            ok = w_publish(bars, i, next, abort_flag);
-        }
+        if (!ok) break;
+        w_next(p, cur, next);
+        ok = w_publish(bars, i, next, abort_flag);
+        for (int c = it.c0 + 1; ok && c < it.c1; ++c) ok = load_q(c);
     }
     // the last release of every stage must arrive before exit; when the CTA
     // gave up, only the copies already issued
