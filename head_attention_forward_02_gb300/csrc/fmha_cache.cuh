@@ -26,6 +26,7 @@ __device__ int g_test_flag;   // never written
 
 constexpr int kD = 128;                  // head dim
 constexpr int kRows = 128;               // rows of a tile (MMA M)
+constexpr int kMaxCacheRows = 1 << 30;   // of an entry: row numbers and tile bounds stay in 32 bits
 constexpr int kPanelBytes = kRows * 128; // 128 rows of one 128-byte swizzled panel
 constexpr unsigned long long kTimeoutNs = 4000000000ull;
 constexpr unsigned long long kDrainNs = 200000000ull;
@@ -390,6 +391,12 @@ __device__ __forceinline__ int cache_entry(const int *idx, int b, int B_cache, b
 // ---------------------------------------------------------------------------
 
 inline bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+// Do the n bytes at p and the m bytes at q share any?
+inline bool overlap(const void *p, size_t n, const void *q, size_t m) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + m && b < a + n;
+}
 
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;

@@ -43,7 +43,6 @@ struct EvictParams {
     int *kept;                           // [B, H_k, budget]
     int *new_seqlen;                     // [B]
     int B, H_k, B_cache, S_max, B_out, S_out, budget, recent;
-    int row;                             // bytes of one head's row
     int in_place;
 };
 
@@ -324,6 +323,7 @@ extern "C" int fmha_cache_evict(fmha_tensor k_cache, fmha_tensor v_cache, const 
     if (B < 0 || H_k <= 0 || D != kD || budget <= 0 || recent < 0 || recent > budget) return FMHA_ERR_INVALID_ARG;
     if (B == 0) return FMHA_OK;
     if (S_max <= 0 || B_cache <= 0 || S_out <= 0 || B_out <= 0 || budget > S_out) return FMHA_ERR_INVALID_ARG;
+    if (S_max > kMaxCacheRows || S_out > kMaxCacheRows) return FMHA_ERR_INVALID_ARG;
     if (!seqlen || !kept || !new_seqlen || !acc || !acc_out) return FMHA_ERR_INVALID_ARG;
     if (!k_cache.data || !v_cache.data || !k_out.data || !v_out.data) return FMHA_ERR_INVALID_ARG;
     const int dt = k_cache.dtype;
@@ -344,14 +344,12 @@ extern "C" int fmha_cache_evict(fmha_tensor k_cache, fmha_tensor v_cache, const 
             return FMHA_ERR_INVALID_ARG;
     } else {
         const size_t in_b = (size_t)B_cache * S_max * H_k, out_b = (size_t)B_out * S_out * H_k;
-        struct Range { const char *p; size_t n; };
-        const Range in[3] = {{(const char *)k_cache.data, in_b * row}, {(const char *)v_cache.data, in_b * row},
-                             {(const char *)acc, in_b * sizeof(float)}};
-        const Range out[3] = {{(const char *)k_out.data, out_b * row}, {(const char *)v_out.data, out_b * row},
-                              {(const char *)acc_out, out_b * sizeof(float)}};
+        struct Range { const void *p; size_t n; };
+        const Range in[3] = {{k_cache.data, in_b * row}, {v_cache.data, in_b * row}, {acc, in_b * sizeof(float)}};
+        const Range out[3] = {{k_out.data, out_b * row}, {v_out.data, out_b * row}, {acc_out, out_b * sizeof(float)}};
         for (const Range &i : in)
             for (const Range &o : out)
-                if (i.p < o.p + o.n && o.p < i.p + i.n) return FMHA_ERR_INVALID_ARG;
+                if (overlap(i.p, i.n, o.p, o.n)) return FMHA_ERR_INVALID_ARG;
     }
     if (seqlen == new_seqlen) return FMHA_ERR_INVALID_ARG;      // every CTA of a sequence reads its length
     const int rc = check_device();
@@ -379,7 +377,6 @@ extern "C" int fmha_cache_evict(fmha_tensor k_cache, fmha_tensor v_cache, const 
     p.S_out = S_out;
     p.budget = budget;
     p.recent = recent;
-    p.row = row;
     p.in_place = in_place ? 1 : 0;
     // CTAs of a head's selection: while all fit the SMs at once (clusters of
     // eight do not pack: half) and each has 2048 rows; 1024 threads where 512

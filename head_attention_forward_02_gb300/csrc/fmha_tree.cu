@@ -28,8 +28,8 @@
 // has an MMA warp of its own, and one group's MMAs run under the other's
 // softmax.  The reference m is kept lazily: O is rescaled only when the row
 // maximum has grown by more than 2^8.
-// P is rounded to the inputs' type for the P V product (relative 2^-9 / 2^-12
-// / 2^-4 a weight), its row sum and O stay in fp32.
+// P is rounded to the inputs' type for the P V product (by up to 2^-8 / 2^-11 /
+// 2^-4 of a weight for bf16 / fp16 / e4m3), its row sum and O stay in fp32.
 //
 // A unit cut between CTAs leaves normalised fp32 partials and their LSE in the
 // workspace, at most two per CTA, and a second kernel joins them; units that
@@ -942,7 +942,8 @@ int64_t tree_max_tiles(const TreeShape &s, int B, int T, int H_k, int S_max) {
 }
 
 bool tree_sizes_ok(int B, int T, int H, int H_k, int D, int S_max) {
-    return B > 0 && T > 0 && H > 0 && H_k > 0 && H % H_k == 0 && H / H_k <= kRows && D == kD && S_max > 0;
+    return B > 0 && T > 0 && H > 0 && H_k > 0 && H % H_k == 0 && H / H_k <= kRows && D == kD && S_max > 0 &&
+           S_max <= kMaxCacheRows;
 }
 
 using TreeKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, TreeParams);
@@ -986,7 +987,7 @@ extern "C" int fmha_tree_fwd(fmha_tensor q, fmha_tensor k_cache, fmha_tensor v_c
         return FMHA_ERR_INVALID_ARG;
     if (tree_mask && mask_batch_stride != 0 && mask_batch_stride < (int64_t)T * T) return FMHA_ERR_INVALID_ARG;
     if (B == 0 || T == 0) return FMHA_OK;
-    if (S_max <= 0 || B_cache <= 0 || !seqlen) return FMHA_ERR_INVALID_ARG;
+    if (S_max <= 0 || S_max > kMaxCacheRows || B_cache <= 0 || !seqlen) return FMHA_ERR_INVALID_ARG;
     if (!q.data || !k_cache.data || !v_cache.data || !k_new.data || !v_new.data || !o.data) return FMHA_ERR_INVALID_ARG;
     const int dt = q.dtype;
     if (dt != FMHA_F16 && dt != FMHA_BF16 && dt != FMHA_E4M3) return FMHA_ERR_UNSUPPORTED;
@@ -1000,6 +1001,13 @@ extern "C" int fmha_tree_fwd(fmha_tensor q, fmha_tensor k_cache, fmha_tensor v_c
     const TreeShape sh = tree_shape(T, H / H_k);
     if (!workspace || misaligned(workspace, 256) ||
         workspace_bytes < fmha_tree_workspace_size(B, T, H, H_k, D, S_max))
+        return FMHA_ERR_INVALID_ARG;
+    // a unit's inputs are read by several CTAs, at their own times
+    const size_t row = kD * (dt == FMHA_E4M3 ? 1 : 2), q_bytes = (size_t)B * T * H * row;
+    const size_t new_bytes = (size_t)B * T * H_k * row, cache_bytes = (size_t)B_cache * S_max * H_k * row;
+    if (overlap(o.data, q_bytes, q.data, q_bytes) || overlap(o.data, q_bytes, k_new.data, new_bytes) ||
+        overlap(o.data, q_bytes, v_new.data, new_bytes) || overlap(o.data, q_bytes, k_cache.data, cache_bytes) ||
+        overlap(o.data, q_bytes, v_cache.data, cache_bytes))
         return FMHA_ERR_INVALID_ARG;
     int rc = check_device();
     if (rc != FMHA_OK) return rc;
@@ -1077,7 +1085,8 @@ extern "C" int fmha_tree_commit(fmha_tensor k_cache, fmha_tensor v_cache, fmha_t
                                 const int *batch_idx, const int *path, const int *n_accept, cudaStream_t stream) {
     if (B < 0 || T < 0 || P < 0 || H_k <= 0 || D != kD) return FMHA_ERR_INVALID_ARG;
     if (B == 0 || P == 0) return FMHA_OK;
-    if (T == 0 || S_max <= 0 || B_cache <= 0 || !seqlen || !path || !n_accept) return FMHA_ERR_INVALID_ARG;
+    if (T == 0 || S_max <= 0 || S_max > kMaxCacheRows || B_cache <= 0 || !seqlen || !path || !n_accept)
+        return FMHA_ERR_INVALID_ARG;
     if (!k_cache.data || !v_cache.data || !k_new.data || !v_new.data) return FMHA_ERR_INVALID_ARG;
     const int dt = k_cache.dtype;
     if (dt != FMHA_F16 && dt != FMHA_BF16 && dt != FMHA_E4M3) return FMHA_ERR_UNSUPPORTED;
@@ -1088,6 +1097,12 @@ extern "C" int fmha_tree_commit(fmha_tensor k_cache, fmha_tensor v_cache, fmha_t
     if (misaligned(seqlen, 4) || misaligned(batch_idx, 4) || misaligned(path, 4) || misaligned(n_accept, 4))
         return FMHA_ERR_INVALID_ARG;
     if (B > 65535) return FMHA_ERR_UNSUPPORTED;
+    const size_t row = (size_t)H_k * kD * (dt == FMHA_E4M3 ? 1 : 2);
+    const size_t new_bytes = (size_t)B * T * row, cache_bytes = (size_t)B_cache * S_max * row;
+    for (const void *c : {k_cache.data, v_cache.data})
+        if (overlap(c, cache_bytes, k_new.data, new_bytes) || overlap(c, cache_bytes, v_new.data, new_bytes))
+            return FMHA_ERR_INVALID_ARG;
+    if (overlap(k_cache.data, cache_bytes, v_cache.data, cache_bytes)) return FMHA_ERR_INVALID_ARG;
     const int rc = check_device();
     if (rc != FMHA_OK) return rc;
     CommitParams p{};
@@ -1103,7 +1118,7 @@ extern "C" int fmha_tree_commit(fmha_tensor k_cache, fmha_tensor v_cache, fmha_t
     p.P = P;
     p.B_cache = B_cache;
     p.S_max = S_max;
-    p.row16 = H_k * kD * (dt == FMHA_E4M3 ? 1 : 2) / 16;
+    p.row16 = (int)(row / 16);
     const int threads = p.row16 >= 256 ? 256 : (p.row16 + 31) / 32 * 32;
     fmha_tree_commit_kernel<<<dim3(P, B), threads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? FMHA_OK : FMHA_ERR_CUDA;

@@ -636,10 +636,9 @@ extern "C" int fmha_cache_weights(fmha_tensor q, fmha_tensor k_cache, const floa
     for (const void *ptr : {(const void *)lse, (const void *)acc_in, (const void *)acc_out, (const void *)seqlen,
                             (const void *)batch_idx, (const void *)n_query})
         if (misaligned(ptr, 4)) return FMHA_ERR_INVALID_ARG;
-    if ((int64_t)B * Sq >= (int64_t(1) << 31) / kRows || S_max > (1 << 30)) return FMHA_ERR_INVALID_ARG;
+    if ((int64_t)B * Sq >= (int64_t(1) << 31) / kRows || S_max > kMaxCacheRows) return FMHA_ERR_INVALID_ARG;
     const size_t acc_bytes = (size_t)B_cache * H_k * S_max * sizeof(float);
-    const char *ai = reinterpret_cast<const char *>(acc_in), *ao = reinterpret_cast<const char *>(acc_out);
-    if (acc_in && ai != ao && ai < ao + acc_bytes && ao < ai + acc_bytes) return FMHA_ERR_INVALID_ARG;
+    if (acc_in && acc_in != acc_out && overlap(acc_in, acc_bytes, acc_out, acc_bytes)) return FMHA_ERR_INVALID_ARG;
     if (!workspace || misaligned(workspace, 256) || workspace_bytes < fmha_cache_weights_workspace_size())
         return FMHA_ERR_INVALID_ARG;
     const int rc = check_device();
@@ -680,7 +679,8 @@ extern "C" int fmha_cache_weights(fmha_tensor q, fmha_tensor k_cache, const floa
     const cuuint32_t bq[3] = {box_d, (cuuint32_t)p.G, (cuuint32_t)p.TB};
     const cuuint64_t dk[4] = {kD, (cuuint64_t)H_k, (cuuint64_t)S_max, (cuuint64_t)B_cache};
     const cuuint32_t bk[4] = {box_d, 1, kRows, 1};
-    if (!make_map(&tq, dt, q.data, 3, dq, bq) || !make_map(&tk, dt, k_cache.data, 4, dk, bk, row_promotion(dt))) return FMHA_ERR_CUDA;
+    if (!make_map(&tq, dt, q.data, 3, dq, bq) || !make_map(&tk, dt, k_cache.data, 4, dk, bk, row_promotion(dt)))
+        return FMHA_ERR_CUDA;
 
     auto kern = dt == FMHA_BF16  ? w_kernel<FMHA_BF16>(one)
                 : dt == FMHA_F16 ? w_kernel<FMHA_F16>(one) : w_kernel<FMHA_E4M3>(one);

@@ -296,9 +296,10 @@ size_t fmha_gen_workspace_size(int B, int H, int H_k, int D, int S_max);
  *                      draft need not see itself.
  *   lse                float [B, H, T], or NULL
  * All tensors share one dtype, FMHA_F16, FMHA_BF16 or FMHA_E4M3; D must be
- * 128 and H / H_k at most 128.  Device pointers must be 16-byte aligned
- * (int32 and lse 4-byte).  P is rounded to the tensors' dtype before P.V (its
- * row sum is not), and O with saturation for e4m3.
+ * 128, H / H_k at most 128 and S_max at most 2^30.  Device pointers must be
+ * 16-byte aligned (int32 and lse 4-byte), and o and lse apart from the inputs.
+ * P is rounded to the tensors' dtype before P.V (its row sum is not), and O
+ * with saturation for e4m3.
  * Requirements the host cannot check: 0 <= seqlen[b] <= S_max, 0 <=
  * batch_idx[b] < B_cache, 0 <= n_draft[b] <= T; a kernel that meets a
  * violation clamps the length or the count, or reads zeros for the missing
@@ -336,7 +337,9 @@ size_t fmha_tree_workspace_size(int B, int T, int H, int H_k, int D, int S_max);
  * with e and L = seqlen[b] as there.  seqlen is not changed (the caller adds
  * n_accept to it).  Layouts as fmha_tree_fwd; path int32 [B, P], n_accept
  * int32 [B].  A draft may appear more than once.  Entries of path at or past
- * n_accept are not read.  Two sequences must not share an entry.
+ * n_accept are not read.  Two sequences must not share an entry; K_new and
+ * V_new are apart from the caches, and those from one another.  S_max at most
+ * 2^30.
  * In device memory, so checked there: 0 <= seqlen[b], 0 <= n_accept[b] <= P,
  * seqlen[b] + n_accept[b] <= S_max, batch_idx[b] in [0, B_cache) and path in
  * [0, T); a kernel that meets a violation clamps the count, or writes nothing
@@ -370,8 +373,8 @@ int fmha_tree_commit(fmha_tensor k_cache, fmha_tensor v_cache, fmha_tensor k_new
  * of q's dtype (FMHA_F16, FMHA_BF16, FMHA_E4M3); lse float [B, H, Sq];
  * acc_in, acc_out float [B_cache, H_k, S_max], the same array or apart; seqlen,
  * batch_idx, n_query int32 [B] (the last two may be NULL).  H / H_k at most
- * 128.  q and k_cache 16-byte, the others 4-byte aligned.  Sums are fp32 in an
- * order that does not depend on timing.
+ * 128, S_max at most 2^30.  q and k_cache 16-byte, the others 4-byte aligned.
+ * Sums are fp32 in an order that does not depend on timing.
  * seqlen and batch_idx are treated as in fmha_tree_fwd, n_query as n_draft
  * there; nothing is written for a missing entry.  Two sequences must not share
  * an entry.  Cached rows at or past L are never used.
@@ -409,9 +412,9 @@ size_t fmha_cache_weights_workspace_size(void);
  * batch_idx, out_idx int32 [B] (the last two may be NULL: entry b).  The
  * output is the input itself (k_out.data == k_cache.data, and then v_out,
  * acc_out, B_out, S_out and out_idx are the input's too), or apart from it in
- * memory.  1 <= budget <= S_out, 0 <= recent <= budget.  new_seqlen is another
- * array than seqlen.  K, V 16-byte, the others 4-byte aligned; dtype FMHA_F16,
- * FMHA_BF16 or FMHA_E4M3.
+ * memory.  1 <= budget <= S_out, 0 <= recent <= budget, S_max and S_out at
+ * most 2^30.  new_seqlen is another array than seqlen.  K, V 16-byte, the
+ * others 4-byte aligned; dtype FMHA_F16, FMHA_BF16 or FMHA_E4M3.
  * seqlen, batch_idx and out_idx are treated as in fmha_tree_fwd; nothing is
  * moved from or to a missing entry.  Two sequences must not share an entry of
  * the output, nor, in place, of the input.

@@ -38,7 +38,7 @@ def call_tree(fm, **kw):
     *[({n: None}, -1) for n in ("q", "kc", "vc", "kn", "vn", "o")],
     *[({n: P + 8}, -2) for n in ("q", "kc", "vc", "kn", "vn", "o")],
     *[({n + "_dt": F16}, -2) for n in ("kc", "vc", "kn", "vn", "o")],
-    (dict(dt=5), -2), (dict(B=1 << 20, T=1 << 10), -1),
+    (dict(dt=5), -2), (dict(B=1 << 20, T=1 << 10), -1), (dict(S=(1 << 30) + 1), -1),
     (dict(B=0, q=None, sl=None, ws=None), 0), (dict(T=0, q=None, sl=None, ws=None), 0),
 ])
 def test_tree_refusals(fm, kw, code):
@@ -56,7 +56,8 @@ def test_tree_workspace_size(fm):
     assert size(64, 33, 32, 8, 128, 100000) == 2 * 152 * (2 * row + meta)
     assert size(64, 33, 32, 8, 128, 100000) <= 41 << 20
     for bad in [(0, 8, 32, 8, 128, 10), (1, 0, 32, 8, 128, 10), (1, 8, 3, 2, 128, 10), (1, 8, 32, 8, 64, 10),
-                (1, 8, 32, 8, 128, 0), (1, 8, 129, 1, 128, 10)]:
+                (1, 8, 32, 8, 128, 0), (1, 8, 129, 1, 128, 10),
+                (1, 8, 32, 8, 128, (1 << 30) + 1)]:
         assert size(*bad) == 0
 
 
@@ -72,7 +73,7 @@ def call_commit(fm, **kw):
     (dict(D=64), -1), (dict(H_k=0), -1), (dict(B=-1), -1), (dict(P=-1), -1), (dict(T=0), -1), (dict(S=0), -1),
     (dict(Bc=0), -1), (dict(sl=None), -1), (dict(path=None), -1), (dict(na=None), -1), (dict(path=P + 2), -1),
     *[({n: None}, -1) for n in ("kc", "vc", "kn", "vn")], *[({n: P + 8}, -2) for n in ("kc", "vc", "kn", "vn")],
-    (dict(vn_dt=F16), -2), (dict(dt=9), -2), (dict(B=70000), -2),
+    (dict(vn_dt=F16), -2), (dict(dt=9), -2), (dict(B=70000), -2), (dict(S=(1 << 30) + 1), -1),
     (dict(B=0, kc=None, sl=None), 0), (dict(P=0, path=None, sl=None), 0),
 ])
 def test_commit_refusals(fm, kw, code):
@@ -95,7 +96,7 @@ def call_weights(fm, **kw):
     (dict(kc=None), -1), (dict(scale=-1.0), -1), (dict(mask=1), -1), (dict(mask=3), -1), (dict(ws=None), -1),
     (dict(ws=P + 16), -1), (dict(ws_bytes=16), -1), (dict(lse=P + 2), -1), (dict(ai=P2 + 1), -1),
     (dict(ao=P2 + 4), -1), (dict(ai=P3 + 4 * 2 * 2 * 64 - 4), -1),      # neither the same array nor apart
-    (dict(q=P + 8), -2), (dict(kc=P + 8), -2), (dict(kc_dt=E4M3), -2), (dict(dt=4), -2),
+    (dict(q=P + 8), -2), (dict(kc=P + 8), -2), (dict(kc_dt=E4M3), -2), (dict(dt=4), -2), (dict(S=(1 << 30) + 1), -1),
     (dict(B=0, q=None, ws=None), 0), (dict(Sq=0, q=None, ws=None), 0),
 ])
 def test_weights_refusals(fm, kw, code):
@@ -118,7 +119,8 @@ def call_evict(fm, **kw):
     (dict(sl=None), -1), (dict(kept=None), -1), (dict(ns=None), -1), (dict(ns=P), -1), (dict(acc=None), -1),
     (dict(ao=None), -1), (dict(ao=6 * P + 2), -1),
     *[({n: None}, -1) for n in ("kc", "vc", "ko", "vo")], *[({n: 7 * P + 8}, -2) for n in ("kc", "vc", "ko", "vo")],
-    (dict(vo_dt=E4M3), -2), (dict(dt=3), -2), (dict(B=70000), -2),
+    (dict(vo_dt=E4M3), -2), (dict(dt=3), -2), (dict(B=70000), -2), (dict(S=(1 << 30) + 1), -1),
+    (dict(So=(1 << 30) + 1), -1),
     # in place means all three arrays, with the sizes and entries of the input
     (dict(ko=P), -1), (dict(ko=P, vo=2 * P, ao=3 * P), -1), (dict(ko=P, vo=2 * P, ao=3 * P, So=64, oi=P3), -1),
     # else the output is apart from the input
@@ -127,6 +129,18 @@ def call_evict(fm, **kw):
 ])
 def test_evict_refusals(fm, kw, code):
     assert call_evict(fm, **kw) == code
+
+
+def test_outputs_over_inputs_are_refused(fm):
+    a = dict(q=P, kc=2 * P, vc=3 * P, kn=4 * P, vn=5 * P, ws=6 * P)
+    for n in ("q", "kc", "vc", "kn", "vn"):
+        size = 2 * 128 * 2 * (64 * 2 if n in ("kc", "vc") else 4 * (8 if n == "q" else 2))       # bytes
+        assert call_tree(fm, **a, o=a[n]) == -1
+        assert call_tree(fm, **a, o=a[n] + size - 16) == -1
+    c = dict(kc=P, vc=2 * P, kn=3 * P, vn=4 * P)
+    for x, y in (("kc", "vc"), ("kc", "kn"), ("kc", "vn"), ("vc", "kn"), ("vc", "vn")):
+        assert call_commit(fm, **{**c, y: c[x]}) == -1
+        assert call_commit(fm, **{**c, y: c[x] + 2 * 64 * 2 * 128 * 2 - 16}) == -1               # the cache's last bytes
 
 
 def test_host_tensors_are_refused(fm):
