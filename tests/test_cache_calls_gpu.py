@@ -114,6 +114,40 @@ def test_work_on_another_stream_than_the_current_one(fm):
     assert new.tolist() == [1000, 1000] and bool((kept[:, :, 1:] > kept[:, :, :-1]).all())
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_what_a_call_makes_for_itself_belongs_to_its_stream(fm, handle):
+    """The current stream is busy: a zero fill or a workspace left to it would come after, or under, the kernels."""
+    c = tc.make("bf16", 40, 8, 2, 900, [900, 301], mask="causal", seed=22)
+    c["want"] -= c["acc"].double()                        # from nothing
+    t = tt.make("bf16", 40, 8, 2, 900, [900, 301], seed=23)
+    args = c["q"].cuda(), c["kc"].cuda(), c["lse"].cuda(), i32(c["seqlen"])
+    d = tt.on_gpu(t)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    for _ in range(2):                                    # the kernels are loaded before the streams part
+        fm.cache_weights(*args, mask="causal", stream=stream)
+        fm.tree_fwd(*d["args"], **d["kw"], stream=stream)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    r = fm.cache_weights(*args, mask="causal", stream=stream)
+    o, lse = fm.tree_fwd(*d["args"], **d["kw"], stream=stream)
+    side.synchronize()
+    assert not torch.cuda.current_stream().query()        # none of it waited for the current stream
+    torch.full((1 << 22,), 7, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert fm.device_status(reset=True) == 0
+    tc.check_weights(c, r, torch.zeros_like(c["acc"]))
+    tt.check(t, o, lse)
+
+
+def test_an_output_over_an_input_is_refused(fm):
+    a = {k: bf(*s) for k, s in TREE.items()}
+    with pytest.raises(fm.FmhaError):
+        fm.tree_fwd(*a.values(), i32([4, 4]), out=a["q"])
+    with pytest.raises(fm.FmhaError):
+        fm.tree_commit(a["k_cache"], a["k_cache"], a["k_new"], a["v_new"], i32([4, 4]), i32([[0], [0]]), i32([1, 1]))
+
+
 @pytest.mark.parametrize("op", ["tree_blocks", "tree_split", "weights"])
 def test_expired_wait_is_reported_and_the_context_stays_usable(fm, op):
     """With the bounded waits limited to 1 ms the producers first wait for a
