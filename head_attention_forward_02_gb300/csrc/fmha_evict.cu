@@ -24,6 +24,8 @@
 // place, the rows of a head move down one after another: row i comes from a
 // row at or after it, so a CTA walks them in blocks, reads a whole block into
 // registers, and writes it only after all of it was read.
+#include <type_traits>
+
 #include "fmha_cache.cuh"
 
 namespace fmha {
@@ -57,26 +59,36 @@ __device__ __forceinline__ int evict_len(const EvictParams &p, int b, bool repor
     return clamped(p.seqlen[b], 0, p.S_max, report);
 }
 
-// A word of shared memory in CTA `rank` of the cluster, at the address that
-// `p` has in this one.
-__device__ __forceinline__ uint32_t cluster_word(const uint32_t *p, uint32_t rank) {
-    uint32_t a, v;
+// Shared memory of CTA `rank` of the cluster, at the address that `p` has in
+// this one: add to a word there, store one.
+__device__ __forceinline__ uint32_t cluster_addr(const uint32_t *p, uint32_t rank) {
+    uint32_t a;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
+    return a;
 }
-__device__ __forceinline__ void cluster_sync() {
+__device__ __forceinline__ void cluster_add(const uint32_t *p, uint32_t rank, uint32_t v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_store(const uint32_t *p, uint32_t rank, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // grid (CS * H_k, B), clusters of CS CTAs of TH threads along x
 template <int CS, int TH>
 __global__ void __launch_bounds__(TH) fmha_evict_select_kernel(const EvictParams p) {
     constexpr int kSelWarps = TH / 32;
-    __shared__ uint32_t hist[2][kBins];          // of alternate passes: one is read by the cluster while the next is filled
+    __shared__ alignas(16) uint32_t hist[kBins];                     // of this CTA's keys
+    __shared__ alignas(16) uint32_t sum[CS > 1 ? 3 : 1][CS > 1 ? kBins : 4];   // the cluster's, by pass: every CTA adds to all
     __shared__ uint32_t warp_sum[kSelWarps], warp_eq[kSelWarps];
-    __shared__ uint32_t s_digit, s_above, s_tot[2];
+    __shared__ uint32_t s_digit, s_above, cta_gt[CS], cta_eq[CS];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int g = blockIdx.x / CS, rank = blockIdx.x % CS, b = blockIdx.y;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -104,48 +116,70 @@ __global__ void __launch_bounds__(TH) fmha_evict_select_kernel(const EvictParams
     constexpr int kBlock = 32 * kSelKeys;
     const bool once = run <= kBlock;
     uint32_t key[kSelKeys];
-    auto load = [&](int base) {
-        float x[kSelKeys];
+    float x[kSelKeys];
+    auto fetch = [&](int base) {
 #pragma unroll
         for (int k = 0; k < kSelKeys; ++k) {
             const int i = base + 32 * k + lane;
             x[k] = i < hi ? acc[i] : 0.f;
         }
+    };
+    auto to_keys = [&]() {
 #pragma unroll
         for (int k = 0; k < kSelKeys; ++k) key[k] = score_key(x[k]);
     };
-    if (once) load(lo);
+    auto load = [&](int base) {
+        fetch(base);
+        to_keys();
+    };
+    if (once) fetch(lo);
+    for (int i = tid; i < kBins; i += TH) hist[i] = 0;
+    if (CS > 1) {
+        for (int i = tid; i < 3 * kBins; i += TH) sum[0][i] = 0;
+        cluster_arrive();                        // met below: nobody adds to a sum before it is zeroed
+    }
+    if (once) to_keys();
+    if (CS > 1) cluster_wait();
+    __syncthreads();
 
     // the need-th largest key: its digits, and how many keys equal to it stay
     uint32_t prefix = 0, want = need;
-    for (int i = tid; i < kBins; i += TH) hist[0][i] = 0;
-    __syncthreads();
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-        uint32_t *h = hist[pass & 1], *other = hist[(pass & 1) ^ 1];
         for (int base = lo; base < hi; base += kBlock) {
             if (!once) load(base);
 #pragma unroll
             for (int k = 0; k < kSelKeys; ++k)
                 if (base + 32 * k + lane < hi && (pass == 0 || (key[k] >> (shift + bits)) == prefix))
-                    atomicAdd(&h[(key[k] >> shift) & ((1u << bits) - 1)], 1u);
+                    atomicAdd(&hist[(key[k] >> shift) & ((1u << bits) - 1)], 1u);
         }
-        // every CTA's histogram is complete, and nobody reads the other buffer any more
-        if (CS > 1) cluster_sync();
-        else __syncthreads();
-        // bins from the top, two a thread: the one in which the count passes `want`
+        __syncthreads();
+        if (CS > 1) {
+            // few of the bins hold a key: those go to every CTA
+            for (int i = tid; i < kBins; i += TH) {
+                const uint32_t c = hist[i];
+                if (c == 0) continue;
+                hist[i] = 0;
+#pragma unroll
+                for (int r = 0; r < CS; ++r) cluster_add(&sum[pass][i], r, c);
+            }
+            cluster_arrive();
+            cluster_wait();
+        }
+        // bins from the top, PER a thread: the one in which the count passes `want`
         constexpr int PER = kBins / TH;
+        using Bins = std::conditional_t<PER == 4, uint4, uint2>;
+        static_assert(PER == 4 || PER == 2, "bins of a thread");
+        Bins *own = reinterpret_cast<Bins *>(CS > 1 ? sum[CS > 1 ? pass : 0] : hist) + (TH - 1 - tid);
+        const Bins v = *own;
+        if (CS == 1) *own = Bins{};
         uint32_t n[PER], mine = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-            const int bin = kBins - 1 - (tid * PER + i);
-            n[i] = 0;
-#pragma unroll
-            for (int c = 0; c < CS; ++c) n[i] += CS > 1 ? cluster_word(&h[bin], c) : h[bin];
+            n[i] = reinterpret_cast<const uint32_t *>(&v)[PER - 1 - i];
             mine += n[i];
         }
-        for (int i = tid; i < kBins; i += TH) other[i] = 0;
         uint32_t incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -195,15 +229,18 @@ __global__ void __launch_bounds__(TH) fmha_evict_select_kernel(const EvictParams
     uint32_t at_gt = __reduce_add_sync(0xffffffffu, lane < warp ? wg : 0u);
     uint32_t at_eq = __reduce_add_sync(0xffffffffu, lane < warp ? we : 0u);
     if (CS > 1) {
+        // the CTAs before this one
         const uint32_t tg = __reduce_add_sync(0xffffffffu, wg), te = __reduce_add_sync(0xffffffffu, we);
-        if (tid == 0) {
-            s_tot[0] = tg;
-            s_tot[1] = te;
+        if (tid < CS) {
+            cluster_store(&cta_gt[rank], tid, tg);
+            cluster_store(&cta_eq[rank], tid, te);
         }
-        cluster_sync();
-        for (int c = 0; c < rank; ++c) {
-            at_gt += cluster_word(&s_tot[0], c);
-            at_eq += cluster_word(&s_tot[1], c);
+        cluster_arrive();
+        cluster_wait();                          // no CTA reaches into another's shared memory after this
+#pragma unroll
+        for (int c = 0; c < CS; ++c) {
+            at_gt += c < rank ? cta_gt[c] : 0u;
+            at_eq += c < rank ? cta_eq[c] : 0u;
         }
     }
     const uint32_t lt = (1u << lane) - 1u;
@@ -221,7 +258,6 @@ __global__ void __launch_bounds__(TH) fmha_evict_select_kernel(const EvictParams
             at_eq += __popc(me);
         }
     }
-    if (CS > 1) cluster_sync();                  // the others have read this CTA's shared memory
 }
 
 // A CTA moves slices of SL bytes of a head's rows: 16-byte pieces, a thread
