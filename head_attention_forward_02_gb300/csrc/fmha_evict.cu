@@ -260,13 +260,14 @@ __global__ void __launch_bounds__(TH) fmha_evict_select_kernel(const EvictParams
     }
 }
 
-// A CTA moves slices of SL bytes of a head's rows: 16-byte pieces, a thread
-// holds four rows' of a block.
+// A CTA moves slices of SL bytes of a head's rows in 16-byte pieces, four rows'
+// of a block a thread; eight where a head is walked by few CTAs, each block a
+// round trip to memory (2048 of 4096 rows in place: 24.6 -> 20.5 us).
 template <int SL>
 struct MoveCfg {
     static constexpr int PIECES = SL / 16;
     static constexpr int ROWS_AT_ONCE = kMoveThreads / PIECES;
-    static constexpr int PER = 4;
+    static constexpr int PER = SL == 64 ? 8 : 4;
     static constexpr int BLOCK = ROWS_AT_ONCE * PER;
 };
 
@@ -340,7 +341,12 @@ __global__ void __launch_bounds__(kMoveThreads) fmha_evict_move_kernel(const Evi
             }
         }
     __syncthreads();
-    for (int i = n + chunk * kMoveThreads + tid; i < p.S_out; i += chunks * kMoveThreads) o[i] = 0.f;
+    float *z = o + n;
+    const int rest = p.S_out - n, lead = imin(rest, (int)(-reinterpret_cast<uintptr_t>(z) & 15) / 4);
+    const int quads = (rest - lead) / 4;
+    for (int i = chunk * kMoveThreads + tid; i < quads; i += chunks * kMoveThreads)
+        reinterpret_cast<float4 *>(z + lead)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (chunk == 0 && tid < rest - 4 * quads) z[tid < lead ? tid : tid + 4 * quads] = 0.f;
 }
 
 }  // namespace
