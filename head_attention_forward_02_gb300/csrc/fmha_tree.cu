@@ -34,6 +34,15 @@
 // A unit cut between CTAs leaves normalised fp32 partials and their LSE in the
 // workspace, at most two per CTA, and a second kernel joins them; units that
 // one CTA covers are written to O directly.
+//
+// Measured (kernel and merge): B=32, T=64, 8192 keys, H=32, H_k=8, bf16 223 us:
+// 5.0 TB/s and 1.24 PFLOP/s at once, near both; the two groups take a 64 KB pair
+// of K and V tiles in 3100 cycles, at the copy rate it would arrive in 2840.
+// One row block (SPLIT): B=16, T=27, 4096 ragged f16 keys 53.5 us, 3.4 TB/s;
+// B=16, T=5, H=64, H_k=8, 16384 ragged e4m3 keys 84 us, 4.1 TB/s.  There a
+// group's chain S -> softmax -> P V -> next S takes 3000 cycles a tile of its
+// own, and of the time 4 us are launch and schedule, 7 to 10 the spread of the
+// CTAs' ends, 5 the merge.  B=1, T=8, 1000 keys: 13.7 us, all latency.
 #include "fmha_cache.cuh"
 
 namespace fmha {

@@ -18,12 +18,21 @@
 //
 // A unit is 512 keys of one kv head (four MMA tiles that share the query
 // stream: with two, a chunk took the 1950 cycles that the SMs together need to
-// fetch theirs from L2) and its query chunks (TB = 128 / G tokens each).  The chunks of all
-// units form one sequence, kv heads fastest, so that a CTA reads the heads'
-// rows of the same keys one after another (they are adjacent in the cache);
-// the sequence is cut evenly over the CTAs; a unit that is cut
-// leaves partial sums (a float a key) in the workspace and a second kernel adds
-// them in CTA order, so results do not depend on timing.
+// fetch theirs from L2) and its query chunks (TB = 128 / G tokens each).  The
+// chunks of all units form one sequence, kv heads fastest, so that a CTA reads
+// the heads' rows of the same keys one after another (they are adjacent in the
+// cache).  The sequence is cut evenly over the CTAs; a unit that is cut leaves
+// partial sums (a float a key) in the workspace and a second kernel adds them
+// in CTA order, so results do not depend on timing.
+//
+// Measured: one token a sequence (B=32, H=32, H_k=8, 8192 keys, ragged) 63 us,
+// 5.6 TB/s of keys; the last 33 tokens of four e4m3 prompts of 16384 (H=64,
+// H_k=8) 33 us; every row of a prompt of 4096 (H=32, H_k=8, causal) 67 us,
+// 1.02 PFLOP/s.  A chunk takes 3700 cycles where its MMAs and its exponentials
+// need 2050 each: S has one TMEM buffer a tile, so the chain freed -> issued ->
+// there -> loaded -> half of it added is serial for a tile, and four tiles in
+// flight do not fill either unit (without the exponentials the prompt takes
+// 62 us, without the LSE loads 64, without both and 7/8 of the MMAs 47).
 #include "fmha_cache.cuh"
 
 namespace fmha {
@@ -468,16 +477,16 @@ __device__ void w_sum(const WParams &p, WBars *bars, uint32_t tmem, int warp, in
                 for (int q = 0; q < cols; q += 32) {
                     // a bit for every column that counts; the others' scores become -inf
                     const int l = lo - q, h = cols - q;
-                    const uint32_t m = (l <= 0 ? 0xffffffffu : l >= 32 ? 0u : 0xffffffffu << l) &
-                                       (h >= 32 ? 0xffffffffu : (1u << h) - 1u);
-                    if (__all_sync(0xffffffffu, m == 0u)) continue;
+                    const uint32_t vis = (l <= 0 ? 0xffffffffu : l >= 32 ? 0u : 0xffffffffu << l) &
+                                         (h >= 32 ? 0xffffffffu : (1u << h) - 1u);
+                    if (__all_sync(0xffffffffu, vis == 0u)) continue;
                     uint32_t s[32];
                     tmem_ld32(s_tm + q, s);
                     tmem_wait_ld(s);
-                    if (!__all_sync(0xffffffffu, m == 0xffffffffu)) {
+                    if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) {
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
-                            if (!((m >> k) & 1u)) s[k] = 0xff800000u;
+                            if (!((vis >> k) & 1u)) s[k] = 0xff800000u;
                     }
                     add(s, q);
                 }
@@ -498,11 +507,8 @@ __device__ void w_sum(const WParams &p, WBars *bars, uint32_t tmem, int warp, in
             parts |= 1 << slot;
             p.part[((int64_t)2 * blockIdx.x + slot) * p.UK + r] = total;
             if (threadIdx.x == 0) {
-                WMeta m;
-                m.row = at;
-                m.keys = it.entry < 0 ? 0 : imin(p.UK, it.L - it.tile * p.UK);
-                m.last = it.ends;
-                p.meta[2 * blockIdx.x + slot] = m;
+                const int keys = it.entry < 0 ? 0 : imin(p.UK, it.L - it.tile * p.UK);
+                p.meta[2 * blockIdx.x + slot] = WMeta{at, keys, it.ends};
             }
         }
     }
