@@ -77,6 +77,10 @@ struct TreeCfg : ElemCfg<ELEM> {
     // log2 of the largest P right after the reference is set; up to 2^8 later.
     // e4m3 underflows 2^9 below 1, so its weights start 2^4 up.
     static constexpr float BIAS = B::FP8 ? 4.f : 0.f;
+    // What a unit's ends cost a CTA, in tiles' time: the ring runs empty and is
+    // filled again (of 16 ragged f16 sequences, 40 us, a CTA of two units' parts
+    // would end 4 us after one that stays in a unit).
+    static constexpr int EDGE = NS / 2;
     // TMEM: S of each group, P over S, then O of each group
     static constexpr int O_COL = 2 * kRows;
 };
@@ -97,6 +101,7 @@ struct TreeParams {
     int B, T, H, H_k, G, B_cache, S_max;
     int TB;                             // tokens of a row block
     int NRB;
+    int edge;                           // tiles that a unit's ends cost beside its own
     int ncta;
     float c;                            // scale * log2(e)
     float out_scale;
@@ -120,7 +125,8 @@ static_assert(sizeof(TreeBars) <= 1024, "barrier block");
 
 // ---------------------------------------------------------------------------
 // Work: the tiles of all (sequence b, kv head g, row-block group u), u fastest
-// so that the units that read the same keys run at the same time.
+// so that the units that read the same keys run at the same time.  A unit is
+// `edge` tiles of nothing, for the work at its ends, and then its own.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ int tree_cached(const TreeParams &p, int b, bool report) {
@@ -137,12 +143,12 @@ __device__ __forceinline__ int tree_tiles(int L, int n) { return (L + kRows - 1)
 
 __device__ __forceinline__ int64_t tree_seq_tiles(const TreeParams &p, int b) {
     const int n = tree_drafts(p, b, false);
-    return (int64_t)p.H_k * tree_groups(p, n) * tree_tiles(tree_cached(p, b, false), n);
+    return (int64_t)p.H_k * tree_groups(p, n) * (tree_tiles(tree_cached(p, b, false), n) + p.edge);
 }
 
 // Where the producer is in this CTA's tiles [G0, G1).
 struct TreeCursor {
-    int64_t off, G0, G1;                // off: first tile of the unit at hand
+    int64_t off, G0, G1;                // off: where the unit at hand begins
     int b, g, u;
     int L, n, entry, nt, nu;            // of sequence b
 };
@@ -190,8 +196,8 @@ __device__ void tree_schedule(const TreeParams &p, TreeCursor &cur, int lane) {
             cur.off = __shfl_sync(0xffffffffu, base + incl - n, l);
             tree_load_seq(p, cur);
             // whole units of this sequence that end at or before G0
-            const int skip = (int)((cur.G0 - cur.off) / cur.nt);
-            cur.off += (int64_t)skip * cur.nt;
+            const int skip = (int)((cur.G0 - cur.off) / (cur.nt + p.edge));
+            cur.off += (int64_t)skip * (cur.nt + p.edge);
             cur.g = skip / cur.nu;
             cur.u = skip % cur.nu;
             return;
@@ -208,8 +214,9 @@ __device__ bool tree_next(const TreeParams &p, TreeCursor &cur, TreeItem &it) {
         cur.g = cur.u = 0;
         tree_load_seq(p, cur);
     }
-    it.t0 = (int)(max(cur.G0, cur.off) - cur.off);
-    it.t1 = (int)(min(cur.G1, cur.off + cur.nt) - cur.off);
+    it.t0 = imax(0, (int)(max(cur.G0, cur.off) - cur.off) - p.edge);
+    it.t1 = (int)(min(cur.G1, cur.off + p.edge + cur.nt) - cur.off) - p.edge;
+    if (it.t1 <= 0) return false;       // the range ends before the unit's first tile
     it.b = cur.b;
     it.g = cur.g;
     it.u = cur.u;
@@ -218,7 +225,7 @@ __device__ bool tree_next(const TreeParams &p, TreeCursor &cur, TreeItem &it) {
     it.n = cur.n;
     it.nt = cur.nt;
     it.nc = (cur.L + kRows - 1) / kRows;
-    cur.off += cur.nt;
+    cur.off += p.edge + cur.nt;
     if (++cur.u == cur.nu) {
         cur.u = 0;
         ++cur.g;
@@ -962,6 +969,10 @@ TreeKernel tree_kernel_for(int dt) {
            : dt == FMHA_F16 ? fmha_tree_kernel<FMHA_F16, SPLIT> : fmha_tree_kernel<FMHA_E4M3, SPLIT>;
 }
 template <int ELEM>
+int tree_edge(int nrb) {
+    return nrb == 2 ? TreeCfg<ELEM, false>::EDGE : TreeCfg<ELEM, true>::EDGE;
+}
+template <int ELEM>
 int tree_smem(int nrb) {
     return nrb == 2 ? TreeCfg<ELEM, false>::SMEM_BYTES : TreeCfg<ELEM, true>::SMEM_BYTES;
 }
@@ -1040,6 +1051,7 @@ extern "C" int fmha_tree_fwd(fmha_tensor q, fmha_tensor k_cache, fmha_tensor v_c
     p.S_max = S_max;
     p.TB = sh.TB;
     p.NRB = sh.NRB;
+    p.edge = dt == FMHA_E4M3 ? tree_edge<FMHA_E4M3>(sh.NRB) : tree_edge<FMHA_BF16>(sh.NRB);
     p.ncta = imin(sms, tree_ctas(tree_max_tiles(sh, B, T, H_k, S_max)));
     p.part_o = static_cast<float *>(workspace);
     p.part_lse = p.part_o + (size_t)2 * p.ncta * sh.NRB * kRows * kD;
