@@ -460,7 +460,7 @@ __device__ void w_sum(const WParams &p, WBars *bars, uint32_t tmem, int warp, in
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[x]));
             };
-            if (cols == kRows && __all_sync(0xffffffffu, lo == 0)) {
+            if (p.NMMA == kRows && cols == p.TB * p.G && __all_sync(0xffffffffu, lo == 0)) {
 #pragma unroll 1
                 for (int q = 0; q < kRows; q += 64) {
                     uint32_t s[2][32];
@@ -554,6 +554,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
     if (warp == kWMma) {
         tmem_alloc(smem_u32(&bars->tmem_base), 512);
         tmem_relinquish();
+    }
+    // rows of a full chunk that hold no query (G = 3: two) are zero, so that
+    // all 128 columns can be summed (those have an LSE that makes them 0)
+    if (p.NMMA == kRows && p.TB * p.G < kRows) {
+        const int pieces = (kRows - p.TB * p.G) * 8;
+        for (int i = threadIdx.x; i < pieces * C::NQ * C::PANELS; i += kWThreads)
+            *reinterpret_cast<uint4 *>(smem + C::OFF_Q + (i / pieces) * kPanelBytes + p.TB * p.G * 128 + i % pieces * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        proxy_fence();
     }
     WCursor cur;
     int gate = 0;
