@@ -35,14 +35,15 @@
 // workspace, at most two per CTA, and a second kernel joins them; units that
 // one CTA covers are written to O directly.
 //
-// Measured (kernel and merge): B=32, T=64, 8192 keys, H=32, H_k=8, bf16 223 us:
-// 5.0 TB/s and 1.24 PFLOP/s at once, near both; the two groups take a 64 KB pair
+// Measured (kernel and merge): B=32, T=64, 8192 keys, H=32, H_k=8, bf16 221 us:
+// 5.0 TB/s and 1.25 PFLOP/s at once, near both; the two groups take a 64 KB pair
 // of K and V tiles in 3100 cycles, at the copy rate it would arrive in 2840.
-// One row block (SPLIT): B=16, T=27, 4096 ragged f16 keys 53.5 us, 3.4 TB/s;
-// B=16, T=5, H=64, H_k=8, 16384 ragged e4m3 keys 84 us, 4.1 TB/s.  There a
-// group's chain S -> softmax -> P V -> next S takes 3000 cycles a tile of its
-// own, and of the time 4 us are launch and schedule, 7 to 10 the spread of the
-// CTAs' ends, 5 the merge.  B=1, T=8, 1000 keys: 13.7 us, all latency.
+// One row block (SPLIT): B=16, T=27, 4096 ragged f16 keys 51 us, 3.5 TB/s
+// (between the first and the last tile 5.8); B=16, T=5, H=64, H_k=8, 16384
+// ragged e4m3 keys 82 us, 4.2 TB/s.  There a group's chain S -> softmax -> P V
+// -> next S takes 3000 cycles a tile of its own; of the time 4 us pass before
+// the first S, 4 at a unit's ends, 5 between the first CTA's end and the last,
+// and 4 to 6 in the merge.  B=1, T=8, 1000 keys: 13.7 us, all latency.
 #include "fmha_cache.cuh"
 
 namespace fmha {
@@ -814,7 +815,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 // of the schedule is worked out again.  Nearly every cut unit has two
 // partials: their rows are fetched in the same round trip as the metadata and
 // joined by straight code (the kernel is short enough that its instruction
-// fetches count); more partials take the loop.
+// fetches count); more partials take the loop.  Bound by L2: 64 drafts of 32
+// sequences leave 40 MB of partials, read in 9.6 us (four rows a warp, all
+// loads first, made 16 sequences of 27 drafts 55 us instead of 51).
 constexpr int kMergeWarps = 8;
 
 template <int ELEM>
