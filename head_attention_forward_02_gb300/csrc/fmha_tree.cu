@@ -81,7 +81,7 @@ struct TreeCfg : ElemCfg<ELEM> {
     // What a unit's ends cost a CTA, in tiles' time: the ring runs empty and is
     // filled again (of 16 ragged f16 sequences, 40 us, a CTA of two units' parts
     // would end 4 us after one that stays in a unit).
-    static constexpr int EDGE = NS / 2;
+    [[maybe_unused]] static constexpr int EDGE = NS / 2;
     // TMEM: S of each group, P over S, then O of each group
     static constexpr int O_COL = 2 * kRows;
 };
@@ -103,6 +103,7 @@ struct TreeParams {
     int TB;                             // tokens of a row block
     int NRB;
     int edge;                           // tiles that a unit's ends cost beside its own
+    int whole;                          // units are not cut: a CTA takes those that begin in its part
     int ncta;
     float c;                            // scale * log2(e)
     float out_scale;
@@ -196,8 +197,8 @@ __device__ void tree_schedule(const TreeParams &p, TreeCursor &cur, int lane) {
             cur.b = bb + l;
             cur.off = __shfl_sync(0xffffffffu, base + incl - n, l);
             tree_load_seq(p, cur);
-            // whole units of this sequence that end at or before G0
-            const int skip = (int)((cur.G0 - cur.off) / (cur.nt + p.edge));
+            // units of this sequence that end at or before G0, or begin before it
+            const int skip = (int)((cur.G0 - cur.off + (p.whole ? cur.nt + p.edge - 1 : 0)) / (cur.nt + p.edge));
             cur.off += (int64_t)skip * (cur.nt + p.edge);
             cur.g = skip / cur.nu;
             cur.u = skip % cur.nu;
@@ -215,8 +216,8 @@ __device__ bool tree_next(const TreeParams &p, TreeCursor &cur, TreeItem &it) {
         cur.g = cur.u = 0;
         tree_load_seq(p, cur);
     }
-    it.t0 = imax(0, (int)(max(cur.G0, cur.off) - cur.off) - p.edge);
-    it.t1 = (int)(min(cur.G1, cur.off + p.edge + cur.nt) - cur.off) - p.edge;
+    it.t0 = p.whole ? 0 : imax(0, (int)(max(cur.G0, cur.off) - cur.off) - p.edge);
+    it.t1 = p.whole ? cur.nt : (int)(min(cur.G1, cur.off + p.edge + cur.nt) - cur.off) - p.edge;
     if (it.t1 <= 0) return false;       // the range ends before the unit's first tile
     it.b = cur.b;
     it.g = cur.g;
@@ -960,6 +961,21 @@ int64_t tree_max_tiles(const TreeShape &s, int B, int T, int H_k, int S_max) {
     return (int64_t)B * H_k * s.groups * (((int64_t)S_max + kRows - 1) / kRows + (T + kRows - 1) / kRows);
 }
 
+// Are units left whole?  Then there are no partials and no merge (the host saves
+// 2.7 us of 25 as well), but a CTA may take a unit more than its share.  So they
+// are where the longest CTA, by the cache's size since only the device knows the
+// lengths, has few tiles: six, or ten of two blocks, whose partials are twice
+// as large, if no more than six of them are above the average.  Cut / whole in
+// us, H_k=8, G=4: B=1 T=8 256 keys 11.6 / 11.0, 768 13.7 / 13.7, 1000 13.7 / 15.1;
+// B=4, 500 ragged 15.9 / 13.0; B=32, 256 24.0 / 20.5; B=24, 500 ragged 23.7 / 25.3;
+// B=16, 1000 ragged 23.3 / 26.0; two blocks (T=64): B=1, 512 19.1 / 17.7, 1000
+// 20.6 / 24.0; B=8, 500 28.7 / 19.1; B=16, 1000 42.8 / 30.0, ragged 38.6 / 36.5.
+bool tree_whole(const TreeShape &s, int B, int T, int H_k, int S_max, int ncta) {
+    const int64_t units = (int64_t)B * H_k * s.groups, tiles = tree_max_tiles(s, B, T, H_k, S_max) / units;
+    const int64_t most = tiles * ((units + ncta - 1) / ncta);
+    return most <= (s.NRB == 2 ? 10 : 6) && most * ncta - tiles * units <= (int64_t)6 * ncta;
+}
+
 bool tree_sizes_ok(int B, int T, int H, int H_k, int D, int S_max) {
     return B > 0 && T > 0 && H > 0 && H_k > 0 && H % H_k == 0 && H / H_k <= kRows && D == kD && S_max > 0 &&
            S_max <= kMaxCacheRows;
@@ -1056,6 +1072,7 @@ extern "C" int fmha_tree_fwd(fmha_tensor q, fmha_tensor k_cache, fmha_tensor v_c
     p.NRB = sh.NRB;
     p.edge = dt == FMHA_E4M3 ? tree_edge<FMHA_E4M3>(sh.NRB) : tree_edge<FMHA_BF16>(sh.NRB);
     p.ncta = imin(sms, tree_ctas(tree_max_tiles(sh, B, T, H_k, S_max)));
+    p.whole = tree_whole(sh, B, T, H_k, S_max, p.ncta);
     p.part_o = static_cast<float *>(workspace);
     p.part_lse = p.part_o + (size_t)2 * p.ncta * sh.NRB * kRows * kD;
     p.meta = reinterpret_cast<TreeMeta *>(p.part_lse + (size_t)2 * p.ncta * sh.NRB * kRows);
@@ -1087,6 +1104,7 @@ extern "C" int fmha_tree_fwd(fmha_tensor q, fmha_tensor k_cache, fmha_tensor v_c
         return cuda_failed();
     kern<<<p.ncta, kTreeThreads, smem, stream>>>(tq, tc[0], tc[1], tn[0], tn[1], p);
     if (cudaGetLastError() != cudaSuccess) return FMHA_ERR_CUDA;
+    if (p.whole) return FMHA_OK;
 
     const int rows = sh.NRB * p.TB * p.G;                 // of a unit
     auto merge = dt == FMHA_BF16 ? fmha_tree_merge_kernel<FMHA_BF16>

@@ -117,6 +117,29 @@ def test_tree_matches_the_formula(fm, name):
     check(c, o, lse)
 
 
+# the same lengths in caches whose size leaves units whole, or has them cut
+SIZES = {
+    "one_block": dict(dtype="bf16", T=7, H=9, H_k=3, seqlen=[127, 128, 129, 0, 300], n_draft=[7, 1, 3, 5, 0]),
+    "two_blocks": dict(dtype="f16", T=64, H=8, H_k=2, seqlen=[541, 0, 512, 130], n_draft=[64, 33, 32, 1]),
+    "three_blocks": dict(dtype="e4m3", T=40, H=16, H_k=2, seqlen=[300, 399], n_draft=[40, 17]),
+    "two_draft_tiles": dict(dtype="bf16", T=131, H=2, H_k=2, seqlen=[77, 200, 0], n_draft=[131, 128, 129]),
+    "rows_without_keys": dict(dtype="bf16", T=20, H=8, H_k=2, seqlen=[0, 0, 5], n_draft=[20, 9, 20], mask="any"),
+    "more_units_than_ctas": dict(dtype="bf16", T=3, H=8, H_k=8, seqlen=[(i * 41) % 250 for i in range(50)],
+                                 n_draft=[i % 4 for i in range(50)]),
+}
+
+
+@pytest.mark.parametrize("S_max", [600, 5000])
+@pytest.mark.parametrize("name", SIZES)
+def test_tree_of_whole_and_of_cut_units(fm, name, S_max):
+    c = make(seed=50 + len(name), S_max=S_max, **SIZES[name])
+    d, (o, lse) = on_gpu(c), outputs(c)
+    fm.tree_fwd(*d["args"], **d["kw"], out=o, lse=lse)
+    torch.cuda.synchronize()
+    assert fm.device_status(reset=True) == 0
+    check(c, o, lse)
+
+
 def test_tree_scales_and_no_lse(fm):
     c = make("bf16", 6, 8, 2, 300, [290, 3], seed=5)
     d, (o, lse) = on_gpu(c), outputs(c)
