@@ -81,7 +81,8 @@ struct TreeCfg : ElemCfg<ELEM> {
     // What a unit's ends cost a CTA, in tiles' time: the ring runs empty and is
     // filled again (of 16 ragged f16 sequences, 40 us, a CTA of two units' parts
     // would end 4 us after one that stays in a unit).
-    [[maybe_unused]] static constexpr int EDGE = NS / 2;
+    static constexpr int EDGE = NS / 2;
+    static_assert(EDGE >= 1, "a ring of two tiles");
     // TMEM: S of each group, P over S, then O of each group
     static constexpr int O_COL = 2 * kRows;
 };

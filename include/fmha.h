@@ -310,7 +310,8 @@ size_t fmha_gen_workspace_size(int B, int H, int H_k, int D, int S_max);
  * workspace: caller-owned scratch of at least fmha_tree_workspace_size(...)
  * bytes, 256-byte aligned; nothing in it needs initialising; it must not be
  * shared with a call that may run concurrently.  The call allocates nothing
- * and is asynchronous on `stream` (a kernel, and a merge kernel unless the cache is short).
+ * and is asynchronous on `stream` (a kernel, and a merge kernel unless the
+ * cache is short).
  * Returns FMHA_OK, FMHA_ERR_INVALID_ARG (bad sizes or pointers, scale not
  * finite and > 0, mask stride, workspace too small or misaligned),
  * FMHA_ERR_UNSUPPORTED (dtype, alignment, device) or FMHA_ERR_CUDA.  B = 0 or
