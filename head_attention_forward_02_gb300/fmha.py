@@ -342,20 +342,37 @@ def fmha_tree_commit(k_cache, v_cache, k_new, v_new, B, T, P, H_k, D, B_cache, S
 
 
 # The operators below are called once a layer and token, where a call's Python
-# steps outlast its kernels: every tensor is looked at once, and the C function
-# is called directly (tree_fwd: 41 -> 24 us to enqueue).
+# steps outlast its kernels.  So tensors are looked at once, a group at a time
+# (_check only names what did not fit), the C function is called directly, and
+# scratch comes from torch's allocator without a tensor around it, which alone
+# took 6 us (tree_fwd: 41 -> 24 -> 19 us, weights 20 -> 14 to enqueue).
+_current_device, _raw_stream, _alloc, _free = (
+    getattr(torch._C, name, None) for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream",
+                                               "_cuda_cudaCachingAllocator_raw_alloc",
+                                               "_cuda_cudaCachingAllocator_raw_delete"))
 
-def _check(name: str, t, shape: tuple, dtype, index: int) -> None:
-    """Refuse a tensor that the library would misread: it takes only an address."""
-    if t is None or (t.shape == shape and t.dtype is dtype and t.get_device() == index and t.is_contiguous()):
-        return
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, not on the call's device cuda:{index}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
-    raise ValueError(f"{name} is not contiguous")
+
+def _fit(index: int, dtype, shape: tuple, *tensors) -> bool:
+    """Would the library, which takes only addresses, read these tensors right?"""
+    for t in tensors:
+        if t is not None and not (t.dtype is dtype and t.shape == shape and t.get_device() == index
+                                  and t.is_contiguous()):
+            return False
+    return True
+
+
+def _check(index: int, dtype, shape: tuple, **tensors) -> None:
+    """Refuse the first of the tensors that the library would misread."""
+    for name, t in tensors.items():
+        if _fit(index, dtype, shape, t):
+            continue
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, not on the call's device cuda:{index}")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, not {dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        raise ValueError(f"{name} is not contiguous")
 
 
 def _device_and_code(t: torch.Tensor) -> Tuple[int, int]:
@@ -381,18 +398,13 @@ def _on(stream, index: int):
     return torch.cuda.stream(stream)
 
 
-def _raw_stream(index: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(index)
-
-
-def _workspace(workspace, nbytes: int, device) -> Tuple[torch.Tensor, int]:
-    if workspace is None:
-        workspace = torch.empty(nbytes or 1, dtype=torch.uint8, device=device)
-    elif workspace.device != device:
-        raise ValueError(f"workspace is on {workspace.device}, not on {device}")
-    elif not workspace.is_contiguous():
+def _given(workspace: torch.Tensor, index: int) -> Tuple[int, int]:
+    """Address and bytes of a caller's workspace."""
+    if workspace.get_device() != index:
+        raise ValueError(f"workspace is on {workspace.device}, not on cuda:{index}")
+    if not workspace.is_contiguous():
         raise ValueError("workspace is not contiguous")
-    return workspace, workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _raise(rc: int) -> None:
@@ -418,7 +430,7 @@ def tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_ne
     workspace with torch when not given; rows of drafts at or past n_draft[b]
     are not written.  Returns (O, LSE)."""
     index, code = _device_and_code(q)
-    if stream is not None or torch.cuda.current_device() != index:
+    if stream is not None or _current_device() != index:
         with _on(stream, index):
             return tree_fwd(q, k_cache, v_cache, k_new, v_new, seqlen, tree_mask=tree_mask, n_draft=n_draft,
                             batch_idx=batch_idx, scale=scale, out_scale=out_scale, out=out, lse=lse,
@@ -427,33 +439,43 @@ def tree_fwd(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_ne
         raise ValueError("q is [B, T, H, 128] and the caches are [B_cache, S_max, H_k, 128]")
     (B, T, H, D), (B_cache, S_max, H_k, _) = q.shape, k_cache.shape
     dt, cache, new, per_seq = q.dtype, (B_cache, S_max, H_k, D), (B, T, H_k, D), (B,)
-    _check("q", q, (B, T, H, D), dt, index)
-    _check("k_cache", k_cache, cache, dt, index)
-    _check("v_cache", v_cache, cache, dt, index)
-    _check("k_new", k_new, new, dt, index)
-    _check("v_new", v_new, new, dt, index)
-    _check("seqlen", seqlen, per_seq, torch.int32, index)
-    _check("n_draft", n_draft, per_seq, torch.int32, index)
-    _check("batch_idx", batch_idx, per_seq, torch.int32, index)
+    if not (_fit(index, dt, cache, k_cache, v_cache) and _fit(index, dt, new, k_new, v_new)
+            and _fit(index, torch.int32, per_seq, seqlen, n_draft, batch_idx)):
+        _check(index, dt, cache, k_cache=k_cache, v_cache=v_cache)
+        _check(index, dt, new, k_new=k_new, v_new=v_new)
+        _check(index, torch.int32, per_seq, seqlen=seqlen, n_draft=n_draft, batch_idx=batch_idx)
     stride = 0
     if tree_mask is not None:
         if tree_mask.dtype not in (torch.bool, torch.uint8):
             raise ValueError(f"tree_mask has dtype {tree_mask.dtype}, not bool or uint8")
-        stride = 0 if tree_mask.dim() == 2 else T * T
-        _check("tree_mask", tree_mask, (T, T) if tree_mask.dim() == 2 else (B, T, T), tree_mask.dtype, index)
+        each = tree_mask.dim() == 3
+        stride = T * T if each else 0
+        if not _fit(index, tree_mask.dtype, (B, T, T) if each else (T, T), tree_mask):
+            _check(index, tree_mask.dtype, (B, T, T) if each else (T, T), tree_mask=tree_mask)
     if out is None:
         out = torch.empty_like(q)
     if lse is None and return_lse:
         lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
-    _check("out", out, (B, T, H, D), dt, index)
-    _check("lse", lse, (B, H, T), torch.float32, index)
-    ws, nbytes = _workspace(workspace, _tree_workspace_size(B, T, H, H_k, D, S_max), q.device)
-    _raise(lib().fmha_tree_fwd(
-        fmha_tensor(q.data_ptr(), code), fmha_tensor(k_cache.data_ptr(), code), fmha_tensor(v_cache.data_ptr(), code),
-        fmha_tensor(k_new.data_ptr(), code), fmha_tensor(v_new.data_ptr(), code), fmha_tensor(out.data_ptr(), code),
-        _ptr(lse), B, T, H, H_k, D, B_cache, S_max, seqlen.data_ptr(), _ptr(batch_idx), _ptr(n_draft),
-        _ptr(tree_mask), stride, 1.0 / math.sqrt(D) if scale is None else scale, out_scale, ws.data_ptr(), nbytes,
-        _raw_stream(index)))
+    if not (_fit(index, dt, q.shape, q, out) and _fit(index, torch.float32, (B, H, T), lse)):
+        _check(index, dt, q.shape, q=q, out=out)
+        _check(index, torch.float32, (B, H, T), lse=lse)
+    raw = _raw_stream(index)
+    if workspace is None:
+        nbytes = _tree_workspace_size(B, T, H, H_k, D, S_max)
+        ws = _alloc(nbytes or 1, raw)
+    else:
+        ws, nbytes = _given(workspace, index)
+    try:
+        rc = lib().fmha_tree_fwd(
+            fmha_tensor(q.data_ptr(), code), fmha_tensor(k_cache.data_ptr(), code),
+            fmha_tensor(v_cache.data_ptr(), code), fmha_tensor(k_new.data_ptr(), code),
+            fmha_tensor(v_new.data_ptr(), code), fmha_tensor(out.data_ptr(), code), _ptr(lse), B, T, H, H_k, D, B_cache,
+            S_max, seqlen.data_ptr(), _ptr(batch_idx), _ptr(n_draft), _ptr(tree_mask), stride,
+            1.0 / math.sqrt(D) if scale is None else scale, out_scale, ws, nbytes, raw)
+    finally:
+        if workspace is None:
+            _free(ws)                       # for what this stream runs next
+    _raise(rc)
     return out, lse
 
 
@@ -465,21 +487,20 @@ def tree_commit(k_cache: torch.Tensor, v_cache: torch.Tensor, k_new: torch.Tenso
     seqlen[b] + i of sequence b's entry.  path int32 [B, P]; n_accept, seqlen,
     batch_idx int32 [B].  seqlen is not changed."""
     index, code = _device_and_code(k_cache)
-    if stream is not None or torch.cuda.current_device() != index:
+    if stream is not None or _current_device() != index:
         with _on(stream, index):
             return tree_commit(k_cache, v_cache, k_new, v_new, seqlen, path, n_accept, batch_idx=batch_idx)
     if k_cache.dim() != 4 or k_new.dim() != 4 or path.dim() != 2:
         raise ValueError("the caches are [B_cache, S_max, H_k, 128], k_new is [B, T, H_k, 128] and path is [B, P]")
     (B_cache, S_max, H_k, D), (B, T, _, _), P = k_cache.shape, k_new.shape, path.shape[1]
     dt, cache, new, per_seq = k_cache.dtype, (B_cache, S_max, H_k, D), (B, T, H_k, D), (B,)
-    _check("k_cache", k_cache, cache, dt, index)
-    _check("v_cache", v_cache, cache, dt, index)
-    _check("k_new", k_new, new, dt, index)
-    _check("v_new", v_new, new, dt, index)
-    _check("path", path, (B, P), torch.int32, index)
-    _check("seqlen", seqlen, per_seq, torch.int32, index)
-    _check("n_accept", n_accept, per_seq, torch.int32, index)
-    _check("batch_idx", batch_idx, per_seq, torch.int32, index)
+    if not (_fit(index, dt, cache, k_cache, v_cache) and _fit(index, dt, new, k_new, v_new)
+            and _fit(index, torch.int32, per_seq, seqlen, n_accept, batch_idx)
+            and _fit(index, torch.int32, (B, P), path)):
+        _check(index, dt, cache, k_cache=k_cache, v_cache=v_cache)
+        _check(index, dt, new, k_new=k_new, v_new=v_new)
+        _check(index, torch.int32, per_seq, seqlen=seqlen, n_accept=n_accept, batch_idx=batch_idx)
+        _check(index, torch.int32, (B, P), path=path)
     _raise(lib().fmha_tree_commit(
         fmha_tensor(k_cache.data_ptr(), code), fmha_tensor(v_cache.data_ptr(), code),
         fmha_tensor(k_new.data_ptr(), code), fmha_tensor(v_new.data_ptr(), code), B, T, P, H_k, D, B_cache, S_max,
@@ -525,7 +546,7 @@ def cache_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor, seq
     or "causal" (q-end).  Updates acc in place unless ``out`` is given; with
     neither, returns a new array that is zero past every length."""
     index, code = _device_and_code(q)
-    if stream is not None or torch.cuda.current_device() != index:
+    if stream is not None or _current_device() != index:
         with _on(stream, index):
             return cache_weights(q, k_cache, lse, seqlen, acc=acc, out=out, n_query=n_query, batch_idx=batch_idx,
                                  mask=mask, scale=scale, workspace=workspace)
@@ -537,22 +558,32 @@ def cache_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.Tensor, seq
         raise ValueError(f"mask is none or causal, not {mask!r}")
     (B, Sq, H, D), (B_cache, S_max, H_k, _) = q.shape, k_cache.shape
     dt, scores, per_seq = q.dtype, (B_cache, H_k, S_max), (B,)
-    _check("q", q, (B, Sq, H, D), dt, index)
-    _check("k_cache", k_cache, (B_cache, S_max, H_k, D), dt, index)
-    _check("lse", lse, (B, H, Sq), torch.float32, index)
-    _check("seqlen", seqlen, per_seq, torch.int32, index)
-    _check("n_query", n_query, per_seq, torch.int32, index)
-    _check("batch_idx", batch_idx, per_seq, torch.int32, index)
+    if not (_fit(index, dt, q.shape, q) and _fit(index, dt, (B_cache, S_max, H_k, D), k_cache)
+            and _fit(index, torch.float32, (B, H, Sq), lse)
+            and _fit(index, torch.int32, per_seq, seqlen, n_query, batch_idx)):
+        _check(index, dt, q.shape, q=q)
+        _check(index, dt, (B_cache, S_max, H_k, D), k_cache=k_cache)
+        _check(index, torch.float32, (B, H, Sq), lse=lse)
+        _check(index, torch.int32, per_seq, seqlen=seqlen, n_query=n_query, batch_idx=batch_idx)
     if out is None:
         out = torch.zeros(scores, dtype=torch.float32, device=q.device) if acc is None else acc
-    _check("acc", acc, scores, torch.float32, index)
-    _check("out", out, scores, torch.float32, index)
-    ws, nbytes = _workspace(workspace, _weights_workspace_size(), q.device)
-    _raise(lib().fmha_cache_weights(
-        fmha_tensor(q.data_ptr(), code), fmha_tensor(k_cache.data_ptr(), code), lse.data_ptr(), _ptr(acc),
-        out.data_ptr(), B, Sq, H, H_k, D, B_cache, S_max, seqlen.data_ptr(), _ptr(batch_idx), _ptr(n_query),
-        1.0 / math.sqrt(D) if scale is None else scale, _MASKS[mask], ws.data_ptr(), nbytes,
-        _raw_stream(index)))
+    if not _fit(index, torch.float32, scores, acc, out):
+        _check(index, torch.float32, scores, acc=acc, out=out)
+    raw = _raw_stream(index)
+    if workspace is None:
+        nbytes = _weights_workspace_size()
+        ws = _alloc(nbytes, raw)
+    else:
+        ws, nbytes = _given(workspace, index)
+    try:
+        rc = lib().fmha_cache_weights(
+            fmha_tensor(q.data_ptr(), code), fmha_tensor(k_cache.data_ptr(), code), lse.data_ptr(), _ptr(acc),
+            out.data_ptr(), B, Sq, H, H_k, D, B_cache, S_max, seqlen.data_ptr(), _ptr(batch_idx), _ptr(n_query),
+            1.0 / math.sqrt(D) if scale is None else scale, _MASKS[mask], ws, nbytes, raw)
+    finally:
+        if workspace is None:
+            _free(ws)                       # for what this stream runs next
+    _raise(rc)
     return out
 
 
@@ -568,7 +599,7 @@ def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor,
     H_k, 128] and acc_out [B_out, H_k, S_out] are given (out_idx: their
     entries).  Returns (kept int32 [B, H_k, budget], new_seqlen int32 [B])."""
     index, code = _device_and_code(k_cache)
-    if stream is not None or torch.cuda.current_device() != index:
+    if stream is not None or _current_device() != index:
         with _on(stream, index):
             return cache_evict(k_cache, v_cache, acc, seqlen, budget, recent=recent, batch_idx=batch_idx, k_out=k_out,
                                v_out=v_out, acc_out=acc_out, out_idx=out_idx, kept=kept, new_seqlen=new_seqlen)
@@ -585,17 +616,16 @@ def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor,
         kept = torch.empty((B, H_k, max(budget, 0)), dtype=torch.int32, device=k_cache.device)
     if new_seqlen is None:
         new_seqlen = torch.empty(per_seq, dtype=torch.int32, device=k_cache.device)
-    _check("k_cache", k_cache, cache, dt, index)
-    _check("v_cache", v_cache, cache, dt, index)
-    _check("acc", acc, (B_cache, H_k, S_max), torch.float32, index)
-    _check("k_out", k_out, moved, dt, index)
-    _check("v_out", v_out, moved, dt, index)
-    _check("acc_out", acc_out, (B_out, H_k, S_out), torch.float32, index)
-    _check("seqlen", seqlen, per_seq, torch.int32, index)
-    _check("batch_idx", batch_idx, per_seq, torch.int32, index)
-    _check("out_idx", out_idx, per_seq, torch.int32, index)
-    _check("new_seqlen", new_seqlen, per_seq, torch.int32, index)
-    _check("kept", kept, (B, H_k, max(budget, 0)), torch.int32, index)
+    if not (_fit(index, dt, cache, k_cache, v_cache) and _fit(index, torch.float32, (B_cache, H_k, S_max), acc)
+            and _fit(index, dt, moved, k_out, v_out) and _fit(index, torch.float32, (B_out, H_k, S_out), acc_out)
+            and _fit(index, torch.int32, per_seq, seqlen, batch_idx, out_idx, new_seqlen)
+            and _fit(index, torch.int32, (B, H_k, max(budget, 0)), kept)):
+        _check(index, dt, cache, k_cache=k_cache, v_cache=v_cache)
+        _check(index, torch.float32, (B_cache, H_k, S_max), acc=acc)
+        _check(index, dt, moved, k_out=k_out, v_out=v_out)
+        _check(index, torch.float32, (B_out, H_k, S_out), acc_out=acc_out)
+        _check(index, torch.int32, per_seq, seqlen=seqlen, batch_idx=batch_idx, out_idx=out_idx, new_seqlen=new_seqlen)
+        _check(index, torch.int32, (B, H_k, max(budget, 0)), kept=kept)
     _raise(lib().fmha_cache_evict(
         fmha_tensor(k_cache.data_ptr(), code), fmha_tensor(v_cache.data_ptr(), code), acc.data_ptr(),
         fmha_tensor(k_out.data_ptr(), code), fmha_tensor(v_out.data_ptr(), code), acc_out.data_ptr(), B, H_k, D,

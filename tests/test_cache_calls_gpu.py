@@ -140,6 +140,35 @@ def test_what_a_call_makes_for_itself_belongs_to_its_stream(fm, handle):
     tt.check(t, o, lse)
 
 
+@pytest.mark.parametrize("op", ["tree", "weights"])
+def test_scratch_of_a_captured_call_stays_its_own(fm, op):
+    """What the call took from the allocator belongs to the graph: later tensors get none of it."""
+    if op == "tree":
+        c = tt.make("bf16", 70, 8, 2, 3000, [2900, 1501], seed=24)
+        d, (o, lse) = tt.on_gpu(c), tt.outputs(c)
+        size = fm.fmha_tree_workspace_size(2, 70, 8, 2, 128, 3000)
+        run = lambda: fm.tree_fwd(*d["args"], **d["kw"], out=o, lse=lse)
+        check = lambda: tt.check(c, o, lse)
+    else:
+        c = tc.make("bf16", 140, 8, 2, 1500, [1500, 701], mask="causal", seed=25)
+        args = c["q"].cuda(), c["kc"].cuda(), c["lse"].cuda(), i32(c["seqlen"])
+        acc, o = c["acc"].cuda(), torch.zeros(c["acc"].shape, device="cuda")
+        size = fm.fmha_cache_weights_workspace_size()
+        run = lambda: fm.cache_weights(*args, mask="causal", acc=acc, out=o)
+        check = lambda: tc.check_weights(c, o, torch.zeros_like(c["acc"]))
+    run()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    later = [torch.full((size,), 0x5a, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    o.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert fm.device_status(reset=True) == 0
+    assert all(bool((t == 0x5a).all()) for t in later)
+    check()
+
+
 def test_an_output_over_an_input_is_refused(fm):
     a = {k: bf(*s) for k, s in TREE.items()}
     with pytest.raises(fm.FmhaError):
