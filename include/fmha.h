@@ -381,8 +381,8 @@ int fmha_tree_commit(fmha_tensor k_cache, fmha_tensor v_cache, fmha_tensor k_new
  * an entry.  Cached rows at or past L are never used.
  * workspace: fmha_cache_weights_workspace_size() bytes (whatever the sizes,
  * 0.3 MB), 256-byte aligned, no initialisation, not shared with a concurrent
- * call.  Asynchronous on `stream` (one kernel, a second one where a sequence's
- * rows fill more than one chunk of 128).  Returns FMHA_OK,
+ * call.  Asynchronous on `stream` (one kernel, mostly a second one where a
+ * sequence's rows may fill more than one chunk of 128).  Returns FMHA_OK,
  * FMHA_ERR_INVALID_ARG, FMHA_ERR_UNSUPPORTED (dtype, alignment, device) or
  * FMHA_ERR_CUDA.  B = 0 or Sq = 0 succeeds without a launch and writes nothing.
  */

@@ -115,6 +115,28 @@ def test_weights_match_the_formula(fm, name):
         assert torch.equal(acc[e, :, :L], out[e, :, :L])
 
 
+# two chunks of queries: units that are left whole, or cut since they are more than the CTAs
+W_TWO = {
+    "whole": dict(dtype="bf16", Sq=40, H=16, H_k=4, S_max=700, seqlen=[700, 0, 40, 300], n_query=[40, 3, 0, 33], mask="causal"),
+    "whole_e4m3": dict(dtype="e4m3", Sq=64, H=32, H_k=8, S_max=130, seqlen=[130, 64]),
+    "whole_long": dict(dtype="f16", Sq=33, H=8, H_k=2, S_max=6000, seqlen=[6000, 33, 5119], mask="causal"),
+    "whole_odd_group": dict(dtype="bf16", Sq=50, H=9, H_k=3, S_max=520, seqlen=[513, 50, 7, 512], n_query=[50, 50, 7, 43],
+                            mask="causal"),
+    "cut": dict(dtype="bf16", Sq=40, H=16, H_k=4, S_max=300, seqlen=[(i * 37) % 300 for i in range(60)],
+                n_query=[min(40, (i * 37) % 300) for i in range(60)], mask="causal"),
+}
+
+
+@pytest.mark.parametrize("name", W_TWO)
+def test_weights_of_two_chunks(fm, name):
+    c = make(seed=70 + len(name), **W_TWO[name])
+    out = torch.full(c["acc"].shape, 3.0, device="cuda")
+    r = weights(fm, c, acc=c["acc"].cuda(), out=out)
+    torch.cuda.synchronize()
+    assert fm.device_status(reset=True) == 0
+    check_weights(c, r, torch.full(c["acc"].shape, 3.0))
+
+
 def test_weights_from_nothing_and_of_rows_without_keys(fm):
     c = make("bf16", 4, 8, 2, 300, [290, 17], seed=4)
     c["want"] -= c["acc"].double()
