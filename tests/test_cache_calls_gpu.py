@@ -247,3 +247,47 @@ def test_nothing_is_written_outside_the_outputs(fm):
     torch.cuda.synchronize()
     assert bufs[4][0].tolist() == [101, 100, 101]
     assert all(ok() for _, ok in bufs)
+
+
+def test_offsets_past_32_bits(fm):
+    """One entry of 2^31 elements behind another: every operator at its far end, against fp64 on the device."""
+    S, H_k, H, T, e = 1 << 22, 4, 8, 2, 1
+    g = torch.Generator(device="cuda").manual_seed(51)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=torch.bfloat16)
+    k, v = (torch.empty((2, S, H_k, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for c in (k, v):
+        c[0].zero_()
+        c[1].normal_(generator=g)
+    q, kn, vn = rnd(1, T, H, 128), rnd(1, T, H_k, 128), rnd(1, T, H_k, 128)
+    L, idx = S - T, i32([e])
+    o, lse = fm.tree_fwd(q, k, v, kn, vn, i32([L]), batch_idx=idx)
+    fm.tree_commit(k, v, kn, vn, i32([L]), i32([[0, 1]]), i32([T]), batch_idx=idx)
+    assert torch.equal(k[e, L:], kn[0]) and torch.equal(v[e, L:], vn[0]) and not bool(k[0].any()) and not bool(v[0].any())
+    acc = fm.cache_weights(q, k, lse, i32([S]), batch_idx=idx, mask="causal")
+    assert fm.device_status(reset=True) == 0 and not bool(acc[0].any())
+    see = torch.arange(S, device="cuda")[None, :] <= L + torch.arange(T, device="cuda")[:, None]
+    for gg in (0, H_k - 1):
+        keys, vals = k[e, :, gg].double(), v[e, :, gg].double()
+        x = torch.einsum("thd,kd->thk", q[0, :, 2 * gg:2 * gg + 2].double(), keys) * 128 ** -0.5
+        x = x.masked_fill(~see[:, None, :], float("-inf"))
+        w = torch.softmax(x, -1)
+        want = torch.einsum("thk,kd->thd", w, vals)
+        # an average of 4 million values of size 1: every weight is rounded by up to 2^-8 of itself, independently of its
+        # value's sign, and O once more
+        err = (o[0, :, 2 * gg:2 * gg + 2].double() - want).abs()
+        assert bool((err <= 2.0 ** -8 * torch.einsum("thk,kd->thd", w, vals.abs()) + 2.0 ** -8 * want.abs()).all())
+        exact = torch.logsumexp(x, -1)
+        assert bool(((lse[0, 2 * gg:2 * gg + 2].T.double() - exact).abs() <= 1e-4).all())
+        # an exponential of an argument below 32 that is rounded a few times, 2^-18 in all, and the LSE above
+        total = w.sum((0, 1))
+        assert bool(((acc[e, gg].double() - total).abs() <= 2e-4 * total).all())
+    budget, recent = 1000, 10
+    ko, vo = (torch.zeros((1, budget, H_k, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ao = torch.zeros((1, H_k, budget), device="cuda")
+    kept, new = fm.cache_evict(k, v, acc, i32([S]), budget, recent=recent, batch_idx=idx, k_out=ko, v_out=vo, acc_out=ao)
+    assert fm.device_status(reset=True) == 0 and new.tolist() == [budget]
+    for gg in range(H_k):
+        top = torch.sort(acc[e, gg, :S - recent], descending=True, stable=True).indices[:budget - recent]
+        rows = torch.cat([torch.sort(top).values, torch.arange(S - recent, S, device="cuda")])
+        assert torch.equal(kept[0, gg].long(), rows) and torch.equal(ao[0, gg], acc[e, gg, rows])
+        assert torch.equal(ko[0, :, gg], k[e, rows, gg]) and torch.equal(vo[0, :, gg], v[e, rows, gg])
