@@ -398,6 +398,26 @@ inline bool overlap(const void *p, size_t n, const void *q, size_t m) {
     return a < b + m && b < a + n;
 }
 
+// An array of a call, or none (p NULL).
+struct Bytes {
+    const void *p;
+    size_t n;
+};
+inline bool overlap(const Bytes &a, const Bytes &b) { return a.p && b.p && overlap(a.p, a.n, b.p, b.n); }
+
+// Does an output lie over an input, or over another output?  Thread blocks run
+// at their own times, so what one of them overwrites others may not have read.
+template <int N, int M>
+bool outputs_clash(const Bytes (&out)[N], const Bytes (&in)[M]) {
+    for (int i = 0; i < N; ++i) {
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out[j])) return true;
+        for (const Bytes &b : in)
+            if (overlap(out[i], b)) return true;
+    }
+    return false;
+}
+
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;

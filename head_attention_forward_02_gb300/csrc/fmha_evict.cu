@@ -383,21 +383,18 @@ extern "C" int fmha_cache_evict(fmha_tensor k_cache, fmha_tensor v_cache, const 
         if (misaligned(ptr, 4)) return FMHA_ERR_INVALID_ARG;
     if (B > 65535) return FMHA_ERR_UNSUPPORTED;
     const int row = kD * (dt == FMHA_E4M3 ? 1 : 2);
-    // the output is the input (all three, same sizes and entries), or apart from it
+    // the output is the input (all three, same sizes and entries), or apart from
+    // it; either way K, V, the scores and the lists are arrays of their own
     const bool in_place = k_out.data == k_cache.data;
-    if (in_place) {
-        if (v_out.data != v_cache.data || acc_out != acc || B_out != B_cache || S_out != S_max || out_idx != batch_idx)
-            return FMHA_ERR_INVALID_ARG;
-    } else {
-        const size_t in_b = (size_t)B_cache * S_max * H_k, out_b = (size_t)B_out * S_out * H_k;
-        struct Range { const void *p; size_t n; };
-        const Range in[3] = {{k_cache.data, in_b * row}, {v_cache.data, in_b * row}, {acc, in_b * sizeof(float)}};
-        const Range out[3] = {{k_out.data, out_b * row}, {v_out.data, out_b * row}, {acc_out, out_b * sizeof(float)}};
-        for (const Range &i : in)
-            for (const Range &o : out)
-                if (overlap(i.p, i.n, o.p, o.n)) return FMHA_ERR_INVALID_ARG;
-    }
-    if (seqlen == new_seqlen) return FMHA_ERR_INVALID_ARG;      // every CTA of a sequence reads its length
+    if (in_place &&
+        (v_out.data != v_cache.data || acc_out != acc || B_out != B_cache || S_out != S_max || out_idx != batch_idx))
+        return FMHA_ERR_INVALID_ARG;
+    const size_t in_b = (size_t)B_cache * S_max * H_k, out_b = (size_t)B_out * S_out * H_k, seq_b = (size_t)B * sizeof(int);
+    const Bytes out[5] = {{k_out.data, out_b * row}, {v_out.data, out_b * row}, {acc_out, out_b * sizeof(float)},
+                          {kept, (size_t)H_k * budget * seq_b}, {new_seqlen, seq_b}};
+    const Bytes in[3] = {{k_cache.data, in_b * row}, {v_cache.data, in_b * row}, {acc, in_b * sizeof(float)}};
+    const Bytes seq[3] = {{seqlen, seq_b}, {batch_idx, seq_b}, {out_idx, seq_b}};
+    if (outputs_clash(out, seq) || (!in_place && outputs_clash(out, in))) return FMHA_ERR_INVALID_ARG;
     const int rc = check_device();
     if (rc != FMHA_OK) return rc;
     const int sms = sm_count();

@@ -413,9 +413,11 @@ size_t fmha_cache_weights_workspace_size(void);
  * batch_idx, out_idx int32 [B] (the last two may be NULL: entry b).  The
  * output is the input itself (k_out.data == k_cache.data, and then v_out,
  * acc_out, B_out, S_out and out_idx are the input's too), or apart from it in
- * memory.  1 <= budget <= S_out, 0 <= recent <= budget, S_max and S_out at
- * most 2^30.  new_seqlen is another array than seqlen.  K, V 16-byte, the
- * others 4-byte aligned; dtype FMHA_F16, FMHA_BF16 or FMHA_E4M3.
+ * memory; k_out, v_out, acc_out, kept and new_seqlen are apart from one another
+ * and from seqlen, batch_idx and out_idx (so in place K and V are two arrays).
+ * 1 <= budget <= S_out, 0 <= recent <= budget, S_max and S_out at most 2^30.
+ * K, V 16-byte, the others 4-byte aligned; dtype FMHA_F16, FMHA_BF16 or
+ * FMHA_E4M3.
  * seqlen, batch_idx and out_idx are treated as in fmha_tree_fwd; nothing is
  * moved from or to a missing entry.  Two sequences must not share an entry of
  * the output, nor, in place, of the input.

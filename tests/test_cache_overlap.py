@@ -1,0 +1,85 @@
+"""Calls of the cache operators whose outputs lie over their inputs or over one
+another are refused on the host, before the device is looked at: other thread
+blocks still read, or also write, what one of them overwrites."""
+import pytest
+import torch
+
+from tests.test_cache_abi import E4M3, call_evict, fm  # noqa: F401  (fm: the fixture)
+
+M = 1 << 24                                              # fake addresses, far apart: never dereferenced
+
+
+def apart(*names):
+    return {n: (i + 1) * M for i, n in enumerate(names)}
+
+
+def clash(a, x, y, n):
+    """Array y moved to where x, of n bytes, begins, and to its last 16 bytes."""
+    return [{**a, y: a[x]}, {**a, y: a[x] + n - 16}]
+
+
+# ---------------------------------------------------------------------------
+# Eviction: B = 2 sequences, 2 heads, entries of 64 rows (out: 40), budget 32, bf16
+# ---------------------------------------------------------------------------
+
+EVICT = apart("kc", "vc", "acc", "ko", "vo", "ao", "sl", "bi", "oi", "kept", "ns")
+ROWS_IN, ROWS_OUT = 2 * 64 * 2, 2 * 40 * 2               # rows of all heads and entries
+EVICT_BYTES = dict(kc=ROWS_IN * 256, vc=ROWS_IN * 256, acc=ROWS_IN * 4, ko=ROWS_OUT * 256, vo=ROWS_OUT * 256,
+                   ao=ROWS_OUT * 4, kept=2 * 2 * 32 * 4)
+
+
+def in_place(**kw):
+    a = {**EVICT, "oi": EVICT["bi"], **kw}
+    return dict(a, ko=a["kc"], vo=a["vc"], ao=a["acc"], So=64)
+
+
+@pytest.fixture
+def past_the_checks(fm):  # noqa: F811
+    """What a call that nothing is wrong with answers where there is no device."""
+    if torch.cuda.is_available():
+        pytest.skip("a device would be given the fake addresses")
+    r = call_evict(fm, **EVICT)
+    assert r != -1 and call_evict(fm, **in_place()) == r
+    return r
+
+
+@pytest.mark.parametrize("dt", [1, E4M3])
+def test_evict_in_place_of_one_array_as_k_and_v(fm, past_the_checks, dt):  # noqa: F811
+    """K's and V's thread blocks would move the same rows down, each at its own pace."""
+    n = ROWS_IN * (128 if dt == E4M3 else 256)
+    for vc in (EVICT["kc"], EVICT["kc"] + n - 16, EVICT["kc"] - n + 16):
+        assert call_evict(fm, **in_place(vc=vc), dt=dt) == -1
+    assert call_evict(fm, **in_place(vc=EVICT["kc"] + n), dt=dt) == past_the_checks      # next to one another
+
+
+@pytest.mark.parametrize("x,y", [("ko", "vo"), ("ko", "ao"), ("vo", "ao"), ("ko", "kept"), ("vo", "kept"), ("ao", "kept"),
+                                 ("ko", "ns"), ("vo", "ns"), ("ao", "ns"), ("kept", "ns")])
+def test_evict_outputs_over_one_another(fm, past_the_checks, x, y):  # noqa: F811
+    for a in clash(EVICT, x, y, EVICT_BYTES[x]):
+        assert call_evict(fm, **a) == -1
+
+
+@pytest.mark.parametrize("x,y", [(i, o) for i in ("kc", "vc", "acc") for o in ("kept", "ns")])
+def test_evict_lists_over_the_input(fm, past_the_checks, x, y):  # noqa: F811
+    for a in clash(EVICT, x, y, EVICT_BYTES[x]):
+        assert call_evict(fm, **a) == -1
+        assert call_evict(fm, **in_place(**{y: a[y]})) == -1
+
+
+@pytest.mark.parametrize("x", ["ko", "vo", "ao", "kept"])
+@pytest.mark.parametrize("y", ["sl", "bi", "oi"])
+def test_evict_outputs_over_the_sequences(fm, past_the_checks, x, y):  # noqa: F811
+    for a in clash(EVICT, x, y, EVICT_BYTES[x]):
+        assert call_evict(fm, **a) == -1
+
+
+@pytest.mark.parametrize("y", ["sl", "bi", "oi"])
+def test_evict_new_lengths_over_the_sequences(fm, past_the_checks, y):  # noqa: F811
+    for off in (-4, 0, 4):                               # int32 of two sequences: one element in common, or both
+        assert call_evict(fm, **{**EVICT, "ns": EVICT[y] + off}) == -1
+    for off in (-8, 8):
+        assert call_evict(fm, **{**EVICT, "ns": EVICT[y] + off}) == past_the_checks
+
+
+def test_evict_of_one_array_as_k_and_v_into_two_others(fm, past_the_checks):  # noqa: F811
+    assert call_evict(fm, **{**EVICT, "vc": EVICT["kc"]}) == past_the_checks     # both only read it
