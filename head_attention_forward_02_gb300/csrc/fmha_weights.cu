@@ -665,6 +665,12 @@ extern "C" int fmha_cache_weights(fmha_tensor q, fmha_tensor k_cache, const floa
     if (acc_in && acc_in != acc_out && overlap(acc_in, acc_bytes, acc_out, acc_bytes)) return FMHA_ERR_INVALID_ARG;
     if (!workspace || misaligned(workspace, 256) || workspace_bytes < fmha_cache_weights_workspace_size())
         return FMHA_ERR_INVALID_ARG;
+    const size_t seq_bytes = (size_t)B * sizeof(int), row = kD * (dt == FMHA_E4M3 ? 1 : 2);
+    const Bytes out[2] = {{acc_out, acc_bytes}, {workspace, fmha_cache_weights_workspace_size()}};
+    const Bytes in[6] = {{q.data, (size_t)B * Sq * H * row}, {k_cache.data, (size_t)B_cache * S_max * H_k * row},
+                         {lse, (size_t)B * H * Sq * sizeof(float)}, {seqlen, seq_bytes}, {batch_idx, seq_bytes},
+                         {n_query, seq_bytes}};
+    if (outputs_clash(out, in) || overlap(out[1], Bytes{acc_in, acc_bytes})) return FMHA_ERR_INVALID_ARG;
     const int rc = check_device();
     if (rc != FMHA_OK) return rc;
     const int sms = sm_count();

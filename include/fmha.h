@@ -373,7 +373,8 @@ int fmha_tree_commit(fmha_tensor k_cache, fmha_tensor v_cache, fmha_tensor k_new
  * Layouts (contiguous): q [B, Sq, H, 128]; k_cache [B_cache, S_max, H_k, 128]
  * of q's dtype (FMHA_F16, FMHA_BF16, FMHA_E4M3); lse float [B, H, Sq];
  * acc_in, acc_out float [B_cache, H_k, S_max], the same array or apart; seqlen,
- * batch_idx, n_query int32 [B] (the last two may be NULL).  H / H_k at most
+ * batch_idx, n_query int32 [B] (the last two may be NULL).  The workspace, and
+ * acc_out but for acc_in, are apart from the other arrays.  H / H_k at most
  * 128, S_max at most 2^30.  q and k_cache 16-byte, the others 4-byte aligned.
  * Sums are fp32 in an order that does not depend on timing.
  * seqlen and batch_idx are treated as in fmha_tree_fwd, n_query as n_draft

@@ -4,7 +4,7 @@ blocks still read, or also write, what one of them overwrites."""
 import pytest
 import torch
 
-from tests.test_cache_abi import E4M3, call_evict, fm  # noqa: F401  (fm: the fixture)
+from tests.test_cache_abi import E4M3, call_evict, call_weights, fm  # noqa: F401  (fm: the fixture)
 
 M = 1 << 24                                              # fake addresses, far apart: never dereferenced
 
@@ -83,3 +83,41 @@ def test_evict_new_lengths_over_the_sequences(fm, past_the_checks, y):  # noqa: 
 
 def test_evict_of_one_array_as_k_and_v_into_two_others(fm, past_the_checks):  # noqa: F811
     assert call_evict(fm, **{**EVICT, "vc": EVICT["kc"]}) == past_the_checks     # both only read it
+
+
+# ---------------------------------------------------------------------------
+# Weights: 2 sequences, 4 queries, 8 heads on 2, entries of 64 rows, bf16
+# ---------------------------------------------------------------------------
+
+WEIGHTS = apart("q", "kc", "lse", "ai", "ao", "sl", "bi", "nq", "ws")
+WEIGHTS_BYTES = dict(q=2 * 4 * 8 * 256, kc=2 * 64 * 2 * 256, lse=2 * 8 * 4 * 4, ai=2 * 2 * 64 * 4, ao=2 * 2 * 64 * 4)
+
+
+@pytest.fixture
+def weights_past_the_checks(fm):  # noqa: F811
+    if torch.cuda.is_available():
+        pytest.skip("a device would be given the fake addresses")
+    r = call_weights(fm, **WEIGHTS)
+    assert r != -1 and call_weights(fm, **{**WEIGHTS, "ai": WEIGHTS["ao"]}) == r
+    return r
+
+
+@pytest.mark.parametrize("x", ["q", "kc", "lse"])
+def test_weights_scores_over_an_input(fm, weights_past_the_checks, x):  # noqa: F811
+    """Blocks that are not done read the queries, keys and LSE that the first ones would overwrite."""
+    for a in clash(WEIGHTS, x, "ao", WEIGHTS_BYTES[x]):
+        assert call_weights(fm, **a) == -1
+        assert call_weights(fm, **{**a, "ai": a["ao"]}) == -1
+    assert call_weights(fm, **{**WEIGHTS, "ao": WEIGHTS[x] + WEIGHTS_BYTES[x]}) == weights_past_the_checks
+
+
+@pytest.mark.parametrize("y", ["sl", "bi", "nq"])
+def test_weights_scores_over_the_sequences(fm, weights_past_the_checks, y):  # noqa: F811
+    for a in clash(WEIGHTS, "ao", y, WEIGHTS_BYTES["ao"]):
+        assert call_weights(fm, **a) == -1
+
+
+@pytest.mark.parametrize("x", ["q", "kc", "lse", "ai", "ao", "sl", "bi", "nq"])
+def test_weights_scratch_over_an_array(fm, weights_past_the_checks, x):  # noqa: F811
+    for off in (0, 256 - fm.fmha_cache_weights_workspace_size() // 256 * 256):
+        assert call_weights(fm, **{**WEIGHTS, "ws": WEIGHTS[x] + off}) == -1
