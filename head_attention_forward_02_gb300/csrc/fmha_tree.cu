@@ -1045,10 +1045,13 @@ extern "C" int fmha_tree_fwd(fmha_tensor q, fmha_tensor k_cache, fmha_tensor v_c
     // a unit's inputs are read by several CTAs, at their own times
     const size_t row = kD * (dt == FMHA_E4M3 ? 1 : 2), q_bytes = (size_t)B * T * H * row;
     const size_t new_bytes = (size_t)B * T * H_k * row, cache_bytes = (size_t)B_cache * S_max * H_k * row;
-    if (overlap(o.data, q_bytes, q.data, q_bytes) || overlap(o.data, q_bytes, k_new.data, new_bytes) ||
-        overlap(o.data, q_bytes, v_new.data, new_bytes) || overlap(o.data, q_bytes, k_cache.data, cache_bytes) ||
-        overlap(o.data, q_bytes, v_cache.data, cache_bytes))
-        return FMHA_ERR_INVALID_ARG;
+    const size_t seq_bytes = (size_t)B * sizeof(int);
+    const Bytes out[3] = {{o.data, q_bytes}, {lse, (size_t)B * H * T * sizeof(float)},
+                          {workspace, fmha_tree_workspace_size(B, T, H, H_k, D, S_max)}};
+    const Bytes in[9] = {{q.data, q_bytes}, {k_cache.data, cache_bytes}, {v_cache.data, cache_bytes},
+                         {k_new.data, new_bytes}, {v_new.data, new_bytes}, {seqlen, seq_bytes}, {batch_idx, seq_bytes},
+                         {n_draft, seq_bytes}, {tree_mask, (size_t)(B - 1) * mask_batch_stride + (size_t)T * T}};
+    if (outputs_clash(out, in)) return FMHA_ERR_INVALID_ARG;
     int rc = check_device();
     if (rc != FMHA_OK) return rc;
     const int sms = sm_count();

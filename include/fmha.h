@@ -297,7 +297,8 @@ size_t fmha_gen_workspace_size(int B, int H, int H_k, int D, int S_max);
  *   lse                float [B, H, T], or NULL
  * All tensors share one dtype, FMHA_F16, FMHA_BF16 or FMHA_E4M3; D must be
  * 128, H / H_k at most 128 and S_max at most 2^30.  Device pointers must be
- * 16-byte aligned (int32 and lse 4-byte), and o and lse apart from the inputs.
+ * 16-byte aligned (int32 and lse 4-byte); o, lse and the workspace are apart
+ * from the inputs and from one another.
  * P is rounded to the tensors' dtype before P.V (its row sum is not), and O
  * with saturation for e4m3.
  * Requirements the host cannot check: 0 <= seqlen[b] <= S_max, 0 <=

@@ -4,7 +4,7 @@ blocks still read, or also write, what one of them overwrites."""
 import pytest
 import torch
 
-from tests.test_cache_abi import E4M3, call_evict, call_weights, fm  # noqa: F401  (fm: the fixture)
+from tests.test_cache_abi import E4M3, call_evict, call_tree, call_weights, fm  # noqa: F401  (fm: the fixture)
 
 M = 1 << 24                                              # fake addresses, far apart: never dereferenced
 
@@ -121,3 +121,53 @@ def test_weights_scores_over_the_sequences(fm, weights_past_the_checks, y):  # n
 def test_weights_scratch_over_an_array(fm, weights_past_the_checks, x):  # noqa: F811
     for off in (0, 256 - fm.fmha_cache_weights_workspace_size() // 256 * 256):
         assert call_weights(fm, **{**WEIGHTS, "ws": WEIGHTS[x] + off}) == -1
+
+
+# ---------------------------------------------------------------------------
+# Drafts: 2 sequences of 4, 8 heads on 2, entries of 64 rows, bf16
+# ---------------------------------------------------------------------------
+
+TREE = apart("q", "kc", "vc", "kn", "vn", "o", "lse", "sl", "bi", "nd", "mask", "ws")
+TREE_BYTES = dict(q=2 * 4 * 8 * 256, o=2 * 4 * 8 * 256, kc=2 * 64 * 2 * 256, vc=2 * 64 * 2 * 256, kn=2 * 4 * 2 * 256,
+                  vn=2 * 4 * 2 * 256, lse=2 * 8 * 4 * 4)
+
+
+@pytest.fixture
+def tree_past_the_checks(fm):  # noqa: F811
+    if torch.cuda.is_available():
+        pytest.skip("a device would be given the fake addresses")
+    r = call_tree(fm, **TREE)
+    assert r != -1 and call_tree(fm, **{**TREE, "lse": None, "mask": None, "bi": None, "nd": None}) == r
+    return r
+
+
+@pytest.mark.parametrize("x", ["q", "kc", "vc", "kn", "vn", "o"])
+def test_tree_lse_over_another_array(fm, tree_past_the_checks, x):  # noqa: F811
+    for a in clash(TREE, x, "lse", TREE_BYTES[x]):
+        assert call_tree(fm, **a) == -1
+    assert call_tree(fm, **{**TREE, "lse": TREE[x] + TREE_BYTES[x]}) == tree_past_the_checks
+
+
+@pytest.mark.parametrize("x", ["o", "lse"])
+@pytest.mark.parametrize("y", ["sl", "bi", "nd"])
+def test_tree_outputs_over_the_sequences(fm, tree_past_the_checks, x, y):  # noqa: F811
+    for a in clash(TREE, x, y, TREE_BYTES[x]):
+        assert call_tree(fm, **a) == -1
+
+
+@pytest.mark.parametrize("x", ["o", "lse"])
+def test_tree_outputs_over_the_mask(fm, tree_past_the_checks, x):  # noqa: F811
+    """One mask of 4 x 4 bytes, or one for each of the two sequences, 100 bytes apart."""
+    end = TREE[x] + TREE_BYTES[x]
+    for ms in (0, 100):
+        assert call_tree(fm, **{**TREE, "mask": TREE[x] - 15, "ms": ms}) == -1
+        assert call_tree(fm, **{**TREE, "mask": TREE[x] - 100 - 15, "ms": ms}) == (-1 if ms else tree_past_the_checks)
+        assert call_tree(fm, **{**TREE, "mask": end - 1, "ms": ms}) == -1
+        assert call_tree(fm, **{**TREE, "mask": end, "ms": ms}) == tree_past_the_checks
+
+
+@pytest.mark.parametrize("x", ["q", "kc", "vc", "kn", "vn", "o", "lse", "sl", "bi", "nd", "mask"])
+def test_tree_scratch_over_an_array(fm, tree_past_the_checks, x):  # noqa: F811
+    assert call_tree(fm, **{**TREE, "ws": TREE[x], "ws_bytes": 1 << 40}) == -1
+    last = 256 - fm.fmha_tree_workspace_size(2, 4, 8, 2, 128, 64) // 256 * 256
+    assert call_tree(fm, **{**TREE, "ws": TREE[x] + last}) == -1
