@@ -1145,10 +1145,11 @@ extern "C" int fmha_tree_commit(fmha_tensor k_cache, fmha_tensor v_cache, fmha_t
     if (B > 65535) return FMHA_ERR_UNSUPPORTED;
     const size_t row = (size_t)H_k * kD * (dt == FMHA_E4M3 ? 1 : 2);
     const size_t new_bytes = (size_t)B * T * row, cache_bytes = (size_t)B_cache * S_max * row;
-    for (const void *c : {k_cache.data, v_cache.data})
-        if (overlap(c, cache_bytes, k_new.data, new_bytes) || overlap(c, cache_bytes, v_new.data, new_bytes))
-            return FMHA_ERR_INVALID_ARG;
-    if (overlap(k_cache.data, cache_bytes, v_cache.data, cache_bytes)) return FMHA_ERR_INVALID_ARG;
+    const size_t seq_bytes = (size_t)B * sizeof(int);
+    const Bytes out[2] = {{k_cache.data, cache_bytes}, {v_cache.data, cache_bytes}};
+    const Bytes in[6] = {{k_new.data, new_bytes}, {v_new.data, new_bytes}, {seqlen, seq_bytes}, {batch_idx, seq_bytes},
+                         {path, P * seq_bytes}, {n_accept, seq_bytes}};
+    if (outputs_clash(out, in)) return FMHA_ERR_INVALID_ARG;
     const int rc = check_device();
     if (rc != FMHA_OK) return rc;
     CommitParams p{};

@@ -339,9 +339,8 @@ size_t fmha_tree_workspace_size(int B, int T, int H, int H_k, int D, int S_max);
  * with e and L = seqlen[b] as there.  seqlen is not changed (the caller adds
  * n_accept to it).  Layouts as fmha_tree_fwd; path int32 [B, P], n_accept
  * int32 [B].  A draft may appear more than once.  Entries of path at or past
- * n_accept are not read.  Two sequences must not share an entry; K_new and
- * V_new are apart from the caches, and those from one another.  S_max at most
- * 2^30.
+ * n_accept are not read.  Two sequences must not share an entry; the caches are
+ * apart from all other arrays and from one another.  S_max at most 2^30.
  * In device memory, so checked there: 0 <= seqlen[b], 0 <= n_accept[b] <= P,
  * seqlen[b] + n_accept[b] <= S_max, batch_idx[b] in [0, B_cache) and path in
  * [0, T); a kernel that meets a violation clamps the count, or writes nothing

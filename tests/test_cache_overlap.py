@@ -4,7 +4,7 @@ blocks still read, or also write, what one of them overwrites."""
 import pytest
 import torch
 
-from tests.test_cache_abi import E4M3, call_evict, call_tree, call_weights, fm  # noqa: F401  (fm: the fixture)
+from tests.test_cache_abi import E4M3, call_commit, call_evict, call_tree, call_weights, fm  # noqa: F401  (fm: the fixture)
 
 M = 1 << 24                                              # fake addresses, far apart: never dereferenced
 
@@ -171,3 +171,23 @@ def test_tree_scratch_over_an_array(fm, tree_past_the_checks, x):  # noqa: F811
     assert call_tree(fm, **{**TREE, "ws": TREE[x], "ws_bytes": 1 << 40}) == -1
     last = 256 - fm.fmha_tree_workspace_size(2, 4, 8, 2, 128, 64) // 256 * 256
     assert call_tree(fm, **{**TREE, "ws": TREE[x] + last}) == -1
+
+
+# ---------------------------------------------------------------------------
+# Commit: 2 sequences of 4 drafts, 3 accepted at most, 2 heads, entries of 64 rows, bf16
+# ---------------------------------------------------------------------------
+
+COMMIT = apart("kc", "vc", "kn", "vn", "sl", "bi", "path", "na")
+
+
+@pytest.mark.parametrize("x", ["kc", "vc"])
+@pytest.mark.parametrize("y", ["sl", "bi", "path", "na"])
+def test_commit_cache_over_the_sequences(fm, x, y):  # noqa: F811
+    """A thread block a draft: each reads its sequence's length, entry and path while others write rows."""
+    if torch.cuda.is_available():
+        pytest.skip("a device would be given the fake addresses")
+    r = call_commit(fm, **COMMIT)
+    assert r != -1 and call_commit(fm, **{**COMMIT, "bi": None}) == r
+    for a in clash(COMMIT, x, y, 2 * 64 * 2 * 256):
+        assert call_commit(fm, **a) == -1
+    assert call_commit(fm, **{**COMMIT, y: COMMIT[x] + 2 * 64 * 2 * 256}) == r
