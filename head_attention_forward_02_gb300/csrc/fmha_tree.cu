@@ -26,10 +26,14 @@
 // (TMEM lane = row, so no exchange between threads), written back to TMEM over
 // S in two halves, and O += P V of a half as soon as it is there.  Each group
 // has an MMA warp of its own, and one group's MMAs run under the other's
-// softmax.  The reference m is kept lazily: O is rescaled only when the row
-// maximum has grown by more than 2^8.
+// softmax.  The reference m is kept lazily: O is rescaled only when P would
+// leave a range in which the type holds it well.
 // P is rounded to the inputs' type for the P V product (by up to 2^-8 / 2^-11 /
-// 2^-4 of a weight for bf16 / fp16 / e4m3), its row sum and O stay in fp32.
+// 2^-4 of a weight for bf16 / fp16 / e4m3, where it is not subnormal there), its
+// row sum and O stay in fp32.  e4m3 has 2^-9 for its last step: of many keys
+// far below one (a sink before a long context) all would round to nothing, so
+// there the reference also moves down again, before small weights have cost
+// more than 2^-5 of their row's.
 //
 // A unit cut between CTAs leaves normalised fp32 partials and their LSE in the
 // workspace, at most two per CTA, and a second kernel joins them; units that
@@ -51,7 +55,6 @@ namespace fmha {
 namespace {
 
 constexpr int kTreeMaxCtas = 152;            // CTAs of the attention kernel at most (bounds the workspace)
-constexpr float kRescaleLog2 = 8.0f;
 constexpr int kStagesMax = 12;
 constexpr int kItems = 4;                    // work items published ahead
 constexpr int kTreeProd = 8, kTreeMma = 9;   // warps: two softmax groups of four, producer, an MMA issuer a group
@@ -75,9 +78,18 @@ struct TreeCfg : ElemCfg<ELEM> {
     static constexpr int OFF_STAT = OFF_BARS + 1024;          // SPLIT: (m, l) of group 1's rows
     static constexpr int SMEM_BYTES = OFF_STAT + kRows * 8 + 1024;   // 1 KB alignment
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-    // log2 of the largest P right after the reference is set; up to 2^8 later.
-    // e4m3 underflows 2^9 below 1, so its weights start 2^4 up.
+    // log2 of the largest P right after the reference is set, and how far it may
+    // grow before the reference is set again (e4m3 ends at 448).
     static constexpr float BIAS = B::FP8 ? 4.f : 0.f;
+    static constexpr float GROWN = B::FP8 ? 8.75f : 8.f;
+    // e4m3: P below 2^-6 is rounded to steps of 2^-9, so a tile's 128 weights are
+    // off by 2^-3 together at most.  So that these sum to 2^-5 of the row's sum
+    // at most, a row whose sum is below LOST a tile gets a lower reference from a
+    // tile without a P of 2^(BIAS - 1) (a tile with one adds more than LOST).
+    // By 2^DOWN at most, and not above SUM_MAX, so that nothing overflows: what a
+    // tile could lose then is below 2^-33 of the sum.  (0.4% of 75 us for 16 x 5
+    // drafts on 16384 keys, where it is hardly ever needed.)
+    static constexpr float LOST = 4.f, DOWN = 40.f, SUM_MAX = 0x1p30f;
     // What a unit's ends cost a CTA, in tiles' time: the ring runs empty and is
     // filled again (of 16 ragged f16 sequences, 40 us, a CTA of two units' parts
     // would end 4 us after one that stays in a unit).
@@ -505,6 +517,8 @@ __device__ void tree_softmax(const TreeParams &p, uint8_t *smem, TreeBars *bars,
         const bool work = __any_sync(0xffffffffu, row_ok);   // else the warp only keeps step
         float m = -INFINITY;                            // reference (log2 units) of P and O
         float l = 0.f;                                  // row sum
+        float lost = 0.f;                               // e4m3: tiles so far, each in the units P had then,
+        float low = -INFINITY;                          // and the maximum below which a tile moves m down
         bool ok = true;
         constexpr int kStep = C::SPLIT ? 2 : 1;
         const int tb = it.t0 + (C::SPLIT ? x : 0);
@@ -578,14 +592,15 @@ __device__ void tree_softmax(const TreeParams &p, uint8_t *smem, TreeBars *bars,
                     for (int y = 0; y < 4; ++y)
                         mx[y] = max3(mx[y], __uint_as_float(s[q][k + 2 * y]), __uint_as_float(s[q][k + 2 * y + 1]));
             const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
-            const bool need = tmax > m + kRescaleLog2;
+            const bool need = tmax > m + C::GROWN || (C::FP8 && tmax < low);
             if (__any_sync(0xffffffffu, need)) {
                 float alpha = 1.f;
                 if (need) {
-                    const float ref = tmax - C::BIAS;
+                    const float ref = fmaxf(tmax - C::BIAS, m - C::DOWN);
                     alpha = m == -INFINITY ? 0.f : ex2(m - ref);
                     m = ref;
                     l *= alpha;
+                    lost *= alpha;
                 }
                 if (t > tb) {
                     // the P V of the tile before is in O: S, issued behind it, is there
@@ -600,6 +615,7 @@ __device__ void tree_softmax(const TreeParams &p, uint8_t *smem, TreeBars *bars,
                     }
                 }
             }
+            lost += 1.f;
             // a row that has seen no key yet: every score is -inf, P = 0
             const float mr = m == -INFINITY ? 0.f : -m;
             const uint64_t c2 = pack_f2(p.c, p.c), m2 = pack_f2(mr, mr);
@@ -643,6 +659,7 @@ __device__ void tree_softmax(const TreeParams &p, uint8_t *smem, TreeBars *bars,
             unpack_f2(ls[0], la, lb);
             unpack_f2(ls[1], lc, ld);
             l += (la + lb) + (lc + ld);
+            if constexpr (C::FP8) low = l < fminf(C::LOST * (lost + 1.f), C::SUM_MAX) ? m + (C::BIAS - 1.f) : -INFINITY;
         }
         if (!ok) break;
 

@@ -299,8 +299,10 @@ size_t fmha_gen_workspace_size(int B, int H, int H_k, int D, int S_max);
  * 128, H / H_k at most 128 and S_max at most 2^30.  Device pointers must be
  * 16-byte aligned (int32 and lse 4-byte); o, lse and the workspace are apart
  * from the inputs and from one another.
- * P is rounded to the tensors' dtype before P.V (its row sum is not), and O
- * with saturation for e4m3.
+ * P is rounded to the tensors' dtype before P.V (its row sum is not): a weight
+ * by half a step at most, and with e4m3 the weights too small for its normal
+ * range by 2^-5 of their row's at most, together.  O is rounded with saturation
+ * for e4m3.
  * Requirements the host cannot check: 0 <= seqlen[b] <= S_max, 0 <=
  * batch_idx[b] < B_cache, 0 <= n_draft[b] <= T; a kernel that meets a
  * violation clamps the length or the count, or reads zeros for the missing
