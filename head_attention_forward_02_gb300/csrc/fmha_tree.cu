@@ -79,9 +79,11 @@ struct TreeCfg : ElemCfg<ELEM> {
     static constexpr int SMEM_BYTES = OFF_STAT + kRows * 8 + 1024;   // 1 KB alignment
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
     // log2 of the largest P right after the reference is set, and how far it may
-    // grow before the reference is set again (e4m3 ends at 448).
-    static constexpr float BIAS = B::FP8 ? 4.f : 0.f;
-    static constexpr float GROWN = B::FP8 ? 8.75f : 8.f;
+    // grow before the reference is set again (e4m3 ends at 448, fp16 at 65504).
+    // fp16's steps are 2^-24 and more: with its largest at 2^7 a weight is off by
+    // 2^-32 of the row's sum at most where P is below its normal range.
+    static constexpr float BIAS = B::FP8 ? 4.f : ELEM == FMHA_F16 ? 7.f : 0.f;
+    static constexpr float GROWN = B::FP8 ? 8.75f : ELEM == FMHA_F16 ? 15.f : 8.f;
     // e4m3: P below 2^-6 is rounded to steps of 2^-9, so a tile's 128 weights are
     // off by 2^-3 together at most.  So that these sum to 2^-5 of the row's sum
     // at most, a row whose sum is below LOST a tile gets a lower reference from a

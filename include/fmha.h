@@ -300,9 +300,9 @@ size_t fmha_gen_workspace_size(int B, int H, int H_k, int D, int S_max);
  * 16-byte aligned (int32 and lse 4-byte); o, lse and the workspace are apart
  * from the inputs and from one another.
  * P is rounded to the tensors' dtype before P.V (its row sum is not): a weight
- * by half a step at most, and with e4m3 the weights too small for its normal
- * range by 2^-5 of their row's at most, together.  O is rounded with saturation
- * for e4m3.
+ * by half a step, and below the type's normal range by 2^-32 (fp16) of the row's
+ * sum, or all of these together by 2^-5 of it (e4m3), at most.  O is rounded
+ * with saturation for e4m3.
  * Requirements the host cannot check: 0 <= seqlen[b] <= S_max, 0 <=
  * batch_idx[b] < B_cache, 0 <= n_draft[b] <= T; a kernel that meets a
  * violation clamps the length or the count, or reads zeros for the missing

@@ -4,8 +4,8 @@ to the tensors' type before P V must not lose.
 
 O against its formula in 64 bits.  What is allowed: a weight is off by half a
 step of its type, those in its subnormal range together by SMALL of their row's
-sum (for e4m3 the reference is set again before more is lost), and O's own
-rounding."""
+sum (for e4m3 the reference is set again before more is lost; for fp16 each is
+off by 2^-25 where the row's largest is 2^7 or more), and O's own rounding."""
 import pytest
 import torch
 
@@ -15,7 +15,7 @@ from tests.test_tree_gpu import fm  # noqa: F401  (the fixture)
 pytestmark = pytest.mark.gpu
 
 L, H_K, G, B = 16384, 8, 8, 19               # 152 units that read one entry: a CTA goes through nearly a whole unit
-SMALL = {"e4m3": 2.0 ** -5, "bf16": 0.0}
+SMALL = {"e4m3": 2.0 ** -5, "f16": L * 2.0 ** -32, "bf16": 0.0}
 
 
 def scores(g, far):
@@ -59,7 +59,7 @@ def make(dtype, T, far, seed):
 
 
 @pytest.mark.parametrize("T", [2, 20], ids=["one_block", "two_blocks"])
-@pytest.mark.parametrize("dtype,far", [("e4m3", 1.0), ("e4m3", 0.8), ("bf16", 1.0)])
+@pytest.mark.parametrize("dtype,far", [("e4m3", 1.0), ("e4m3", 0.8), ("f16", 1.6), ("f16", 1.3), ("bf16", 1.0)])
 def test_many_small_weights_beside_a_large_one(fm, dtype, far, T):  # noqa: F811
     q, k, v, kn, vn = make(dtype, T, far, 3)
     i32 = lambda n, x: torch.full((n,), x, dtype=torch.int32, device="cuda")
