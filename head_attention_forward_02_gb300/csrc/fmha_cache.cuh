@@ -12,6 +12,8 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <cfloat>
+#include <cmath>
 #include <mutex>
 
 #include "fmha_common.h"
@@ -389,6 +391,11 @@ __device__ __forceinline__ int cache_entry(const int *idx, int b, int B_cache, b
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+
+// A scale for scores in log2 units.  The kernels' FMAs flush subnormals, and a
+// masked score times a scale of 0 would be NaN.  The smallest normal gives
+// scores below 2^100 the same weights (off by 2^-26).
+inline float log2_scale(float scale) { return fminf(fmaxf(scale * kLog2e, FLT_MIN), FLT_MAX); }
 
 inline bool misaligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 

@@ -1099,7 +1099,7 @@ extern "C" int fmha_tree_fwd(fmha_tensor q, fmha_tensor k_cache, fmha_tensor v_c
     p.part_o = static_cast<float *>(workspace);
     p.part_lse = p.part_o + (size_t)2 * p.ncta * sh.NRB * kRows * kD;
     p.meta = reinterpret_cast<TreeMeta *>(p.part_lse + (size_t)2 * p.ncta * sh.NRB * kRows);
-    p.c = scale * kLog2e;
+    p.c = log2_scale(scale);
     p.out_scale = out_scale;
 
     // ---- tensor maps: boxes of one swizzle panel of dims ----

@@ -693,7 +693,7 @@ extern "C" int fmha_cache_weights(fmha_tensor q, fmha_tensor k_cache, const floa
     p.TB = w_tokens(Sq, p.G);
     p.NMMA = (p.TB * p.G + 15) / 16 * 16;
     p.causal = mask == FMHA_MASK_CAUSAL;
-    p.c = scale * kLog2e;
+    p.c = log2_scale(scale);
     const int chunks = (Sq + p.TB - 1) / p.TB;
     // units of 512 keys, or of half that where they would not fill the SMs
     const bool one = chunks == 1;
