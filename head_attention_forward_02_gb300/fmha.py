@@ -392,7 +392,8 @@ def _on(stream, index: int):
     if stream is None:
         return torch.cuda.device(index)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=index)
+        # torch takes a handle of 0, the default stream's, for none given, and makes a new stream
+        stream = torch.cuda.ExternalStream(int(stream), device=index) if int(stream) else torch.cuda.default_stream(index)
     if stream.device.index != index:
         raise ValueError(f"the stream is of {stream.device}, not of the tensors' cuda:{index}")
     return torch.cuda.stream(stream)
