@@ -112,27 +112,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, r);
 }
 
-// The same with its polling loop inlined, for places where many values are
-// live (around a call the compiler would save them all).
-__device__ __forceinline__ bool warp_wait_inline(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
-    bool r = mbar_try_wait(bar, parity);
-    if (!r) {
-        const unsigned long long t0 = globaltimer();
-        for (uint32_t it = 1;; ++it) {
-            if ((r = mbar_try_wait(bar, parity))) break;
-            if ((it & 63) == 0) {
-                if (*abort_flag) break;
-                if (globaltimer() - t0 > g_wait_ns) {
-                    *abort_flag = 1;
-                    atomicExch(&g_status, FMHA_ERR_TIMEOUT);
-                    break;
-                }
-            }
-        }
-    }
-    return __all_sync(0xffffffffu, r);
-}
-
 // Bounded wait that ignores the abort flag (only while draining).
 __device__ __noinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity) {
     const unsigned long long t0 = globaltimer();
@@ -291,17 +270,6 @@ __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
                  : "memory");
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
