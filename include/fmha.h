@@ -329,8 +329,8 @@ int fmha_tree_fwd(fmha_tensor q, fmha_tensor k_cache, fmha_tensor v_cache,
 
 /*
  * Workspace bytes fmha_tree_fwd needs for these sizes: two sets of fp32
- * partial rows per thread block of the attention kernel, at most 40 MB
- * whatever the sizes.  0 for invalid sizes.
+ * partial rows per thread block of the attention kernel, at most
+ * 40200000 whatever the sizes.  0 for invalid sizes.
  */
 size_t fmha_tree_workspace_size(int B, int T, int H, int H_k, int D, int S_max);
 
@@ -382,12 +382,13 @@ int fmha_tree_commit(fmha_tensor k_cache, fmha_tensor v_cache, fmha_tensor k_new
  * seqlen and batch_idx are treated as in fmha_tree_fwd, n_query as n_draft
  * there; nothing is written for a missing entry.  Two sequences must not share
  * an entry.  Cached rows at or past L are never used.
- * workspace: fmha_cache_weights_workspace_size() bytes (whatever the sizes,
- * 0.3 MB), 256-byte aligned, no initialisation, not shared with a concurrent
- * call.  Asynchronous on `stream` (one kernel, mostly a second one where a
- * sequence's rows may fill more than one chunk of 128).  Returns FMHA_OK,
- * FMHA_ERR_INVALID_ARG, FMHA_ERR_UNSUPPORTED (dtype, alignment, device) or
- * FMHA_ERR_CUDA.  B = 0 or Sq = 0 succeeds without a launch and writes nothing.
+ * workspace: fmha_cache_weights_workspace_size() bytes (whatever the sizes, at
+ * most 630000), 256-byte aligned, no initialisation, not shared with a
+ * concurrent call.  Asynchronous on `stream` (one kernel, mostly a second one
+ * where a sequence's rows may fill more than one chunk of 128).  Returns
+ * FMHA_OK, FMHA_ERR_INVALID_ARG, FMHA_ERR_UNSUPPORTED (dtype, alignment,
+ * device) or FMHA_ERR_CUDA.  B = 0 or Sq = 0 succeeds without a launch and
+ * writes nothing.
  */
 int fmha_cache_weights(fmha_tensor q, fmha_tensor k_cache, const float *lse, const float *acc_in, float *acc_out,
                        int B, int Sq, int H, int H_k, int D, int B_cache, int S_max,
