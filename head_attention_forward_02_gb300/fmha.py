@@ -123,13 +123,13 @@ def device_status(reset: bool = False) -> int:
 
 
 def set_wait_limit_ns(ns: int) -> int:
-    """Test hook (see fmha_set_wait_limit_ns): the forward kernels' bounded waits
+    """Test hook (see fmha_set_wait_limit_ns): the kernels' bounded waits
     give up after ns nanoseconds; 0 restores the default."""
     return lib().fmha_set_wait_limit_ns(int(ns))
 
 
 def set_test_gate(on: bool) -> int:
-    """Test hook (see fmha_set_test_gate): the forward's producer first waits for
+    """Test hook (see fmha_set_test_gate): the kernels' producers first wait for
     a flag that nothing sets."""
     return lib().fmha_set_test_gate(1 if on else 0)
 

@@ -296,9 +296,9 @@ size_t fmha_gen_workspace_size(int B, int H, int H_k, int D, int S_max);
  *                      draft need not see itself.
  *   lse                float [B, H, T], or NULL
  * All tensors share one dtype, FMHA_F16, FMHA_BF16 or FMHA_E4M3; D must be
- * 128, H / H_k at most 128 and S_max at most 2^30.  Device pointers must be
- * 16-byte aligned (int32 and lse 4-byte); o, lse and the workspace are apart
- * from the inputs and from one another.
+ * 128, H / H_k at most 128, S_max at most 2^30 and B * T below 2^24.  Device
+ * pointers must be 16-byte aligned (int32 and lse 4-byte); o, lse and the
+ * workspace are apart from the inputs and from one another.
  * P is rounded to the tensors' dtype before P.V (its row sum is not): a weight
  * by half a step, and below the type's normal range by 2^-32 (fp16) of the row's
  * sum, or all of these together by 2^-5 of it (e4m3), at most.  O is rounded
@@ -377,7 +377,8 @@ int fmha_tree_commit(fmha_tensor k_cache, fmha_tensor v_cache, fmha_tensor k_new
  * acc_in, acc_out float [B_cache, H_k, S_max], the same array or apart; seqlen,
  * batch_idx, n_query int32 [B] (the last two may be NULL).  The workspace, and
  * acc_out but for acc_in, are apart from the other arrays.  H / H_k at most
- * 128, S_max at most 2^30.  q and k_cache 16-byte, the others 4-byte aligned.
+ * 128, S_max at most 2^30, B * Sq below 2^24.  q and k_cache 16-byte, the
+ * others 4-byte aligned.
  * Sums are fp32 in an order that does not depend on timing.
  * seqlen and batch_idx are treated as in fmha_tree_fwd, n_query as n_draft
  * there; nothing is written for a missing entry.  Two sequences must not share
@@ -487,8 +488,9 @@ const char *fmha_status_string(int status);
  * fmha_device_status -- read the device-side status word of the current
  * device: FMHA_OK, FMHA_ERR_TIMEOUT if a kernel gave up a bounded wait
  * (it then skipped its remaining work and released its resources), or
- * FMHA_ERR_INVALID_ARG if fmha_gen_fwd met a sequence length or cache entry
- * outside its bounds.
+ * FMHA_ERR_INVALID_ARG if fmha_gen_fwd, fmha_tree_fwd, fmha_tree_commit,
+ * fmha_cache_weights or fmha_cache_evict met a length, count, cache entry or
+ * draft outside its bounds.
  * Synchronises the device.  reset != 0 clears the word.  Returns
  * FMHA_ERR_CUDA if the word cannot be read.
  */
@@ -496,19 +498,21 @@ int fmha_device_status(int reset);
 
 /*
  * fmha_set_wait_limit_ns -- test hook for the failure path of fmha_fwd,
- * fmha_fwd_splitkv, fmha_gen_fwd and fmha_bwd: their bounded on-device waits
- * give up after ns nanoseconds instead of 4 s (ns = 0 restores 4 s).  A wait
- * that expires records FMHA_ERR_TIMEOUT for fmha_device_status and makes the
- * call's CTAs stop issuing work, wait (bounded) for the copies and MMAs they
- * have in flight, free their tensor memory and exit; the outputs of that call
- * are then undefined and the context stays usable.  Applies to launches that
- * start after the call returns.  Returns FMHA_OK or FMHA_ERR_CUDA.
+ * fmha_fwd_splitkv, fmha_gen_fwd, fmha_tree_fwd, fmha_cache_weights and
+ * fmha_bwd: their bounded on-device waits give up after ns nanoseconds instead
+ * of 4 s (ns = 0 restores 4 s).  A wait that expires records FMHA_ERR_TIMEOUT
+ * for fmha_device_status and makes the call's CTAs stop issuing work, wait
+ * (bounded) for the copies and MMAs they have in flight, free their tensor
+ * memory and exit; the outputs of that call are then undefined and the context
+ * stays usable.  Applies to launches that start after the call returns.
+ * Returns FMHA_OK or FMHA_ERR_CUDA.
  */
 int fmha_set_wait_limit_ns(unsigned long long ns);
 
 /*
  * fmha_set_test_gate -- test hook: while on (on != 0), the producer warp of
- * every fmha_fwd / fmha_fwd_splitkv CTA, of every fmha_gen_fwd attention CTA
+ * every fmha_fwd / fmha_fwd_splitkv CTA, of every fmha_gen_fwd and
+ * fmha_tree_fwd attention CTA, of every fmha_cache_weights CTA that reads keys
  * and of every fmha_bwd dQ and dK/dV CTA first waits for a device flag that
  * nothing sets, so that bounded wait expires after the limit of
  * fmha_set_wait_limit_ns and the launch takes the failure path above before
