@@ -165,6 +165,11 @@ int fmha_set_test_gate(int on) {
 }
 
 int fmha_device_status(int reset) {
+    // the copies below wait for the default stream alone, not for streams created without blocking on it
+    if (cudaDeviceSynchronize() != cudaSuccess) {
+        cudaGetLastError();
+        return FMHA_ERR_CUDA;
+    }
     const int a = fmha::sm103_read_status(reset);
     const int b = fmha::gen_read_status(reset);
     const int c = fmha::bwd_read_status(reset);
