@@ -9,25 +9,42 @@
 #include "fmha_common.h"
 
 namespace fmha {
-int gen_read_status(int reset);   // fmha_gen.cu: the generation kernels' status word
+int *gen_status_word();   // fmha_gen.cu: the generation kernels' status word
 int gen_set_wait_limit(unsigned long long ns);   // fmha_gen.cu: its wait limit (0: 4 s)
 int gen_set_test_gate(int on);                   // fmha_gen.cu: its producer test gate
-int bwd_read_status(int reset);   // fmha_bwd.cu: the backward kernels' status word
+int *bwd_status_word();   // fmha_bwd.cu: the backward kernels' status word
 int bwd_set_wait_limit(unsigned long long ns);   // fmha_bwd.cu: its wait limit (0: 4 s)
 int bwd_set_test_gate(int on);                   // fmha_bwd.cu: its producer test gate
-int tree_read_status(int reset);   // fmha_tree.cu: the drafted-tree kernels' status word
+int *tree_status_word();   // fmha_tree.cu: the drafted-tree kernels' status word
 int tree_set_wait_limit(unsigned long long ns);  // fmha_tree.cu: its wait limit (0: 4 s)
 int tree_set_test_gate(int on);                  // fmha_tree.cu: its producer test gate
-int weights_read_status(int reset);              // fmha_weights.cu: likewise
+int *weights_status_word();                      // fmha_weights.cu: likewise
 int weights_set_wait_limit(unsigned long long ns);
 int weights_set_test_gate(int on);
-int evict_read_status(int reset);                // fmha_evict.cu: its status word (it has no waits)
+int *evict_status_word();                        // fmha_evict.cu: its status word (it has no waits)
 }
 
 namespace fmha {
 namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// The first error among the kernels' status words, and the words cleared: one
+// launch and one copy for all (a copy a word and file took 58 us a call).
+constexpr int kWords = 6;
+struct StatusWords {
+    int *word[kWords];
+};
+__device__ int g_first_error;
+
+__global__ void gather_status_kernel(const StatusWords w, int reset) {
+    const int lane = threadIdx.x;
+    int v = 0;
+    if (lane < kWords) v = reset ? atomicExch(w.word[lane], 0) : atomicOr(w.word[lane], 0);
+    const unsigned hit = __ballot_sync(0xffffffffu, v != 0);
+    v = __shfl_sync(0xffffffffu, v, hit ? __ffs(hit) - 1 : 0);
+    if (lane == 0) g_first_error = v;
+}
 
 }  // namespace
 
@@ -165,20 +182,22 @@ int fmha_set_test_gate(int on) {
 }
 
 int fmha_device_status(int reset) {
-    // the copies below wait for the default stream alone, not for streams created without blocking on it
-    if (cudaDeviceSynchronize() != cudaSuccess) {
-        cudaGetLastError();
-        return FMHA_ERR_CUDA;
+    using namespace fmha;
+    static std::mutex mu;                // of g_first_error
+    std::lock_guard<std::mutex> lk(mu);
+    // the launch below waits for the default stream alone, not for streams created without blocking on it
+    bool ok = cudaDeviceSynchronize() == cudaSuccess;
+    const StatusWords w = {sm103_status_word(), gen_status_word(), bwd_status_word(),
+                           tree_status_word(), weights_status_word(), evict_status_word()};
+    for (const int *p : w.word) ok = ok && p;
+    int v = 0;
+    if (ok) {
+        gather_status_kernel<<<1, 32>>>(w, reset);
+        ok = cudaGetLastError() == cudaSuccess && cudaMemcpyFromSymbol(&v, g_first_error, sizeof(v)) == cudaSuccess;
     }
-    const int a = fmha::sm103_read_status(reset);
-    const int b = fmha::gen_read_status(reset);
-    const int c = fmha::bwd_read_status(reset);
-    const int d = fmha::tree_read_status(reset);
-    const int e = fmha::weights_read_status(reset);
-    const int f = fmha::evict_read_status(reset);
-    for (int s : {a, b, c, d, e})
-        if (s != FMHA_OK) return s;
-    return f;
+    if (ok) return v;
+    cudaGetLastError();
+    return FMHA_ERR_CUDA;
 }
 
 int fmha_kv_tile_range(int q_row0, int q_rows, int Sq, int Sk, int mask, int causal_type,

@@ -1276,15 +1276,7 @@ int bwd_set_test_gate(int on) {
     return FMHA_OK;
 }
 
-int bwd_read_status(int reset) {
-    int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_bwd_status, sizeof(int)) != cudaSuccess) return FMHA_ERR_CUDA;
-    if (reset && v != 0) {
-        const int z = 0;
-        if (cudaMemcpyToSymbol(g_bwd_status, &z, sizeof(int)) != cudaSuccess) return FMHA_ERR_CUDA;
-    }
-    return v;
-}
+int *bwd_status_word() { return symbol_address(g_bwd_status); }
 
 }  // namespace fmha
 

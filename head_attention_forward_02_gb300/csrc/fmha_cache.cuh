@@ -4,7 +4,7 @@
 //
 // Everything is in an unnamed namespace: each translation unit that includes
 // this file has its own status word, wait limit and test gate, which its
-// read_status / set_wait_limit / set_test_gate functions serve.
+// status_word / set_wait_limit / set_test_gate functions serve.
 #pragma once
 
 #include <cuda.h>
@@ -469,14 +469,6 @@ inline int cache_set_wait_limit(unsigned long long ns) {
 inline int cache_set_test_gate(int on) {
     const int v = on ? 1 : 0;
     return cudaMemcpyToSymbol(g_test_gate, &v, sizeof(v)) == cudaSuccess ? FMHA_OK : cuda_failed();
-}
-
-inline int cache_read_status(int reset) {
-    int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_status, sizeof(int)) != cudaSuccess) return cuda_failed();
-    const int z = 0;
-    if (reset && v != 0 && cudaMemcpyToSymbol(g_status, &z, sizeof(z)) != cudaSuccess) return cuda_failed();
-    return v;
 }
 
 }  // namespace

@@ -42,6 +42,17 @@ struct Params {
 FMHA_HD int imin(int a, int b) { return a < b ? a : b; }
 FMHA_HD int imax(int a, int b) { return a > b ? a : b; }
 
+#if defined(__CUDACC__)
+// Where a __device__ variable is on the current device; NULL without one.
+template <class T>
+inline T *symbol_address(const T &symbol) {
+    void *p = nullptr;
+    if (cudaGetSymbolAddress(&p, symbol) == cudaSuccess) return static_cast<T *>(p);
+    cudaGetLastError();
+    return nullptr;
+}
+#endif
+
 // Key-tile bounds of one query tile ("CUTLASS Blackwell FMHA 示例完全解析",
 // §融合扩展点: the mask classes report a trip count and split it into tiles
 // that need the mask and tiles that do not).
@@ -80,7 +91,7 @@ int check_device();
 int launch_simt(const Params &p, cudaStream_t stream);
 int launch_sm103(const Params &p, cudaStream_t stream);
 int launch_combine(const Params &p, cudaStream_t stream);
-int sm103_read_status(int reset);
+int *sm103_status_word();                          // NULL: no device
 int sm103_set_wait_limit(unsigned long long ns);   // 0: the default (4 s)
 int sm103_set_test_gate(int on);
 

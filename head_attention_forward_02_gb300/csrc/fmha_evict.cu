@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kMoveThreads) fmha_evict_move_kernel(const Evi
 
 }  // namespace
 
-int evict_read_status(int reset) { return cache_read_status(reset); }
+int *evict_status_word() { return symbol_address(g_status); }
 
 }  // namespace fmha
 

@@ -1435,15 +1435,7 @@ int gen_set_test_gate(int on) {
     return FMHA_OK;
 }
 
-int gen_read_status(int reset) {
-    int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_gen_status, sizeof(int)) != cudaSuccess) return FMHA_ERR_CUDA;
-    if (reset && v != 0) {
-        const int z = 0;
-        if (cudaMemcpyToSymbol(g_gen_status, &z, sizeof(int)) != cudaSuccess) return FMHA_ERR_CUDA;
-    }
-    return v;
-}
+int *gen_status_word() { return symbol_address(g_gen_status); }
 
 }  // namespace fmha
 

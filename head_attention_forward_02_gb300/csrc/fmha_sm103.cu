@@ -1716,20 +1716,6 @@ int sm103_set_test_gate(int on) {
     return FMHA_OK;
 }
 
-int sm103_read_status(int reset) {
-    int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_status, sizeof(int)) != cudaSuccess) {
-        cudaGetLastError();
-        return FMHA_ERR_CUDA;
-    }
-    if (reset) {
-        const int zero = 0;
-        if (cudaMemcpyToSymbol(g_status, &zero, sizeof(int)) != cudaSuccess) {
-            cudaGetLastError();
-            return FMHA_ERR_CUDA;
-        }
-    }
-    return v;
-}
+int *sm103_status_word() { return symbol_address(g_status); }
 
 }  // namespace fmha

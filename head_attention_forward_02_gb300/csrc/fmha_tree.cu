@@ -1020,7 +1020,7 @@ int tree_smem(int nrb) {
 
 int tree_set_wait_limit(unsigned long long ns) { return cache_set_wait_limit(ns); }
 int tree_set_test_gate(int on) { return cache_set_test_gate(on); }
-int tree_read_status(int reset) { return cache_read_status(reset); }
+int *tree_status_word() { return symbol_address(g_status); }
 
 }  // namespace fmha
 

@@ -632,7 +632,7 @@ int w_tokens(int Sq, int G) { return imin(kRows / G, Sq); }
 
 int weights_set_wait_limit(unsigned long long ns) { return cache_set_wait_limit(ns); }
 int weights_set_test_gate(int on) { return cache_set_test_gate(on); }
-int weights_read_status(int reset) { return cache_read_status(reset); }
+int *weights_status_word() { return symbol_address(g_status); }
 
 }  // namespace fmha
 
