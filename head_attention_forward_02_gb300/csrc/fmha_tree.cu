@@ -39,15 +39,17 @@
 // workspace, at most two per CTA, and a second kernel joins them; units that
 // one CTA covers are written to O directly.
 //
-// Measured (kernel and merge): B=32, T=64, 8192 keys, H=32, H_k=8, bf16 221 us:
-// 5.0 TB/s and 1.25 PFLOP/s at once, near both; the two groups take a 64 KB pair
-// of K and V tiles in 3100 cycles, at the copy rate it would arrive in 2840.
-// One row block (SPLIT): B=16, T=27, 4096 ragged f16 keys 51 us, 3.5 TB/s
-// (between the first and the last tile 5.8); B=16, T=5, H=64, H_k=8, 16384
-// ragged e4m3 keys 82 us, 4.2 TB/s.  There a group's chain S -> softmax -> P V
-// -> next S takes 3000 cycles a tile of its own; of the time 4 us pass before
-// the first S, 4 at a unit's ends, 5 between the first CTA's end and the last,
-// and 4 to 6 in the merge.  B=1, T=8, 1000 keys: 13.7 us, all latency.
+// Measured (kernel and merge, in us; S: from the start to the first S of a CTA,
+// tiles: from a unit's first S to its last P V, ends: what its units' ends take, all
+// of the average CTA; spread: from its end to the last one's):
+//                                              all   S  tiles  ends  spread  merge
+//   B=32 T=64 32/8 heads, 8192 keys, bf16      221   7    175    17       6     12
+//   B=16 T=27 32/8, 4096 ragged, f16            51   5     23     6       5      6
+//   B=16 T=5  64/8, 16384 ragged, e4m3       75-84   4     58     5      10      4
+// (e4m3: 75 on one GPU, 84 on another.)  In the tiles' time keys and values come
+// at 6.2, 7.9 (with what the ring held before) and 6.1 TB/s.  The spread of e4m3
+// is not the cut's: CTAs take 680 to 940 ns a tile, the same ones pass after
+// pass.  B=1, T=8, 1000 keys: 13.7 us, all latency.
 #include "fmha_cache.cuh"
 
 namespace fmha {
