@@ -22,6 +22,7 @@ int *weights_status_word();                      // fmha_weights.cu: likewise
 int weights_set_wait_limit(unsigned long long ns);
 int weights_set_test_gate(int on);
 int *evict_status_word();                        // fmha_evict.cu: its status word (it has no waits)
+int *page_status_word();                         // fmha_page.cu: likewise
 }
 
 namespace fmha {
@@ -31,7 +32,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 // The first error among the kernels' status words, and the words cleared: one
 // launch and one copy for all (a copy a word and file took 58 us a call).
-constexpr int kWords = 6;
+constexpr int kWords = 7;
 struct StatusWords {
     int *word[kWords];
 };
@@ -188,7 +189,7 @@ int fmha_device_status(int reset) {
     // the launch below waits for the default stream alone, not for streams created without blocking on it
     bool ok = cudaDeviceSynchronize() == cudaSuccess;
     const StatusWords w = {sm103_status_word(), gen_status_word(), bwd_status_word(),
-                           tree_status_word(), weights_status_word(), evict_status_word()};
+                           tree_status_word(), weights_status_word(), evict_status_word(), page_status_word()};
     for (const int *p : w.word) ok = ok && p;
     int v = 0;
     if (ok) {

@@ -1,0 +1,544 @@
+// fmha_page.cu -- the plan of a step on a paged K/V cache (block tables and
+// slot maps from request lengths), and the write of new keys and values into
+// pages of e4m3 codes with a scale per page and kv head.
+//
+// Plan: with P tokens a page, L = seqlen[b] and n = n_new[b], n < 0 drops the
+// last -n tokens, and the pages that become empty go onto a stack of free
+// ones, in the order of the sequences; n >= 0 needs ceil((L + n) / P) -
+// ceil(L / P) pages from its top.  With c_b the running sum of these needs, a
+// sequence gets all of them if c_b is at most what the stack holds, else none.
+// Sums of whole numbers, so no order of threads shows.
+//
+// One cluster of up to eight CTAs does it in one launch: every CTA scans all
+// sequences for itself (5 words each, kept in shared memory), the cluster
+// waits until all have read what the call may overwrite in place, and then
+// each thread takes every (cluster size * 1024)-th page taken, page given back
+// and token, and finds its sequence by bisection.  What a token's slot needs of
+// pages taken by this call comes from the stack, not from the table that
+// other threads write, so there is nothing else to wait for.  Bound by latency
+// (a launch, two dependent reads, a scan, a bisection).
+//
+// Write: a run of tokens with consecutive slots in one page (some of them
+// perhaps left out, by a negative slot); for each kv head
+// and of K and V, a = max |x| over it and
+//   s = max(scale before, 2^e), e the least with a <= 448 * 2^e
+// (a run that begins its page: s = 2^e), rows before the run are rounded again
+// to code * (scale before / s) where the scale grew, and the new rows are
+// e4m3(x / s).  Scales are powers of two: e4m3 has the same relative step in
+// every binade, so a finer scale would not make values more exact, and x / s and
+// the old rows' factor are exact, which leaves each value one rounding (a row
+// whose scale grows into e4m3's subnormals: two).
+//
+// Bound by memory: 2 bytes in and 1 out an element.  A CTA takes 16 tokens of one
+// head, K or V; a run of up to eight rows is a warp's (a decode step's are
+// one), a longer one is spread over the CTA's warps, all its loads in flight at
+// once and held in registers between the maximum and the rounding.
+#include <cooperative_groups.h>
+
+#include "fmha_cache.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace fmha {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Plan
+// ---------------------------------------------------------------------------
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanSeqs = 8192;          // sequences at most: five words each in shared memory
+
+struct PlanParams {
+    const int *seqlen, *n_new, *batch_idx, *n_free;
+    int *table, *free_list, *n_free_out, *slots, *positions, *cu_new, *new_seqlen;
+    int B, N, entries, width, shift, cap;   // cap: pages of the cache, and elements of free_list
+};
+
+struct PlanSums {
+    long long need, given, tokens;
+};
+
+// Exclusive sums over the CTA's threads; total: of all.
+__device__ PlanSums plan_scan(PlanSums v, PlanSums &total) {
+    __shared__ PlanSums warp_sum[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    PlanSums incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long a = __shfl_up_sync(0xffffffffu, incl.need, o), b = __shfl_up_sync(0xffffffffu, incl.given, o),
+                        c = __shfl_up_sync(0xffffffffu, incl.tokens, o);
+        if (lane >= o) {
+            incl.need += a;
+            incl.given += b;
+            incl.tokens += c;
+        }
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    PlanSums base = {0, 0, 0};
+    total = base;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
+        const PlanSums s = warp_sum[w];
+        if (w < warp) base = PlanSums{base.need + s.need, base.given + s.given, base.tokens + s.tokens};
+        total = PlanSums{total.need + s.need, total.given + s.given, total.tokens + s.tokens};
+    }
+    return PlanSums{base.need + incl.need - v.need, base.given + incl.given - v.given, base.tokens + incl.tokens - v.tokens};
+}
+
+// The last of the n ascending values that is at most x (the first is 0).
+__device__ __forceinline__ int last_at_most(const int *v, int n, int x) {
+    int lo = 0, hi = n;                  // v[lo] <= x; v[hi] > x
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (v[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// What a request asks for, with everything outside its bounds clamped.
+struct PlanRequest {
+    int L, n;                            // cached tokens, change (at least -L)
+    bool fits;                           // its table row and the call's tokens hold it
+};
+__device__ __forceinline__ PlanRequest plan_request(const PlanParams &p, int b, bool report) {
+    PlanRequest r;
+    const int most = p.width << p.shift;
+    const bool entry = cache_entry(p.batch_idx, b, p.entries, report) >= 0;
+    r.L = clamped(p.seqlen[b], 0, most, report);
+    r.n = clamped(p.n_new[b], -r.L, 0x7fffffff, report);
+    r.fits = entry && r.n <= most - r.L;
+    if (!entry && r.n < 0) r.n = 0;      // no row to take pages from
+    if (entry && !r.fits && report) atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
+    return r;
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) fmha_page_plan_kernel(const PlanParams p) {
+    extern __shared__ int smem_i[];
+    __shared__ int s_granted;
+    int *s_len = smem_i, *s_new = s_len + p.B, *s_need = s_new + p.B, *s_given = s_need + p.B, *s_cu = s_given + p.B;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int mask = (1 << p.shift) - 1;
+    const bool report = rank == 0;
+    if (threadIdx.x == 0) s_granted = 0;
+
+    // ---- every CTA: the sums of pages needed, pages given back and tokens before each sequence ----
+    const int per = (p.B + blockDim.x - 1) / blockDim.x, b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
+    PlanSums mine = {0, 0, 0};
+    for (int b = b0; b < b1; ++b) {
+        const PlanRequest r = plan_request(p, b, report);
+        const int had = (r.L + mask) >> p.shift, want = (int)(((long long)r.L + r.n + mask) >> p.shift);
+        s_len[b] = r.fits ? r.L : ~r.L;  // a request that cannot fit: the complement
+        s_new[b] = r.n;
+        if (r.fits && r.n > 0) mine.need += want - had;
+        if (r.n < 0) mine.given += had - want;
+        mine.tokens += r.n > 0 ? r.n : 0;
+    }
+    PlanSums total;
+    PlanSums at = plan_scan(mine, total);
+    const int spare = clamped(p.n_free[0], 0, p.cap, report && threadIdx.x == 0);
+    const bool over = spare + total.given > p.cap;            // more pages than there are: a page given twice
+    const int avail = over ? p.cap : (int)(spare + total.given);
+    if (report && threadIdx.x == 0 && (over || total.tokens > p.N)) atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
+    long long granted = 0;               // the largest sum of needs that the stack holds
+    for (int b = b0; b < b1; ++b) {
+        const int L = s_len[b] < 0 ? ~s_len[b] : s_len[b], n = s_new[b];
+        const int had = (L + mask) >> p.shift, want = (int)(((long long)L + n + mask) >> p.shift);
+        s_need[b] = (int)min(at.need, 0x7fffffffll);
+        s_given[b] = (int)min(at.given, (long long)avail - spare);
+        s_cu[b] = (int)min(at.tokens, (long long)p.N);
+        if (s_len[b] >= 0 && n > 0) at.need += want - had;
+        if (n < 0) at.given += had - want;
+        at.tokens += n > 0 ? n : 0;
+        if (at.need <= avail) granted = at.need;
+    }
+    if (granted > 0) atomicMax(&s_granted, (int)granted);
+    // all CTAs have read the lengths and the count that the call may write in place
+    cluster.sync();
+
+    const int taken = s_granted, given = avail - spare, tokens = (int)min(total.tokens, (long long)p.N);
+    const int first = rank * blockDim.x + threadIdx.x, step = ranks * blockDim.x;
+    auto row = [&](int b) { return p.table + (int64_t)(p.batch_idx ? p.batch_idx[b] : b) * p.width; };
+    auto len = [&](int b) { return s_len[b] < 0 ? ~s_len[b] : s_len[b]; };
+    auto need = [&](int b) {
+        return s_len[b] >= 0 && s_new[b] > 0 ? ((s_len[b] + s_new[b] + mask) >> p.shift) - ((s_len[b] + mask) >> p.shift) : 0;
+    };
+    auto granted_to = [&](int b) { return s_len[b] >= 0 && (need(b) == 0 || (long long)s_need[b] + need(b) <= taken); };
+    // j-th page given back; k-th page taken, from the stack's top down
+    auto page_given = [&](int j) {
+        const int b = last_at_most(s_given, p.B, j);
+        return row(b)[((len(b) + s_new[b] + mask) >> p.shift) + j - s_given[b]];
+    };
+    auto page_taken = [&](int k) {
+        const int i = avail - 1 - k;
+        return i < spare ? p.free_list[i] : page_given(i - spare);
+    };
+    if (first == 0) {
+        p.n_free_out[0] = avail - taken;
+        p.cu_new[p.B] = tokens;
+    }
+    for (int b = first; b < p.B; b += step) {
+        p.cu_new[b] = s_cu[b];
+        p.new_seqlen[b] = s_new[b] < 0 || granted_to(b) ? len(b) + s_new[b] : len(b);
+    }
+    for (int j = first; j < given; j += step) p.free_list[spare + j] = page_given(j);
+    for (int k = first; k < taken; k += step) {
+        const int b = last_at_most(s_need, p.B, k);
+        row(b)[((s_len[b] + mask) >> p.shift) + k - s_need[b]] = page_taken(k);
+    }
+    for (int i = first; i < p.N; i += step) {
+        int pos = -1, slot = -1;
+        if (i < tokens) {
+            const int b = last_at_most(s_cu, p.B, i);
+            const int L = len(b), x = i - s_cu[b];
+            pos = L + x;
+            if (granted_to(b)) {
+                const int had = (L + mask) >> p.shift, at_page = pos >> p.shift;
+                const int page = at_page < had ? row(b)[at_page] : page_taken(s_need[b] + at_page - had);
+                if (page >= 0 && page < p.cap) slot = (page << p.shift) + (pos & mask);
+                else atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
+            }
+        }
+        p.slots[i] = slot;
+        p.positions[i] = pos;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Write
+// ---------------------------------------------------------------------------
+
+constexpr int kWriteChunk = 16;          // tokens of a CTA
+constexpr int kWriteWarps = 8;
+constexpr int kWarpRows = 8;             // longest run of a single warp
+constexpr int kLowest = -60, kHighest = 60;   // exponents of the scales
+
+struct WriteParams {
+    const uint8_t *x[2];                 // new keys, values: [N, H_k, 128] with strides
+    int64_t x_t[2], x_h[2];              // in bytes
+    uint8_t *pages[2];                   // [n_pages, H_k, P, 128]
+    float *scale[2];                     // [n_pages, H_k]
+    const int *slots;                    // [N]
+    int N, H_k, shift, slots_end;        // slots_end: n_pages * P
+};
+
+template <bool BF>
+__device__ __forceinline__ float2 wide2(uint32_t w) {
+    if constexpr (BF) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+template <bool BF>
+__device__ __forceinline__ float abs_max(uint4 v, float a) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = wide2<BF>(w[i]);
+        a = fmaxf(a, fmaxf(fabsf(x.x), fabsf(x.y)));         // a NaN does not count
+    }
+    return a;
+}
+template <bool BF>
+__device__ __forceinline__ uint2 codes8(uint4 v, float inv) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float2 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[i] = wide2<BF>(w[i]);
+        x[i].x *= inv;
+        x[i].y *= inv;
+    }
+    return make_uint2(pack4_e4m3(x[0].x, x[0].y, x[1].x, x[1].y), pack4_e4m3(x[2].x, x[2].y, x[3].x, x[3].y));
+}
+
+// The least power of two that brings a to 448 = 1.75 * 2^8 or below it, within
+// the bounds.
+__device__ __forceinline__ int scale_exponent(float a) {
+    const uint32_t u = __float_as_uint(a);
+    const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return min(max(e, kLowest), kHighest);
+}
+
+__device__ __forceinline__ float warp_max(float a) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return a;
+}
+
+// Four codes times a power of two (or any factor), rounded again.
+__device__ __forceinline__ uint32_t again4(uint32_t c, float f) {
+    const __half2 lo = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3));
+    const __half2 hi = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3));
+    const float2 a = __half22float2(lo), b = __half22float2(hi);
+    return pack4_e4m3(a.x * f, a.y * f, b.x * f, b.y * f);
+}
+
+// A run: tokens [i, i + n) become rows [off, off + n) of a page.
+struct Run {
+    uint8_t *rows;                       // the page's head: its first row
+    float *scale;
+    int off;
+};
+__device__ __forceinline__ Run run_of(const WriteParams &p, int slot, int g, int kv) {
+    const int64_t head = (int64_t)(slot >> p.shift) * p.H_k + g;
+    return Run{(kv ? p.pages[1] : p.pages[0]) + ((head << p.shift) << 7), (kv ? p.scale[1] : p.scale[0]) + head, slot & ((1 << p.shift) - 1)};
+}
+
+// The scale of a run whose largest value is a; old: what it was (rows before).
+__device__ __forceinline__ float run_scale(const Run &r, float a, float &old) {
+    const float s = __uint_as_float((uint32_t)(scale_exponent(a) + 127) << 23);
+    old = r.off > 0 ? *r.scale : 0.f;
+    return fmaxf(old, s);
+}
+
+// Rows [first, off) of the page by `step` groups of eight lanes, each a row at a time, four in flight.
+__device__ __forceinline__ void rescale_rows(const Run &r, float f, int first, int step) {
+    uint4 *rows = reinterpret_cast<uint4 *>(r.rows) + (threadIdx.x & 7);
+    for (int j = first; j < r.off; j += 4 * step) {
+        uint4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (j + k * step < r.off) v[k] = rows[(j + k * step) * 8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (j + k * step < r.off)
+                rows[(j + k * step) * 8] = make_uint4(again4(v[k].x, f), again4(v[k].y, f), again4(v[k].z, f), again4(v[k].w, f));
+    }
+}
+
+template <bool BF>
+__global__ void __launch_bounds__(32 * kWriteWarps) fmha_page_write_kernel(const WriteParams p) {
+    __shared__ int s_len[kWriteChunk];   // of the long run that begins at a token
+    __shared__ float s_max[kWriteWarps];
+    const int c0 = blockIdx.x * kWriteChunk, g = blockIdx.y, kv = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int P = 1 << p.shift;
+    // where runs begin, and how far they go
+    const int i = c0 + lane;
+    const int slot = lane < kWriteChunk && i < p.N ? p.slots[i] : -1;
+    const bool inside = slot >= 0 && slot < p.slots_end;
+    bool begins = inside;
+    for (int j = 1; begins && j <= min(i, slot & (P - 1)); ++j) {
+        const int other = p.slots[i - j];
+        if (other == slot - j) begins = false;               // of the same run
+        else if (other >= 0) break;
+    }
+    if (warp == 0 && g == 0 && kv == 0 && slot >= p.slots_end) atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
+    const unsigned starts = __ballot_sync(0xffffffffu, begins);
+    if (starts == 0) return;             // the same in every warp
+    // selected, not indexed: an index would put the parameters into local memory
+    const int64_t x_t = kv ? p.x_t[1] : p.x_t[0];
+    const uint8_t *x0 = kv ? p.x[1] + g * p.x_h[1] : p.x[0] + g * p.x_h[0];
+    unsigned longer = 0;                 // runs for the whole CTA: the same in every warp
+    int nth = 0;
+    for (unsigned todo = starts; todo; todo &= todo - 1, ++nth) {
+        const int t = __ffs(todo) - 1, s = __shfl_sync(0xffffffffu, slot, t);
+        const int room = min(P - (s & (P - 1)), p.N - (c0 + t));
+        int n = 1;
+        while (n < room) {
+            const int j = n + lane, at = j < room ? p.slots[c0 + t + j] : 0;
+            const unsigned stop = __ballot_sync(0xffffffffu, j >= room || (at >= 0 && at != s + j));
+            n += stop ? __ffs(stop) - 1 : 32;
+            if (stop) break;
+        }
+        if (n > kWarpRows) {
+            longer |= 1u << t;
+            if (warp == 0 && lane == 0) s_len[t] = n;
+            continue;
+        }
+        if (nth % kWriteWarps != warp) continue;
+        // half a warp a row, all rows in flight
+        const Run r = run_of(p, s, g, kv);
+        const int half = lane >> 4, col = (lane & 15) * 16;
+        const uint8_t *x = x0 + (c0 + t) * x_t + col;
+        uint4 v[kWarpRows / 2];
+        bool live[kWarpRows / 2];
+        float a = 0.f, old;
+#pragma unroll
+        for (int k = 0; k < kWarpRows / 2; ++k) {
+            live[k] = 2 * k + half < n && p.slots[c0 + t + 2 * k + half] >= 0;
+            if (2 * k + half < n) v[k] = *reinterpret_cast<const uint4 *>(x + (2 * k + half) * x_t);
+        }
+#pragma unroll
+        for (int k = 0; k < kWarpRows / 2; ++k)
+            if (live[k]) a = abs_max<BF>(v[k], a);
+        const float sc = run_scale(r, warp_max(a), old);
+        if (r.off > 0 && sc > old) rescale_rows(r, old / sc, lane >> 3, 4);
+        const float inv = 1.f / sc;
+#pragma unroll
+        for (int k = 0; k < kWarpRows / 2; ++k)
+            if (live[k])
+                *reinterpret_cast<uint2 *>(r.rows + (r.off + 2 * k + half) * 128 + col / 2) = codes8<BF>(v[k], inv);
+        __syncwarp();
+        if (lane == 0) *r.scale = sc;
+    }
+    if (longer == 0) return;
+    __syncthreads();
+    for (; longer; longer &= longer - 1) {
+        const int t = __ffs(longer) - 1, s = __shfl_sync(0xffffffffu, slot, t);
+        const int n = s_len[t];
+        const Run r = run_of(p, s, g, kv);
+        const int row0 = warp * 2 + (lane >> 4), col = (lane & 15) * 16;
+        const uint8_t *x = x0 + (c0 + t) * x_t + col;
+        uint4 v[8];                      // rows row0, row0 + 16, ... of at most 128
+        unsigned live = 0;
+        float a = 0.f, old;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (16 * k + row0 >= n) continue;
+            v[k] = *reinterpret_cast<const uint4 *>(x + (16 * k + row0) * x_t);
+            live |= (p.slots[c0 + t + 16 * k + row0] >= 0 ? 1u : 0u) << k;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (live >> k & 1) a = abs_max<BF>(v[k], a);
+        a = warp_max(a);
+        if (lane == 0) s_max[warp] = a;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWriteWarps; ++w) a = fmaxf(a, s_max[w]);
+        const float sc = run_scale(r, a, old);
+        __syncthreads();                 // all have read the scale and the maxima
+        if (r.off > 0 && sc > old) rescale_rows(r, old / sc, threadIdx.x >> 3, 32);
+        const float inv = 1.f / sc;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (live >> k & 1)
+                *reinterpret_cast<uint2 *>(r.rows + (r.off + 16 * k + row0) * 128 + col / 2) = codes8<BF>(v[k], inv);
+        if (threadIdx.x == 0) *r.scale = sc;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+int log2_page(int page_size) {
+    for (int s = 4; s <= 7; ++s)
+        if (page_size == 1 << s) return s;
+    return -1;
+}
+
+}  // namespace
+
+int *page_status_word() { return symbol_address(g_status); }
+
+}  // namespace fmha
+
+using namespace fmha;
+
+extern "C" int fmha_page_plan(const int *seqlen, const int *n_new, const int *batch_idx, int *table, int *free_list,
+                              const int *n_free, int *n_free_out, int *slots, int *positions, int *cu_new,
+                              int *new_seqlen, int B, int N, int B_table, int max_pages, int n_pages, int page_size,
+                              cudaStream_t stream) {
+    const int shift = log2_page(page_size);
+    if (B < 0 || N < 0 || shift < 0) return FMHA_ERR_INVALID_ARG;
+    if (B == 0 && N == 0) return FMHA_OK;
+    if (B == 0 || B_table <= 0 || max_pages <= 0 || n_pages <= 0 || max_pages > kMaxCacheRows >> shift ||
+        n_pages > 0x7fffffff >> shift)
+        return FMHA_ERR_INVALID_ARG;
+    if (!seqlen || !n_new || !table || !free_list || !n_free || !n_free_out || !cu_new || !new_seqlen ||
+        (N > 0 && (!slots || !positions)))
+        return FMHA_ERR_INVALID_ARG;
+    for (const void *ptr : {(const void *)seqlen, (const void *)n_new, (const void *)batch_idx, (const void *)table,
+                            (const void *)free_list, (const void *)n_free, (const void *)n_free_out, (const void *)slots,
+                            (const void *)positions, (const void *)cu_new, (const void *)new_seqlen})
+        if (misaligned(ptr, 4)) return FMHA_ERR_INVALID_ARG;
+    if (B > kPlanSeqs) return FMHA_ERR_UNSUPPORTED;
+    const size_t seqs = (size_t)B * sizeof(int), rows = (size_t)N * sizeof(int);
+    const Bytes out[7] = {{table, (size_t)B_table * max_pages * sizeof(int)}, {free_list, (size_t)n_pages * sizeof(int)},
+                          {n_free_out, sizeof(int)}, {N ? slots : nullptr, rows}, {N ? positions : nullptr, rows},
+                          {cu_new, seqs + sizeof(int)}, {new_seqlen, seqs}};
+    // the lengths and the count of free pages may be their own outputs
+    const Bytes in[4] = {{n_new, seqs}, {batch_idx, seqs}, {new_seqlen == seqlen ? nullptr : seqlen, seqs},
+                         {n_free_out == n_free ? nullptr : n_free, sizeof(int)}};
+    if (outputs_clash(out, in)) return FMHA_ERR_INVALID_ARG;
+    const int rc = check_device();
+    if (rc != FMHA_OK) return rc;
+    PlanParams p{};
+    p.seqlen = seqlen;
+    p.n_new = n_new;
+    p.batch_idx = batch_idx;
+    p.n_free = n_free;
+    p.table = table;
+    p.free_list = free_list;
+    p.n_free_out = n_free_out;
+    p.slots = slots;
+    p.positions = positions;
+    p.cu_new = cu_new;
+    p.new_seqlen = new_seqlen;
+    p.B = B;
+    p.N = N;
+    p.entries = B_table;
+    p.width = max_pages;
+    p.shift = shift;
+    p.cap = n_pages;
+    const int smem = 5 * B * (int)sizeof(int);
+    if (smem > 47 * 1024 &&
+        cudaFuncSetAttribute(fmha_page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return cuda_failed();
+    cudaLaunchConfig_t cfg = {};
+    // one CTA where every thread has a token or a sequence at most
+    const int ranks = N > kPlanThreads || B > kPlanThreads ? 8 : 1;
+    cfg.gridDim = dim3(ranks);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ranks;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, fmha_page_plan_kernel, p) != cudaSuccess) return cuda_failed();
+    return FMHA_OK;
+}
+
+extern "C" int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_t k_head_stride, fmha_tensor v_new,
+                               int64_t v_token_stride, int64_t v_head_stride, const int *slots, fmha_tensor k_pages,
+                               fmha_tensor v_pages, float *k_scale, float *v_scale, int N, int H_k, int D, int n_pages,
+                               int page_size, cudaStream_t stream) {
+    const int shift = log2_page(page_size);
+    if (N < 0 || H_k <= 0 || H_k > 65535 || D != kD || shift < 0) return FMHA_ERR_INVALID_ARG;
+    if (N == 0) return FMHA_OK;
+    if (n_pages <= 0 || n_pages > 0x7fffffff >> shift || !slots || !k_scale || !v_scale) return FMHA_ERR_INVALID_ARG;
+    if (!k_new.data || !v_new.data || !k_pages.data || !v_pages.data) return FMHA_ERR_INVALID_ARG;
+    const int dt = k_new.dtype;
+    if ((dt != FMHA_F16 && dt != FMHA_BF16) || v_new.dtype != dt || k_pages.dtype != FMHA_E4M3 || v_pages.dtype != FMHA_E4M3)
+        return FMHA_ERR_UNSUPPORTED;
+    for (const void *ptr : {k_new.data, v_new.data, k_pages.data, v_pages.data})
+        if (misaligned(ptr, 16)) return FMHA_ERR_UNSUPPORTED;
+    for (int64_t s : {k_token_stride, k_head_stride, v_token_stride, v_head_stride}) {
+        if (s < 0 || s > (int64_t(1) << 40)) return FMHA_ERR_INVALID_ARG;
+        if (s % 8 != 0) return FMHA_ERR_UNSUPPORTED;
+    }
+    if (misaligned(slots, 4) || misaligned(k_scale, 4) || misaligned(v_scale, 4)) return FMHA_ERR_INVALID_ARG;
+    const size_t pages = ((size_t)n_pages * H_k << shift) * kD, scales = (size_t)n_pages * H_k * sizeof(float);
+    const auto span = [&](int64_t t, int64_t h) { return (size_t)((N - 1) * t + (H_k - 1) * h + kD) * 2; };
+    const Bytes out[4] = {{k_pages.data, pages}, {v_pages.data, pages}, {k_scale, scales}, {v_scale, scales}};
+    const Bytes in[3] = {{k_new.data, span(k_token_stride, k_head_stride)}, {v_new.data, span(v_token_stride, v_head_stride)},
+                         {slots, (size_t)N * sizeof(int)}};
+    if (outputs_clash(out, in)) return FMHA_ERR_INVALID_ARG;
+    const int rc = check_device();
+    if (rc != FMHA_OK) return rc;
+    WriteParams p{};
+    const fmha_tensor x[2] = {k_new, v_new}, c[2] = {k_pages, v_pages};
+    for (int i = 0; i < 2; ++i) {
+        p.x[i] = static_cast<const uint8_t *>(x[i].data);
+        p.x_t[i] = 2 * (i ? v_token_stride : k_token_stride);
+        p.x_h[i] = 2 * (i ? v_head_stride : k_head_stride);
+        p.pages[i] = static_cast<uint8_t *>(c[i].data);
+        p.scale[i] = i ? v_scale : k_scale;
+    }
+    p.slots = slots;
+    p.N = N;
+    p.H_k = H_k;
+    p.shift = shift;
+    p.slots_end = n_pages << shift;
+    const dim3 grid((unsigned)(((int64_t)N + kWriteChunk - 1) / kWriteChunk), H_k, 2);
+    if (dt == FMHA_BF16) fmha_page_write_kernel<true><<<grid, 32 * kWriteWarps, 0, stream>>>(p);
+    else fmha_page_write_kernel<false><<<grid, 32 * kWriteWarps, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? FMHA_OK : FMHA_ERR_CUDA;
+}

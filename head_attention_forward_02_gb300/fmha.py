@@ -19,6 +19,7 @@ _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfmha.so
 
 F16, BF16, E4M3 = 0, 1, 2
 MASK_NONE, MASK_RESIDUAL, MASK_CAUSAL = 0, 1, 2
+ROPE_HALF, ROPE_PAIRS = 0, 1
 CAUSAL_QBEGIN, CAUSAL_QEND = 0, 1
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT = 0, -1, -2, -3, -4
 
@@ -33,6 +34,10 @@ EXPORTED = ("fmha_fwd", "fmha_fwd_simt", "fmha_fwd_splitkv", "fmha_fwd_splitkv_w
 
 class fmha_tensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int)]
+
+
+class fmha_strides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
 class FmhaError(RuntimeError):
@@ -93,6 +98,14 @@ def lib():
         L.fmha_cache_evict.restype = ctypes.c_int
         L.fmha_cache_evict.argtypes = [fmha_tensor] * 2 + [ctypes.c_void_p] + [fmha_tensor] * 2 + [
             ctypes.c_void_p] + [ctypes.c_int] * 7 + [ctypes.c_void_p] * 3 + [ctypes.c_int] * 2 + [ctypes.c_void_p] * 3
+        L.fmha_page_plan.restype = ctypes.c_int
+        L.fmha_page_plan.argtypes = [ctypes.c_void_p] * 11 + [ctypes.c_int] * 6 + [ctypes.c_void_p]
+        L.fmha_page_write.restype = ctypes.c_int
+        L.fmha_page_write.argtypes = ([fmha_tensor] + [ctypes.c_int64] * 2) * 2 + [ctypes.c_void_p] + [
+            fmha_tensor] * 2 + [ctypes.c_void_p] * 2 + [ctypes.c_int] * 5 + [ctypes.c_void_p]
+        L.fmha_rope.restype = ctypes.c_int
+        L.fmha_rope.argtypes = [fmha_tensor, fmha_strides] * 4 + [ctypes.c_int] * 6 + [ctypes.c_void_p] * 2 + [
+            ctypes.c_float] + [ctypes.c_int] * 2 + [ctypes.c_void_p]
         L.fmha_bwd.restype = ctypes.c_int
         L.fmha_bwd.argtypes = [fmha_tensor] * 5 + [ctypes.c_void_p] + [fmha_tensor] * 3 + [ctypes.c_int] * 5 + [
             ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
@@ -633,6 +646,252 @@ def cache_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, acc: torch.Tensor,
         B_cache, S_max, B_out, S_out, seqlen.data_ptr(), _ptr(batch_idx), _ptr(out_idx), budget, recent,
         kept.data_ptr(), new_seqlen.data_ptr(), _raw_stream(index)))
     return kept, new_seqlen
+
+
+# ---------------------------------------------------------------------------
+# Paged caches of e4m3 codes, and rotary positions
+# ---------------------------------------------------------------------------
+
+def fmha_page_plan(seqlen, n_new, batch_idx, table, free_list, n_free, n_free_out, slots, positions, cu_new, new_seqlen,
+                   B, N, B_table, max_pages, n_pages, page_size, stream=None) -> int:
+    """Same arguments, order and status codes as the C function fmha_page_plan."""
+    return lib().fmha_page_plan(
+        _ptr(seqlen), _ptr(n_new), _ptr(batch_idx), _ptr(table), _ptr(free_list), _ptr(n_free), _ptr(n_free_out),
+        _ptr(slots), _ptr(positions), _ptr(cu_new), _ptr(new_seqlen), int(B), int(N), int(B_table), int(max_pages),
+        int(n_pages), int(page_size), _stream(stream))
+
+
+def page_plan(seqlen: torch.Tensor, n_new: torch.Tensor, table: torch.Tensor, free_list: torch.Tensor,
+              n_free: torch.Tensor, *, page_size: int, max_tokens: Optional[int] = None,
+              batch_idx: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+              positions: Optional[torch.Tensor] = None, cu_new: Optional[torch.Tensor] = None,
+              new_seqlen: Optional[torch.Tensor] = None, n_free_out: Optional[torch.Tensor] = None, stream=None):
+    """Block tables and slot maps of a step from request lengths (see
+    fmha_page_plan).
+
+    seqlen, n_new, batch_idx int32 [B]; table int32 [B_table, max_pages] and
+    free_list int32 [n_pages], both changed in place; n_free int32 [1], changed
+    in place unless ``n_free_out`` is given.  The step's tensors have
+    ``max_tokens`` rows (or as many as ``slots``).  Returns (slots, positions,
+    cu_new [B + 1], new_seqlen [B]), all int32; ``new_seqlen`` may be seqlen."""
+    index = n_free.get_device()
+    if index < 0:
+        raise ValueError(f"the tensors are on {n_free.device}, not on a CUDA device")
+    if stream is not None or _current_device() != index:
+        with _on(stream, index):
+            return page_plan(seqlen, n_new, table, free_list, n_free, page_size=page_size, max_tokens=max_tokens,
+                             batch_idx=batch_idx, slots=slots, positions=positions, cu_new=cu_new,
+                             new_seqlen=new_seqlen, n_free_out=n_free_out)
+    if table.dim() != 2 or seqlen.dim() != 1 or free_list.dim() != 1:
+        raise ValueError("seqlen is [B], the table is [B_table, max_pages] and free_list is [n_pages]")
+    if slots is None and positions is None and max_tokens is None:
+        raise ValueError("max_tokens, slots or positions say how many rows the step has")
+    N = max_tokens if max_tokens is not None else (slots if slots is not None else positions).shape[0]
+    i32, B = torch.int32, seqlen.shape[0]
+    new = lambda n: torch.empty((n,), dtype=i32, device=n_free.device)
+    slots = new(N) if slots is None else slots
+    positions = new(N) if positions is None else positions
+    cu_new = new(B + 1) if cu_new is None else cu_new
+    new_seqlen = new(B) if new_seqlen is None else new_seqlen
+    n_free_out = n_free if n_free_out is None else n_free_out
+    per_seq, rows = (B,), (N,)
+    if not (_fit(index, i32, per_seq, seqlen, n_new, batch_idx, new_seqlen) and _fit(index, i32, rows, slots, positions)
+            and _fit(index, i32, (B + 1,), cu_new) and _fit(index, i32, (1,), n_free, n_free_out)
+            and _fit(index, i32, table.shape, table) and _fit(index, i32, free_list.shape, free_list)):
+        _check(index, i32, per_seq, seqlen=seqlen, n_new=n_new, batch_idx=batch_idx, new_seqlen=new_seqlen)
+        _check(index, i32, rows, slots=slots, positions=positions)
+        _check(index, i32, (B + 1,), cu_new=cu_new)
+        _check(index, i32, (1,), n_free=n_free, n_free_out=n_free_out)
+        _check(index, i32, table.shape, table=table)
+        _check(index, i32, free_list.shape, free_list=free_list)
+    _raise(lib().fmha_page_plan(
+        seqlen.data_ptr(), n_new.data_ptr(), _ptr(batch_idx), table.data_ptr(), free_list.data_ptr(), n_free.data_ptr(),
+        n_free_out.data_ptr(), slots.data_ptr(), positions.data_ptr(), cu_new.data_ptr(), new_seqlen.data_ptr(), B, N,
+        table.shape[0], table.shape[1], free_list.shape[0], page_size, _raw_stream(index)))
+    return slots, positions, cu_new, new_seqlen
+
+
+def fmha_page_write(k_new, k_token_stride, k_head_stride, v_new, v_token_stride, v_head_stride, slots, k_pages, v_pages,
+                    k_scale, v_scale, N, H_k, D, n_pages, page_size, stream=None) -> int:
+    """Same arguments, order and status codes as the C function fmha_page_write."""
+    return lib().fmha_page_write(
+        _tensor(k_new), int(k_token_stride), int(k_head_stride), _tensor(v_new), int(v_token_stride), int(v_head_stride),
+        _ptr(slots), _tensor(k_pages), _tensor(v_pages), _ptr(k_scale), _ptr(v_scale), int(N), int(H_k), int(D),
+        int(n_pages), int(page_size), _stream(stream))
+
+
+def _fit_strided(index: int, dtype, shape: tuple, t) -> bool:
+    """As _fit, for a tensor of which the last dimension alone has to be contiguous."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index and (t.shape[-1] <= 1 or t.stride(-1) == 1)
+
+
+def _check_strided(index: int, dtype, shape: tuple, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is None or _fit_strided(index, dtype, shape, t):
+            continue
+        if t.get_device() == index and t.dtype is dtype and t.shape == shape:
+            raise ValueError(f"{name}'s last dimension is not contiguous")
+        _check(index, dtype, shape, **{name: t})
+
+
+def _fit_pages(index: int, k_pages, v_pages, k_scale, v_scale) -> Tuple[int, int, int, int]:
+    """(n_pages, H_k, page_size, D) of a paged cache, once its arrays are looked at."""
+    if k_pages.dim() != 4:
+        raise ValueError("the pages are [n_pages, H_k, page_size, 128]")
+    shape, e4m3 = k_pages.shape, torch.float8_e4m3fn
+    if not (_fit(index, e4m3, shape, k_pages, v_pages) and _fit(index, torch.float32, shape[:2], k_scale, v_scale)):
+        _check(index, e4m3, shape, k_pages=k_pages, v_pages=v_pages)
+        _check(index, torch.float32, shape[:2], k_scale=k_scale, v_scale=v_scale)
+    return shape
+
+
+def page_write(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor, k_pages: torch.Tensor,
+               v_pages: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, *, stream=None) -> None:
+    """Write new keys and values into a paged cache at their slots (see
+    fmha_page_write).
+
+    k_new, v_new bf16 or f16 [N, H_k, 128], of any strides that are multiples
+    of 8 (pieces of a projection's rows); slots int32 [N], negative: not
+    written; k_pages, v_pages e4m3 [n_pages, H_k, page_size, 128]; k_scale,
+    v_scale float [n_pages, H_k]."""
+    index, code = _device_and_code(k_new)
+    if stream is not None or _current_device() != index:
+        with _on(stream, index):
+            return page_write(k_new, v_new, slots, k_pages, v_pages, k_scale, v_scale)
+    if k_new.dim() != 3:
+        raise ValueError("k_new and v_new are [N, H_k, 128]")
+    n_pages, H_k, P, D = _fit_pages(index, k_pages, v_pages, k_scale, v_scale)
+    N, dt = k_new.shape[0], k_new.dtype
+    if not (_fit_strided(index, dt, (N, H_k, D), k_new) and _fit_strided(index, dt, (N, H_k, D), v_new)
+            and _fit(index, torch.int32, (N,), slots)):
+        _check_strided(index, dt, (N, H_k, D), k_new=k_new, v_new=v_new)
+        _check(index, torch.int32, (N,), slots=slots)
+    (kt, kh, _), (vt, vh, _) = k_new.stride(), v_new.stride()
+    _raise(lib().fmha_page_write(
+        fmha_tensor(k_new.data_ptr(), code), kt, kh, fmha_tensor(v_new.data_ptr(), code), vt, vh, slots.data_ptr(),
+        fmha_tensor(k_pages.data_ptr(), E4M3), fmha_tensor(v_pages.data_ptr(), E4M3), k_scale.data_ptr(),
+        v_scale.data_ptr(), N, H_k, D, n_pages, P, _raw_stream(index)))
+
+
+def fmha_rope(q, q_strides, k, k_strides, q_out, q_out_strides, k_out, k_out_strides, B, S, H, H_k, D, rot, positions,
+              inv_freq, magnitude, layout, transpose, stream=None) -> int:
+    """Same arguments, order and status codes as the C function fmha_rope;
+    strides as (batch, token, head) in elements."""
+    return lib().fmha_rope(
+        _tensor(q), fmha_strides(*q_strides), _tensor(k), fmha_strides(*k_strides), _tensor(q_out),
+        fmha_strides(*q_out_strides), _tensor(k_out), fmha_strides(*k_out_strides), int(B), int(S), int(H), int(H_k),
+        int(D), int(rot), _ptr(positions), _ptr(inv_freq), float(magnitude), int(layout), int(transpose),
+        _stream(stream))
+
+
+def rope_frequencies(rot: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     trained: Optional[int] = None, slow: float = 1.0, fast: float = 32.0, device=None):
+    """Rotary frequencies for fmha_rope, and the magnitude that goes with them:
+    (inv_freq float64 [rot / 2], magnitude).
+
+    ``scaling`` for contexts ``factor`` times as long as the model was trained on:
+      "none"      inv_freq[i] = base ** (-2 i / rot)
+      "linear"    all of them divided by factor
+      "ntk"       a larger base, base * factor ** (rot / (rot - 2)): the first
+                  pair turns as before, the last factor times slower
+      "by_parts"  pairs that turn at least ``fast`` times within ``trained``
+                  positions as before, those that turn ``slow`` times at most
+                  factor times slower, a linear blend between; the magnitude
+                  is 0.1 ln(factor) + 1
+    """
+    if rot <= 0 or rot % 2:
+        raise ValueError(f"rot is even and positive, not {rot}")
+    if not (base > 0 and factor >= 1):
+        raise ValueError("base is positive and factor at least 1")
+    i2 = torch.arange(0, rot, 2, dtype=torch.float64)
+    if scaling == "ntk":
+        base = base * factor ** (rot / (rot - 2)) if rot > 2 else base
+    inv_freq, magnitude = base ** (-i2 / rot), 1.0
+    if scaling == "linear":
+        inv_freq = inv_freq / factor
+    elif scaling == "by_parts":
+        if trained is None or not fast > slow:
+            raise ValueError("by_parts needs trained, the positions the model was trained on, and fast above slow")
+        turns = trained * inv_freq / (2 * math.pi)
+        keep = ((turns - slow) / (fast - slow)).clamp(0, 1)
+        inv_freq, magnitude = inv_freq * (keep + (1 - keep) / factor), 0.1 * math.log(factor) + 1
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"scaling is none, linear, ntk or by_parts, not {scaling!r}")
+    return inv_freq.to(device) if device is not None else inv_freq, magnitude
+
+
+def _rope_strides(t: torch.Tensor) -> fmha_strides:
+    s = t.stride()
+    return fmha_strides(s[0], s[1], s[2]) if len(s) == 4 else fmha_strides(0, s[0], s[1])
+
+
+_NO_TENSOR, _NO_STRIDES = fmha_tensor(None, BF16), fmha_strides(0, 0, 0)
+
+
+def _rope(q, k, inv_freq, positions, interleaved, magnitude, q_out, k_out, out_dtype, stream, transpose):
+    index, code = _device_and_code(q)
+    if stream is not None or _current_device() != index:
+        with _on(stream, index):
+            return _rope(q, k, inv_freq, positions, interleaved, magnitude, q_out, k_out, out_dtype, None, transpose)
+    if q.dim() not in (3, 4):
+        raise ValueError("q is [B, S, H, D] or [N, H, D], and k alike")
+    lead, H, D, dt = q.shape[:-2], q.shape[-2], q.shape[-1], q.dtype
+    B, S = lead if len(lead) == 2 else (1, lead[0])
+    H_k = 0
+    if k is not None:
+        if k.dim() != q.dim():
+            raise ValueError("k has as many dimensions as q")
+        H_k = k.shape[-2]
+        if not _fit_strided(index, dt, (*lead, H_k, D), k):
+            _check_strided(index, dt, (*lead, H_k, D), k=k)
+    elif k_out is not None:
+        raise ValueError("k_out comes with k")
+    odt = out_dtype or (q_out.dtype if q_out is not None else dt)
+    if odt not in _TORCH_DTYPE:
+        raise FmhaError(ERR_UNSUPPORTED, f"dtype {odt}: {status_string(ERR_UNSUPPORTED)}")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=odt, device=q.device)
+    if k_out is None and k is not None:
+        k_out = torch.empty(k.shape, dtype=odt, device=q.device)
+    if not (_fit_strided(index, dt, q.shape, q) and _fit_strided(index, odt, q.shape, q_out)
+            and (k is None or _fit_strided(index, odt, k.shape, k_out))
+            and _fit(index, torch.int32, lead, positions) and _fit(index, torch.float64, (inv_freq.shape[0],), inv_freq)):
+        _check_strided(index, dt, q.shape, q=q)
+        _check_strided(index, odt, q.shape, q_out=q_out)
+        if k is not None:
+            _check_strided(index, odt, k.shape, k_out=k_out)
+        _check(index, torch.int32, lead, positions=positions)
+        _check(index, torch.float64, (inv_freq.shape[0],), inv_freq=inv_freq)
+    ocode = _TORCH_DTYPE[odt]
+    kt, kos = (_NO_TENSOR, _NO_TENSOR) if k is None else (fmha_tensor(k.data_ptr(), code), fmha_tensor(k_out.data_ptr(), ocode))
+    ks, ko = (_NO_STRIDES, _NO_STRIDES) if k is None else (_rope_strides(k), _rope_strides(k_out))
+    _raise(lib().fmha_rope(
+        fmha_tensor(q.data_ptr(), code), _rope_strides(q), kt, ks, fmha_tensor(q_out.data_ptr(), ocode),
+        _rope_strides(q_out), kos, ko, B, S, H, H_k, D, 2 * inv_freq.shape[0], _ptr(positions), inv_freq.data_ptr(),
+        magnitude, ROPE_PAIRS if interleaved else ROPE_HALF, transpose, _raw_stream(index)))
+    return q_out, k_out
+
+
+def rope(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tensor, *,
+         positions: Optional[torch.Tensor] = None, interleaved: bool = False, magnitude: float = 1.0,
+         q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, out_dtype=None, stream=None):
+    """Rotary positions of queries and keys (see fmha_rope).
+
+    q [B, S, H, D] or packed [N, H, D], k alike with H_k heads, or None, bf16
+    or f16, of any strides with a contiguous last dimension; inv_freq float64
+    [rot / 2] on the device (see rope_frequencies), rot at most D; positions
+    int32 [B, S] or [N], None: 0, 1, ... in every sequence.  Pairs are elements
+    i and i + rot / 2, or with ``interleaved`` 2 i and 2 i + 1.  Allocates the
+    outputs, of the inputs' type or ``out_dtype`` (e4m3), unless given; in place
+    with q_out=q and k_out=k.  Returns (q_out, k_out)."""
+    return _rope(q, k, inv_freq, positions, interleaved, magnitude, q_out, k_out, out_dtype, stream, 0)
+
+
+def rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], inv_freq: torch.Tensor, *,
+             positions: Optional[torch.Tensor] = None, interleaved: bool = False, magnitude: float = 1.0,
+             q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of rope's inputs from those of its outputs; arguments as rope."""
+    return _rope(dq, dk, inv_freq, positions, interleaved, magnitude, q_out, k_out, None, stream, 1)
 
 
 def fmha_bwd(q, k, v, o, dout, lse, dq, dk, dv, B, H, Sq, Sk, D, scale, mask, causal_type, workspace,

@@ -438,6 +438,140 @@ int fmha_cache_evict(fmha_tensor k_cache, fmha_tensor v_cache, const float *acc,
                      int budget, int recent, int *kept, int *new_seqlen, cudaStream_t stream);
 
 /*
+ * Paged caches.  Keys and values lie in pages of P = page_size tokens (16, 32,
+ * 64 or 128), held as e4m3 codes with one scale per page and kv head:
+ *   k_pages, v_pages   FMHA_E4M3 [n_pages, H_k, P, 128]
+ *   k_scale, v_scale   float [n_pages, H_k]
+ * and a key is k_scale[page, g] * code.  Row e of a block table, int32
+ * [B_table, max_pages], lists the pages of a sequence's tokens in order; the
+ * slot of a token is page * P + its row there.  A step is fmha_page_plan (which
+ * tokens come, where they go), fmha_rope (their positions), fmha_page_write
+ * and fmha_page_fwd.  The pages of the sources have no counterpart but the plan
+ * of one ("decode attention, paged KV, fp8/KV quantisation").
+ *
+ * fmha_page_plan -- block tables and slot maps from request lengths.
+ *
+ * Sequence b, with table row e = batch_idx ? batch_idx[b] : b, has L =
+ * seqlen[b] cached tokens, whose pages are table[e, 0 .. ceil(L / P) - 1], and
+ * n = n_new[b] says what the step does to it:
+ *   n < 0: its last -n tokens are dropped (n = -L: it has ended; n = -3: three
+ *          drafts were not accepted).  The pages that become empty go onto the
+ *          stack of free pages, free_list[0 .. n_free - 1], in the order of
+ *          the sequences and of their pages.
+ *   n >= 0: its n new tokens need ceil((L + n) / P) - ceil(L / P) pages.  After
+ *          all drops, they are taken from the stack's top, the sequences in
+ *          order; a sequence for which what is left does not suffice gets none,
+ *          and so do those after it that need any.
+ * Outputs
+ *   table, free_list   in place; entries behind what is in use stay as they were
+ *   n_free_out         free pages now (n_free itself, or another)
+ *   new_seqlen [B]     L + n, or L where the pages did not suffice (seqlen
+ *                      itself, or another)
+ *   cu_new [B + 1]     first row of each sequence's new tokens in the step's
+ *                      packed tensors, those without pages included
+ *   positions [N]      of row i, new token t of its sequence: L + t; -1 for rows
+ *                      behind the last one
+ *   slots [N]          its slot; -1 without pages and behind the last row
+ * All int32 on the device.  N is the rows that the arrays of the step have,
+ * at least the sum of all n > 0.  n_pages: pages of the cache, and elements of
+ * free_list.  max_pages * P at most 2^30, n_pages * P below 2^31, B at most
+ * 8192 (else FMHA_ERR_UNSUPPORTED).  Outputs are apart from the inputs, but for
+ * the two that may be their own, and from one another.
+ * In device memory, so checked there: 0 <= L <= max_pages * P; L + n at most
+ * that (else the sequence gets no pages); -L <= n; the sum of n > 0 at most N
+ * (rows from N on are dropped, and cu_new ends at N); batch_idx in [0, B_table)
+ * and no two alike; 0 <= n_free, and with the pages given back at most n_pages;
+ * pages in [0, n_pages) (else the slot is -1).  A kernel that meets a violation
+ * clamps, and fmha_device_status then reports FMHA_ERR_INVALID_ARG (not for
+ * two equal batch_idx, whose results are undefined).
+ * No workspace; one launch, asynchronous on `stream`.  Returns FMHA_OK,
+ * FMHA_ERR_INVALID_ARG, FMHA_ERR_UNSUPPORTED or FMHA_ERR_CUDA.  B = 0 and
+ * N = 0 succeed without a launch.
+ */
+int fmha_page_plan(const int *seqlen, const int *n_new, const int *batch_idx, int *table, int *free_list,
+                   const int *n_free, int *n_free_out, int *slots, int *positions, int *cu_new, int *new_seqlen,
+                   int B, int N, int B_table, int max_pages, int n_pages, int page_size, cudaStream_t stream);
+
+/*
+ * fmha_page_write -- new keys and values into pages, at their slots.
+ *
+ * The tokens i with slots[i] in one page form a run.  For each kv head, with a
+ * the largest |x| of the run's keys (values) and e the least exponent in
+ * [-60, 60] with a <= 448 * 2^e:
+ *   s = 2^e                            where the run begins its page (row 0),
+ *   s = max(k_scale[page, g], 2^e)     elsewhere;
+ * where s is larger than the scale before, the rows before the run become
+ * e4m3(code * (scale before / s)); the run's rows are e4m3(x / s), rounded to
+ * nearest even with saturation; k_scale[page, g] = s.  Rows behind the run, and
+ * pages without a run, stay as they were.  slots[i] = -1 (any negative): the
+ * token is not written.  A NaN stays one and does not count in a, an infinity
+ * counts as more than the range of scales holds and is written as 448.
+ *
+ * Layouts: k_new, v_new FMHA_F16 or FMHA_BF16 [N, H_k, 128] with strides, in
+ * elements, of tokens and heads (multiples of 8; pieces of a projection's
+ * rows need no copy); slots int32 [N]; the cache as above.  D must be 128.
+ * Data pointers 16-byte aligned (scales and slots 4-byte).  The cache's arrays
+ * are apart from the others and from one another.
+ * The slots of a page's tokens are consecutive for consecutive i, as
+ * fmha_page_plan gives them, where none is negative in between; such a token's
+ * row keeps its codes.  No slot comes twice.  (Otherwise that page's contents
+ * are undefined.)  A slot at or past n_pages * P is not written, and
+ * fmha_device_status reports FMHA_ERR_INVALID_ARG.
+ * No workspace; one launch.  Returns FMHA_OK, FMHA_ERR_INVALID_ARG,
+ * FMHA_ERR_UNSUPPORTED (dtype, alignment, device) or FMHA_ERR_CUDA.  N = 0
+ * succeeds without a launch.
+ */
+int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_t k_head_stride, fmha_tensor v_new,
+                    int64_t v_token_stride, int64_t v_head_stride, const int *slots, fmha_tensor k_pages,
+                    fmha_tensor v_pages, float *k_scale, float *v_scale, int N, int H_k, int D, int n_pages,
+                    int page_size, cudaStream_t stream);
+
+/* Which elements of a head fmha_rope turns together. */
+enum fmha_rope_layout {
+    FMHA_ROPE_HALF = 0,   /* i and i + rot / 2 */
+    FMHA_ROPE_PAIRS = 1   /* 2 i and 2 i + 1 */
+};
+#define FMHA_ROPE_MAX_DIM 256
+
+/* Strides of a [B, S, heads, D] tensor, in elements; D is contiguous. */
+typedef struct fmha_strides {
+    int64_t batch, token, head;
+} fmha_strides;
+
+/*
+ * fmha_rope -- rotary positions of queries and keys, or the gradient.
+ *
+ * Pair i of the first rot elements of every head of a token at position t is
+ * turned by t * inv_freq[i] and multiplied by `magnitude`:
+ *   y_a = magnitude * (x_a cos - x_b sin),  y_b = magnitude * (x_b cos + x_a sin)
+ * with a, b by `layout`; transpose != 0: by the opposite angle, which makes
+ * the gradient of x from that of y.  The other D - rot elements are copied.
+ * Computed in fp32 from angles that are exact to 2^-24 of a turn at any
+ * position, and rounded once.  Longer contexts are the caller's choice of
+ * inv_freq and magnitude.
+ *
+ * Layouts: q, q_out [B, S, H, D] and k, k_out [B, S, H_k, D] with strides of
+ * their own; H or H_k may be 0 (that tensor is then not looked at).  positions
+ * int32 [B, S], or NULL: the token's index in its sequence; a token with a
+ * negative position is left out (its output rows stay as they were).
+ * inv_freq double [rot / 2], finite, radians a position.  rot even, at most D;
+ * D at most 256; B * S below 2^31.  Inputs FMHA_F16 or FMHA_BF16, outputs of
+ * the same type or FMHA_E4M3 (saturating).  No alignment beyond the element's
+ * is needed; it is fastest where addresses and strides are multiples of 16
+ * bytes, D of 8, and rot of 16 (PAIRS: 8).
+ * An output is its input itself (same address and strides), or apart from all
+ * inputs and the other output; pieces of the same tokens' rows, side by side,
+ * are apart.  No two elements of an output share a place.
+ * No workspace; one launch.  Returns FMHA_OK, FMHA_ERR_INVALID_ARG,
+ * FMHA_ERR_UNSUPPORTED (dtype, device) or FMHA_ERR_CUDA.  B = 0, S = 0 or no
+ * heads succeed without a launch.
+ */
+int fmha_rope(fmha_tensor q, fmha_strides q_strides, fmha_tensor k, fmha_strides k_strides, fmha_tensor q_out,
+              fmha_strides q_out_strides, fmha_tensor k_out, fmha_strides k_out_strides, int B, int S, int H, int H_k,
+              int D, int rot, const int *positions, const double *inv_freq, float magnitude, int layout,
+              int transpose, cudaStream_t stream);
+
+/*
  * fmha_bwd -- backward pass of fmha_fwd: dQ, dK, dV from dO ("CUTLASS
  * Blackwell FMHA 示例完全解析", §FMHA for Blackwell 反向 (Backward): row sums
  * of O * dO, a dK/dV kernel and a dQ kernel, Q and K blocking 128, causal
@@ -489,8 +623,8 @@ const char *fmha_status_string(int status);
  * device: FMHA_OK, FMHA_ERR_TIMEOUT if a kernel gave up a bounded wait
  * (it then skipped its remaining work and released its resources), or
  * FMHA_ERR_INVALID_ARG if fmha_gen_fwd, fmha_tree_fwd, fmha_tree_commit,
- * fmha_cache_weights or fmha_cache_evict met a length, count, cache entry or
- * draft outside its bounds.
+ * fmha_cache_weights, fmha_cache_evict, fmha_page_plan or fmha_page_write met a
+ * length, count, cache entry, draft, page or slot outside its bounds.
  * Synchronises the device.  reset != 0 clears the word.  Returns
  * FMHA_ERR_CUDA if the word cannot be read.
  */

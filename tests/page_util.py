@@ -1,0 +1,113 @@
+"""Plain forms of the paged-cache operators on the CPU, in whole numbers and 64
+bits, for the tests."""
+from __future__ import annotations
+
+import torch
+
+from tests import cache_util as cu
+
+E4M3 = torch.float8_e4m3fn
+VALUES = torch.arange(256, dtype=torch.uint8).view(E4M3).float().double()      # of every code
+
+
+def up(a, b):
+    return -(-a // b)
+
+
+def plan(seqlen, n_new, table, free_list, n_free, page, rows, entry=None):
+    """The plan's outputs from lists; table (list of lists) and free_list are changed."""
+    B, width = len(seqlen), len(table[0])
+    entry = entry or list(range(B))
+    stack = list(free_list[:n_free])
+    new_len, slots, pos, cu_new = list(seqlen), [-1] * rows, [-1] * rows, [0]
+    for b, n in enumerate(n_new):
+        if n < 0:
+            keep = max(0, seqlen[b] + n)
+            stack += [table[entry[b]][i] for i in range(up(keep, page), up(seqlen[b], page))]
+            new_len[b] = keep
+    for i, x in enumerate(stack):                       # where the stack reached, its pages stay written
+        free_list[i] = x
+    stopped = False
+    for b, n in enumerate(n_new):
+        L = seqlen[b]
+        fits = True
+        if n >= 0:
+            fits = L + n <= width * page
+            need = up(L + n, page) - up(L, page) if fits else 0
+            if need > len(stack) or (need and stopped):
+                stopped = fits = False
+                stopped = True
+            elif fits:
+                for i in range(need):
+                    table[entry[b]][up(L, page) + i] = stack.pop()
+                new_len[b] = L + n
+        for t in range(max(n, 0)):
+            i = cu_new[-1] + t
+            if i < rows:
+                pos[i] = L + t
+                slots[i] = table[entry[b]][(L + t) // page] * page + (L + t) % page if fits else -1
+        cu_new.append(min(rows, cu_new[-1] + max(n, 0)))
+    return slots, pos, cu_new, new_len, len(stack)
+
+
+def rope(x, inv_freq, pos, interleaved, magnitude, transpose=False):
+    """Turned x [..., heads, D] in 64 bits, and the bound on what fp32 may be off by."""
+    r = 2 * len(inv_freq)
+    ang = pos.double()[..., None, None] * inv_freq.double()
+    c, s = torch.cos(ang) * magnitude, torch.sin(ang) * magnitude * (-1 if transpose else 1)
+    x = x.double()
+    i = torch.arange(r // 2)
+    a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + r // 2)
+    y, tol = x.clone(), torch.zeros_like(x)
+    y[..., a] = x[..., a] * c - x[..., b] * s
+    y[..., b] = x[..., b] * c + x[..., a] * s
+    # sine and cosine: the angle is off by 2^-25 half turns, 9.4e-8, and they by
+    # 2^-23 more; three fp32 roundings behind them
+    both = (x[..., a].abs() + x[..., b].abs()) * abs(magnitude) * 2.0 ** -21
+    tol[..., a] = tol[..., b] = both
+    return y, tol
+
+
+def exponent(a):
+    """Least e in [-60, 60] with a <= 448 * 2^e."""
+    e = -60
+    while e < 60 and a > 448.0 * 2.0 ** e:
+        e += 1
+    return e
+
+
+def codes(x):
+    """e4m3 codes of 64-bit values that 32 bits hold: nearest even, saturating."""
+    return x.clamp(-448, 448).float().to(E4M3).view(torch.uint8)
+
+
+def write(new, slots, pages, scale):
+    """new [N, H_k, 128] into pages (uint8 codes [n, H_k, P, 128]) and scale, both changed."""
+    P, x = pages.shape[2], new.double()
+    i = 0
+    while i < len(slots):
+        if slots[i] < 0 or slots[i] >= pages.shape[0] * P:
+            i += 1
+            continue
+        n, p, off = 1, slots[i] // P, slots[i] % P
+        while i + n < len(slots) and off + n < P and (slots[i + n] < 0 or slots[i + n] == slots[i] + n):
+            n += 1
+        for g in range(pages.shape[1]):
+            live = torch.tensor(slots[i:i + n]) >= 0
+            run = x[i:i + n, g][live]
+            top = run.abs().nan_to_num(nan=0.0, posinf=float("inf")).max().item()
+            s, old = 2.0 ** exponent(top), scale[p, g].item()
+            if off > 0:
+                if s > old:
+                    pages[p, g, :off] = codes(VALUES[pages[p, g, :off].long()] * (old / s))
+                s = max(s, old)
+            pages[p, g, off:off + n][live] = codes(run / s)
+            scale[p, g] = s
+        i += n
+
+
+def draw_pages(gen, n_pages, H_k, P, lo=-8, hi=-4):
+    """Codes and power-of-two scales of a cache whose values are about one."""
+    c = cu.draw(gen, (n_pages, H_k, P, 128), "e4m3", 64.0)
+    s = torch.exp2(torch.randint(lo, hi, (n_pages, H_k), generator=gen).float())
+    return c, s
