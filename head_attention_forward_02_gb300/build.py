@@ -13,7 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfmha.so")
 SOURCES = ["fmha_api.cu", "fmha_simt.cu", "fmha_sm103.cu", "fmha_splitkv.cu", "fmha_gen.cu", "fmha_bwd.cu",
-           "fmha_tree.cu", "fmha_weights.cu", "fmha_evict.cu", "fmha_rope.cu", "fmha_page.cu"]
+           "fmha_tree.cu", "fmha_weights.cu", "fmha_evict.cu", "fmha_rope.cu", "fmha_page.cu", "fmha_paged.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -23,6 +23,9 @@ int weights_set_wait_limit(unsigned long long ns);
 int weights_set_test_gate(int on);
 int *evict_status_word();                        // fmha_evict.cu: its status word (it has no waits)
 int *page_status_word();                         // fmha_page.cu: likewise
+int *paged_status_word();                        // fmha_paged.cu: its status word, wait limit and test gate
+int paged_set_wait_limit(unsigned long long ns);
+int paged_set_test_gate(int on);
 }
 
 namespace fmha {
@@ -32,7 +35,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 // The first error among the kernels' status words, and the words cleared: one
 // launch and one copy for all (a copy a word and file took 58 us a call).
-constexpr int kWords = 7;
+constexpr int kWords = 8;
 struct StatusWords {
     int *word[kWords];
 };
@@ -170,7 +173,8 @@ int fmha_set_wait_limit_ns(unsigned long long ns) {
     const int c = fmha::bwd_set_wait_limit(ns);
     const int d = fmha::tree_set_wait_limit(ns);
     const int e = fmha::weights_set_wait_limit(ns);
-    return a != FMHA_OK ? a : b != FMHA_OK ? b : c != FMHA_OK ? c : d != FMHA_OK ? d : e;
+    const int f = fmha::paged_set_wait_limit(ns);
+    return a != FMHA_OK ? a : b != FMHA_OK ? b : c != FMHA_OK ? c : d != FMHA_OK ? d : e != FMHA_OK ? e : f;
 }
 
 int fmha_set_test_gate(int on) {
@@ -179,7 +183,8 @@ int fmha_set_test_gate(int on) {
     const int c = fmha::bwd_set_test_gate(on);
     const int d = fmha::tree_set_test_gate(on);
     const int e = fmha::weights_set_test_gate(on);
-    return a != FMHA_OK ? a : b != FMHA_OK ? b : c != FMHA_OK ? c : d != FMHA_OK ? d : e;
+    const int f = fmha::paged_set_test_gate(on);
+    return a != FMHA_OK ? a : b != FMHA_OK ? b : c != FMHA_OK ? c : d != FMHA_OK ? d : e != FMHA_OK ? e : f;
 }
 
 int fmha_device_status(int reset) {
@@ -189,7 +194,8 @@ int fmha_device_status(int reset) {
     // the launch below waits for the default stream alone, not for streams created without blocking on it
     bool ok = cudaDeviceSynchronize() == cudaSuccess;
     const StatusWords w = {sm103_status_word(), gen_status_word(), bwd_status_word(),
-                           tree_status_word(), weights_status_word(), evict_status_word(), page_status_word()};
+                           tree_status_word(), weights_status_word(), evict_status_word(), page_status_word(),
+                           paged_status_word()};
     for (const int *p : w.word) ok = ok && p;
     int v = 0;
     if (ok) {

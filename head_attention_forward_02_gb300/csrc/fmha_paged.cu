@@ -1,0 +1,1179 @@
+// fmha_paged.cu -- attention over a paged K/V cache held in e4m3 with a scale
+// for each page and kv head.
+//
+// Operation: sequence b has L = seqlen[b] cached tokens, its last n among them
+// the call's own (packed rows cu_q[b] .. cu_q[b + 1] - 1 of q); token j lies in
+// row j % P of page p_j = table[e, j / P].  With c_j, d_j the codes of its key
+// and value of kv head g, x_j = scale * k_scale[p_j, g] * q . c_j and, for
+// query t, the keys j <= L - n + t (all without a mask),
+//   O = out_scale * sum_j exp(x_j - LSE) v_scale[p_j, g] d_j,  LSE = ln sum_j exp(x_j).
+//
+// The codes go from the pages to the tensor cores as they are (TMA into
+// swizzled shared memory, kind::f8f6f4), so q and the weights P have to be
+// e4m3 there too.  One e4m3 number holds four bits, which is not enough of
+// either; but as a sum of several the product stays exact, and with the roles
+// swapped, S^T = K Q^T (M = 128 keys) and O^T = V^T P^T (M = 128 dims), each
+// further term costs columns of N, not another pass over K or V:
+//   q  = 2^k (q_0 + q_1 / 16), each 4 bits: all 8 bits of a bf16 row's
+//        elements down to 2^-13 of its largest (2^k: a power of two per row); f16
+//        has a third term, added to the second's columns by an MMA of its own;
+//   P' = p_0 + p_1 / 16, off by 2^-8 of a weight at most, 16 times less than
+//        the rounding that made the codes.
+// A group of 16 query rows is thus 32 columns, [16 first terms | 16 second],
+// and a unit one such group or up to four (prompt chunks), of one kv head.
+//
+// e4m3 ends at 448 and 2^-9, so P' = exp2(y_j - m) with y_j = x_j log2(e) +
+// log2(v_scale) is relative to a reference m per row, and products are
+// accumulated in TMEM only over a group of at most eight key tiles with the
+// same reference: the next group sets its own, from the maximum of its first
+// tile, and the O^T of the one before is added in fp32 registers, from one of
+// two TMEM buffers, under the softmax of the next.  A score that outgrows the
+// reference opens a new group early.  So nothing depends on how far a tile is
+// below the largest: of a group's weight, what e4m3's smallest steps lose is
+// 2^-8 at most (1024 weights of 2^-14 where the largest is 2^4 or more).
+// Row sums are of the unrounded weights, in fp32.
+//
+// Work: the key tiles of all units form one sequence cut evenly over the CTAs,
+// one an SM; units that a cut goes through leave normalised fp32 partials,
+// which a second kernel joins.  Roles: a producer (page ids, TMA, a ring of
+// 128-key tiles), two warps that split q, one MMA issuer, and the softmax
+// warps, a thread a key and, for O^T, a dim.  Their scales are fetched two tiles ahead.
+#include "fmha_cache.cuh"
+
+namespace fmha {
+namespace {
+
+constexpr int kPagedMaxCtas = 152;       // bounds the workspace
+constexpr int kPagedItems = 4;           // work items published ahead
+constexpr int kGroupTiles = 8;           // key tiles with one reference
+constexpr float kBias = 4.f;             // log2 of a group's largest P' where its reference is set
+constexpr float kGrown = 8.75f;          // and how far it may grow: e4m3 ends at 2^8.8
+constexpr int kStagesPaged = 6;
+constexpr int kPagedBars = 5120;         // barrier block
+constexpr float kNone = 1e30f;           // -m of a row that has seen no key in its group
+constexpr float kLeastScale = 0x1p-60f, kMostScale = 0x1p60f;   // of values
+
+template <bool BF_, int NG_>
+struct PagedCfg {
+    static constexpr bool BF = BF_;
+    static constexpr int NG = NG_;                            // groups of 16 query rows a unit holds
+    static constexpr int R = 16 * NG;                         // its rows
+    static constexpr int WG = NG == 1 ? 1 : 2;                // softmax warpgroups; one takes groups w, w + WG, ...
+    static constexpr int GPW = NG / WG;
+    static constexpr int SW = 4 * WG;                         // softmax warps
+    static constexpr int QW = SW, PROD = SW + 2, MMA = SW + 3;   // two q warps, producer, MMA issuer
+    static constexpr int THREADS = 32 * (SW + 4);
+    static constexpr int COLS = 32 * NG;                      // of S^T and O^T
+    static constexpr int O_COL = 2 * COLS;                    // TMEM: two S^T, then two O^T
+    static constexpr int TMEM_COLS = 4 * COLS;
+    static constexpr int P_ROW = COLS;                        // bytes of a key's P^T row
+    static constexpr int P_BYTES = kRows * P_ROW;
+    static constexpr uint64_t P_SWZ = NG == 1 ? 6 : 2;        // 32-byte or 128-byte swizzle
+    static constexpr int Q_BYTES = (BF ? 32 : 48) * NG * 128; // first and second terms, then f16's third
+    static constexpr int STAGE = 2 * kPanelBytes;             // K and V of 128 keys
+    static constexpr int OFF_P = 2 * Q_BYTES;
+    static constexpr int OFF_KV = OFF_P + 2 * P_BYTES;
+    static constexpr int NS_FIT = (226 * 1024 - kPagedBars - OFF_KV) / STAGE;
+    static constexpr int NS = NS_FIT < kStagesPaged ? NS_FIT : kStagesPaged;
+    static constexpr int OFF_BARS = OFF_KV + NS * STAGE;
+    static constexpr int SMEM_BYTES = OFF_BARS + kPagedBars + 1024; // 1 KB alignment
+    static_assert(SMEM_BYTES <= 227 * 1024 && OFF_KV % 1024 == 0 && OFF_P % 1024 == 0, "shared memory");
+};
+
+struct PagedMeta {                       // whose partial a workspace slot holds
+    int row0, h0, rows;                  // first q row and head of its unit; rows (0: no partial here)
+    int last;                            // the unit ends with this partial
+};
+
+struct PagedParams {
+    const uint8_t *q;                    // [N, H, 128]
+    void *o;
+    float *lse;                          // [N, H] or NULL
+    const float *k_scale, *v_scale;      // [n_pages, H_k]
+    const int *table, *seqlen, *batch_idx, *cu_q;
+    float *part_o, *part_lse;            // [2 * ncta][R][D], [2 * ncta][R]
+    PagedMeta *meta;                     // [2 * ncta]
+    int B, N, max_q, H, H_k, G, B_table, width, n_pages, shift;
+    int tau, tau_log;                    // tokens of a unit, a power of two
+    int subs;                            // units of a token (groups of more than R heads)
+    int causal, edge, ncta;
+    float c, out_scale;                  // c: scale * log2(e)
+};
+
+struct PagedItem {
+    int g, L, base, entry;               // base: token t of the sequence sees keys up to base + t
+    int row0, tok0, h0, rows;            // first q row, token and head; rows (0: no more items)
+    int t0, t1, nt;                      // this CTA's tiles [t0, t1) of the unit's nt
+};
+
+struct PagedBars {
+    uint64_t q_full[2], q_empty[2], drain;
+    uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+    uint64_t kv_full[kStagesPaged], kv_empty[kStagesPaged];
+    uint64_t item_full[kPagedItems], item_empty[kPagedItems];
+    PagedItem item[kPagedItems];
+    uint32_t tmem_base;
+    int abort;
+    int fresh[2];                        // of a P^T buffer's tile: it begins a group; and the group's O^T buffer
+    alignas(16) float qscale[2][64];     // of a q slot's rows: 2^k,
+    alignas(16) int lim[2][64], at[2][64];   // the last key they see, and q row * H + head (-1: none)
+    alignas(16) float nm[64], w[64];     // of the group: -m, 2^(m - M)
+    float top[64];                       // M, the largest m so far
+    alignas(16) float am[64], beta[64];  // factors for what was summed before, for the group before
+    float red[8][32];                    // by warp: maxima or sums of its rows
+    float inv[64];                       // by row: out_scale / sum
+};
+static_assert(sizeof(PagedBars) <= kPagedBars, "barrier block");
+
+// ---------------------------------------------------------------------------
+// PTX wrappers that this kernel adds
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint64_t desc_sw(uint32_t saddr, uint32_t lbo, uint32_t sbo, uint64_t swz) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (swz << 61);
+}
+// e4m3 operands, fp32 accumulator, M = 128; A and B K-major or MN-major
+__device__ __forceinline__ uint32_t paged_idesc(int n, bool mn) {
+    return (1u << 4) | ((mn ? 3u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+}
+__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float redux_max(float x) {
+    float y;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Both terms' columns of NR rows of a group: hi[NR], mid[NR]
+template <int NR>
+__device__ __forceinline__ void ld_terms(uint32_t taddr, uint32_t (&r)[2 * NR]) {
+    if constexpr (NR == 16) {
+        tmem_ld32(taddr, r);
+        tmem_wait_ld(r);
+    } else if constexpr (NR == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr));
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                     : "r"(taddr + 16));
+        tmem_wait_ld16(r);
+    } else {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(taddr));
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr + 16));
+        asm volatile("tcgen05.wait::ld.sync.aligned;"
+                     : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                     :
+                     : "memory");
+    }
+}
+
+// Named barrier 1 over the softmax threads, with a vote.
+template <int N>
+__device__ __forceinline__ void soft_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ bool soft_any(bool v) {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, 1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r)
+                 : "r"((uint32_t)v), "n"(N)
+                 : "memory");
+    return r != 0;
+}
+
+// Two weights as two e4m3 terms each (first weight in the low byte): p = hi +
+// mid / 16, by way of f16, whose 11 bits hold a rest exactly.
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &mid) {
+    const uint32_t h = pack2<false>(a, b);
+    const __half2 p = *reinterpret_cast<const __half2 *>(&h);
+    const __nv_fp8x2_storage_t f = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(p), __NV_SATFINITE, __NV_E4M3);
+    const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2(f, __NV_E4M3));
+    const __half2 rest = __hmul2(__hsub2(p, back), __float2half2_rn(16.f));
+    hi = f;
+    mid = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
+}
+
+// ---------------------------------------------------------------------------
+// Work: of every sequence b, kv head g: blocks v of tau tokens, each in `subs`
+// units.  Block v's tiles reach to the last key that one of its tokens sees.
+// A unit is `edge` tiles of nothing, for the work at its ends, and then its own.
+// ---------------------------------------------------------------------------
+
+struct PagedSeq {
+    int L, n, row0, entry;
+    int base, nv, full, all;             // blocks; the first `full` end within L, the others have `all` tiles
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedParams &p, int b, bool report) {
+    PagedSeq s;
+    s.L = clamped(p.seqlen[b], 0, p.width << p.shift, report);
+    s.row0 = p.cu_q ? clamped(p.cu_q[b], 0, p.N, report) : b;
+    s.n = p.cu_q ? clamped(clamped(p.cu_q[b + 1], s.row0, p.N, report) - s.row0, 0, p.max_q, report) : 1;
+    s.entry = cache_entry(p.batch_idx, b, p.B_table, report);
+    s.base = s.L - s.n;
+    s.nv = (s.n + p.tau - 1) >> p.tau_log;
+    s.full = p.causal ? imin(s.n, s.L) >> p.tau_log : 0;
+    s.all = imax(1, (s.L + kRows - 1) / kRows);
+    return s;
+}
+__device__ __forceinline__ int paged_tiles(const PagedParams &p, const PagedSeq &s, int v) {
+    return v < s.full ? (imax(s.base, 0) + ((v + 1) << p.tau_log) + kRows - 1) / kRows : s.all;
+}
+// sum over k = 0 .. x of floor(k / 2^s), x >= -1
+__device__ __forceinline__ int64_t floor_sum(int64_t x, int s) {
+    const int64_t q = (x + 1) >> s, r = (x + 1) - (q << s);
+    return ((q * (q - 1) / 2) << s) + q * r;
+}
+// tiles and edges of a head's blocks before block v
+__device__ __forceinline__ int64_t paged_before(const PagedParams &p, const PagedSeq &s, int v) {
+    const int f = imin(v, s.full), sh = 7 - p.tau_log;
+    const int64_t d = (int64_t)(imax(s.base, 0) - 1) >> p.tau_log;     // tiles of block i: floor((i + 1 + d) / 2^sh) + 1
+    const int64_t tiles = floor_sum(d + f, sh) - floor_sum(d, sh) + f + (int64_t)(v - f) * s.all;
+    return (tiles + (int64_t)v * p.edge) * p.subs;
+}
+
+struct PagedCursor {
+    PagedSeq s;
+    int64_t off, G0, G1;                 // off: where the unit at hand begins; this CTA's range
+    int b, g, v, sub;
+};
+
+// One warp: this CTA's range and its first unit (the same in every lane).
+__device__ void paged_schedule(const PagedParams &p, PagedCursor &cur, int lane) {
+    auto size = [&](int b) {
+        const PagedSeq s = paged_seq(p, b, false);
+        return p.H_k * paged_before(p, s, s.nv);
+    };
+    const int64_t n0 = lane < p.B ? size(lane) : 0;          // kept: most batches are this small
+    int64_t T = n0;
+    for (int b = lane + 32; b < p.B; b += 32) T += size(b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) T += __shfl_xor_sync(0xffffffffu, T, o);
+    const int64_t per = (T + gridDim.x - 1) / gridDim.x;
+    cur.G0 = min((int64_t)blockIdx.x * per, T);
+    cur.G1 = min(cur.G0 + per, T);
+    cur.b = p.B;
+    cur.off = T;
+    cur.g = cur.v = cur.sub = 0;
+    if (blockIdx.x == gridDim.x - 1)     // reports values outside their bounds, once a call
+        for (int b = lane; b < p.B; b += 32) paged_seq(p, b, true);
+    int64_t base = 0;
+    for (int bb = 0; bb < p.B && cur.G0 < cur.G1; bb += 32) {
+        const int b = bb + lane;
+        const int64_t n = bb == 0 ? n0 : b < p.B ? size(b) : 0;
+        int64_t incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, n > 0 && base + incl > cur.G0);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            cur.b = bb + l;
+            cur.off = __shfl_sync(0xffffffffu, base + incl - n, l);
+            cur.s = paged_seq(p, cur.b, false);
+            const int64_t head = paged_before(p, cur.s, cur.s.nv);
+            int64_t x = cur.G0 - cur.off;
+            cur.g = (int)(x / head);
+            x -= cur.g * head;
+            int lo = 0, hi = cur.s.nv;                        // the block that x lies in
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (paged_before(p, cur.s, mid) <= x) lo = mid;
+                else hi = mid;
+            }
+            cur.v = lo;
+            const int64_t at = paged_before(p, cur.s, lo);
+            const int unit = paged_tiles(p, cur.s, lo) + p.edge;
+            cur.sub = (int)((x - at) / unit);
+            cur.off += cur.g * head + at + (int64_t)cur.sub * unit;
+            return;
+        }
+        base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+__device__ bool paged_next(const PagedParams &p, PagedCursor &cur, PagedItem &it) {
+    it.rows = 0;
+    if (cur.b >= p.B || cur.off >= cur.G1) return false;
+    while (cur.s.nv == 0 || cur.g == p.H_k) {                // the next sequence that has tokens
+        if (++cur.b >= p.B) return false;
+        cur.g = cur.v = cur.sub = 0;
+        cur.s = paged_seq(p, cur.b, false);
+    }
+    const int nt = paged_tiles(p, cur.s, cur.v);
+    it.t0 = imax(0, (int)(max(cur.G0, cur.off) - cur.off) - p.edge);
+    it.t1 = (int)(min(cur.G1, cur.off + p.edge + nt) - cur.off) - p.edge;
+    if (it.t1 <= 0) return false;        // the range ends before the unit's first tile
+    it.nt = nt;
+    it.g = cur.g;
+    it.L = cur.s.L;
+    it.base = p.causal ? cur.s.base : cur.s.L;
+    it.entry = cur.s.entry;
+    it.tok0 = cur.v << p.tau_log;
+    it.row0 = cur.s.row0 + it.tok0;
+    it.h0 = cur.g * p.G;
+    if (p.subs == 1) {
+        it.rows = imin(p.tau, cur.s.n - it.tok0) * p.G;
+    } else {                             // rows are heads of one token
+        const int R = (p.G + p.subs - 1) / p.subs;
+        it.h0 += cur.sub * R;
+        it.rows = imin(R, p.G - cur.sub * R);
+    }
+    cur.off += p.edge + nt;
+    if (++cur.sub == p.subs) {
+        cur.sub = 0;
+        if (++cur.v == cur.s.nv) {
+            cur.v = 0;
+            ++cur.g;
+        }
+    }
+    return true;
+}
+
+// ---------------------------------------------------------------------------
+// Roles
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ bool paged_take(PagedBars *bars, uint32_t i, PagedItem &it, volatile int *abort_flag, int lane) {
+    const uint32_t st = i % kPagedItems;
+    if (!warp_wait(smem_u32(&bars->item_full[st]), (i / kPagedItems) & 1, abort_flag)) return false;
+    it = bars->item[st];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[st]));
+    return it.rows > 0;
+}
+
+// Page of a sequence's token, or -1 (no such entry, or a page outside the cache).
+__device__ __forceinline__ int page_id(const PagedParams &p, int entry, int i, bool report) {
+    const int id = entry >= 0 ? p.table[(int64_t)entry * p.width + i] : -1;
+    if (id >= 0 && id < p.n_pages) return id;
+    if (report && entry >= 0) atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
+    return -1;
+}
+
+// The producer warp: publishes items and loads their K and V tiles, a lane a
+// page.  Ids are fetched a tile ahead.
+template <class C>
+__device__ void paged_producer(const PagedParams &p, PagedCursor &cur, int gate, const CUtensorMap *tmK,
+                               const CUtensorMap *tmV, uint8_t *smem, PagedBars *bars, int lane) {
+    volatile int *abort_flag = &bars->abort;
+    bool ok = true;
+    if (gate) ok = __all_sync(0xffffffffu, lane > 0 || test_gate_open(abort_flag));
+    uint32_t fill = 0, qn = 0;
+    const int P = 1 << p.shift, per = kRows >> p.shift;       // pages of a tile
+    auto publish = [&](uint32_t i, const PagedItem &it) -> bool {
+        const uint32_t st = i % kPagedItems;
+        if (i >= kPagedItems && !warp_wait(smem_u32(&bars->item_empty[st]), (i / kPagedItems - 1) & 1, abort_flag)) return false;
+        if (lane == 0) {
+            bars->item[st] = it;
+            mbar_arrive(smem_u32(&bars->item_full[st]));
+        }
+        __syncwarp();
+        return true;
+    };
+    PagedItem it, next;
+    if (ok) {
+        paged_next(p, cur, it);
+        ok = publish(0, it);
+    }
+    while (ok && it.rows > 0) {
+        ++qn;
+        const int pages = (it.L + P - 1) >> p.shift;
+        auto id_of = [&](int t) {
+            const int i = t * per + lane;
+            return lane < per && i < pages && t < it.t1 ? page_id(p, it.entry, i, true) : -1;
+        };
+        int id = id_of(it.t0);
+        for (int t = it.t0; t < it.t1; ++t) {
+            const int ahead = id_of(t + 1);
+            const uint32_t st = fill % C::NS;
+            if (fill >= C::NS && !warp_wait(smem_u32(&bars->kv_empty[st]), (fill / C::NS - 1) & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            const int here = imax(0, imin(per, pages - t * per));
+            const uint32_t fb = smem_u32(&bars->kv_full[st]);
+            if (lane == 0) mbar_expect_tx(fb, 2 * here * (P << 7));
+            __syncwarp();
+            if (lane < here) {
+                const uint32_t dst = smem_u32(smem + C::OFF_KV + st * C::STAGE) + lane * (P << 7);
+                // a page outside the cache: a coordinate outside it, which reads zeros
+                const int head = id >= 0 ? id * p.H_k + it.g : p.n_pages * p.H_k;
+                tma_load_3d(dst, tmK, fb, 0, 0, head);
+                tma_load_3d(dst + kPanelBytes, tmV, fb, 0, 0, head);
+            }
+            ++fill;
+            id = ahead;
+            if (t == it.t0) {            // the next item is worked out behind the first tile's loads
+                paged_next(p, cur, next);
+                ok = publish(qn, next);
+                if (!ok) break;
+            }
+        }
+        it = next;
+    }
+    // the last release of every stage must arrive before exit; when the CTA
+    // gave up, only the copies already issued
+    for (uint32_t f = fill > C::NS ? fill - C::NS : 0; f < fill; ++f) {
+        if (ok) ok = warp_wait(smem_u32(&bars->kv_empty[f % C::NS]), (f / C::NS) & 1, abort_flag);
+        if (!ok) mbar_wait_drain(smem_u32(&bars->kv_full[f % C::NS]), (f / C::NS) & 1);
+    }
+    for (uint32_t i = qn > 2 ? qn - 2 : 0; ok && i < qn; ++i)
+        ok = warp_wait(smem_u32(&bars->q_empty[i & 1]), (i >> 1) & 1, abort_flag);
+}
+
+// Two warps: an item's rows of q as e4m3 terms in shared memory, and what the
+// softmax needs to know of each row.
+template <class C>
+__device__ void paged_queries(const PagedParams &p, uint8_t *smem, PagedBars *bars, int half, int lane) {
+    volatile int *abort_flag = &bars->abort;
+    PagedItem it;
+    for (uint32_t i = 0; paged_take(bars, i, it, abort_flag, lane); ++i) {
+        const int slot = i & 1;
+        if (i >= 2 && !warp_wait(smem_u32(&bars->q_empty[slot]), ((i >> 1) - 1) & 1, abort_flag)) break;
+        uint8_t *qs = smem + slot * C::Q_BYTES;
+        const int rows = (it.rows + 15) & ~15;
+        for (int r0 = half * 8; r0 < rows; r0 += 16) {
+            uint2 v[8];
+            int at[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = r0 + k, t = p.subs == 1 ? r / p.G : 0;
+                at[k] = r < it.rows ? (it.row0 + t) * p.H + it.h0 + r - t * p.G : -1;
+                v[k] = at[k] >= 0 ? *reinterpret_cast<const uint2 *>(p.q + ((int64_t)at[k] * kD + lane * 4) * 2) : make_uint2(0u, 0u);
+                if (lane == k) {
+                    bars->at[slot][r] = at[k];
+                    bars->lim[slot][r] = it.base + it.tok0 + t;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float x[4];
+                const uint32_t w[2] = {v[k].x, v[k].y};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if constexpr (C::BF) {
+                        x[2 * j] = __uint_as_float(w[j] << 16);
+                        x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                    } else {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+                        x[2 * j] = f.x;
+                        x[2 * j + 1] = f.y;
+                    }
+                }
+                uint32_t top = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+                top = __reduce_max_sync(0xffffffffu, top);
+                // largest element to [2^7, 2^8); a row with an infinity or a NaN is one of NaN
+                const int e = max((int)(top >> 23) - 127, -100);
+                const float up = top < 0x7f800000u ? __uint_as_float((uint32_t)(127 + 7 - e) << 23) : __uint_as_float(0x7fc00000u);
+                float hi[4], y[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = x[j] * up;
+                const int r = r0 + k, row = 32 * (r >> 4) + (r & 15);
+                // 16-byte chunk lane / 4 of a 128-byte row, swizzled
+                auto put = [&](int row_, uint32_t c) {
+                    *reinterpret_cast<uint32_t *>(qs + row_ * 128 + ((((lane >> 2) ^ (row_ & 7)) << 4) | ((lane & 3) << 2))) = c;
+                };
+                auto term = [&](uint32_t c) {                // its values, taken off, and the rest times 16
+                    const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3)));
+                    const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3)));
+                    hi[0] = a.x, hi[1] = a.y, hi[2] = b.x, hi[3] = b.y;
+                };
+                const uint32_t c0 = pack4_e4m3(y[0], y[1], y[2], y[3]);
+                put(row, c0);
+                term(c0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) y[j] = (y[j] - hi[j]) * 16.f;
+                const uint32_t c1 = pack4_e4m3(y[0], y[1], y[2], y[3]);
+                put(row + 16, c1);
+                if constexpr (!C::BF) {
+                    term(c1);
+                    // behind the first two terms' rows; in the units of the second
+                    const uint32_t c2 = pack4_e4m3(y[0] - hi[0], y[1] - hi[1], y[2] - hi[2], y[3] - hi[3]);
+                    put(32 * C::NG + r, c2);
+                }
+                if (lane == 0) bars->qscale[slot][r] = __uint_as_float((uint32_t)(127 + e - 7) << 23);
+            }
+        }
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[slot]));
+    }
+}
+
+// MMA issuer (one warp, one elected lane).  S^T and P^T are double-buffered: S^T
+// of tile j + 1 is issued before the P V of tile j, so the softmax of one runs
+// under the MMAs of the other.
+template <class C>
+__device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int lane) {
+    volatile int *abort_flag = &bars->abort;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
+    const uint64_t q0 = desc_sw(smem_u32(smem), 16, 1024, 2);
+    const uint64_t p0 = desc_sw(smem_u32(smem + C::OFF_P), C::P_BYTES, 8 * C::P_ROW, C::P_SWZ);
+    const uint64_t k0 = desc_sw(smem_u32(smem + C::OFF_KV), 16, 1024, 2);
+    const uint64_t v0 = desc_sw(smem_u32(smem + C::OFF_KV + kPanelBytes), kPanelBytes, 1024, 2);   // MN-major
+    uint32_t j = 0;                      // tiles so far
+    bool ok = true;
+    PagedItem it;
+    int ng_before = 1;                   // of the tile before
+    auto issue_pv = [&](uint32_t c, int ng) -> bool {
+        const uint32_t b = c & 1, st = c % C::NS;
+        if (!warp_wait(smem_u32(&bars->p_full[b]), (c >> 1) & 1, abort_flag)) return false;
+        tc_fence_after();
+        const int f = *reinterpret_cast<volatile int *>(&bars->fresh[b]);
+        const uint32_t idesc = paged_idesc(32 * ng, true);
+        const uint64_t v = v0 + ((st * C::STAGE) >> 4), pt = p0 + ((b * C::P_BYTES) >> 4);
+        const uint32_t o_tm = tmem + C::O_COL + (f >> 1) * C::COLS;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)   // 32 keys
+            mma_ss<true>(o_tm, v + ((kk * 32 * 128) >> 4), pt + ((kk * 32 * C::P_ROW) >> 4), idesc, kk > 0 || !(f & 1) ? 1u : 0u);
+        tc_commit(smem_u32(&bars->pv_done[b]));
+        tc_commit(smem_u32(&bars->kv_empty[st]));
+        return true;
+    };
+    for (uint32_t i = 0; ok && paged_take(bars, i, it, abort_flag, lane); ++i) {
+        const int slot = i & 1, ng = (it.rows + 15) >> 4;
+        if (!warp_wait(smem_u32(&bars->q_full[slot]), (i >> 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+        }
+        const uint32_t idesc = paged_idesc(32 * ng, false), idesc16 = paged_idesc(16, false);
+        const uint64_t q = q0 + ((slot * C::Q_BYTES) >> 4);
+        for (int t = it.t0; t < it.t1; ++t) {
+            const uint32_t b = j & 1, st = j % C::NS;
+            if (!warp_wait(smem_u32(&bars->kv_full[st]), (j / C::NS) & 1, abort_flag) ||
+                (j >= 2 && !warp_wait(smem_u32(&bars->s_free[b]), ((j >> 1) - 1) & 1, abort_flag))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint64_t k = k0 + ((st * C::STAGE) >> 4);
+            const uint32_t s_tm = tmem + b * C::COLS;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)   // 32 dims: 32 bytes of a row
+                mma_ss<true>(s_tm, k + ((kk * 32) >> 4), q + ((kk * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
+            if constexpr (!C::BF) {
+                for (int g = 0; g < ng; ++g)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ss<true>(s_tm + 32 * g + 16, k + ((kk * 32) >> 4),
+                                     q + (((32 * C::NG + 16 * g) * 128 + kk * 32) >> 4), idesc16, 1u);
+            }
+            tc_commit(smem_u32(&bars->s_full[b]));
+            if (t + 1 >= it.t1) tc_commit(smem_u32(&bars->q_empty[slot]));
+            if (t > it.t0 && !issue_pv(j - 1, ng_before)) {
+                ok = false;
+                break;
+            }
+            ng_before = ng;
+            ++j;
+        }
+        // the item's last P V: its epilogue does not wait for the next item's loads
+        if (ok) ok = issue_pv(j - 1, ng);
+    }
+    // no tensor-core operation may be in flight when TMEM is released
+    tc_commit(smem_u32(&bars->drain));
+    mbar_wait_drain(smem_u32(&bars->drain), 0);
+}
+
+// Softmax and epilogue.  Thread r of a warpgroup is key r of every tile (TMEM
+// lane of S^T), and dim r of O^T.
+template <class C, int NR>
+__device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *bars, uint32_t tmem, int warp, int lane) {
+    constexpr int ST = 32 * C::SW, GPW = C::GPW;
+    volatile int *abort_flag = &bars->abort;
+    const int wg = warp >> 2, r = (warp & 3) * 32 + lane, tid = warp * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint64_t sixteenth = pack_f2(0.0625f, 0.0625f);
+    uint32_t j = 0, par = 0;             // tiles, groups so far
+    int parts = 0;                       // bit s: slot s of this CTA holds a partial
+    PagedItem it;
+    for (uint32_t i = 0;; ++i) {
+        // a false return is either the end or an abort: all warps leave together
+        const bool more = paged_take(bars, i, it, abort_flag, lane);
+        if (soft_any<ST>(!more)) break;
+        const int slot = i & 1, ng = (it.rows + 15) >> 4;
+        const bool qok = warp_wait(smem_u32(&bars->q_full[slot]), (i >> 1) & 1, abort_flag);
+        uint64_t l[GPW][NR / 2];         // this key's part of the row sums, relative to M
+        float o[GPW][NR];                // dim r of the rows, relative to M
+#pragma unroll
+        for (int x = 0; x < GPW; ++x)
+#pragma unroll
+            for (int k = 0; k < NR; ++k) {
+                l[x][k / 2] = 0;
+                o[x][k] = 0.f;
+            }
+        if (tid < C::R) bars->top[tid] = -INFINITY;
+        // ids two tiles ahead, scales one
+        const int pages = (it.L + (1 << p.shift) - 1) >> p.shift;
+        auto id_of = [&](int t) {
+            const int key = t * kRows + r;
+            return t < it.t1 && (key >> p.shift) < pages ? page_id(p, it.entry, key >> p.shift, false) : -1;
+        };
+        auto scale_of = [&](const float *s, int id) { return id >= 0 ? s[(int64_t)id * p.H_k + it.g] : 1.f; };
+        const int id0 = id_of(it.t0);
+        int id1 = id_of(it.t0 + 1);
+        float sk = scale_of(p.k_scale, id0), sv = scale_of(p.v_scale, id0);
+        int since = kGroupTiles;         // tiles of the group so far
+        bool ok = qok, first = true;
+        for (int t = it.t0; t < it.t1; ++t, ++j) {
+            const float sk1 = scale_of(p.k_scale, id1), sv1 = scale_of(p.v_scale, id1);
+            id1 = id_of(t + 2);
+            const uint32_t b = j & 1;
+            const int key = t * kRows + r, nk = it.L - t * kRows;
+            ok = warp_wait(smem_u32(&bars->s_full[b]), (j >> 1) & 1, abort_flag) && ok;
+            if (nk < kRows && wg == 0) {
+                // rows past the keys (of an earlier tile, or of nothing): V is
+                // zeroed so that P = 0 contributes 0
+                const uint32_t st = j % C::NS;
+                ok = warp_wait(smem_u32(&bars->kv_full[st]), (j / C::NS) & 1, abort_flag) && ok;
+                if (ok && r >= nk) {
+                    proxy_fence();
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + C::OFF_KV + st * C::STAGE + kPanelBytes + r * 128);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                __syncwarp();
+            }
+            tc_fence_after();
+            const float svc = fminf(fmaxf(sv, kLeastScale), kMostScale);
+            const float a = p.c * sk, lsv = log2f(svc);
+            const uint64_t a2 = pack_f2(a, a), lsv2 = pack_f2(lsv, lsv);
+            const bool masked = nk < kRows || t * kRows + kRows - 1 > it.base + it.tok0;
+            uint64_t y[GPW][NR / 2];     // scores in log2 units, with the value's scale
+#pragma unroll
+            for (int x = 0; x < GPW; ++x) {
+                const int grp = wg + C::WG * x;
+                if (grp >= ng) continue;
+                uint32_t s[2 * NR];
+                ld_terms<NR>(lane_base + b * C::COLS + 32 * grp, s);
+                const float4 *g4 = reinterpret_cast<const float4 *>(&bars->qscale[slot][16 * grp]);
+#pragma unroll
+                for (int k = 0; k < NR; k += 4) {
+                    const float4 gg = g4[k / 4];
+                    const uint64_t t0 = fma_f2(pack_f2(__uint_as_float(s[NR + k]), __uint_as_float(s[NR + k + 1])), sixteenth,
+                                               pack_f2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
+                    const uint64_t t1 = fma_f2(pack_f2(__uint_as_float(s[NR + k + 2]), __uint_as_float(s[NR + k + 3])), sixteenth,
+                                               pack_f2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])));
+                    y[x][k / 2] = fma_f2(t0, mul_f2(pack_f2(gg.x, gg.y), a2), lsv2);
+                    y[x][k / 2 + 1] = fma_f2(t1, mul_f2(pack_f2(gg.z, gg.w), a2), lsv2);
+                }
+                if (masked) {
+                    const int4 *lim = reinterpret_cast<const int4 *>(&bars->lim[slot][16 * grp]);
+#pragma unroll
+                    for (int k = 0; k < NR; k += 4) {
+                        const int4 m = lim[k / 4];
+                        float u, v;
+                        unpack_f2(y[x][k / 2], u, v);
+                        y[x][k / 2] = pack_f2(r < nk && key <= m.x ? u : -INFINITY, r < nk && key <= m.y ? v : -INFINITY);
+                        unpack_f2(y[x][k / 2 + 1], u, v);
+                        y[x][k / 2 + 1] = pack_f2(r < nk && key <= m.z ? u : -INFINITY, r < nk && key <= m.w ? v : -INFINITY);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[b]));
+            // does a score outgrow the group's reference?
+            bool fresh = since == kGroupTiles, out = false;
+            if (!fresh) {
+#pragma unroll
+                for (int x = 0; x < GPW; ++x) {
+                    const int grp = wg + C::WG * x;
+                    if (grp >= ng) continue;
+                    float top = -INFINITY;
+                    const float4 *n4 = reinterpret_cast<const float4 *>(&bars->nm[16 * grp]);
+#pragma unroll
+                    for (int k = 0; k < NR; k += 4) {
+                        const float4 nm = n4[k / 4];
+                        float u, v;
+                        unpack_f2(add_f2(y[x][k / 2], pack_f2(nm.x, nm.y)), u, v);
+                        top = max3(top, u, v);
+                        unpack_f2(add_f2(y[x][k / 2 + 1], pack_f2(nm.z, nm.w)), u, v);
+                        top = max3(top, u, v);
+                    }
+                    out |= top > kGrown;
+                }
+            }
+            if (soft_any<ST>(out || !ok)) {
+                if (soft_any<ST>(!ok)) {
+                    ok = false;
+                    break;
+                }
+                fresh = true;
+            }
+            if (fresh) {
+                // the group's reference: the tile's maximum of every row
+#pragma unroll
+                for (int x = 0; x < GPW; ++x) {
+                    const int grp = wg + C::WG * x;
+                    if (grp >= ng) continue;
+#pragma unroll
+                    for (int k = 0; k < NR; k += 2) {
+                        float u, v;
+                        unpack_f2(y[x][k / 2], u, v);
+                        u = redux_max(u);
+                        v = redux_max(v);
+                        if (lane == 0) {
+                            bars->red[warp][16 * x + k] = u;
+                            bars->red[warp][16 * x + k + 1] = v;
+                        }
+                    }
+                }
+                soft_sync<ST>();
+                if (tid < 16 * ng && (tid & 15) < NR) {
+                    const int grp = tid >> 4, w0 = 4 * (grp % C::WG), at = 16 * (grp / C::WG) + (tid & 15);
+                    const float top = fmaxf(fmaxf(bars->red[w0][at], bars->red[w0 + 1][at]),
+                                            fmaxf(bars->red[w0 + 2][at], bars->red[w0 + 3][at]));
+                    const float m = top - kBias, before = first ? -INFINITY : -bars->nm[tid], M = bars->top[tid];
+                    const float Mn = fmaxf(M, m);
+                    // without a key every factor is 0, and the next key is above the reference
+                    auto factor = [&](float x) { return x < -0.5f * kNone ? 0.f : ex2(x - Mn); };
+                    bars->am[tid] = factor(M);
+                    bars->beta[tid] = factor(before);
+                    bars->w[tid] = factor(m);
+                    bars->top[tid] = Mn;
+                    bars->nm[tid] = m == -INFINITY ? kNone : -m;
+                }
+                soft_sync<ST>();
+#pragma unroll
+                for (int x = 0; x < GPW; ++x) {
+                    const int grp = wg + C::WG * x;
+                    if (grp >= ng) continue;
+#pragma unroll
+                    for (int k = 0; k < NR; k += 2)
+                        l[x][k / 2] = mul_f2(l[x][k / 2], pack_f2(bars->am[16 * grp + k], bars->am[16 * grp + k + 1]));
+                }
+                ++par;
+                since = 0;
+            }
+            ++since;
+            // weights, their sums, and both terms into P^T
+            const float isv = 1.f / svc;
+            const uint64_t isv2 = pack_f2(isv, isv);
+            uint8_t *prow = smem + C::OFF_P + b * C::P_BYTES + r * C::P_ROW;
+            const uint32_t swz = C::NG == 1 ? (r >> 2) & 1 : r & 7;
+#pragma unroll
+            for (int x = 0; x < GPW; ++x) {
+                const int grp = wg + C::WG * x;
+                if (grp >= ng) continue;
+                const float4 *n4 = reinterpret_cast<const float4 *>(&bars->nm[16 * grp]);
+                const float4 *w4 = reinterpret_cast<const float4 *>(&bars->w[16 * grp]);
+                uint32_t hi[NR / 4], mid[NR / 4];
+#pragma unroll
+                for (int k = 0; k < NR; k += 4) {
+                    const float4 nm = n4[k / 4], w = w4[k / 4];
+                    float e[4];
+                    unpack_f2(add_f2(y[x][k / 2], pack_f2(nm.x, nm.y)), e[0], e[1]);
+                    unpack_f2(add_f2(y[x][k / 2 + 1], pack_f2(nm.z, nm.w)), e[2], e[3]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) e[q] = ex2(e[q]);
+                    l[x][k / 2] = fma_f2(pack_f2(e[0], e[1]), mul_f2(pack_f2(w.x, w.y), isv2), l[x][k / 2]);
+                    l[x][k / 2 + 1] = fma_f2(pack_f2(e[2], e[3]), mul_f2(pack_f2(w.z, w.w), isv2), l[x][k / 2 + 1]);
+                    uint32_t h0, h1, m0, m1;
+                    split2(e[0], e[1], h0, m0);
+                    split2(e[2], e[3], h1, m1);
+                    hi[k / 4] = h0 | (h1 << 16);
+                    mid[k / 4] = m0 | (m1 << 16);
+                }
+                uint8_t *ph = prow + (((2 * grp) ^ swz) << 4), *pm = prow + (((2 * grp + 1) ^ swz) << 4);
+                if constexpr (NR == 16) {
+                    *reinterpret_cast<uint4 *>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(pm) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                } else if constexpr (NR == 8) {
+                    *reinterpret_cast<uint2 *>(ph) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2 *>(pm) = make_uint2(mid[0], mid[1]);
+                } else {
+                    *reinterpret_cast<uint32_t *>(ph) = hi[0];
+                    *reinterpret_cast<uint32_t *>(pm) = mid[0];
+                }
+            }
+            if (tid == 0) bars->fresh[b] = (fresh ? 1 : 0) | (int)((par & 1) << 1);
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[b]));
+            sk = sk1;
+            sv = sv1;
+            if (fresh && !first) {
+                // the group before: its last P V is that of tile j - 1
+                ok = warp_wait(smem_u32(&bars->pv_done[b ^ 1]), ((j - 1) >> 1) & 1, abort_flag);
+                if (soft_any<ST>(!ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int x = 0; x < GPW; ++x) {
+                    const int grp = wg + C::WG * x;
+                    if (grp >= ng) continue;
+                    uint32_t s[2 * NR];
+                    ld_terms<NR>(lane_base + C::O_COL + ((par & 1) ^ 1) * C::COLS + 32 * grp, s);
+#pragma unroll
+                    for (int k = 0; k < NR; ++k)
+                        o[x][k] = o[x][k] * bars->am[16 * grp + k] +
+                                  fmaf(__uint_as_float(s[NR + k]), 0.0625f, __uint_as_float(s[k])) * bars->beta[16 * grp + k];
+                }
+                tc_fence_before();
+            }
+            first = false;
+        }
+        if (!ok) break;                  // voted: the same in every warp
+
+        // epilogue: the last group, the row sums, then O of a unit that this CTA covers alone, else a partial
+        ok = warp_wait(smem_u32(&bars->pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, abort_flag);
+        if (soft_any<ST>(!ok)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int x = 0; x < GPW; ++x) {
+            const int grp = wg + C::WG * x;
+            if (grp >= ng) continue;
+            uint32_t s[2 * NR];
+            ld_terms<NR>(lane_base + C::O_COL + (par & 1) * C::COLS + 32 * grp, s);
+#pragma unroll
+            for (int k = 0; k < NR; ++k)
+                o[x][k] += fmaf(__uint_as_float(s[NR + k]), 0.0625f, __uint_as_float(s[k])) * bars->w[16 * grp + k];
+#pragma unroll
+            for (int k = 0; k < NR; k += 2) {
+                float u, v;
+                unpack_f2(l[x][k / 2], u, v);
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) {
+                    u += __shfl_xor_sync(0xffffffffu, u, d);
+                    v += __shfl_xor_sync(0xffffffffu, v, d);
+                }
+                if (lane == 0) {
+                    bars->red[warp][16 * x + k] = u;
+                    bars->red[warp][16 * x + k + 1] = v;
+                }
+            }
+        }
+        tc_fence_before();
+        soft_sync<ST>();
+        // slot 2 * cta: a unit that an earlier CTA began; 2 * cta + 1: one that begins here
+        const bool whole = it.t1 - it.t0 == it.nt;
+        const int part = 2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
+        if (tid == 0 && !whole) {
+            parts |= it.t0 == 0 ? 2 : 1;
+            p.meta[part] = PagedMeta{it.row0, it.h0, it.rows, it.t1 == it.nt};
+        }
+        if (tid < it.rows && (tid & 15) < NR) {
+            const int grp = tid >> 4, w0 = 4 * (grp % C::WG), at = 16 * (grp / C::WG) + (tid & 15);
+            const float sum = (bars->red[w0][at] + bars->red[w0 + 1][at]) + (bars->red[w0 + 2][at] + bars->red[w0 + 3][at]);
+            const bool empty = sum == 0.f;                    // the row saw no key
+            const float lse = empty ? -INFINITY : (bars->top[tid] + log2f(sum)) * kLn2;
+            bars->inv[tid] = empty ? 0.f : (whole ? p.out_scale : 1.f) / sum;
+            if (!whole) p.part_lse[(int64_t)part * C::R + tid] = lse;
+            else if (p.lse) p.lse[bars->at[slot][tid]] = lse;
+        }
+        soft_sync<ST>();
+#pragma unroll
+        for (int x = 0; x < GPW; ++x) {
+            const int grp = wg + C::WG * x;
+#pragma unroll
+            for (int k = 0; k < NR; ++k) {
+                const int row = 16 * grp + k;
+                if (row >= it.rows) continue;
+                const float v = bars->inv[row] == 0.f ? 0.f : o[x][k] * bars->inv[row];
+                if (!whole) {
+                    p.part_o[((int64_t)part * C::R + row) * kD + r] = v;
+                } else {
+                    uint16_t *dst = static_cast<uint16_t *>(p.o) + (int64_t)bars->at[slot][row] * kD + r;
+                    *dst = (uint16_t)pack2<C::BF>(v, 0.f);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->q_empty[slot]));
+        soft_sync<ST>();                 // the scratch rows may be rewritten after this
+    }
+    if (tid == 0)                        // empty slots; one that is missing (a CTA that gave up) also ends its unit
+        for (int s = 0; s < 2; ++s)
+            if (!(parts >> s & 1)) p.meta[2 * blockIdx.x + s] = PagedMeta{0, 0, 0, 1};
+}
+
+template <bool BF, int NG, int NR>
+__global__ void __launch_bounds__((PagedCfg<BF, NG>::THREADS), 1)
+    fmha_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
+    using C = PagedCfg<BF, NG>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    PagedBars *bars = reinterpret_cast<PagedBars *>(smem + C::OFF_BARS);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&bars->q_full[s]), 2);            // the q warps
+            mbar_init(smem_u32(&bars->q_empty[s]), 1 + C::SW);   // the MMA warp's commit and the softmax warps
+            mbar_init(smem_u32(&bars->s_full[s]), 1);
+            mbar_init(smem_u32(&bars->s_free[s]), C::SW);
+            mbar_init(smem_u32(&bars->p_full[s]), C::SW);
+            mbar_init(smem_u32(&bars->pv_done[s]), 1);
+        }
+        mbar_init(smem_u32(&bars->drain), 1);
+        for (int s = 0; s < C::NS; ++s) {
+            mbar_init(smem_u32(&bars->kv_full[s]), 1);
+            mbar_init(smem_u32(&bars->kv_empty[s]), 1);
+        }
+        for (int s = 0; s < kPagedItems; ++s) {
+            mbar_init(smem_u32(&bars->item_full[s]), 1);
+            mbar_init(smem_u32(&bars->item_empty[s]), C::SW + 3);   // the softmax, q and MMA warps
+        }
+        bars->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == C::MMA) {
+        tmem_alloc(smem_u32(&bars->tmem_base), C::TMEM_COLS);
+        tmem_relinquish();
+    }
+    PagedCursor cur;
+    int gate = 0;
+    if (warp == C::PROD) {
+        if (lane == 0) {
+            prefetch_tmap(&tmK);
+            prefetch_tmap(&tmV);
+        }
+        gate = g_test_gate;              // read along with the lengths
+        paged_schedule(p, cur, lane);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    // the merge kernel may be scheduled as CTAs of this grid exit; it waits
+    // for this grid's completion before it reads the partials
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp < C::SW) paged_softmax<C, NR>(p, smem, bars, tmem, warp, lane);
+    else if (warp < C::PROD) paged_queries<C>(p, smem, bars, warp - C::QW, lane);
+    else if (warp == C::PROD) paged_producer<C>(p, cur, gate, &tmK, &tmV, smem, bars, lane);
+    else paged_mma<C>(smem, bars, tmem, lane);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == C::MMA) {
+        __syncwarp();
+        tmem_dealloc(tmem, C::TMEM_COLS);
+    }
+}
+
+// Joins the partials of the units that several CTAs covered:
+//   O = out_scale * sum_c w_c O_c / sum_c w_c with w_c = exp(LSE_c - max LSE).
+// CTA (c, y) takes rows, a warp each, of the unit that CTA c of the kernel above
+// began and did not end; the metadata says how far it goes on.
+constexpr int kPagedMergeWarps = 4;
+
+template <bool BF>
+__global__ void __launch_bounds__(32 * kPagedMergeWarps) fmha_paged_merge_kernel(const PagedParams p, int R) {
+    const int lane = threadIdx.x & 31, c0 = blockIdx.x;
+    const int r = blockIdx.y * kPagedMergeWarps + (threadIdx.x >> 5);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (c0 + 1 >= p.ncta || r >= R) return;
+    const PagedMeta m = p.meta[2 * c0 + 1];
+    if (r >= m.rows) return;                                 // also: CTA c0 began no unit that it did not end
+    // the partials of CTAs c0 .. c0 + n - 1
+    int n = 1;
+    for (;;) {
+        const int c = c0 + n + lane;
+        const unsigned hit = __ballot_sync(0xffffffffu, c >= p.ncta || p.meta[2 * c].last);
+        n += hit ? __ffs(hit) : 32;
+        if (hit) break;
+    }
+    n = imin(n, p.ncta - c0);
+    auto slot = [&](int c) { return ((int64_t)2 * (c0 + c) + (c == 0 ? 1 : 0)) * R + r; };
+    float mx = -INFINITY;
+    bool nan = false;
+    for (int c = lane; c < n; c += 32) {
+        const float v = p.part_lse[slot(c)];
+        nan |= v != v;
+        mx = fmaxf(mx, v);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (mx == -INFINITY || __any_sync(0xffffffffu, nan)) mx = 0.f;   // no key: weights 0; NaN in, NaN out
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    for (int cb = 0; cb < n; cb += 8) {
+        float4 v[8];                                         // eight partials in flight
+        float w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int64_t s = slot(imin(cb + k, n - 1));
+            v[k] = reinterpret_cast<const float4 *>(p.part_o)[s * (kD / 4) + lane];
+            w[k] = p.part_lse[s];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float x = cb + k < n ? __expf(w[k] - mx) : 0.f;
+            sum += x;
+            acc.x += x * v[k].x;
+            acc.y += x * v[k].y;
+            acc.z += x * v[k].z;
+            acc.w += x * v[k].w;
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : p.out_scale / sum;
+    const int t = p.subs == 1 ? r / p.G : 0;
+    const int64_t at = (int64_t)(m.row0 + t) * p.H + m.h0 + r - t * p.G;
+    reinterpret_cast<uint2 *>(p.o)[at * (kD / 4) + lane] =
+        make_uint2(pack2<BF>(acc.x * inv, acc.y * inv), pack2<BF>(acc.z * inv, acc.w * inv));
+    if (lane == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : mx + logf(sum);
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+// Query rows of a unit: one group of 16 where a sequence's rows of a kv head
+// fit it, else four.
+int paged_rows(int64_t max_q, int G) { return max_q * G <= 16 ? 16 : 64; }
+
+using PagedKernel = void (*)(CUtensorMap, CUtensorMap, PagedParams);
+template <bool BF>
+PagedKernel paged_kernel(int rows, int per_unit) {
+    if (rows == 64) return fmha_paged_kernel<BF, 4, 16>;
+    return per_unit <= 4 ? fmha_paged_kernel<BF, 1, 4> : per_unit <= 8 ? fmha_paged_kernel<BF, 1, 8> : fmha_paged_kernel<BF, 1, 16>;
+}
+template <bool BF>
+int paged_smem(int rows) {
+    return rows == 64 ? PagedCfg<BF, 4>::SMEM_BYTES : PagedCfg<BF, 1>::SMEM_BYTES;
+}
+template <bool BF>
+int paged_threads(int rows) {
+    return rows == 64 ? PagedCfg<BF, 4>::THREADS : PagedCfg<BF, 1>::THREADS;
+}
+
+}  // namespace
+
+int paged_set_wait_limit(unsigned long long ns) { return cache_set_wait_limit(ns); }
+int paged_set_test_gate(int on) { return cache_set_test_gate(on); }
+int *paged_status_word() { return symbol_address(g_status); }
+
+}  // namespace fmha
+
+using namespace fmha;
+
+extern "C" size_t fmha_page_workspace_size(int max_q, int H, int H_k) {
+    if (max_q <= 0 || H <= 0 || H_k <= 0 || H % H_k != 0 || H / H_k > kRows) return 0;
+    // two partials a CTA: an fp32 row of O and its LSE for every row of a unit, and whose they are
+    return (size_t)2 * kPagedMaxCtas * (paged_rows(max_q, H / H_k) * (kD + 1) * sizeof(float) + sizeof(PagedMeta));
+}
+
+extern "C" int fmha_page_fwd(fmha_tensor q, fmha_tensor k_pages, fmha_tensor v_pages, const float *k_scale,
+                             const float *v_scale, fmha_tensor o, float *lse, int B, int N, int max_q, int H, int H_k,
+                             int D, int n_pages, int page_size, int B_table, int max_pages, const int *table,
+                             const int *seqlen, const int *batch_idx, const int *cu_q, float scale, float out_scale,
+                             int mask, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    int shift = 4;
+    while (shift < 7 && page_size != 1 << shift) ++shift;
+    if (B < 0 || N < 0 || H <= 0 || H_k <= 0 || H % H_k != 0 || H / H_k > kRows || D != kD || page_size != 1 << shift)
+        return FMHA_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !(scale < INFINITY) || !(out_scale == out_scale) || out_scale == INFINITY || out_scale == -INFINITY)
+        return FMHA_ERR_INVALID_ARG;
+    if (mask != FMHA_MASK_NONE && mask != FMHA_MASK_CAUSAL) return FMHA_ERR_INVALID_ARG;
+    if (B == 0 || N == 0) return FMHA_OK;
+    if (max_q <= 0 || n_pages <= 0 || B_table <= 0 || max_pages <= 0 || max_pages > kMaxCacheRows >> shift ||
+        (int64_t)n_pages * H_k > 0x7ffffffe || n_pages > 0x7fffffff >> shift || (int64_t)N * H > 0x7fffffff ||
+        (!cu_q && N != B))
+        return FMHA_ERR_INVALID_ARG;
+    if (!q.data || !k_pages.data || !v_pages.data || !o.data || !k_scale || !v_scale || !table || !seqlen)
+        return FMHA_ERR_INVALID_ARG;
+    const int dt = q.dtype;
+    if ((dt != FMHA_F16 && dt != FMHA_BF16) || o.dtype != dt || k_pages.dtype != FMHA_E4M3 || v_pages.dtype != FMHA_E4M3)
+        return FMHA_ERR_UNSUPPORTED;
+    for (const void *ptr : {q.data, k_pages.data, v_pages.data, o.data})
+        if (misaligned(ptr, 16)) return FMHA_ERR_UNSUPPORTED;
+    for (const void *ptr : {(const void *)k_scale, (const void *)v_scale, (const void *)lse, (const void *)table,
+                            (const void *)seqlen, (const void *)batch_idx, (const void *)cu_q})
+        if (misaligned(ptr, 4)) return FMHA_ERR_INVALID_ARG;
+    const size_t need = fmha_page_workspace_size(max_q, H, H_k);
+    if (!workspace || misaligned(workspace, 256) || workspace_bytes < need) return FMHA_ERR_INVALID_ARG;
+    // a unit's inputs are read by several CTAs, at their own times
+    const size_t rows_bytes = (size_t)N * H * kD * 2, pages = ((size_t)n_pages * H_k << shift) * kD;
+    const size_t scales = (size_t)n_pages * H_k * sizeof(float), seqs = (size_t)B * sizeof(int);
+    const Bytes out[3] = {{o.data, rows_bytes}, {lse, (size_t)N * H * sizeof(float)}, {workspace, need}};
+    const Bytes in[9] = {{q.data, rows_bytes}, {k_pages.data, pages}, {v_pages.data, pages}, {k_scale, scales},
+                         {v_scale, scales}, {table, (size_t)B_table * max_pages * sizeof(int)}, {seqlen, seqs},
+                         {batch_idx, seqs}, {cu_q, seqs + sizeof(int)}};
+    if (outputs_clash(out, in)) return FMHA_ERR_INVALID_ARG;
+    const int rc = check_device();
+    if (rc != FMHA_OK) return rc;
+    const int sms = sm_count();
+    if (sms <= 0) return FMHA_ERR_CUDA;
+
+    const int G = H / H_k, R = paged_rows(max_q, G);
+    PagedParams p{};
+    p.q = static_cast<const uint8_t *>(q.data);
+    p.o = o.data;
+    p.lse = lse;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.table = table;
+    p.seqlen = seqlen;
+    p.batch_idx = batch_idx;
+    p.cu_q = cu_q;
+    p.B = B;
+    p.N = N;
+    p.max_q = max_q;
+    p.H = H;
+    p.H_k = H_k;
+    p.G = G;
+    p.B_table = B_table;
+    p.width = max_pages;
+    p.n_pages = n_pages;
+    p.shift = shift;
+    p.subs = G > R ? (G + R - 1) / R : 1;
+    while (p.subs == 1 && (2 << p.tau_log) * G <= R) ++p.tau_log;
+    p.tau = 1 << p.tau_log;
+    p.causal = mask == FMHA_MASK_CAUSAL;
+    p.edge = 2;
+    // a CTA a tile at most, of the tiles that there can be
+    const int64_t units = (int64_t)H_k * p.subs * ((int64_t)B + (N >> p.tau_log));
+    const int64_t tiles = (((int64_t)max_pages << shift) + kRows - 1) / kRows;
+    p.ncta = (int)(units >= kPagedMaxCtas || units * tiles >= kPagedMaxCtas ? kPagedMaxCtas : units * tiles);
+    p.ncta = imin(p.ncta, sms);
+    p.part_o = static_cast<float *>(workspace);
+    p.part_lse = p.part_o + (size_t)2 * p.ncta * R * kD;
+    p.meta = reinterpret_cast<PagedMeta *>(p.part_lse + (size_t)2 * p.ncta * R);
+    p.c = log2_scale(scale);
+    p.out_scale = out_scale;
+
+    CUtensorMap tm[2];
+    for (int kv = 0; kv < 2; ++kv) {
+        // [n_pages * H_k, P, 128]: the rows of one page and head
+        const cuuint64_t dims[3] = {kD, (cuuint64_t)page_size, (cuuint64_t)n_pages * H_k};
+        const cuuint32_t box[3] = {kD, (cuuint32_t)page_size, 1};
+        if (!make_map(&tm[kv], FMHA_E4M3, kv ? v_pages.data : k_pages.data, 3, dims, box)) return FMHA_ERR_CUDA;
+    }
+    const bool bf = dt == FMHA_BF16;
+    const int per_unit = imin(R, G * imin(p.tau, max_q));
+    auto kern = bf ? paged_kernel<true>(R, per_unit) : paged_kernel<false>(R, per_unit);
+    const int smem = bf ? paged_smem<true>(R) : paged_smem<false>(R), threads = bf ? paged_threads<true>(R) : paged_threads<false>(R);
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return cuda_failed();
+    kern<<<p.ncta, threads, smem, stream>>>(tm[0], tm[1], p);
+    if (cudaGetLastError() != cudaSuccess) return FMHA_ERR_CUDA;
+
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.ncta, (R + kPagedMergeWarps - 1) / kPagedMergeWarps);
+    cfg.blockDim = dim3(32 * kPagedMergeWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto merge = bf ? fmha_paged_merge_kernel<true> : fmha_paged_merge_kernel<false>;
+    if (cudaLaunchKernelEx(&cfg, merge, p, R) != cudaSuccess) return cuda_failed();
+    return FMHA_OK;
+}

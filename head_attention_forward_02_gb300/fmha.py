@@ -103,6 +103,12 @@ def lib():
         L.fmha_page_write.restype = ctypes.c_int
         L.fmha_page_write.argtypes = ([fmha_tensor] + [ctypes.c_int64] * 2) * 2 + [ctypes.c_void_p] + [
             fmha_tensor] * 2 + [ctypes.c_void_p] * 2 + [ctypes.c_int] * 5 + [ctypes.c_void_p]
+        L.fmha_page_fwd.restype = ctypes.c_int
+        L.fmha_page_fwd.argtypes = [fmha_tensor] * 3 + [ctypes.c_void_p] * 2 + [fmha_tensor, ctypes.c_void_p] + [
+            ctypes.c_int] * 10 + [ctypes.c_void_p] * 4 + [ctypes.c_float, ctypes.c_float, ctypes.c_int, ctypes.c_void_p,
+                                                          ctypes.c_size_t, ctypes.c_void_p]
+        L.fmha_page_workspace_size.restype = ctypes.c_size_t
+        L.fmha_page_workspace_size.argtypes = [ctypes.c_int] * 3
         L.fmha_rope.restype = ctypes.c_int
         L.fmha_rope.argtypes = [fmha_tensor, fmha_strides] * 4 + [ctypes.c_int] * 6 + [ctypes.c_void_p] * 2 + [
             ctypes.c_float] + [ctypes.c_int] * 2 + [ctypes.c_void_p]
@@ -771,6 +777,85 @@ def page_write(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor, k_
         fmha_tensor(k_new.data_ptr(), code), kt, kh, fmha_tensor(v_new.data_ptr(), code), vt, vh, slots.data_ptr(),
         fmha_tensor(k_pages.data_ptr(), E4M3), fmha_tensor(v_pages.data_ptr(), E4M3), k_scale.data_ptr(),
         v_scale.data_ptr(), N, H_k, D, n_pages, P, _raw_stream(index)))
+
+
+def fmha_page_fwd(q, k_pages, v_pages, k_scale, v_scale, o, lse, B, N, max_q, H, H_k, D, n_pages, page_size, B_table,
+                  max_pages, table, seqlen, batch_idx, cu_q, scale, out_scale, mask, workspace, workspace_bytes,
+                  stream=None) -> int:
+    """Same arguments, order and status codes as the C function fmha_page_fwd."""
+    return lib().fmha_page_fwd(
+        _tensor(q), _tensor(k_pages), _tensor(v_pages), _ptr(k_scale), _ptr(v_scale), _tensor(o), _ptr(lse), int(B), int(N),
+        int(max_q), int(H), int(H_k), int(D), int(n_pages), int(page_size), int(B_table), int(max_pages), _ptr(table),
+        _ptr(seqlen), _ptr(batch_idx), _ptr(cu_q), float(scale), float(out_scale), int(mask), _ptr(workspace),
+        int(workspace_bytes), _stream(stream))
+
+
+def fmha_page_workspace_size(max_q, H, H_k) -> int:
+    return int(lib().fmha_page_workspace_size(int(max_q), int(H), int(H_k)))
+
+
+_page_workspace_size = functools.lru_cache(maxsize=256)(fmha_page_workspace_size)
+
+
+def page_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
+             v_scale: torch.Tensor, table: torch.Tensor, seqlen: torch.Tensor, *, cu_q: Optional[torch.Tensor] = None,
+             max_q: Optional[int] = None, batch_idx: Optional[torch.Tensor] = None, mask: str = "causal",
+             scale: Optional[float] = None, out_scale: float = 1.0, out: Optional[torch.Tensor] = None,
+             lse: Optional[torch.Tensor] = None, return_lse: bool = True, workspace: Optional[torch.Tensor] = None,
+             stream=None):
+    """Attention over a paged e4m3 cache (see fmha_page_fwd).
+
+    q bf16 or f16 [N, H, 128], the rows of all sequences behind one another as
+    cu_q int32 [B + 1] says, at most max_q (None: N) of one sequence; cu_q None: one row a
+    sequence.  k_pages, v_pages e4m3 [n_pages, H_k, page_size, 128]; k_scale,
+    v_scale float [n_pages, H_k]; table int32 [B_table, max_pages]; seqlen,
+    batch_idx int32 [B].  mask "causal" (q-end) or "none".  Allocates O, LSE
+    [N, H] and the workspace with torch when not given; rows behind the last
+    sequence are not written.  Returns (O, LSE)."""
+    index, code = _device_and_code(q)
+    if stream is not None or _current_device() != index:
+        with _on(stream, index):
+            return page_fwd(q, k_pages, v_pages, k_scale, v_scale, table, seqlen, cu_q=cu_q, max_q=max_q,
+                            batch_idx=batch_idx, mask=mask, scale=scale, out_scale=out_scale, out=out, lse=lse,
+                            return_lse=return_lse, workspace=workspace)
+    if q.dim() != 3 or table.dim() != 2 or seqlen.dim() != 1:
+        raise ValueError("q is [N, H, 128], the table is [B_table, max_pages] and seqlen is [B]")
+    if mask not in ("none", "causal"):
+        raise ValueError(f"mask is none or causal, not {mask!r}")
+    n_pages, H_k, P, D = _fit_pages(index, k_pages, v_pages, k_scale, v_scale)
+    (N, H, _), (B_table, width), B, dt = q.shape, table.shape, seqlen.shape[0], q.dtype
+    if cu_q is None and N != B:
+        raise ValueError(f"{N} rows of q for {B} sequences need cu_q")
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and return_lse:
+        lse = torch.empty((N, H), dtype=torch.float32, device=q.device)
+    if not (_fit(index, dt, (N, H, D), q, out) and _fit(index, torch.float32, (N, H), lse)
+            and _fit(index, torch.int32, (B,), seqlen, batch_idx) and _fit(index, torch.int32, (B + 1,), cu_q)
+            and _fit(index, torch.int32, (B_table, width), table)):
+        _check(index, dt, (N, H, D), q=q, out=out)
+        _check(index, torch.float32, (N, H), lse=lse)
+        _check(index, torch.int32, (B,), seqlen=seqlen, batch_idx=batch_idx)
+        _check(index, torch.int32, (B + 1,), cu_q=cu_q)
+        _check(index, torch.int32, (B_table, width), table=table)
+    most = 1 if cu_q is None else N if max_q is None else max_q
+    raw = _raw_stream(index)
+    if workspace is None:
+        nbytes = _page_workspace_size(most, H, H_k)
+        ws = _alloc(nbytes or 1, raw)
+    else:
+        ws, nbytes = _given(workspace, index)
+    try:
+        rc = lib().fmha_page_fwd(
+            fmha_tensor(q.data_ptr(), code), fmha_tensor(k_pages.data_ptr(), E4M3), fmha_tensor(v_pages.data_ptr(), E4M3),
+            k_scale.data_ptr(), v_scale.data_ptr(), fmha_tensor(out.data_ptr(), code), _ptr(lse), B, N, most, H, H_k, D,
+            n_pages, P, B_table, width, table.data_ptr(), seqlen.data_ptr(), _ptr(batch_idx), _ptr(cu_q),
+            1.0 / math.sqrt(D) if scale is None else scale, out_scale, _MASKS[mask], ws, nbytes, raw)
+    finally:
+        if workspace is None:
+            _free(ws)                       # for what this stream runs next
+    _raise(rc)
+    return out, lse
 
 
 def fmha_rope(q, q_strides, k, k_strides, q_out, q_out_strides, k_out, k_out_strides, B, S, H, H_k, D, rot, positions,

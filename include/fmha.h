@@ -526,6 +526,57 @@ int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_t k_head_st
                     fmha_tensor v_pages, float *k_scale, float *v_scale, int N, int H_k, int D, int n_pages,
                     int page_size, cudaStream_t stream);
 
+/*
+ * fmha_page_fwd -- attention over a paged cache: of one token a sequence, of
+ * some (drafts, the ends of prompts) or of whole chunks of prompts, mixed as
+ * they come.  Their keys and values are in the cache already (fmha_page_write).
+ *
+ * Sequence b has the packed rows cu_q[b] .. cu_q[b + 1] - 1 of q (cu_q NULL:
+ * row b alone), n of them, and L = seqlen[b] cached tokens, those of the call
+ * included, in the pages of table row e = batch_idx ? batch_idx[b] : b.  With
+ * key j of kv head g, k_scale[page_j, g] * code, its row t and query head h of g
+ *   O[row, h, :] = out_scale * softmax(scale * q . keys) values
+ *   lse[row, h]  = natural-log log-sum-exp of the scaled scores
+ * over the keys j <= L - n + t (FMHA_MASK_CAUSAL, q-end aligned: the last row
+ * sees every key) or all L (FMHA_MASK_NONE).  No key at all: O = 0, lse = -inf.
+ * Rows behind cu_q[B] are left as they were.
+ *
+ * Layouts (contiguous): q, o [N, H, 128], FMHA_F16 or FMHA_BF16; the cache as
+ * above; table int32 [B_table, max_pages]; seqlen, batch_idx int32 [B]; cu_q
+ * int32 [B + 1], ascending; lse float [N, H] or NULL.  batch_idx may be NULL,
+ * and sequences may share a table row or pages.  max_q: the most rows that a
+ * sequence has.  D must be 128, H / H_k at most 128, N * H and n_pages *
+ * page_size below 2^31, max_pages * page_size at most 2^30.  Data pointers
+ * 16-byte aligned, the others 4-byte.  o, lse and the workspace are apart from
+ * the inputs and from one another.
+ * q and the codes enter the products as they are (elements of q below 2^-13,
+ * f16 2^-10, of their row's largest are rounded, by 2^-21 of it at most), scores,
+ * sums and O are fp32; a weight is rounded by 2^-8 of itself at most, and below
+ * that all of them together by 2^-8 of the row's sum.  A q row that holds an
+ * infinity or a NaN gives NaN.  v_scale counts as 2^-60 or 2^60 outside these.
+ * Requirements the host cannot check: 0 <= seqlen[b] <= max_pages * page_size,
+ * 0 <= batch_idx[b] < B_table, cu_q ascending within [0, N] and in steps of
+ * max_q at most, pages in [0, n_pages); a kernel that meets a violation clamps
+ * the length or the rows, or reads zeros for the missing page, and
+ * fmha_device_status then reports FMHA_ERR_INVALID_ARG.  Table entries and
+ * cached rows at or past a sequence's length are never used, and may hold any
+ * bits; a value that only some of a call's rows see must be finite.
+ *
+ * workspace: fmha_page_workspace_size(max_q, H, H_k) bytes (10.1 MB at most),
+ * 256-byte aligned, no initialisation, not shared with a concurrent call.  The
+ * call allocates nothing and is asynchronous on `stream` (two kernels).
+ * Returns FMHA_OK, FMHA_ERR_INVALID_ARG (bad sizes or pointers, scale not
+ * finite and > 0, workspace too small or misaligned), FMHA_ERR_UNSUPPORTED
+ * (dtype, alignment, device) or FMHA_ERR_CUDA.  B = 0 or N = 0 succeeds without
+ * a launch.
+ */
+int fmha_page_fwd(fmha_tensor q, fmha_tensor k_pages, fmha_tensor v_pages, const float *k_scale, const float *v_scale,
+                  fmha_tensor o, float *lse, int B, int N, int max_q, int H, int H_k, int D, int n_pages,
+                  int page_size, int B_table, int max_pages, const int *table, const int *seqlen,
+                  const int *batch_idx, const int *cu_q, float scale, float out_scale, int mask, void *workspace,
+                  size_t workspace_bytes, cudaStream_t stream);
+size_t fmha_page_workspace_size(int max_q, int H, int H_k);
+
 /* Which elements of a head fmha_rope turns together. */
 enum fmha_rope_layout {
     FMHA_ROPE_HALF = 0,   /* i and i + rot / 2 */
@@ -623,7 +674,7 @@ const char *fmha_status_string(int status);
  * device: FMHA_OK, FMHA_ERR_TIMEOUT if a kernel gave up a bounded wait
  * (it then skipped its remaining work and released its resources), or
  * FMHA_ERR_INVALID_ARG if fmha_gen_fwd, fmha_tree_fwd, fmha_tree_commit,
- * fmha_cache_weights, fmha_cache_evict, fmha_page_plan or fmha_page_write met a
+ * fmha_cache_weights, fmha_cache_evict, fmha_page_plan, fmha_page_write or fmha_page_fwd met a
  * length, count, cache entry, draft, page or slot outside its bounds.
  * Synchronises the device.  reset != 0 clears the word.  Returns
  * FMHA_ERR_CUDA if the word cannot be read.
@@ -632,8 +683,8 @@ int fmha_device_status(int reset);
 
 /*
  * fmha_set_wait_limit_ns -- test hook for the failure path of fmha_fwd,
- * fmha_fwd_splitkv, fmha_gen_fwd, fmha_tree_fwd, fmha_cache_weights and
- * fmha_bwd: their bounded on-device waits give up after ns nanoseconds instead
+ * fmha_fwd_splitkv, fmha_gen_fwd, fmha_tree_fwd, fmha_cache_weights,
+ * fmha_page_fwd and fmha_bwd: their bounded on-device waits give up after ns nanoseconds instead
  * of 4 s (ns = 0 restores 4 s).  A wait that expires records FMHA_ERR_TIMEOUT
  * for fmha_device_status and makes the call's CTAs stop issuing work, wait
  * (bounded) for the copies and MMAs they have in flight, free their tensor
@@ -645,8 +696,8 @@ int fmha_set_wait_limit_ns(unsigned long long ns);
 
 /*
  * fmha_set_test_gate -- test hook: while on (on != 0), the producer warp of
- * every fmha_fwd / fmha_fwd_splitkv CTA, of every fmha_gen_fwd and
- * fmha_tree_fwd attention CTA, of every fmha_cache_weights CTA that reads keys
+ * every fmha_fwd / fmha_fwd_splitkv CTA, of every fmha_gen_fwd, fmha_tree_fwd
+ * and fmha_page_fwd attention CTA, of every fmha_cache_weights CTA that reads keys
  * and of every fmha_bwd dQ and dK/dV CTA first waits for a device flag that
  * nothing sets, so that bounded wait expires after the limit of
  * fmha_set_wait_limit_ns and the launch takes the failure path above before
