@@ -29,10 +29,11 @@
 // the old rows' factor are exact, which leaves each value one rounding (a row
 // whose scale grows into e4m3's subnormals: two).
 //
-// Bound by memory: 2 bytes in and 1 out an element.  A CTA takes 16 tokens of one
-// head, K or V; a run of up to eight rows is a warp's (a decode step's are
-// one), a longer one is spread over the CTA's warps, all its loads in flight at
-// once and held in registers between the maximum and the rounding.
+// Bound by memory: 2 bytes in and 1 out an element.  A CTA takes the runs that
+// begin in 16 tokens, for some heads, and each of its warps one run of one
+// head's K or V: two rows a load, 16 rows in flight and in registers, so that
+// runs of up to 16 tokens are read once; of longer ones the first 16 rows stay
+// and the others are read again from L2, without a word between the warps.
 #include <cooperative_groups.h>
 
 #include "fmha_cache.cuh"
@@ -212,7 +213,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fmha_page_plan_kernel(const P
 
 constexpr int kWriteChunk = 16;          // tokens of a CTA
 constexpr int kWriteWarps = 8;
-constexpr int kWarpRows = 8;             // longest run of a single warp
+constexpr int kBatchRows = 16;           // rows that a warp has in registers
 constexpr int kLowest = -60, kHighest = 60;   // exponents of the scales
 
 struct WriteParams {
@@ -222,6 +223,7 @@ struct WriteParams {
     float *scale[2];                     // [n_pages, H_k]
     const int *slots;                    // [N]
     int N, H_k, shift, slots_end;        // slots_end: n_pages * P
+    int pairs;                           // of (head, K or V) that a CTA takes
 };
 
 template <bool BF>
@@ -307,106 +309,74 @@ __device__ __forceinline__ void rescale_rows(const Run &r, float f, int first, i
     }
 }
 
+// A warp takes (run, head, K or V) items of the CTA's chunk.
 template <bool BF>
-__global__ void __launch_bounds__(32 * kWriteWarps) fmha_page_write_kernel(const WriteParams p) {
-    __shared__ int s_len[kWriteChunk];   // of the long run that begins at a token
-    __shared__ float s_max[kWriteWarps];
-    const int c0 = blockIdx.x * kWriteChunk, g = blockIdx.y, kv = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int P = 1 << p.shift;
-    // where runs begin, and how far they go
+__global__ void __launch_bounds__(32 * kWriteWarps, 3) fmha_page_write_kernel(const WriteParams p) {
+    const int c0 = blockIdx.x * kWriteChunk, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int P = 1 << p.shift, half = lane >> 4, col = (lane & 15) * 16;
+    // where runs begin
     const int i = c0 + lane;
     const int slot = lane < kWriteChunk && i < p.N ? p.slots[i] : -1;
     const bool inside = slot >= 0 && slot < p.slots_end;
+    if (warp == 0 && blockIdx.y == 0 && slot >= p.slots_end) atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
     bool begins = inside;
     for (int j = 1; begins && j <= min(i, slot & (P - 1)); ++j) {
         const int other = p.slots[i - j];
         if (other == slot - j) begins = false;               // of the same run
         else if (other >= 0) break;
     }
-    if (warp == 0 && g == 0 && kv == 0 && slot >= p.slots_end) atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
     const unsigned starts = __ballot_sync(0xffffffffu, begins);
-    if (starts == 0) return;             // the same in every warp
-    // selected, not indexed: an index would put the parameters into local memory
-    const int64_t x_t = kv ? p.x_t[1] : p.x_t[0];
-    const uint8_t *x0 = kv ? p.x[1] + g * p.x_h[1] : p.x[0] + g * p.x_h[0];
-    unsigned longer = 0;                 // runs for the whole CTA: the same in every warp
-    int nth = 0;
-    for (unsigned todo = starts; todo; todo &= todo - 1, ++nth) {
-        const int t = __ffs(todo) - 1, s = __shfl_sync(0xffffffffu, slot, t);
+    const int pair0 = blockIdx.y * p.pairs, pairs = min(p.pairs, 2 * p.H_k - pair0);
+    const int items = __popc(starts) * pairs;
+    for (int item = warp; item < items; item += kWriteWarps) {
+        const int nth = item / pairs, pair = pair0 + item - nth * pairs;
+        unsigned rest = starts;
+        for (int k = 0; k < nth; ++k) rest &= rest - 1;
+        const int t = __ffs(rest) - 1, s = __shfl_sync(0xffffffffu, slot, t);
+        const int g = pair >> 1, kv = pair & 1;
+        const int *slots = p.slots + c0 + t;
+        // how far the run goes
         const int room = min(P - (s & (P - 1)), p.N - (c0 + t));
         int n = 1;
         while (n < room) {
-            const int j = n + lane, at = j < room ? p.slots[c0 + t + j] : 0;
+            const int j = n + lane, at = j < room ? slots[j] : 0;
             const unsigned stop = __ballot_sync(0xffffffffu, j >= room || (at >= 0 && at != s + j));
             n += stop ? __ffs(stop) - 1 : 32;
             if (stop) break;
         }
-        if (n > kWarpRows) {
-            longer |= 1u << t;
-            if (warp == 0 && lane == 0) s_len[t] = n;
-            continue;
-        }
-        if (nth % kWriteWarps != warp) continue;
-        // half a warp a row, all rows in flight
         const Run r = run_of(p, s, g, kv);
-        const int half = lane >> 4, col = (lane & 15) * 16;
-        const uint8_t *x = x0 + (c0 + t) * x_t + col;
-        uint4 v[kWarpRows / 2];
-        bool live[kWarpRows / 2];
+        // selected, not indexed: an index would put the parameters into local memory
+        const int64_t x_t = kv ? p.x_t[1] : p.x_t[0];
+        const uint8_t *x = (kv ? p.x[1] + g * p.x_h[1] : p.x[0] + g * p.x_h[0]) + (c0 + t) * x_t + col;
+        uint4 v[kBatchRows / 2];
+        unsigned live;                   // of the batch's rows: those that are written
+        auto load = [&](int j0) {
+            live = __ballot_sync(0xffffffffu, lane < kBatchRows && j0 + lane < n && slots[j0 + lane] >= 0) >> half;
+#pragma unroll
+            for (int k = 0; k < kBatchRows / 2; ++k)
+                if (live >> (2 * k) & 1) v[k] = *reinterpret_cast<const uint4 *>(x + (j0 + 2 * k + half) * x_t);
+        };
         float a = 0.f, old;
+        for (int j0 = (n - 1) / kBatchRows * kBatchRows; j0 >= 0; j0 -= kBatchRows) {
+            load(j0);                    // the first batch last: it stays
 #pragma unroll
-        for (int k = 0; k < kWarpRows / 2; ++k) {
-            live[k] = 2 * k + half < n && p.slots[c0 + t + 2 * k + half] >= 0;
-            if (2 * k + half < n) v[k] = *reinterpret_cast<const uint4 *>(x + (2 * k + half) * x_t);
+            for (int k = 0; k < kBatchRows / 2; ++k)
+                if (live >> (2 * k) & 1) a = abs_max<BF>(v[k], a);
         }
-#pragma unroll
-        for (int k = 0; k < kWarpRows / 2; ++k)
-            if (live[k]) a = abs_max<BF>(v[k], a);
         const float sc = run_scale(r, warp_max(a), old);
         if (r.off > 0 && sc > old) rescale_rows(r, old / sc, lane >> 3, 4);
         const float inv = 1.f / sc;
+        for (int j0 = 0;;) {
 #pragma unroll
-        for (int k = 0; k < kWarpRows / 2; ++k)
-            if (live[k])
-                *reinterpret_cast<uint2 *>(r.rows + (r.off + 2 * k + half) * 128 + col / 2) = codes8<BF>(v[k], inv);
+            for (int k = 0; k < kBatchRows / 2; ++k)
+                if (live >> (2 * k) & 1)
+                    *reinterpret_cast<uint2 *>(r.rows + (r.off + j0 + 2 * k + half) * 128 + col / 2) = codes8<BF>(v[k], inv);
+            j0 += kBatchRows;
+            if (j0 >= n) break;
+            load(j0);
+        }
         __syncwarp();
         if (lane == 0) *r.scale = sc;
-    }
-    if (longer == 0) return;
-    __syncthreads();
-    for (; longer; longer &= longer - 1) {
-        const int t = __ffs(longer) - 1, s = __shfl_sync(0xffffffffu, slot, t);
-        const int n = s_len[t];
-        const Run r = run_of(p, s, g, kv);
-        const int row0 = warp * 2 + (lane >> 4), col = (lane & 15) * 16;
-        const uint8_t *x = x0 + (c0 + t) * x_t + col;
-        uint4 v[8];                      // rows row0, row0 + 16, ... of at most 128
-        unsigned live = 0;
-        float a = 0.f, old;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (16 * k + row0 >= n) continue;
-            v[k] = *reinterpret_cast<const uint4 *>(x + (16 * k + row0) * x_t);
-            live |= (p.slots[c0 + t + 16 * k + row0] >= 0 ? 1u : 0u) << k;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (live >> k & 1) a = abs_max<BF>(v[k], a);
-        a = warp_max(a);
-        if (lane == 0) s_max[warp] = a;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kWriteWarps; ++w) a = fmaxf(a, s_max[w]);
-        const float sc = run_scale(r, a, old);
-        __syncthreads();                 // all have read the scale and the maxima
-        if (r.off > 0 && sc > old) rescale_rows(r, old / sc, threadIdx.x >> 3, 32);
-        const float inv = 1.f / sc;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (live >> k & 1)
-                *reinterpret_cast<uint2 *>(r.rows + (r.off + 16 * k + row0) * 128 + col / 2) = codes8<BF>(v[k], inv);
-        if (threadIdx.x == 0) *r.scale = sc;
     }
 }
 
@@ -537,7 +507,12 @@ extern "C" int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_
     p.H_k = H_k;
     p.shift = shift;
     p.slots_end = n_pages << shift;
-    const dim3 grid((unsigned)(((int64_t)N + kWriteChunk - 1) / kWriteChunk), H_k, 2);
+    // few tokens: as many CTAs as there are (head, K or V) pairs for every chunk;
+    // many: a CTA's warps share a chunk's pairs
+    const int64_t chunks = ((int64_t)N + kWriteChunk - 1) / kWriteChunk;
+    p.pairs = chunks >= 2 * 152 ? 8 : chunks >= 152 ? 4 : chunks >= 76 ? 2 : 1;
+    const dim3 grid((unsigned)chunks, (2 * H_k + p.pairs - 1) / p.pairs);
+    if (grid.y > 65535) return FMHA_ERR_UNSUPPORTED;
     if (dt == FMHA_BF16) fmha_page_write_kernel<true><<<grid, 32 * kWriteWarps, 0, stream>>>(p);
     else fmha_page_write_kernel<false><<<grid, 32 * kWriteWarps, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? FMHA_OK : FMHA_ERR_CUDA;

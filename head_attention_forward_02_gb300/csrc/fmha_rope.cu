@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeBatch = 5;            // items whose loads a thread has in flight
+constexpr int kRopeTok = 4;              // tokens of a CTA at most
 
 struct RopeTensor {
     const uint8_t *in;
@@ -87,59 +88,57 @@ __device__ __forceinline__ void store1(uint8_t *p, float y) {
     else *reinterpret_cast<uint16_t *>(p) = (uint16_t)pack2<BF>(y, 0.f);
 }
 
-// Where an item's elements are: its tensor, and the offset of the token's head.
-struct RopeItem {
-    int which, t;                        // tensor; token of the CTA, -1: nothing to do
-    int64_t in, out;                     // elements
-};
-
-__device__ __forceinline__ RopeItem rope_item(const RopeParams &p, int64_t first, int i) {
-    RopeItem it;
-    it.t = i / p.heads;
-    const int h = i - it.t * p.heads;
-    const uint32_t n = (uint32_t)first + it.t;               // tokens are below 2^31
-    it.which = h >= p.H;
-    const RopeTensor &x = p.x[it.which];
-    const int hh = it.which ? h - p.H : h;
-    const uint32_t b = n / (uint32_t)p.S, s = n - b * p.S;
-    it.in = b * x.in_b + s * x.in_t + hh * x.in_h;
-    it.out = b * x.out_b + s * x.out_t + hh * x.out_h;
-    return it;
-}
-
 // VEC: 16-byte accesses.  A work item is then, of one head, eight pairs (HALF:
 // eight elements of either half, else four pairs, eight elements in a row) or
 // eight elements behind `rot`; without VEC it is one pair or one element.
 template <bool BF, bool FP8, bool HALF, bool VEC>
-__global__ void __launch_bounds__(kRopeThreads) fmha_rope_kernel(const RopeParams p) {
-    extern __shared__ __align__(16) float2 cs[];             // [tok][rot / 2] cosine and sine
-    __shared__ int pos[8];
+__global__ void __launch_bounds__(kRopeThreads, 3) fmha_rope_kernel(const RopeParams p) {
+    extern __shared__ __align__(16) float2 cs[];             // of the CTA's tokens, cosine and sine of every pair
+    __shared__ int pos[kRopeTok];
+    __shared__ int64_t base_in[2][kRopeTok], base_out[2][kRopeTok];   // where a token's heads begin, by tensor
     const int64_t first = (int64_t)blockIdx.x * p.tok;
     const int ntok = (int)min((int64_t)p.tok, p.tokens - first);
     const int items = ntok * p.heads, half = p.rot >> 1;
     const int c = threadIdx.x, rows = blockDim.y;
     const int tid = threadIdx.y * blockDim.x + threadIdx.x, nthr = blockDim.x * blockDim.y;
-    constexpr int W = VEC ? 8 : 1;
-    const int turned = HALF || !VEC ? half / W : p.rot / W;  // items of a head that are turned
+    constexpr int W = VEC ? 8 : 1, PAIRS = !VEC ? 1 : HALF ? 8 : 4;   // elements, pairs of an item
+    const int turned = half / PAIRS;                         // items of a head that are turned
     const bool turn = c < turned;
-    const int a = turn ? (HALF ? c * W : VEC ? c * W : 2 * c) : p.rot + (c - turned) * W;   // first element
-    if (tid < ntok) pos[tid] = p.positions ? p.positions[first + tid] : (int)((first + tid) % p.S);
+    const int a = turn ? (HALF || VEC ? c * W : 2 * c) : p.rot + (c - turned) * W;   // first element
+    if (tid < ntok) {
+        const uint32_t n = (uint32_t)first + tid, b = n / (uint32_t)p.S, s = n - b * p.S;
+        pos[tid] = p.positions ? p.positions[n] : (int)s;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            base_in[w][tid] = b * p.x[w].in_b + s * p.x[w].in_t;
+            base_out[w][tid] = b * p.x[w].out_b + s * p.x[w].out_t;
+        }
+    }
+    __syncthreads();
+    // an item's token, tensor and head
+    auto place = [&](int i, int &t, int &h) -> bool {
+        t = 0;
+#pragma unroll
+        for (int k = 1; k < kRopeTok; ++k) t += i >= k * p.heads;
+        h = i - t * p.heads;
+        const bool key = h >= p.H;
+        if (key) h -= p.H;
+        return key;
+    };
     bool ready = false;
     for (int i0 = threadIdx.y; i0 < items || !ready; i0 += kRopeBatch * rows) {
-        RopeItem it[kRopeBatch];
         uint4 u[kRopeBatch], v[kRopeBatch];
         float fu[kRopeBatch], fv[kRopeBatch];
+        unsigned todo = 0;
 #pragma unroll
         for (int k = 0; k < kRopeBatch; ++k) {
             const int i = i0 + k * rows;
-            it[k].t = -1;
             if (i >= items) continue;
-            it[k] = rope_item(p, first, i);
-            if (!turn && p.in_place[it[k].which]) {
-                it[k].t = -1;
-                continue;
-            }
-            const uint8_t *src = p.x[it[k].which].in + (it[k].in + a) * 2;
+            int t, h;
+            const bool key = place(i, t, h);
+            if ((!turn && (key ? p.in_place[1] : p.in_place[0])) || pos[t] < 0) continue;   // pos < 0: a row without a position
+            todo |= 1u << k;
+            const uint8_t *src = (key ? p.x[1].in : p.x[0].in) + (base_in[key][t] + h * (key ? p.x[1].in_h : p.x[0].in_h) + a) * 2;
             if constexpr (VEC) {
                 u[k] = *reinterpret_cast<const uint4 *>(src);
                 if (HALF && turn) v[k] = *reinterpret_cast<const uint4 *>(src + half * 2);
@@ -150,22 +149,26 @@ __global__ void __launch_bounds__(kRopeThreads) fmha_rope_kernel(const RopeParam
         }
         if (!ready) {                                        // under the first loads
             ready = true;
-            __syncthreads();
             for (int x = tid; x < ntok * half; x += nthr) {
                 const int t = x / half, f = x - t * half;
                 const uint64_t phase = (uint64_t)(int64_t)pos[t] * turn_fraction(p.inv_freq[f]);
                 float s, co;
                 sincospif((float)(int64_t)phase * 0x1p-63f, &s, &co);
-                cs[x] = make_float2(co * p.magnitude, s * p.magnitude * p.sign);
+                // two pairs of every item side by side, so that a load's threads read a row of them
+                const int at = VEC ? (((f % PAIRS) >> 1) * turned + f / PAIRS) * 2 + (f & 1) : f;
+                cs[t * half + at] = make_float2(co * p.magnitude, s * p.magnitude * p.sign);
             }
             __syncthreads();
         }
 #pragma unroll
         for (int k = 0; k < kRopeBatch; ++k) {
-            if (it[k].t < 0 || pos[it[k].t] < 0) continue;   // a row without a position
-            uint8_t *dst = p.x[it[k].which].out + (it[k].out + a) * (FP8 ? 1 : 2);
-            const float2 *w = cs + it[k].t * half;
+            if (!(todo >> k & 1)) continue;
+            int t, h;
+            const bool key = place(i0 + k * rows, t, h);
+            uint8_t *dst = (key ? p.x[1].out : p.x[0].out) +
+                           (base_out[key][t] + h * (key ? p.x[1].out_h : p.x[0].out_h) + a) * (FP8 ? 1 : 2);
             if constexpr (VEC) {
+                const float4 *w = reinterpret_cast<const float4 *>(cs + t * half) + c;
                 const uint32_t uu[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
                 float y[8], z[8];
 #pragma unroll
@@ -176,33 +179,33 @@ __global__ void __launch_bounds__(kRopeThreads) fmha_rope_kernel(const RopeParam
                 }
                 if (HALF && turn) {
                     const uint32_t vv[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-                    float r[8];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float2 x = widen2<BF>(vv[j]);
-                        const float4 cc = *reinterpret_cast<const float4 *>(w + a + 2 * j);
-                        r[2 * j] = y[2 * j] * cc.x - x.x * cc.y;
-                        z[2 * j] = x.x * cc.x + y[2 * j] * cc.y;
-                        r[2 * j + 1] = y[2 * j + 1] * cc.z - x.y * cc.w;
-                        z[2 * j + 1] = x.y * cc.z + y[2 * j + 1] * cc.w;
+                        const float4 cc = w[j * turned];
+                        const float y0 = y[2 * j], y1 = y[2 * j + 1];
+                        y[2 * j] = y0 * cc.x - x.x * cc.y;
+                        z[2 * j] = x.x * cc.x + y0 * cc.y;
+                        y[2 * j + 1] = y1 * cc.z - x.y * cc.w;
+                        z[2 * j + 1] = x.y * cc.z + y1 * cc.w;
                     }
-                    store8<BF, FP8>(dst, r);
                     store8<BF, FP8>(dst + half * (FP8 ? 1 : 2), z);
-                } else {
-                    if (turn) {
+                } else if (turn) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 cc = w[a / 2 + j];
-                            const float x0 = y[2 * j], x1 = y[2 * j + 1];
-                            y[2 * j] = x0 * cc.x - x1 * cc.y;
-                            y[2 * j + 1] = x1 * cc.x + x0 * cc.y;
+                    for (int j = 0; j < 2; ++j) {
+                        const float4 cc = w[j * turned];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const float x0 = y[4 * j + 2 * q], x1 = y[4 * j + 2 * q + 1], co = q ? cc.z : cc.x, s = q ? cc.w : cc.y;
+                            y[4 * j + 2 * q] = x0 * co - x1 * s;
+                            y[4 * j + 2 * q + 1] = x1 * co + x0 * s;
                         }
                     }
-                    store8<BF, FP8>(dst, y);
                 }
+                store8<BF, FP8>(dst, y);
             } else {
                 if (turn) {
-                    const float2 cc = w[c];
+                    const float2 cc = cs[t * half + c];
                     store1<BF, FP8>(dst, fu[k] * cc.x - fv[k] * cc.y);
                     store1<BF, FP8>(dst + (HALF ? half : 1) * (FP8 ? 1 : 2), fv[k] * cc.x + fu[k] * cc.y);
                 } else {
@@ -363,7 +366,7 @@ extern "C" int fmha_rope(fmha_tensor q, fmha_strides q_strides, fmha_tensor k, f
     p.sign = transpose ? -1.f : 1.f;
     const bool half = layout == FMHA_ROPE_HALF;
     p.chunks = vec ? (half ? rot / 16 : rot / 8) + (D - rot) / 8 : rot / 2 + (D - rot);
-    p.tok = p.tokens >= 4 * 4 * 152 ? 4 : 1;
+    p.tok = p.tokens >= 4 * kRopeTok * 152 ? kRopeTok : 1;
     const dim3 block(p.chunks, p.chunks >= kRopeThreads ? 1 : kRopeThreads / p.chunks);
     const dim3 grid((unsigned)((p.tokens + p.tok - 1) / p.tok));
     const int smem = p.tok * (rot / 2) * (int)sizeof(float2);
