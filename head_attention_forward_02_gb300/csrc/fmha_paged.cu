@@ -28,16 +28,24 @@
 // same reference: the next group sets its own, from the maximum of its first
 // tile, and the O^T of the one before is added in fp32 registers, from one of
 // two TMEM buffers, under the softmax of the next.  A score that outgrows the
-// reference opens a new group early.  So nothing depends on how far a tile is
-// below the largest: of a group's weight, what e4m3's smallest steps lose is
-// 2^-8 at most (1024 weights of 2^-14 where the largest is 2^4 or more).
+// reference opens a new group early.  So a long context of small weights behind
+// a large one is not rounded to nothing: of a group's weight, what e4m3's
+// smallest steps lose is 2^-8 at most (1024 weights of 2^-14 where the largest is
+// 2^4 or more), or 2^-42 a key of the largest weight of all (a reference is not
+// more than 2^24 below the highest so far, which keeps fp32 in its range).
 // Row sums are of the unrounded weights, in fp32.
 //
 // Work: the key tiles of all units form one sequence cut evenly over the CTAs,
 // one an SM; units that a cut goes through leave normalised fp32 partials,
-// which a second kernel joins.  Roles: a producer (page ids, TMA, a ring of
-// 128-key tiles), two warps that split q, one MMA issuer, and the softmax
-// warps, a thread a key and, for O^T, a dim.  Their scales are fetched two tiles ahead.
+// which a second kernel joins.  A CTA's producer warp (page ids, TMA, the
+// scales by cp.async) fills a ring of 128-key tiles, a q warp splits the next
+// unit's rows into terms, and two pipelines, each an MMA issuer and four softmax
+// warps with S^T, P^T and O^T of their own, go through the tiles: in units of
+// up to 32 rows each takes every other tile with all rows, from a ring of its
+// own, and their O are added up at the end; in larger ones both take every
+// tile, each with half the groups.  A softmax thread is a key, and for O^T a dim.
+// One pipeline of eight softmax warps with a vote for each tile spent 3550
+// cycles a tile of 64 rows, issuing 45% of them.
 #include "fmha_cache.cuh"
 
 namespace fmha {
@@ -48,8 +56,9 @@ constexpr int kPagedItems = 4;           // work items published ahead
 constexpr int kGroupTiles = 8;           // key tiles with one reference
 constexpr float kBias = 4.f;             // log2 of a group's largest P' where its reference is set
 constexpr float kGrown = 8.75f;          // and how far it may grow: e4m3 ends at 2^8.8
+constexpr float kBelow = 24.f;           // how far a reference may be below the highest before it
 constexpr int kStagesPaged = 6;
-constexpr int kPagedBars = 5120;         // barrier block
+constexpr int kPagedBars = 6144;         // barrier block
 constexpr float kNone = 1e30f;           // -m of a row that has seen no key in its group
 constexpr float kLeastScale = 0x1p-60f, kMostScale = 0x1p60f;   // of values
 
@@ -58,26 +67,32 @@ struct PagedCfg {
     static constexpr bool BF = BF_;
     static constexpr int NG = NG_;                            // groups of 16 query rows a unit holds
     static constexpr int R = 16 * NG;                         // its rows
-    static constexpr int WG = NG == 1 ? 1 : 2;                // softmax warpgroups; one takes groups w, w + WG, ...
-    static constexpr int GPW = NG / WG;
-    static constexpr int SW = 4 * WG;                         // softmax warps
-    static constexpr int QW = SW, PROD = SW + 2, MMA = SW + 3;   // two q warps, producer, MMA issuer
+    static constexpr bool SPLIT = NG <= 2;                    // the pipelines share tiles out, else groups
+    static constexpr int GPW = SPLIT ? NG : NG / 2;           // groups of a pipeline
+    static constexpr int SW = 8;                              // softmax warps
+    static constexpr int QW = SW, PROD = SW + 1, MMA = SW + 2;   // q warp, producer, two MMA issuers
     static constexpr int THREADS = 32 * (SW + 4);
-    static constexpr int COLS = 32 * NG;                      // of S^T and O^T
-    static constexpr int O_COL = 2 * COLS;                    // TMEM: two S^T, then two O^T
-    static constexpr int TMEM_COLS = 4 * COLS;
+    static constexpr int COLS = 32 * GPW;                     // of a pipeline's S^T and O^T
+    static constexpr int PIPE_COLS = 4 * COLS;                // TMEM: two S^T, then two O^T
+    static constexpr int TMEM_COLS = 2 * PIPE_COLS;
     static constexpr int P_ROW = COLS;                        // bytes of a key's P^T row
     static constexpr int P_BYTES = kRows * P_ROW;
-    static constexpr uint64_t P_SWZ = NG == 1 ? 6 : 2;        // 32-byte or 128-byte swizzle
+    static constexpr uint64_t P_SWZ = GPW == 1 ? 6 : 4;       // 32-byte or 64-byte swizzle
     static constexpr int Q_BYTES = (BF ? 32 : 48) * NG * 128; // first and second terms, then f16's third
     static constexpr int STAGE = 2 * kPanelBytes;             // K and V of 128 keys
-    static constexpr int OFF_P = 2 * Q_BYTES;
-    static constexpr int OFF_KV = OFF_P + 2 * P_BYTES;
+    static constexpr int OFF_P = 2 * Q_BYTES;                 // two buffers a pipeline
+    static constexpr int OFF_KV = OFF_P + 4 * P_BYTES;
     static constexpr int NS_FIT = (226 * 1024 - kPagedBars - OFF_KV) / STAGE;
-    static constexpr int NS = NS_FIT < kStagesPaged ? NS_FIT : kStagesPaged;
+    static constexpr int NS = (NS_FIT < kStagesPaged ? NS_FIT : kStagesPaged) & ~1;
+    static constexpr int RING = SPLIT ? NS / 2 : NS;          // stages of a ring
     static constexpr int OFF_BARS = OFF_KV + NS * STAGE;
-    static constexpr int SMEM_BYTES = OFF_BARS + kPagedBars + 1024; // 1 KB alignment
+    static constexpr int SMEM_BYTES = OFF_BARS + kPagedBars + 1024;   // 1 KB alignment
     static_assert(SMEM_BYTES <= 227 * 1024 && OFF_KV % 1024 == 0 && OFF_P % 1024 == 0, "shared memory");
+    static_assert(!SPLIT || 2 * P_BYTES >= R * kD * 4, "pipeline 1 hands its O over in its P^T buffers");
+
+    static __device__ __forceinline__ int group(int w, int x) { return SPLIT ? x : w + 2 * x; }   // x-th of pipeline w
+    static __device__ __forceinline__ int groups(int w, int ng) { return SPLIT ? ng : (ng - w + 1) >> 1; }
+    static __device__ __forceinline__ int position(int grp) { return SPLIT ? grp : 2 * (grp & 1) + (grp >> 1); }   // in q's tile
 };
 
 struct PagedMeta {                       // whose partial a workspace slot holds
@@ -107,21 +122,24 @@ struct PagedItem {
 };
 
 struct PagedBars {
-    uint64_t q_full[2], q_empty[2], drain;
-    uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+    uint64_t q_full[2], q_empty[2], drain[2], stat_full, epi_done;
+    uint64_t s_full[2][2], s_free[2][2], p_full[2][2], pv_done[2][2];   // by pipeline and buffer
     uint64_t kv_full[kStagesPaged], kv_empty[kStagesPaged];
     uint64_t item_full[kPagedItems], item_empty[kPagedItems];
     PagedItem item[kPagedItems];
     uint32_t tmem_base;
     int abort;
-    int fresh[2];                        // of a P^T buffer's tile: it begins a group; and the group's O^T buffer
+    int fresh[2][2];                     // of a P^T buffer's tile: it begins a group; and (bit 1) the group's O^T buffer
+    alignas(16) float zero[16];
+    alignas(16) float scale[kStagesPaged][2][8];   // k_scale, v_scale of a stage's pages
     alignas(16) float qscale[2][64];     // of a q slot's rows: 2^k,
     alignas(16) int lim[2][64], at[2][64];   // the last key they see, and q row * H + head (-1: none)
-    alignas(16) float nm[64], w[64];     // of the group: -m, 2^(m - M)
-    float top[64];                       // M, the largest m so far
-    alignas(16) float am[64], beta[64];  // factors for what was summed before, for the group before
+    alignas(16) float nm[2][64];         // by pipeline and row: -m,
+    alignas(16) float am[2][64];         // 2^(m before - m),
+    float top[2][64];                    // the largest m so far, then (epilogue) the factor of O
     float red[8][32];                    // by warp: maxima or sums of its rows
-    float inv[64];                       // by row: out_scale / sum
+    float stat_m[32], stat_l[32];        // pipeline 1's references and sums
+    float other[32];                     // factor of pipeline 1's O
 };
 static_assert(sizeof(PagedBars) <= kPagedBars, "barrier block");
 
@@ -174,21 +192,6 @@ __device__ __forceinline__ void ld_terms(uint32_t taddr, uint32_t (&r)[2 * NR]) 
                      :
                      : "memory");
     }
-}
-
-// Named barrier 1 over the softmax threads, with a vote.
-template <int N>
-__device__ __forceinline__ void soft_sync() {
-    asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
-}
-template <int N>
-__device__ __forceinline__ bool soft_any(bool v) {
-    uint32_t r;
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, 1, %2, p;\nselp.u32 %0, 1, 0, q;\n}\n"
-                 : "=r"(r)
-                 : "r"((uint32_t)v), "n"(N)
-                 : "memory");
-    return r != 0;
 }
 
 // Two weights as two e4m3 terms each (first weight in the low byte): p = hi +
@@ -363,15 +366,23 @@ __device__ __forceinline__ int page_id(const PagedParams &p, int entry, int i, b
     return -1;
 }
 
+// Stage and parity of the n-th tile of ring x.
+template <class C>
+__device__ __forceinline__ uint32_t ring_stage(int x, uint32_t n) { return (C::SPLIT ? x * C::RING : 0) + n % C::RING; }
+template <class C>
+__device__ __forceinline__ uint32_t ring_parity(uint32_t n) { return (n / C::RING) & 1; }
+
+__device__ const float g_one = 1.f;
+
 // The producer warp: publishes items and loads their K and V tiles, a lane a
-// page.  Ids are fetched a tile ahead.
+// page, with the pages' scales.  Ids are fetched a tile ahead.
 template <class C>
 __device__ void paged_producer(const PagedParams &p, PagedCursor &cur, int gate, const CUtensorMap *tmK,
                                const CUtensorMap *tmV, uint8_t *smem, PagedBars *bars, int lane) {
     volatile int *abort_flag = &bars->abort;
     bool ok = true;
     if (gate) ok = __all_sync(0xffffffffu, lane > 0 || test_gate_open(abort_flag));
-    uint32_t fill = 0, qn = 0;
+    uint32_t fill[2] = {0, 0}, qn = 0;
     const int P = 1 << p.shift, per = kRows >> p.shift;       // pages of a tile
     auto publish = [&](uint32_t i, const PagedItem &it) -> bool {
         const uint32_t st = i % kPagedItems;
@@ -398,8 +409,9 @@ __device__ void paged_producer(const PagedParams &p, PagedCursor &cur, int gate,
         int id = id_of(it.t0);
         for (int t = it.t0; t < it.t1; ++t) {
             const int ahead = id_of(t + 1);
-            const uint32_t st = fill % C::NS;
-            if (fill >= C::NS && !warp_wait(smem_u32(&bars->kv_empty[st]), (fill / C::NS - 1) & 1, abort_flag)) {
+            const int x = C::SPLIT ? (t - it.t0) & 1 : 0;
+            const uint32_t n = x ? fill[1] : fill[0], st = ring_stage<C>(x, n);
+            if (n >= C::RING && !warp_wait(smem_u32(&bars->kv_empty[st]), ring_parity<C>(n) ^ 1, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -413,8 +425,17 @@ __device__ void paged_producer(const PagedParams &p, PagedCursor &cur, int gate,
                 const int head = id >= 0 ? id * p.H_k + it.g : p.n_pages * p.H_k;
                 tma_load_3d(dst, tmK, fb, 0, 0, head);
                 tma_load_3d(dst + kPanelBytes, tmV, fb, 0, 0, head);
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const float *src = id >= 0 ? (kv ? p.v_scale : p.k_scale) + head : &g_one;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&bars->scale[st][kv][lane])), "l"(src)
+                                 : "memory");
+                }
             }
-            ++fill;
+            // every lane's arrival, when its copies are there
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
+            if (x) ++fill[1];
+            else ++fill[0];
             id = ahead;
             if (t == it.t0) {            // the next item is worked out behind the first tile's loads
                 paged_next(p, cur, next);
@@ -426,18 +447,21 @@ __device__ void paged_producer(const PagedParams &p, PagedCursor &cur, int gate,
     }
     // the last release of every stage must arrive before exit; when the CTA
     // gave up, only the copies already issued
-    for (uint32_t f = fill > C::NS ? fill - C::NS : 0; f < fill; ++f) {
-        if (ok) ok = warp_wait(smem_u32(&bars->kv_empty[f % C::NS]), (f / C::NS) & 1, abort_flag);
-        if (!ok) mbar_wait_drain(smem_u32(&bars->kv_full[f % C::NS]), (f / C::NS) & 1);
-    }
+#pragma unroll
+    for (int x = 0; x < (C::SPLIT ? 2 : 1); ++x)
+        for (uint32_t n = fill[x] > C::RING ? fill[x] - C::RING : 0; n < fill[x]; ++n) {
+            const uint32_t st = ring_stage<C>(x, n);
+            if (ok) ok = warp_wait(smem_u32(&bars->kv_empty[st]), ring_parity<C>(n), abort_flag);
+            if (!ok) mbar_wait_drain(smem_u32(&bars->kv_full[st]), ring_parity<C>(n));
+        }
     for (uint32_t i = qn > 2 ? qn - 2 : 0; ok && i < qn; ++i)
         ok = warp_wait(smem_u32(&bars->q_empty[i & 1]), (i >> 1) & 1, abort_flag);
 }
 
-// Two warps: an item's rows of q as e4m3 terms in shared memory, and what the
+// One warp: an item's rows of q as e4m3 terms in shared memory, and what the
 // softmax needs to know of each row.
 template <class C>
-__device__ void paged_queries(const PagedParams &p, uint8_t *smem, PagedBars *bars, int half, int lane) {
+__device__ void paged_queries(const PagedParams &p, uint8_t *smem, PagedBars *bars, int lane) {
     volatile int *abort_flag = &bars->abort;
     PagedItem it;
     for (uint32_t i = 0; paged_take(bars, i, it, abort_flag, lane); ++i) {
@@ -445,7 +469,7 @@ __device__ void paged_queries(const PagedParams &p, uint8_t *smem, PagedBars *ba
         if (i >= 2 && !warp_wait(smem_u32(&bars->q_empty[slot]), ((i >> 1) - 1) & 1, abort_flag)) break;
         uint8_t *qs = smem + slot * C::Q_BYTES;
         const int rows = (it.rows + 15) & ~15;
-        for (int r0 = half * 8; r0 < rows; r0 += 16) {
+        for (int r0 = 0; r0 < rows; r0 += 8) {
             uint2 v[8];
             int at[8];
 #pragma unroll
@@ -483,7 +507,7 @@ __device__ void paged_queries(const PagedParams &p, uint8_t *smem, PagedBars *ba
                 float hi[4], y[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) y[j] = x[j] * up;
-                const int r = r0 + k, row = 32 * (r >> 4) + (r & 15);
+                const int r = r0 + k, pos = C::position(r >> 4), row = 32 * pos + (r & 15);
                 // 16-byte chunk lane / 4 of a 128-byte row, swizzled
                 auto put = [&](int row_, uint32_t c) {
                     *reinterpret_cast<uint32_t *>(qs + row_ * 128 + ((((lane >> 2) ^ (row_ & 7)) << 4) | ((lane & 3) << 2))) = c;
@@ -504,7 +528,7 @@ __device__ void paged_queries(const PagedParams &p, uint8_t *smem, PagedBars *ba
                     term(c1);
                     // behind the first two terms' rows; in the units of the second
                     const uint32_t c2 = pack4_e4m3(y[0] - hi[0], y[1] - hi[1], y[2] - hi[2], y[3] - hi[3]);
-                    put(32 * C::NG + r, c2);
+                    put(32 * C::NG + 16 * pos + (r & 15), c2);
                 }
                 if (lane == 0) bars->qscale[slot][r] = __uint_as_float((uint32_t)(127 + e - 7) << 23);
             }
@@ -515,48 +539,60 @@ __device__ void paged_queries(const PagedParams &p, uint8_t *smem, PagedBars *ba
     }
 }
 
-// MMA issuer (one warp, one elected lane).  S^T and P^T are double-buffered: S^T
-// of tile j + 1 is issued before the P V of tile j, so the softmax of one runs
-// under the MMAs of the other.
+// MMA issuer of pipeline w (one warp, one elected lane).  S^T and P^T are
+// double-buffered: S^T of the pipeline's next tile is issued before the P V of
+// this one, so the softmax of one runs under the MMAs of the other.
 template <class C>
-__device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int lane) {
+__device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int w, int lane) {
     volatile int *abort_flag = &bars->abort;
-    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0) + w * C::PIPE_COLS;
     const uint64_t q0 = desc_sw(smem_u32(smem), 16, 1024, 2);
-    const uint64_t p0 = desc_sw(smem_u32(smem + C::OFF_P), C::P_BYTES, 8 * C::P_ROW, C::P_SWZ);
+    const uint64_t p0 = desc_sw(smem_u32(smem + C::OFF_P + w * 2 * C::P_BYTES), C::P_BYTES, 8 * C::P_ROW, C::P_SWZ);
     const uint64_t k0 = desc_sw(smem_u32(smem + C::OFF_KV), 16, 1024, 2);
     const uint64_t v0 = desc_sw(smem_u32(smem + C::OFF_KV + kPanelBytes), kPanelBytes, 1024, 2);   // MN-major
-    uint32_t j = 0;                      // tiles so far
+    constexpr int kStep = C::SPLIT ? 2 : 1;
+    uint32_t c = 0, m = 0;               // tiles of the ring so far, tiles of MMAs so far
     bool ok = true;
     PagedItem it;
-    int ng_before = 1;                   // of the tile before
-    auto issue_pv = [&](uint32_t c, int ng) -> bool {
-        const uint32_t b = c & 1, st = c % C::NS;
-        if (!warp_wait(smem_u32(&bars->p_full[b]), (c >> 1) & 1, abort_flag)) return false;
+    auto issue_pv = [&](uint32_t mm, uint32_t st, int na) -> bool {
+        const uint32_t b = mm & 1;
+        if (!warp_wait(smem_u32(&bars->p_full[w][b]), (mm >> 1) & 1, abort_flag)) return false;
         tc_fence_after();
-        const int f = *reinterpret_cast<volatile int *>(&bars->fresh[b]);
-        const uint32_t idesc = paged_idesc(32 * ng, true);
+        const int f = *reinterpret_cast<volatile int *>(&bars->fresh[w][b]);
+        const uint32_t idesc = paged_idesc(32 * na, true);
         const uint64_t v = v0 + ((st * C::STAGE) >> 4), pt = p0 + ((b * C::P_BYTES) >> 4);
-        const uint32_t o_tm = tmem + C::O_COL + (f >> 1) * C::COLS;
+        const uint32_t o_tm = tmem + (2 + (f >> 1)) * C::COLS;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)   // 32 keys
             mma_ss<true>(o_tm, v + ((kk * 32 * 128) >> 4), pt + ((kk * 32 * C::P_ROW) >> 4), idesc, kk > 0 || !(f & 1) ? 1u : 0u);
-        tc_commit(smem_u32(&bars->pv_done[b]));
+        tc_commit(smem_u32(&bars->pv_done[w][b]));
         tc_commit(smem_u32(&bars->kv_empty[st]));
         return true;
     };
     for (uint32_t i = 0; ok && paged_take(bars, i, it, abort_flag, lane); ++i) {
-        const int slot = i & 1, ng = (it.rows + 15) >> 4;
+        const int slot = i & 1, na = C::groups(w, (it.rows + 15) >> 4);
         if (!warp_wait(smem_u32(&bars->q_full[slot]), (i >> 1) & 1, abort_flag)) {
             ok = false;
             break;
         }
-        const uint32_t idesc = paged_idesc(32 * ng, false), idesc16 = paged_idesc(16, false);
-        const uint64_t q = q0 + ((slot * C::Q_BYTES) >> 4);
-        for (int t = it.t0; t < it.t1; ++t) {
-            const uint32_t b = j & 1, st = j % C::NS;
-            if (!warp_wait(smem_u32(&bars->kv_full[st]), (j / C::NS) & 1, abort_flag) ||
-                (j >= 2 && !warp_wait(smem_u32(&bars->s_free[b]), ((j >> 1) - 1) & 1, abort_flag))) {
+        const uint32_t idesc = paged_idesc(32 * na, false), idesc16 = paged_idesc(16, false);
+        // this pipeline's groups are side by side in q's tile
+        const int pos0 = C::SPLIT ? 0 : 2 * w;
+        const uint64_t q = q0 + ((slot * C::Q_BYTES + pos0 * 32 * 128) >> 4);
+        const uint64_t q3 = q0 + ((slot * C::Q_BYTES + (32 * C::NG + 16 * pos0) * 128) >> 4);
+        const int tb = it.t0 + (C::SPLIT ? w : 0);
+        uint32_t st_before = 0;
+        for (int t = tb; t < it.t1; t += kStep, ++c) {
+            const uint32_t st = ring_stage<C>(w, c), b = m & 1;
+            if (!warp_wait(smem_u32(&bars->kv_full[st]), ring_parity<C>(c), abort_flag)) {
+                ok = false;
+                break;
+            }
+            if (!C::SPLIT && na == 0) {  // nothing to do with this tile
+                if (lane == 0) mbar_arrive(smem_u32(&bars->kv_empty[st]));
+                continue;
+            }
+            if (m >= 2 && !warp_wait(smem_u32(&bars->s_free[w][b]), ((m >> 1) - 1) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -567,49 +603,63 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
             for (int kk = 0; kk < 4; ++kk)   // 32 dims: 32 bytes of a row
                 mma_ss<true>(s_tm, k + ((kk * 32) >> 4), q + ((kk * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
             if constexpr (!C::BF) {
-                for (int g = 0; g < ng; ++g)
+                for (int g = 0; g < na; ++g)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ss<true>(s_tm + 32 * g + 16, k + ((kk * 32) >> 4),
-                                     q + (((32 * C::NG + 16 * g) * 128 + kk * 32) >> 4), idesc16, 1u);
+                        mma_ss<true>(s_tm + 32 * g + 16, k + ((kk * 32) >> 4), q3 + ((g * 16 * 128 + kk * 32) >> 4), idesc16, 1u);
             }
-            tc_commit(smem_u32(&bars->s_full[b]));
-            if (t + 1 >= it.t1) tc_commit(smem_u32(&bars->q_empty[slot]));
-            if (t > it.t0 && !issue_pv(j - 1, ng_before)) {
+            tc_commit(smem_u32(&bars->s_full[w][b]));
+            if (t + kStep >= it.t1) tc_commit(smem_u32(&bars->q_empty[slot]));
+            if (t > tb && !issue_pv(m - 1, st_before, na)) {
                 ok = false;
                 break;
             }
-            ng_before = ng;
-            ++j;
+            st_before = st;
+            ++m;
         }
-        // the item's last P V: its epilogue does not wait for the next item's loads
-        if (ok) ok = issue_pv(j - 1, ng);
+        if (!ok) break;
+        if (tb >= it.t1 || na == 0) tc_commit(smem_u32(&bars->q_empty[slot]));
+        else ok = issue_pv(m - 1, st_before, na);   // the item's last P V: its epilogue does not wait for the next item's loads
     }
     // no tensor-core operation may be in flight when TMEM is released
-    tc_commit(smem_u32(&bars->drain));
-    mbar_wait_drain(smem_u32(&bars->drain), 0);
+    tc_commit(smem_u32(&bars->drain[w]));
+    mbar_wait_drain(smem_u32(&bars->drain[w]), 0);
 }
 
-// Softmax and epilogue.  Thread r of a warpgroup is key r of every tile (TMEM
-// lane of S^T), and dim r of O^T.
+// Named barrier of a pipeline's softmax threads, and votes over them.
+__device__ __forceinline__ void soft_sync(int w) { asm volatile("bar.sync %0, 128;" ::"r"(1 + w) : "memory"); }
+__device__ __forceinline__ bool soft_any(int w, bool v) {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, %2, 128, p;\nselp.u32 %0, 1, 0, q;\n}\n"
+                 : "=r"(r)
+                 : "r"((uint32_t)v), "r"(1 + w)
+                 : "memory");
+    return r != 0;
+}
+
+// Softmax and epilogue of pipeline w.  Thread r is key r of its tiles (TMEM lane
+// of S^T), and dim r of O^T.
 template <class C, int NR>
-__device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *bars, uint32_t tmem, int warp, int lane) {
-    constexpr int ST = 32 * C::SW, GPW = C::GPW;
+__device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *bars, uint32_t tmem_all, int warp, int lane) {
+    constexpr int GPW = C::GPW, kStep = C::SPLIT ? 2 : 1;
     volatile int *abort_flag = &bars->abort;
-    const int wg = warp >> 2, r = (warp & 3) * 32 + lane, tid = warp * 32 + lane;
-    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const int w = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t tmem = tmem_all + w * C::PIPE_COLS + ((uint32_t)((warp & 3) * 32) << 16);
+    uint8_t *pbuf = smem + C::OFF_P + w * 2 * C::P_BYTES;
+    float *scratch = reinterpret_cast<float *>(smem + C::OFF_P + 2 * C::P_BYTES);   // pipeline 1's O at a unit's end
     const uint64_t sixteenth = pack_f2(0.0625f, 0.0625f);
-    uint32_t j = 0, par = 0;             // tiles, groups so far
+    uint32_t c = 0, n = 0, par = 0;      // tiles so far, of its ring and groups
     int parts = 0;                       // bit s: slot s of this CTA holds a partial
     PagedItem it;
     for (uint32_t i = 0;; ++i) {
         // a false return is either the end or an abort: all warps leave together
         const bool more = paged_take(bars, i, it, abort_flag, lane);
-        if (soft_any<ST>(!more)) break;
-        const int slot = i & 1, ng = (it.rows + 15) >> 4;
-        const bool qok = warp_wait(smem_u32(&bars->q_full[slot]), (i >> 1) & 1, abort_flag);
-        uint64_t l[GPW][NR / 2];         // this key's part of the row sums, relative to M
-        float o[GPW][NR];                // dim r of the rows, relative to M
+        if (soft_any(w, !more)) break;
+        const int slot = i & 1, ng = (it.rows + 15) >> 4, na = C::groups(w, ng);
+        const int tb = it.t0 + (C::SPLIT ? w : 0);
+        bool ok = warp_wait(smem_u32(&bars->q_full[slot]), (i >> 1) & 1, abort_flag);
+        uint64_t l[GPW][NR / 2];         // this key's part of the row sums, relative to m
+        float o[GPW][NR];                // dim r of the rows, relative to m of the groups added
 #pragma unroll
         for (int x = 0; x < GPW; ++x)
 #pragma unroll
@@ -617,30 +667,37 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                 l[x][k / 2] = 0;
                 o[x][k] = 0.f;
             }
-        if (tid < C::R) bars->top[tid] = -INFINITY;
-        // ids two tiles ahead, scales one
-        const int pages = (it.L + (1 << p.shift) - 1) >> p.shift;
-        auto id_of = [&](int t) {
-            const int key = t * kRows + r;
-            return t < it.t1 && (key >> p.shift) < pages ? page_id(p, it.entry, key >> p.shift, false) : -1;
+        if (r < C::R) {
+            bars->top[w][r] = -INFINITY;
+            bars->nm[w][r] = kNone;
+        }
+        // O^T of a group of P V that is done, added and brought to another reference
+        auto add_group = [&](uint32_t buf, bool scaled) {
+#pragma unroll
+            for (int x = 0; x < GPW; ++x) {
+                if (x >= na) continue;
+                uint32_t s[2 * NR];
+                ld_terms<NR>(tmem + (2 + buf) * C::COLS + 32 * x, s);
+                const float *am = &bars->am[w][16 * C::group(w, x)];
+#pragma unroll
+                for (int k = 0; k < NR; ++k) {
+                    o[x][k] += fmaf(__uint_as_float(s[NR + k]), 0.0625f, __uint_as_float(s[k]));
+                    if (scaled) o[x][k] *= am[k];
+                }
+            }
+            tc_fence_before();
         };
-        auto scale_of = [&](const float *s, int id) { return id >= 0 ? s[(int64_t)id * p.H_k + it.g] : 1.f; };
-        const int id0 = id_of(it.t0);
-        int id1 = id_of(it.t0 + 1);
-        float sk = scale_of(p.k_scale, id0), sv = scale_of(p.v_scale, id0);
         int since = kGroupTiles;         // tiles of the group so far
-        bool ok = qok, first = true;
-        for (int t = it.t0; t < it.t1; ++t, ++j) {
-            const float sk1 = scale_of(p.k_scale, id1), sv1 = scale_of(p.v_scale, id1);
-            id1 = id_of(t + 2);
-            const uint32_t b = j & 1;
+        bool first = true;
+        if (na == 0) n += it.t1 - it.t0; // a pipeline without groups has no tiles
+        for (int t = tb; na > 0 && t < it.t1; t += kStep, ++c, ++n) {
+            const uint32_t b = c & 1, st = ring_stage<C>(w, n);
             const int key = t * kRows + r, nk = it.L - t * kRows;
-            ok = warp_wait(smem_u32(&bars->s_full[b]), (j >> 1) & 1, abort_flag) && ok;
-            if (nk < kRows && wg == 0) {
-                // rows past the keys (of an earlier tile, or of nothing): V is
-                // zeroed so that P = 0 contributes 0
-                const uint32_t st = j % C::NS;
-                ok = warp_wait(smem_u32(&bars->kv_full[st]), (j / C::NS) & 1, abort_flag) && ok;
+            ok = warp_wait(smem_u32(&bars->s_full[w][b]), (c >> 1) & 1, abort_flag) && ok;
+            ok = warp_wait(smem_u32(&bars->kv_full[st]), ring_parity<C>(n), abort_flag) && ok;   // the scales, and V
+            if (nk < kRows) {
+                // rows past the keys (of an earlier tile, or of nothing): V is zeroed so that P = 0 contributes
+                // 0 (by both pipelines where both use the tile: each before its own P V)
                 if (ok && r >= nk) {
                     proxy_fence();
                     uint4 *v = reinterpret_cast<uint4 *>(smem + C::OFF_KV + st * C::STAGE + kPanelBytes + r * 128);
@@ -650,82 +707,72 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                 __syncwarp();
             }
             tc_fence_after();
-            const float svc = fminf(fmaxf(sv, kLeastScale), kMostScale);
-            const float a = p.c * sk, lsv = log2f(svc);
+            const float sv = fminf(fmaxf(bars->scale[st][1][r >> p.shift], kLeastScale), kMostScale);
+            const float a = p.c * bars->scale[st][0][r >> p.shift], lsv = log2f(sv);
             const uint64_t a2 = pack_f2(a, a), lsv2 = pack_f2(lsv, lsv);
             const bool masked = nk < kRows || t * kRows + kRows - 1 > it.base + it.tok0;
-            uint64_t y[GPW][NR / 2];     // scores in log2 units, with the value's scale
-#pragma unroll
-            for (int x = 0; x < GPW; ++x) {
-                const int grp = wg + C::WG * x;
-                if (grp >= ng) continue;
-                uint32_t s[2 * NR];
-                ld_terms<NR>(lane_base + b * C::COLS + 32 * grp, s);
-                const float4 *g4 = reinterpret_cast<const float4 *>(&bars->qscale[slot][16 * grp]);
-#pragma unroll
-                for (int k = 0; k < NR; k += 4) {
-                    const float4 gg = g4[k / 4];
-                    const uint64_t t0 = fma_f2(pack_f2(__uint_as_float(s[NR + k]), __uint_as_float(s[NR + k + 1])), sixteenth,
-                                               pack_f2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
-                    const uint64_t t1 = fma_f2(pack_f2(__uint_as_float(s[NR + k + 2]), __uint_as_float(s[NR + k + 3])), sixteenth,
-                                               pack_f2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])));
-                    y[x][k / 2] = fma_f2(t0, mul_f2(pack_f2(gg.x, gg.y), a2), lsv2);
-                    y[x][k / 2 + 1] = fma_f2(t1, mul_f2(pack_f2(gg.z, gg.w), a2), lsv2);
-                }
-                if (masked) {
-                    const int4 *lim = reinterpret_cast<const int4 *>(&bars->lim[slot][16 * grp]);
-#pragma unroll
-                    for (int k = 0; k < NR; k += 4) {
-                        const int4 m = lim[k / 4];
-                        float u, v;
-                        unpack_f2(y[x][k / 2], u, v);
-                        y[x][k / 2] = pack_f2(r < nk && key <= m.x ? u : -INFINITY, r < nk && key <= m.y ? v : -INFINITY);
-                        unpack_f2(y[x][k / 2 + 1], u, v);
-                        y[x][k / 2 + 1] = pack_f2(r < nk && key <= m.z ? u : -INFINITY, r < nk && key <= m.w ? v : -INFINITY);
-                    }
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[b]));
-            // does a score outgrow the group's reference?
-            bool fresh = since == kGroupTiles, out = false;
-            if (!fresh) {
+            bool fresh = since == kGroupTiles;
+            uint64_t e[GPW][NR / 2];     // scores in log2 units, with the value's scale, over the reference
+            for (;;) {
+                float top = -INFINITY;
 #pragma unroll
                 for (int x = 0; x < GPW; ++x) {
-                    const int grp = wg + C::WG * x;
-                    if (grp >= ng) continue;
-                    float top = -INFINITY;
-                    const float4 *n4 = reinterpret_cast<const float4 *>(&bars->nm[16 * grp]);
+                    if (x >= na) continue;
+                    uint32_t s[2 * NR];
+                    ld_terms<NR>(tmem + b * C::COLS + 32 * x, s);
+                    const int row = 16 * C::group(w, x);
+                    const float4 *g4 = reinterpret_cast<const float4 *>(&bars->qscale[slot][row]);
+                    const float4 *n4 = reinterpret_cast<const float4 *>(fresh ? bars->zero : &bars->nm[w][row]);
 #pragma unroll
                     for (int k = 0; k < NR; k += 4) {
-                        const float4 nm = n4[k / 4];
+                        const float4 gg = g4[k / 4], nm = n4[k / 4];
+                        const uint64_t t0 = fma_f2(pack_f2(__uint_as_float(s[NR + k]), __uint_as_float(s[NR + k + 1])), sixteenth,
+                                                   pack_f2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
+                        const uint64_t t1 = fma_f2(pack_f2(__uint_as_float(s[NR + k + 2]), __uint_as_float(s[NR + k + 3])),
+                                                   sixteenth, pack_f2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])));
+                        e[x][k / 2] = fma_f2(t0, mul_f2(pack_f2(gg.x, gg.y), a2), add_f2(pack_f2(nm.x, nm.y), lsv2));
+                        e[x][k / 2 + 1] = fma_f2(t1, mul_f2(pack_f2(gg.z, gg.w), a2), add_f2(pack_f2(nm.z, nm.w), lsv2));
+                    }
+                    if (masked) {
+                        const int4 *lim = reinterpret_cast<const int4 *>(&bars->lim[slot][row]);
+#pragma unroll
+                        for (int k = 0; k < NR; k += 4) {
+                            const int4 m = lim[k / 4];
+                            float u, v;
+                            unpack_f2(e[x][k / 2], u, v);
+                            e[x][k / 2] = pack_f2(r < nk && key <= m.x ? u : -INFINITY, r < nk && key <= m.y ? v : -INFINITY);
+                            unpack_f2(e[x][k / 2 + 1], u, v);
+                            e[x][k / 2 + 1] = pack_f2(r < nk && key <= m.z ? u : -INFINITY, r < nk && key <= m.w ? v : -INFINITY);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < NR; k += 2) {
                         float u, v;
-                        unpack_f2(add_f2(y[x][k / 2], pack_f2(nm.x, nm.y)), u, v);
-                        top = max3(top, u, v);
-                        unpack_f2(add_f2(y[x][k / 2 + 1], pack_f2(nm.z, nm.w)), u, v);
+                        unpack_f2(e[x][k / 2], u, v);
                         top = max3(top, u, v);
                     }
-                    out |= top > kGrown;
                 }
-            }
-            if (soft_any<ST>(out || !ok)) {
-                if (soft_any<ST>(!ok)) {
+                // does a score outgrow the group's reference?  Then it begins anew here.
+                if (!soft_any(w, !ok || (!fresh && top > kGrown))) break;
+                if (soft_any(w, !ok)) {
                     ok = false;
                     break;
                 }
                 fresh = true;
             }
+            if (!ok) break;              // voted: the same in every warp
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[w][b]));
             if (fresh) {
                 // the group's reference: the tile's maximum of every row
 #pragma unroll
                 for (int x = 0; x < GPW; ++x) {
-                    const int grp = wg + C::WG * x;
-                    if (grp >= ng) continue;
+                    if (x >= na) continue;
 #pragma unroll
                     for (int k = 0; k < NR; k += 2) {
                         float u, v;
-                        unpack_f2(y[x][k / 2], u, v);
+                        unpack_f2(e[x][k / 2], u, v);
                         u = redux_max(u);
                         v = redux_max(v);
                         if (lane == 0) {
@@ -734,63 +781,58 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                         }
                     }
                 }
-                soft_sync<ST>();
-                if (tid < 16 * ng && (tid & 15) < NR) {
-                    const int grp = tid >> 4, w0 = 4 * (grp % C::WG), at = 16 * (grp / C::WG) + (tid & 15);
-                    const float top = fmaxf(fmaxf(bars->red[w0][at], bars->red[w0 + 1][at]),
-                                            fmaxf(bars->red[w0 + 2][at], bars->red[w0 + 3][at]));
-                    const float m = top - kBias, before = first ? -INFINITY : -bars->nm[tid], M = bars->top[tid];
-                    const float Mn = fmaxf(M, m);
-                    // without a key every factor is 0, and the next key is above the reference
-                    auto factor = [&](float x) { return x < -0.5f * kNone ? 0.f : ex2(x - Mn); };
-                    bars->am[tid] = factor(M);
-                    bars->beta[tid] = factor(before);
-                    bars->w[tid] = factor(m);
-                    bars->top[tid] = Mn;
-                    bars->nm[tid] = m == -INFINITY ? kNone : -m;
+                soft_sync(w);
+                if (r < 16 * na && (r & 15) < NR) {
+                    const int row = 16 * C::group(w, r >> 4) + (r & 15);
+                    const float top = fmaxf(fmaxf(bars->red[4 * w][r], bars->red[4 * w + 1][r]),
+                                            fmaxf(bars->red[4 * w + 2][r], bars->red[4 * w + 3][r]));
+                    const float M = bars->top[w][row], m = fmaxf(top - kBias, M - kBelow), nm = bars->nm[w][row];
+                    bars->top[w][row] = fmaxf(M, m);
+                    // without a key so far: nothing to keep, and the next key is above the reference
+                    bars->am[w][row] = nm == kNone ? 0.f : ex2(-nm - m);
+                    bars->nm[w][row] = m == -INFINITY ? kNone : -m;
                 }
-                soft_sync<ST>();
+                soft_sync(w);
 #pragma unroll
                 for (int x = 0; x < GPW; ++x) {
-                    const int grp = wg + C::WG * x;
-                    if (grp >= ng) continue;
+                    if (x >= na) continue;
+                    const int row = 16 * C::group(w, x);
 #pragma unroll
-                    for (int k = 0; k < NR; k += 2)
-                        l[x][k / 2] = mul_f2(l[x][k / 2], pack_f2(bars->am[16 * grp + k], bars->am[16 * grp + k + 1]));
+                    for (int k = 0; k < NR; k += 2) {
+                        const uint64_t nm2 = *reinterpret_cast<const uint64_t *>(&bars->nm[w][row + k]);
+                        l[x][k / 2] = mul_f2(l[x][k / 2], *reinterpret_cast<const uint64_t *>(&bars->am[w][row + k]));
+                        e[x][k / 2] = add_f2(e[x][k / 2], nm2);
+                    }
                 }
                 ++par;
                 since = 0;
             }
             ++since;
             // weights, their sums, and both terms into P^T
-            const float isv = 1.f / svc;
+            const float isv = 1.f / sv;
             const uint64_t isv2 = pack_f2(isv, isv);
-            uint8_t *prow = smem + C::OFF_P + b * C::P_BYTES + r * C::P_ROW;
-            const uint32_t swz = C::NG == 1 ? (r >> 2) & 1 : r & 7;
+            uint8_t *prow = pbuf + b * C::P_BYTES + r * C::P_ROW;
+            const uint32_t swz = GPW == 1 ? (r >> 2) & 1 : (r >> 1) & 3;
 #pragma unroll
             for (int x = 0; x < GPW; ++x) {
-                const int grp = wg + C::WG * x;
-                if (grp >= ng) continue;
-                const float4 *n4 = reinterpret_cast<const float4 *>(&bars->nm[16 * grp]);
-                const float4 *w4 = reinterpret_cast<const float4 *>(&bars->w[16 * grp]);
+                if (x >= na) continue;
                 uint32_t hi[NR / 4], mid[NR / 4];
 #pragma unroll
                 for (int k = 0; k < NR; k += 4) {
-                    const float4 nm = n4[k / 4], w = w4[k / 4];
-                    float e[4];
-                    unpack_f2(add_f2(y[x][k / 2], pack_f2(nm.x, nm.y)), e[0], e[1]);
-                    unpack_f2(add_f2(y[x][k / 2 + 1], pack_f2(nm.z, nm.w)), e[2], e[3]);
+                    float v[4];
+                    unpack_f2(e[x][k / 2], v[0], v[1]);
+                    unpack_f2(e[x][k / 2 + 1], v[2], v[3]);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) e[q] = ex2(e[q]);
-                    l[x][k / 2] = fma_f2(pack_f2(e[0], e[1]), mul_f2(pack_f2(w.x, w.y), isv2), l[x][k / 2]);
-                    l[x][k / 2 + 1] = fma_f2(pack_f2(e[2], e[3]), mul_f2(pack_f2(w.z, w.w), isv2), l[x][k / 2 + 1]);
+                    for (int q = 0; q < 4; ++q) v[q] = ex2(v[q]);
+                    l[x][k / 2] = fma_f2(pack_f2(v[0], v[1]), isv2, l[x][k / 2]);
+                    l[x][k / 2 + 1] = fma_f2(pack_f2(v[2], v[3]), isv2, l[x][k / 2 + 1]);
                     uint32_t h0, h1, m0, m1;
-                    split2(e[0], e[1], h0, m0);
-                    split2(e[2], e[3], h1, m1);
-                    hi[k / 4] = h0 | (h1 << 16);
-                    mid[k / 4] = m0 | (m1 << 16);
+                    split2(v[0], v[1], h0, m0);
+                    split2(v[2], v[3], h1, m1);
+                    hi[k / 4] = __byte_perm(h0, h1, 0x5410);
+                    mid[k / 4] = __byte_perm(m0, m1, 0x5410);
                 }
-                uint8_t *ph = prow + (((2 * grp) ^ swz) << 4), *pm = prow + (((2 * grp + 1) ^ swz) << 4);
+                uint8_t *ph = prow + (((2 * x) ^ swz) << 4), *pm = prow + (((2 * x + 1) ^ swz) << 4);
                 if constexpr (NR == 16) {
                     *reinterpret_cast<uint4 *>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     *reinterpret_cast<uint4 *>(pm) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
@@ -802,50 +844,33 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                     *reinterpret_cast<uint32_t *>(pm) = mid[0];
                 }
             }
-            if (tid == 0) bars->fresh[b] = (fresh ? 1 : 0) | (int)((par & 1) << 1);
+            if (r == 0) bars->fresh[w][b] = (fresh ? 1 : 0) | (int)((par & 1) << 1);
             proxy_fence();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[b]));
-            sk = sk1;
-            sv = sv1;
+            if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[w][b]));
             if (fresh && !first) {
-                // the group before: its last P V is that of tile j - 1
-                ok = warp_wait(smem_u32(&bars->pv_done[b ^ 1]), ((j - 1) >> 1) & 1, abort_flag);
-                if (soft_any<ST>(!ok)) {
+                // the group before: its last P V is that of this pipeline's tile before
+                ok = warp_wait(smem_u32(&bars->pv_done[w][b ^ 1]), ((c - 1) >> 1) & 1, abort_flag);
+                if (soft_any(w, !ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-#pragma unroll
-                for (int x = 0; x < GPW; ++x) {
-                    const int grp = wg + C::WG * x;
-                    if (grp >= ng) continue;
-                    uint32_t s[2 * NR];
-                    ld_terms<NR>(lane_base + C::O_COL + ((par & 1) ^ 1) * C::COLS + 32 * grp, s);
-#pragma unroll
-                    for (int k = 0; k < NR; ++k)
-                        o[x][k] = o[x][k] * bars->am[16 * grp + k] +
-                                  fmaf(__uint_as_float(s[NR + k]), 0.0625f, __uint_as_float(s[k])) * bars->beta[16 * grp + k];
-                }
-                tc_fence_before();
+                add_group((par & 1) ^ 1, true);
             }
             first = false;
         }
-        if (!ok) break;                  // voted: the same in every warp
+        if (soft_any(w, !ok)) break;
 
-        // epilogue: the last group, the row sums, then O of a unit that this CTA covers alone, else a partial
-        ok = warp_wait(smem_u32(&bars->pv_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, abort_flag);
-        if (soft_any<ST>(!ok)) break;
-        tc_fence_after();
+        // epilogue: the last group and the row sums
+        if (!first) {
+            ok = warp_wait(smem_u32(&bars->pv_done[w][(c - 1) & 1]), ((c - 1) >> 1) & 1, abort_flag);
+            if (soft_any(w, !ok)) break;
+            tc_fence_after();
+            add_group(par & 1, false);
+        }
 #pragma unroll
-        for (int x = 0; x < GPW; ++x) {
-            const int grp = wg + C::WG * x;
-            if (grp >= ng) continue;
-            uint32_t s[2 * NR];
-            ld_terms<NR>(lane_base + C::O_COL + (par & 1) * C::COLS + 32 * grp, s);
-#pragma unroll
-            for (int k = 0; k < NR; ++k)
-                o[x][k] += fmaf(__uint_as_float(s[NR + k]), 0.0625f, __uint_as_float(s[k])) * bars->w[16 * grp + k];
+        for (int x = 0; x < GPW; ++x)
 #pragma unroll
             for (int k = 0; k < NR; k += 2) {
                 float u, v;
@@ -860,47 +885,91 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                     bars->red[warp][16 * x + k + 1] = v;
                 }
             }
+        soft_sync(w);
+        // this pipeline's rows: a thread each
+        const int grp = C::group(w, r >> 4), row = 16 * grp + (r & 15);
+        const bool mine = r < 16 * GPW && (r & 15) < NR && row < it.rows;
+        float sum = 0.f, m = -INFINITY;
+        if (mine) {
+            sum = (bars->red[4 * w][r] + bars->red[4 * w + 1][r]) + (bars->red[4 * w + 2][r] + bars->red[4 * w + 3][r]);
+            const float nm = bars->nm[w][row];
+            m = nm == kNone ? -INFINITY : -nm;
         }
-        tc_fence_before();
-        soft_sync<ST>();
+        const bool two = C::SPLIT && it.t1 - it.t0 > 1;      // pipeline 1 has an O of the same rows
+        if (C::SPLIT && w == 1) {
+            if (mine) {
+                bars->stat_m[row] = m;
+                bars->stat_l[row] = sum;
+            }
+            if (two) {
+#pragma unroll
+                for (int x = 0; x < GPW; ++x)
+#pragma unroll
+                    for (int k = 0; k < NR; ++k) scratch[(16 * x + k) * kD + r] = o[x][k];
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&bars->stat_full));
+                mbar_arrive(smem_u32(&bars->q_empty[slot]));
+            }
+            // pipeline 0 reads this one's O: not overwritten before it has
+            ok = warp_wait(smem_u32(&bars->epi_done), i & 1, abort_flag);
+            if (soft_any(w, !ok)) break;
+            continue;
+        }
+        if (C::SPLIT) {
+            ok = warp_wait(smem_u32(&bars->stat_full), i & 1, abort_flag);
+            if (soft_any(w, !ok)) break;
+        }
         // slot 2 * cta: a unit that an earlier CTA began; 2 * cta + 1: one that begins here
         const bool whole = it.t1 - it.t0 == it.nt;
         const int part = 2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
-        if (tid == 0 && !whole) {
+        if (w == 0 && r == 0 && !whole) {
             parts |= it.t0 == 0 ? 2 : 1;
             p.meta[part] = PagedMeta{it.row0, it.h0, it.rows, it.t1 == it.nt};
         }
-        if (tid < it.rows && (tid & 15) < NR) {
-            const int grp = tid >> 4, w0 = 4 * (grp % C::WG), at = 16 * (grp / C::WG) + (tid & 15);
-            const float sum = (bars->red[w0][at] + bars->red[w0 + 1][at]) + (bars->red[w0 + 2][at] + bars->red[w0 + 3][at]);
+        if (mine) {
+            float f0 = 1.f, f1 = 0.f;
+            if (two) {
+                const float m1 = bars->stat_m[row], mm = fmaxf(m, m1);
+                f0 = m == -INFINITY ? 0.f : ex2(m - mm);
+                f1 = m1 == -INFINITY ? 0.f : ex2(m1 - mm);
+                sum = sum * f0 + bars->stat_l[row] * f1;
+                m = mm;
+            }
             const bool empty = sum == 0.f;                    // the row saw no key
-            const float lse = empty ? -INFINITY : (bars->top[tid] + log2f(sum)) * kLn2;
-            bars->inv[tid] = empty ? 0.f : (whole ? p.out_scale : 1.f) / sum;
-            if (!whole) p.part_lse[(int64_t)part * C::R + tid] = lse;
-            else if (p.lse) p.lse[bars->at[slot][tid]] = lse;
+            const float lse = empty ? -INFINITY : (m + log2f(sum)) * kLn2;
+            const float inv = empty ? 0.f : (whole ? p.out_scale : 1.f) / sum;
+            bars->top[w][row] = f0 * inv;
+            if (C::SPLIT) bars->other[row] = f1 * inv;
+            if (!whole) p.part_lse[(int64_t)part * C::R + row] = lse;
+            else if (p.lse) p.lse[bars->at[slot][row]] = lse;
         }
-        soft_sync<ST>();
+        soft_sync(w);
 #pragma unroll
-        for (int x = 0; x < GPW; ++x) {
-            const int grp = wg + C::WG * x;
+        for (int x = 0; x < GPW; ++x)
 #pragma unroll
             for (int k = 0; k < NR; ++k) {
-                const int row = 16 * grp + k;
-                if (row >= it.rows) continue;
-                const float v = bars->inv[row] == 0.f ? 0.f : o[x][k] * bars->inv[row];
+                const int rr = 16 * C::group(w, x) + k;
+                if (rr >= it.rows) continue;
+                const float f0 = bars->top[w][rr];
+                float v = f0 == 0.f ? 0.f : o[x][k] * f0;
+                if (two) v = fmaf(scratch[rr * kD + r], bars->other[rr], v);
                 if (!whole) {
-                    p.part_o[((int64_t)part * C::R + row) * kD + r] = v;
+                    p.part_o[((int64_t)part * C::R + rr) * kD + r] = v;
                 } else {
-                    uint16_t *dst = static_cast<uint16_t *>(p.o) + (int64_t)bars->at[slot][row] * kD + r;
+                    uint16_t *dst = static_cast<uint16_t *>(p.o) + (int64_t)bars->at[slot][rr] * kD + r;
                     *dst = (uint16_t)pack2<C::BF>(v, 0.f);
                 }
             }
-        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->q_empty[slot]));
-        soft_sync<ST>();                 // the scratch rows may be rewritten after this
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&bars->q_empty[slot]));
+            if (C::SPLIT) mbar_arrive(smem_u32(&bars->epi_done));
+        }
+        soft_sync(w);                    // the scratch rows may be rewritten after this
     }
-    if (tid == 0)                        // empty slots; one that is missing (a CTA that gave up) also ends its unit
+    if (threadIdx.x == 0)                // empty slots; one that is missing (a CTA that gave up) also ends its unit
         for (int s = 0; s < 2; ++s)
             if (!(parts >> s & 1)) p.meta[2 * blockIdx.x + s] = PagedMeta{0, 0, 0, 1};
 }
@@ -915,26 +984,31 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG>::THREADS), 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(&bars->q_full[s]), 2);            // the q warps
-            mbar_init(smem_u32(&bars->q_empty[s]), 1 + C::SW);   // the MMA warp's commit and the softmax warps
-            mbar_init(smem_u32(&bars->s_full[s]), 1);
-            mbar_init(smem_u32(&bars->s_free[s]), C::SW);
-            mbar_init(smem_u32(&bars->p_full[s]), C::SW);
-            mbar_init(smem_u32(&bars->pv_done[s]), 1);
+            mbar_init(smem_u32(&bars->q_full[s]), 1);
+            mbar_init(smem_u32(&bars->q_empty[s]), 2 + C::SW);   // the MMA warps' commits and the softmax warps
+            mbar_init(smem_u32(&bars->drain[s]), 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(smem_u32(&bars->s_full[s][b]), 1);
+                mbar_init(smem_u32(&bars->s_free[s][b]), 4);
+                mbar_init(smem_u32(&bars->p_full[s][b]), 4);
+                mbar_init(smem_u32(&bars->pv_done[s][b]), 1);
+            }
         }
-        mbar_init(smem_u32(&bars->drain), 1);
+        mbar_init(smem_u32(&bars->stat_full), 4);
+        mbar_init(smem_u32(&bars->epi_done), 4);
         for (int s = 0; s < C::NS; ++s) {
-            mbar_init(smem_u32(&bars->kv_full[s]), 1);
-            mbar_init(smem_u32(&bars->kv_empty[s]), 1);
+            mbar_init(smem_u32(&bars->kv_full[s]), 33);          // the producer's bytes, and its lanes' scales
+            mbar_init(smem_u32(&bars->kv_empty[s]), C::SPLIT ? 1 : 2);   // the MMA warps that use a tile
         }
         for (int s = 0; s < kPagedItems; ++s) {
             mbar_init(smem_u32(&bars->item_full[s]), 1);
             mbar_init(smem_u32(&bars->item_empty[s]), C::SW + 3);   // the softmax, q and MMA warps
         }
+        for (int k = 0; k < 16; ++k) bars->zero[k] = 0.f;
         bars->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == C::MMA) {
+    if (warp == C::MMA) {                // pipeline 0's issuer
         tmem_alloc(smem_u32(&bars->tmem_base), C::TMEM_COLS);
         tmem_relinquish();
     }
@@ -956,9 +1030,9 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG>::THREADS), 1)
     // for this grid's completion before it reads the partials
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp < C::SW) paged_softmax<C, NR>(p, smem, bars, tmem, warp, lane);
-    else if (warp < C::PROD) paged_queries<C>(p, smem, bars, warp - C::QW, lane);
+    else if (warp == C::QW) paged_queries<C>(p, smem, bars, lane);
     else if (warp == C::PROD) paged_producer<C>(p, cur, gate, &tmK, &tmV, smem, bars, lane);
-    else paged_mma<C>(smem, bars, tmem, lane);
+    else paged_mma<C>(smem, bars, tmem, warp - C::MMA, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -1035,23 +1109,23 @@ __global__ void __launch_bounds__(32 * kPagedMergeWarps) fmha_paged_merge_kernel
 // Host side
 // ---------------------------------------------------------------------------
 
-// Query rows of a unit: one group of 16 where a sequence's rows of a kv head
-// fit it, else four.
-int paged_rows(int64_t max_q, int G) { return max_q * G <= 16 ? 16 : 64; }
+// Query rows of a unit: as many groups of 16 as a sequence's rows of a kv head
+// fill, one, two or (also for more) four.
+int paged_rows(int64_t max_q, int G) { return max_q * G <= 16 ? 16 : max_q * G <= 32 ? 32 : 64; }
 
 using PagedKernel = void (*)(CUtensorMap, CUtensorMap, PagedParams);
-template <bool BF>
-PagedKernel paged_kernel(int rows, int per_unit) {
-    if (rows == 64) return fmha_paged_kernel<BF, 4, 16>;
-    return per_unit <= 4 ? fmha_paged_kernel<BF, 1, 4> : per_unit <= 8 ? fmha_paged_kernel<BF, 1, 8> : fmha_paged_kernel<BF, 1, 16>;
+struct PagedLaunch {
+    PagedKernel kernel;
+    int smem, threads;
+};
+template <bool BF, int NG, int NR>
+PagedLaunch paged_launch() {
+    return {fmha_paged_kernel<BF, NG, NR>, PagedCfg<BF, NG>::SMEM_BYTES, PagedCfg<BF, NG>::THREADS};
 }
 template <bool BF>
-int paged_smem(int rows) {
-    return rows == 64 ? PagedCfg<BF, 4>::SMEM_BYTES : PagedCfg<BF, 1>::SMEM_BYTES;
-}
-template <bool BF>
-int paged_threads(int rows) {
-    return rows == 64 ? PagedCfg<BF, 4>::THREADS : PagedCfg<BF, 1>::THREADS;
+PagedLaunch paged_kernel(int rows, int per_unit) {
+    return rows == 64 ? paged_launch<BF, 4, 16>() : rows == 32 ? paged_launch<BF, 2, 16>()
+           : per_unit <= 4 ? paged_launch<BF, 1, 4>() : per_unit <= 8 ? paged_launch<BF, 1, 8>() : paged_launch<BF, 1, 16>();
 }
 
 }  // namespace
@@ -1158,10 +1232,9 @@ extern "C" int fmha_page_fwd(fmha_tensor q, fmha_tensor k_pages, fmha_tensor v_p
     }
     const bool bf = dt == FMHA_BF16;
     const int per_unit = imin(R, G * imin(p.tau, max_q));
-    auto kern = bf ? paged_kernel<true>(R, per_unit) : paged_kernel<false>(R, per_unit);
-    const int smem = bf ? paged_smem<true>(R) : paged_smem<false>(R), threads = bf ? paged_threads<true>(R) : paged_threads<false>(R);
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return cuda_failed();
-    kern<<<p.ncta, threads, smem, stream>>>(tm[0], tm[1], p);
+    const PagedLaunch k = bf ? paged_kernel<true>(R, per_unit) : paged_kernel<false>(R, per_unit);
+    if (cudaFuncSetAttribute(k.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, k.smem) != cudaSuccess) return cuda_failed();
+    k.kernel<<<p.ncta, k.threads, k.smem, stream>>>(tm[0], tm[1], p);
     if (cudaGetLastError() != cudaSuccess) return FMHA_ERR_CUDA;
 
     cudaLaunchConfig_t cfg = {};
