@@ -23,16 +23,17 @@
 // and a unit one such group or up to four (prompt chunks), of one kv head.
 //
 // e4m3 ends at 448 and 2^-9, so P' = exp2(y_j - m) with y_j = x_j log2(e) +
-// log2(v_scale) is relative to a reference m per row, and products are
-// accumulated in TMEM only over a group of at most eight key tiles with the
-// same reference: the next group sets its own, from the maximum of its first
-// tile, and the O^T of the one before is added in fp32 registers, from one of
-// two TMEM buffers, under the softmax of the next.  A score that outgrows the
-// reference opens a new group early.  So a long context of small weights behind
-// a large one is not rounded to nothing: of a group's weight, what e4m3's
-// smallest steps lose is 2^-8 at most (1024 weights of 2^-14 where the largest is
-// 2^4 or more), or 2^-42 a key of the largest weight of all (a reference is not
-// more than 2^24 below the highest so far, which keeps fp32 in its range).
+// log2(v_scale) is relative to a reference m per row, that a group of at most
+// eight key tiles has: the next group sets its own, up or down, from the maximum
+// of its first tile, and O^T in TMEM and the row sums are brought to it.  A
+// score that outgrows the reference opens a new group early (of 64 rows some do
+// in every sixth tile; a reference up to 2^2 higher, if one was that high before,
+// makes these fewer).
+// So a long context of small weights behind a large one is not rounded to
+// nothing: of a group's weight, what e4m3's smallest steps lose is 2^-6 at most
+// (1024 weights of 2^-14 where the largest is 2^2 or more), or 2^-42 a key of the
+// largest weight of all (a reference is not more than 2^24 below the highest so
+// far, which keeps fp32 in its range).
 // Row sums are of the unrounded weights, in fp32.
 //
 // Work: the key tiles of all units form one sequence cut evenly over the CTAs,
@@ -56,6 +57,7 @@ constexpr int kPagedItems = 4;           // work items published ahead
 constexpr int kGroupTiles = 8;           // key tiles with one reference
 constexpr float kBias = 4.f;             // log2 of a group's largest P' where its reference is set
 constexpr float kGrown = 8.75f;          // and how far it may grow: e4m3 ends at 2^8.8
+constexpr float kAbove = 2.f;            // how far it may be set higher, to an earlier one
 constexpr float kBelow = 24.f;           // how far a reference may be below the highest before it
 constexpr int kStagesPaged = 6;
 constexpr int kPagedBars = 6144;         // barrier block
@@ -67,13 +69,13 @@ struct PagedCfg {
     static constexpr bool BF = BF_;
     static constexpr int NG = NG_;                            // groups of 16 query rows a unit holds
     static constexpr int R = 16 * NG;                         // its rows
-    static constexpr bool SPLIT = NG <= 2;                    // the pipelines share tiles out, else groups
+    static constexpr bool SPLIT = NG == 1;                    // the pipelines share tiles out, else groups
     static constexpr int GPW = SPLIT ? NG : NG / 2;           // groups of a pipeline
     static constexpr int SW = 8;                              // softmax warps
     static constexpr int QW = SW, PROD = SW + 1, MMA = SW + 2;   // q warp, producer, two MMA issuers
     static constexpr int THREADS = 32 * (SW + 4);
     static constexpr int COLS = 32 * GPW;                     // of a pipeline's S^T and O^T
-    static constexpr int PIPE_COLS = 4 * COLS;                // TMEM: two S^T, then two O^T
+    static constexpr int PIPE_COLS = 4 * COLS;                // TMEM: two S^T, then O^T (and nothing, to a power of two)
     static constexpr int TMEM_COLS = 2 * PIPE_COLS;
     static constexpr int P_ROW = COLS;                        // bytes of a key's P^T row
     static constexpr int P_BYTES = kRows * P_ROW;
@@ -83,16 +85,17 @@ struct PagedCfg {
     static constexpr int OFF_P = 2 * Q_BYTES;                 // two buffers a pipeline
     static constexpr int OFF_KV = OFF_P + 4 * P_BYTES;
     static constexpr int NS_FIT = (226 * 1024 - kPagedBars - OFF_KV) / STAGE;
-    static constexpr int NS = (NS_FIT < kStagesPaged ? NS_FIT : kStagesPaged) & ~1;
+    static constexpr int NS = NS_FIT < kStagesPaged ? NS_FIT : kStagesPaged;
     static constexpr int RING = SPLIT ? NS / 2 : NS;          // stages of a ring
     static constexpr int OFF_BARS = OFF_KV + NS * STAGE;
     static constexpr int SMEM_BYTES = OFF_BARS + kPagedBars + 1024;   // 1 KB alignment
     static_assert(SMEM_BYTES <= 227 * 1024 && OFF_KV % 1024 == 0 && OFF_P % 1024 == 0, "shared memory");
+    static_assert(!SPLIT || NS % 2 == 0, "a ring a pipeline");
     static_assert(!SPLIT || 2 * P_BYTES >= R * kD * 4, "pipeline 1 hands its O over in its P^T buffers");
 
     static __device__ __forceinline__ int group(int w, int x) { return SPLIT ? x : w + 2 * x; }   // x-th of pipeline w
     static __device__ __forceinline__ int groups(int w, int ng) { return SPLIT ? ng : (ng - w + 1) >> 1; }
-    static __device__ __forceinline__ int position(int grp) { return SPLIT ? grp : 2 * (grp & 1) + (grp >> 1); }   // in q's tile
+    static __device__ __forceinline__ int position(int grp) { return SPLIT ? grp : GPW * (grp & 1) + (grp >> 1); }   // in q's tile
 };
 
 struct PagedMeta {                       // whose partial a workspace slot holds
@@ -129,7 +132,6 @@ struct PagedBars {
     PagedItem item[kPagedItems];
     uint32_t tmem_base;
     int abort;
-    int fresh[2][2];                     // of a P^T buffer's tile: it begins a group; and (bit 1) the group's O^T buffer
     alignas(16) float zero[16];
     alignas(16) float scale[kStagesPaged][2][8];   // k_scale, v_scale of a stage's pages
     alignas(16) float qscale[2][64];     // of a q slot's rows: 2^k,
@@ -166,12 +168,12 @@ __device__ __forceinline__ float redux_max(float x) {
     return y;
 }
 
-// Both terms' columns of NR rows of a group: hi[NR], mid[NR]
+// Both terms' columns of NR rows of a group: first[NR], second[NR]; and the wait
+// for them (which holds back other loads: hoisted above it they took too many registers).
 template <int NR>
 __device__ __forceinline__ void ld_terms(uint32_t taddr, uint32_t (&r)[2 * NR]) {
     if constexpr (NR == 16) {
         tmem_ld32(taddr, r);
-        tmem_wait_ld(r);
     } else if constexpr (NR == 8) {
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -179,7 +181,6 @@ __device__ __forceinline__ void ld_terms(uint32_t taddr, uint32_t (&r)[2 * NR]) 
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                      : "r"(taddr + 16));
-        tmem_wait_ld16(r);
     } else {
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -187,11 +188,66 @@ __device__ __forceinline__ void ld_terms(uint32_t taddr, uint32_t (&r)[2 * NR]) 
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                      : "r"(taddr + 16));
-        asm volatile("tcgen05.wait::ld.sync.aligned;"
-                     : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
-                     :
+    }
+}
+template <int NR>
+__device__ __forceinline__ void st_terms(uint32_t taddr, const uint32_t (&r)[2 * NR]) {
+    if constexpr (NR == 16) {
+        tmem_st16(taddr, *reinterpret_cast<const uint32_t(*)[16]>(r));
+        tmem_st16(taddr + 16, *reinterpret_cast<const uint32_t(*)[16]>(r + 16));
+    } else if constexpr (NR == 8) {
+        tmem_st8(taddr, *reinterpret_cast<const uint32_t(*)[8]>(r));
+        tmem_st8(taddr + 16, *reinterpret_cast<const uint32_t(*)[8]>(r + 8));
+    } else {
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                     "r"(r[2]), "r"(r[3])
+                     : "memory");
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr + 16), "r"(r[4]), "r"(r[5]),
+                     "r"(r[6]), "r"(r[7])
                      : "memory");
     }
+}
+template <int NR>
+__device__ __forceinline__ void wait_terms(uint32_t (&r)[2 * NR]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+    if constexpr (NR >= 8)
+        asm volatile("" : "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+    if constexpr (NR >= 16) {
+        asm volatile("" : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]));
+        asm volatile("" : "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+    }
+}
+
+// Bounded waits as in fmha_cache.cuh, but with a hint that lets the hardware
+// suspend the warp for up to 20 us: most of a CTA's warps wait most of the time,
+// and polling took as many issue slots as the softmax.
+__device__ __forceinline__ bool hinted_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ bool hinted_slow(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    const unsigned long long t0 = globaltimer();
+    for (;;) {
+        if (hinted_try(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (globaltimer() - t0 > g_wait_ns) {
+            *abort_flag = 1;
+            atomicExch(&g_status, FMHA_ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    const bool r = hinted_try(bar, parity) || hinted_slow(bar, parity, abort_flag);
+    return __all_sync(0xffffffffu, r);
 }
 
 // Two weights as two e4m3 terms each (first weight in the low byte): p = hi +
@@ -351,7 +407,7 @@ __device__ bool paged_next(const PagedParams &p, PagedCursor &cur, PagedItem &it
 
 __device__ __forceinline__ bool paged_take(PagedBars *bars, uint32_t i, PagedItem &it, volatile int *abort_flag, int lane) {
     const uint32_t st = i % kPagedItems;
-    if (!warp_wait(smem_u32(&bars->item_full[st]), (i / kPagedItems) & 1, abort_flag)) return false;
+    if (!wait_all(smem_u32(&bars->item_full[st]), (i / kPagedItems) & 1, abort_flag)) return false;
     it = bars->item[st];
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[st]));
@@ -386,7 +442,7 @@ __device__ void paged_producer(const PagedParams &p, PagedCursor &cur, int gate,
     const int P = 1 << p.shift, per = kRows >> p.shift;       // pages of a tile
     auto publish = [&](uint32_t i, const PagedItem &it) -> bool {
         const uint32_t st = i % kPagedItems;
-        if (i >= kPagedItems && !warp_wait(smem_u32(&bars->item_empty[st]), (i / kPagedItems - 1) & 1, abort_flag)) return false;
+        if (i >= kPagedItems && !wait_all(smem_u32(&bars->item_empty[st]), (i / kPagedItems - 1) & 1, abort_flag)) return false;
         if (lane == 0) {
             bars->item[st] = it;
             mbar_arrive(smem_u32(&bars->item_full[st]));
@@ -411,7 +467,7 @@ __device__ void paged_producer(const PagedParams &p, PagedCursor &cur, int gate,
             const int ahead = id_of(t + 1);
             const int x = C::SPLIT ? (t - it.t0) & 1 : 0;
             const uint32_t n = x ? fill[1] : fill[0], st = ring_stage<C>(x, n);
-            if (n >= C::RING && !warp_wait(smem_u32(&bars->kv_empty[st]), ring_parity<C>(n) ^ 1, abort_flag)) {
+            if (n >= C::RING && !wait_all(smem_u32(&bars->kv_empty[st]), ring_parity<C>(n) ^ 1, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -451,11 +507,11 @@ __device__ void paged_producer(const PagedParams &p, PagedCursor &cur, int gate,
     for (int x = 0; x < (C::SPLIT ? 2 : 1); ++x)
         for (uint32_t n = fill[x] > C::RING ? fill[x] - C::RING : 0; n < fill[x]; ++n) {
             const uint32_t st = ring_stage<C>(x, n);
-            if (ok) ok = warp_wait(smem_u32(&bars->kv_empty[st]), ring_parity<C>(n), abort_flag);
+            if (ok) ok = wait_all(smem_u32(&bars->kv_empty[st]), ring_parity<C>(n), abort_flag);
             if (!ok) mbar_wait_drain(smem_u32(&bars->kv_full[st]), ring_parity<C>(n));
         }
     for (uint32_t i = qn > 2 ? qn - 2 : 0; ok && i < qn; ++i)
-        ok = warp_wait(smem_u32(&bars->q_empty[i & 1]), (i >> 1) & 1, abort_flag);
+        ok = wait_all(smem_u32(&bars->q_empty[i & 1]), (i >> 1) & 1, abort_flag);
 }
 
 // One warp: an item's rows of q as e4m3 terms in shared memory, and what the
@@ -466,7 +522,7 @@ __device__ void paged_queries(const PagedParams &p, uint8_t *smem, PagedBars *ba
     PagedItem it;
     for (uint32_t i = 0; paged_take(bars, i, it, abort_flag, lane); ++i) {
         const int slot = i & 1;
-        if (i >= 2 && !warp_wait(smem_u32(&bars->q_empty[slot]), ((i >> 1) - 1) & 1, abort_flag)) break;
+        if (i >= 2 && !wait_all(smem_u32(&bars->q_empty[slot]), ((i >> 1) - 1) & 1, abort_flag)) break;
         uint8_t *qs = smem + slot * C::Q_BYTES;
         const int rows = (it.rows + 15) & ~15;
         for (int r0 = 0; r0 < rows; r0 += 8) {
@@ -554,37 +610,36 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
     uint32_t c = 0, m = 0;               // tiles of the ring so far, tiles of MMAs so far
     bool ok = true;
     PagedItem it;
-    auto issue_pv = [&](uint32_t mm, uint32_t st, int na) -> bool {
+    auto issue_pv = [&](uint32_t mm, uint32_t st, int na, bool begins) -> bool {
         const uint32_t b = mm & 1;
-        if (!warp_wait(smem_u32(&bars->p_full[w][b]), (mm >> 1) & 1, abort_flag)) return false;
+        if (!wait_all(smem_u32(&bars->p_full[w][b]), (mm >> 1) & 1, abort_flag)) return false;
         tc_fence_after();
-        const int f = *reinterpret_cast<volatile int *>(&bars->fresh[w][b]);
         const uint32_t idesc = paged_idesc(32 * na, true);
         const uint64_t v = v0 + ((st * C::STAGE) >> 4), pt = p0 + ((b * C::P_BYTES) >> 4);
-        const uint32_t o_tm = tmem + (2 + (f >> 1)) * C::COLS;
+        const uint32_t o_tm = tmem + 2 * C::COLS;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)   // 32 keys
-            mma_ss<true>(o_tm, v + ((kk * 32 * 128) >> 4), pt + ((kk * 32 * C::P_ROW) >> 4), idesc, kk > 0 || !(f & 1) ? 1u : 0u);
+            mma_ss<true>(o_tm, v + ((kk * 32 * 128) >> 4), pt + ((kk * 32 * C::P_ROW) >> 4), idesc, kk > 0 || !begins ? 1u : 0u);
         tc_commit(smem_u32(&bars->pv_done[w][b]));
         tc_commit(smem_u32(&bars->kv_empty[st]));
         return true;
     };
     for (uint32_t i = 0; ok && paged_take(bars, i, it, abort_flag, lane); ++i) {
         const int slot = i & 1, na = C::groups(w, (it.rows + 15) >> 4);
-        if (!warp_wait(smem_u32(&bars->q_full[slot]), (i >> 1) & 1, abort_flag)) {
+        if (!wait_all(smem_u32(&bars->q_full[slot]), (i >> 1) & 1, abort_flag)) {
             ok = false;
             break;
         }
         const uint32_t idesc = paged_idesc(32 * na, false), idesc16 = paged_idesc(16, false);
         // this pipeline's groups are side by side in q's tile
-        const int pos0 = C::SPLIT ? 0 : 2 * w;
+        const int pos0 = C::SPLIT ? 0 : C::GPW * w;
         const uint64_t q = q0 + ((slot * C::Q_BYTES + pos0 * 32 * 128) >> 4);
         const uint64_t q3 = q0 + ((slot * C::Q_BYTES + (32 * C::NG + 16 * pos0) * 128) >> 4);
         const int tb = it.t0 + (C::SPLIT ? w : 0);
         uint32_t st_before = 0;
         for (int t = tb; t < it.t1; t += kStep, ++c) {
             const uint32_t st = ring_stage<C>(w, c), b = m & 1;
-            if (!warp_wait(smem_u32(&bars->kv_full[st]), ring_parity<C>(c), abort_flag)) {
+            if (!wait_all(smem_u32(&bars->kv_full[st]), ring_parity<C>(c), abort_flag)) {
                 ok = false;
                 break;
             }
@@ -592,7 +647,7 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
                 if (lane == 0) mbar_arrive(smem_u32(&bars->kv_empty[st]));
                 continue;
             }
-            if (m >= 2 && !warp_wait(smem_u32(&bars->s_free[w][b]), ((m >> 1) - 1) & 1, abort_flag)) {
+            if (m >= 2 && !wait_all(smem_u32(&bars->s_free[w][b]), ((m >> 1) - 1) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -610,7 +665,7 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
             }
             tc_commit(smem_u32(&bars->s_full[w][b]));
             if (t + kStep >= it.t1) tc_commit(smem_u32(&bars->q_empty[slot]));
-            if (t > tb && !issue_pv(m - 1, st_before, na)) {
+            if (t > tb && !issue_pv(m - 1, st_before, na, t - kStep == tb)) {
                 ok = false;
                 break;
             }
@@ -619,7 +674,7 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
         }
         if (!ok) break;
         if (tb >= it.t1 || na == 0) tc_commit(smem_u32(&bars->q_empty[slot]));
-        else ok = issue_pv(m - 1, st_before, na);   // the item's last P V: its epilogue does not wait for the next item's loads
+        else ok = issue_pv(m - 1, st_before, na, tb + kStep >= it.t1);   // the item's last P V: its epilogue does not wait for the next item's loads
     }
     // no tensor-core operation may be in flight when TMEM is released
     tc_commit(smem_u32(&bars->drain[w]));
@@ -648,7 +703,7 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
     uint8_t *pbuf = smem + C::OFF_P + w * 2 * C::P_BYTES;
     float *scratch = reinterpret_cast<float *>(smem + C::OFF_P + 2 * C::P_BYTES);   // pipeline 1's O at a unit's end
     const uint64_t sixteenth = pack_f2(0.0625f, 0.0625f);
-    uint32_t c = 0, n = 0, par = 0;      // tiles so far, of its ring and groups
+    uint32_t c = 0, n = 0;               // tiles so far, and of its ring
     int parts = 0;                       // bit s: slot s of this CTA holds a partial
     PagedItem it;
     for (uint32_t i = 0;; ++i) {
@@ -657,44 +712,24 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
         if (soft_any(w, !more)) break;
         const int slot = i & 1, ng = (it.rows + 15) >> 4, na = C::groups(w, ng);
         const int tb = it.t0 + (C::SPLIT ? w : 0);
-        bool ok = warp_wait(smem_u32(&bars->q_full[slot]), (i >> 1) & 1, abort_flag);
+        bool ok = wait_all(smem_u32(&bars->q_full[slot]), (i >> 1) & 1, abort_flag);
         uint64_t l[GPW][NR / 2];         // this key's part of the row sums, relative to m
-        float o[GPW][NR];                // dim r of the rows, relative to m of the groups added
 #pragma unroll
         for (int x = 0; x < GPW; ++x)
 #pragma unroll
-            for (int k = 0; k < NR; ++k) {
-                l[x][k / 2] = 0;
-                o[x][k] = 0.f;
-            }
+            for (int k = 0; k < NR / 2; ++k) l[x][k] = 0;
         if (r < C::R) {
             bars->top[w][r] = -INFINITY;
             bars->nm[w][r] = kNone;
         }
-        // O^T of a group of P V that is done, added and brought to another reference
-        auto add_group = [&](uint32_t buf, bool scaled) {
-#pragma unroll
-            for (int x = 0; x < GPW; ++x) {
-                if (x >= na) continue;
-                uint32_t s[2 * NR];
-                ld_terms<NR>(tmem + (2 + buf) * C::COLS + 32 * x, s);
-                const float *am = &bars->am[w][16 * C::group(w, x)];
-#pragma unroll
-                for (int k = 0; k < NR; ++k) {
-                    o[x][k] += fmaf(__uint_as_float(s[NR + k]), 0.0625f, __uint_as_float(s[k]));
-                    if (scaled) o[x][k] *= am[k];
-                }
-            }
-            tc_fence_before();
-        };
         int since = kGroupTiles;         // tiles of the group so far
         bool first = true;
         if (na == 0) n += it.t1 - it.t0; // a pipeline without groups has no tiles
         for (int t = tb; na > 0 && t < it.t1; t += kStep, ++c, ++n) {
             const uint32_t b = c & 1, st = ring_stage<C>(w, n);
             const int key = t * kRows + r, nk = it.L - t * kRows;
-            ok = warp_wait(smem_u32(&bars->s_full[w][b]), (c >> 1) & 1, abort_flag) && ok;
-            ok = warp_wait(smem_u32(&bars->kv_full[st]), ring_parity<C>(n), abort_flag) && ok;   // the scales, and V
+            ok = wait_all(smem_u32(&bars->s_full[w][b]), (c >> 1) & 1, abort_flag) && ok;
+            ok = wait_all(smem_u32(&bars->kv_full[st]), ring_parity<C>(n), abort_flag) && ok;   // the scales, and V
             if (nk < kRows) {
                 // rows past the keys (of an earlier tile, or of nothing): V is zeroed so that P = 0 contributes
                 // 0 (by both pipelines where both use the tile: each before its own P V)
@@ -708,7 +743,7 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
             }
             tc_fence_after();
             const float sv = fminf(fmaxf(bars->scale[st][1][r >> p.shift], kLeastScale), kMostScale);
-            const float a = p.c * bars->scale[st][0][r >> p.shift], lsv = log2f(sv);
+            const float a = p.c * bars->scale[st][0][r >> p.shift], lsv = __log2f(sv);
             const uint64_t a2 = pack_f2(a, a), lsv2 = pack_f2(lsv, lsv);
             const bool masked = nk < kRows || t * kRows + kRows - 1 > it.base + it.tok0;
             bool fresh = since == kGroupTiles;
@@ -720,6 +755,7 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                     if (x >= na) continue;
                     uint32_t s[2 * NR];
                     ld_terms<NR>(tmem + b * C::COLS + 32 * x, s);
+                    wait_terms<NR>(s);
                     const int row = 16 * C::group(w, x);
                     const float4 *g4 = reinterpret_cast<const float4 *>(&bars->qscale[slot][row]);
                     const float4 *n4 = reinterpret_cast<const float4 *>(fresh ? bars->zero : &bars->nm[w][row]);
@@ -786,30 +822,56 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                     const int row = 16 * C::group(w, r >> 4) + (r & 15);
                     const float top = fmaxf(fmaxf(bars->red[4 * w][r], bars->red[4 * w + 1][r]),
                                             fmaxf(bars->red[4 * w + 2][r], bars->red[4 * w + 3][r]));
-                    const float M = bars->top[w][row], m = fmaxf(top - kBias, M - kBelow), nm = bars->nm[w][row];
+                    const float M = bars->top[w][row], own = top - kBias, nm = bars->nm[w][row];
+                    const float m = fmaxf(fmaxf(own, fminf(M, own + kAbove)), M - kBelow);
                     bars->top[w][row] = fmaxf(M, m);
                     // without a key so far: nothing to keep, and the next key is above the reference
                     bars->am[w][row] = nm == kNone ? 0.f : ex2(-nm - m);
                     bars->nm[w][row] = m == -INFINITY ? kNone : -m;
                 }
-                soft_sync(w);
+                ok = first || wait_all(smem_u32(&bars->pv_done[w][b ^ 1]), ((c - 1) >> 1) & 1, abort_flag);
+                if (soft_any(w, !ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
 #pragma unroll
                 for (int x = 0; x < GPW; ++x) {
                     if (x >= na) continue;
                     const int row = 16 * C::group(w, x);
+                    if (!first) {        // O^T, whose last P V is that of this pipeline's tile before
+                        uint32_t s[2 * NR];
+                        ld_terms<NR>(tmem + 2 * C::COLS + 32 * x, s);
+                        wait_terms<NR>(s);
 #pragma unroll
-                    for (int k = 0; k < NR; k += 2) {
-                        const uint64_t nm2 = *reinterpret_cast<const uint64_t *>(&bars->nm[w][row + k]);
-                        l[x][k / 2] = mul_f2(l[x][k / 2], *reinterpret_cast<const uint64_t *>(&bars->am[w][row + k]));
-                        e[x][k / 2] = add_f2(e[x][k / 2], nm2);
+                        for (int k = 0; k < NR; k += 4) {
+                            const float4 am = *reinterpret_cast<const float4 *>(&bars->am[w][row + k]);
+                            const float f[4] = {am.x, am.y, am.z, am.w};
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                s[k + q] = __float_as_uint(__uint_as_float(s[k + q]) * f[q]);
+                                s[NR + k + q] = __float_as_uint(__uint_as_float(s[NR + k + q]) * f[q]);
+                            }
+                        }
+                        st_terms<NR>(tmem + 2 * C::COLS + 32 * x, s);
+                    }
+#pragma unroll
+                    for (int k = 0; k < NR; k += 4) {
+                        const float4 nm = *reinterpret_cast<const float4 *>(&bars->nm[w][row + k]);
+                        const float4 am = *reinterpret_cast<const float4 *>(&bars->am[w][row + k]);
+                        l[x][k / 2] = mul_f2(l[x][k / 2], pack_f2(am.x, am.y));
+                        l[x][k / 2 + 1] = mul_f2(l[x][k / 2 + 1], pack_f2(am.z, am.w));
+                        e[x][k / 2] = add_f2(e[x][k / 2], pack_f2(nm.x, nm.y));
+                        e[x][k / 2 + 1] = add_f2(e[x][k / 2 + 1], pack_f2(nm.z, nm.w));
                     }
                 }
-                ++par;
+                tmem_wait_st();
+                tc_fence_before();
                 since = 0;
             }
             ++since;
             // weights, their sums, and both terms into P^T
-            const float isv = 1.f / sv;
+            const float isv = ex2(-lsv);     // of the same rounded logarithm
             const uint64_t isv2 = pack_f2(isv, isv);
             uint8_t *prow = pbuf + b * C::P_BYTES + r * C::P_ROW;
             const uint32_t swz = GPW == 1 ? (r >> 2) & 1 : (r >> 1) & 3;
@@ -844,31 +906,33 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                     *reinterpret_cast<uint32_t *>(pm) = mid[0];
                 }
             }
-            if (r == 0) bars->fresh[w][b] = (fresh ? 1 : 0) | (int)((par & 1) << 1);
             proxy_fence();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[w][b]));
-            if (fresh && !first) {
-                // the group before: its last P V is that of this pipeline's tile before
-                ok = warp_wait(smem_u32(&bars->pv_done[w][b ^ 1]), ((c - 1) >> 1) & 1, abort_flag);
-                if (soft_any(w, !ok)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                add_group((par & 1) ^ 1, true);
-            }
             first = false;
         }
         if (soft_any(w, !ok)) break;
 
-        // epilogue: the last group and the row sums
+        // epilogue: O, a dim a thread, and the row sums
+        float o[GPW][NR];
         if (!first) {
-            ok = warp_wait(smem_u32(&bars->pv_done[w][(c - 1) & 1]), ((c - 1) >> 1) & 1, abort_flag);
+            ok = wait_all(smem_u32(&bars->pv_done[w][(c - 1) & 1]), ((c - 1) >> 1) & 1, abort_flag);
             if (soft_any(w, !ok)) break;
             tc_fence_after();
-            add_group(par & 1, false);
         }
+#pragma unroll
+        for (int x = 0; x < GPW; ++x) {
+            uint32_t s[2 * NR];
+            const bool there = !first && x < na;
+            if (there) {
+                ld_terms<NR>(tmem + 2 * C::COLS + 32 * x, s);
+                wait_terms<NR>(s);
+            }
+#pragma unroll
+            for (int k = 0; k < NR; ++k)
+                o[x][k] = there ? fmaf(__uint_as_float(s[NR + k]), 0.0625f, __uint_as_float(s[k])) : 0.f;
+        }
+        tc_fence_before();
 #pragma unroll
         for (int x = 0; x < GPW; ++x)
 #pragma unroll
@@ -913,12 +977,12 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                 mbar_arrive(smem_u32(&bars->q_empty[slot]));
             }
             // pipeline 0 reads this one's O: not overwritten before it has
-            ok = warp_wait(smem_u32(&bars->epi_done), i & 1, abort_flag);
+            ok = wait_all(smem_u32(&bars->epi_done), i & 1, abort_flag);
             if (soft_any(w, !ok)) break;
             continue;
         }
         if (C::SPLIT) {
-            ok = warp_wait(smem_u32(&bars->stat_full), i & 1, abort_flag);
+            ok = wait_all(smem_u32(&bars->stat_full), i & 1, abort_flag);
             if (soft_any(w, !ok)) break;
         }
         // slot 2 * cta: a unit that an earlier CTA began; 2 * cta + 1: one that begins here
@@ -1029,10 +1093,13 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG>::THREADS), 1)
     // the merge kernel may be scheduled as CTAs of this grid exit; it waits
     // for this grid's completion before it reads the partials
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp < C::SW) paged_softmax<C, NR>(p, smem, bars, tmem, warp, lane);
-    else if (warp == C::QW) paged_queries<C>(p, smem, bars, lane);
-    else if (warp == C::PROD) paged_producer<C>(p, cur, gate, &tmK, &tmV, smem, bars, lane);
-    else paged_mma<C>(smem, bars, tmem, warp - C::MMA, lane);
+    if (warp < C::SW) {
+        paged_softmax<C, NR>(p, smem, bars, tmem, warp, lane);
+    } else {
+        if (warp == C::QW) paged_queries<C>(p, smem, bars, lane);
+        else if (warp == C::PROD) paged_producer<C>(p, cur, gate, &tmK, &tmV, smem, bars, lane);
+        else paged_mma<C>(smem, bars, tmem, warp - C::MMA, lane);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
