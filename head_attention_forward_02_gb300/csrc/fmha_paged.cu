@@ -64,16 +64,21 @@ constexpr int kPagedBars = 6144;         // barrier block
 constexpr float kNone = 1e30f;           // -m of a row that has seen no key in its group
 constexpr float kLeastScale = 0x1p-60f, kMostScale = 0x1p60f;   // of values
 
-template <bool BF_, int NG_>
+template <bool BF_, int NG_, int NR_>
 struct PagedCfg {
     static constexpr bool BF = BF_;
-    static constexpr int NG = NG_;                            // groups of 16 query rows a unit holds
+    static constexpr int NG = NG_;                            // groups of 16 query rows a unit holds,
+    static constexpr int NR = NR_;                            // of which so many are computed
     static constexpr int R = 16 * NG;                         // its rows
     static constexpr bool SPLIT = NG == 1;                    // the pipelines share tiles out, else groups
     static constexpr int GPW = SPLIT ? NG : NG / 2;           // groups of a pipeline
     static constexpr int SW = 8;                              // softmax warps
-    static constexpr int QW = SW, PROD = SW + 1, MMA = SW + 2;   // q warp, producer, two MMA issuers
-    static constexpr int THREADS = 32 * (SW + 4);
+    // Producer warps: issuing a TMA load takes one warp 80 ns, and a tile of 16-token
+    // pages is 16 of them (98 us instead of 67 for eight sequences of 32768); the
+    // wider softmax needs the registers (above 12 warps, 128 a thread).
+    static constexpr int NP = NR <= 8 ? 4 : 1;
+    static constexpr int QW = SW, PROD = SW + 1, MMA = PROD + NP;   // q warp, producers, two MMA issuers
+    static constexpr int THREADS = 32 * (MMA + 2);
     static constexpr int COLS = 32 * GPW;                     // of a pipeline's S^T and O^T
     static constexpr int PIPE_COLS = 4 * COLS;                // TMEM: two S^T, then O^T (and nothing, to a power of two)
     static constexpr int TMEM_COLS = 2 * PIPE_COLS;
@@ -430,17 +435,19 @@ __device__ __forceinline__ uint32_t ring_parity(uint32_t n) { return (n / C::RIN
 
 __device__ const float g_one = 1.f;
 
-// The producer warp: publishes items and loads their K and V tiles, a lane a
-// page, with the pages' scales.  Ids are fetched a tile ahead.
+// Producer warp x: loads its share of the K and V tiles, a lane a page's K or V
+// with its scale.  Ids are fetched a tile ahead.  Warp 0 also publishes the items.
 template <class C>
 __device__ void paged_producer(const PagedParams &p, PagedCursor &cur, int gate, const CUtensorMap *tmK,
-                               const CUtensorMap *tmV, uint8_t *smem, PagedBars *bars, int lane) {
+                               const CUtensorMap *tmV, uint8_t *smem, PagedBars *bars, int x, int lane) {
     volatile int *abort_flag = &bars->abort;
+    const int job = lane * C::NP + x, kv = job & 1;           // of a tile: page job / 2, its K or V
     bool ok = true;
     if (gate) ok = __all_sync(0xffffffffu, lane > 0 || test_gate_open(abort_flag));
     uint32_t fill[2] = {0, 0}, qn = 0;
     const int P = 1 << p.shift, per = kRows >> p.shift;       // pages of a tile
     auto publish = [&](uint32_t i, const PagedItem &it) -> bool {
+        if (x > 0) return true;
         const uint32_t st = i % kPagedItems;
         if (i >= kPagedItems && !wait_all(smem_u32(&bars->item_empty[st]), (i / kPagedItems - 1) & 1, abort_flag)) return false;
         if (lane == 0) {
@@ -459,38 +466,35 @@ __device__ void paged_producer(const PagedParams &p, PagedCursor &cur, int gate,
         ++qn;
         const int pages = (it.L + P - 1) >> p.shift;
         auto id_of = [&](int t) {
-            const int i = t * per + lane;
-            return lane < per && i < pages && t < it.t1 ? page_id(p, it.entry, i, true) : -1;
+            const int i = t * per + (job >> 1);
+            return job < 2 * per && i < pages && t < it.t1 ? page_id(p, it.entry, i, true) : -1;
         };
         int id = id_of(it.t0);
         for (int t = it.t0; t < it.t1; ++t) {
             const int ahead = id_of(t + 1);
-            const int x = C::SPLIT ? (t - it.t0) & 1 : 0;
-            const uint32_t n = x ? fill[1] : fill[0], st = ring_stage<C>(x, n);
+            const int ring = C::SPLIT ? (t - it.t0) & 1 : 0;
+            const uint32_t n = ring ? fill[1] : fill[0], st = ring_stage<C>(ring, n);
             if (n >= C::RING && !wait_all(smem_u32(&bars->kv_empty[st]), ring_parity<C>(n) ^ 1, abort_flag)) {
                 ok = false;
                 break;
             }
             const int here = imax(0, imin(per, pages - t * per));
             const uint32_t fb = smem_u32(&bars->kv_full[st]);
-            if (lane == 0) mbar_expect_tx(fb, 2 * here * (P << 7));
+            const int jobs = (2 * here - x + C::NP - 1) / C::NP;     // of this warp
+            if (lane == 0) mbar_expect_tx(fb, imax(0, jobs) * (P << 7));
             __syncwarp();
-            if (lane < here) {
-                const uint32_t dst = smem_u32(smem + C::OFF_KV + st * C::STAGE) + lane * (P << 7);
+            if (job < 2 * here) {
+                const uint32_t dst = smem_u32(smem + C::OFF_KV + st * C::STAGE) + kv * kPanelBytes + (job >> 1) * (P << 7);
                 // a page outside the cache: a coordinate outside it, which reads zeros
                 const int head = id >= 0 ? id * p.H_k + it.g : p.n_pages * p.H_k;
-                tma_load_3d(dst, tmK, fb, 0, 0, head);
-                tma_load_3d(dst + kPanelBytes, tmV, fb, 0, 0, head);
-#pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const float *src = id >= 0 ? (kv ? p.v_scale : p.k_scale) + head : &g_one;
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&bars->scale[st][kv][lane])), "l"(src)
-                                 : "memory");
-                }
+                tma_load_3d(dst, kv ? tmV : tmK, fb, 0, 0, head);
+                const float *src = id >= 0 ? (kv ? p.v_scale : p.k_scale) + head : &g_one;
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&bars->scale[st][kv][job >> 1])), "l"(src)
+                             : "memory");
             }
             // every lane's arrival, when its copies are there
             asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
-            if (x) ++fill[1];
+            if (ring) ++fill[1];
             else ++fill[0];
             id = ahead;
             if (t == it.t0) {            // the next item is worked out behind the first tile's loads
@@ -504,94 +508,100 @@ __device__ void paged_producer(const PagedParams &p, PagedCursor &cur, int gate,
     // the last release of every stage must arrive before exit; when the CTA
     // gave up, only the copies already issued
 #pragma unroll
-    for (int x = 0; x < (C::SPLIT ? 2 : 1); ++x)
-        for (uint32_t n = fill[x] > C::RING ? fill[x] - C::RING : 0; n < fill[x]; ++n) {
-            const uint32_t st = ring_stage<C>(x, n);
+    for (int ring = 0; ring < (C::SPLIT ? 2 : 1); ++ring)
+        for (uint32_t n = fill[ring] > C::RING ? fill[ring] - C::RING : 0; n < fill[ring]; ++n) {
+            const uint32_t st = ring_stage<C>(ring, n);
             if (ok) ok = wait_all(smem_u32(&bars->kv_empty[st]), ring_parity<C>(n), abort_flag);
             if (!ok) mbar_wait_drain(smem_u32(&bars->kv_full[st]), ring_parity<C>(n));
         }
-    for (uint32_t i = qn > 2 ? qn - 2 : 0; ok && i < qn; ++i)
+    for (uint32_t i = qn > 2 ? qn - 2 : 0; x == 0 && ok && i < qn; ++i)
         ok = wait_all(smem_u32(&bars->q_empty[i & 1]), (i >> 1) & 1, abort_flag);
 }
 
-// One warp: an item's rows of q as e4m3 terms in shared memory, and what the
-// softmax needs to know of each row.
+// Rows r0 .. r0 + N - 1 of an item's q as e4m3 terms in shared memory, and what
+// the softmax needs to know of each row; by a warp.
+template <class C, int N>
+__device__ __forceinline__ void paged_terms(const PagedParams &p, uint8_t *smem, PagedBars *bars, const PagedItem &it, int slot,
+                                            int r0, int lane) {
+    uint8_t *qs = smem + slot * C::Q_BYTES;
+    uint2 v[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int r = r0 + k, t = p.subs == 1 ? r / p.G : 0;
+        const int at = r < it.rows ? (it.row0 + t) * p.H + it.h0 + r - t * p.G : -1;
+        v[k] = at >= 0 ? *reinterpret_cast<const uint2 *>(p.q + ((int64_t)at * kD + lane * 4) * 2) : make_uint2(0u, 0u);
+        if (lane == k) {
+            bars->at[slot][r] = at;
+            bars->lim[slot][r] = it.base + it.tok0 + t;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        float x[4];
+        const uint32_t w[2] = {v[k].x, v[k].y};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            if constexpr (C::BF) {
+                x[2 * j] = __uint_as_float(w[j] << 16);
+                x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+                x[2 * j] = f.x;
+                x[2 * j + 1] = f.y;
+            }
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+        top = __reduce_max_sync(0xffffffffu, top);
+        // largest element to [2^7, 2^8); a row with an infinity or a NaN is one of NaN
+        const int e = max((int)(top >> 23) - 127, -100);
+        const float up = top < 0x7f800000u ? __uint_as_float((uint32_t)(127 + 7 - e) << 23) : __uint_as_float(0x7fc00000u);
+        const int r = r0 + k, pos = C::position(r >> 4), row = 32 * pos + (r & 15);
+        // in f16, which holds a row's elements exactly where the terms do
+        __half2 rest[2];
+        uint32_t code[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t h = pack2<false>(x[2 * j] * up, x[2 * j + 1] * up);
+            rest[j] = *reinterpret_cast<const __half2 *>(&h);
+        }
+        // the next term of what is left: its codes to a row of the tile, and taken off
+        auto term = [&](int row_) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                code[j] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest[j]), __NV_SATFINITE, __NV_E4M3);
+                rest[j] = __hsub2(rest[j], __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)code[j], __NV_E4M3)));
+            }
+            // 16-byte chunk lane / 4 of a 128-byte row, swizzled
+            *reinterpret_cast<uint32_t *>(qs + row_ * 128 + ((((lane >> 2) ^ (row_ & 7)) << 4) | ((lane & 3) << 2))) =
+                __byte_perm(code[0], code[1], 0x5410);
+        };
+        term(row);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) rest[j] = __hmul2(rest[j], __float2half2_rn(16.f));
+        term(row + 16);
+        if constexpr (!C::BF) term(32 * C::NG + 16 * pos + (r & 15));    // behind the others' rows, in units of the second
+        if (lane == 0) bars->qscale[slot][r] = __uint_as_float((uint32_t)(127 + e - 7) << 23);
+    }
+}
+
+// One warp: the rows of every item but the first, an item ahead of the softmax.
+// The first's are shared out among the softmax warps, which have nothing to do
+// then (one warp took 6 us for 32 rows from a cold cache).
 template <class C>
 __device__ void paged_queries(const PagedParams &p, uint8_t *smem, PagedBars *bars, int lane) {
     volatile int *abort_flag = &bars->abort;
     PagedItem it;
     for (uint32_t i = 0; paged_take(bars, i, it, abort_flag, lane); ++i) {
         const int slot = i & 1;
+        if (i == 0) continue;
         if (i >= 2 && !wait_all(smem_u32(&bars->q_empty[slot]), ((i >> 1) - 1) & 1, abort_flag)) break;
-        uint8_t *qs = smem + slot * C::Q_BYTES;
         const int rows = (it.rows + 15) & ~15;
-        for (int r0 = 0; r0 < rows; r0 += 8) {
-            uint2 v[8];
-            int at[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int r = r0 + k, t = p.subs == 1 ? r / p.G : 0;
-                at[k] = r < it.rows ? (it.row0 + t) * p.H + it.h0 + r - t * p.G : -1;
-                v[k] = at[k] >= 0 ? *reinterpret_cast<const uint2 *>(p.q + ((int64_t)at[k] * kD + lane * 4) * 2) : make_uint2(0u, 0u);
-                if (lane == k) {
-                    bars->at[slot][r] = at[k];
-                    bars->lim[slot][r] = it.base + it.tok0 + t;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                float x[4];
-                const uint32_t w[2] = {v[k].x, v[k].y};
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if constexpr (C::BF) {
-                        x[2 * j] = __uint_as_float(w[j] << 16);
-                        x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-                    } else {
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
-                        x[2 * j] = f.x;
-                        x[2 * j + 1] = f.y;
-                    }
-                }
-                uint32_t top = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-                top = __reduce_max_sync(0xffffffffu, top);
-                // largest element to [2^7, 2^8); a row with an infinity or a NaN is one of NaN
-                const int e = max((int)(top >> 23) - 127, -100);
-                const float up = top < 0x7f800000u ? __uint_as_float((uint32_t)(127 + 7 - e) << 23) : __uint_as_float(0x7fc00000u);
-                float hi[4], y[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = x[j] * up;
-                const int r = r0 + k, pos = C::position(r >> 4), row = 32 * pos + (r & 15);
-                // 16-byte chunk lane / 4 of a 128-byte row, swizzled
-                auto put = [&](int row_, uint32_t c) {
-                    *reinterpret_cast<uint32_t *>(qs + row_ * 128 + ((((lane >> 2) ^ (row_ & 7)) << 4) | ((lane & 3) << 2))) = c;
-                };
-                auto term = [&](uint32_t c) {                // its values, taken off, and the rest times 16
-                    const float2 a = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3)));
-                    const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3)));
-                    hi[0] = a.x, hi[1] = a.y, hi[2] = b.x, hi[3] = b.y;
-                };
-                const uint32_t c0 = pack4_e4m3(y[0], y[1], y[2], y[3]);
-                put(row, c0);
-                term(c0);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) y[j] = (y[j] - hi[j]) * 16.f;
-                const uint32_t c1 = pack4_e4m3(y[0], y[1], y[2], y[3]);
-                put(row + 16, c1);
-                if constexpr (!C::BF) {
-                    term(c1);
-                    // behind the first two terms' rows; in the units of the second
-                    const uint32_t c2 = pack4_e4m3(y[0] - hi[0], y[1] - hi[1], y[2] - hi[2], y[3] - hi[3]);
-                    put(32 * C::NG + 16 * pos + (r & 15), c2);
-                }
-                if (lane == 0) bars->qscale[slot][r] = __uint_as_float((uint32_t)(127 + e - 7) << 23);
-            }
-        }
+        for (int r0 = 0; r0 < rows; r0 += 8) paged_terms<C, 8>(p, smem, bars, it, slot, r0, lane);
         proxy_fence();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[slot]));
+        if (lane < C::SW) mbar_arrive(smem_u32(&bars->q_full[slot]));
     }
 }
 
@@ -712,6 +722,13 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
         if (soft_any(w, !more)) break;
         const int slot = i & 1, ng = (it.rows + 15) >> 4, na = C::groups(w, ng);
         const int tb = it.t0 + (C::SPLIT ? w : 0);
+        if (i == 0) {
+            constexpr int N = C::R / C::SW;
+            if (warp * N < ((it.rows + 15) & ~15)) paged_terms<C, N>(p, smem, bars, it, slot, warp * N, lane);
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[slot]));
+        }
         bool ok = wait_all(smem_u32(&bars->q_full[slot]), (i >> 1) & 1, abort_flag);
         uint64_t l[GPW][NR / 2];         // this key's part of the row sums, relative to m
 #pragma unroll
@@ -1039,16 +1056,16 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
 }
 
 template <bool BF, int NG, int NR>
-__global__ void __launch_bounds__((PagedCfg<BF, NG>::THREADS), 1)
+__global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
     fmha_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
-    using C = PagedCfg<BF, NG>;
+    using C = PagedCfg<BF, NG, NR>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     PagedBars *bars = reinterpret_cast<PagedBars *>(smem + C::OFF_BARS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_u32(&bars->q_full[s]), 1);
+            mbar_init(smem_u32(&bars->q_full[s]), C::SW);        // the softmax warps, or the q warp for them
             mbar_init(smem_u32(&bars->q_empty[s]), 2 + C::SW);   // the MMA warps' commits and the softmax warps
             mbar_init(smem_u32(&bars->drain[s]), 1);
             for (int b = 0; b < 2; ++b) {
@@ -1061,7 +1078,7 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG>::THREADS), 1)
         mbar_init(smem_u32(&bars->stat_full), 4);
         mbar_init(smem_u32(&bars->epi_done), 4);
         for (int s = 0; s < C::NS; ++s) {
-            mbar_init(smem_u32(&bars->kv_full[s]), 33);          // the producer's bytes, and its lanes' scales
+            mbar_init(smem_u32(&bars->kv_full[s]), 33 * C::NP);  // a producer's bytes, and its lanes' scales
             mbar_init(smem_u32(&bars->kv_empty[s]), C::SPLIT ? 1 : 2);   // the MMA warps that use a tile
         }
         for (int s = 0; s < kPagedItems; ++s) {
@@ -1078,7 +1095,7 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG>::THREADS), 1)
     }
     PagedCursor cur;
     int gate = 0;
-    if (warp == C::PROD) {
+    if (warp >= C::PROD && warp < C::MMA) {
         if (lane == 0) {
             prefetch_tmap(&tmK);
             prefetch_tmap(&tmV);
@@ -1097,7 +1114,7 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG>::THREADS), 1)
         paged_softmax<C, NR>(p, smem, bars, tmem, warp, lane);
     } else {
         if (warp == C::QW) paged_queries<C>(p, smem, bars, lane);
-        else if (warp == C::PROD) paged_producer<C>(p, cur, gate, &tmK, &tmV, smem, bars, lane);
+        else if (warp < C::MMA) paged_producer<C>(p, cur, gate, &tmK, &tmV, smem, bars, warp - C::PROD, lane);
         else paged_mma<C>(smem, bars, tmem, warp - C::MMA, lane);
     }
     tc_fence_before();
@@ -1187,7 +1204,7 @@ struct PagedLaunch {
 };
 template <bool BF, int NG, int NR>
 PagedLaunch paged_launch() {
-    return {fmha_paged_kernel<BF, NG, NR>, PagedCfg<BF, NG>::SMEM_BYTES, PagedCfg<BF, NG>::THREADS};
+    return {fmha_paged_kernel<BF, NG, NR>, PagedCfg<BF, NG, NR>::SMEM_BYTES, PagedCfg<BF, NG, NR>::THREADS};
 }
 template <bool BF>
 PagedLaunch paged_kernel(int rows, int per_unit) {
