@@ -10,13 +10,15 @@
 // Sums of whole numbers, so no order of threads shows.
 //
 // One cluster of up to eight CTAs does it in one launch: every CTA scans all
-// sequences for itself (5 words each, kept in shared memory), the cluster
+// sequences for itself (six words each, kept in shared memory), the cluster
 // waits until all have read what the call may overwrite in place, and then
-// each thread takes every (cluster size * 1024)-th page taken, page given back
-// and token, and finds its sequence by bisection.  What a token's slot needs of
-// pages taken by this call comes from the stack, not from the table that
-// other threads write, so there is nothing else to wait for.  Bound by latency
-// (a launch, two dependent reads, a scan, a bisection).
+// the pages given back, the pages taken, the sequences and the tokens (by fours
+// where there are many) are one list of jobs that the threads share out; a job finds its sequence by
+// bisection.  What a token's slot needs of pages taken by this call comes from
+// the stack, not from the table that other threads write, so there is nothing
+// else to wait for.  Bound by latency (a launch, two dependent reads, a scan, a
+// bisection): 700 sequences with 30000 tokens took 18.0 us as four lists one
+// after the other, a token a job.
 //
 // Write: a run of tokens with consecutive slots in one page (some of them
 // perhaps left out, by a negative slot); for each kv head
@@ -30,10 +32,11 @@
 // whose scale grows into e4m3's subnormals: two).
 //
 // Bound by memory: 2 bytes in and 1 out an element.  A CTA takes the runs that
-// begin in 16 tokens, for some heads, and each of its warps one run of one
-// head's K or V: two rows a load, 16 rows in flight and in registers, so that
-// runs of up to 16 tokens are read once; of longer ones the first 16 rows stay
-// and the others are read again from L2, without a word between the warps.
+// begin in 16 tokens, for some heads' K or V, and each of its warps a run of
+// up to 16 rows of one of them: two rows a load, all in flight at once, under the
+// loads of their slots, and in registers between the maximum and the rounding.
+// A longer run (of pages of 32 and more) is spread over two to eight warps, 16
+// rows each, the next head's rows fetched under the rounding of this one's.
 #include <cooperative_groups.h>
 
 #include "fmha_cache.cuh"
@@ -48,12 +51,13 @@ namespace {
 // ---------------------------------------------------------------------------
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanSeqs = 8192;          // sequences at most: five words each in shared memory
+constexpr int kPlanSeqs = 8192;          // sequences at most: six words each in shared memory
 
 struct PlanParams {
     const int *seqlen, *n_new, *batch_idx, *n_free;
     int *table, *free_list, *n_free_out, *slots, *positions, *cu_new, *new_seqlen;
     int B, N, entries, width, shift, cap;   // cap: pages of the cache, and elements of free_list
+    int job;                             // tokens of a job: 1 or 4
 };
 
 struct PlanSums {
@@ -101,17 +105,18 @@ __device__ __forceinline__ int last_at_most(const int *v, int n, int x) {
 // What a request asks for, with everything outside its bounds clamped.
 struct PlanRequest {
     int L, n;                            // cached tokens, change (at least -L)
-    bool fits;                           // its table row and the call's tokens hold it
+    int entry;                           // its table row, -1: none
+    bool fits;                           // its table row holds it
 };
 __device__ __forceinline__ PlanRequest plan_request(const PlanParams &p, int b, bool report) {
     PlanRequest r;
     const int most = p.width << p.shift;
-    const bool entry = cache_entry(p.batch_idx, b, p.entries, report) >= 0;
+    r.entry = cache_entry(p.batch_idx, b, p.entries, report);
     r.L = clamped(p.seqlen[b], 0, most, report);
     r.n = clamped(p.n_new[b], -r.L, 0x7fffffff, report);
-    r.fits = entry && r.n <= most - r.L;
-    if (!entry && r.n < 0) r.n = 0;      // no row to take pages from
-    if (entry && !r.fits && report) atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
+    r.fits = r.entry >= 0 && r.n <= most - r.L;
+    if (r.entry < 0 && r.n < 0) r.n = 0; // no row to take pages from
+    if (r.entry >= 0 && !r.fits && report) atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
     return r;
 }
 
@@ -119,11 +124,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fmha_page_plan_kernel(const P
     extern __shared__ int smem_i[];
     __shared__ int s_granted;
     int *s_len = smem_i, *s_new = s_len + p.B, *s_need = s_new + p.B, *s_given = s_need + p.B, *s_cu = s_given + p.B;
+    int *s_entry = s_cu + p.B;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
     const int mask = (1 << p.shift) - 1;
     const bool report = rank == 0;
     if (threadIdx.x == 0) s_granted = 0;
+    const int n_free = p.n_free[0];
 
     // ---- every CTA: the sums of pages needed, pages given back and tokens before each sequence ----
     const int per = (p.B + blockDim.x - 1) / blockDim.x, b0 = min(p.B, (int)threadIdx.x * per), b1 = min(p.B, b0 + per);
@@ -133,13 +140,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fmha_page_plan_kernel(const P
         const int had = (r.L + mask) >> p.shift, want = (int)(((long long)r.L + r.n + mask) >> p.shift);
         s_len[b] = r.fits ? r.L : ~r.L;  // a request that cannot fit: the complement
         s_new[b] = r.n;
+        s_entry[b] = r.entry;
         if (r.fits && r.n > 0) mine.need += want - had;
         if (r.n < 0) mine.given += had - want;
         mine.tokens += r.n > 0 ? r.n : 0;
     }
     PlanSums total;
     PlanSums at = plan_scan(mine, total);
-    const int spare = clamped(p.n_free[0], 0, p.cap, report && threadIdx.x == 0);
+    const int spare = clamped(n_free, 0, p.cap, report && threadIdx.x == 0);
     const bool over = spare + total.given > p.cap;            // more pages than there are: a page given twice
     const int avail = over ? p.cap : (int)(spare + total.given);
     if (report && threadIdx.x == 0 && (over || total.tokens > p.N)) atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
@@ -160,8 +168,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fmha_page_plan_kernel(const P
     cluster.sync();
 
     const int taken = s_granted, given = avail - spare, tokens = (int)min(total.tokens, (long long)p.N);
-    const int first = rank * blockDim.x + threadIdx.x, step = ranks * blockDim.x;
-    auto row = [&](int b) { return p.table + (int64_t)(p.batch_idx ? p.batch_idx[b] : b) * p.width; };
+    auto row = [&](int b) { return p.table + (int64_t)s_entry[b] * p.width; };
     auto len = [&](int b) { return s_len[b] < 0 ? ~s_len[b] : s_len[b]; };
     auto need = [&](int b) {
         return s_len[b] >= 0 && s_new[b] > 0 ? ((s_len[b] + s_new[b] + mask) >> p.shift) - ((s_len[b] + mask) >> p.shift) : 0;
@@ -176,34 +183,64 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fmha_page_plan_kernel(const P
         const int i = avail - 1 - k;
         return i < spare ? p.free_list[i] : page_given(i - spare);
     };
-    if (first == 0) {
-        p.n_free_out[0] = avail - taken;
-        p.cu_new[p.B] = tokens;
-    }
-    for (int b = first; b < p.B; b += step) {
-        p.cu_new[b] = s_cu[b];
-        p.new_seqlen[b] = s_new[b] < 0 || granted_to(b) ? len(b) + s_new[b] : len(b);
-    }
-    for (int j = first; j < given; j += step) p.free_list[spare + j] = page_given(j);
-    for (int k = first; k < taken; k += step) {
-        const int b = last_at_most(s_need, p.B, k);
-        row(b)[((s_len[b] + mask) >> p.shift) + k - s_need[b]] = page_taken(k);
-    }
-    for (int i = first; i < p.N; i += step) {
-        int pos = -1, slot = -1;
-        if (i < tokens) {
-            const int b = last_at_most(s_cu, p.B, i);
-            const int L = len(b), x = i - s_cu[b];
-            pos = L + x;
-            if (granted_to(b)) {
-                const int had = (L + mask) >> p.shift, at_page = pos >> p.shift;
-                const int page = at_page < had ? row(b)[at_page] : page_taken(s_need[b] + at_page - had);
-                if (page >= 0 && page < p.cap) slot = (page << p.shift) + (pos & mask);
-                else atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
+    const int quads = (p.N + p.job - 1) / p.job;
+    const bool wide = p.job == 4 && ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
+    const long long jobs = (long long)given + taken + p.B + quads;
+    for (long long x = rank * blockDim.x + threadIdx.x; x < jobs; x += (long long)ranks * blockDim.x) {
+        if (x < quads) {
+            int pos[4] = {-1, -1, -1, -1}, slot[4] = {-1, -1, -1, -1};
+            const int i0 = (int)x * p.job;
+            if (i0 < tokens) {
+                int b = last_at_most(s_cu, p.B, i0), before = -1, page = -1;
+                bool ok = granted_to(b);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = i0 + k;
+                    if (i >= tokens || k >= p.job) break;
+                    while (b + 1 < p.B && s_cu[b + 1] <= i) {       // the next sequence with tokens
+                        ++b;
+                        ok = granted_to(b);
+                        before = -1;
+                    }
+                    const int L = len(b);
+                    pos[k] = L + i - s_cu[b];
+                    if (!ok) continue;
+                    const int had = (L + mask) >> p.shift, at = pos[k] >> p.shift;
+                    if (at != before) page = at < had ? row(b)[at] : page_taken(s_need[b] + at - had);
+                    before = at;
+                    if (page >= 0 && page < p.cap) slot[k] = (page << p.shift) + (pos[k] & mask);
+                    else atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
+                }
+            }
+            if (wide && i0 + 4 <= p.N) {
+                *reinterpret_cast<int4 *>(p.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+                *reinterpret_cast<int4 *>(p.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < p.job && i0 + k < p.N) {
+                        p.slots[i0 + k] = slot[k];
+                        p.positions[i0 + k] = pos[k];
+                    }
+            }
+            continue;
+        }
+        const long long y = x - quads;
+        if (y < taken) {
+            const int k = (int)y, b = last_at_most(s_need, p.B, k);
+            row(b)[((s_len[b] + mask) >> p.shift) + k - s_need[b]] = page_taken(k);
+        } else if (y < (long long)taken + given) {
+            const int j = (int)(y - taken);
+            p.free_list[spare + j] = page_given(j);
+        } else {
+            const int b = (int)(y - taken - given);
+            p.cu_new[b] = s_cu[b];
+            p.new_seqlen[b] = s_new[b] < 0 || granted_to(b) ? len(b) + s_new[b] : len(b);
+            if (b == 0) {
+                p.n_free_out[0] = avail - taken;
+                p.cu_new[p.B] = tokens;
             }
         }
-        p.slots[i] = slot;
-        p.positions[i] = pos;
     }
 }
 
@@ -211,9 +248,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fmha_page_plan_kernel(const P
 // Write
 // ---------------------------------------------------------------------------
 
-constexpr int kWriteChunk = 16;          // tokens of a CTA
 constexpr int kWriteWarps = 8;
-constexpr int kBatchRows = 16;           // rows that a warp has in registers
+constexpr int kBatchRows = 16;           // tokens of a CTA, and rows that a warp has in registers
 constexpr int kLowest = -60, kHighest = 60;   // exponents of the scales
 
 struct WriteParams {
@@ -309,74 +345,134 @@ __device__ __forceinline__ void rescale_rows(const Run &r, float f, int first, i
     }
 }
 
-// A warp takes (run, head, K or V) items of the CTA's chunk.
+// Rows [j0, j0 + 16) of a run in a warp's registers, two rows a load; the loads
+// are issued whether or not the rows turn out to be written.
+struct Batch {
+    uint4 v[kBatchRows / 2];
+    unsigned live;                       // bit 2 k + half of a lane's half: row 2 k + half is written
+};
+__device__ __forceinline__ void batch_load(Batch &b, const uint8_t *x, int64_t x_t, int j0, int end) {
+    const int half = (threadIdx.x >> 4) & 1;
+#pragma unroll
+    for (int k = 0; k < kBatchRows / 2; ++k)
+        if (j0 + 2 * k + half < end) b.v[k] = *reinterpret_cast<const uint4 *>(x + (j0 + 2 * k + half) * x_t);
+}
+__device__ __forceinline__ void batch_live(Batch &b, const int *slots, int j0, int n) {
+    const int lane = threadIdx.x & 31;
+    b.live = __ballot_sync(0xffffffffu, lane < kBatchRows && j0 + lane < n && slots[j0 + lane] >= 0) >> (lane >> 4);
+}
+template <bool BF>
+__device__ __forceinline__ float batch_max(const Batch &b, float a) {
+#pragma unroll
+    for (int k = 0; k < kBatchRows / 2; ++k)
+        if (b.live >> (2 * k) & 1) a = abs_max<BF>(b.v[k], a);
+    return a;
+}
+template <bool BF>
+__device__ __forceinline__ void batch_store(const Batch &b, const Run &r, int j0, float inv) {
+    const int half = (threadIdx.x >> 4) & 1;
+    uint8_t *dst = r.rows + (r.off + j0 + half) * 128 + (threadIdx.x & 15) * 8;
+#pragma unroll
+    for (int k = 0; k < kBatchRows / 2; ++k)
+        if (b.live >> (2 * k) & 1) *reinterpret_cast<uint2 *>(dst + 2 * k * 128) = codes8<BF>(b.v[k], inv);
+}
+
+// How far the run that begins at slots[0] = s goes, at most `room` tokens.
+__device__ __forceinline__ int run_length(const int *slots, int s, int room) {
+    const int lane = threadIdx.x & 31;
+    int n = 1;
+    while (n < room) {
+        const int j = n + lane, at = j < room ? slots[j] : 0;
+        const unsigned stop = __ballot_sync(0xffffffffu, j >= room || (at >= 0 && at != s + j));
+        n += stop ? __ffs(stop) - 1 : 32;
+        if (stop) break;
+    }
+    return n;
+}
+
 template <bool BF>
 __global__ void __launch_bounds__(32 * kWriteWarps, 3) fmha_page_write_kernel(const WriteParams p) {
-    const int c0 = blockIdx.x * kWriteChunk, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int P = 1 << p.shift, half = lane >> 4, col = (lane & 15) * 16;
+    __shared__ float s_max[2][kWriteWarps];
+    const int c0 = blockIdx.x * kBatchRows, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int P = 1 << p.shift;
     // where runs begin
     const int i = c0 + lane;
-    const int slot = lane < kWriteChunk && i < p.N ? p.slots[i] : -1;
+    const bool here = lane < kBatchRows && i < p.N;
+    const int slot = here ? p.slots[i] : -1, before = here && i > 0 ? p.slots[i - 1] : -1;
     const bool inside = slot >= 0 && slot < p.slots_end;
     if (warp == 0 && blockIdx.y == 0 && slot >= p.slots_end) atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
     bool begins = inside;
     for (int j = 1; begins && j <= min(i, slot & (P - 1)); ++j) {
-        const int other = p.slots[i - j];
+        const int other = j == 1 ? before : p.slots[i - j];
         if (other == slot - j) begins = false;               // of the same run
         else if (other >= 0) break;
     }
-    const unsigned starts = __ballot_sync(0xffffffffu, begins);
+    unsigned starts = __ballot_sync(0xffffffffu, begins);
+    if (starts == 0) return;             // the same in every warp
     const int pair0 = blockIdx.y * p.pairs, pairs = min(p.pairs, 2 * p.H_k - pair0);
+    // new rows of a pair, from a token on; selected, not indexed: an index would put the parameters into local memory
+    auto rows_of = [&](int pair, int t, int64_t &x_t) {
+        const int g = pair >> 1, kv = pair & 1;
+        x_t = kv ? p.x_t[1] : p.x_t[0];
+        return (kv ? p.x[1] + g * p.x_h[1] : p.x[0] + g * p.x_h[0]) + (c0 + t) * x_t + (lane & 15) * 16;
+    };
+    // the last run is the only one that can have more than 16 rows, which all warps then share
+    const int last = 31 - __clz(starts), s_last = __shfl_sync(0xffffffffu, slot, last);
+    const int room_last = min(P - (s_last & (P - 1)), p.N - (c0 + last));
+    const int n_last = room_last > kBatchRows ? run_length(p.slots + c0 + last, s_last, room_last) : 0;
+    const bool longer = n_last > kBatchRows;
+    if (longer) starts &= ~(1u << last);
     const int items = __popc(starts) * pairs;
     for (int item = warp; item < items; item += kWriteWarps) {
         const int nth = item / pairs, pair = pair0 + item - nth * pairs;
         unsigned rest = starts;
         for (int k = 0; k < nth; ++k) rest &= rest - 1;
         const int t = __ffs(rest) - 1, s = __shfl_sync(0xffffffffu, slot, t);
-        const int g = pair >> 1, kv = pair & 1;
         const int *slots = p.slots + c0 + t;
-        // how far the run goes
-        const int room = min(P - (s & (P - 1)), p.N - (c0 + t));
-        int n = 1;
-        while (n < room) {
-            const int j = n + lane, at = j < room ? slots[j] : 0;
-            const unsigned stop = __ballot_sync(0xffffffffu, j >= room || (at >= 0 && at != s + j));
-            n += stop ? __ffs(stop) - 1 : 32;
-            if (stop) break;
-        }
-        const Run r = run_of(p, s, g, kv);
-        // selected, not indexed: an index would put the parameters into local memory
-        const int64_t x_t = kv ? p.x_t[1] : p.x_t[0];
-        const uint8_t *x = (kv ? p.x[1] + g * p.x_h[1] : p.x[0] + g * p.x_h[0]) + (c0 + t) * x_t + col;
-        uint4 v[kBatchRows / 2];
-        unsigned live;                   // of the batch's rows: those that are written
-        auto load = [&](int j0) {
-            live = __ballot_sync(0xffffffffu, lane < kBatchRows && j0 + lane < n && slots[j0 + lane] >= 0) >> half;
-#pragma unroll
-            for (int k = 0; k < kBatchRows / 2; ++k)
-                if (live >> (2 * k) & 1) v[k] = *reinterpret_cast<const uint4 *>(x + (j0 + 2 * k + half) * x_t);
-        };
-        float a = 0.f, old;
-        for (int j0 = (n - 1) / kBatchRows * kBatchRows; j0 >= 0; j0 -= kBatchRows) {
-            load(j0);                    // the first batch last: it stays
-#pragma unroll
-            for (int k = 0; k < kBatchRows / 2; ++k)
-                if (live >> (2 * k) & 1) a = abs_max<BF>(v[k], a);
-        }
-        const float sc = run_scale(r, warp_max(a), old);
+        const int room = min(min(P - (s & (P - 1)), p.N - (c0 + t)), kBatchRows);
+        const Run r = run_of(p, s, pair >> 1, pair & 1);
+        int64_t x_t;
+        const uint8_t *x = rows_of(pair, t, x_t);
+        Batch b;
+        batch_load(b, x, x_t, 0, room);
+        batch_live(b, slots, 0, run_length(slots, s, room));
+        float old;
+        const float sc = run_scale(r, warp_max(batch_max<BF>(b, 0.f)), old);
         if (r.off > 0 && sc > old) rescale_rows(r, old / sc, lane >> 3, 4);
-        const float inv = 1.f / sc;
-        for (int j0 = 0;;) {
-#pragma unroll
-            for (int k = 0; k < kBatchRows / 2; ++k)
-                if (live >> (2 * k) & 1)
-                    *reinterpret_cast<uint2 *>(r.rows + (r.off + j0 + 2 * k + half) * 128 + col / 2) = codes8<BF>(v[k], inv);
-            j0 += kBatchRows;
-            if (j0 >= n) break;
-            load(j0);
-        }
+        batch_store<BF>(b, r, 0, 1.f / sc);
         __syncwarp();
         if (lane == 0) *r.scale = sc;
+    }
+    if (!longer) return;
+    // 16 rows a warp: two, four or eight warps a pair, and the other pairs beside it; the next ones' rows are
+    // fetched ahead
+    const int team = n_last <= 2 * kBatchRows ? 2 : n_last <= 4 * kBatchRows ? 4 : 8;
+    const int sub = warp % team, first = warp - sub, j0 = sub * kBatchRows, abreast = kWriteWarps / team;
+    Batch b;
+    auto fetch = [&](int q) {
+        if (q >= pairs) return;
+        int64_t x_t;
+        const uint8_t *x = rows_of(pair0 + q, last, x_t);
+        batch_load(b, x, x_t, j0, n_last);
+    };
+    fetch(warp / team);
+    batch_live(b, p.slots + c0 + last, j0, n_last);
+    for (int q0 = 0, buf = 0; q0 < pairs; q0 += abreast, buf ^= 1) {
+        const int q = q0 + warp / team;
+        const bool on = q < pairs;       // the same in every warp of a team
+        const Run r = run_of(p, s_last, (pair0 + (on ? q : 0)) >> 1, (pair0 + (on ? q : 0)) & 1);
+        float a = warp_max(batch_max<BF>(b, 0.f)), old;
+        if (lane == 0) s_max[buf][warp] = a;
+        __syncthreads();
+        for (int w = 0; w < team; ++w) a = fmaxf(a, s_max[buf][first + w]);
+        const float sc = run_scale(r, a, old);
+        if (on) {
+            if (r.off > 0 && sc > old) rescale_rows(r, old / sc, sub * 4 + (lane >> 3), 4 * team);
+            batch_store<BF>(b, r, j0, 1.f / sc);
+        }
+        fetch(q + abreast);
+        __syncthreads();                 // all have read the scale
+        if (on && sub == 0 && lane == 0) *r.scale = sc;
     }
 }
 
@@ -444,13 +540,14 @@ extern "C" int fmha_page_plan(const int *seqlen, const int *n_new, const int *ba
     p.width = max_pages;
     p.shift = shift;
     p.cap = n_pages;
-    const int smem = 5 * B * (int)sizeof(int);
+    p.job = N > 8 * kPlanThreads ? 4 : 1;
+    const int smem = 6 * B * (int)sizeof(int);
     if (smem > 47 * 1024 &&
         cudaFuncSetAttribute(fmha_page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
         return cuda_failed();
     cudaLaunchConfig_t cfg = {};
-    // one CTA where every thread has a token or a sequence at most
-    const int ranks = N > kPlanThreads || B > kPlanThreads ? 8 : 1;
+    // one CTA where every thread has a few jobs at most
+    const int ranks = N > 4 * kPlanThreads || B > kPlanThreads ? 8 : 1;
     cfg.gridDim = dim3(ranks);
     cfg.blockDim = dim3(kPlanThreads);
     cfg.dynamicSmemBytes = smem;
@@ -467,18 +564,18 @@ extern "C" int fmha_page_plan(const int *seqlen, const int *n_new, const int *ba
 }
 
 extern "C" int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_t k_head_stride, fmha_tensor v_new,
-                               int64_t v_token_stride, int64_t v_head_stride, const int *slots, fmha_tensor k_pages,
-                               fmha_tensor v_pages, float *k_scale, float *v_scale, int N, int H_k, int D, int n_pages,
+                               int64_t v_token_stride, int64_t v_head_stride, const int *slots, void *k_pages,
+                               void *v_pages, float *k_scale, float *v_scale, int N, int H_k, int D, int n_pages,
                                int page_size, cudaStream_t stream) {
     const int shift = log2_page(page_size);
     if (N < 0 || H_k <= 0 || H_k > 65535 || D != kD || shift < 0) return FMHA_ERR_INVALID_ARG;
     if (N == 0) return FMHA_OK;
     if (n_pages <= 0 || n_pages > 0x7fffffff >> shift || !slots || !k_scale || !v_scale) return FMHA_ERR_INVALID_ARG;
-    if (!k_new.data || !v_new.data || !k_pages.data || !v_pages.data) return FMHA_ERR_INVALID_ARG;
+    if (!k_new.data || !v_new.data || !k_pages || !v_pages) return FMHA_ERR_INVALID_ARG;
     const int dt = k_new.dtype;
-    if ((dt != FMHA_F16 && dt != FMHA_BF16) || v_new.dtype != dt || k_pages.dtype != FMHA_E4M3 || v_pages.dtype != FMHA_E4M3)
+    if ((dt != FMHA_F16 && dt != FMHA_BF16) || v_new.dtype != dt)
         return FMHA_ERR_UNSUPPORTED;
-    for (const void *ptr : {k_new.data, v_new.data, k_pages.data, v_pages.data})
+    for (const void *ptr : {(const void *)k_new.data, (const void *)v_new.data, (const void *)k_pages, (const void *)v_pages})
         if (misaligned(ptr, 16)) return FMHA_ERR_UNSUPPORTED;
     for (int64_t s : {k_token_stride, k_head_stride, v_token_stride, v_head_stride}) {
         if (s < 0 || s > (int64_t(1) << 40)) return FMHA_ERR_INVALID_ARG;
@@ -487,19 +584,20 @@ extern "C" int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_
     if (misaligned(slots, 4) || misaligned(k_scale, 4) || misaligned(v_scale, 4)) return FMHA_ERR_INVALID_ARG;
     const size_t pages = ((size_t)n_pages * H_k << shift) * kD, scales = (size_t)n_pages * H_k * sizeof(float);
     const auto span = [&](int64_t t, int64_t h) { return (size_t)((N - 1) * t + (H_k - 1) * h + kD) * 2; };
-    const Bytes out[4] = {{k_pages.data, pages}, {v_pages.data, pages}, {k_scale, scales}, {v_scale, scales}};
+    const Bytes out[4] = {{k_pages, pages}, {v_pages, pages}, {k_scale, scales}, {v_scale, scales}};
     const Bytes in[3] = {{k_new.data, span(k_token_stride, k_head_stride)}, {v_new.data, span(v_token_stride, v_head_stride)},
                          {slots, (size_t)N * sizeof(int)}};
     if (outputs_clash(out, in)) return FMHA_ERR_INVALID_ARG;
     const int rc = check_device();
     if (rc != FMHA_OK) return rc;
     WriteParams p{};
-    const fmha_tensor x[2] = {k_new, v_new}, c[2] = {k_pages, v_pages};
+    const fmha_tensor x[2] = {k_new, v_new};
+    void *const c[2] = {k_pages, v_pages};
     for (int i = 0; i < 2; ++i) {
         p.x[i] = static_cast<const uint8_t *>(x[i].data);
         p.x_t[i] = 2 * (i ? v_token_stride : k_token_stride);
         p.x_h[i] = 2 * (i ? v_head_stride : k_head_stride);
-        p.pages[i] = static_cast<uint8_t *>(c[i].data);
+        p.pages[i] = static_cast<uint8_t *>(c[i]);
         p.scale[i] = i ? v_scale : k_scale;
     }
     p.slots = slots;
@@ -507,10 +605,10 @@ extern "C" int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_
     p.H_k = H_k;
     p.shift = shift;
     p.slots_end = n_pages << shift;
-    // few tokens: as many CTAs as there are (head, K or V) pairs for every chunk;
-    // many: a CTA's warps share a chunk's pairs
-    const int64_t chunks = ((int64_t)N + kWriteChunk - 1) / kWriteChunk;
-    p.pairs = chunks >= 2 * 152 ? 8 : chunks >= 152 ? 4 : chunks >= 76 ? 2 : 1;
+    // Few tokens: as many CTAs as there are (head, K or V) pairs for every 16 of
+    // them.  Many: a CTA's warps share out the pairs, or a long run's rows.
+    const int64_t chunks = ((int64_t)N + kBatchRows - 1) / kBatchRows;
+    p.pairs = chunks >= 2 * 152 ? (shift >= 6 ? 4 : 8) : chunks >= 152 ? 4 : chunks >= 76 ? 2 : 1;
     const dim3 grid((unsigned)chunks, (2 * H_k + p.pairs - 1) / p.pairs);
     if (grid.y > 65535) return FMHA_ERR_UNSUPPORTED;
     if (dt == FMHA_BF16) fmha_page_write_kernel<true><<<grid, 32 * kWriteWarps, 0, stream>>>(p);

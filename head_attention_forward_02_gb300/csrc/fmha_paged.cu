@@ -1228,7 +1228,7 @@ extern "C" size_t fmha_page_workspace_size(int max_q, int H, int H_k) {
     return (size_t)2 * kPagedMaxCtas * (paged_rows(max_q, H / H_k) * (kD + 1) * sizeof(float) + sizeof(PagedMeta));
 }
 
-extern "C" int fmha_page_fwd(fmha_tensor q, fmha_tensor k_pages, fmha_tensor v_pages, const float *k_scale,
+extern "C" int fmha_page_fwd(fmha_tensor q, const void *k_pages, const void *v_pages, const float *k_scale,
                              const float *v_scale, fmha_tensor o, float *lse, int B, int N, int max_q, int H, int H_k,
                              int D, int n_pages, int page_size, int B_table, int max_pages, const int *table,
                              const int *seqlen, const int *batch_idx, const int *cu_q, float scale, float out_scale,
@@ -1245,12 +1245,12 @@ extern "C" int fmha_page_fwd(fmha_tensor q, fmha_tensor k_pages, fmha_tensor v_p
         (int64_t)n_pages * H_k > 0x7ffffffe || n_pages > 0x7fffffff >> shift || (int64_t)N * H > 0x7fffffff ||
         (!cu_q && N != B))
         return FMHA_ERR_INVALID_ARG;
-    if (!q.data || !k_pages.data || !v_pages.data || !o.data || !k_scale || !v_scale || !table || !seqlen)
+    if (!q.data || !k_pages || !v_pages || !o.data || !k_scale || !v_scale || !table || !seqlen)
         return FMHA_ERR_INVALID_ARG;
     const int dt = q.dtype;
-    if ((dt != FMHA_F16 && dt != FMHA_BF16) || o.dtype != dt || k_pages.dtype != FMHA_E4M3 || v_pages.dtype != FMHA_E4M3)
+    if ((dt != FMHA_F16 && dt != FMHA_BF16) || o.dtype != dt)
         return FMHA_ERR_UNSUPPORTED;
-    for (const void *ptr : {q.data, k_pages.data, v_pages.data, o.data})
+    for (const void *ptr : {(const void *)q.data, k_pages, v_pages, (const void *)o.data})
         if (misaligned(ptr, 16)) return FMHA_ERR_UNSUPPORTED;
     for (const void *ptr : {(const void *)k_scale, (const void *)v_scale, (const void *)lse, (const void *)table,
                             (const void *)seqlen, (const void *)batch_idx, (const void *)cu_q})
@@ -1261,7 +1261,7 @@ extern "C" int fmha_page_fwd(fmha_tensor q, fmha_tensor k_pages, fmha_tensor v_p
     const size_t rows_bytes = (size_t)N * H * kD * 2, pages = ((size_t)n_pages * H_k << shift) * kD;
     const size_t scales = (size_t)n_pages * H_k * sizeof(float), seqs = (size_t)B * sizeof(int);
     const Bytes out[3] = {{o.data, rows_bytes}, {lse, (size_t)N * H * sizeof(float)}, {workspace, need}};
-    const Bytes in[9] = {{q.data, rows_bytes}, {k_pages.data, pages}, {v_pages.data, pages}, {k_scale, scales},
+    const Bytes in[9] = {{q.data, rows_bytes}, {k_pages, pages}, {v_pages, pages}, {k_scale, scales},
                          {v_scale, scales}, {table, (size_t)B_table * max_pages * sizeof(int)}, {seqlen, seqs},
                          {batch_idx, seqs}, {cu_q, seqs + sizeof(int)}};
     if (outputs_clash(out, in)) return FMHA_ERR_INVALID_ARG;
@@ -1312,7 +1312,7 @@ extern "C" int fmha_page_fwd(fmha_tensor q, fmha_tensor k_pages, fmha_tensor v_p
         // [n_pages * H_k, P, 128]: the rows of one page and head
         const cuuint64_t dims[3] = {kD, (cuuint64_t)page_size, (cuuint64_t)n_pages * H_k};
         const cuuint32_t box[3] = {kD, (cuuint32_t)page_size, 1};
-        if (!make_map(&tm[kv], FMHA_E4M3, kv ? v_pages.data : k_pages.data, 3, dims, box)) return FMHA_ERR_CUDA;
+        if (!make_map(&tm[kv], FMHA_E4M3, kv ? v_pages : k_pages, 3, dims, box)) return FMHA_ERR_CUDA;
     }
     const bool bf = dt == FMHA_BF16;
     const int per_unit = imin(R, G * imin(p.tau, max_q));

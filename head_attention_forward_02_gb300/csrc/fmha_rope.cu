@@ -24,8 +24,9 @@ namespace fmha {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 5;            // items whose loads a thread has in flight
-constexpr int kRopeTok = 4;              // tokens of a CTA at most
+constexpr int kRopeTok = 8;              // tokens of a CTA at most
+// items whose loads a thread has in flight: of two 16-byte pieces, or of one
+constexpr int rope_batch(bool half) { return half ? 5 : 8; }
 
 struct RopeTensor {
     const uint8_t *in;
@@ -41,6 +42,7 @@ struct RopeParams {
     int S, H, heads, D, rot;             // heads: of q and k together
     int chunks;                          // work items of a head
     int tok;                             // tokens of a CTA
+    uint32_t magic;                      // i / heads is the high word of i * magic, for 8 * 512 items (one head: 0)
     float magnitude, sign;
     int in_place[2];
 };
@@ -93,6 +95,7 @@ __device__ __forceinline__ void store1(uint8_t *p, float y) {
 // eight elements behind `rot`; without VEC it is one pair or one element.
 template <bool BF, bool FP8, bool HALF, bool VEC>
 __global__ void __launch_bounds__(kRopeThreads, 3) fmha_rope_kernel(const RopeParams p) {
+    constexpr int kBatch = rope_batch(HALF);
     extern __shared__ __align__(16) float2 cs[];             // of the CTA's tokens, cosine and sine of every pair
     __shared__ int pos[kRopeTok];
     __shared__ int64_t base_in[2][kRopeTok], base_out[2][kRopeTok];   // where a token's heads begin, by tensor
@@ -117,21 +120,19 @@ __global__ void __launch_bounds__(kRopeThreads, 3) fmha_rope_kernel(const RopePa
     __syncthreads();
     // an item's token, tensor and head
     auto place = [&](int i, int &t, int &h) -> bool {
-        t = 0;
-#pragma unroll
-        for (int k = 1; k < kRopeTok; ++k) t += i >= k * p.heads;
+        t = p.tok == 1 ? 0 : p.magic ? (int)__umulhi(i, p.magic) : i;
         h = i - t * p.heads;
         const bool key = h >= p.H;
         if (key) h -= p.H;
         return key;
     };
     bool ready = false;
-    for (int i0 = threadIdx.y; i0 < items || !ready; i0 += kRopeBatch * rows) {
-        uint4 u[kRopeBatch], v[kRopeBatch];
-        float fu[kRopeBatch], fv[kRopeBatch];
+    for (int i0 = threadIdx.y; i0 < items || !ready; i0 += kBatch * rows) {
+        uint4 u[kBatch], v[kBatch];
+        float fu[kBatch], fv[kBatch];
         unsigned todo = 0;
 #pragma unroll
-        for (int k = 0; k < kRopeBatch; ++k) {
+        for (int k = 0; k < kBatch; ++k) {
             const int i = i0 + k * rows;
             if (i >= items) continue;
             int t, h;
@@ -161,13 +162,17 @@ __global__ void __launch_bounds__(kRopeThreads, 3) fmha_rope_kernel(const RopePa
             __syncthreads();
         }
 #pragma unroll
-        for (int k = 0; k < kRopeBatch; ++k) {
+        for (int k = 0; k < kBatch; ++k) {
             if (!(todo >> k & 1)) continue;
             int t, h;
             const bool key = place(i0 + k * rows, t, h);
             uint8_t *dst = (key ? p.x[1].out : p.x[0].out) +
                            (base_out[key][t] + h * (key ? p.x[1].out_h : p.x[0].out_h) + a) * (FP8 ? 1 : 2);
             if constexpr (VEC) {
+                if (!FP8 && !turn) {     // behind rot: as they are
+                    *reinterpret_cast<uint4 *>(dst) = u[k];
+                    continue;
+                }
                 const float4 *w = reinterpret_cast<const float4 *>(cs + t * half) + c;
                 const uint32_t uu[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
                 float y[8], z[8];
@@ -220,12 +225,16 @@ __global__ void __launch_bounds__(kRopeThreads, 3) fmha_rope_kernel(const RopePa
 // Host side: tensors [B, S, heads, D] with strides
 // ---------------------------------------------------------------------------
 
+struct Strides {
+    int64_t batch, token, head;
+};
+
 struct Extent {
     int64_t size, stride;
 };
 
 // The tensor's dimensions of more than one element, outermost last.
-int extents(const fmha_strides &s, int B, int S, int heads, Extent (&d)[3]) {
+int extents(const Strides &s, int B, int S, int heads, Extent (&d)[3]) {
     const Extent all[3] = {{heads, s.head}, {S, s.token}, {B, s.batch}};
     int n = 0;
     for (const Extent &e : all) {
@@ -238,7 +247,7 @@ int extents(const fmha_strides &s, int B, int S, int heads, Extent (&d)[3]) {
 }
 
 // No two elements at one place?
-bool writable(const fmha_strides &s, int B, int S, int heads, int D) {
+bool writable(const Strides &s, int B, int S, int heads, int D) {
     Extent d[3];
     const int n = extents(s, B, S, heads, d);
     int64_t span = D;
@@ -249,13 +258,13 @@ bool writable(const fmha_strides &s, int B, int S, int heads, int D) {
     return true;
 }
 
-int64_t span_elements(const fmha_strides &s, int B, int S, int heads, int D) {
+int64_t span_elements(const Strides &s, int B, int S, int heads, int D) {
     return (B - 1) * s.batch + (S - 1) * s.token + (heads - 1) * s.head + D;
 }
 
 struct View {
     const void *p;
-    fmha_strides s;
+    Strides s;
     int heads, E;                        // E: bytes of an element
 };
 
@@ -294,8 +303,9 @@ void rope_launch(const RopeParams &p, bool half, bool vec, dim3 grid, dim3 block
 
 using namespace fmha;
 
-extern "C" int fmha_rope(fmha_tensor q, fmha_strides q_strides, fmha_tensor k, fmha_strides k_strides, fmha_tensor q_out,
-                         fmha_strides q_out_strides, fmha_tensor k_out, fmha_strides k_out_strides, int B, int S, int H,
+extern "C" int fmha_rope(fmha_tensor q, int64_t q_b, int64_t q_t, int64_t q_h, fmha_tensor k, int64_t k_b, int64_t k_t,
+                         int64_t k_h, fmha_tensor q_out, int64_t q_out_b, int64_t q_out_t, int64_t q_out_h,
+                         fmha_tensor k_out, int64_t k_out_b, int64_t k_out_t, int64_t k_out_h, int B, int S, int H,
                          int H_k, int D, int rot, const int *positions, const double *inv_freq, float magnitude,
                          int layout, int transpose, cudaStream_t stream) {
     if (B < 0 || S < 0 || H < 0 || H_k < 0 || H + (int64_t)H_k > 65535 || D <= 0 || D > FMHA_ROPE_MAX_DIM || rot <= 0 ||
@@ -307,7 +317,8 @@ extern "C" int fmha_rope(fmha_tensor q, fmha_strides q_strides, fmha_tensor k, f
     if ((int64_t)B * S >= (int64_t(1) << 31) || !inv_freq || misaligned(inv_freq, 8) || misaligned(positions, 4))
         return FMHA_ERR_INVALID_ARG;
     const fmha_tensor in[2] = {q, k}, out[2] = {q_out, k_out};
-    const fmha_strides si[2] = {q_strides, k_strides}, so[2] = {q_out_strides, k_out_strides};
+    const Strides si[2] = {{q_b, q_t, q_h}, {k_b, k_t, k_h}};
+    const Strides so[2] = {{q_out_b, q_out_t, q_out_h}, {k_out_b, k_out_t, k_out_h}};
     const int heads[2] = {H, H_k};
     View vi[2] = {}, vo[2] = {};
     RopeParams p{};
@@ -324,7 +335,7 @@ extern "C" int fmha_rope(fmha_tensor q, fmha_strides q_strides, fmha_tensor k, f
             return FMHA_ERR_UNSUPPORTED;
         const int oe = odt == FMHA_E4M3 ? 1 : 2;
         if (misaligned(in[i].data, 2) || misaligned(out[i].data, oe)) return FMHA_ERR_UNSUPPORTED;
-        for (const fmha_strides &s : {si[i], so[i]})
+        for (const Strides &s : {si[i], so[i]})
             for (int64_t v : {s.batch, s.token, s.head})
                 if (v < 0 || v > (int64_t(1) << 40)) return FMHA_ERR_INVALID_ARG;
         if (!writable(so[i], B, S, heads[i], D)) return FMHA_ERR_INVALID_ARG;
@@ -334,7 +345,7 @@ extern "C" int fmha_rope(fmha_tensor q, fmha_strides q_strides, fmha_tensor k, f
         p.x[i] = {static_cast<const uint8_t *>(in[i].data), static_cast<uint8_t *>(out[i].data), si[i].batch, si[i].token,
                   si[i].head, so[i].batch, so[i].token, so[i].head};
         // 16-byte accesses (8-byte stores of e4m3); strides that are never stepped along do not count
-        const auto odd = [&](const fmha_strides &s) {
+        const auto odd = [&](const Strides &s) {
             return (B > 1 && s.batch % 8 != 0) || (S > 1 && s.token % 8 != 0) || (heads[i] > 1 && s.head % 8 != 0);
         };
         vec = vec && !misaligned(in[i].data, 16) && !misaligned(out[i].data, 8 * oe) && !odd(si[i]) && !odd(so[i]);
@@ -366,8 +377,13 @@ extern "C" int fmha_rope(fmha_tensor q, fmha_strides q_strides, fmha_tensor k, f
     p.sign = transpose ? -1.f : 1.f;
     const bool half = layout == FMHA_ROPE_HALF;
     p.chunks = vec ? (half ? rot / 16 : rot / 8) + (D - rot) / 8 : rot / 2 + (D - rot);
-    p.tok = p.tokens >= 4 * kRopeTok * 152 ? kRopeTok : 1;
     const dim3 block(p.chunks, p.chunks >= kRopeThreads ? 1 : kRopeThreads / p.chunks);
+    // Many tokens: as many a CTA as its threads take in one batch of loads (a CTA
+    // of 4 tokens of 32 heads of 64, 16 bytes a thread and item, 4 items, took 27.9 us
+    // for 16376 tokens).  Few: a CTA each.
+    const int fill = rope_batch(half) * (int)block.y / p.heads;
+    p.tok = p.tokens < 4 * 4 * 152 || p.heads > 512 ? 1 : fill < 1 ? 1 : fill > kRopeTok ? kRopeTok : fill;
+    p.magic = p.heads > 1 ? (uint32_t)(((uint64_t(1) << 32) + p.heads - 1) / p.heads) : 0;
     const dim3 grid((unsigned)((p.tokens + p.tok - 1) / p.tok));
     const int smem = p.tok * (rot / 2) * (int)sizeof(float2);
     if (dt == FMHA_BF16) {

@@ -36,10 +36,6 @@ class fmha_tensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int)]
 
 
-class fmha_strides(ctypes.Structure):
-    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
-
-
 class FmhaError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{msg} (status {status})")
@@ -101,16 +97,16 @@ def lib():
         L.fmha_page_plan.restype = ctypes.c_int
         L.fmha_page_plan.argtypes = [ctypes.c_void_p] * 11 + [ctypes.c_int] * 6 + [ctypes.c_void_p]
         L.fmha_page_write.restype = ctypes.c_int
-        L.fmha_page_write.argtypes = ([fmha_tensor] + [ctypes.c_int64] * 2) * 2 + [ctypes.c_void_p] + [
-            fmha_tensor] * 2 + [ctypes.c_void_p] * 2 + [ctypes.c_int] * 5 + [ctypes.c_void_p]
+        L.fmha_page_write.argtypes = ([fmha_tensor] + [ctypes.c_int64] * 2) * 2 + [ctypes.c_void_p] * 5 + [
+            ctypes.c_int] * 5 + [ctypes.c_void_p]
         L.fmha_page_fwd.restype = ctypes.c_int
-        L.fmha_page_fwd.argtypes = [fmha_tensor] * 3 + [ctypes.c_void_p] * 2 + [fmha_tensor, ctypes.c_void_p] + [
+        L.fmha_page_fwd.argtypes = [fmha_tensor] + [ctypes.c_void_p] * 4 + [fmha_tensor, ctypes.c_void_p] + [
             ctypes.c_int] * 10 + [ctypes.c_void_p] * 4 + [ctypes.c_float, ctypes.c_float, ctypes.c_int, ctypes.c_void_p,
                                                           ctypes.c_size_t, ctypes.c_void_p]
         L.fmha_page_workspace_size.restype = ctypes.c_size_t
         L.fmha_page_workspace_size.argtypes = [ctypes.c_int] * 3
         L.fmha_rope.restype = ctypes.c_int
-        L.fmha_rope.argtypes = [fmha_tensor, fmha_strides] * 4 + [ctypes.c_int] * 6 + [ctypes.c_void_p] * 2 + [
+        L.fmha_rope.argtypes = ([fmha_tensor] + [ctypes.c_int64] * 3) * 4 + [ctypes.c_int] * 6 + [ctypes.c_void_p] * 2 + [
             ctypes.c_float] + [ctypes.c_int] * 2 + [ctypes.c_void_p]
         L.fmha_bwd.restype = ctypes.c_int
         L.fmha_bwd.argtypes = [fmha_tensor] * 5 + [ctypes.c_void_p] + [fmha_tensor] * 3 + [ctypes.c_int] * 5 + [
@@ -722,7 +718,7 @@ def fmha_page_write(k_new, k_token_stride, k_head_stride, v_new, v_token_stride,
     """Same arguments, order and status codes as the C function fmha_page_write."""
     return lib().fmha_page_write(
         _tensor(k_new), int(k_token_stride), int(k_head_stride), _tensor(v_new), int(v_token_stride), int(v_head_stride),
-        _ptr(slots), _tensor(k_pages), _tensor(v_pages), _ptr(k_scale), _ptr(v_scale), int(N), int(H_k), int(D),
+        _ptr(slots), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), int(N), int(H_k), int(D),
         int(n_pages), int(page_size), _stream(stream))
 
 
@@ -744,10 +740,14 @@ def _fit_pages(index: int, k_pages, v_pages, k_scale, v_scale) -> Tuple[int, int
     """(n_pages, H_k, page_size, D) of a paged cache, once its arrays are looked at."""
     if k_pages.dim() != 4:
         raise ValueError("the pages are [n_pages, H_k, page_size, 128]")
-    shape, e4m3 = k_pages.shape, torch.float8_e4m3fn
-    if not (_fit(index, e4m3, shape, k_pages, v_pages) and _fit(index, torch.float32, shape[:2], k_scale, v_scale)):
+    shape, e4m3, f32 = k_pages.shape, torch.float8_e4m3fn, torch.float32
+    if not (k_pages.dtype is e4m3 and k_pages.get_device() == index and k_pages.is_contiguous()
+            and v_pages.dtype is e4m3 and v_pages.get_device() == index and v_pages.is_contiguous() and v_pages.shape == shape
+            and k_scale.dtype is f32 and k_scale.get_device() == index and k_scale.is_contiguous()
+            and v_scale.dtype is f32 and v_scale.get_device() == index and v_scale.is_contiguous()
+            and k_scale.shape == shape[:2] and v_scale.shape == shape[:2]):
         _check(index, e4m3, shape, k_pages=k_pages, v_pages=v_pages)
-        _check(index, torch.float32, shape[:2], k_scale=k_scale, v_scale=v_scale)
+        _check(index, f32, shape[:2], k_scale=k_scale, v_scale=v_scale)
     return shape
 
 
@@ -767,16 +767,15 @@ def page_write(k_new: torch.Tensor, v_new: torch.Tensor, slots: torch.Tensor, k_
     if k_new.dim() != 3:
         raise ValueError("k_new and v_new are [N, H_k, 128]")
     n_pages, H_k, P, D = _fit_pages(index, k_pages, v_pages, k_scale, v_scale)
-    N, dt = k_new.shape[0], k_new.dtype
-    if not (_fit_strided(index, dt, (N, H_k, D), k_new) and _fit_strided(index, dt, (N, H_k, D), v_new)
-            and _fit(index, torch.int32, (N,), slots)):
+    new, dt, N = k_new.shape, k_new.dtype, k_new.shape[0]
+    if not (new == (N, H_k, D) and v_new.shape == new and v_new.dtype is dt and v_new.get_device() == index
+            and k_new.stride(2) == 1 and v_new.stride(2) == 1 and _fit(index, torch.int32, (N,), slots)):
         _check_strided(index, dt, (N, H_k, D), k_new=k_new, v_new=v_new)
         _check(index, torch.int32, (N,), slots=slots)
     (kt, kh, _), (vt, vh, _) = k_new.stride(), v_new.stride()
     _raise(lib().fmha_page_write(
         fmha_tensor(k_new.data_ptr(), code), kt, kh, fmha_tensor(v_new.data_ptr(), code), vt, vh, slots.data_ptr(),
-        fmha_tensor(k_pages.data_ptr(), E4M3), fmha_tensor(v_pages.data_ptr(), E4M3), k_scale.data_ptr(),
-        v_scale.data_ptr(), N, H_k, D, n_pages, P, _raw_stream(index)))
+        k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), N, H_k, D, n_pages, P, _raw_stream(index)))
 
 
 def fmha_page_fwd(q, k_pages, v_pages, k_scale, v_scale, o, lse, B, N, max_q, H, H_k, D, n_pages, page_size, B_table,
@@ -784,7 +783,7 @@ def fmha_page_fwd(q, k_pages, v_pages, k_scale, v_scale, o, lse, B, N, max_q, H,
                   stream=None) -> int:
     """Same arguments, order and status codes as the C function fmha_page_fwd."""
     return lib().fmha_page_fwd(
-        _tensor(q), _tensor(k_pages), _tensor(v_pages), _ptr(k_scale), _ptr(v_scale), _tensor(o), _ptr(lse), int(B), int(N),
+        _tensor(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _tensor(o), _ptr(lse), int(B), int(N),
         int(max_q), int(H), int(H_k), int(D), int(n_pages), int(page_size), int(B_table), int(max_pages), _ptr(table),
         _ptr(seqlen), _ptr(batch_idx), _ptr(cu_q), float(scale), float(out_scale), int(mask), _ptr(workspace),
         int(workspace_bytes), _stream(stream))
@@ -847,8 +846,8 @@ def page_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_sc
         ws, nbytes = _given(workspace, index)
     try:
         rc = lib().fmha_page_fwd(
-            fmha_tensor(q.data_ptr(), code), fmha_tensor(k_pages.data_ptr(), E4M3), fmha_tensor(v_pages.data_ptr(), E4M3),
-            k_scale.data_ptr(), v_scale.data_ptr(), fmha_tensor(out.data_ptr(), code), _ptr(lse), B, N, most, H, H_k, D,
+            fmha_tensor(q.data_ptr(), code), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), fmha_tensor(out.data_ptr(), code), _ptr(lse), B, N, most, H, H_k, D,
             n_pages, P, B_table, width, table.data_ptr(), seqlen.data_ptr(), _ptr(batch_idx), _ptr(cu_q),
             1.0 / math.sqrt(D) if scale is None else scale, out_scale, _MASKS[mask], ws, nbytes, raw)
     finally:
@@ -863,10 +862,9 @@ def fmha_rope(q, q_strides, k, k_strides, q_out, q_out_strides, k_out, k_out_str
     """Same arguments, order and status codes as the C function fmha_rope;
     strides as (batch, token, head) in elements."""
     return lib().fmha_rope(
-        _tensor(q), fmha_strides(*q_strides), _tensor(k), fmha_strides(*k_strides), _tensor(q_out),
-        fmha_strides(*q_out_strides), _tensor(k_out), fmha_strides(*k_out_strides), int(B), int(S), int(H), int(H_k),
-        int(D), int(rot), _ptr(positions), _ptr(inv_freq), float(magnitude), int(layout), int(transpose),
-        _stream(stream))
+        _tensor(q), *map(int, q_strides), _tensor(k), *map(int, k_strides), _tensor(q_out), *map(int, q_out_strides),
+        _tensor(k_out), *map(int, k_out_strides), int(B), int(S), int(H), int(H_k), int(D), int(rot), _ptr(positions),
+        _ptr(inv_freq), float(magnitude), int(layout), int(transpose), _stream(stream))
 
 
 def rope_frequencies(rot: int, *, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -905,55 +903,64 @@ def rope_frequencies(rot: int, *, base: float = 10000.0, scaling: str = "none", 
     return inv_freq.to(device) if device is not None else inv_freq, magnitude
 
 
-def _rope_strides(t: torch.Tensor) -> fmha_strides:
-    s = t.stride()
-    return fmha_strides(s[0], s[1], s[2]) if len(s) == 4 else fmha_strides(0, s[0], s[1])
-
-
-_NO_TENSOR, _NO_STRIDES = fmha_tensor(None, BF16), fmha_strides(0, 0, 0)
+_NO_TENSOR = fmha_tensor(None, BF16)
 
 
 def _rope(q, k, inv_freq, positions, interleaved, magnitude, q_out, k_out, out_dtype, stream, transpose):
-    index, code = _device_and_code(q)
+    index, dt = q.get_device(), q.dtype
+    code = _TORCH_DTYPE.get(dt)
+    if index < 0 or code is None:
+        _device_and_code(q)
     if stream is not None or _current_device() != index:
         with _on(stream, index):
             return _rope(q, k, inv_freq, positions, interleaved, magnitude, q_out, k_out, out_dtype, None, transpose)
-    if q.dim() not in (3, 4):
+    shape, qs = q.shape, q.stride()
+    if len(shape) == 4:
+        (B, S, H, D), qb = shape, qs[0]
+    elif len(shape) == 3:
+        (S, H, D), B, qb = shape, 1, 0
+    else:
         raise ValueError("q is [B, S, H, D] or [N, H, D], and k alike")
-    lead, H, D, dt = q.shape[:-2], q.shape[-2], q.shape[-1], q.dtype
-    B, S = lead if len(lead) == 2 else (1, lead[0])
-    H_k = 0
-    if k is not None:
-        if k.dim() != q.dim():
-            raise ValueError("k has as many dimensions as q")
-        H_k = k.shape[-2]
-        if not _fit_strided(index, dt, (*lead, H_k, D), k):
-            _check_strided(index, dt, (*lead, H_k, D), k=k)
-    elif k_out is not None:
-        raise ValueError("k_out comes with k")
-    odt = out_dtype or (q_out.dtype if q_out is not None else dt)
-    if odt not in _TORCH_DTYPE:
+    lead, H_k, kt, kot = shape[:-2], 0, _NO_TENSOR, _NO_TENSOR
+    kb = k_t = k_h = kob = ko_t = ko_h = 0
+    odt = out_dtype or (dt if q_out is None else q_out.dtype)
+    ocode = code if odt is dt else _TORCH_DTYPE.get(odt)
+    if ocode is None:
         raise FmhaError(ERR_UNSUPPORTED, f"dtype {odt}: {status_string(ERR_UNSUPPORTED)}")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=odt, device=q.device)
-    if k_out is None and k is not None:
-        k_out = torch.empty(k.shape, dtype=odt, device=q.device)
-    if not (_fit_strided(index, dt, q.shape, q) and _fit_strided(index, odt, q.shape, q_out)
-            and (k is None or _fit_strided(index, odt, k.shape, k_out))
-            and _fit(index, torch.int32, lead, positions) and _fit(index, torch.float64, (inv_freq.shape[0],), inv_freq)):
-        _check_strided(index, dt, q.shape, q=q)
-        _check_strided(index, odt, q.shape, q_out=q_out)
+        q_out = torch.empty(shape, dtype=odt, device=q.device)
+    qos = q_out.stride()
+    ok = (q_out.shape == shape and q_out.dtype is odt and q_out.get_device() == index
+          and (D == 1 or (qs[-1] == 1 and qos[-1] == 1)))
+    if k is not None:
+        H_k = k.shape[-2] if k.dim() > 1 else 0
+        k_shape, ks = (*lead, H_k, D), k.stride()
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=odt, device=q.device)
+        kos = k_out.stride()
+        ok = ok and (k.shape == k_shape and k_out.shape == k_shape and k.dtype is dt and k_out.dtype is odt
+                     and k.get_device() == index and k_out.get_device() == index
+                     and (D == 1 or (ks[-1] == 1 and kos[-1] == 1)))
+        if ok:
+            kt, kot = fmha_tensor(k.data_ptr(), code), fmha_tensor(k_out.data_ptr(), ocode)
+            (k_t, k_h), (ko_t, ko_h) = ks[-3:-1], kos[-3:-1]
+            kb, kob = (ks[0], kos[0]) if len(shape) == 4 else (0, 0)
+    elif k_out is not None:
+        raise ValueError("k_out comes with k")
+    if not (ok and inv_freq.dtype is torch.float64 and inv_freq.dim() == 1 and inv_freq.get_device() == index
+            and inv_freq.is_contiguous() and _fit(index, torch.int32, lead, positions)):
+        _check_strided(index, dt, shape, q=q)
+        _check_strided(index, odt, shape, q_out=q_out)
         if k is not None:
-            _check_strided(index, odt, k.shape, k_out=k_out)
+            _check_strided(index, dt, k_shape, k=k)
+            _check_strided(index, odt, k_shape, k_out=k_out)
         _check(index, torch.int32, lead, positions=positions)
-        _check(index, torch.float64, (inv_freq.shape[0],), inv_freq=inv_freq)
-    ocode = _TORCH_DTYPE[odt]
-    kt, kos = (_NO_TENSOR, _NO_TENSOR) if k is None else (fmha_tensor(k.data_ptr(), code), fmha_tensor(k_out.data_ptr(), ocode))
-    ks, ko = (_NO_STRIDES, _NO_STRIDES) if k is None else (_rope_strides(k), _rope_strides(k_out))
+        _check(index, torch.float64, (inv_freq.numel(),), inv_freq=inv_freq)
     _raise(lib().fmha_rope(
-        fmha_tensor(q.data_ptr(), code), _rope_strides(q), kt, ks, fmha_tensor(q_out.data_ptr(), ocode),
-        _rope_strides(q_out), kos, ko, B, S, H, H_k, D, 2 * inv_freq.shape[0], _ptr(positions), inv_freq.data_ptr(),
-        magnitude, ROPE_PAIRS if interleaved else ROPE_HALF, transpose, _raw_stream(index)))
+        fmha_tensor(q.data_ptr(), code), qb, qs[-3], qs[-2], kt, kb, k_t, k_h, fmha_tensor(q_out.data_ptr(), ocode),
+        qos[0] if len(shape) == 4 else 0, qos[-3], qos[-2], kot, kob, ko_t, ko_h, B, S, H, H_k, D, 2 * inv_freq.shape[0],
+        None if positions is None else positions.data_ptr(), inv_freq.data_ptr(), magnitude,
+        ROPE_PAIRS if interleaved else ROPE_HALF, transpose, _raw_stream(index)))
     return q_out, k_out
 
 

@@ -440,7 +440,7 @@ int fmha_cache_evict(fmha_tensor k_cache, fmha_tensor v_cache, const float *acc,
 /*
  * Paged caches.  Keys and values lie in pages of P = page_size tokens (16, 32,
  * 64 or 128), held as e4m3 codes with one scale per page and kv head:
- *   k_pages, v_pages   FMHA_E4M3 [n_pages, H_k, P, 128]
+ *   k_pages, v_pages   e4m3 bytes [n_pages, H_k, P, 128]
  *   k_scale, v_scale   float [n_pages, H_k]
  * and a key is k_scale[page, g] * code.  Row e of a block table, int32
  * [B_table, max_pages], lists the pages of a sequence's tokens in order; the
@@ -522,9 +522,9 @@ int fmha_page_plan(const int *seqlen, const int *n_new, const int *batch_idx, in
  * succeeds without a launch.
  */
 int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_t k_head_stride, fmha_tensor v_new,
-                    int64_t v_token_stride, int64_t v_head_stride, const int *slots, fmha_tensor k_pages,
-                    fmha_tensor v_pages, float *k_scale, float *v_scale, int N, int H_k, int D, int n_pages,
-                    int page_size, cudaStream_t stream);
+                    int64_t v_token_stride, int64_t v_head_stride, const int *slots, void *k_pages, void *v_pages,
+                    float *k_scale, float *v_scale, int N, int H_k, int D, int n_pages, int page_size,
+                    cudaStream_t stream);
 
 /*
  * fmha_page_fwd -- attention over a paged cache: of one token a sequence, of
@@ -570,8 +570,8 @@ int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_t k_head_st
  * (dtype, alignment, device) or FMHA_ERR_CUDA.  B = 0 or N = 0 succeeds without
  * a launch.
  */
-int fmha_page_fwd(fmha_tensor q, fmha_tensor k_pages, fmha_tensor v_pages, const float *k_scale, const float *v_scale,
-                  fmha_tensor o, float *lse, int B, int N, int max_q, int H, int H_k, int D, int n_pages,
+int fmha_page_fwd(fmha_tensor q, const void *k_pages, const void *v_pages, const float *k_scale,
+                  const float *v_scale, fmha_tensor o, float *lse, int B, int N, int max_q, int H, int H_k, int D, int n_pages,
                   int page_size, int B_table, int max_pages, const int *table, const int *seqlen,
                   const int *batch_idx, const int *cu_q, float scale, float out_scale, int mask, void *workspace,
                   size_t workspace_bytes, cudaStream_t stream);
@@ -583,11 +583,6 @@ enum fmha_rope_layout {
     FMHA_ROPE_PAIRS = 1   /* 2 i and 2 i + 1 */
 };
 #define FMHA_ROPE_MAX_DIM 256
-
-/* Strides of a [B, S, heads, D] tensor, in elements; D is contiguous. */
-typedef struct fmha_strides {
-    int64_t batch, token, head;
-} fmha_strides;
 
 /*
  * fmha_rope -- rotary positions of queries and keys, or the gradient.
@@ -601,8 +596,9 @@ typedef struct fmha_strides {
  * position, and rounded once.  Longer contexts are the caller's choice of
  * inv_freq and magnitude.
  *
- * Layouts: q, q_out [B, S, H, D] and k, k_out [B, S, H_k, D] with strides of
- * their own; H or H_k may be 0 (that tensor is then not looked at).  positions
+ * Layouts: q, q_out [B, S, H, D] and k, k_out [B, S, H_k, D], D contiguous, with
+ * strides of their own, in elements, of sequences (_b), tokens (_t) and heads
+ * (_h); H or H_k may be 0 (that tensor is then not looked at).  positions
  * int32 [B, S], or NULL: the token's index in its sequence; a token with a
  * negative position is left out (its output rows stay as they were).
  * inv_freq double [rot / 2], finite, radians a position.  rot even, at most D;
@@ -617,10 +613,11 @@ typedef struct fmha_strides {
  * FMHA_ERR_UNSUPPORTED (dtype, device) or FMHA_ERR_CUDA.  B = 0, S = 0 or no
  * heads succeed without a launch.
  */
-int fmha_rope(fmha_tensor q, fmha_strides q_strides, fmha_tensor k, fmha_strides k_strides, fmha_tensor q_out,
-              fmha_strides q_out_strides, fmha_tensor k_out, fmha_strides k_out_strides, int B, int S, int H, int H_k,
-              int D, int rot, const int *positions, const double *inv_freq, float magnitude, int layout,
-              int transpose, cudaStream_t stream);
+int fmha_rope(fmha_tensor q, int64_t q_b, int64_t q_t, int64_t q_h, fmha_tensor k, int64_t k_b, int64_t k_t,
+              int64_t k_h, fmha_tensor q_out, int64_t q_out_b, int64_t q_out_t, int64_t q_out_h, fmha_tensor k_out,
+              int64_t k_out_b, int64_t k_out_t, int64_t k_out_h, int B, int S, int H, int H_k, int D, int rot,
+              const int *positions, const double *inv_freq, float magnitude, int layout, int transpose,
+              cudaStream_t stream);
 
 /*
  * fmha_bwd -- backward pass of fmha_fwd: dQ, dK, dV from dO ("CUTLASS

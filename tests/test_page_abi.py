@@ -75,11 +75,11 @@ PAGE_BYTES, SCALE_BYTES = 6 * 2 * 32 * 128, 6 * 2 * 4
 
 
 def call_write(fm, **kw):
-    a = dict(WRITE, N=5, H_k=2, D=128, n=6, P=32, kt=256, kh=128, vt=256, vh=128, dt=BF16, pdt=E4M3)
+    a = dict(WRITE, N=5, H_k=2, D=128, n=6, P=32, kt=256, kh=128, vt=256, vh=128, dt=BF16)
     a.update(kw)
     t = lambda x, d: fm.fmha_tensor(a[x], a.get(x + "_dt", d))
     return fm.lib().fmha_page_write(t("k", a["dt"]), a["kt"], a["kh"], t("v", a["dt"]), a["vt"], a["vh"], a["slots"],
-                                    t("kp", a["pdt"]), t("vp", a["pdt"]), a["ks"], a["vs"], a["N"], a["H_k"], a["D"], a["n"],
+                                    a["kp"], a["vp"], a["ks"], a["vs"], a["N"], a["H_k"], a["D"], a["n"],
                                     a["P"], None)
 
 
@@ -88,7 +88,7 @@ def call_write(fm, **kw):
     (dict(H_k=65536), -1), (dict(kt=-8), -1), (dict(vh=1 << 41), -1), (dict(kt=260), -2), (dict(vh=4), -2),
     *[({x: None}, -1) for x in WRITE], *[({x: WRITE[x] + 8}, -2) for x in ("k", "v", "kp", "vp")],
     *[({x: WRITE[x] + 2}, -1) for x in ("slots", "ks", "vs")],
-    (dict(dt=E4M3), -2), (dict(v_dt=F16), -2), (dict(kp_dt=BF16), -2), (dict(vp_dt=BF16), -2), (dict(dt=7), -2),
+    (dict(dt=E4M3), -2), (dict(v_dt=F16), -2), (dict(dt=7), -2),
     (dict(N=0, k=None, slots=None), 0),
 ])
 def test_write_refusals(fm, kw, code):
@@ -122,9 +122,8 @@ def call_rope(fm, **kw):
     a.update(kw)
     odt = a["dt"] if a["odt"] is None else a["odt"]
     t = lambda x, d: fm.fmha_tensor(a[x], a.get(x + "_dt", d))
-    s = fm.fmha_strides
-    return fm.lib().fmha_rope(t("q", a["dt"]), s(*a["qs"]), t("k", a["dt"]), s(*a["ks"]), t("qo", odt), s(*a["qos"]),
-                              t("ko", odt), s(*a["kos"]), a["B"], a["S"], a["H"], a["H_k"], a["D"], a["rot"], a["pos"], a["f"],
+    return fm.lib().fmha_rope(t("q", a["dt"]), *a["qs"], t("k", a["dt"]), *a["ks"], t("qo", odt), *a["qos"],
+                              t("ko", odt), *a["kos"], a["B"], a["S"], a["H"], a["H_k"], a["D"], a["rot"], a["pos"], a["f"],
                               a["m"], a["layout"], a["tr"], None)
 
 
