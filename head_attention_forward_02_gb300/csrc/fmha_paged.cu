@@ -301,8 +301,15 @@ __device__ __forceinline__ int64_t floor_sum(int64_t x, int s) {
 // tiles and edges of a head's blocks before block v
 __device__ __forceinline__ int64_t paged_before(const PagedParams &p, const PagedSeq &s, int v) {
     const int f = imin(v, s.full), sh = 7 - p.tau_log;
-    const int64_t d = (int64_t)(imax(s.base, 0) - 1) >> p.tau_log;     // tiles of block i: floor((i + 1 + d) / 2^sh) + 1
-    const int64_t tiles = floor_sum(d + f, sh) - floor_sum(d, sh) + f + (int64_t)(v - f) * s.all;
+    int64_t tiles;
+    if (sh >= 0) {
+        const int64_t d = (int64_t)(imax(s.base, 0) - 1) >> p.tau_log; // tiles of block i: floor((i + 1 + d) / 2^sh) + 1
+        tiles = floor_sum(d + f, sh) - floor_sum(d, sh) + f;
+    } else {                             // 2 (i + 1) + d + 1
+        const int64_t d = (int64_t)(imax(s.base, 0) - 1) >> 7;
+        tiles = (int64_t)f * (f + 1) + f * (d + 1);
+    }
+    tiles += (int64_t)(v - f) * s.all;
     return (tiles + (int64_t)v * p.edge) * p.subs;
 }
 
@@ -518,6 +525,46 @@ __device__ void paged_producer(const PagedParams &p, PagedCursor &cur, int gate,
         ok = wait_all(smem_u32(&bars->q_empty[i & 1]), (i >> 1) & 1, abort_flag);
 }
 
+// Four elements of a row of q times a power of two that brings the row's largest
+// to [2^7, 2^8); g: what takes it back.  A row with an infinity or a NaN becomes
+// one of NaN.  By a warp, four elements a lane.
+template <bool BF>
+__device__ __forceinline__ void row_scaled(uint2 v, float (&y)[4], float &g) {
+    const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if constexpr (BF) {
+            y[2 * j] = __uint_as_float(w[j] << 16);
+            y[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+            y[2 * j] = f.x;
+            y[2 * j + 1] = f.y;
+        }
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(y[j]) & 0x7fffffffu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    const int e = max((int)(top >> 23) - 127, -100);
+    const float up = top < 0x7f800000u ? __uint_as_float((uint32_t)(127 + 7 - e) << 23) : __uint_as_float(0x7fc00000u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] *= up;
+    g = __uint_as_float((uint32_t)(127 + e - 7) << 23);
+}
+
+// The next term of four elements: its codes; and `rest` without it.  In f16, which
+// holds a row's scaled elements exactly where the terms do.
+__device__ __forceinline__ uint32_t take_term(__half2 (&rest)[2]) {
+    uint32_t code[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        code[j] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest[j]), __NV_SATFINITE, __NV_E4M3);
+        rest[j] = __hsub2(rest[j], __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)code[j], __NV_E4M3)));
+    }
+    return __byte_perm(code[0], code[1], 0x5410);
+}
+
 // Rows r0 .. r0 + N - 1 of an item's q as e4m3 terms in shared memory, and what
 // the softmax needs to know of each row; by a warp.
 template <class C, int N>
@@ -537,52 +584,25 @@ __device__ __forceinline__ void paged_terms(const PagedParams &p, uint8_t *smem,
     }
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        float x[4];
-        const uint32_t w[2] = {v[k].x, v[k].y};
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if constexpr (C::BF) {
-                x[2 * j] = __uint_as_float(w[j] << 16);
-                x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-            } else {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
-                x[2 * j] = f.x;
-                x[2 * j + 1] = f.y;
-            }
-        }
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
-        top = __reduce_max_sync(0xffffffffu, top);
-        // largest element to [2^7, 2^8); a row with an infinity or a NaN is one of NaN
-        const int e = max((int)(top >> 23) - 127, -100);
-        const float up = top < 0x7f800000u ? __uint_as_float((uint32_t)(127 + 7 - e) << 23) : __uint_as_float(0x7fc00000u);
+        float y[4], g;
+        row_scaled<C::BF>(v[k], y, g);
         const int r = r0 + k, pos = C::position(r >> 4), row = 32 * pos + (r & 15);
-        // in f16, which holds a row's elements exactly where the terms do
         __half2 rest[2];
-        uint32_t code[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const uint32_t h = pack2<false>(x[2 * j] * up, x[2 * j + 1] * up);
+            const uint32_t h = pack2<false>(y[2 * j], y[2 * j + 1]);
             rest[j] = *reinterpret_cast<const __half2 *>(&h);
         }
-        // the next term of what is left: its codes to a row of the tile, and taken off
+        // 16-byte chunk lane / 4 of a 128-byte row, swizzled
         auto term = [&](int row_) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                code[j] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest[j]), __NV_SATFINITE, __NV_E4M3);
-                rest[j] = __hsub2(rest[j], __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)code[j], __NV_E4M3)));
-            }
-            // 16-byte chunk lane / 4 of a 128-byte row, swizzled
-            *reinterpret_cast<uint32_t *>(qs + row_ * 128 + ((((lane >> 2) ^ (row_ & 7)) << 4) | ((lane & 3) << 2))) =
-                __byte_perm(code[0], code[1], 0x5410);
+            *reinterpret_cast<uint32_t *>(qs + row_ * 128 + ((((lane >> 2) ^ (row_ & 7)) << 4) | ((lane & 3) << 2))) = take_term(rest);
         };
         term(row);
 #pragma unroll
         for (int j = 0; j < 2; ++j) rest[j] = __hmul2(rest[j], __float2half2_rn(16.f));
         term(row + 16);
         if constexpr (!C::BF) term(32 * C::NG + 16 * pos + (r & 15));    // behind the others' rows, in units of the second
-        if (lane == 0) bars->qscale[slot][r] = __uint_as_float((uint32_t)(127 + e - 7) << 23);
+        if (lane == 0) bars->qscale[slot][r] = g;
     }
 }
 
@@ -1126,6 +1146,536 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
     }
 }
 
+// ---------------------------------------------------------------------------
+// Chunks of prompts: units of up to 256 rows, and the roles not swapped.
+//
+// With 64 rows a unit the kernel above is bound by what its softmax does across
+// threads (a key each): the scores of 32 rows a thread, their references and
+// votes took 3400 cycles a tile where the MMAs need 800.  Here S = Q K^T has
+// the rows as M: a thread is a row (TMEM lane), its reference, sum and limit are
+// in registers, nothing is exchanged, and a page's scale is one factor for its
+// columns.  Two row blocks of 128 share a tile, each with its softmax group and
+// MMA issuer, which take turns, so that one group's MMAs run under the other's
+// softmax.  The terms are passes of their own into the same accumulator:
+//   S  = Q_0 K^T + Q_1 K^T (+ Q_2 K^T, f16), without a factor of 16, so that elements
+//        of q below 2^-9 (f16 2^-6) of their row's largest are off by 2^-17 of it;
+//   O += P_0 V + P_1 V, where P_1, what e4m3 left of a weight, is e5m2: its
+//        smallest step is 2^-16, so a weight is off by 2^-7 of itself or by 2^-17
+//        where the row's largest is 2^4 or more, and a reference serves 64 tiles.
+// Bound by the tensor cores: four e4m3 products of 128 x 128 x 128 a block and
+// tile, which is the time of the two that bf16 operands would take.
+// ---------------------------------------------------------------------------
+
+constexpr int kRowsSlots = 9;            // ring of K and V tiles
+constexpr int kRowsTiles = 64;           // tiles that a reference serves at most
+constexpr int kRowsThreads = 352;        // two softmax groups of four warps, producer, an MMA issuer a group
+
+template <bool BF_>
+struct RowsCfg {
+    static constexpr bool BF = BF_;
+    static constexpr int NT = BF ? 2 : 3;                     // terms of q
+    static constexpr int R = 2 * kRows;
+    static constexpr int Q_BYTES = NT * kPanelBytes;          // of a block
+    static constexpr int OFF_KV = 2 * Q_BYTES;
+    static constexpr int NS_FIT = (226 * 1024 - 4096 - OFF_KV) / kPanelBytes;
+    static constexpr int NS = NS_FIT < kRowsSlots ? NS_FIT : kRowsSlots;
+    static constexpr int OFF_BARS = OFF_KV + NS * kPanelBytes;
+    static constexpr int SMEM_BYTES = OFF_BARS + 4096 + 1024;
+    static_assert(SMEM_BYTES <= 227 * 1024 && NS >= 4, "shared memory");
+};
+
+struct RowsBars {
+    uint64_t q_full[2], drain[2], s_full[2], p_full[2][2], o_full[2], turn[2];   // by group; p_full by half
+    uint64_t kv_full[kRowsSlots], kv_empty[kRowsSlots];
+    uint64_t item_full[kPagedItems], item_empty[kPagedItems];
+    PagedItem item[kPagedItems];
+    uint32_t tmem_base;
+    int abort;
+    float scale[kRowsSlots][2][8];       // k_scale, v_scale of a V slot's pages
+    float qscale[2 * kRows];
+};
+static_assert(sizeof(RowsBars) <= 4096, "barrier block");
+
+__device__ __forceinline__ bool rows_take(RowsBars *bars, uint32_t i, PagedItem &it, volatile int *abort_flag, int lane) {
+    const uint32_t st = i % kPagedItems;
+    if (!wait_all(smem_u32(&bars->item_full[st]), (i / kPagedItems) & 1, abort_flag)) return false;
+    it = bars->item[st];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[st]));
+    return it.rows > 0;
+}
+
+// The producer warp: tile c of the CTA is slots 2 c (K) and 2 c + 1 (V) of the ring.
+template <class C>
+__device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, const CUtensorMap *tmK, const CUtensorMap *tmV,
+                              uint8_t *smem, RowsBars *bars, int lane) {
+    volatile int *abort_flag = &bars->abort;
+    bool ok = true;
+    if (gate) ok = __all_sync(0xffffffffu, lane > 0 || test_gate_open(abort_flag));
+    uint32_t n = 0, qn = 0;
+    const int P = 1 << p.shift, per = kRows >> p.shift;
+    auto publish = [&](uint32_t i, const PagedItem &it) -> bool {
+        const uint32_t st = i % kPagedItems;
+        if (i >= kPagedItems && !wait_all(smem_u32(&bars->item_empty[st]), (i / kPagedItems - 1) & 1, abort_flag)) return false;
+        if (lane == 0) {
+            bars->item[st] = it;
+            mbar_arrive(smem_u32(&bars->item_full[st]));
+        }
+        __syncwarp();
+        return true;
+    };
+    PagedItem it, next;
+    if (ok) {
+        paged_next(p, cur, it);
+        ok = publish(0, it);
+    }
+    while (ok && it.rows > 0) {
+        ++qn;
+        const int pages = (it.L + P - 1) >> p.shift;
+        auto id_of = [&](int t) {
+            const int i = t * per + lane;
+            return lane < per && i < pages && t < it.t1 ? page_id(p, it.entry, i, true) : -1;
+        };
+        int id = id_of(it.t0);
+        for (int t = it.t0; ok && t < it.t1; ++t) {
+            const int ahead = id_of(t + 1), here = imax(0, imin(per, pages - t * per));
+            // a page outside the cache: a coordinate outside it, which reads zeros
+            const int head = id >= 0 ? id * p.H_k + it.g : p.n_pages * p.H_k;
+            for (int kv = 0; kv < 2; ++kv, ++n) {
+                const uint32_t st = n % C::NS;
+                if (n >= C::NS && !wait_all(smem_u32(&bars->kv_empty[st]), (n / C::NS - 1) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t fb = smem_u32(&bars->kv_full[st]);
+                if (lane == 0) mbar_expect_tx(fb, here * (P << 7));
+                __syncwarp();
+                if (lane < here) {
+                    tma_load_3d(smem_u32(smem + C::OFF_KV + st * kPanelBytes) + lane * (P << 7), kv ? tmV : tmK, fb, 0, 0, head);
+                    // both scales come with V: its slot, not K's, is kept until the softmax has read them
+                    if (kv) {
+                        const float *ks = id >= 0 ? p.k_scale + head : &g_one, *vs = id >= 0 ? p.v_scale + head : &g_one;
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&bars->scale[st][0][lane])), "l"(ks)
+                                     : "memory");
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&bars->scale[st][1][lane])), "l"(vs)
+                                     : "memory");
+                    }
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
+            }
+            id = ahead;
+            if (ok && t == it.t0) {
+                paged_next(p, cur, next);
+                ok = publish(qn, next);
+            }
+        }
+        it = next;
+    }
+    for (uint32_t f = n > C::NS ? n - C::NS : 0; f < n; ++f) {
+        if (ok) ok = wait_all(smem_u32(&bars->kv_empty[f % C::NS]), (f / C::NS) & 1, abort_flag);
+        if (!ok) mbar_wait_drain(smem_u32(&bars->kv_full[f % C::NS]), (f / C::NS) & 1);
+    }
+}
+
+// MMA issuer of group x.  MMAs of one warp execute in issue order, so S of the
+// next tile may overwrite the columns of P once P V is issued, and S being there
+// says that the P V before it is.
+template <class C>
+__device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x, int lane) {
+    volatile int *abort_flag = &bars->abort;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
+    const uint32_t s_tm = tmem + x * kRows, o_tm = tmem + 2 * kRows + x * kD;
+    constexpr uint32_t kIdS = mma_idesc(0u, kRows, false), kIdP0 = mma_idesc(0u, kD, true);
+    constexpr uint32_t kIdP1 = kIdP0 | (1u << 7);            // A (the weights' second term) e5m2
+    const uint64_t q = smem_desc(smem_u32(smem + x * C::Q_BYTES), 16, 1024);
+    const uint64_t k0 = smem_desc(smem_u32(smem + C::OFF_KV), 16, 1024);
+    const uint64_t v0 = smem_desc(smem_u32(smem + C::OFF_KV), kPanelBytes, 1024);
+    uint32_t c = 0, m = 0, turns = 0, items = 0;   // tiles; of this group; its turns; items that it had rows of
+    bool ok = true;
+    PagedItem it;
+    for (uint32_t i = 0; ok && rows_take(bars, i, it, abort_flag, lane); ++i) {
+        const bool both = it.rows > kRows;
+        if (x == 1 && !both) {           // nothing to do with these tiles
+            for (int t = it.t0; ok && t < it.t1; ++t, ++c)
+                for (uint32_t n = 2 * c; ok && n < 2 * c + 2; ++n) {
+                    ok = wait_all(smem_u32(&bars->kv_full[n % C::NS]), (n / C::NS) & 1, abort_flag);
+                    if (ok && lane == 0) mbar_arrive(smem_u32(&bars->kv_empty[n % C::NS]));
+                }
+            continue;
+        }
+        if (!wait_all(smem_u32(&bars->q_full[x]), items++ & 1, abort_flag)) {
+            ok = false;
+            break;
+        }
+        bool first = true;
+        for (int t = it.t0; ok && t <= it.t1; ++t) {
+            // the tiles of this step first: their waits are off the chain
+            const uint32_t nk = 2 * c, nv = 2 * c - 1, kst = nk % C::NS, vst = nv % C::NS;
+            if ((t > it.t0 && !wait_all(smem_u32(&bars->kv_full[vst]), (nv / C::NS) & 1, abort_flag)) ||
+                (t < it.t1 && !wait_all(smem_u32(&bars->kv_full[kst]), (nk / C::NS) & 1, abort_flag))) {
+                ok = false;
+                break;
+            }
+            if (t > it.t0) {             // P V of the tile before
+                const int halves = it.L - (t - 1) * kRows > kRows / 2 ? 2 : 1;
+                const uint64_t v = v0 + ((vst * kPanelBytes) >> 4);
+                for (int h = 0; h < halves; ++h) {
+                    if (!wait_all(smem_u32(&bars->p_full[x][h]), (m - 1) & 1, abort_flag) ||
+                        (both && h == 0 && !wait_all(smem_u32(&bars->turn[x]), (turns & 1) ^ (x ^ 1), abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int term = 0; term < 2; ++term)
+#pragma unroll
+                        for (int kk = 0; kk < 2; ++kk)       // 32 keys: 8 columns of P, 32 rows of V
+                            mma_ts<true>(o_tm, s_tm + term * 32 + h * 16 + kk * 8, v + (((h * 2 + kk) * 32 * 128) >> 4),
+                                         term ? kIdP1 : kIdP0, !first || h > 0 || term > 0 || kk > 0 ? 1u : 0u);
+                }
+                if (!ok) break;
+                first = false;
+            }
+            if (both && t == it.t0 && !wait_all(smem_u32(&bars->turn[x]), (turns & 1) ^ (x ^ 1), abort_flag)) {
+                ok = false;
+                break;
+            }
+            if (t < it.t1) {
+                tc_fence_after();
+                const uint64_t k = k0 + ((kst * kPanelBytes) >> 4);
+#pragma unroll
+                for (int term = 0; term < C::NT; ++term)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        mma_ss<true>(s_tm, q + ((term * kPanelBytes + kk * 32) >> 4), k + ((kk * 32) >> 4), kIdS,
+                                     term > 0 || kk > 0 ? 1u : 0u);
+                        // the other warp wakes up behind the MMAs still to issue
+                        if (both && term == C::NT - 1 && kk == 1 && lane == 0) mbar_arrive(smem_u32(&bars->turn[x ^ 1]));
+                    }
+                tc_commit(smem_u32(&bars->s_full[x]));       // also: P V of the tile before is done
+                tc_commit(smem_u32(&bars->kv_empty[kst]));
+                ++c;
+                ++m;
+            }
+            if (t > it.t0) tc_commit(smem_u32(&bars->kv_empty[vst]));
+            if (both) {
+                if (t >= it.t1 && lane == 0) mbar_arrive(smem_u32(&bars->turn[x ^ 1]));
+                ++turns;
+            }
+        }
+        if (!ok) break;
+        tc_commit(smem_u32(&bars->o_full[x]));
+    }
+    // no tensor-core operation may be in flight when TMEM is released
+    tc_commit(smem_u32(&bars->drain[x]));
+    mbar_wait_drain(smem_u32(&bars->drain[x]), 0);
+}
+
+// Eight rows of q, r0 .. r0 + 7 of the unit, as terms: rows of the group's tiles.
+template <class C>
+__device__ __forceinline__ void rows_terms(const PagedParams &p, uint8_t *tile, float *qscale, const PagedItem &it, int r0, int lane) {
+    uint2 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int r = r0 + k, t = p.subs == 1 ? r / p.G : 0;
+        v[k] = r < it.rows ? *reinterpret_cast<const uint2 *>(
+                                 p.q + (((int64_t)(it.row0 + t) * p.H + it.h0 + r - t * p.G) * kD + lane * 4) * 2)
+                           : make_uint2(0u, 0u);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        float y[4], g;
+        row_scaled<C::BF>(v[k], y, g);
+        __half2 rest[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t h = pack2<false>(y[2 * j], y[2 * j + 1]);
+            rest[j] = *reinterpret_cast<const __half2 *>(&h);
+        }
+        const int row = (r0 + k) & (kRows - 1);
+#pragma unroll
+        for (int term = 0; term < C::NT; ++term)
+            *reinterpret_cast<uint32_t *>(tile + term * kPanelBytes + row * 128 +
+                                          ((((lane >> 2) ^ (row & 7)) << 4) | ((lane & 3) << 2))) = take_term(rest);
+        if (lane == 0) qscale[r0 + k] = g;
+    }
+}
+
+// Two weights: their first term in e4m3, and what it leaves in e5m2.
+__device__ __forceinline__ void split2_wide(float a, float b, uint32_t &hi, uint32_t &mid) {
+    const uint32_t h = pack2<false>(a, b);
+    const __half2 p = *reinterpret_cast<const __half2 *>(&h);
+    hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(p), __NV_SATFINITE, __NV_E4M3);
+    const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3));
+    mid = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(p, back)), __NV_SATFINITE, __NV_E5M2);
+}
+
+// Softmax and epilogue of group x, a row a thread.
+template <class C>
+__device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars, uint32_t tmem, int warp, int lane) {
+    volatile int *abort_flag = &bars->abort;
+    const int x = warp >> 2, lr = (warp & 3) * 32 + lane, r = x * kRows + lr;      // row of the block, of the unit
+    const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t s_tm = lane_base + x * kRows, o_tm = lane_base + 2 * kRows + x * kD;
+    uint32_t c = 0, m_tiles = 0, items = 0;             // tiles; of this group; items that it had rows of
+    int parts = 0;                                      // bit s: slot s of this CTA holds a partial
+    PagedItem it;
+    for (uint32_t i = 0; rows_take(bars, i, it, abort_flag, lane); ++i) {
+        if (x == 1 && it.rows <= kRows) {
+            c += it.t1 - it.t0;
+            continue;
+        }
+        // this warp's rows of q; the S MMAs of the item before are done, their scores were read
+        for (int k = 0; k < 32; k += 8)
+            rows_terms<C>(p, smem + x * C::Q_BYTES, bars->qscale, it, x * kRows + (warp & 3) * 32 + k, lane);
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[x]));
+        const int tok = p.subs == 1 ? r / p.G : 0;
+        const int64_t at = (int64_t)(it.row0 + tok) * p.H + it.h0 + r - tok * p.G;
+        const bool row_ok = r < it.rows;
+        const bool work = __any_sync(0xffffffffu, row_ok);   // else the warp only keeps step
+        const int lim = it.base + it.tok0 + tok;        // last key it sees
+        const float fq = p.c * bars->qscale[r];
+        float m = -INFINITY, M = -INFINITY;             // reference (log2 units) of P and O, and the highest so far
+        float l = 0.f;                                  // row sum
+        int since = kRowsTiles;
+        bool ok = true;
+        for (int t = it.t0; t < it.t1; ++t, ++c, ++m_tiles) {
+            const int nk = it.L - t * kRows, halves = nk > kRows / 2 ? 2 : 1;
+            const uint32_t n = 2 * c + 1, vst = n % C::NS;
+            // scores, and the scales that come with V
+            if (!wait_all(smem_u32(&bars->s_full[x]), m_tiles & 1, abort_flag) ||
+                !wait_all(smem_u32(&bars->kv_full[vst]), (n / C::NS) & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            if (nk < kRows) {
+                // rows past the keys: V is zeroed so that P = 0 contributes 0 (by each group before its own P V)
+                if (lr >= nk) {
+                    proxy_fence();
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + C::OFF_KV + vst * kPanelBytes + lr * 128);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
+                    proxy_fence();
+                }
+                __syncwarp();
+            }
+            if (!work) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&bars->p_full[x][0]));
+                    mbar_arrive(smem_u32(&bars->p_full[x][1]));
+                }
+                continue;
+            }
+            tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_ld32(s_tm + 32 * q, s[q]);
+            // factor and summand of 16 columns, a page or a part of one (looked up twice: they do not fit the registers)
+            const volatile float *ks = bars->scale[vst][0], *vs = bars->scale[vst][1];
+            auto factor = [&](int u) { return fmaxf(fq * ks[(16 * u) >> p.shift], FLT_MIN); };   // not 0: -inf stays -inf
+            auto summand = [&](int u) { return __log2f(fminf(fmaxf(vs[(16 * u) >> p.shift], kLeastScale), kMostScale)); };
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_wait_ld(s[q]);
+            const int cnt = imin(nk, lim - t * kRows + 1);   // visible keys
+            if (__any_sync(0xffffffffu, cnt < kRows)) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (32 * q + k >= cnt) s[q][k] = 0xff800000u;
+            }
+            float tmax = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const uint32_t *su = s[u >> 1] + 16 * (u & 1);
+                float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 16; k += 4) {
+                    a = max3(a, __uint_as_float(su[k]), __uint_as_float(su[k + 1]));
+                    b = max3(b, __uint_as_float(su[k + 2]), __uint_as_float(su[k + 3]));
+                }
+                tmax = fmaxf(tmax, fmaf(fmaxf(a, b), factor(u), summand(u)));
+            }
+            const bool need = tmax > m + kGrown || since == kRowsTiles;
+            if (since == kRowsTiles) since = 0;
+            ++since;
+            if (__any_sync(0xffffffffu, need)) {
+                float alpha = 1.f;
+                if (need) {
+                    const float own = tmax - kBias, ref = fmaxf(fmaxf(own, fminf(M, own + kAbove)), M - kBelow);
+                    alpha = m == -INFINITY ? 0.f : ex2(m - ref);
+                    m = ref;
+                    M = fmaxf(M, ref);
+                    l *= alpha;
+                }
+                if (t > it.t0) {
+                    // the P V of the tile before is in O: S, issued behind it, is there
+#pragma unroll 1
+                    for (int q = 0; q < 8; ++q) {
+                        uint32_t o[16];
+                        tmem_ld16(o_tm + 16 * q, o);
+                        tmem_wait_ld16(o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                        tmem_st16(o_tm + 16 * q, o);
+                    }
+                }
+            }
+            // a row that has seen no key yet: every score is -inf, P = 0
+            const float mr = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (h < halves) {
+#pragma unroll
+                    for (int q = 2 * h; q < 2 * h + 2; ++q) {
+                        uint32_t w0[8], w1[8];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float fu = factor(2 * q + u), du = summand(2 * q + u);
+                            const uint64_t f2 = pack_f2(fu, fu), d2 = pack_f2(du - mr, du - mr);
+                            uint64_t sum[2] = {0, 0};
+#pragma unroll
+                            for (int k = 0; k < 16; k += 4) {
+                                const uint32_t *sk = s[q] + 16 * u + k;
+                                float e[4];
+                                unpack_f2(fma_f2(pack_f2(__uint_as_float(sk[0]), __uint_as_float(sk[1])), f2, d2), e[0], e[1]);
+                                unpack_f2(fma_f2(pack_f2(__uint_as_float(sk[2]), __uint_as_float(sk[3])), f2, d2), e[2], e[3]);
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) e[y] = ex2(e[y]);
+                                sum[0] = add_f2(sum[0], pack_f2(e[0], e[1]));
+                                sum[1] = add_f2(sum[1], pack_f2(e[2], e[3]));
+                                uint32_t h0, h1, m0, m1;
+                                split2_wide(e[0], e[1], h0, m0);
+                                split2_wide(e[2], e[3], h1, m1);
+                                w0[4 * u + k / 4] = __byte_perm(h0, h1, 0x5410);
+                                w1[4 * u + k / 4] = __byte_perm(m0, m1, 0x5410);
+                            }
+                            float a, b;
+                            unpack_f2(add_f2(sum[0], sum[1]), a, b);
+                            l = fmaf(a + b, ex2(-du), l);
+                        }
+                        tmem_st8(s_tm + 8 * q, w0);
+                        tmem_st8(s_tm + 32 + 8 * q, w1);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[x][h]));
+            }
+        }
+        if (!ok) break;
+
+        // epilogue: O of a unit that this CTA covers alone, else a partial
+        if (!wait_all(smem_u32(&bars->o_full[x]), items++ & 1, abort_flag)) break;
+        const bool whole = it.t1 - it.t0 == it.nt;
+        const int part = 2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
+        if (threadIdx.x == 0 && !whole) {
+            parts |= it.t0 == 0 ? 2 : 1;
+            p.meta[part] = PagedMeta{it.row0, it.h0, it.rows, it.t1 == it.nt};
+        }
+        if (work) {
+            tc_fence_after();
+            const bool empty = l == 0.f;                // the row saw no key
+            const float inv = (whole ? p.out_scale : 1.f) / l;
+            const float lse = empty ? -INFINITY : (m + log2f(l)) * kLn2;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                uint32_t o[32];
+                tmem_ld32(o_tm + 32 * q, o);
+                tmem_wait_ld(o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = empty ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
+                if (row_ok && !whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + ((int64_t)part * C::R + r) * kD + 32 * q);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                } else if (row_ok) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) + at * kD + 32 * q);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) w[k] = pack2<C::BF>(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) dst[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                }
+            }
+            if (row_ok) {
+                if (!whole) p.part_lse[(int64_t)part * C::R + r] = lse;
+                else if (p.lse) p.lse[at] = lse;
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+    }
+    if (threadIdx.x == 0)               // empty slots; one that is missing (a CTA that gave up) also ends its unit
+        for (int s = 0; s < 2; ++s)
+            if (!(parts >> s & 1)) p.meta[2 * blockIdx.x + s] = PagedMeta{0, 0, 0, 1};
+}
+
+template <bool BF>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+    fmha_paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
+    using C = RowsCfg<BF>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    RowsBars *bars = reinterpret_cast<RowsBars *>(smem + C::OFF_BARS);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(smem_u32(&bars->q_full[x]), 4);
+            mbar_init(smem_u32(&bars->s_full[x]), 1);
+            mbar_init(smem_u32(&bars->p_full[x][0]), 4);
+            mbar_init(smem_u32(&bars->p_full[x][1]), 4);
+            mbar_init(smem_u32(&bars->o_full[x]), 1);
+            mbar_init(smem_u32(&bars->drain[x]), 1);
+            mbar_init(smem_u32(&bars->turn[x]), 1);
+        }
+        for (int s = 0; s < C::NS; ++s) {
+            mbar_init(smem_u32(&bars->kv_full[s]), 33);          // the bytes, and the lanes' scales
+            mbar_init(smem_u32(&bars->kv_empty[s]), 2);          // the MMA warps
+        }
+        for (int s = 0; s < kPagedItems; ++s) {
+            mbar_init(smem_u32(&bars->item_full[s]), 1);
+            mbar_init(smem_u32(&bars->item_empty[s]), 10);       // the softmax and MMA warps
+        }
+        bars->abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) {
+        tmem_alloc(smem_u32(&bars->tmem_base), 512);
+        tmem_relinquish();
+    }
+    PagedCursor cur;
+    int gate = 0;
+    if (warp == 8) {
+        if (lane == 0) {
+            prefetch_tmap(&tmK);
+            prefetch_tmap(&tmV);
+        }
+        gate = g_test_gate;
+        paged_schedule(p, cur, lane);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp < 8) rows_softmax<C>(p, smem, bars, tmem, warp, lane);
+    else if (warp == 8) rows_producer<C>(p, cur, gate, &tmK, &tmV, smem, bars, lane);
+    else rows_mma<C>(smem, bars, tmem, warp - 9, lane);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) {
+        __syncwarp();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 // Joins the partials of the units that several CTAs covered:
 //   O = out_scale * sum_c w_c O_c / sum_c w_c with w_c = exp(LSE_c - max LSE).
 // CTA (c, y) takes rows, a warp each, of the unit that CTA c of the kernel above
@@ -1194,8 +1744,11 @@ __global__ void __launch_bounds__(32 * kPagedMergeWarps) fmha_paged_merge_kernel
 // ---------------------------------------------------------------------------
 
 // Query rows of a unit: as many groups of 16 as a sequence's rows of a kv head
-// fill, one, two or (also for more) four.
-int paged_rows(int64_t max_q, int G) { return max_q * G <= 16 ? 16 : max_q * G <= 32 ? 32 : 64; }
+// fill, one, two or (also for more) four; 256, the kernel for chunks, where
+// sequences have 64 and more on average.
+int paged_rows(int64_t max_q, int G, int64_t N, int B) {
+    return max_q * G <= 16 ? 16 : max_q * G <= 32 ? 32 : max_q * G <= 64 || N * G < (int64_t)64 * B ? 64 : 2 * kRows;
+}
 
 using PagedKernel = void (*)(CUtensorMap, CUtensorMap, PagedParams);
 struct PagedLaunch {
@@ -1208,6 +1761,7 @@ PagedLaunch paged_launch() {
 }
 template <bool BF>
 PagedLaunch paged_kernel(int rows, int per_unit) {
+    if (rows == 2 * kRows) return {fmha_paged_rows_kernel<BF>, RowsCfg<BF>::SMEM_BYTES, kRowsThreads};
     return rows == 64 ? paged_launch<BF, 4, 16>() : rows == 32 ? paged_launch<BF, 2, 16>()
            : per_unit <= 4 ? paged_launch<BF, 1, 4>() : per_unit <= 8 ? paged_launch<BF, 1, 8>() : paged_launch<BF, 1, 16>();
 }
@@ -1225,7 +1779,7 @@ using namespace fmha;
 extern "C" size_t fmha_page_workspace_size(int max_q, int H, int H_k) {
     if (max_q <= 0 || H <= 0 || H_k <= 0 || H % H_k != 0 || H / H_k > kRows) return 0;
     // two partials a CTA: an fp32 row of O and its LSE for every row of a unit, and whose they are
-    return (size_t)2 * kPagedMaxCtas * (paged_rows(max_q, H / H_k) * (kD + 1) * sizeof(float) + sizeof(PagedMeta));
+    return (size_t)2 * kPagedMaxCtas * (paged_rows(max_q, H / H_k, 64, 1) * (kD + 1) * sizeof(float) + sizeof(PagedMeta));
 }
 
 extern "C" int fmha_page_fwd(fmha_tensor q, const void *k_pages, const void *v_pages, const float *k_scale,
@@ -1270,7 +1824,7 @@ extern "C" int fmha_page_fwd(fmha_tensor q, const void *k_pages, const void *v_p
     const int sms = sm_count();
     if (sms <= 0) return FMHA_ERR_CUDA;
 
-    const int G = H / H_k, R = paged_rows(max_q, G);
+    const int G = H / H_k, R = paged_rows(max_q, G, N, B);
     PagedParams p{};
     p.q = static_cast<const uint8_t *>(q.data);
     p.o = o.data;

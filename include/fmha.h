@@ -442,7 +442,7 @@ int fmha_cache_evict(fmha_tensor k_cache, fmha_tensor v_cache, const float *acc,
  * 64 or 128), held as e4m3 codes with one scale per page and kv head:
  *   k_pages, v_pages   e4m3 bytes [n_pages, H_k, P, 128]
  *   k_scale, v_scale   float [n_pages, H_k]
- * and a key is k_scale[page, g] * code.  Row e of a block table, int32
+ * and a key is k_scale[page, g] * code, with scales of 0 or more.  Row e of a block table, int32
  * [B_table, max_pages], lists the pages of a sequence's tokens in order; the
  * slot of a token is page * P + its row there.  A step is fmha_page_plan (which
  * tokens come, where they go), fmha_rope (their positions), fmha_page_write
@@ -549,9 +549,9 @@ int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_t k_head_st
  * page_size below 2^31, max_pages * page_size at most 2^30.  Data pointers
  * 16-byte aligned, the others 4-byte.  o, lse and the workspace are apart from
  * the inputs and from one another.
- * q and the codes enter the products as they are (elements of q below 2^-13,
- * f16 2^-10, of their row's largest are rounded, by 2^-21 of it at most), scores,
- * sums and O are fp32; a weight is rounded by 2^-8 of itself at most, and below
+ * q and the codes enter the products as they are (elements of q below 2^-9,
+ * f16 2^-6, of their row's largest are rounded, by 2^-17 of it at most), scores,
+ * sums and O are fp32; a weight is rounded by 2^-7 of itself at most, and below
  * that all of them together by 2^-6 of the row's sum.  A q row that holds an
  * infinity or a NaN gives NaN.  v_scale counts as 2^-60 or 2^60 outside these.
  * Requirements the host cannot check: 0 <= seqlen[b] <= max_pages * page_size,
@@ -562,7 +562,7 @@ int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_t k_head_st
  * cached rows at or past a sequence's length are never used, and may hold any
  * bits; a value that only some of a call's rows see must be finite.
  *
- * workspace: fmha_page_workspace_size(max_q, H, H_k) bytes (10.1 MB at most),
+ * workspace: fmha_page_workspace_size(max_q, H, H_k) bytes (40.2 MB at most),
  * 256-byte aligned, no initialisation, not shared with a concurrent call.  The
  * call allocates nothing and is asynchronous on `stream` (two kernels).
  * Returns FMHA_OK, FMHA_ERR_INVALID_ARG (bad sizes or pointers, scale not

@@ -113,10 +113,11 @@ def draw_pages(gen, n_pages, H_k, P, lo=-8, hi=-4):
     return c, s
 
 
-def attend(q, kc, ks, vc, vs, see, scale, out_scale, dtype):
+def attend(q, kc, ks, vc, vs, see, scale, out_scale, dtype, chunk=False):
     """One sequence and kv head in 64 bits: q [n, G, 128]; kc, vc codes' values
-    [L, 128]; ks, vs their scales [L]; see [n, L].  Returns O, LSE and the
-    bounds on their errors."""
+    [L, 128]; ks, vs their scales [L]; see [n, L]; chunk: sequences of 64 rows and
+    more, which a kernel of their own takes.  Returns O, LSE and the bounds on
+    their errors."""
     n, G, _ = q.shape
     L = kc.shape[0]
     keys, vals = kc * ks[:, None], vc * vs[:, None]
@@ -131,16 +132,17 @@ def attend(q, kc, ks, vc, vs, see, scale, out_scale, dtype):
     o = torch.einsum("tgk,kd->tgd", w, vals) * out_scale
     seen = see[:, None, :].double()
     # a score: 128 products summed in fp32, each addition off by 2^-23 of the
-    # partial sum; elements of q by 2^-21 of the row's largest; then a few fp32
+    # partial sum; elements of q by 2^-21 (chunk: 2^-17) of the row's largest; then a few fp32
     # roundings of the score, of its exponential and of the sums
     a = (torch.einsum("tgd,kd->tgk", q.abs(), keys.abs()) * scale * seen).amax(-1)
     top = q.abs().amax(-1)
-    ds = (a * 134 * 2.0 ** -23 + top * 2.0 ** -21 * (keys.abs().sum(-1)[None, None] * seen).amax(-1) * scale +
+    ds = (a * 134 * 2.0 ** -23 + top * 2.0 ** (-17 if chunk else -21) * (keys.abs().sum(-1)[None, None] * seen).amax(-1) * scale +
           lse.abs().nan_to_num(0, 0, 0) * 2.0 ** -21 + 1e-5)
-    # a weight: two terms of four bits (2^-8) from f16's eleven (2^-11); and
-    # where the terms end, 2^-14 where the largest weight is 2^4 or more
+    # a weight: two terms of four bits (2^-8; chunk: of four and three, 2^-7) from
+    # f16's eleven (2^-11); and where the terms end, 2^-14 (2^-17) where the
+    # largest weight is 2^4 or more
     ab = torch.einsum("tgk,kd->tgd", w, vals.abs()) * abs(out_scale)
     low = (w * vs).amax(-1, keepdim=True) * torch.einsum("tgk,kd->tgd", seen.expand(n, G, L), vc.abs()) * abs(out_scale)
-    tol = ab * (2.0 ** -8 + 2.0 ** -11 + 2 * ds[..., None]) + low * 2.0 ** -18
+    tol = ab * (2.0 ** (-7 if chunk else -8) + 2.0 ** -11 + 2 * ds[..., None]) + low * 2.0 ** -18
     tol = tol + (o.abs() + tol) * cu.HALF[dtype] + cu.SUBHALF[dtype]
     return o, lse, tol, ds

@@ -84,6 +84,7 @@ def sequence(c, b, g, x):
 def check(c, o, lse, scale=128 ** -0.5, out_scale=1.0, rows=None):
     o, lse = o.cpu(), lse.cpu()
     G, at = c["H"] // c["H_k"], 0
+    chunk = max(c["n"]) * G > 64 and len(c["q"]) * G >= 64 * len(c["L"])
     for b, (L, n) in enumerate(zip(c["L"], c["n"])):
         pick = torch.arange(n) if rows is None else torch.tensor(sorted({r for r in rows(n) if r < n}), dtype=torch.long)
         j, t = torch.arange(L), pick[:, None]
@@ -91,7 +92,7 @@ def check(c, o, lse, scale=128 ** -0.5, out_scale=1.0, rows=None):
         for g in range(c["H_k"]):
             h = slice(g * G, (g + 1) * G)
             want, wl, tol, tl = pu.attend(cu.f64(c["q"][at + pick][:, h]), *sequence(c, b, g, "k"), *sequence(c, b, g, "v"), see,
-                                          scale, out_scale, c["dtype"])
+                                          scale, out_scale, c["dtype"], chunk)
             cu.close(cu.f64(o[at + pick][:, h]), want, tol, f"O of sequence {b} head {g}")
             cu.close(lse[at + pick][:, h].double(), wl, tl, f"LSE of sequence {b} head {g}")
         at += n
@@ -133,6 +134,11 @@ CASES = {
     "peaked": dict(dtype="bf16", H=8, H_k=2, P=64, lengths=[2999, 1500], q_scale=30.0),
     "flat": dict(dtype="f16", H=8, H_k=2, P=64, lengths=[2999], q_scale=2.0 ** -10),
     "scales_apart": dict(dtype="bf16", H=8, H_k=2, P=16, lengths=[777, 400], news=[3, 1], lo=-20, hi=4),
+    "chunk_of_one_head": dict(dtype="bf16", H=2, H_k=2, P=16, lengths=[700, 300], news=[300, 257]),
+    "chunk_of_half_units": dict(dtype="f16", H=8, H_k=2, P=32, lengths=[400, 130, 900], news=[31, 33, 97]),
+    "chunk_scales_apart": dict(dtype="bf16", H=16, H_k=2, P=16, lengths=[777, 400], news=[70, 40], lo=-20, hi=4),
+    "chunk_peaked": dict(dtype="f16", H=8, H_k=2, P=128, lengths=[1999], news=[140], q_scale=30.0),
+    "chunk_and_tokens": dict(dtype="bf16", H=8, H_k=2, P=64, lengths=[900, 800, 700, 1], news=[120, 1, 1, 1]),
     "odd_rows_of_a_unit": dict(dtype="bf16", H=16, H_k=2, P=64, lengths=[600], news=[27]),
 }
 
@@ -179,7 +185,7 @@ def test_pages_of_zeros(fm):
 
 
 @pytest.mark.parametrize("shape", ["sink", "rising", "falling", "steps"])
-@pytest.mark.parametrize("n", [1, 5])
+@pytest.mark.parametrize("n", [1, 5, 40])
 def test_small_weights_that_together_count(fm, shape, n):
     """A key far above thousands of equal ones, and scores that rise or fall over the context."""
     L, c = 16384, make("bf16", 16, 2, 64, [16384], [n], seed=7)
@@ -211,12 +217,13 @@ def test_small_weights_that_together_count(fm, shape, n):
     check(c, o, lse)
 
 
-def test_rows_that_are_not_finite(fm):
-    c = make("bf16", 8, 2, 32, [300, 200], [4, 1], seed=8)
+@pytest.mark.parametrize("n", [4, 150])
+def test_rows_that_are_not_finite(fm, n):
+    c = make("bf16", 8, 2, 32, [300, 200], [n, 1], seed=8)
     c["q"][1, 3, 5] = float("nan")
     c["q"][2, 0, 7] = float("inf")
     o, lse, status = run(fm, c)
-    bad = torch.zeros(5, 8, dtype=torch.bool)
+    bad = torch.zeros(n + 1, 8, dtype=torch.bool)
     bad[1, 3] = bad[2, 0] = True
     assert torch.equal(torch.isnan(o).any(-1).cpu(), bad) and torch.equal(torch.isnan(o).all(-1).cpu(), bad)
     assert torch.equal(torch.isnan(lse).cpu(), bad)
@@ -225,7 +232,7 @@ def test_rows_that_are_not_finite(fm):
     assert torch.equal(o.cpu()[~bad], o2.cpu()[~bad]) and torch.equal(lse.cpu()[~bad], lse2.cpu()[~bad])
 
 
-@pytest.mark.parametrize("news", [None, [5, 30, 1]])
+@pytest.mark.parametrize("news", [None, [5, 30, 1], [200, 100, 77]])
 def test_it_repeats_bit_for_bit(fm, news):
     c = make("bf16", 32, 8, 64, [5000, 3333, 1000], news, seed=9)
     o, lse, _ = run(fm, c)
@@ -234,9 +241,10 @@ def test_it_repeats_bit_for_bit(fm, news):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("k", [1, 40])
 @pytest.mark.parametrize("what", ["length", "negative", "entry", "page", "rows", "order", "most"])
-def test_values_outside_their_bounds_are_reported(fm, what):
-    c = make("bf16", 8, 2, 32, [300, 200, 100], [2, 3, 1], seed=10, entries=[0, 1, 2])
+def test_values_outside_their_bounds_are_reported(fm, what, k):
+    c = make("bf16", 8, 2, 32, [300, 200, 100], [2 * k, 3 * k, k], seed=10, entries=[0, 1, 2])
     d, (o, lse) = on_gpu(c), outputs(c)
     table, seqlen, cu_q, idx = d["args"][5], d["args"][6], d["kw"]["cu_q"], d["kw"]["batch_idx"]
     if what == "length":
@@ -253,14 +261,14 @@ def test_values_outside_their_bounds_are_reported(fm, what):
     elif what == "order":
         cu_q[2] = 1
     else:
-        d["kw"]["max_q"] = 2
+        d["kw"]["max_q"] = 2 * k
     fm.page_fwd(*d["args"], **d["kw"], out=o, lse=lse)
     torch.cuda.synchronize()
     assert fm.device_status(reset=True) == fm.ERR_INVALID_ARG
-    one = dict(c, L=[300], n=[2], q=c["q"][:2])          # the first sequence is served all the same
-    check(one, o[:2], lse[:2])
+    one = dict(c, L=[300], n=[2 * k], q=c["q"][:2 * k])  # the first sequence is served all the same
+    check(one, o[:2 * k], lse[:2 * k])
     if what in ("negative", "entry"):
-        assert bool((o[2:5] == 0).all())
+        assert bool((o[2 * k:5 * k] == 0).all())
     if what == "page":                                   # zeros for that page
         c["kc"].view(torch.uint8)[c["table"][1, 2].long()] = 0
         c["vc"].view(torch.uint8)[c["table"][1, 2].long()] = 0
