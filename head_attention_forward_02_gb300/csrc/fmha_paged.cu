@@ -1192,7 +1192,6 @@ struct RowsBars {
     uint32_t tmem_base;
     int abort;
     float scale[kRowsSlots][2][8];       // k_scale, v_scale of a V slot's pages
-    float qscale[2 * kRows];
 };
 static_assert(sizeof(RowsBars) <= 4096, "barrier block");
 
@@ -1371,33 +1370,33 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
     mbar_wait_drain(smem_u32(&bars->drain[x]), 0);
 }
 
-// Eight rows of q, r0 .. r0 + 7 of the unit, as terms: rows of the group's tiles.
+// A warp's 32 rows of the unit's q, from r0 on, as terms in the group's tiles; at:
+// of the lane's row, q row * H + head (-1: none).  All loads go out first (eight at
+// a time, with a division a row, took 9 us a unit).  g: the lane's row's scale.
 template <class C>
-__device__ __forceinline__ void rows_terms(const PagedParams &p, uint8_t *tile, float *qscale, const PagedItem &it, int r0, int lane) {
-    uint2 v[8];
+__device__ __forceinline__ void rows_terms(const PagedParams &p, uint8_t *tile, int at, int r0, int lane, float &g) {
+    uint2 v[32];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int r = r0 + k, t = p.subs == 1 ? r / p.G : 0;
-        v[k] = r < it.rows ? *reinterpret_cast<const uint2 *>(
-                                 p.q + (((int64_t)(it.row0 + t) * p.H + it.h0 + r - t * p.G) * kD + lane * 4) * 2)
-                           : make_uint2(0u, 0u);
+    for (int k = 0; k < 32; ++k) {
+        const int a = __shfl_sync(0xffffffffu, at, k);
+        v[k] = a >= 0 ? *reinterpret_cast<const uint2 *>(p.q + ((int64_t)a * kD + lane * 4) * 2) : make_uint2(0u, 0u);
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        float y[4], g;
-        row_scaled<C::BF>(v[k], y, g);
+    for (int k = 0; k < 32; ++k) {
+        float y[4], gk;
+        row_scaled<C::BF>(v[k], y, gk);
+        if (lane == k) g = gk;
         __half2 rest[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const uint32_t h = pack2<false>(y[2 * j], y[2 * j + 1]);
             rest[j] = *reinterpret_cast<const __half2 *>(&h);
         }
-        const int row = (r0 + k) & (kRows - 1);
+        const int row = r0 + k;
 #pragma unroll
         for (int term = 0; term < C::NT; ++term)
             *reinterpret_cast<uint32_t *>(tile + term * kPanelBytes + row * 128 +
                                           ((((lane >> 2) ^ (row & 7)) << 4) | ((lane & 3) << 2))) = take_term(rest);
-        if (lane == 0) qscale[r0 + k] = g;
     }
 }
 
@@ -1425,18 +1424,18 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
             c += it.t1 - it.t0;
             continue;
         }
+        const int tok = p.subs == 1 ? r / p.G : 0;
+        const bool row_ok = r < it.rows;
+        const int at = row_ok ? (it.row0 + tok) * p.H + it.h0 + r - tok * p.G : -1;
         // this warp's rows of q; the S MMAs of the item before are done, their scores were read
-        for (int k = 0; k < 32; k += 8)
-            rows_terms<C>(p, smem + x * C::Q_BYTES, bars->qscale, it, x * kRows + (warp & 3) * 32 + k, lane);
+        float g = 0.f;
+        rows_terms<C>(p, smem + x * C::Q_BYTES, at, (warp & 3) * 32, lane, g);
         proxy_fence();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[x]));
-        const int tok = p.subs == 1 ? r / p.G : 0;
-        const int64_t at = (int64_t)(it.row0 + tok) * p.H + it.h0 + r - tok * p.G;
-        const bool row_ok = r < it.rows;
         const bool work = __any_sync(0xffffffffu, row_ok);   // else the warp only keeps step
         const int lim = it.base + it.tok0 + tok;        // last key it sees
-        const float fq = p.c * bars->qscale[r];
+        const float fq = p.c * g;
         float m = -INFINITY, M = -INFINITY;             // reference (log2 units) of P and O, and the highest so far
         float l = 0.f;                                  // row sum
         int since = kRowsTiles;
@@ -1474,10 +1473,11 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
             uint32_t s[4][32];
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_ld32(s_tm + 32 * q, s[q]);
-            // factor and summand of 16 columns, a page or a part of one (looked up twice: they do not fit the registers)
-            const volatile float *ks = bars->scale[vst][0], *vs = bars->scale[vst][1];
-            auto factor = [&](int u) { return fmaxf(fq * ks[(16 * u) >> p.shift], FLT_MIN); };   // not 0: -inf stays -inf
-            auto summand = [&](int u) { return __log2f(fminf(fmaxf(vs[(16 * u) >> p.shift], kLeastScale), kMostScale)); };
+            // k_scale and log2 of v_scale of 16 columns, a page or a part of one: in lane u those of columns 16 u ...
+            const float lane_ks = bars->scale[vst][0][(16 * (lane & 7)) >> p.shift];
+            const float lane_vs = __log2f(fminf(fmaxf(bars->scale[vst][1][(16 * (lane & 7)) >> p.shift], kLeastScale), kMostScale));
+            auto factor = [&](int u) { return fmaxf(fq * __shfl_sync(0xffffffffu, lane_ks, u), FLT_MIN); };   // not 0: -inf stays -inf
+            auto summand = [&](int u) { return __shfl_sync(0xffffffffu, lane_vs, u); };
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_wait_ld(s[q]);
             const int cnt = imin(nk, lim - t * kRows + 1);   // visible keys
@@ -1595,7 +1595,7 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
 #pragma unroll
                     for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 } else if (row_ok) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) + at * kD + 32 * q);
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.o) + (int64_t)at * kD + 32 * q);
                     uint32_t w[16];
 #pragma unroll
                     for (int k = 0; k < 16; ++k) w[k] = pack2<C::BF>(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
@@ -1745,9 +1745,11 @@ __global__ void __launch_bounds__(32 * kPagedMergeWarps) fmha_paged_merge_kernel
 
 // Query rows of a unit: as many groups of 16 as a sequence's rows of a kv head
 // fill, one, two or (also for more) four; 256, the kernel for chunks, where
-// sequences have 64 and more on average.
+// sequences have 112 and more on average (four sequences of 8192 keys, 4 heads a
+// kv head, four groups / chunks in us: 20 tokens each 47.9 / 51.9, 32 55.5 / 53.4,
+// 64 83.6 / 65.3).
 int paged_rows(int64_t max_q, int G, int64_t N, int B) {
-    return max_q * G <= 16 ? 16 : max_q * G <= 32 ? 32 : max_q * G <= 64 || N * G < (int64_t)64 * B ? 64 : 2 * kRows;
+    return max_q * G <= 16 ? 16 : max_q * G <= 32 ? 32 : max_q * G <= 64 || N * G < (int64_t)112 * B ? 64 : 2 * kRows;
 }
 
 using PagedKernel = void (*)(CUtensorMap, CUtensorMap, PagedParams);
@@ -1779,7 +1781,7 @@ using namespace fmha;
 extern "C" size_t fmha_page_workspace_size(int max_q, int H, int H_k) {
     if (max_q <= 0 || H <= 0 || H_k <= 0 || H % H_k != 0 || H / H_k > kRows) return 0;
     // two partials a CTA: an fp32 row of O and its LSE for every row of a unit, and whose they are
-    return (size_t)2 * kPagedMaxCtas * (paged_rows(max_q, H / H_k, 64, 1) * (kD + 1) * sizeof(float) + sizeof(PagedMeta));
+    return (size_t)2 * kPagedMaxCtas * (paged_rows(max_q, H / H_k, 112, 1) * (kD + 1) * sizeof(float) + sizeof(PagedMeta));
 }
 
 extern "C" int fmha_page_fwd(fmha_tensor q, const void *k_pages, const void *v_pages, const float *k_scale,

@@ -115,8 +115,7 @@ def draw_pages(gen, n_pages, H_k, P, lo=-8, hi=-4):
 
 def attend(q, kc, ks, vc, vs, see, scale, out_scale, dtype, chunk=False):
     """One sequence and kv head in 64 bits: q [n, G, 128]; kc, vc codes' values
-    [L, 128]; ks, vs their scales [L]; see [n, L]; chunk: sequences of 64 rows and
-    more, which a kernel of their own takes.  Returns O, LSE and the bounds on
+    [L, 128]; ks, vs their scales [L]; see [n, L]; chunk: sequences of many rows, which a kernel of their own takes.  Returns O, LSE and the bounds on
     their errors."""
     n, G, _ = q.shape
     L = kc.shape[0]
