@@ -1155,8 +1155,7 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 // the rows as M: a thread is a row (TMEM lane), its reference, sum and limit are
 // in registers, nothing is exchanged, and a page's scale is one factor for its
 // columns.  Two row blocks of 128 share a tile, each with its softmax group and
-// MMA issuer, which take turns, so that one group's MMAs run under the other's
-// softmax.  The terms are passes of their own into the same accumulator:
+// MMA issuer.  The terms are passes of their own into the same accumulator:
 //   S  = Q_0 K^T + Q_1 K^T (+ Q_2 K^T, f16), without a factor of 16, so that elements
 //        of q below 2^-9 (f16 2^-6) of their row's largest are off by 2^-17 of it;
 //   O += P_0 V + P_1 V, where P_1, what e4m3 left of a weight, is e5m2: its
@@ -1166,7 +1165,7 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 // tile, which is the time of the two that bf16 operands would take.
 // ---------------------------------------------------------------------------
 
-constexpr int kRowsSlots = 9;            // ring of K and V tiles
+constexpr int kRowsSlots = 5;            // ring of K and V tiles at most
 constexpr int kRowsTiles = 64;           // tiles that a reference serves at most
 constexpr int kRowsThreads = 352;        // two softmax groups of four warps, producer, an MMA issuer a group
 
@@ -1176,16 +1175,16 @@ struct RowsCfg {
     static constexpr int NT = BF ? 2 : 3;                     // terms of q
     static constexpr int R = 2 * kRows;
     static constexpr int Q_BYTES = NT * kPanelBytes;          // of a block
-    static constexpr int OFF_KV = 2 * Q_BYTES;
-    static constexpr int NS_FIT = (226 * 1024 - 4096 - OFF_KV) / kPanelBytes;
-    static constexpr int NS = NS_FIT < kRowsSlots ? NS_FIT : kRowsSlots;
+    static constexpr int OFF_P = 2 * Q_BYTES;                 // both terms of a block's P
+    static constexpr int OFF_KV = OFF_P + 4 * kPanelBytes;
+    static constexpr int NS = (226 * 1024 - 4096 - OFF_KV) / kPanelBytes;
     static constexpr int OFF_BARS = OFF_KV + NS * kPanelBytes;
     static constexpr int SMEM_BYTES = OFF_BARS + 4096 + 1024;
-    static_assert(SMEM_BYTES <= 227 * 1024 && NS >= 4, "shared memory");
+    static_assert(SMEM_BYTES <= 227 * 1024 && NS >= 3 && NS <= kRowsSlots, "shared memory");
 };
 
 struct RowsBars {
-    uint64_t q_full[2], drain[2], s_full[2], p_full[2][2], o_full[2], turn[2];   // by group; p_full by half
+    uint64_t q_full[2], drain[2], s_full[2], s_free[2], p_full[2][2], pv_done[2];   // by group; p_full by half
     uint64_t kv_full[kRowsSlots], kv_empty[kRowsSlots];
     uint64_t item_full[kPagedItems], item_empty[kPagedItems];
     PagedItem item[kPagedItems];
@@ -1276,9 +1275,10 @@ __device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, 
     }
 }
 
-// MMA issuer of group x.  MMAs of one warp execute in issue order, so S of the
-// next tile may overwrite the columns of P once P V is issued, and S being there
-// says that the P V before it is.
+// MMA issuer of group x.  P lies in shared memory, apart from S, so that S of the
+// next tile is issued as soon as the softmax has this one's in registers, and
+// P V while it is at the next: with P over S in TMEM a group waited 1700 of 5700
+// cycles a tile for P V and S, one after the other (256 us for 4 chunks of 512).
 template <class C>
 __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x, int lane) {
     volatile int *abort_flag = &bars->abort;
@@ -1289,12 +1289,12 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
     const uint64_t q = smem_desc(smem_u32(smem + x * C::Q_BYTES), 16, 1024);
     const uint64_t k0 = smem_desc(smem_u32(smem + C::OFF_KV), 16, 1024);
     const uint64_t v0 = smem_desc(smem_u32(smem + C::OFF_KV), kPanelBytes, 1024);
-    uint32_t c = 0, m = 0, turns = 0, items = 0;   // tiles; of this group; its turns; items that it had rows of
+    const uint64_t p0 = smem_desc(smem_u32(smem + C::OFF_P + x * 2 * kPanelBytes), 16, 1024);
+    uint32_t c = 0, m = 0, items = 0;    // tiles; of this group; items that it had rows of
     bool ok = true;
     PagedItem it;
     for (uint32_t i = 0; ok && rows_take(bars, i, it, abort_flag, lane); ++i) {
-        const bool both = it.rows > kRows;
-        if (x == 1 && !both) {           // nothing to do with these tiles
+        if (x == 1 && it.rows <= kRows) {   // nothing to do with these tiles
             for (int t = it.t0; ok && t < it.t1; ++t, ++c)
                 for (uint32_t n = 2 * c; ok && n < 2 * c + 2; ++n) {
                     ok = wait_all(smem_u32(&bars->kv_full[n % C::NS]), (n / C::NS) & 1, abort_flag);
@@ -1306,21 +1306,37 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
             ok = false;
             break;
         }
-        bool first = true;
         for (int t = it.t0; ok && t <= it.t1; ++t) {
-            // the tiles of this step first: their waits are off the chain
-            const uint32_t nk = 2 * c, nv = 2 * c - 1, kst = nk % C::NS, vst = nv % C::NS;
-            if ((t > it.t0 && !wait_all(smem_u32(&bars->kv_full[vst]), (nv / C::NS) & 1, abort_flag)) ||
-                (t < it.t1 && !wait_all(smem_u32(&bars->kv_full[kst]), (nk / C::NS) & 1, abort_flag))) {
-                ok = false;
-                break;
+            if (t < it.t1) {             // S of this tile
+                const uint32_t n = 2 * c, st = n % C::NS;
+                if (!wait_all(smem_u32(&bars->kv_full[st]), (n / C::NS) & 1, abort_flag) ||
+                    (m > 0 && !wait_all(smem_u32(&bars->s_free[x]), (m - 1) & 1, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t k = k0 + ((st * kPanelBytes) >> 4);
+#pragma unroll
+                for (int term = 0; term < C::NT; ++term)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ss<true>(s_tm, q + ((term * kPanelBytes + kk * 32) >> 4), k + ((kk * 32) >> 4), kIdS,
+                                     term > 0 || kk > 0 ? 1u : 0u);
+                tc_commit(smem_u32(&bars->s_full[x]));
+                tc_commit(smem_u32(&bars->kv_empty[st]));
+                ++c;
+                ++m;
             }
-            if (t > it.t0) {             // P V of the tile before
+            if (t > it.t0) {             // P V of the tile before, which is tile m - 1, or m - 2 if S of this one was issued
+                const uint32_t mm = m - (t < it.t1 ? 2 : 1), n = 2 * (c - (t < it.t1 ? 2 : 1)) + 1, st = n % C::NS;
+                if (!wait_all(smem_u32(&bars->kv_full[st]), (n / C::NS) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
                 const int halves = it.L - (t - 1) * kRows > kRows / 2 ? 2 : 1;
-                const uint64_t v = v0 + ((vst * kPanelBytes) >> 4);
+                const uint64_t v = v0 + ((st * kPanelBytes) >> 4);
                 for (int h = 0; h < halves; ++h) {
-                    if (!wait_all(smem_u32(&bars->p_full[x][h]), (m - 1) & 1, abort_flag) ||
-                        (both && h == 0 && !wait_all(smem_u32(&bars->turn[x]), (turns & 1) ^ (x ^ 1), abort_flag))) {
+                    if (!wait_all(smem_u32(&bars->p_full[x][h]), mm & 1, abort_flag)) {
                         ok = false;
                         break;
                     }
@@ -1328,42 +1344,16 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
 #pragma unroll
                     for (int term = 0; term < 2; ++term)
 #pragma unroll
-                        for (int kk = 0; kk < 2; ++kk)       // 32 keys: 8 columns of P, 32 rows of V
-                            mma_ts<true>(o_tm, s_tm + term * 32 + h * 16 + kk * 8, v + (((h * 2 + kk) * 32 * 128) >> 4),
-                                         term ? kIdP1 : kIdP0, !first || h > 0 || term > 0 || kk > 0 ? 1u : 0u);
+                        for (int kk = 0; kk < 2; ++kk)       // 32 keys: 32 bytes of P's rows, 32 rows of V
+                            mma_ss<true>(o_tm, p0 + ((term * kPanelBytes + (h * 2 + kk) * 32) >> 4),
+                                         v + (((h * 2 + kk) * 32 * 128) >> 4), term ? kIdP1 : kIdP0,
+                                         t - 1 > it.t0 || h > 0 || term > 0 || kk > 0 ? 1u : 0u);
                 }
                 if (!ok) break;
-                first = false;
-            }
-            if (both && t == it.t0 && !wait_all(smem_u32(&bars->turn[x]), (turns & 1) ^ (x ^ 1), abort_flag)) {
-                ok = false;
-                break;
-            }
-            if (t < it.t1) {
-                tc_fence_after();
-                const uint64_t k = k0 + ((kst * kPanelBytes) >> 4);
-#pragma unroll
-                for (int term = 0; term < C::NT; ++term)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        mma_ss<true>(s_tm, q + ((term * kPanelBytes + kk * 32) >> 4), k + ((kk * 32) >> 4), kIdS,
-                                     term > 0 || kk > 0 ? 1u : 0u);
-                        // the other warp wakes up behind the MMAs still to issue
-                        if (both && term == C::NT - 1 && kk == 1 && lane == 0) mbar_arrive(smem_u32(&bars->turn[x ^ 1]));
-                    }
-                tc_commit(smem_u32(&bars->s_full[x]));       // also: P V of the tile before is done
-                tc_commit(smem_u32(&bars->kv_empty[kst]));
-                ++c;
-                ++m;
-            }
-            if (t > it.t0) tc_commit(smem_u32(&bars->kv_empty[vst]));
-            if (both) {
-                if (t >= it.t1 && lane == 0) mbar_arrive(smem_u32(&bars->turn[x ^ 1]));
-                ++turns;
+                tc_commit(smem_u32(&bars->pv_done[x]));
+                tc_commit(smem_u32(&bars->kv_empty[st]));
             }
         }
-        if (!ok) break;
-        tc_commit(smem_u32(&bars->o_full[x]));
     }
     // no tensor-core operation may be in flight when TMEM is released
     tc_commit(smem_u32(&bars->drain[x]));
@@ -1416,7 +1406,8 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
     const int x = warp >> 2, lr = (warp & 3) * 32 + lane, r = x * kRows + lr;      // row of the block, of the unit
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_tm = lane_base + x * kRows, o_tm = lane_base + 2 * kRows + x * kD;
-    uint32_t c = 0, m_tiles = 0, items = 0;             // tiles; of this group; items that it had rows of
+    uint8_t *prow = smem + C::OFF_P + x * 2 * kPanelBytes + lr * 128;
+    uint32_t c = 0, m_tiles = 0;                        // tiles; of this group
     int parts = 0;                                      // bit s: slot s of this CTA holds a partial
     PagedItem it;
     for (uint32_t i = 0; rows_take(bars, i, it, abort_flag, lane); ++i) {
@@ -1463,6 +1454,12 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
             if (!work) {
                 tc_fence_before();
                 __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[x]));
+                // S comes ahead of P V: not a tile ahead of the warps that write P
+                if (t > it.t0 && !wait_all(smem_u32(&bars->pv_done[x]), (m_tiles - 1) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
                 if (lane == 0) {
                     mbar_arrive(smem_u32(&bars->p_full[x][0]));
                     mbar_arrive(smem_u32(&bars->p_full[x][1]));
@@ -1480,6 +1477,9 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
             auto summand = [&](int u) { return __shfl_sync(0xffffffffu, lane_vs, u); };
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_wait_ld(s[q]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[x]));
             const int cnt = imin(nk, lim - t * kRows + 1);   // visible keys
             if (__any_sync(0xffffffffu, cnt < kRows)) {
 #pragma unroll
@@ -1503,6 +1503,11 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
             const bool need = tmax > m + kGrown || since == kRowsTiles;
             if (since == kRowsTiles) since = 0;
             ++since;
+            // O, and the room for P, are free once the P V of the tile before is done
+            if (t > it.t0 && !wait_all(smem_u32(&bars->pv_done[x]), (m_tiles - 1) & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
             if (__any_sync(0xffffffffu, need)) {
                 float alpha = 1.f;
                 if (need) {
@@ -1513,7 +1518,7 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
                     l *= alpha;
                 }
                 if (t > it.t0) {
-                    // the P V of the tile before is in O: S, issued behind it, is there
+                    tc_fence_after();
 #pragma unroll 1
                     for (int q = 0; q < 8; ++q) {
                         uint32_t o[16];
@@ -1558,11 +1563,19 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
                             unpack_f2(add_f2(sum[0], sum[1]), a, b);
                             l = fmaf(a + b, ex2(-du), l);
                         }
-                        tmem_st8(s_tm + 8 * q, w0);
-                        tmem_st8(s_tm + 32 + 8 * q, w1);
+                        // 16-byte chunks 2 q and 2 q + 1 of the row, swizzled
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(prow + (((2 * q + u) ^ (lr & 7)) << 4));
+                            dst[0] = make_uint4(w0[4 * u], w0[4 * u + 1], w0[4 * u + 2], w0[4 * u + 3]);
+                            dst[kPanelBytes / 16] = make_uint4(w1[4 * u], w1[4 * u + 1], w1[4 * u + 2], w1[4 * u + 3]);
+                        }
                     }
-                    tmem_wait_st();
-                    tc_fence_before();
+                    proxy_fence();
+                    if (h == 0) {        // O may have been stored to above
+                        tmem_wait_st();
+                        tc_fence_before();
+                    }
                     __syncwarp();
                 }
                 if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[x][h]));
@@ -1571,7 +1584,7 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
         if (!ok) break;
 
         // epilogue: O of a unit that this CTA covers alone, else a partial
-        if (!wait_all(smem_u32(&bars->o_full[x]), items++ & 1, abort_flag)) break;
+        if (!wait_all(smem_u32(&bars->pv_done[x]), (m_tiles - 1) & 1, abort_flag)) break;
         const bool whole = it.t1 - it.t0 == it.nt;
         const int part = 2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
         if (threadIdx.x == 0 && !whole) {
@@ -1630,9 +1643,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             mbar_init(smem_u32(&bars->s_full[x]), 1);
             mbar_init(smem_u32(&bars->p_full[x][0]), 4);
             mbar_init(smem_u32(&bars->p_full[x][1]), 4);
-            mbar_init(smem_u32(&bars->o_full[x]), 1);
+            mbar_init(smem_u32(&bars->s_free[x]), 4);
+            mbar_init(smem_u32(&bars->pv_done[x]), 1);
             mbar_init(smem_u32(&bars->drain[x]), 1);
-            mbar_init(smem_u32(&bars->turn[x]), 1);
         }
         for (int s = 0; s < C::NS; ++s) {
             mbar_init(smem_u32(&bars->kv_full[s]), 33);          // the bytes, and the lanes' scales
