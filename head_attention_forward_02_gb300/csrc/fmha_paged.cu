@@ -255,16 +255,29 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile
     return __all_sync(0xffffffffu, r);
 }
 
-// Two weights as two e4m3 terms each (first weight in the low byte): p = hi +
-// mid / 16, by way of f16, whose 11 bits hold a rest exactly.
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &mid) {
-    const uint32_t h = pack2<false>(a, b);
-    const __half2 p = *reinterpret_cast<const __half2 *>(&h);
-    const __nv_fp8x2_storage_t f = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(p), __NV_SATFINITE, __NV_E4M3);
-    const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2(f, __NV_E4M3));
-    const __half2 rest = __hmul2(__hsub2(p, back), __float2half2_rn(16.f));
-    hi = f;
-    mid = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
+// Four weights as two terms each (first weight in the low byte), by way of f16,
+// whose 11 bits hold a rest exactly: p = hi + mid / 16 in e4m3, or, WIDE, hi + mid
+// with mid in e5m2.  In one piece of PTX, since a 16-bit code that passes through
+// C++ costs an instruction to widen it.
+template <bool WIDE>
+__device__ __forceinline__ void split4(const float (&e)[4], uint32_t &hi, uint32_t &mid) {
+    const uint32_t p = pack2<false>(e[0], e[1]), q = pack2<false>(e[2], e[3]);
+    if constexpr (WIDE) {
+        asm("{\n.reg .b16 a, b;\n.reg .b32 x, y;\n"
+            "cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\ncvt.rn.satfinite.e4m3x2.f16x2 b, %3;\nmov.b32 %0, {a, b};\n"
+            "cvt.rn.f16x2.e4m3x2 x, a;\ncvt.rn.f16x2.e4m3x2 y, b;\nsub.rn.f16x2 x, %2, x;\nsub.rn.f16x2 y, %3, y;\n"
+            "cvt.rn.satfinite.e5m2x2.f16x2 a, x;\ncvt.rn.satfinite.e5m2x2.f16x2 b, y;\nmov.b32 %1, {a, b};\n}\n"
+            : "=r"(hi), "=r"(mid)
+            : "r"(p), "r"(q));
+    } else {
+        asm("{\n.reg .b16 a, b;\n.reg .b32 x, y;\n"
+            "cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\ncvt.rn.satfinite.e4m3x2.f16x2 b, %3;\nmov.b32 %0, {a, b};\n"
+            "cvt.rn.f16x2.e4m3x2 x, a;\ncvt.rn.f16x2.e4m3x2 y, b;\nsub.rn.f16x2 x, %2, x;\nsub.rn.f16x2 y, %3, y;\n"
+            "mul.rn.f16x2 x, x, %4;\nmul.rn.f16x2 y, y, %4;\n"
+            "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\ncvt.rn.satfinite.e4m3x2.f16x2 b, y;\nmov.b32 %1, {a, b};\n}\n"
+            : "=r"(hi), "=r"(mid)
+            : "r"(p), "r"(q), "r"(0x4c004c00u));             // 16, 16
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -555,14 +568,13 @@ __device__ __forceinline__ void row_scaled(uint2 v, float (&y)[4], float &g) {
 
 // The next term of four elements: its codes; and `rest` without it.  In f16, which
 // holds a row's scaled elements exactly where the terms do.
-__device__ __forceinline__ uint32_t take_term(__half2 (&rest)[2]) {
-    uint32_t code[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        code[j] = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest[j]), __NV_SATFINITE, __NV_E4M3);
-        rest[j] = __hsub2(rest[j], __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)code[j], __NV_E4M3)));
-    }
-    return __byte_perm(code[0], code[1], 0x5410);
+__device__ __forceinline__ uint32_t take_term(uint32_t (&rest)[2]) {
+    uint32_t code;
+    asm("{\n.reg .b16 a, b;\n.reg .b32 x, y;\n"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, %1;\ncvt.rn.satfinite.e4m3x2.f16x2 b, %2;\nmov.b32 %0, {a, b};\n"
+        "cvt.rn.f16x2.e4m3x2 x, a;\ncvt.rn.f16x2.e4m3x2 y, b;\nsub.rn.f16x2 %1, %1, x;\nsub.rn.f16x2 %2, %2, y;\n}\n"
+        : "=&r"(code), "+r"(rest[0]), "+r"(rest[1]));
+    return code;
 }
 
 // Rows r0 .. r0 + N - 1 of an item's q as e4m3 terms in shared memory, and what
@@ -587,19 +599,14 @@ __device__ __forceinline__ void paged_terms(const PagedParams &p, uint8_t *smem,
         float y[4], g;
         row_scaled<C::BF>(v[k], y, g);
         const int r = r0 + k, pos = C::position(r >> 4), row = 32 * pos + (r & 15);
-        __half2 rest[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t h = pack2<false>(y[2 * j], y[2 * j + 1]);
-            rest[j] = *reinterpret_cast<const __half2 *>(&h);
-        }
+        uint32_t rest[2] = {pack2<false>(y[0], y[1]), pack2<false>(y[2], y[3])};
         // 16-byte chunk lane / 4 of a 128-byte row, swizzled
         auto term = [&](int row_) {
             *reinterpret_cast<uint32_t *>(qs + row_ * 128 + ((((lane >> 2) ^ (row_ & 7)) << 4) | ((lane & 3) << 2))) = take_term(rest);
         };
         term(row);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) rest[j] = __hmul2(rest[j], __float2half2_rn(16.f));
+        for (int j = 0; j < 2; ++j) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(rest[j]) : "r"(0x4c004c00u));   // by 16
         term(row + 16);
         if constexpr (!C::BF) term(32 * C::NG + 16 * pos + (r & 15));    // behind the others' rows, in units of the second
         if (lane == 0) bars->qscale[slot][r] = g;
@@ -925,11 +932,7 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                     for (int q = 0; q < 4; ++q) v[q] = ex2(v[q]);
                     l[x][k / 2] = fma_f2(pack_f2(v[0], v[1]), isv2, l[x][k / 2]);
                     l[x][k / 2 + 1] = fma_f2(pack_f2(v[2], v[3]), isv2, l[x][k / 2 + 1]);
-                    uint32_t h0, h1, m0, m1;
-                    split2(v[0], v[1], h0, m0);
-                    split2(v[2], v[3], h1, m1);
-                    hi[k / 4] = __byte_perm(h0, h1, 0x5410);
-                    mid[k / 4] = __byte_perm(m0, m1, 0x5410);
+                    split4<false>(v, hi[k / 4], mid[k / 4]);
                 }
                 uint8_t *ph = prow + (((2 * x) ^ swz) << 4), *pm = prow + (((2 * x + 1) ^ swz) << 4);
                 if constexpr (NR == 16) {
@@ -1160,13 +1163,15 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 //        of q below 2^-9 (f16 2^-6) of their row's largest are off by 2^-17 of it;
 //   O += P_0 V + P_1 V, where P_1, what e4m3 left of a weight, is e5m2: its
 //        smallest step is 2^-16, so a weight is off by 2^-7 of itself or by 2^-17
-//        where the row's largest is 2^4 or more, and a reference serves 64 tiles.
+//        where the group's largest is 1 or more; a group has 16 tiles, and loses
+//        2^-6 of its weight at most.
 // Bound by the tensor cores: four e4m3 products of 128 x 128 x 128 a block and
 // tile, which is the time of the two that bf16 operands would take.
 // ---------------------------------------------------------------------------
 
 constexpr int kRowsSlots = 5;            // ring of K and V tiles at most
-constexpr int kRowsTiles = 64;           // tiles that a reference serves at most
+constexpr int kRowsTiles = 16;           // tiles that a reference serves at most
+constexpr float kRowsBias = 2.f;         // as kBias: lower, as the steps are finer and a rescaling of O costs a tile's exponentials
 constexpr int kRowsThreads = 352;        // two softmax groups of four warps, producer, an MMA issuer a group
 
 template <bool BF_>
@@ -1376,27 +1381,13 @@ __device__ __forceinline__ void rows_terms(const PagedParams &p, uint8_t *tile, 
         float y[4], gk;
         row_scaled<C::BF>(v[k], y, gk);
         if (lane == k) g = gk;
-        __half2 rest[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t h = pack2<false>(y[2 * j], y[2 * j + 1]);
-            rest[j] = *reinterpret_cast<const __half2 *>(&h);
-        }
+        uint32_t rest[2] = {pack2<false>(y[0], y[1]), pack2<false>(y[2], y[3])};
         const int row = r0 + k;
 #pragma unroll
         for (int term = 0; term < C::NT; ++term)
             *reinterpret_cast<uint32_t *>(tile + term * kPanelBytes + row * 128 +
                                           ((((lane >> 2) ^ (row & 7)) << 4) | ((lane & 3) << 2))) = take_term(rest);
     }
-}
-
-// Two weights: their first term in e4m3, and what it leaves in e5m2.
-__device__ __forceinline__ void split2_wide(float a, float b, uint32_t &hi, uint32_t &mid) {
-    const uint32_t h = pack2<false>(a, b);
-    const __half2 p = *reinterpret_cast<const __half2 *>(&h);
-    hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(p), __NV_SATFINITE, __NV_E4M3);
-    const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3));
-    mid = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(p, back)), __NV_SATFINITE, __NV_E5M2);
 }
 
 // Softmax and epilogue of group x, a row a thread.
@@ -1511,7 +1502,7 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
             if (__any_sync(0xffffffffu, need)) {
                 float alpha = 1.f;
                 if (need) {
-                    const float own = tmax - kBias, ref = fmaxf(fmaxf(own, fminf(M, own + kAbove)), M - kBelow);
+                    const float own = tmax - kRowsBias, ref = fmaxf(fmaxf(own, fminf(M, own + kAbove)), M - kBelow);
                     alpha = m == -INFINITY ? 0.f : ex2(m - ref);
                     m = ref;
                     M = fmaxf(M, ref);
@@ -1553,11 +1544,7 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
                                 for (int y = 0; y < 4; ++y) e[y] = ex2(e[y]);
                                 sum[0] = add_f2(sum[0], pack_f2(e[0], e[1]));
                                 sum[1] = add_f2(sum[1], pack_f2(e[2], e[3]));
-                                uint32_t h0, h1, m0, m1;
-                                split2_wide(e[0], e[1], h0, m0);
-                                split2_wide(e[2], e[3], h1, m1);
-                                w0[4 * u + k / 4] = __byte_perm(h0, h1, 0x5410);
-                                w1[4 * u + k / 4] = __byte_perm(m0, m1, 0x5410);
+                                split4<true>(e, w0[4 * u + k / 4], w1[4 * u + k / 4]);
                             }
                             float a, b;
                             unpack_f2(add_f2(sum[0], sum[1]), a, b);
