@@ -1679,8 +1679,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 // Joins the partials of the units that several CTAs covered:
 //   O = out_scale * sum_c w_c O_c / sum_c w_c with w_c = exp(LSE_c - max LSE).
 // CTA (c, y) takes rows, a warp each, of the unit that CTA c of the kernel above
-// began and did not end; the metadata says how far it goes on.
+// began and did not end; the metadata says how far it goes on.  Nearly every cut
+// unit has two partials: their rows are fetched in the same round trip as the
+// metadata and joined by straight code; more take the loop.
 constexpr int kPagedMergeWarps = 4;
+
+template <bool BF>
+__device__ __forceinline__ void paged_store_row(const PagedParams &p, const PagedMeta &m, int r, float4 acc, float sum, float mx,
+                                                int lane) {
+    const float inv = sum == 0.f ? 0.f : p.out_scale / sum;
+    const int t = p.subs == 1 ? r / p.G : 0;
+    const int64_t at = (int64_t)(m.row0 + t) * p.H + m.h0 + r - t * p.G;
+    reinterpret_cast<uint2 *>(p.o)[at * (kD / 4) + lane] =
+        make_uint2(pack2<BF>(acc.x * inv, acc.y * inv), pack2<BF>(acc.z * inv, acc.w * inv));
+    if (lane == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : mx + logf(sum);
+}
 
 template <bool BF>
 __global__ void __launch_bounds__(32 * kPagedMergeWarps) fmha_paged_merge_kernel(const PagedParams p, int R) {
@@ -1688,10 +1701,23 @@ __global__ void __launch_bounds__(32 * kPagedMergeWarps) fmha_paged_merge_kernel
     const int r = blockIdx.y * kPagedMergeWarps + (threadIdx.x >> 5);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (c0 + 1 >= p.ncta || r >= R) return;
+    auto slot = [&](int c) { return ((int64_t)2 * (c0 + c) + (c == 0 ? 1 : 0)) * R + r; };
+    const float4 *o_c = reinterpret_cast<const float4 *>(p.part_o) + lane;
     const PagedMeta m = p.meta[2 * c0 + 1];
+    const bool two = p.meta[2 * (c0 + 1)].last;
+    const float la = p.part_lse[slot(0)], lb = p.part_lse[slot(1)];
+    const float4 a = o_c[slot(0) * (kD / 4)], b = o_c[slot(1) * (kD / 4)];
     if (r >= m.rows) return;                                 // also: CTA c0 began no unit that it did not end
+    if (two) {
+        float mx = fmaxf(la, lb);
+        if (mx == -INFINITY || la != la || lb != lb) mx = 0.f;   // no key: weights 0; NaN in, NaN out
+        const float wa = __expf(la - mx), wb = __expf(lb - mx);
+        const float4 o = make_float4(wa * a.x + wb * b.x, wa * a.y + wb * b.y, wa * a.z + wb * b.z, wa * a.w + wb * b.w);
+        paged_store_row<BF>(p, m, r, o, wa + wb, mx, lane);
+        return;
+    }
     // the partials of CTAs c0 .. c0 + n - 1
-    int n = 1;
+    int n = 2;
     for (;;) {
         const int c = c0 + n + lane;
         const unsigned hit = __ballot_sync(0xffffffffu, c >= p.ncta || p.meta[2 * c].last);
@@ -1699,7 +1725,6 @@ __global__ void __launch_bounds__(32 * kPagedMergeWarps) fmha_paged_merge_kernel
         if (hit) break;
     }
     n = imin(n, p.ncta - c0);
-    auto slot = [&](int c) { return ((int64_t)2 * (c0 + c) + (c == 0 ? 1 : 0)) * R + r; };
     float mx = -INFINITY;
     bool nan = false;
     for (int c = lane; c < n; c += 32) {
@@ -1731,12 +1756,7 @@ __global__ void __launch_bounds__(32 * kPagedMergeWarps) fmha_paged_merge_kernel
             acc.w += x * v[k].w;
         }
     }
-    const float inv = sum == 0.f ? 0.f : p.out_scale / sum;
-    const int t = p.subs == 1 ? r / p.G : 0;
-    const int64_t at = (int64_t)(m.row0 + t) * p.H + m.h0 + r - t * p.G;
-    reinterpret_cast<uint2 *>(p.o)[at * (kD / 4) + lane] =
-        make_uint2(pack2<BF>(acc.x * inv, acc.y * inv), pack2<BF>(acc.z * inv, acc.w * inv));
-    if (lane == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : mx + logf(sum);
+    paged_store_row<BF>(p, m, r, acc, sum, mx, lane);
 }
 
 // ---------------------------------------------------------------------------
