@@ -697,9 +697,14 @@ def page_plan(seqlen: torch.Tensor, n_new: torch.Tensor, table: torch.Tensor, fr
     new_seqlen = new(B) if new_seqlen is None else new_seqlen
     n_free_out = n_free if n_free_out is None else n_free_out
     per_seq, rows = (B,), (N,)
-    if not (_fit(index, i32, per_seq, seqlen, n_new, batch_idx, new_seqlen) and _fit(index, i32, rows, slots, positions)
-            and _fit(index, i32, (B + 1,), cu_new) and _fit(index, i32, (1,), n_free, n_free_out)
-            and _fit(index, i32, table.shape, table) and _fit(index, i32, free_list.shape, free_list)):
+    given = ((seqlen, n_new, new_seqlen, slots, positions, cu_new, table, free_list, n_free)
+             + (() if batch_idx is None else (batch_idx,)) + (() if n_free_out is n_free else (n_free_out,)))
+    ok = (n_new.shape == per_seq and new_seqlen.shape == per_seq and slots.shape == rows and positions.shape == rows
+          and cu_new.shape == (B + 1,) and n_free.shape == (1,) and n_free_out.shape == (1,)
+          and (batch_idx is None or batch_idx.shape == per_seq))
+    for t in given:
+        ok = ok and t.dtype is i32 and t.get_device() == index and t.is_contiguous()
+    if not ok:
         _check(index, i32, per_seq, seqlen=seqlen, n_new=n_new, batch_idx=batch_idx, new_seqlen=new_seqlen)
         _check(index, i32, rows, slots=slots, positions=positions)
         _check(index, i32, (B + 1,), cu_new=cu_new)
@@ -811,7 +816,10 @@ def page_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_sc
     batch_idx int32 [B].  mask "causal" (q-end) or "none".  Allocates O, LSE
     [N, H] and the workspace with torch when not given; rows behind the last
     sequence are not written.  Returns (O, LSE)."""
-    index, code = _device_and_code(q)
+    index, dt = q.get_device(), q.dtype
+    code = _TORCH_DTYPE.get(dt)
+    if index < 0 or code is None:
+        _device_and_code(q)
     if stream is not None or _current_device() != index:
         with _on(stream, index):
             return page_fwd(q, k_pages, v_pages, k_scale, v_scale, table, seqlen, cu_q=cu_q, max_q=max_q,
@@ -822,16 +830,19 @@ def page_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_sc
     if mask not in ("none", "causal"):
         raise ValueError(f"mask is none or causal, not {mask!r}")
     n_pages, H_k, P, D = _fit_pages(index, k_pages, v_pages, k_scale, v_scale)
-    (N, H, _), (B_table, width), B, dt = q.shape, table.shape, seqlen.shape[0], q.dtype
+    (N, H, _), (B_table, width), B = q.shape, table.shape, seqlen.shape[0]
     if cu_q is None and N != B:
         raise ValueError(f"{N} rows of q for {B} sequences need cu_q")
     if out is None:
         out = torch.empty_like(q)
     if lse is None and return_lse:
         lse = torch.empty((N, H), dtype=torch.float32, device=q.device)
-    if not (_fit(index, dt, (N, H, D), q, out) and _fit(index, torch.float32, (N, H), lse)
-            and _fit(index, torch.int32, (B,), seqlen, batch_idx) and _fit(index, torch.int32, (B + 1,), cu_q)
-            and _fit(index, torch.int32, (B_table, width), table)):
+    i32, shape = torch.int32, q.shape
+    if not (shape[2] == D and q.is_contiguous() and out.shape == shape and out.dtype is dt and out.get_device() == index
+            and out.is_contiguous() and seqlen.dtype is i32 and seqlen.get_device() == index and seqlen.is_contiguous()
+            and table.dtype is i32 and table.get_device() == index and table.is_contiguous()
+            and (lse is None or _fit(index, torch.float32, (N, H), lse))
+            and (batch_idx is None or _fit(index, i32, (B,), batch_idx)) and (cu_q is None or _fit(index, i32, (B + 1,), cu_q))):
         _check(index, dt, (N, H, D), q=q, out=out)
         _check(index, torch.float32, (N, H), lse=lse)
         _check(index, torch.int32, (B,), seqlen=seqlen, batch_idx=batch_idx)
@@ -847,8 +858,9 @@ def page_fwd(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_sc
     try:
         rc = lib().fmha_page_fwd(
             fmha_tensor(q.data_ptr(), code), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), fmha_tensor(out.data_ptr(), code), _ptr(lse), B, N, most, H, H_k, D,
-            n_pages, P, B_table, width, table.data_ptr(), seqlen.data_ptr(), _ptr(batch_idx), _ptr(cu_q),
+            v_scale.data_ptr(), fmha_tensor(out.data_ptr(), code), None if lse is None else lse.data_ptr(), B, N, most, H, H_k, D,
+            n_pages, P, B_table, width, table.data_ptr(), seqlen.data_ptr(),
+            None if batch_idx is None else batch_idx.data_ptr(), None if cu_q is None else cu_q.data_ptr(),
             1.0 / math.sqrt(D) if scale is None else scale, out_scale, _MASKS[mask], ws, nbytes, raw)
     finally:
         if workspace is None:

@@ -163,3 +163,65 @@ def test_rope_outputs_over_inputs(fm, no_device):
     assert call_rope(fm, **row, k=k + 2 * 512, qo=R["q"], ko=k + 2 * 512) == past # a token further on
     # q's heads, and in another layout head by head: interleaved spans that are not pieces of tokens
     assert call_rope(fm, qo=R["q"] + 2, qos=(1280, 256, 64)) == -1
+
+
+# ---------------------------------------------------------------------------
+# Attention: 3 sequences, 7 rows, 8 heads on 2, 6 pages of 32, a table of 4 rows of 5
+# ---------------------------------------------------------------------------
+
+FWD = apart("q", "kp", "vp", "ks", "vs", "o", "lse", "tab", "sl", "bi", "cu", "ws")
+
+
+def call_fwd(fm, **kw):
+    a = dict(FWD, B=3, N=7, mq=4, H=8, H_k=2, D=128, n=6, P=32, Bt=4, mp=5, scale=0.1, out_scale=1.0, mask=2, ws_bytes=1 << 30, dt=BF16)
+    a.update(kw)
+    t = lambda x: fm.fmha_tensor(a[x], a.get(x + "_dt", a["dt"]))
+    return fm.lib().fmha_page_fwd(t("q"), a["kp"], a["vp"], a["ks"], a["vs"], t("o"), a["lse"], a["B"], a["N"], a["mq"], a["H"],
+                                  a["H_k"], a["D"], a["n"], a["P"], a["Bt"], a["mp"], a["tab"], a["sl"], a["bi"], a["cu"],
+                                  a["scale"], a["out_scale"], a["mask"], a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=-1), -1), (dict(N=-1), -1), (dict(D=64), -1), (dict(H=3), -1), (dict(H=258, H_k=2), -1), (dict(H_k=0), -1),
+    (dict(P=8), -1), (dict(P=100), -1), (dict(P=0), -1), (dict(P=256), -1), (dict(mq=0), -1), (dict(n=0), -1), (dict(Bt=0), -1), (dict(mp=0), -1),
+    (dict(mp=(1 << 25) + 1), -1), (dict(n=1 << 26), -1), (dict(N=1 << 28), -1), (dict(cu=None), -1),
+    (dict(scale=0.0), -1), (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(out_scale=float("inf")), -1),
+    (dict(out_scale=float("nan")), -1), (dict(mask=1), -1), (dict(mask=3), -1), (dict(ws=None), -1), (dict(ws=FWD["ws"] + 128), -1),
+    (dict(ws_bytes=1000), -1), *[({x: None}, -1) for x in ("q", "kp", "vp", "ks", "vs", "o", "tab", "sl")],
+    *[({x: FWD[x] + 8}, -2) for x in ("q", "kp", "vp", "o")],
+    *[({x: FWD[x] + 2}, -1) for x in ("ks", "vs", "lse", "tab", "sl", "bi", "cu")],
+    (dict(dt=E4M3), -2), (dict(o_dt=F16), -2), (dict(dt=8), -2),
+    (dict(B=0, q=None, ws=None), 0), (dict(N=0, q=None, ws=None), 0),
+])
+def test_fwd_refusals(fm, kw, code):
+    assert call_fwd(fm, **kw) == code
+
+
+def test_fwd_outputs_over_inputs_and_one_another(fm, no_device):
+    past = call_fwd(fm)
+    assert past not in (-1, 0)
+    assert call_fwd(fm, N=3, cu=None) == past and call_fwd(fm, bi=None, lse=None) == past
+    assert call_fwd(fm, vp=FWD["kp"], vs=FWD["ks"]) == past                       # both are only read
+    rows, ws = 7 * 8 * 256, fm.fmha_page_workspace_size(4, 8, 2)
+    size = dict(q=rows, kp=PAGE_BYTES, vp=PAGE_BYTES, ks=SCALE_BYTES, vs=SCALE_BYTES, o=rows, lse=7 * 8 * 4, tab=80, sl=12, bi=12,
+                cu=16, ws=ws)
+    for x in ("o", "lse", "ws"):
+        for y in FWD:
+            if x == y:
+                continue
+            assert call_fwd(fm, **{y: FWD[x]}) == -1, (x, y)
+            end = FWD[x] + (size[x] + 255) // 256 * 256
+            assert call_fwd(fm, **{y: end}) == past, (x, y)
+            if size[x] > 16 and y != "ws":
+                assert call_fwd(fm, **{y: FWD[x] + size[x] - 16}) == -1, (x, y)
+
+
+def test_page_workspace_size(fm):
+    size = fm.fmha_page_workspace_size
+    row, meta = (128 + 1) * 4, 16
+    for max_q, H, H_k, rows in ((1, 32, 8, 16), (4, 32, 8, 16), (5, 32, 8, 32), (8, 32, 8, 32), (9, 32, 8, 64), (16, 32, 8, 64),
+                                (17, 32, 8, 256), (1, 128, 1, 256), (1, 64, 1, 64), (1000, 8, 8, 256)):
+        assert size(max_q, H, H_k) == 2 * 152 * (rows * row + meta)
+    assert size(1000, 8, 8) <= 40_200_000
+    for bad in ((0, 8, 8), (1, 8, 3), (1, 129, 1), (1, 0, 1), (1, 8, 0), (-1, 8, 8)):
+        assert size(*bad) == 0
