@@ -60,18 +60,17 @@ constexpr float kGrown = 8.75f;          // and how far it may grow: e4m3 ends a
 constexpr float kAbove = 2.f;            // how far it may be set higher, to an earlier one
 constexpr float kBelow = 24.f;           // how far a reference may be below the highest before it
 constexpr int kStagesPaged = 6;
-constexpr int kPagedBars = 6144;         // barrier block
+constexpr int kPagedBars = 4096;         // barrier block
 constexpr float kNone = 1e30f;           // -m of a row that has seen no key in its group
 constexpr float kLeastScale = 0x1p-60f, kMostScale = 0x1p60f;   // of values
 
 template <bool BF_, int NG_, int NR_>
 struct PagedCfg {
     static constexpr bool BF = BF_;
-    static constexpr int NG = NG_;                            // groups of 16 query rows a unit holds,
-    static constexpr int NR = NR_;                            // of which so many are computed
+    static constexpr int NG = NG_;                            // groups of 16 query rows a unit holds, one or two,
+    static constexpr int NR = NR_;                            // of whose rows so many are computed
     static constexpr int R = 16 * NG;                         // its rows
-    static constexpr bool SPLIT = NG == 1;                    // the pipelines share tiles out, else groups
-    static constexpr int GPW = SPLIT ? NG : NG / 2;           // groups of a pipeline
+    static constexpr bool SPLIT = NG == 1;                    // the pipelines share out the tiles, else the groups
     static constexpr int SW = 8;                              // softmax warps
     // Producer warps: issuing a TMA load takes one warp 80 ns, and a tile of 16-token
     // pages is 16 of them (98 us instead of 67 for eight sequences of 32768); the
@@ -79,12 +78,12 @@ struct PagedCfg {
     static constexpr int NP = NR <= 8 ? 4 : 1;
     static constexpr int QW = SW, PROD = SW + 1, MMA = PROD + NP;   // q warp, producers, two MMA issuers
     static constexpr int THREADS = 32 * (MMA + 2);
-    static constexpr int COLS = 32 * GPW;                     // of a pipeline's S^T and O^T
+    static constexpr int COLS = 32;                           // of a pipeline's S^T and O^T: a group's
     static constexpr int PIPE_COLS = 4 * COLS;                // TMEM: two S^T, then O^T (and nothing, to a power of two)
     static constexpr int TMEM_COLS = 2 * PIPE_COLS;
     static constexpr int P_ROW = COLS;                        // bytes of a key's P^T row
     static constexpr int P_BYTES = kRows * P_ROW;
-    static constexpr uint64_t P_SWZ = GPW == 1 ? 6 : 4;       // 32-byte or 64-byte swizzle
+    static constexpr uint64_t P_SWZ = 6;                      // 32-byte swizzle
     static constexpr int Q_BYTES = (BF ? 32 : 48) * NG * 128; // first and second terms, then f16's third
     static constexpr int STAGE = 2 * kPanelBytes;             // K and V of 128 keys
     static constexpr int OFF_P = 2 * Q_BYTES;                 // two buffers a pipeline
@@ -97,10 +96,6 @@ struct PagedCfg {
     static_assert(SMEM_BYTES <= 227 * 1024 && OFF_KV % 1024 == 0 && OFF_P % 1024 == 0, "shared memory");
     static_assert(!SPLIT || NS % 2 == 0, "a ring a pipeline");
     static_assert(!SPLIT || 2 * P_BYTES >= R * kD * 4, "pipeline 1 hands its O over in its P^T buffers");
-
-    static __device__ __forceinline__ int group(int w, int x) { return SPLIT ? x : w + 2 * x; }   // x-th of pipeline w
-    static __device__ __forceinline__ int groups(int w, int ng) { return SPLIT ? ng : (ng - w + 1) >> 1; }
-    static __device__ __forceinline__ int position(int grp) { return SPLIT ? grp : GPW * (grp & 1) + (grp >> 1); }   // in q's tile
 };
 
 struct PagedMeta {                       // whose partial a workspace slot holds
@@ -139,14 +134,14 @@ struct PagedBars {
     int abort;
     alignas(16) float zero[16];
     alignas(16) float scale[kStagesPaged][2][8];   // k_scale, v_scale of a stage's pages
-    alignas(16) float qscale[2][64];     // of a q slot's rows: 2^k,
-    alignas(16) int lim[2][64], at[2][64];   // the last key they see, and q row * H + head (-1: none)
-    alignas(16) float nm[2][64];         // by pipeline and row: -m,
-    alignas(16) float am[2][64];         // 2^(m before - m),
-    float top[2][64];                    // the largest m so far, then (epilogue) the factor of O
-    float red[8][32];                    // by warp: maxima or sums of its rows
-    float stat_m[32], stat_l[32];        // pipeline 1's references and sums
-    float other[32];                     // factor of pipeline 1's O
+    alignas(16) float qscale[2][32];     // of a q slot's rows: 2^k,
+    alignas(16) int lim[2][32], at[2][32];   // the last key they see, and q row * H + head (-1: none)
+    alignas(16) float nm[2][32];         // by pipeline and row: -m,
+    alignas(16) float am[2][32];         // 2^(m before - m),
+    float top[2][32];                    // the largest m so far, then (epilogue) the factor of O
+    float red[8][16];                    // by warp: maxima or sums of its rows
+    float stat_m[16], stat_l[16];        // pipeline 1's references and sums
+    float other[16];                     // factor of pipeline 1's O
 };
 static_assert(sizeof(PagedBars) <= kPagedBars, "barrier block");
 
@@ -159,7 +154,7 @@ __device__ __forceinline__ uint64_t desc_sw(uint32_t saddr, uint32_t lbo, uint32
            ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (swz << 61);
 }
 // e4m3 operands, fp32 accumulator, M = 128; A and B K-major or MN-major
-__device__ __forceinline__ uint32_t paged_idesc(int n, bool mn) {
+__device__ constexpr uint32_t paged_idesc(int n, bool mn) {
     return (1u << 4) | ((mn ? 3u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 }
 __device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
@@ -314,15 +309,8 @@ __device__ __forceinline__ int64_t floor_sum(int64_t x, int s) {
 // tiles and edges of a head's blocks before block v
 __device__ __forceinline__ int64_t paged_before(const PagedParams &p, const PagedSeq &s, int v) {
     const int f = imin(v, s.full), sh = 7 - p.tau_log;
-    int64_t tiles;
-    if (sh >= 0) {
-        const int64_t d = (int64_t)(imax(s.base, 0) - 1) >> p.tau_log; // tiles of block i: floor((i + 1 + d) / 2^sh) + 1
-        tiles = floor_sum(d + f, sh) - floor_sum(d, sh) + f;
-    } else {                             // 2 (i + 1) + d + 1
-        const int64_t d = (int64_t)(imax(s.base, 0) - 1) >> 7;
-        tiles = (int64_t)f * (f + 1) + f * (d + 1);
-    }
-    tiles += (int64_t)(v - f) * s.all;
+    const int64_t d = (int64_t)(imax(s.base, 0) - 1) >> p.tau_log;     // tiles of block i: floor((i + 1 + d) / 2^sh) + 1
+    const int64_t tiles = floor_sum(d + f, sh) - floor_sum(d, sh) + f + (int64_t)(v - f) * s.all;
     return (tiles + (int64_t)v * p.edge) * p.subs;
 }
 
@@ -598,7 +586,7 @@ __device__ __forceinline__ void paged_terms(const PagedParams &p, uint8_t *smem,
     for (int k = 0; k < N; ++k) {
         float y[4], g;
         row_scaled<C::BF>(v[k], y, g);
-        const int r = r0 + k, pos = C::position(r >> 4), row = 32 * pos + (r & 15);
+        const int r = r0 + k, row = 32 * (r >> 4) + (r & 15);
         uint32_t rest[2] = {pack2<false>(y[0], y[1]), pack2<false>(y[2], y[3])};
         // 16-byte chunk lane / 4 of a 128-byte row, swizzled
         auto term = [&](int row_) {
@@ -608,7 +596,7 @@ __device__ __forceinline__ void paged_terms(const PagedParams &p, uint8_t *smem,
 #pragma unroll
         for (int j = 0; j < 2; ++j) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(rest[j]) : "r"(0x4c004c00u));   // by 16
         term(row + 16);
-        if constexpr (!C::BF) term(32 * C::NG + 16 * pos + (r & 15));    // behind the others' rows, in units of the second
+        if constexpr (!C::BF) term(32 * C::NG + r);    // behind the others' rows, in units of the second
         if (lane == 0) bars->qscale[slot][r] = g;
     }
 }
@@ -647,31 +635,31 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
     uint32_t c = 0, m = 0;               // tiles of the ring so far, tiles of MMAs so far
     bool ok = true;
     PagedItem it;
-    auto issue_pv = [&](uint32_t mm, uint32_t st, int na, bool begins) -> bool {
+    auto issue_pv = [&](uint32_t mm, uint32_t st, bool begins) -> bool {
         const uint32_t b = mm & 1;
         if (!wait_all(smem_u32(&bars->p_full[w][b]), (mm >> 1) & 1, abort_flag)) return false;
         tc_fence_after();
-        const uint32_t idesc = paged_idesc(32 * na, true);
         const uint64_t v = v0 + ((st * C::STAGE) >> 4), pt = p0 + ((b * C::P_BYTES) >> 4);
         const uint32_t o_tm = tmem + 2 * C::COLS;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)   // 32 keys
-            mma_ss<true>(o_tm, v + ((kk * 32 * 128) >> 4), pt + ((kk * 32 * C::P_ROW) >> 4), idesc, kk > 0 || !begins ? 1u : 0u);
+            mma_ss<true>(o_tm, v + ((kk * 32 * 128) >> 4), pt + ((kk * 32 * C::P_ROW) >> 4), paged_idesc(32, true),
+                         kk > 0 || !begins ? 1u : 0u);
         tc_commit(smem_u32(&bars->pv_done[w][b]));
         tc_commit(smem_u32(&bars->kv_empty[st]));
         return true;
     };
     for (uint32_t i = 0; ok && paged_take(bars, i, it, abort_flag, lane); ++i) {
-        const int slot = i & 1, na = C::groups(w, (it.rows + 15) >> 4);
+        const int slot = i & 1;
+        const bool on = C::SPLIT || 16 * w < it.rows;
         if (!wait_all(smem_u32(&bars->q_full[slot]), (i >> 1) & 1, abort_flag)) {
             ok = false;
             break;
         }
-        const uint32_t idesc = paged_idesc(32 * na, false), idesc16 = paged_idesc(16, false);
-        // this pipeline's groups are side by side in q's tile
-        const int pos0 = C::SPLIT ? 0 : C::GPW * w;
-        const uint64_t q = q0 + ((slot * C::Q_BYTES + pos0 * 32 * 128) >> 4);
-        const uint64_t q3 = q0 + ((slot * C::Q_BYTES + (32 * C::NG + 16 * pos0) * 128) >> 4);
+        // this pipeline's group in q's tile
+        const int grp = C::SPLIT ? 0 : w;
+        const uint64_t q = q0 + ((slot * C::Q_BYTES + grp * 32 * 128) >> 4);
+        const uint64_t q3 = q0 + ((slot * C::Q_BYTES + (32 * C::NG + 16 * grp) * 128) >> 4);
         const int tb = it.t0 + (C::SPLIT ? w : 0);
         uint32_t st_before = 0;
         for (int t = tb; t < it.t1; t += kStep, ++c) {
@@ -680,7 +668,7 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
                 ok = false;
                 break;
             }
-            if (!C::SPLIT && na == 0) {  // nothing to do with this tile
+            if (!on) {                   // nothing to do with this tile
                 if (lane == 0) mbar_arrive(smem_u32(&bars->kv_empty[st]));
                 continue;
             }
@@ -693,16 +681,15 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
             const uint32_t s_tm = tmem + b * C::COLS;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)   // 32 dims: 32 bytes of a row
-                mma_ss<true>(s_tm, k + ((kk * 32) >> 4), q + ((kk * 32) >> 4), idesc, kk > 0 ? 1u : 0u);
+                mma_ss<true>(s_tm, k + ((kk * 32) >> 4), q + ((kk * 32) >> 4), paged_idesc(32, false), kk > 0 ? 1u : 0u);
             if constexpr (!C::BF) {
-                for (int g = 0; g < na; ++g)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ss<true>(s_tm + 32 * g + 16, k + ((kk * 32) >> 4), q3 + ((g * 16 * 128 + kk * 32) >> 4), idesc16, 1u);
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_ss<true>(s_tm + 16, k + ((kk * 32) >> 4), q3 + ((kk * 32) >> 4), paged_idesc(16, false), 1u);
             }
             tc_commit(smem_u32(&bars->s_full[w][b]));
             if (t + kStep >= it.t1) tc_commit(smem_u32(&bars->q_empty[slot]));
-            if (t > tb && !issue_pv(m - 1, st_before, na, t - kStep == tb)) {
+            if (t > tb && !issue_pv(m - 1, st_before, t - kStep == tb)) {
                 ok = false;
                 break;
             }
@@ -710,8 +697,8 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
             ++m;
         }
         if (!ok) break;
-        if (tb >= it.t1 || na == 0) tc_commit(smem_u32(&bars->q_empty[slot]));
-        else ok = issue_pv(m - 1, st_before, na, tb + kStep >= it.t1);   // the item's last P V: its epilogue does not wait for the next item's loads
+        if (tb >= it.t1 || !on) tc_commit(smem_u32(&bars->q_empty[slot]));
+        else ok = issue_pv(m - 1, st_before, tb + kStep >= it.t1);   // the item's last P V: its epilogue does not wait for the next item's loads
     }
     // no tensor-core operation may be in flight when TMEM is released
     tc_commit(smem_u32(&bars->drain[w]));
@@ -733,7 +720,7 @@ __device__ __forceinline__ bool soft_any(int w, bool v) {
 // of S^T), and dim r of O^T.
 template <class C, int NR>
 __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *bars, uint32_t tmem_all, int warp, int lane) {
-    constexpr int GPW = C::GPW, kStep = C::SPLIT ? 2 : 1;
+    constexpr int kStep = C::SPLIT ? 2 : 1;
     volatile int *abort_flag = &bars->abort;
     const int w = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t tmem = tmem_all + w * C::PIPE_COLS + ((uint32_t)((warp & 3) * 32) << 16);
@@ -747,7 +734,8 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
         // a false return is either the end or an abort: all warps leave together
         const bool more = paged_take(bars, i, it, abort_flag, lane);
         if (soft_any(w, !more)) break;
-        const int slot = i & 1, ng = (it.rows + 15) >> 4, na = C::groups(w, ng);
+        const int slot = i & 1, row0 = C::SPLIT ? 0 : 16 * w;     // this pipeline's rows
+        const bool on = row0 < it.rows;
         const int tb = it.t0 + (C::SPLIT ? w : 0);
         if (i == 0) {
             constexpr int N = C::R / C::SW;
@@ -757,19 +745,17 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
             if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[slot]));
         }
         bool ok = wait_all(smem_u32(&bars->q_full[slot]), (i >> 1) & 1, abort_flag);
-        uint64_t l[GPW][NR / 2];         // this key's part of the row sums, relative to m
+        uint64_t l[NR / 2];         // this key's part of the row sums, relative to m
 #pragma unroll
-        for (int x = 0; x < GPW; ++x)
-#pragma unroll
-            for (int k = 0; k < NR / 2; ++k) l[x][k] = 0;
+            for (int k = 0; k < NR / 2; ++k) l[k] = 0;
         if (r < C::R) {
             bars->top[w][r] = -INFINITY;
             bars->nm[w][r] = kNone;
         }
         int since = kGroupTiles;         // tiles of the group so far
         bool first = true;
-        if (na == 0) n += it.t1 - it.t0; // a pipeline without groups has no tiles
-        for (int t = tb; na > 0 && t < it.t1; t += kStep, ++c, ++n) {
+        if (!on) n += it.t1 - it.t0;     // a pipeline without rows has no tiles
+        for (int t = tb; on && t < it.t1; t += kStep, ++c, ++n) {
             const uint32_t b = c & 1, st = ring_stage<C>(w, n);
             const int key = t * kRows + r, nk = it.L - t * kRows;
             ok = wait_all(smem_u32(&bars->s_full[w][b]), (c >> 1) & 1, abort_flag) && ok;
@@ -791,46 +777,41 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
             const uint64_t a2 = pack_f2(a, a), lsv2 = pack_f2(lsv, lsv);
             const bool masked = nk < kRows || t * kRows + kRows - 1 > it.base + it.tok0;
             bool fresh = since == kGroupTiles;
-            uint64_t e[GPW][NR / 2];     // scores in log2 units, with the value's scale, over the reference
+            uint64_t e[NR / 2];     // scores in log2 units, with the value's scale, over the reference
             for (;;) {
                 float top = -INFINITY;
+                uint32_t s[2 * NR];
+                ld_terms<NR>(tmem + b * C::COLS, s);
+                wait_terms<NR>(s);
+                const float4 *g4 = reinterpret_cast<const float4 *>(&bars->qscale[slot][row0]);
+                const float4 *n4 = reinterpret_cast<const float4 *>(fresh ? bars->zero : &bars->nm[w][row0]);
 #pragma unroll
-                for (int x = 0; x < GPW; ++x) {
-                    if (x >= na) continue;
-                    uint32_t s[2 * NR];
-                    ld_terms<NR>(tmem + b * C::COLS + 32 * x, s);
-                    wait_terms<NR>(s);
-                    const int row = 16 * C::group(w, x);
-                    const float4 *g4 = reinterpret_cast<const float4 *>(&bars->qscale[slot][row]);
-                    const float4 *n4 = reinterpret_cast<const float4 *>(fresh ? bars->zero : &bars->nm[w][row]);
+                for (int k = 0; k < NR; k += 4) {
+                    const float4 gg = g4[k / 4], nm = n4[k / 4];
+                    const uint64_t t0 = fma_f2(pack_f2(__uint_as_float(s[NR + k]), __uint_as_float(s[NR + k + 1])), sixteenth,
+                                               pack_f2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
+                    const uint64_t t1 = fma_f2(pack_f2(__uint_as_float(s[NR + k + 2]), __uint_as_float(s[NR + k + 3])),
+                                               sixteenth, pack_f2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])));
+                    e[k / 2] = fma_f2(t0, mul_f2(pack_f2(gg.x, gg.y), a2), add_f2(pack_f2(nm.x, nm.y), lsv2));
+                    e[k / 2 + 1] = fma_f2(t1, mul_f2(pack_f2(gg.z, gg.w), a2), add_f2(pack_f2(nm.z, nm.w), lsv2));
+                }
+                if (masked) {
+                    const int4 *lim = reinterpret_cast<const int4 *>(&bars->lim[slot][row0]);
 #pragma unroll
                     for (int k = 0; k < NR; k += 4) {
-                        const float4 gg = g4[k / 4], nm = n4[k / 4];
-                        const uint64_t t0 = fma_f2(pack_f2(__uint_as_float(s[NR + k]), __uint_as_float(s[NR + k + 1])), sixteenth,
-                                                   pack_f2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])));
-                        const uint64_t t1 = fma_f2(pack_f2(__uint_as_float(s[NR + k + 2]), __uint_as_float(s[NR + k + 3])),
-                                                   sixteenth, pack_f2(__uint_as_float(s[k + 2]), __uint_as_float(s[k + 3])));
-                        e[x][k / 2] = fma_f2(t0, mul_f2(pack_f2(gg.x, gg.y), a2), add_f2(pack_f2(nm.x, nm.y), lsv2));
-                        e[x][k / 2 + 1] = fma_f2(t1, mul_f2(pack_f2(gg.z, gg.w), a2), add_f2(pack_f2(nm.z, nm.w), lsv2));
-                    }
-                    if (masked) {
-                        const int4 *lim = reinterpret_cast<const int4 *>(&bars->lim[slot][row]);
-#pragma unroll
-                        for (int k = 0; k < NR; k += 4) {
-                            const int4 m = lim[k / 4];
-                            float u, v;
-                            unpack_f2(e[x][k / 2], u, v);
-                            e[x][k / 2] = pack_f2(r < nk && key <= m.x ? u : -INFINITY, r < nk && key <= m.y ? v : -INFINITY);
-                            unpack_f2(e[x][k / 2 + 1], u, v);
-                            e[x][k / 2 + 1] = pack_f2(r < nk && key <= m.z ? u : -INFINITY, r < nk && key <= m.w ? v : -INFINITY);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < NR; k += 2) {
+                        const int4 m = lim[k / 4];
                         float u, v;
-                        unpack_f2(e[x][k / 2], u, v);
-                        top = max3(top, u, v);
+                        unpack_f2(e[k / 2], u, v);
+                        e[k / 2] = pack_f2(r < nk && key <= m.x ? u : -INFINITY, r < nk && key <= m.y ? v : -INFINITY);
+                        unpack_f2(e[k / 2 + 1], u, v);
+                        e[k / 2 + 1] = pack_f2(r < nk && key <= m.z ? u : -INFINITY, r < nk && key <= m.w ? v : -INFINITY);
                     }
+                }
+#pragma unroll
+                for (int k = 0; k < NR; k += 2) {
+                    float u, v;
+                    unpack_f2(e[k / 2], u, v);
+                    top = max3(top, u, v);
                 }
                 // does a score outgrow the group's reference?  Then it begins anew here.
                 if (!soft_any(w, !ok || (!fresh && top > kGrown))) break;
@@ -847,23 +828,19 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
             if (fresh) {
                 // the group's reference: the tile's maximum of every row
 #pragma unroll
-                for (int x = 0; x < GPW; ++x) {
-                    if (x >= na) continue;
-#pragma unroll
-                    for (int k = 0; k < NR; k += 2) {
-                        float u, v;
-                        unpack_f2(e[x][k / 2], u, v);
-                        u = redux_max(u);
-                        v = redux_max(v);
-                        if (lane == 0) {
-                            bars->red[warp][16 * x + k] = u;
-                            bars->red[warp][16 * x + k + 1] = v;
-                        }
+                for (int k = 0; k < NR; k += 2) {
+                    float u, v;
+                    unpack_f2(e[k / 2], u, v);
+                    u = redux_max(u);
+                    v = redux_max(v);
+                    if (lane == 0) {
+                        bars->red[warp][k] = u;
+                        bars->red[warp][k + 1] = v;
                     }
                 }
                 soft_sync(w);
-                if (r < 16 * na && (r & 15) < NR) {
-                    const int row = 16 * C::group(w, r >> 4) + (r & 15);
+                if (r < NR) {
+                    const int row = row0 + r;
                     const float top = fmaxf(fmaxf(bars->red[4 * w][r], bars->red[4 * w + 1][r]),
                                             fmaxf(bars->red[4 * w + 2][r], bars->red[4 * w + 3][r]));
                     const float M = bars->top[w][row], own = top - kBias, nm = bars->nm[w][row];
@@ -879,35 +856,30 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                     break;
                 }
                 tc_fence_after();
-#pragma unroll
-                for (int x = 0; x < GPW; ++x) {
-                    if (x >= na) continue;
-                    const int row = 16 * C::group(w, x);
-                    if (!first) {        // O^T, whose last P V is that of this pipeline's tile before
-                        uint32_t s[2 * NR];
-                        ld_terms<NR>(tmem + 2 * C::COLS + 32 * x, s);
-                        wait_terms<NR>(s);
-#pragma unroll
-                        for (int k = 0; k < NR; k += 4) {
-                            const float4 am = *reinterpret_cast<const float4 *>(&bars->am[w][row + k]);
-                            const float f[4] = {am.x, am.y, am.z, am.w};
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                s[k + q] = __float_as_uint(__uint_as_float(s[k + q]) * f[q]);
-                                s[NR + k + q] = __float_as_uint(__uint_as_float(s[NR + k + q]) * f[q]);
-                            }
-                        }
-                        st_terms<NR>(tmem + 2 * C::COLS + 32 * x, s);
-                    }
+                if (!first) {        // O^T, whose last P V is that of this pipeline's tile before
+                    uint32_t s[2 * NR];
+                    ld_terms<NR>(tmem + 2 * C::COLS, s);
+                    wait_terms<NR>(s);
 #pragma unroll
                     for (int k = 0; k < NR; k += 4) {
-                        const float4 nm = *reinterpret_cast<const float4 *>(&bars->nm[w][row + k]);
-                        const float4 am = *reinterpret_cast<const float4 *>(&bars->am[w][row + k]);
-                        l[x][k / 2] = mul_f2(l[x][k / 2], pack_f2(am.x, am.y));
-                        l[x][k / 2 + 1] = mul_f2(l[x][k / 2 + 1], pack_f2(am.z, am.w));
-                        e[x][k / 2] = add_f2(e[x][k / 2], pack_f2(nm.x, nm.y));
-                        e[x][k / 2 + 1] = add_f2(e[x][k / 2 + 1], pack_f2(nm.z, nm.w));
+                        const float4 am = *reinterpret_cast<const float4 *>(&bars->am[w][row0 + k]);
+                        const float f[4] = {am.x, am.y, am.z, am.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            s[k + q] = __float_as_uint(__uint_as_float(s[k + q]) * f[q]);
+                            s[NR + k + q] = __float_as_uint(__uint_as_float(s[NR + k + q]) * f[q]);
+                        }
                     }
+                    st_terms<NR>(tmem + 2 * C::COLS, s);
+                }
+#pragma unroll
+                for (int k = 0; k < NR; k += 4) {
+                    const float4 nm = *reinterpret_cast<const float4 *>(&bars->nm[w][row0 + k]);
+                    const float4 am = *reinterpret_cast<const float4 *>(&bars->am[w][row0 + k]);
+                    l[k / 2] = mul_f2(l[k / 2], pack_f2(am.x, am.y));
+                    l[k / 2 + 1] = mul_f2(l[k / 2 + 1], pack_f2(am.z, am.w));
+                    e[k / 2] = add_f2(e[k / 2], pack_f2(nm.x, nm.y));
+                    e[k / 2 + 1] = add_f2(e[k / 2 + 1], pack_f2(nm.z, nm.w));
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -918,33 +890,29 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
             const float isv = ex2(-lsv);     // of the same rounded logarithm
             const uint64_t isv2 = pack_f2(isv, isv);
             uint8_t *prow = pbuf + b * C::P_BYTES + r * C::P_ROW;
-            const uint32_t swz = GPW == 1 ? (r >> 2) & 1 : (r >> 1) & 3;
+            const uint32_t swz = (r >> 2) & 1;
+            uint32_t hi[NR / 4], mid[NR / 4];
 #pragma unroll
-            for (int x = 0; x < GPW; ++x) {
-                if (x >= na) continue;
-                uint32_t hi[NR / 4], mid[NR / 4];
+            for (int k = 0; k < NR; k += 4) {
+                float v[4];
+                unpack_f2(e[k / 2], v[0], v[1]);
+                unpack_f2(e[k / 2 + 1], v[2], v[3]);
 #pragma unroll
-                for (int k = 0; k < NR; k += 4) {
-                    float v[4];
-                    unpack_f2(e[x][k / 2], v[0], v[1]);
-                    unpack_f2(e[x][k / 2 + 1], v[2], v[3]);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) v[q] = ex2(v[q]);
-                    l[x][k / 2] = fma_f2(pack_f2(v[0], v[1]), isv2, l[x][k / 2]);
-                    l[x][k / 2 + 1] = fma_f2(pack_f2(v[2], v[3]), isv2, l[x][k / 2 + 1]);
-                    split4<false>(v, hi[k / 4], mid[k / 4]);
-                }
-                uint8_t *ph = prow + (((2 * x) ^ swz) << 4), *pm = prow + (((2 * x + 1) ^ swz) << 4);
-                if constexpr (NR == 16) {
-                    *reinterpret_cast<uint4 *>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(pm) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                } else if constexpr (NR == 8) {
-                    *reinterpret_cast<uint2 *>(ph) = make_uint2(hi[0], hi[1]);
-                    *reinterpret_cast<uint2 *>(pm) = make_uint2(mid[0], mid[1]);
-                } else {
-                    *reinterpret_cast<uint32_t *>(ph) = hi[0];
-                    *reinterpret_cast<uint32_t *>(pm) = mid[0];
-                }
+                for (int q = 0; q < 4; ++q) v[q] = ex2(v[q]);
+                l[k / 2] = fma_f2(pack_f2(v[0], v[1]), isv2, l[k / 2]);
+                l[k / 2 + 1] = fma_f2(pack_f2(v[2], v[3]), isv2, l[k / 2 + 1]);
+                split4<false>(v, hi[k / 4], mid[k / 4]);
+            }
+            uint8_t *ph = prow + (swz << 4), *pm = prow + ((1 ^ swz) << 4);
+            if constexpr (NR == 16) {
+                *reinterpret_cast<uint4 *>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(pm) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+            } else if constexpr (NR == 8) {
+                *reinterpret_cast<uint2 *>(ph) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2 *>(pm) = make_uint2(mid[0], mid[1]);
+            } else {
+                *reinterpret_cast<uint32_t *>(ph) = hi[0];
+                *reinterpret_cast<uint32_t *>(pm) = mid[0];
             }
             proxy_fence();
             __syncwarp();
@@ -954,45 +922,40 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
         if (soft_any(w, !ok)) break;
 
         // epilogue: O, a dim a thread, and the row sums
-        float o[GPW][NR];
+        float o[NR];
         if (!first) {
             ok = wait_all(smem_u32(&bars->pv_done[w][(c - 1) & 1]), ((c - 1) >> 1) & 1, abort_flag);
             if (soft_any(w, !ok)) break;
             tc_fence_after();
         }
-#pragma unroll
-        for (int x = 0; x < GPW; ++x) {
-            uint32_t s[2 * NR];
-            const bool there = !first && x < na;
-            if (there) {
-                ld_terms<NR>(tmem + 2 * C::COLS + 32 * x, s);
-                wait_terms<NR>(s);
-            }
-#pragma unroll
-            for (int k = 0; k < NR; ++k)
-                o[x][k] = there ? fmaf(__uint_as_float(s[NR + k]), 0.0625f, __uint_as_float(s[k])) : 0.f;
+        uint32_t s[2 * NR];
+        const bool there = !first;
+        if (there) {
+            ld_terms<NR>(tmem + 2 * C::COLS, s);
+            wait_terms<NR>(s);
         }
-        tc_fence_before();
 #pragma unroll
-        for (int x = 0; x < GPW; ++x)
+        for (int k = 0; k < NR; ++k)
+            o[k] = there ? fmaf(__uint_as_float(s[NR + k]), 0.0625f, __uint_as_float(s[k])) : 0.f;
+        tc_fence_before();
 #pragma unroll
             for (int k = 0; k < NR; k += 2) {
                 float u, v;
-                unpack_f2(l[x][k / 2], u, v);
+                unpack_f2(l[k / 2], u, v);
 #pragma unroll
                 for (int d = 16; d > 0; d >>= 1) {
                     u += __shfl_xor_sync(0xffffffffu, u, d);
                     v += __shfl_xor_sync(0xffffffffu, v, d);
                 }
                 if (lane == 0) {
-                    bars->red[warp][16 * x + k] = u;
-                    bars->red[warp][16 * x + k + 1] = v;
+                    bars->red[warp][k] = u;
+                    bars->red[warp][k + 1] = v;
                 }
             }
         soft_sync(w);
         // this pipeline's rows: a thread each
-        const int grp = C::group(w, r >> 4), row = 16 * grp + (r & 15);
-        const bool mine = r < 16 * GPW && (r & 15) < NR && row < it.rows;
+        const int row = row0 + r;
+        const bool mine = r < NR && row < it.rows;
         float sum = 0.f, m = -INFINITY;
         if (mine) {
             sum = (bars->red[4 * w][r] + bars->red[4 * w + 1][r]) + (bars->red[4 * w + 2][r] + bars->red[4 * w + 3][r]);
@@ -1007,9 +970,7 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
             }
             if (two) {
 #pragma unroll
-                for (int x = 0; x < GPW; ++x)
-#pragma unroll
-                    for (int k = 0; k < NR; ++k) scratch[(16 * x + k) * kD + r] = o[x][k];
+                    for (int k = 0; k < NR; ++k) scratch[k * kD + r] = o[k];
             }
             __syncwarp();
             if (lane == 0) {
@@ -1051,13 +1012,11 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
         }
         soft_sync(w);
 #pragma unroll
-        for (int x = 0; x < GPW; ++x)
-#pragma unroll
             for (int k = 0; k < NR; ++k) {
-                const int rr = 16 * C::group(w, x) + k;
+                const int rr = row0 + k;
                 if (rr >= it.rows) continue;
                 const float f0 = bars->top[w][rr];
-                float v = f0 == 0.f ? 0.f : o[x][k] * f0;
+                float v = f0 == 0.f ? 0.f : o[k] * f0;
                 if (two) v = fmaf(scratch[rr * kD + r], bars->other[rr], v);
                 if (!whole) {
                     p.part_o[((int64_t)part * C::R + rr) * kD + r] = v;
@@ -1169,7 +1128,8 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 // tile, which is the time of the two that bf16 operands would take.
 // ---------------------------------------------------------------------------
 
-constexpr int kRowsSlots = 5;            // ring of K and V tiles at most
+constexpr int kRowsSlots = 8;            // ring of K and V tiles at most
+constexpr int kRowsBars = 4096;          // barrier block
 constexpr int kRowsTiles = 16;           // tiles that a reference serves at most
 constexpr float kRowsBias = 2.f;         // as kBias: lower, as the steps are finer and a rescaling of O costs a tile's exponentials
 constexpr int kRowsThreads = 352;        // two softmax groups of four warps, producer, an MMA issuer a group
@@ -1178,26 +1138,33 @@ template <bool BF_>
 struct RowsCfg {
     static constexpr bool BF = BF_;
     static constexpr int NT = BF ? 2 : 3;                     // terms of q
-    static constexpr int R = 2 * kRows;
-    static constexpr int Q_BYTES = NT * kPanelBytes;          // of a block
-    static constexpr int OFF_P = 2 * Q_BYTES;                 // both terms of a block's P
+    static constexpr int OFF_P = NT * kPanelBytes;            // q's terms, then both terms of each group's P
     static constexpr int OFF_KV = OFF_P + 4 * kPanelBytes;
-    static constexpr int NS = (226 * 1024 - 4096 - OFF_KV) / kPanelBytes;
+    static constexpr int NS_FIT = (226 * 1024 - kRowsBars - OFF_KV) / kPanelBytes;
+    static constexpr int NS = NS_FIT & ~1;
+    static constexpr int RING = NS / 2;                       // slots of a group's ring
     static constexpr int OFF_BARS = OFF_KV + NS * kPanelBytes;
-    static constexpr int SMEM_BYTES = OFF_BARS + 4096 + 1024;
-    static_assert(SMEM_BYTES <= 227 * 1024 && NS >= 3 && NS <= kRowsSlots, "shared memory");
+    static constexpr int SMEM_BYTES = OFF_BARS + kRowsBars + 1024;
+    static_assert(SMEM_BYTES <= 227 * 1024 && RING >= 3 && NS <= kRowsSlots, "shared memory");
+
+    // the n-th K or V tile of group x's ring: K of its c-th tile is n = 2 c, V is 2 c + 1
+    static __device__ __forceinline__ uint32_t slot(int x, uint32_t n) { return x * RING + n % RING; }
+    static __device__ __forceinline__ uint32_t parity(uint32_t n) { return (n / RING) & 1; }
 };
 
 struct RowsBars {
-    uint64_t q_full[2], drain[2], s_full[2], s_free[2], p_full[2][2], pv_done[2];   // by group; p_full by half
+    uint64_t q_full[2], q_empty, drain[2], s_full[2], s_free[2], p_full[2][2], pv_done[2];   // by group; p_full by half
+    uint64_t stat_full, epi_done;
     uint64_t kv_full[kRowsSlots], kv_empty[kRowsSlots];
     uint64_t item_full[kPagedItems], item_empty[kPagedItems];
     PagedItem item[kPagedItems];
     uint32_t tmem_base;
     int abort;
     float scale[kRowsSlots][2][8];       // k_scale, v_scale of a V slot's pages
+    float2 stat[kRows];                  // reference and sum of group 1's rows
+    float qscale[kRows];                 // of the rows of q
 };
-static_assert(sizeof(RowsBars) <= 4096, "barrier block");
+static_assert(sizeof(RowsBars) <= kRowsBars, "barrier block");
 
 __device__ __forceinline__ bool rows_take(RowsBars *bars, uint32_t i, PagedItem &it, volatile int *abort_flag, int lane) {
     const uint32_t st = i % kPagedItems;
@@ -1208,14 +1175,14 @@ __device__ __forceinline__ bool rows_take(RowsBars *bars, uint32_t i, PagedItem 
     return it.rows > 0;
 }
 
-// The producer warp: tile c of the CTA is slots 2 c (K) and 2 c + 1 (V) of the ring.
+// The producer warp: K and V tiles into the rings, with the pages' scales.
 template <class C>
 __device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, const CUtensorMap *tmK, const CUtensorMap *tmV,
                               uint8_t *smem, RowsBars *bars, int lane) {
     volatile int *abort_flag = &bars->abort;
     bool ok = true;
     if (gate) ok = __all_sync(0xffffffffu, lane > 0 || test_gate_open(abort_flag));
-    uint32_t n = 0, qn = 0;
+    uint32_t fill[2] = {0, 0}, qn = 0;
     const int P = 1 << p.shift, per = kRows >> p.shift;
     auto publish = [&](uint32_t i, const PagedItem &it) -> bool {
         const uint32_t st = i % kPagedItems;
@@ -1244,9 +1211,10 @@ __device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, 
             const int ahead = id_of(t + 1), here = imax(0, imin(per, pages - t * per));
             // a page outside the cache: a coordinate outside it, which reads zeros
             const int head = id >= 0 ? id * p.H_k + it.g : p.n_pages * p.H_k;
-            for (int kv = 0; kv < 2; ++kv, ++n) {
-                const uint32_t st = n % C::NS;
-                if (n >= C::NS && !wait_all(smem_u32(&bars->kv_empty[st]), (n / C::NS - 1) & 1, abort_flag)) {
+            const int x = (t - it.t0) & 1;
+            for (int kv = 0; kv < 2; ++kv) {
+                const uint32_t n = x ? fill[1] : fill[0], st = C::slot(x, n);
+                if (n >= C::RING && !wait_all(smem_u32(&bars->kv_empty[st]), C::parity(n) ^ 1, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -1265,6 +1233,8 @@ __device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, 
                     }
                 }
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
+                if (x) ++fill[1];
+                else ++fill[0];
             }
             id = ahead;
             if (ok && t == it.t0) {
@@ -1274,10 +1244,14 @@ __device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, 
         }
         it = next;
     }
-    for (uint32_t f = n > C::NS ? n - C::NS : 0; f < n; ++f) {
-        if (ok) ok = wait_all(smem_u32(&bars->kv_empty[f % C::NS]), (f / C::NS) & 1, abort_flag);
-        if (!ok) mbar_wait_drain(smem_u32(&bars->kv_full[f % C::NS]), (f / C::NS) & 1);
-    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+        for (uint32_t n = fill[x] > C::RING ? fill[x] - C::RING : 0; n < fill[x]; ++n) {
+            const uint32_t st = C::slot(x, n);
+            if (ok) ok = wait_all(smem_u32(&bars->kv_empty[st]), C::parity(n), abort_flag);
+            if (!ok) mbar_wait_drain(smem_u32(&bars->kv_full[st]), C::parity(n));
+        }
+    if (ok && qn > 0) wait_all(smem_u32(&bars->q_empty), (qn - 1) & 1, abort_flag);
 }
 
 // MMA issuer of group x.  P lies in shared memory, apart from S, so that S of the
@@ -1291,30 +1265,24 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
     const uint32_t s_tm = tmem + x * kRows, o_tm = tmem + 2 * kRows + x * kD;
     constexpr uint32_t kIdS = mma_idesc(0u, kRows, false), kIdP0 = mma_idesc(0u, kD, true);
     constexpr uint32_t kIdP1 = kIdP0 | (1u << 7);            // A (the weights' second term) e5m2
-    const uint64_t q = smem_desc(smem_u32(smem + x * C::Q_BYTES), 16, 1024);
+    const uint64_t q = smem_desc(smem_u32(smem), 16, 1024);
     const uint64_t k0 = smem_desc(smem_u32(smem + C::OFF_KV), 16, 1024);
     const uint64_t v0 = smem_desc(smem_u32(smem + C::OFF_KV), kPanelBytes, 1024);
     const uint64_t p0 = smem_desc(smem_u32(smem + C::OFF_P + x * 2 * kPanelBytes), 16, 1024);
-    uint32_t c = 0, m = 0, items = 0;    // tiles; of this group; items that it had rows of
+    uint32_t m = 0;                      // tiles of this group
     bool ok = true;
     PagedItem it;
     for (uint32_t i = 0; ok && rows_take(bars, i, it, abort_flag, lane); ++i) {
-        if (x == 1 && it.rows <= kRows) {   // nothing to do with these tiles
-            for (int t = it.t0; ok && t < it.t1; ++t, ++c)
-                for (uint32_t n = 2 * c; ok && n < 2 * c + 2; ++n) {
-                    ok = wait_all(smem_u32(&bars->kv_full[n % C::NS]), (n / C::NS) & 1, abort_flag);
-                    if (ok && lane == 0) mbar_arrive(smem_u32(&bars->kv_empty[n % C::NS]));
-                }
-            continue;
-        }
-        if (!wait_all(smem_u32(&bars->q_full[x]), items++ & 1, abort_flag)) {
+        if (!wait_all(smem_u32(&bars->q_full[x]), i & 1, abort_flag)) {
             ok = false;
             break;
         }
-        for (int t = it.t0; ok && t <= it.t1; ++t) {
+        const int tb = it.t0 + x;
+        if (tb >= it.t1) tc_commit(smem_u32(&bars->q_empty));   // an item of one tile is group 0's alone
+        for (int t = tb; ok && tb < it.t1 && t < it.t1 + 2; t += 2) {
             if (t < it.t1) {             // S of this tile
-                const uint32_t n = 2 * c, st = n % C::NS;
-                if (!wait_all(smem_u32(&bars->kv_full[st]), (n / C::NS) & 1, abort_flag) ||
+                const uint32_t n = 2 * m, st = C::slot(x, n);
+                if (!wait_all(smem_u32(&bars->kv_full[st]), C::parity(n), abort_flag) ||
                     (m > 0 && !wait_all(smem_u32(&bars->s_free[x]), (m - 1) & 1, abort_flag))) {
                     ok = false;
                     break;
@@ -1329,16 +1297,16 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
                                      term > 0 || kk > 0 ? 1u : 0u);
                 tc_commit(smem_u32(&bars->s_full[x]));
                 tc_commit(smem_u32(&bars->kv_empty[st]));
-                ++c;
+                if (t + 2 >= it.t1) tc_commit(smem_u32(&bars->q_empty));
                 ++m;
             }
-            if (t > it.t0) {             // P V of the tile before, which is tile m - 1, or m - 2 if S of this one was issued
-                const uint32_t mm = m - (t < it.t1 ? 2 : 1), n = 2 * (c - (t < it.t1 ? 2 : 1)) + 1, st = n % C::NS;
-                if (!wait_all(smem_u32(&bars->kv_full[st]), (n / C::NS) & 1, abort_flag)) {
+            if (t > tb) {             // P V of the tile before, which is tile m - 1, or m - 2 if S of this one was issued
+                const uint32_t mm = m - (t < it.t1 ? 2 : 1), n = 2 * mm + 1, st = C::slot(x, n);
+                if (!wait_all(smem_u32(&bars->kv_full[st]), C::parity(n), abort_flag)) {
                     ok = false;
                     break;
                 }
-                const int halves = it.L - (t - 1) * kRows > kRows / 2 ? 2 : 1;
+                const int halves = it.L - (t - 2) * kRows > kRows / 2 ? 2 : 1;
                 const uint64_t v = v0 + ((st * kPanelBytes) >> 4);
                 for (int h = 0; h < halves; ++h) {
                     if (!wait_all(smem_u32(&bars->p_full[x][h]), mm & 1, abort_flag)) {
@@ -1352,7 +1320,7 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
                         for (int kk = 0; kk < 2; ++kk)       // 32 keys: 32 bytes of P's rows, 32 rows of V
                             mma_ss<true>(o_tm, p0 + ((term * kPanelBytes + (h * 2 + kk) * 32) >> 4),
                                          v + (((h * 2 + kk) * 32 * 128) >> 4), term ? kIdP1 : kIdP0,
-                                         t - 1 > it.t0 || h > 0 || term > 0 || kk > 0 ? 1u : 0u);
+                                         t - 2 > tb || h > 0 || term > 0 || kk > 0 ? 1u : 0u);
                 }
                 if (!ok) break;
                 tc_commit(smem_u32(&bars->pv_done[x]));
@@ -1365,19 +1333,20 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
     mbar_wait_drain(smem_u32(&bars->drain[x]), 0);
 }
 
-// A warp's 32 rows of the unit's q, from r0 on, as terms in the group's tiles; at:
-// of the lane's row, q row * H + head (-1: none).  All loads go out first (eight at
-// a time, with a division a row, took 9 us a unit).  g: the lane's row's scale.
+// 16 rows of the unit's q by a warp, from r0 on, as terms in its tiles; at: of lane
+// k's row r0 + k, q row * H + head (-1: none).  All loads go out first (eight at a
+// time, with a division a row, took 9 us for 32).  Returns the scale of lane k's row.
 template <class C>
-__device__ __forceinline__ void rows_terms(const PagedParams &p, uint8_t *tile, int at, int r0, int lane, float &g) {
-    uint2 v[32];
+__device__ __forceinline__ float rows_terms(const PagedParams &p, uint8_t *tile, int at, int r0, int lane) {
+    uint2 v[16];
+    float g = 0.f;
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
+    for (int k = 0; k < 16; ++k) {
         const int a = __shfl_sync(0xffffffffu, at, k);
         v[k] = a >= 0 ? *reinterpret_cast<const uint2 *>(p.q + ((int64_t)a * kD + lane * 4) * 2) : make_uint2(0u, 0u);
     }
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
+    for (int k = 0; k < 16; ++k) {
         float y[4], gk;
         row_scaled<C::BF>(v[k], y, gk);
         if (lane == k) g = gk;
@@ -1388,54 +1357,55 @@ __device__ __forceinline__ void rows_terms(const PagedParams &p, uint8_t *tile, 
             *reinterpret_cast<uint32_t *>(tile + term * kPanelBytes + row * 128 +
                                           ((((lane >> 2) ^ (row & 7)) << 4) | ((lane & 3) << 2))) = take_term(rest);
     }
+    return g;
 }
 
 // Softmax and epilogue of group x, a row a thread.
 template <class C>
 __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars, uint32_t tmem, int warp, int lane) {
     volatile int *abort_flag = &bars->abort;
-    const int x = warp >> 2, lr = (warp & 3) * 32 + lane, r = x * kRows + lr;      // row of the block, of the unit
+    const int x = warp >> 2, r = (warp & 3) * 32 + lane;   // group, row of the unit
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_tm = lane_base + x * kRows, o_tm = lane_base + 2 * kRows + x * kD;
-    uint8_t *prow = smem + C::OFF_P + x * 2 * kPanelBytes + lr * 128;
-    uint32_t c = 0, m_tiles = 0;                        // tiles; of this group
+    uint8_t *prow = smem + C::OFF_P + x * 2 * kPanelBytes + r * 128;
+    uint32_t c = 0;                                     // tiles of this group
     int parts = 0;                                      // bit s: slot s of this CTA holds a partial
     PagedItem it;
     for (uint32_t i = 0; rows_take(bars, i, it, abort_flag, lane); ++i) {
-        if (x == 1 && it.rows <= kRows) {
-            c += it.t1 - it.t0;
-            continue;
-        }
         const int tok = p.subs == 1 ? r / p.G : 0;
         const bool row_ok = r < it.rows;
         const int at = row_ok ? (it.row0 + tok) * p.H + it.h0 + r - tok * p.G : -1;
-        // this warp's rows of q; the S MMAs of the item before are done, their scores were read
-        float g = 0.f;
-        rows_terms<C>(p, smem + x * C::Q_BYTES, at, (warp & 3) * 32, lane, g);
+        // the unit's rows of q, 16 a warp, for both groups; the S MMAs of the item before are done
+        if (i > 0 && !wait_all(smem_u32(&bars->q_empty), (i - 1) & 1, abort_flag)) break;
+        const int k = warp * 16 + (lane & 15), tk = p.subs == 1 ? k / p.G : 0;
+        const float gk = rows_terms<C>(p, smem, k < it.rows ? (it.row0 + tk) * p.H + it.h0 + k - tk * p.G : -1, warp * 16, lane);
+        if (lane < 16) bars->qscale[k] = gk;
         proxy_fence();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[x]));
+        if (lane < 2) mbar_arrive(smem_u32(&bars->q_full[lane]));
+        if (!wait_all(smem_u32(&bars->q_full[x]), i & 1, abort_flag)) break;
         const bool work = __any_sync(0xffffffffu, row_ok);   // else the warp only keeps step
         const int lim = it.base + it.tok0 + tok;        // last key it sees
-        const float fq = p.c * g;
+        const float fq = p.c * bars->qscale[r];
         float m = -INFINITY, M = -INFINITY;             // reference (log2 units) of P and O, and the highest so far
         float l = 0.f;                                  // row sum
         int since = kRowsTiles;
         bool ok = true;
-        for (int t = it.t0; t < it.t1; ++t, ++c, ++m_tiles) {
+        const int tb = it.t0 + x;
+        for (int t = tb; t < it.t1; t += 2, ++c) {
             const int nk = it.L - t * kRows, halves = nk > kRows / 2 ? 2 : 1;
-            const uint32_t n = 2 * c + 1, vst = n % C::NS;
+            const uint32_t n = 2 * c + 1, vst = C::slot(x, n);
             // scores, and the scales that come with V
-            if (!wait_all(smem_u32(&bars->s_full[x]), m_tiles & 1, abort_flag) ||
-                !wait_all(smem_u32(&bars->kv_full[vst]), (n / C::NS) & 1, abort_flag)) {
+            if (!wait_all(smem_u32(&bars->s_full[x]), c & 1, abort_flag) ||
+                !wait_all(smem_u32(&bars->kv_full[vst]), C::parity(n), abort_flag)) {
                 ok = false;
                 break;
             }
             if (nk < kRows) {
                 // rows past the keys: V is zeroed so that P = 0 contributes 0 (by each group before its own P V)
-                if (lr >= nk) {
+                if (r >= nk) {
                     proxy_fence();
-                    uint4 *v = reinterpret_cast<uint4 *>(smem + C::OFF_KV + vst * kPanelBytes + lr * 128);
+                    uint4 *v = reinterpret_cast<uint4 *>(smem + C::OFF_KV + vst * kPanelBytes + r * 128);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
                     proxy_fence();
@@ -1447,7 +1417,7 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[x]));
                 // S comes ahead of P V: not a tile ahead of the warps that write P
-                if (t > it.t0 && !wait_all(smem_u32(&bars->pv_done[x]), (m_tiles - 1) & 1, abort_flag)) {
+                if (t > tb && !wait_all(smem_u32(&bars->pv_done[x]), (c - 1) & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -1495,7 +1465,7 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
             if (since == kRowsTiles) since = 0;
             ++since;
             // O, and the room for P, are free once the P V of the tile before is done
-            if (t > it.t0 && !wait_all(smem_u32(&bars->pv_done[x]), (m_tiles - 1) & 1, abort_flag)) {
+            if (t > tb && !wait_all(smem_u32(&bars->pv_done[x]), (c - 1) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -1508,7 +1478,7 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
                     M = fmaxf(M, ref);
                     l *= alpha;
                 }
-                if (t > it.t0) {
+                if (t > tb) {
                     tc_fence_after();
 #pragma unroll 1
                     for (int q = 0; q < 8; ++q) {
@@ -1553,7 +1523,7 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
                         // 16-byte chunks 2 q and 2 q + 1 of the row, swizzled
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(prow + (((2 * q + u) ^ (lr & 7)) << 4));
+                            uint4 *dst = reinterpret_cast<uint4 *>(prow + (((2 * q + u) ^ (r & 7)) << 4));
                             dst[0] = make_uint4(w0[4 * u], w0[4 * u + 1], w0[4 * u + 2], w0[4 * u + 3]);
                             dst[kPanelBytes / 16] = make_uint4(w1[4 * u], w1[4 * u + 1], w1[4 * u + 2], w1[4 * u + 3]);
                         }
@@ -1571,7 +1541,24 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
         if (!ok) break;
 
         // epilogue: O of a unit that this CTA covers alone, else a partial
-        if (!wait_all(smem_u32(&bars->pv_done[x]), (m_tiles - 1) & 1, abort_flag)) break;
+        if (tb < it.t1 && !wait_all(smem_u32(&bars->pv_done[x]), (c - 1) & 1, abort_flag)) break;
+        const bool two = it.t1 - it.t0 > 1;             // group 1 has an O of the same rows
+        if (x == 1) {
+            bars->stat[r] = make_float2(m, l);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->stat_full));
+            // group 0 reads this group's O: not overwritten before it has
+            if (!wait_all(smem_u32(&bars->epi_done), i & 1, abort_flag)) break;
+            continue;
+        }
+        if (!wait_all(smem_u32(&bars->stat_full), i & 1, abort_flag)) break;
+        const float2 other = bars->stat[r];
+        const float mm = fmaxf(m, other.x);
+        const float f0 = m == -INFINITY && l == 0.f ? 0.f : ex2(m - mm);              // factors of the groups' O; NaN stays NaN
+        const float f1 = other.x == -INFINITY && other.y == 0.f ? 0.f : ex2(other.x - mm);
+        l = l * f0 + other.y * f1;
+        m = mm;
         const bool whole = it.t1 - it.t0 == it.nt;
         const int part = 2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
         if (threadIdx.x == 0 && !whole) {
@@ -1588,10 +1575,18 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
                 uint32_t o[32];
                 tmem_ld32(o_tm + 32 * q, o);
                 tmem_wait_ld(o);
+                uint32_t o1[32];
+                if (two) {
+                    tmem_ld32(o_tm + kD + 32 * q, o1);
+                    tmem_wait_ld(o1);
+                }
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = empty ? 0u : __float_as_uint(__uint_as_float(o[k]) * inv);
+                for (int k = 0; k < 32; ++k) {
+                    const float both = __uint_as_float(o[k]) * f0 + (two ? __uint_as_float(o1[k]) * f1 : 0.f);
+                    o[k] = empty ? 0u : __float_as_uint(both * inv);
+                }
                 if (row_ok && !whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + ((int64_t)part * C::R + r) * kD + 32 * q);
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + ((int64_t)part * kRows + r) * kD + 32 * q);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 } else if (row_ok) {
@@ -1604,12 +1599,13 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
                 }
             }
             if (row_ok) {
-                if (!whole) p.part_lse[(int64_t)part * C::R + r] = lse;
+                if (!whole) p.part_lse[(int64_t)part * kRows + r] = lse;
                 else if (p.lse) p.lse[at] = lse;
             }
         }
         tc_fence_before();
         __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->epi_done));
     }
     if (threadIdx.x == 0)               // empty slots; one that is missing (a CTA that gave up) also ends its unit
         for (int s = 0; s < 2; ++s)
@@ -1626,7 +1622,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
-            mbar_init(smem_u32(&bars->q_full[x]), 4);
+            mbar_init(smem_u32(&bars->q_full[x]), 8);          // the warps that write its rows
             mbar_init(smem_u32(&bars->s_full[x]), 1);
             mbar_init(smem_u32(&bars->p_full[x][0]), 4);
             mbar_init(smem_u32(&bars->p_full[x][1]), 4);
@@ -1636,12 +1632,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         }
         for (int s = 0; s < C::NS; ++s) {
             mbar_init(smem_u32(&bars->kv_full[s]), 33);          // the bytes, and the lanes' scales
-            mbar_init(smem_u32(&bars->kv_empty[s]), 2);          // the MMA warps
+            mbar_init(smem_u32(&bars->kv_empty[s]), 1);          // its group's MMA warp
         }
         for (int s = 0; s < kPagedItems; ++s) {
             mbar_init(smem_u32(&bars->item_full[s]), 1);
             mbar_init(smem_u32(&bars->item_empty[s]), 10);       // the softmax and MMA warps
         }
+        mbar_init(smem_u32(&bars->q_empty), 2);
+        mbar_init(smem_u32(&bars->stat_full), 4);
+        mbar_init(smem_u32(&bars->epi_done), 4);
         bars->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -1763,14 +1762,12 @@ __global__ void __launch_bounds__(32 * kPagedMergeWarps) fmha_paged_merge_kernel
 // Host side
 // ---------------------------------------------------------------------------
 
-// Query rows of a unit: as many groups of 16 as a sequence's rows of a kv head
-// fill, one, two or (also for more) four; 256, the kernel for chunks, where
-// sequences have 112 and more on average (four sequences of 8192 keys, 4 heads a
-// kv head, four groups / chunks in us: 20 tokens each 47.9 / 51.9, 32 55.5 / 53.4,
-// 64 83.6 / 65.3).
-int paged_rows(int64_t max_q, int G, int64_t N, int B) {
-    return max_q * G <= 16 ? 16 : max_q * G <= 32 ? 32 : max_q * G <= 64 || N * G < (int64_t)112 * B ? 64 : 2 * kRows;
-}
+// Query rows of a unit: 16 or 32 where a sequence's rows of a kv head fit them,
+// else 128.  (16 sequences of 28 rows on 6000 keys: 45.6 us in units of 32, 57.1 of
+// 128; 4 sequences of 8192 keys and 64 / 80 / 128 rows: 35 / 48 / 56 in units of 64,
+// two groups a pipeline, 32 / 34 / 37 of 128; 160 / 256 / 2048 rows: 53 / 59 / 229 in
+// units of 256, a block of rows a group, 45 / 50 / 224 of 128.)
+int paged_rows(int64_t max_q, int G) { return max_q * G <= 16 ? 16 : max_q * G <= 32 ? 32 : kRows; }
 
 using PagedKernel = void (*)(CUtensorMap, CUtensorMap, PagedParams);
 struct PagedLaunch {
@@ -1783,9 +1780,9 @@ PagedLaunch paged_launch() {
 }
 template <bool BF>
 PagedLaunch paged_kernel(int rows, int per_unit) {
-    if (rows == 2 * kRows) return {fmha_paged_rows_kernel<BF>, RowsCfg<BF>::SMEM_BYTES, kRowsThreads};
-    return rows == 64 ? paged_launch<BF, 4, 16>() : rows == 32 ? paged_launch<BF, 2, 16>()
-           : per_unit <= 4 ? paged_launch<BF, 1, 4>() : per_unit <= 8 ? paged_launch<BF, 1, 8>() : paged_launch<BF, 1, 16>();
+    if (rows == kRows) return {fmha_paged_rows_kernel<BF>, RowsCfg<BF>::SMEM_BYTES, kRowsThreads};
+    if (rows == 32) return paged_launch<BF, 2, 16>();
+    return per_unit <= 4 ? paged_launch<BF, 1, 4>() : per_unit <= 8 ? paged_launch<BF, 1, 8>() : paged_launch<BF, 1, 16>();
 }
 
 }  // namespace
@@ -1801,7 +1798,7 @@ using namespace fmha;
 extern "C" size_t fmha_page_workspace_size(int max_q, int H, int H_k) {
     if (max_q <= 0 || H <= 0 || H_k <= 0 || H % H_k != 0 || H / H_k > kRows) return 0;
     // two partials a CTA: an fp32 row of O and its LSE for every row of a unit, and whose they are
-    return (size_t)2 * kPagedMaxCtas * (paged_rows(max_q, H / H_k, 112, 1) * (kD + 1) * sizeof(float) + sizeof(PagedMeta));
+    return (size_t)2 * kPagedMaxCtas * (paged_rows(max_q, H / H_k) * (kD + 1) * sizeof(float) + sizeof(PagedMeta));
 }
 
 extern "C" int fmha_page_fwd(fmha_tensor q, const void *k_pages, const void *v_pages, const float *k_scale,
@@ -1846,7 +1843,7 @@ extern "C" int fmha_page_fwd(fmha_tensor q, const void *k_pages, const void *v_p
     const int sms = sm_count();
     if (sms <= 0) return FMHA_ERR_CUDA;
 
-    const int G = H / H_k, R = paged_rows(max_q, G, N, B);
+    const int G = H / H_k, R = paged_rows(max_q, G);
     PagedParams p{};
     p.q = static_cast<const uint8_t *>(q.data);
     p.o = o.data;

@@ -562,7 +562,7 @@ int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_t k_head_st
  * cached rows at or past a sequence's length are never used, and may hold any
  * bits; a value that only some of a call's rows see must be finite.
  *
- * workspace: fmha_page_workspace_size(max_q, H, H_k) bytes (40.2 MB at most),
+ * workspace: fmha_page_workspace_size(max_q, H, H_k) bytes (20.1 MB at most),
  * 256-byte aligned, no initialisation, not shared with a concurrent call.  The
  * call allocates nothing and is asynchronous on `stream` (two kernels).
  * Returns FMHA_OK, FMHA_ERR_INVALID_ARG (bad sizes or pointers, scale not

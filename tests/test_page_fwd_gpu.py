@@ -84,7 +84,7 @@ def sequence(c, b, g, x):
 def check(c, o, lse, scale=128 ** -0.5, out_scale=1.0, rows=None):
     o, lse = o.cpu(), lse.cpu()
     G, at = c["H"] // c["H_k"], 0
-    chunk = max(c["n"]) * G > 64 and len(c["q"]) * G >= 112 * len(c["L"])
+    chunk = max(c["n"]) * G > 32
     for b, (L, n) in enumerate(zip(c["L"], c["n"])):
         pick = torch.arange(n) if rows is None else torch.tensor(sorted({r for r in rows(n) if r < n}), dtype=torch.long)
         j, t = torch.arange(L), pick[:, None]
