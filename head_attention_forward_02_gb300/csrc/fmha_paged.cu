@@ -19,16 +19,16 @@
 //        has a third term, added to the second's columns by an MMA of its own;
 //   P' = p_0 + p_1 / 16, off by 2^-8 of a weight at most, 16 times less than
 //        the rounding that made the codes.
-// A group of 16 query rows is thus 32 columns, [16 first terms | 16 second],
-// and a unit one such group or up to four (prompt chunks), of one kv head.
+// A group of 16 query rows is thus 32 columns, [16 first terms | 16 second], and a
+// unit one or two such groups of one kv head: single tokens, drafts, the ends of
+// prompts.  More rows have a kernel of their own, further down.
 //
 // e4m3 ends at 448 and 2^-9, so P' = exp2(y_j - m) with y_j = x_j log2(e) +
 // log2(v_scale) is relative to a reference m per row, that a group of at most
 // eight key tiles has: the next group sets its own, up or down, from the maximum
 // of its first tile, and O^T in TMEM and the row sums are brought to it.  A
-// score that outgrows the reference opens a new group early (of 64 rows some do
-// in every sixth tile; a reference up to 2^2 higher, if one was that high before,
-// makes these fewer).
+// score that outgrows the reference opens a new group early (a reference up to
+// 2^2 higher, if one was that high before, makes these fewer).
 // So a long context of small weights behind a large one is not rounded to
 // nothing: of a group's weight, what e4m3's smallest steps lose is 2^-6 at most
 // (1024 weights of 2^-14 where the largest is 2^2 or more), or 2^-42 a key of the
@@ -38,15 +38,21 @@
 //
 // Work: the key tiles of all units form one sequence cut evenly over the CTAs,
 // one an SM; units that a cut goes through leave normalised fp32 partials,
-// which a second kernel joins.  A CTA's producer warp (page ids, TMA, the
-// scales by cp.async) fills a ring of 128-key tiles, a q warp splits the next
-// unit's rows into terms, and two pipelines, each an MMA issuer and four softmax
-// warps with S^T, P^T and O^T of their own, go through the tiles: in units of
-// up to 32 rows each takes every other tile with all rows, from a ring of its
-// own, and their O are added up at the end; in larger ones both take every
-// tile, each with half the groups.  A softmax thread is a key, and for O^T a dim.
-// One pipeline of eight softmax warps with a vote for each tile spent 3550
-// cycles a tile of 64 rows, issuing 45% of them.
+// which a second kernel joins.  A CTA's producer warps (page ids, TMA, the scales
+// by cp.async) fill rings of 128-key tiles, a q warp splits the next unit's rows
+// into terms, and two pipelines, each an MMA issuer and four softmax warps with
+// S^T, P^T and O^T of their own, go through the tiles: in units of up to 16 rows
+// each takes every other tile with all rows, from a ring of its own, and their O
+// are added up at the end; of two groups each takes one, of every tile.  A softmax
+// thread is a key, and for O^T a dim.
+//
+// Bound by HBM where there are few rows.  64 sequences of 2100 to 8192 keys, 32/8
+// heads, bf16: 109 us, 6.2 TB/s, 92% of the copy rate (one pipeline, and scales
+// loaded by the softmax threads: 149); 8 of 8200 to 32768 in pages of 16, 64/8 heads,
+// f16: 75 us, 71%; one sequence of 1000: 10.7 us, all latency: 2.5 to the first
+// item, 5 to the first S, 7.5 to the last O, the rest the join.  16 sequences of 1500
+// to 6000 with 7 tokens: 45 us where the bytes take 19: a tile's chain of S, vote,
+// weights and P V takes 1.1 us where its bytes take 0.73.
 #include "fmha_cache.cuh"
 
 namespace fmha {
@@ -113,7 +119,6 @@ struct PagedParams {
     PagedMeta *meta;                     // [2 * ncta]
     int B, N, max_q, H, H_k, G, B_table, width, n_pages, shift;
     int tau, tau_log;                    // tokens of a unit, a power of two
-    int subs;                            // units of a token (groups of more than R heads)
     int causal, edge, ncta;
     float c, out_scale;                  // c: scale * log2(e)
 };
@@ -276,8 +281,8 @@ __device__ __forceinline__ void split4(const float (&e)[4], uint32_t &hi, uint32
 }
 
 // ---------------------------------------------------------------------------
-// Work: of every sequence b, kv head g: blocks v of tau tokens, each in `subs`
-// units.  Block v's tiles reach to the last key that one of its tokens sees.
+// Work: of every sequence b, kv head g: blocks v of tau tokens, a unit each, whose
+// rows are the group's heads of these tokens.  Block v's tiles reach to the last key that one of its tokens sees.
 // A unit is `edge` tiles of nothing, for the work at its ends, and then its own.
 // ---------------------------------------------------------------------------
 
@@ -311,13 +316,13 @@ __device__ __forceinline__ int64_t paged_before(const PagedParams &p, const Page
     const int f = imin(v, s.full), sh = 7 - p.tau_log;
     const int64_t d = (int64_t)(imax(s.base, 0) - 1) >> p.tau_log;     // tiles of block i: floor((i + 1 + d) / 2^sh) + 1
     const int64_t tiles = floor_sum(d + f, sh) - floor_sum(d, sh) + f + (int64_t)(v - f) * s.all;
-    return (tiles + (int64_t)v * p.edge) * p.subs;
+    return tiles + (int64_t)v * p.edge;
 }
 
 struct PagedCursor {
     PagedSeq s;
     int64_t off, G0, G1;                 // off: where the unit at hand begins; this CTA's range
-    int b, g, v, sub;
+    int b, g, v;
 };
 
 // One warp: this CTA's range and its first unit (the same in every lane).
@@ -336,7 +341,7 @@ __device__ void paged_schedule(const PagedParams &p, PagedCursor &cur, int lane)
     cur.G1 = min(cur.G0 + per, T);
     cur.b = p.B;
     cur.off = T;
-    cur.g = cur.v = cur.sub = 0;
+    cur.g = cur.v = 0;
     if (blockIdx.x == gridDim.x - 1)     // reports values outside their bounds, once a call
         for (int b = lane; b < p.B; b += 32) paged_seq(p, b, true);
     int64_t base = 0;
@@ -366,10 +371,7 @@ __device__ void paged_schedule(const PagedParams &p, PagedCursor &cur, int lane)
                 else hi = mid;
             }
             cur.v = lo;
-            const int64_t at = paged_before(p, cur.s, lo);
-            const int unit = paged_tiles(p, cur.s, lo) + p.edge;
-            cur.sub = (int)((x - at) / unit);
-            cur.off += cur.g * head + at + (int64_t)cur.sub * unit;
+            cur.off += cur.g * head + paged_before(p, cur.s, lo);
             return;
         }
         base += __shfl_sync(0xffffffffu, incl, 31);
@@ -381,7 +383,7 @@ __device__ bool paged_next(const PagedParams &p, PagedCursor &cur, PagedItem &it
     if (cur.b >= p.B || cur.off >= cur.G1) return false;
     while (cur.s.nv == 0 || cur.g == p.H_k) {                // the next sequence that has tokens
         if (++cur.b >= p.B) return false;
-        cur.g = cur.v = cur.sub = 0;
+        cur.g = cur.v = 0;
         cur.s = paged_seq(p, cur.b, false);
     }
     const int nt = paged_tiles(p, cur.s, cur.v);
@@ -396,20 +398,11 @@ __device__ bool paged_next(const PagedParams &p, PagedCursor &cur, PagedItem &it
     it.tok0 = cur.v << p.tau_log;
     it.row0 = cur.s.row0 + it.tok0;
     it.h0 = cur.g * p.G;
-    if (p.subs == 1) {
-        it.rows = imin(p.tau, cur.s.n - it.tok0) * p.G;
-    } else {                             // rows are heads of one token
-        const int R = (p.G + p.subs - 1) / p.subs;
-        it.h0 += cur.sub * R;
-        it.rows = imin(R, p.G - cur.sub * R);
-    }
+    it.rows = imin(p.tau, cur.s.n - it.tok0) * p.G;
     cur.off += p.edge + nt;
-    if (++cur.sub == p.subs) {
-        cur.sub = 0;
-        if (++cur.v == cur.s.nv) {
-            cur.v = 0;
-            ++cur.g;
-        }
+    if (++cur.v == cur.s.nv) {
+        cur.v = 0;
+        ++cur.g;
     }
     return true;
 }
@@ -574,7 +567,7 @@ __device__ __forceinline__ void paged_terms(const PagedParams &p, uint8_t *smem,
     uint2 v[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        const int r = r0 + k, t = p.subs == 1 ? r / p.G : 0;
+        const int r = r0 + k, t = r / p.G;
         const int at = r < it.rows ? (it.row0 + t) * p.H + it.h0 + r - t * p.G : -1;
         v[k] = at >= 0 ? *reinterpret_cast<const uint2 *>(p.q + ((int64_t)at * kD + lane * 4) * 2) : make_uint2(0u, 0u);
         if (lane == k) {
@@ -1109,23 +1102,29 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 }
 
 // ---------------------------------------------------------------------------
-// Chunks of prompts: units of up to 256 rows, and the roles not swapped.
+// Chunks of prompts: units of up to 128 rows, and the roles not swapped.
 //
-// With 64 rows a unit the kernel above is bound by what its softmax does across
-// threads (a key each): the scores of 32 rows a thread, their references and
-// votes took 3400 cycles a tile where the MMAs need 800.  Here S = Q K^T has
-// the rows as M: a thread is a row (TMEM lane), its reference, sum and limit are
-// in registers, nothing is exchanged, and a page's scale is one factor for its
-// columns.  Two row blocks of 128 share a tile, each with its softmax group and
-// MMA issuer.  The terms are passes of their own into the same accumulator:
+// With more rows the kernel above is bound by what its softmax does across threads
+// (a key each): the scores of 32 rows a thread, their references and votes took
+// 3400 cycles a tile of 64 rows where the MMAs need 800.  Here S = Q K^T has the
+// rows as M: a thread is a row (TMEM lane), its reference, sum and limit are in
+// registers, nothing is exchanged, and a page's scale is one factor for its
+// columns.  Two groups, each an MMA issuer and four softmax warps with a ring, S, P
+// and O of their own, take every other tile, and their O are added up at the
+// end.  The terms are passes of their own into the same accumulator:
 //   S  = Q_0 K^T + Q_1 K^T (+ Q_2 K^T, f16), without a factor of 16, so that elements
 //        of q below 2^-9 (f16 2^-6) of their row's largest are off by 2^-17 of it;
 //   O += P_0 V + P_1 V, where P_1, what e4m3 left of a weight, is e5m2: its
 //        smallest step is 2^-16, so a weight is off by 2^-7 of itself or by 2^-17
 //        where the group's largest is 1 or more; a group has 16 tiles, and loses
 //        2^-6 of its weight at most.
-// Bound by the tensor cores: four e4m3 products of 128 x 128 x 128 a block and
-// tile, which is the time of the two that bf16 operands would take.
+//
+// The tensor cores do four (f16: five) e4m3 products of 128 x 128 x 128 a tile, the
+// time of the two that bf16 operands would take.  What bounds it is the softmax:
+// of 4 chunks of 512 tokens on 8192 keys (222 us, 840 TFLOP/s; flops 97 at the bf16
+// rate) the tensor pipe is busy 36% of the time, the ALU, which splits the weights,
+// 50%, and a group's tile is a chain of 5300 cycles.  Units of 256 rows, a block a group,
+// were no faster (229); P over S in TMEM, so that S waits for P V, 240 there.
 // ---------------------------------------------------------------------------
 
 constexpr int kRowsSlots = 8;            // ring of K and V tiles at most
@@ -1372,12 +1371,12 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
     int parts = 0;                                      // bit s: slot s of this CTA holds a partial
     PagedItem it;
     for (uint32_t i = 0; rows_take(bars, i, it, abort_flag, lane); ++i) {
-        const int tok = p.subs == 1 ? r / p.G : 0;
+        const int tok = r / p.G;
         const bool row_ok = r < it.rows;
         const int at = row_ok ? (it.row0 + tok) * p.H + it.h0 + r - tok * p.G : -1;
         // the unit's rows of q, 16 a warp, for both groups; the S MMAs of the item before are done
         if (i > 0 && !wait_all(smem_u32(&bars->q_empty), (i - 1) & 1, abort_flag)) break;
-        const int k = warp * 16 + (lane & 15), tk = p.subs == 1 ? k / p.G : 0;
+        const int k = warp * 16 + (lane & 15), tk = k / p.G;
         const float gk = rows_terms<C>(p, smem, k < it.rows ? (it.row0 + tk) * p.H + it.h0 + k - tk * p.G : -1, warp * 16, lane);
         if (lane < 16) bars->qscale[k] = gk;
         proxy_fence();
@@ -1687,7 +1686,7 @@ template <bool BF>
 __device__ __forceinline__ void paged_store_row(const PagedParams &p, const PagedMeta &m, int r, float4 acc, float sum, float mx,
                                                 int lane) {
     const float inv = sum == 0.f ? 0.f : p.out_scale / sum;
-    const int t = p.subs == 1 ? r / p.G : 0;
+    const int t = r / p.G;
     const int64_t at = (int64_t)(m.row0 + t) * p.H + m.h0 + r - t * p.G;
     reinterpret_cast<uint2 *>(p.o)[at * (kD / 4) + lane] =
         make_uint2(pack2<BF>(acc.x * inv, acc.y * inv), pack2<BF>(acc.z * inv, acc.w * inv));
@@ -1864,13 +1863,12 @@ extern "C" int fmha_page_fwd(fmha_tensor q, const void *k_pages, const void *v_p
     p.width = max_pages;
     p.n_pages = n_pages;
     p.shift = shift;
-    p.subs = G > R ? (G + R - 1) / R : 1;
-    while (p.subs == 1 && (2 << p.tau_log) * G <= R) ++p.tau_log;
+    while ((2 << p.tau_log) * G <= R) ++p.tau_log;
     p.tau = 1 << p.tau_log;
     p.causal = mask == FMHA_MASK_CAUSAL;
     p.edge = 2;
     // a CTA a tile at most, of the tiles that there can be
-    const int64_t units = (int64_t)H_k * p.subs * ((int64_t)B + (N >> p.tau_log));
+    const int64_t units = (int64_t)H_k * ((int64_t)B + (N >> p.tau_log));
     const int64_t tiles = (((int64_t)max_pages << shift) + kRows - 1) / kRows;
     p.ncta = (int)(units >= kPagedMaxCtas || units * tiles >= kPagedMaxCtas ? kPagedMaxCtas : units * tiles);
     p.ncta = imin(p.ncta, sms);
