@@ -18,7 +18,7 @@
 //        elements down to 2^-13 of its largest (2^k: a power of two per row); f16
 //        has a third term, added to the second's columns by an MMA of its own;
 //   P' = p_0 + p_1 / 16, off by 2^-8 of a weight at most, 16 times less than
-//        the rounding that made the codes.
+//        the rounding that made the codes; f16: + p_2 / 256, off by 2^-11.
 // A group of 16 query rows is thus 32 columns, [16 first terms | 16 second], and a
 // unit one or two such groups of one kv head: single tokens, drafts, the ends of
 // prompts.  More rows have a kernel of their own, further down.
@@ -85,17 +85,20 @@ struct PagedCfg {
     static constexpr int QW = SW, PROD = SW + 1, MMA = PROD + NP;   // q warp, producers, two MMA issuers
     static constexpr int THREADS = 32 * (MMA + 2);
     static constexpr int COLS = 32;                           // of a pipeline's S^T and O^T: a group's
-    static constexpr int PIPE_COLS = 4 * COLS;                // TMEM: two S^T, then O^T (and nothing, to a power of two)
+    static constexpr bool THIRD = !BF;                        // weights have a third term:
+    static constexpr bool INLINE3 = THIRD && NR <= 8;         // in columns 8 .. 15 of the group, else a tile of its own
+    static constexpr int PIPE_COLS = 4 * COLS;                // TMEM: two S^T, O^T, and O^T of third terms that are apart
     static constexpr int TMEM_COLS = 2 * PIPE_COLS;
     static constexpr int P_ROW = COLS;                        // bytes of a key's P^T row
-    static constexpr int P_BYTES = kRows * P_ROW;
+    static constexpr int P_TILE = kRows * P_ROW;
+    static constexpr int P_BYTES = P_TILE * (THIRD && !INLINE3 ? 2 : 1);
     static constexpr uint64_t P_SWZ = 6;                      // 32-byte swizzle
     static constexpr int Q_BYTES = (BF ? 32 : 48) * NG * 128; // first and second terms, then f16's third
     static constexpr int STAGE = 2 * kPanelBytes;             // K and V of 128 keys
     static constexpr int OFF_P = 2 * Q_BYTES;                 // two buffers a pipeline
     static constexpr int OFF_KV = OFF_P + 4 * P_BYTES;
     static constexpr int NS_FIT = (226 * 1024 - kPagedBars - OFF_KV) / STAGE;
-    static constexpr int NS = NS_FIT < kStagesPaged ? NS_FIT : kStagesPaged;
+    static constexpr int NS = NS_FIT >= kStagesPaged ? kStagesPaged : SPLIT ? NS_FIT & ~1 : NS_FIT;
     static constexpr int RING = SPLIT ? NS / 2 : NS;          // stages of a ring
     static constexpr int OFF_BARS = OFF_KV + NS * STAGE;
     static constexpr int SMEM_BYTES = OFF_BARS + kPagedBars + 1024;   // 1 KB alignment
@@ -226,6 +229,21 @@ __device__ __forceinline__ void wait_terms(uint32_t (&r)[2 * NR]) {
     }
 }
 
+// As split4, with a third term: p = hi + mid / 16 + low / 256.
+__device__ __forceinline__ void split4_third(const float (&e)[4], uint32_t &hi, uint32_t &mid, uint32_t &low) {
+    const uint32_t p = pack2<false>(e[0], e[1]), q = pack2<false>(e[2], e[3]);
+    asm("{\n.reg .b16 a, b;\n.reg .b32 x, y, u, v;\n"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, %3;\ncvt.rn.satfinite.e4m3x2.f16x2 b, %4;\nmov.b32 %0, {a, b};\n"
+        "cvt.rn.f16x2.e4m3x2 x, a;\ncvt.rn.f16x2.e4m3x2 y, b;\nsub.rn.f16x2 x, %3, x;\nsub.rn.f16x2 y, %4, y;\n"
+        "mul.rn.f16x2 x, x, %5;\nmul.rn.f16x2 y, y, %5;\n"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\ncvt.rn.satfinite.e4m3x2.f16x2 b, y;\nmov.b32 %1, {a, b};\n"
+        "cvt.rn.f16x2.e4m3x2 u, a;\ncvt.rn.f16x2.e4m3x2 v, b;\nsub.rn.f16x2 x, x, u;\nsub.rn.f16x2 y, y, v;\n"
+        "mul.rn.f16x2 x, x, %5;\nmul.rn.f16x2 y, y, %5;\n"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\ncvt.rn.satfinite.e4m3x2.f16x2 b, y;\nmov.b32 %2, {a, b};\n}\n"
+        : "=&r"(hi), "=&r"(mid), "=&r"(low)
+        : "r"(p), "r"(q), "r"(0x4c004c00u));                 // 16, 16
+}
+
 // Bounded waits as in fmha_cache.cuh, but with a hint that lets the hardware
 // suspend the warp for up to 20 us: most of a CTA's warps wait most of the time,
 // and polling took as many issue slots as the softmax.
@@ -253,6 +271,34 @@ __device__ __noinline__ bool hinted_slow(uint32_t bar, uint32_t parity, volatile
 __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
     const bool r = hinted_try(bar, parity) || hinted_slow(bar, parity, abort_flag);
     return __all_sync(0xffffffffu, r);
+}
+
+// N consecutive columns, waited for; and stored.
+template <int N>
+__device__ __forceinline__ void ld_cols(uint32_t taddr, uint32_t (&r)[N]) {
+    if constexpr (N == 16) {
+        tmem_ld16(taddr, r);
+        tmem_wait_ld16(r);
+    } else if constexpr (N == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\ntcgen05.wait::ld.sync.aligned;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr)
+                     : "memory");
+    } else {
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\ntcgen05.wait::ld.sync.aligned;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(taddr)
+                     : "memory");
+    }
+}
+template <int N>
+__device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&r)[N]) {
+    if constexpr (N == 16) tmem_st16(taddr, r);
+    else if constexpr (N == 8) tmem_st8(taddr, r);
+    else
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                     "r"(r[2]), "r"(r[3])
+                     : "memory");
 }
 
 // Four weights as two terms each (first weight in the low byte), by way of f16,
@@ -621,7 +667,7 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
     volatile int *abort_flag = &bars->abort;
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0) + w * C::PIPE_COLS;
     const uint64_t q0 = desc_sw(smem_u32(smem), 16, 1024, 2);
-    const uint64_t p0 = desc_sw(smem_u32(smem + C::OFF_P + w * 2 * C::P_BYTES), C::P_BYTES, 8 * C::P_ROW, C::P_SWZ);
+    const uint64_t p0 = desc_sw(smem_u32(smem + C::OFF_P + w * 2 * C::P_BYTES), C::P_TILE, 8 * C::P_ROW, C::P_SWZ);
     const uint64_t k0 = desc_sw(smem_u32(smem + C::OFF_KV), 16, 1024, 2);
     const uint64_t v0 = desc_sw(smem_u32(smem + C::OFF_KV + kPanelBytes), kPanelBytes, 1024, 2);   // MN-major
     constexpr int kStep = C::SPLIT ? 2 : 1;
@@ -638,6 +684,11 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
         for (int kk = 0; kk < 4; ++kk)   // 32 keys
             mma_ss<true>(o_tm, v + ((kk * 32 * 128) >> 4), pt + ((kk * 32 * C::P_ROW) >> 4), paged_idesc(32, true),
                          kk > 0 || !begins ? 1u : 0u);
+        if constexpr (C::THIRD && !C::INLINE3)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                mma_ss<true>(o_tm + C::COLS, v + ((kk * 32 * 128) >> 4), pt + ((C::P_TILE + kk * 32 * C::P_ROW) >> 4),
+                             paged_idesc(16, true), kk > 0 || !begins ? 1u : 0u);
         tc_commit(smem_u32(&bars->pv_done[w][b]));
         tc_commit(smem_u32(&bars->kv_empty[st]));
         return true;
@@ -864,6 +915,14 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                         }
                     }
                     st_terms<NR>(tmem + 2 * C::COLS, s);
+                    if constexpr (C::THIRD) {
+                        uint32_t z[NR];
+                        ld_cols<NR>(tmem + (C::INLINE3 ? 2 * C::COLS + 8 : 3 * C::COLS), z);
+#pragma unroll
+                        for (int k = 0; k < NR; ++k)
+                            z[k] = __float_as_uint(__uint_as_float(z[k]) * bars->am[w][row0 + k]);
+                        st_cols<NR>(tmem + (C::INLINE3 ? 2 * C::COLS + 8 : 3 * C::COLS), z);
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < NR; k += 4) {
@@ -884,7 +943,7 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
             const uint64_t isv2 = pack_f2(isv, isv);
             uint8_t *prow = pbuf + b * C::P_BYTES + r * C::P_ROW;
             const uint32_t swz = (r >> 2) & 1;
-            uint32_t hi[NR / 4], mid[NR / 4];
+            uint32_t hi[NR / 4], mid[NR / 4], low[NR / 4];
 #pragma unroll
             for (int k = 0; k < NR; k += 4) {
                 float v[4];
@@ -894,18 +953,22 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                 for (int q = 0; q < 4; ++q) v[q] = ex2(v[q]);
                 l[k / 2] = fma_f2(pack_f2(v[0], v[1]), isv2, l[k / 2]);
                 l[k / 2 + 1] = fma_f2(pack_f2(v[2], v[3]), isv2, l[k / 2 + 1]);
-                split4<false>(v, hi[k / 4], mid[k / 4]);
+                if constexpr (C::THIRD) split4_third(v, hi[k / 4], mid[k / 4], low[k / 4]);
+                else split4<false>(v, hi[k / 4], mid[k / 4]);
             }
             uint8_t *ph = prow + (swz << 4), *pm = prow + ((1 ^ swz) << 4);
             if constexpr (NR == 16) {
                 *reinterpret_cast<uint4 *>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4 *>(pm) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                if constexpr (C::THIRD) *reinterpret_cast<uint4 *>(ph + C::P_TILE) = make_uint4(low[0], low[1], low[2], low[3]);
             } else if constexpr (NR == 8) {
                 *reinterpret_cast<uint2 *>(ph) = make_uint2(hi[0], hi[1]);
                 *reinterpret_cast<uint2 *>(pm) = make_uint2(mid[0], mid[1]);
+                if constexpr (C::THIRD) *reinterpret_cast<uint2 *>(ph + 8) = make_uint2(low[0], low[1]);
             } else {
                 *reinterpret_cast<uint32_t *>(ph) = hi[0];
                 *reinterpret_cast<uint32_t *>(pm) = mid[0];
+                if constexpr (C::THIRD) *reinterpret_cast<uint32_t *>(ph + 8) = low[0];
             }
             proxy_fence();
             __syncwarp();
@@ -920,16 +983,21 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
             ok = wait_all(smem_u32(&bars->pv_done[w][(c - 1) & 1]), ((c - 1) >> 1) & 1, abort_flag);
             if (soft_any(w, !ok)) break;
             tc_fence_after();
-        }
-        uint32_t s[2 * NR];
-        const bool there = !first;
-        if (there) {
+            uint32_t s[2 * NR];
             ld_terms<NR>(tmem + 2 * C::COLS, s);
             wait_terms<NR>(s);
-        }
 #pragma unroll
-        for (int k = 0; k < NR; ++k)
-            o[k] = there ? fmaf(__uint_as_float(s[NR + k]), 0.0625f, __uint_as_float(s[k])) : 0.f;
+            for (int k = 0; k < NR; ++k) o[k] = fmaf(__uint_as_float(s[NR + k]), 0.0625f, __uint_as_float(s[k]));
+            if constexpr (C::THIRD) {
+                uint32_t z[NR];
+                ld_cols<NR>(tmem + (C::INLINE3 ? 2 * C::COLS + 8 : 3 * C::COLS), z);
+#pragma unroll
+                for (int k = 0; k < NR; ++k) o[k] = fmaf(__uint_as_float(z[k]), 0x1p-8f, o[k]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < NR; ++k) o[k] = 0.f;
+        }
         tc_fence_before();
 #pragma unroll
             for (int k = 0; k < NR; k += 2) {
