@@ -244,6 +244,19 @@ __device__ __forceinline__ void split4_third(const float (&e)[4], uint32_t &hi, 
         : "r"(p), "r"(q), "r"(0x4c004c00u));                 // 16, 16
 }
 
+// As split4<true>, with a third term, in e5m2: p = hi + mid + low.
+__device__ __forceinline__ void split4_wide_third(const float (&e)[4], uint32_t &hi, uint32_t &mid, uint32_t &low) {
+    const uint32_t p = pack2<false>(e[0], e[1]), q = pack2<false>(e[2], e[3]);
+    asm("{\n.reg .b16 a, b;\n.reg .b32 x, y, u, v;\n"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, %3;\ncvt.rn.satfinite.e4m3x2.f16x2 b, %4;\nmov.b32 %0, {a, b};\n"
+        "cvt.rn.f16x2.e4m3x2 x, a;\ncvt.rn.f16x2.e4m3x2 y, b;\nsub.rn.f16x2 x, %3, x;\nsub.rn.f16x2 y, %4, y;\n"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\ncvt.rn.satfinite.e4m3x2.f16x2 b, y;\nmov.b32 %1, {a, b};\n"
+        "cvt.rn.f16x2.e4m3x2 u, a;\ncvt.rn.f16x2.e4m3x2 v, b;\nsub.rn.f16x2 x, x, u;\nsub.rn.f16x2 y, y, v;\n"
+        "cvt.rn.satfinite.e5m2x2.f16x2 a, x;\ncvt.rn.satfinite.e5m2x2.f16x2 b, y;\nmov.b32 %2, {a, b};\n}\n"
+        : "=&r"(hi), "=&r"(mid), "=&r"(low)
+        : "r"(p), "r"(q));
+}
+
 // Bounded waits as in fmha_cache.cuh, but with a hint that lets the hardware
 // suspend the warp for up to 20 us: most of a CTA's warps wait most of the time,
 // and polling took as many issue slots as the softmax.
@@ -302,8 +315,8 @@ __device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&r)[N]) 
 }
 
 // Four weights as two terms each (first weight in the low byte), by way of f16,
-// whose 11 bits hold a rest exactly: p = hi + mid / 16 in e4m3, or, WIDE, hi + mid
-// with mid in e5m2.  In one piece of PTX, since a 16-bit code that passes through
+// whose 11 bits hold a rest exactly: p = hi + mid / 16 in e4m3, or, WIDE, hi + mid.
+// In one piece of PTX, since a 16-bit code that passes through
 // C++ costs an instruction to widen it.
 template <bool WIDE>
 __device__ __forceinline__ void split4(const float (&e)[4], uint32_t &hi, uint32_t &mid) {
@@ -312,7 +325,7 @@ __device__ __forceinline__ void split4(const float (&e)[4], uint32_t &hi, uint32
         asm("{\n.reg .b16 a, b;\n.reg .b32 x, y;\n"
             "cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\ncvt.rn.satfinite.e4m3x2.f16x2 b, %3;\nmov.b32 %0, {a, b};\n"
             "cvt.rn.f16x2.e4m3x2 x, a;\ncvt.rn.f16x2.e4m3x2 y, b;\nsub.rn.f16x2 x, %2, x;\nsub.rn.f16x2 y, %3, y;\n"
-            "cvt.rn.satfinite.e5m2x2.f16x2 a, x;\ncvt.rn.satfinite.e5m2x2.f16x2 b, y;\nmov.b32 %1, {a, b};\n}\n"
+            "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\ncvt.rn.satfinite.e4m3x2.f16x2 b, y;\nmov.b32 %1, {a, b};\n}\n"
             : "=r"(hi), "=r"(mid)
             : "r"(p), "r"(q));
     } else {
@@ -1182,58 +1195,55 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 // end.  The terms are passes of their own into the same accumulator:
 //   S  = Q_0 K^T + Q_1 K^T (+ Q_2 K^T, f16), without a factor of 16, so that elements
 //        of q below 2^-9 (f16 2^-6) of their row's largest are off by 2^-17 of it;
-//   O += P_0 V + P_1 V, where P_1, what e4m3 left of a weight, is e5m2: its
-//        smallest step is 2^-16, so a weight is off by 2^-7 of itself or by 2^-17
-//        where the group's largest is 1 or more; a group has 16 tiles, and loses
-//        2^-6 of its weight at most.
+//   O += P_0 V + P_1 V (f16: + P_2 V, in e5m2), also without a factor of 16: a weight
+//        is off by 2^-8 (f16 2^-11) of itself, or by 2^-10 (f16 2^-13) where the group's
+//        largest is 2^7 or more; a group has 16 tiles, and loses 2^-6 of its weight
+//        at most.  (P_1 in e5m2 under a largest of 2^2 was 3% faster and twice as far off.)
 //
-// The tensor cores do four (f16: five) e4m3 products of 128 x 128 x 128 a tile, the
+// The tensor cores do four (f16: six) e4m3 products of 128 x 128 x 128 a tile, the
 // time of the two that bf16 operands would take.  What bounds it is the softmax:
-// of 4 chunks of 512 tokens on 8192 keys (222 us, 840 TFLOP/s; flops 97 at the bf16
-// rate) the tensor pipe is busy 36% of the time, the ALU, which splits the weights,
-// 50%, and a group's tile is a chain of 5300 cycles.  Units of 256 rows, a block a group,
-// were no faster (229); P over S in TMEM, so that S waits for P V, 240 there.
+// of 4 chunks of 512 tokens on 8192 keys (229 us, 813 TFLOP/s; f16 291; flops 97 at the
+// bf16 rate) the tensor pipe is busy 39% of the time, the ALU, which splits the weights,
+// 44%, and a group's tile is a chain of 5300 cycles.  Units of 256 rows, a block a group,
+// were 3% slower; P over S in TMEM, so that S waits for P V, 8%.
 // ---------------------------------------------------------------------------
 
-constexpr int kRowsSlots = 8;            // ring of K and V tiles at most
 constexpr int kRowsBars = 4096;          // barrier block
 constexpr int kRowsTiles = 16;           // tiles that a reference serves at most
-constexpr float kRowsBias = 2.f;         // as kBias: lower, as the steps are finer and a rescaling of O costs a tile's exponentials
-constexpr int kRowsThreads = 352;        // two softmax groups of four warps, producer, an MMA issuer a group
+constexpr float kRowsBias = 7.f;         // as kBias: higher, for the second term's sake
+constexpr int kRowsThreads = 384;        // two softmax groups of four warps, producers of K and V, an MMA issuer a group
 
 template <bool BF_>
 struct RowsCfg {
     static constexpr bool BF = BF_;
-    static constexpr int NT = BF ? 2 : 3;                     // terms of q
-    static constexpr int OFF_P = NT * kPanelBytes;            // q's terms, then both terms of each group's P
-    static constexpr int OFF_KV = OFF_P + 4 * kPanelBytes;
-    static constexpr int NS_FIT = (226 * 1024 - kRowsBars - OFF_KV) / kPanelBytes;
-    static constexpr int NS = NS_FIT & ~1;
-    static constexpr int RING = NS / 2;                       // slots of a group's ring
-    static constexpr int OFF_BARS = OFF_KV + NS * kPanelBytes;
+    static constexpr int NT = BF ? 2 : 3;                     // terms of q, and of P
+    static constexpr int OFF_P = NT * kPanelBytes;            // q's terms, then those of each group's P
+    static constexpr int OFF_KV = OFF_P + 2 * NT * kPanelBytes;
+    static constexpr int VS = BF ? 2 : 1;                     // slots of a group for V (K: one, free once its S is there)
+    static constexpr int OFF_BARS = OFF_KV + 2 * (1 + VS) * kPanelBytes;
     static constexpr int SMEM_BYTES = OFF_BARS + kRowsBars + 1024;
-    static_assert(SMEM_BYTES <= 227 * 1024 && RING >= 3 && NS <= kRowsSlots, "shared memory");
-
-    // the n-th K or V tile of group x's ring: K of its c-th tile is n = 2 c, V is 2 c + 1
-    static __device__ __forceinline__ uint32_t slot(int x, uint32_t n) { return x * RING + n % RING; }
-    static __device__ __forceinline__ uint32_t parity(uint32_t n) { return (n / RING) & 1; }
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+    static __device__ __forceinline__ int k_at(int x) { return OFF_KV + x * (1 + VS) * kPanelBytes; }
+    static __device__ __forceinline__ int v_at(int x, uint32_t st) { return k_at(x) + (1 + st) * kPanelBytes; }
 };
 
-struct RowsBars {
+template <int VS>
+struct RowsBarsOf {
     uint64_t q_full[2], q_empty, drain[2], s_full[2], s_free[2], p_full[2][2], pv_done[2];   // by group; p_full by half
     uint64_t stat_full, epi_done;
-    uint64_t kv_full[kRowsSlots], kv_empty[kRowsSlots];
+    uint64_t k_full[2][1], k_empty[2][1], v_full[2][VS], v_empty[2][VS], scale_full[2][2];
     uint64_t item_full[kPagedItems], item_empty[kPagedItems];
     PagedItem item[kPagedItems];
     uint32_t tmem_base;
     int abort;
-    float scale[kRowsSlots][2][8];       // k_scale, v_scale of a V slot's pages
+    float scale[2][2][2][8];             // by group and tile mod 2: k_scale, v_scale of its pages
     float2 stat[kRows];                  // reference and sum of group 1's rows
     float qscale[kRows];                 // of the rows of q
 };
-static_assert(sizeof(RowsBars) <= kRowsBars, "barrier block");
+static_assert(sizeof(RowsBarsOf<2>) <= kRowsBars, "barrier block");
 
-__device__ __forceinline__ bool rows_take(RowsBars *bars, uint32_t i, PagedItem &it, volatile int *abort_flag, int lane) {
+template <int VS>
+__device__ __forceinline__ bool rows_take(RowsBarsOf<VS> *bars, uint32_t i, PagedItem &it, volatile int *abort_flag, int lane) {
     const uint32_t st = i % kPagedItems;
     if (!wait_all(smem_u32(&bars->item_full[st]), (i / kPagedItems) & 1, abort_flag)) return false;
     it = bars->item[st];
@@ -1242,11 +1252,17 @@ __device__ __forceinline__ bool rows_take(RowsBars *bars, uint32_t i, PagedItem 
     return it.rows > 0;
 }
 
-// The producer warp: K and V tiles into the rings, with the pages' scales.
-template <class C>
-__device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, const CUtensorMap *tmK, const CUtensorMap *tmV,
-                              uint8_t *smem, RowsBars *bars, int lane) {
+// A producer warp: the groups' tiles of K, with the pages' scales, or (V) of V.  One
+// warp for both held a group's K back behind the other's V (230 us for 4 chunks of
+// 512, f16 400).
+template <class C, bool V>
+__device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, const CUtensorMap *tm, uint8_t *smem, RowsBarsOf<C::VS> *bars,
+                              int lane) {
     volatile int *abort_flag = &bars->abort;
+    constexpr int SLOTS = V ? C::VS : 1;
+    uint64_t (*full)[SLOTS], (*empty)[SLOTS];
+    if constexpr (V) full = bars->v_full, empty = bars->v_empty;
+    else full = bars->k_full, empty = bars->k_empty;
     bool ok = true;
     if (gate) ok = __all_sync(0xffffffffu, lane > 0 || test_gate_open(abort_flag));
     uint32_t fill[2] = {0, 0}, qn = 0;
@@ -1263,79 +1279,90 @@ __device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, 
     };
     PagedItem it, next;
     if (ok) {
-        paged_next(p, cur, it);
-        ok = publish(0, it);
+        if constexpr (V) ok = rows_take(bars, 0, it, abort_flag, lane);
+        else {
+            paged_next(p, cur, it);
+            ok = publish(0, it);
+        }
     }
     while (ok && it.rows > 0) {
         ++qn;
         const int pages = (it.L + P - 1) >> p.shift;
         auto id_of = [&](int t) {
             const int i = t * per + lane;
-            return lane < per && i < pages && t < it.t1 ? page_id(p, it.entry, i, true) : -1;
+            return lane < per && i < pages && t < it.t1 ? page_id(p, it.entry, i, !V) : -1;
         };
         int id = id_of(it.t0);
-        for (int t = it.t0; ok && t < it.t1; ++t) {
+        for (int t = it.t0; t < it.t1; ++t) {
             const int ahead = id_of(t + 1), here = imax(0, imin(per, pages - t * per));
             // a page outside the cache: a coordinate outside it, which reads zeros
             const int head = id >= 0 ? id * p.H_k + it.g : p.n_pages * p.H_k;
             const int x = (t - it.t0) & 1;
-            for (int kv = 0; kv < 2; ++kv) {
-                const uint32_t n = x ? fill[1] : fill[0], st = C::slot(x, n);
-                if (n >= C::RING && !wait_all(smem_u32(&bars->kv_empty[st]), C::parity(n) ^ 1, abort_flag)) {
-                    ok = false;
-                    break;
+            const uint32_t n = x ? fill[1]++ : fill[0]++, st = n % SLOTS;
+            if (n >= SLOTS && !wait_all(smem_u32(&empty[x][st]), (n / SLOTS) & 1 ^ 1, abort_flag)) {
+                if (x) --fill[1];
+                else --fill[0];
+                ok = false;
+                break;
+            }
+            const uint32_t fb = smem_u32(&full[x][st]);
+            if (lane == 0) mbar_expect_tx(fb, here * (P << 7));
+            __syncwarp();
+            if (lane < here) {
+                tma_load_3d(smem_u32(smem + (V ? C::v_at(x, st) : C::k_at(x))) + lane * (P << 7), tm, fb, 0, 0, head);
+                if constexpr (!V) {
+                    // into the place of the tile two before in this group, which was read
+                    // before S of the one before, and so before this slot was free
+                    const float *ks = id >= 0 ? p.k_scale + head : &g_one, *vs = id >= 0 ? p.v_scale + head : &g_one;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&bars->scale[x][n & 1][0][lane])), "l"(ks)
+                                 : "memory");
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&bars->scale[x][n & 1][1][lane])), "l"(vs)
+                                 : "memory");
                 }
-                const uint32_t fb = smem_u32(&bars->kv_full[st]);
-                if (lane == 0) mbar_expect_tx(fb, here * (P << 7));
-                __syncwarp();
-                if (lane < here) {
-                    tma_load_3d(smem_u32(smem + C::OFF_KV + st * kPanelBytes) + lane * (P << 7), kv ? tmV : tmK, fb, 0, 0, head);
-                    // both scales come with V: its slot, not K's, is kept until the softmax has read them
-                    if (kv) {
-                        const float *ks = id >= 0 ? p.k_scale + head : &g_one, *vs = id >= 0 ? p.v_scale + head : &g_one;
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&bars->scale[st][0][lane])), "l"(ks)
-                                     : "memory");
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&bars->scale[st][1][lane])), "l"(vs)
-                                     : "memory");
+            }
+            if constexpr (!V)
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars->scale_full[x][n & 1])) : "memory");
+            id = ahead;
+            if constexpr (!V)
+                if (t == it.t0) {
+                    paged_next(p, cur, next);
+                    if (!publish(qn, next)) {
+                        ok = false;
+                        break;
                     }
                 }
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(fb) : "memory");
-                if (x) ++fill[1];
-                else ++fill[0];
-            }
-            id = ahead;
-            if (ok && t == it.t0) {
-                paged_next(p, cur, next);
-                ok = publish(qn, next);
-            }
         }
-        it = next;
+        if constexpr (V) ok = ok && rows_take(bars, qn, it, abort_flag, lane);
+        else it = next;
     }
+    // no copy may be in flight when the block ends, nor a product that reads one
+    ok = *abort_flag == 0;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
-        for (uint32_t n = fill[x] > C::RING ? fill[x] - C::RING : 0; n < fill[x]; ++n) {
-            const uint32_t st = C::slot(x, n);
-            if (ok) ok = wait_all(smem_u32(&bars->kv_empty[st]), C::parity(n), abort_flag);
-            if (!ok) mbar_wait_drain(smem_u32(&bars->kv_full[st]), C::parity(n));
+        for (uint32_t n = fill[x] > SLOTS ? fill[x] - SLOTS : 0; n < fill[x]; ++n) {
+            const uint32_t st = n % SLOTS;
+            if (ok) ok = wait_all(smem_u32(&empty[x][st]), (n / SLOTS) & 1, abort_flag);
+            if (!ok) mbar_wait_drain(smem_u32(&full[x][st]), (n / SLOTS) & 1);
+            if (!V) mbar_wait_drain(smem_u32(&bars->scale_full[x][n & 1]), n >> 1 & 1);
         }
-    if (ok && qn > 0) wait_all(smem_u32(&bars->q_empty), (qn - 1) & 1, abort_flag);
+    if (!V && ok && qn > 0) wait_all(smem_u32(&bars->q_empty), (qn - 1) & 1, abort_flag);
 }
 
 // MMA issuer of group x.  P lies in shared memory, apart from S, so that S of the
 // next tile is issued as soon as the softmax has this one's in registers, and
 // P V while it is at the next: with P over S in TMEM a group waited 1700 of 5700
-// cycles a tile for P V and S, one after the other (256 us for 4 chunks of 512).
+// cycles a tile for P V and S, one after the other (15% more for 4 chunks of 512).
 template <class C>
-__device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x, int lane) {
+__device__ void rows_mma(uint8_t *smem, RowsBarsOf<C::VS> *bars, uint32_t tmem_any, int x, int lane) {
     volatile int *abort_flag = &bars->abort;
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
     const uint32_t s_tm = tmem + x * kRows, o_tm = tmem + 2 * kRows + x * kD;
-    constexpr uint32_t kIdS = mma_idesc(0u, kRows, false), kIdP0 = mma_idesc(0u, kD, true);
-    constexpr uint32_t kIdP1 = kIdP0 | (1u << 7);            // A (the weights' second term) e5m2
+    constexpr uint32_t kIdS = mma_idesc(0u, kRows, false), kIdP = mma_idesc(0u, kD, true);
+    constexpr uint32_t kIdP2 = kIdP | (1u << 7);             // A (the weights' third term) e5m2
     const uint64_t q = smem_desc(smem_u32(smem), 16, 1024);
-    const uint64_t k0 = smem_desc(smem_u32(smem + C::OFF_KV), 16, 1024);
-    const uint64_t v0 = smem_desc(smem_u32(smem + C::OFF_KV), kPanelBytes, 1024);
-    const uint64_t p0 = smem_desc(smem_u32(smem + C::OFF_P + x * 2 * kPanelBytes), 16, 1024);
+    const uint64_t k = smem_desc(smem_u32(smem + C::k_at(x)), 16, 1024);
+    const uint64_t v0 = smem_desc(smem_u32(smem + C::v_at(x, 0)), kPanelBytes, 1024);
+    const uint64_t p0 = smem_desc(smem_u32(smem + C::OFF_P + x * C::NT * kPanelBytes), 16, 1024);
     uint32_t m = 0;                      // tiles of this group
     bool ok = true;
     PagedItem it;
@@ -1348,14 +1375,12 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
         if (tb >= it.t1) tc_commit(smem_u32(&bars->q_empty));   // an item of one tile is group 0's alone
         for (int t = tb; ok && tb < it.t1 && t < it.t1 + 2; t += 2) {
             if (t < it.t1) {             // S of this tile
-                const uint32_t n = 2 * m, st = C::slot(x, n);
-                if (!wait_all(smem_u32(&bars->kv_full[st]), C::parity(n), abort_flag) ||
+                if (!wait_all(smem_u32(&bars->k_full[x][0]), m & 1, abort_flag) ||
                     (m > 0 && !wait_all(smem_u32(&bars->s_free[x]), (m - 1) & 1, abort_flag))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t k = k0 + ((st * kPanelBytes) >> 4);
 #pragma unroll
                 for (int term = 0; term < C::NT; ++term)
 #pragma unroll
@@ -1363,13 +1388,13 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
                         mma_ss<true>(s_tm, q + ((term * kPanelBytes + kk * 32) >> 4), k + ((kk * 32) >> 4), kIdS,
                                      term > 0 || kk > 0 ? 1u : 0u);
                 tc_commit(smem_u32(&bars->s_full[x]));
-                tc_commit(smem_u32(&bars->kv_empty[st]));
+                tc_commit(smem_u32(&bars->k_empty[x][0]));
                 if (t + 2 >= it.t1) tc_commit(smem_u32(&bars->q_empty));
                 ++m;
             }
             if (t > tb) {             // P V of the tile before, which is tile m - 1, or m - 2 if S of this one was issued
-                const uint32_t mm = m - (t < it.t1 ? 2 : 1), n = 2 * mm + 1, st = C::slot(x, n);
-                if (!wait_all(smem_u32(&bars->kv_full[st]), C::parity(n), abort_flag)) {
+                const uint32_t mm = m - (t < it.t1 ? 2 : 1), st = mm % C::VS;
+                if (!wait_all(smem_u32(&bars->v_full[x][st]), (mm / C::VS) & 1, abort_flag)) {
                     ok = false;
                     break;
                 }
@@ -1382,16 +1407,16 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
                     }
                     tc_fence_after();
 #pragma unroll
-                    for (int term = 0; term < 2; ++term)
+                    for (int term = 0; term < C::NT; ++term)
 #pragma unroll
                         for (int kk = 0; kk < 2; ++kk)       // 32 keys: 32 bytes of P's rows, 32 rows of V
                             mma_ss<true>(o_tm, p0 + ((term * kPanelBytes + (h * 2 + kk) * 32) >> 4),
-                                         v + (((h * 2 + kk) * 32 * 128) >> 4), term ? kIdP1 : kIdP0,
+                                         v + (((h * 2 + kk) * 32 * 128) >> 4), term == 2 ? kIdP2 : kIdP,
                                          t - 2 > tb || h > 0 || term > 0 || kk > 0 ? 1u : 0u);
                 }
                 if (!ok) break;
                 tc_commit(smem_u32(&bars->pv_done[x]));
-                tc_commit(smem_u32(&bars->kv_empty[st]));
+                tc_commit(smem_u32(&bars->v_empty[x][st]));
             }
         }
     }
@@ -1429,12 +1454,12 @@ __device__ __forceinline__ float rows_terms(const PagedParams &p, uint8_t *tile,
 
 // Softmax and epilogue of group x, a row a thread.
 template <class C>
-__device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars, uint32_t tmem, int warp, int lane) {
+__device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBarsOf<C::VS> *bars, uint32_t tmem, int warp, int lane) {
     volatile int *abort_flag = &bars->abort;
     const int x = warp >> 2, r = (warp & 3) * 32 + lane;   // group, row of the unit
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_tm = lane_base + x * kRows, o_tm = lane_base + 2 * kRows + x * kD;
-    uint8_t *prow = smem + C::OFF_P + x * 2 * kPanelBytes + r * 128;
+    uint8_t *prow = smem + C::OFF_P + x * C::NT * kPanelBytes + r * 128;
     uint32_t c = 0;                                     // tiles of this group
     int parts = 0;                                      // bit s: slot s of this CTA holds a partial
     PagedItem it;
@@ -1461,30 +1486,36 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
         const int tb = it.t0 + x;
         for (int t = tb; t < it.t1; t += 2, ++c) {
             const int nk = it.L - t * kRows, halves = nk > kRows / 2 ? 2 : 1;
-            const uint32_t n = 2 * c + 1, vst = C::slot(x, n);
-            // scores, and the scales that come with V
+            // once the P V of the tile before is done, the room for P and O are free; in a
+            // sequence's last tile, V's rows past the keys are zeroed here, so that P = 0 contributes 0
+            auto before_p = [&]() -> bool {
+                if (t > tb && !wait_all(smem_u32(&bars->pv_done[x]), (c - 1) & 1, abort_flag)) return false;
+                if (nk < kRows) {
+                    const uint32_t st = c % C::VS;
+                    if (!wait_all(smem_u32(&bars->v_full[x][st]), (c / C::VS) & 1, abort_flag)) return false;
+                    if (r >= nk) {
+                        proxy_fence();
+                        uint4 *v = reinterpret_cast<uint4 *>(smem + C::v_at(x, st) + r * 128);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
+                        proxy_fence();
+                    }
+                    __syncwarp();
+                }
+                return true;
+            };
+            // scores, and the scales
             if (!wait_all(smem_u32(&bars->s_full[x]), c & 1, abort_flag) ||
-                !wait_all(smem_u32(&bars->kv_full[vst]), C::parity(n), abort_flag)) {
+                !wait_all(smem_u32(&bars->scale_full[x][c & 1]), c >> 1 & 1, abort_flag)) {
                 ok = false;
                 break;
-            }
-            if (nk < kRows) {
-                // rows past the keys: V is zeroed so that P = 0 contributes 0 (by each group before its own P V)
-                if (r >= nk) {
-                    proxy_fence();
-                    uint4 *v = reinterpret_cast<uint4 *>(smem + C::OFF_KV + vst * kPanelBytes + r * 128);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
-                    proxy_fence();
-                }
-                __syncwarp();
             }
             if (!work) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[x]));
                 // S comes ahead of P V: not a tile ahead of the warps that write P
-                if (t > tb && !wait_all(smem_u32(&bars->pv_done[x]), (c - 1) & 1, abort_flag)) {
+                if (!before_p()) {
                     ok = false;
                     break;
                 }
@@ -1499,8 +1530,8 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_ld32(s_tm + 32 * q, s[q]);
             // k_scale and log2 of v_scale of 16 columns, a page or a part of one: in lane u those of columns 16 u ...
-            const float lane_ks = bars->scale[vst][0][(16 * (lane & 7)) >> p.shift];
-            const float lane_vs = __log2f(fminf(fmaxf(bars->scale[vst][1][(16 * (lane & 7)) >> p.shift], kLeastScale), kMostScale));
+            const float lane_ks = bars->scale[x][c & 1][0][(16 * (lane & 7)) >> p.shift];
+            const float lane_vs = __log2f(fminf(fmaxf(bars->scale[x][c & 1][1][(16 * (lane & 7)) >> p.shift], kLeastScale), kMostScale));
             auto factor = [&](int u) { return fmaxf(fq * __shfl_sync(0xffffffffu, lane_ks, u), FLT_MIN); };   // not 0: -inf stays -inf
             auto summand = [&](int u) { return __shfl_sync(0xffffffffu, lane_vs, u); };
 #pragma unroll
@@ -1531,8 +1562,7 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
             const bool need = tmax > m + kGrown || since == kRowsTiles;
             if (since == kRowsTiles) since = 0;
             ++since;
-            // O, and the room for P, are free once the P V of the tile before is done
-            if (t > tb && !wait_all(smem_u32(&bars->pv_done[x]), (c - 1) & 1, abort_flag)) {
+            if (!before_p()) {
                 ok = false;
                 break;
             }
@@ -1565,7 +1595,7 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
                 if (h < halves) {
 #pragma unroll
                     for (int q = 2 * h; q < 2 * h + 2; ++q) {
-                        uint32_t w0[8], w1[8];
+                        uint32_t w[C::NT][8];
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             const float fu = factor(2 * q + u), du = summand(2 * q + u);
@@ -1581,7 +1611,8 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
                                 for (int y = 0; y < 4; ++y) e[y] = ex2(e[y]);
                                 sum[0] = add_f2(sum[0], pack_f2(e[0], e[1]));
                                 sum[1] = add_f2(sum[1], pack_f2(e[2], e[3]));
-                                split4<true>(e, w0[4 * u + k / 4], w1[4 * u + k / 4]);
+                                if constexpr (C::BF) split4<true>(e, w[0][4 * u + k / 4], w[1][4 * u + k / 4]);
+                                else split4_wide_third(e, w[0][4 * u + k / 4], w[1][4 * u + k / 4], w[C::NT - 1][4 * u + k / 4]);
                             }
                             float a, b;
                             unpack_f2(add_f2(sum[0], sum[1]), a, b);
@@ -1591,8 +1622,9 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             uint4 *dst = reinterpret_cast<uint4 *>(prow + (((2 * q + u) ^ (r & 7)) << 4));
-                            dst[0] = make_uint4(w0[4 * u], w0[4 * u + 1], w0[4 * u + 2], w0[4 * u + 3]);
-                            dst[kPanelBytes / 16] = make_uint4(w1[4 * u], w1[4 * u + 1], w1[4 * u + 2], w1[4 * u + 3]);
+#pragma unroll
+                            for (int y = 0; y < C::NT; ++y)
+                                dst[y * (kPanelBytes / 16)] = make_uint4(w[y][4 * u], w[y][4 * u + 1], w[y][4 * u + 2], w[y][4 * u + 3]);
                         }
                     }
                     proxy_fence();
@@ -1685,7 +1717,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     using C = RowsCfg<BF>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    RowsBars *bars = reinterpret_cast<RowsBars *>(smem + C::OFF_BARS);
+    RowsBarsOf<C::VS> *bars = reinterpret_cast<RowsBarsOf<C::VS> *>(smem + C::OFF_BARS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
@@ -1693,17 +1725,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             mbar_init(smem_u32(&bars->s_full[x]), 1);
             mbar_init(smem_u32(&bars->p_full[x][0]), 4);
             mbar_init(smem_u32(&bars->p_full[x][1]), 4);
+            mbar_init(smem_u32(&bars->scale_full[x][0]), 32);  // the producer's lanes
+            mbar_init(smem_u32(&bars->scale_full[x][1]), 32);
             mbar_init(smem_u32(&bars->s_free[x]), 4);
             mbar_init(smem_u32(&bars->pv_done[x]), 1);
             mbar_init(smem_u32(&bars->drain[x]), 1);
-        }
-        for (int s = 0; s < C::NS; ++s) {
-            mbar_init(smem_u32(&bars->kv_full[s]), 33);          // the bytes, and the lanes' scales
-            mbar_init(smem_u32(&bars->kv_empty[s]), 1);          // its group's MMA warp
+            mbar_init(smem_u32(&bars->k_full[x][0]), 1);
+            mbar_init(smem_u32(&bars->k_empty[x][0]), 1);
+            for (int s = 0; s < C::VS; ++s) {
+                mbar_init(smem_u32(&bars->v_full[x][s]), 1);
+                mbar_init(smem_u32(&bars->v_empty[x][s]), 1);
+            }
         }
         for (int s = 0; s < kPagedItems; ++s) {
             mbar_init(smem_u32(&bars->item_full[s]), 1);
-            mbar_init(smem_u32(&bars->item_empty[s]), 10);       // the softmax and MMA warps
+            mbar_init(smem_u32(&bars->item_empty[s]), 11);       // the softmax, V and MMA warps
         }
         mbar_init(smem_u32(&bars->q_empty), 2);
         mbar_init(smem_u32(&bars->stat_full), 4);
@@ -1731,7 +1767,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     const uint32_t tmem = bars->tmem_base;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp < 8) rows_softmax<C>(p, smem, bars, tmem, warp, lane);
-    else if (warp == 8) rows_producer<C>(p, cur, gate, &tmK, &tmV, smem, bars, lane);
+    else if (warp == 8) rows_producer<C, false>(p, cur, gate, &tmK, smem, bars, lane);
+    else if (warp == 11) rows_producer<C, true>(p, cur, 0, &tmV, smem, bars, lane);
     else rows_mma<C>(smem, bars, tmem, warp - 9, lane);
     tc_fence_before();
     __syncthreads();
