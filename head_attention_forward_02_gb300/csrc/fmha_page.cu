@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fmha_page_plan_kernel(const P
         const int i = avail - 1 - k;
         return i < spare ? p.free_list[i] : page_given(i - spare);
     };
-    const int quads = (p.N + p.job - 1) / p.job;
+    const int quads = p.N / p.job + (p.N % p.job != 0);
     const bool wide = p.job == 4 && ((reinterpret_cast<uintptr_t>(p.slots) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
     const long long jobs = (long long)given + taken + p.B + quads;
     for (long long x = rank * blockDim.x + threadIdx.x; x < jobs; x += (long long)ranks * blockDim.x) {
@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fmha_page_plan_kernel(const P
                 bool ok = granted_to(b);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
+                    if (k >= tokens - i0 || k >= p.job) break;
                     const int i = i0 + k;
-                    if (i >= tokens || k >= p.job) break;
                     while (b + 1 < p.B && s_cu[b + 1] <= i) {       // the next sequence with tokens
                         ++b;
                         ok = granted_to(b);
@@ -212,13 +212,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fmha_page_plan_kernel(const P
                     else atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
                 }
             }
-            if (wide && i0 + 4 <= p.N) {
+            if (wide && p.N - i0 >= 4) {
                 *reinterpret_cast<int4 *>(p.slots + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
                 *reinterpret_cast<int4 *>(p.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (k < p.job && i0 + k < p.N) {
+                    if (k < p.job && k < p.N - i0) {
                         p.slots[i0 + k] = slot[k];
                         p.positions[i0 + k] = pos[k];
                     }

@@ -168,3 +168,18 @@ def test_values_outside_their_bounds_are_reported(fm, what):
         assert slots[1].item() == -1 and new_len.tolist() == [41, 20, 8]
     if what == "drop":
         assert new_len.tolist() == [41, 0, 8]
+
+
+def test_as_many_rows_as_32_bits_count(fm):
+    """The rows behind the last token, up to the largest N, are told so too."""
+    n = 2 ** 31 - 1
+    c = make([5, 0], [2, 1], 16, 3, shuffle=False)
+    a, _ = on_gpu(c, False)
+    slots, pos, cu, new_len = fm.page_plan(**a, page_size=16, max_tokens=n)
+    torch.cuda.synchronize()
+    assert fm.device_status(reset=True) == 0
+    page = c["table"][0][0] * 16
+    assert pos[:4].tolist() == [5, 6, 0, -1] and slots[:2].tolist() == [page + 5, page + 6] and cu.tolist() == [0, 2, 3]
+    assert new_len.tolist() == [7, 1]
+    for x in (slots, pos):
+        assert bool((x[3:n // 2] == -1).all()) and bool((x[n // 2:] == -1).all())
