@@ -165,6 +165,38 @@ __device__ __forceinline__ uint64_t desc_sw(uint32_t saddr, uint32_t lbo, uint32
 __device__ constexpr uint32_t paged_idesc(int n, bool mn) {
     return (1u << 4) | ((mn ? 3u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 }
+// Four k-steps of 16 with A in TMEM (16 elements: eight columns)
+template <int BS>
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n.reg .pred p, e;\n.reg .b32 a1, a2, a3;\n.reg .b64 b1, b2, b3;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
+                 "add.u32 a1, %1, 8;\nadd.u64 b1, %2, %5;\nadd.u32 a2, %1, 16;\nadd.u64 b2, b1, %5;\nadd.u32 a3, %1, 24;\nadd.u64 b3, b2, %5;\n"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, 1;\n"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, 1;\n"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, 1;\n}\n" ::"r"(d),
+                 "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(BS >> 4)
+                 : "memory");
+}
+
+// Four k-steps, whose descriptors lie `as` and `bs` apart, under one election: with
+// one a step, a step took an issuing warp 100 cycles next to the softmax warps.
+template <bool FP8, int AS, int BS>
+__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+#define FMHA_MMA4(KIND)                                                                                                   \
+    asm volatile("{\n.reg .pred p, e;\n.reg .b64 a1, a2, a3, b1, b2, b3;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n" \
+                 "add.u64 a1, %1, %5;\nadd.u64 b1, %2, %6;\nadd.u64 a2, a1, %5;\nadd.u64 b2, b1, %6;\n"                  \
+                 "add.u64 a3, a2, %5;\nadd.u64 b3, b2, %6;\n"                                                             \
+                 "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], %1, %2, %3, p;\n"                                       \
+                 "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a1, b1, %3, 1;\n"                                       \
+                 "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a2, b2, %3, 1;\n"                                       \
+                 "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a3, b3, %3, 1;\n}\n" ::"r"(d),                         \
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(AS >> 4), "n"(BS >> 4)                                          \
+                 : "memory")
+    if constexpr (FP8) FMHA_MMA4("f8f6f4");
+    else FMHA_MMA4("f16");
+#undef FMHA_MMA4
+}
+
 __device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
     uint64_t d;
     asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -244,19 +276,6 @@ __device__ __forceinline__ void split4_third(const float (&e)[4], uint32_t &hi, 
         : "r"(p), "r"(q), "r"(0x4c004c00u));                 // 16, 16
 }
 
-// As split4<true>, with a third term, in e5m2: p = hi + mid + low.
-__device__ __forceinline__ void split4_wide_third(const float (&e)[4], uint32_t &hi, uint32_t &mid, uint32_t &low) {
-    const uint32_t p = pack2<false>(e[0], e[1]), q = pack2<false>(e[2], e[3]);
-    asm("{\n.reg .b16 a, b;\n.reg .b32 x, y, u, v;\n"
-        "cvt.rn.satfinite.e4m3x2.f16x2 a, %3;\ncvt.rn.satfinite.e4m3x2.f16x2 b, %4;\nmov.b32 %0, {a, b};\n"
-        "cvt.rn.f16x2.e4m3x2 x, a;\ncvt.rn.f16x2.e4m3x2 y, b;\nsub.rn.f16x2 x, %3, x;\nsub.rn.f16x2 y, %4, y;\n"
-        "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\ncvt.rn.satfinite.e4m3x2.f16x2 b, y;\nmov.b32 %1, {a, b};\n"
-        "cvt.rn.f16x2.e4m3x2 u, a;\ncvt.rn.f16x2.e4m3x2 v, b;\nsub.rn.f16x2 x, x, u;\nsub.rn.f16x2 y, y, v;\n"
-        "cvt.rn.satfinite.e5m2x2.f16x2 a, x;\ncvt.rn.satfinite.e5m2x2.f16x2 b, y;\nmov.b32 %2, {a, b};\n}\n"
-        : "=&r"(hi), "=&r"(mid), "=&r"(low)
-        : "r"(p), "r"(q));
-}
-
 // Bounded waits as in fmha_cache.cuh, but with a hint that lets the hardware
 // suspend the warp for up to 20 us: most of a CTA's warps wait most of the time,
 // and polling took as many issue slots as the softmax.
@@ -315,28 +334,17 @@ __device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&r)[N]) 
 }
 
 // Four weights as two terms each (first weight in the low byte), by way of f16,
-// whose 11 bits hold a rest exactly: p = hi + mid / 16 in e4m3, or, WIDE, hi + mid.
-// In one piece of PTX, since a 16-bit code that passes through
+// whose 11 bits hold a rest exactly: p = hi + mid / 16 in e4m3.  In one piece of PTX, since a 16-bit code that passes through
 // C++ costs an instruction to widen it.
-template <bool WIDE>
 __device__ __forceinline__ void split4(const float (&e)[4], uint32_t &hi, uint32_t &mid) {
     const uint32_t p = pack2<false>(e[0], e[1]), q = pack2<false>(e[2], e[3]);
-    if constexpr (WIDE) {
-        asm("{\n.reg .b16 a, b;\n.reg .b32 x, y;\n"
-            "cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\ncvt.rn.satfinite.e4m3x2.f16x2 b, %3;\nmov.b32 %0, {a, b};\n"
-            "cvt.rn.f16x2.e4m3x2 x, a;\ncvt.rn.f16x2.e4m3x2 y, b;\nsub.rn.f16x2 x, %2, x;\nsub.rn.f16x2 y, %3, y;\n"
-            "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\ncvt.rn.satfinite.e4m3x2.f16x2 b, y;\nmov.b32 %1, {a, b};\n}\n"
-            : "=r"(hi), "=r"(mid)
-            : "r"(p), "r"(q));
-    } else {
-        asm("{\n.reg .b16 a, b;\n.reg .b32 x, y;\n"
-            "cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\ncvt.rn.satfinite.e4m3x2.f16x2 b, %3;\nmov.b32 %0, {a, b};\n"
-            "cvt.rn.f16x2.e4m3x2 x, a;\ncvt.rn.f16x2.e4m3x2 y, b;\nsub.rn.f16x2 x, %2, x;\nsub.rn.f16x2 y, %3, y;\n"
-            "mul.rn.f16x2 x, x, %4;\nmul.rn.f16x2 y, y, %4;\n"
-            "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\ncvt.rn.satfinite.e4m3x2.f16x2 b, y;\nmov.b32 %1, {a, b};\n}\n"
-            : "=r"(hi), "=r"(mid)
-            : "r"(p), "r"(q), "r"(0x4c004c00u));             // 16, 16
-    }
+    asm("{\n.reg .b16 a, b;\n.reg .b32 x, y;\n"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\ncvt.rn.satfinite.e4m3x2.f16x2 b, %3;\nmov.b32 %0, {a, b};\n"
+        "cvt.rn.f16x2.e4m3x2 x, a;\ncvt.rn.f16x2.e4m3x2 y, b;\nsub.rn.f16x2 x, %2, x;\nsub.rn.f16x2 y, %3, y;\n"
+        "mul.rn.f16x2 x, x, %4;\nmul.rn.f16x2 y, y, %4;\n"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\ncvt.rn.satfinite.e4m3x2.f16x2 b, y;\nmov.b32 %1, {a, b};\n}\n"
+        : "=r"(hi), "=r"(mid)
+        : "r"(p), "r"(q), "r"(0x4c004c00u));             // 16, 16
 }
 
 // ---------------------------------------------------------------------------
@@ -693,15 +701,10 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
         tc_fence_after();
         const uint64_t v = v0 + ((st * C::STAGE) >> 4), pt = p0 + ((b * C::P_BYTES) >> 4);
         const uint32_t o_tm = tmem + 2 * C::COLS;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)   // 32 keys
-            mma_ss<true>(o_tm, v + ((kk * 32 * 128) >> 4), pt + ((kk * 32 * C::P_ROW) >> 4), paged_idesc(32, true),
-                         kk > 0 || !begins ? 1u : 0u);
+        // 32 keys a step
+        mma4<true, 32 * 128, 32 * C::P_ROW>(o_tm, v, pt, paged_idesc(32, true), begins ? 0u : 1u);
         if constexpr (C::THIRD && !C::INLINE3)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                mma_ss<true>(o_tm + C::COLS, v + ((kk * 32 * 128) >> 4), pt + ((C::P_TILE + kk * 32 * C::P_ROW) >> 4),
-                             paged_idesc(16, true), kk > 0 || !begins ? 1u : 0u);
+            mma4<true, 32 * 128, 32 * C::P_ROW>(o_tm + C::COLS, v, pt + (C::P_TILE >> 4), paged_idesc(16, true), begins ? 0u : 1u);
         tc_commit(smem_u32(&bars->pv_done[w][b]));
         tc_commit(smem_u32(&bars->kv_empty[st]));
         return true;
@@ -736,14 +739,8 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
             tc_fence_after();
             const uint64_t k = k0 + ((st * C::STAGE) >> 4);
             const uint32_t s_tm = tmem + b * C::COLS;
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)   // 32 dims: 32 bytes of a row
-                mma_ss<true>(s_tm, k + ((kk * 32) >> 4), q + ((kk * 32) >> 4), paged_idesc(32, false), kk > 0 ? 1u : 0u);
-            if constexpr (!C::BF) {
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_ss<true>(s_tm + 16, k + ((kk * 32) >> 4), q3 + ((kk * 32) >> 4), paged_idesc(16, false), 1u);
-            }
+            mma4<true, 32, 32>(s_tm, k, q, paged_idesc(32, false), 0u);      // 32 dims a step: 32 bytes of a row
+            if constexpr (!C::BF) mma4<true, 32, 32>(s_tm + 16, k, q3, paged_idesc(16, false), 1u);
             tc_commit(smem_u32(&bars->s_full[w][b]));
             if (t + kStep >= it.t1) tc_commit(smem_u32(&bars->q_empty[slot]));
             if (t > tb && !issue_pv(m - 1, st_before, t - kStep == tb)) {
@@ -967,7 +964,7 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                 l[k / 2] = fma_f2(pack_f2(v[0], v[1]), isv2, l[k / 2]);
                 l[k / 2 + 1] = fma_f2(pack_f2(v[2], v[3]), isv2, l[k / 2 + 1]);
                 if constexpr (C::THIRD) split4_third(v, hi[k / 4], mid[k / 4], low[k / 4]);
-                else split4<false>(v, hi[k / 4], mid[k / 4]);
+                else split4(v, hi[k / 4], mid[k / 4]);
             }
             uint8_t *ph = prow + (swz << 4), *pm = prow + ((1 ^ swz) << 4);
             if constexpr (NR == 16) {
@@ -1208,30 +1205,32 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 // were 3% slower; P over S in TMEM, so that S waits for P V, 8%.
 // ---------------------------------------------------------------------------
 
-constexpr int kRowsBars = 4096;          // barrier block
+constexpr int kRowsBars = 3072;          // barrier block
 constexpr int kRowsTiles = 16;           // tiles that a reference serves at most
+constexpr float kRowsGrown = 15.f;       // as kGrown: f16 ends at 2^16
 constexpr float kRowsBias = 7.f;         // as kBias: higher, for the second term's sake
-constexpr int kRowsThreads = 384;        // two softmax groups of four warps, producers of K and V, an MMA issuer a group
+constexpr int kRowsConv = 8, kRowsK = 12, kRowsMma = 13, kRowsV = 15;   // first warps of the roles behind the softmax's
+constexpr int kRowsThreads = 512;        // two softmax groups and the converters, of four warps; K's and V's producers, an MMA issuer a group
 
 template <bool BF_>
 struct RowsCfg {
     static constexpr bool BF = BF_;
-    static constexpr int NT = BF ? 2 : 3;                     // terms of q, and of P
-    static constexpr int OFF_P = NT * kPanelBytes;            // q's terms, then those of each group's P
-    static constexpr int OFF_KV = OFF_P + 2 * NT * kPanelBytes;
-    static constexpr int VS = BF ? 2 : 1;                     // slots of a group for V (K: one, free once its S is there)
-    static constexpr int OFF_BARS = OFF_KV + 2 * (1 + VS) * kPanelBytes;
-    static constexpr int SMEM_BYTES = OFF_BARS + kRowsBars + 1024;
+    static constexpr int NT = BF ? 2 : 3;                     // terms of q
+    static constexpr int VS = BF ? 2 : 1;                     // tiles of V as codes
+    static constexpr int OFF_VF = NT * kPanelBytes;           // after q's terms, by group: V in f16,
+    static constexpr int OFF_K = OFF_VF + 4 * kPanelBytes;    // and K (one tile, free once its S is there)
+    static constexpr int OFF_V = OFF_K + 2 * kPanelBytes;     // V as it comes, for both
+    static constexpr int OFF_BARS = OFF_V + VS * kPanelBytes;
+    static constexpr int SMEM_BYTES = OFF_BARS + kRowsBars;   // the array is 1 KB aligned
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-    static __device__ __forceinline__ int k_at(int x) { return OFF_KV + x * (1 + VS) * kPanelBytes; }
-    static __device__ __forceinline__ int v_at(int x, uint32_t st) { return k_at(x) + (1 + st) * kPanelBytes; }
 };
 
 template <int VS>
 struct RowsBarsOf {
-    uint64_t q_full[2], q_empty, drain[2], s_full[2], s_free[2], p_full[2][2], pv_done[2];   // by group; p_full by half
+    uint64_t q_full[2], q_empty, drain[2];                    // by group,
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // and half of a tile
     uint64_t stat_full, epi_done;
-    uint64_t k_full[2][1], k_empty[2][1], v_full[2][VS], v_empty[2][VS], scale_full[2][2];
+    uint64_t k_full[2], k_empty[2], v_full[VS], v_empty[VS], vf_full[2], scale_full[2][2];
     uint64_t item_full[kPagedItems], item_empty[kPagedItems];
     PagedItem item[kPagedItems];
     uint32_t tmem_base;
@@ -1259,10 +1258,6 @@ template <class C, bool V>
 __device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, const CUtensorMap *tm, uint8_t *smem, RowsBarsOf<C::VS> *bars,
                               int lane) {
     volatile int *abort_flag = &bars->abort;
-    constexpr int SLOTS = V ? C::VS : 1;
-    uint64_t (*full)[SLOTS], (*empty)[SLOTS];
-    if constexpr (V) full = bars->v_full, empty = bars->v_empty;
-    else full = bars->k_full, empty = bars->k_empty;
     bool ok = true;
     if (gate) ok = __all_sync(0xffffffffu, lane > 0 || test_gate_open(abort_flag));
     uint32_t fill[2] = {0, 0}, qn = 0;
@@ -1298,18 +1293,17 @@ __device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, 
             // a page outside the cache: a coordinate outside it, which reads zeros
             const int head = id >= 0 ? id * p.H_k + it.g : p.n_pages * p.H_k;
             const int x = (t - it.t0) & 1;
-            const uint32_t n = x ? fill[1]++ : fill[0]++, st = n % SLOTS;
-            if (n >= SLOTS && !wait_all(smem_u32(&empty[x][st]), (n / SLOTS) & 1 ^ 1, abort_flag)) {
-                if (x) --fill[1];
-                else --fill[0];
+            // V's tiles share a ring; K's have a slot a group
+            const uint32_t n = V || x == 0 ? fill[0] : fill[1], st = V ? n % C::VS : 0, lap = V ? n / C::VS : n;
+            const uint32_t full = smem_u32(V ? &bars->v_full[st] : &bars->k_full[x]);
+            if (lap > 0 && !wait_all(smem_u32(V ? &bars->v_empty[st] : &bars->k_empty[x]), lap & 1 ^ 1, abort_flag)) {
                 ok = false;
                 break;
             }
-            const uint32_t fb = smem_u32(&full[x][st]);
-            if (lane == 0) mbar_expect_tx(fb, here * (P << 7));
+            if (lane == 0) mbar_expect_tx(full, here * (P << 7));
             __syncwarp();
             if (lane < here) {
-                tma_load_3d(smem_u32(smem + (V ? C::v_at(x, st) : C::k_at(x))) + lane * (P << 7), tm, fb, 0, 0, head);
+                tma_load_3d(smem_u32(smem + (V ? C::OFF_V + st * kPanelBytes : C::OFF_K + x * kPanelBytes)) + lane * (P << 7), tm, full, 0, 0, head);
                 if constexpr (!V) {
                     // into the place of the tile two before in this group, which was read
                     // before S of the one before, and so before this slot was free
@@ -1322,6 +1316,8 @@ __device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, 
             }
             if constexpr (!V)
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&bars->scale_full[x][n & 1])) : "memory");
+            if (V || x == 0) ++fill[0];
+            else ++fill[1];
             id = ahead;
             if constexpr (!V)
                 if (t == it.t0) {
@@ -1337,15 +1333,70 @@ __device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, 
     }
     // no copy may be in flight when the block ends, nor a product that reads one
     ok = *abort_flag == 0;
+    constexpr uint32_t kSlots = V ? C::VS : 1;
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-        for (uint32_t n = fill[x] > SLOTS ? fill[x] - SLOTS : 0; n < fill[x]; ++n) {
-            const uint32_t st = n % SLOTS;
-            if (ok) ok = wait_all(smem_u32(&empty[x][st]), (n / SLOTS) & 1, abort_flag);
-            if (!ok) mbar_wait_drain(smem_u32(&full[x][st]), (n / SLOTS) & 1);
+    for (int x = 0; x < (V ? 1 : 2); ++x)
+        for (uint32_t n = fill[x] > kSlots ? fill[x] - kSlots : 0; n < fill[x]; ++n) {
+            const uint32_t st = n % kSlots, lap = n / kSlots;
+            if (ok) ok = wait_all(smem_u32(V ? &bars->v_empty[st] : &bars->k_empty[x]), lap & 1, abort_flag);
+            if (!ok) mbar_wait_drain(smem_u32(V ? &bars->v_full[st] : &bars->k_full[x]), lap & 1);
             if (!V) mbar_wait_drain(smem_u32(&bars->scale_full[x][n & 1]), n >> 1 & 1);
         }
     if (!V && ok && qn > 0) wait_all(smem_u32(&bars->q_empty), (qn - 1) & 1, abort_flag);
+}
+
+// Converter warp w: V's codes to f16, a quarter of each tile, from rows of 128
+// bytes to two panels of 64 dims; in a sequence's last tile the rows past the keys
+// are zeros, so that P = 0 contributes 0.
+template <class C>
+__device__ void rows_convert(uint8_t *smem, RowsBarsOf<C::VS> *bars, int w, int lane) {
+    volatile int *abort_flag = &bars->abort;
+    uint32_t n = 0, done[2] = {0, 0};    // tiles, and those of either group
+    PagedItem it;
+    for (uint32_t i = 0; rows_take(bars, i, it, abort_flag, lane); ++i) {
+        bool ok = true;
+        for (int t = it.t0; t < it.t1; ++t, ++n) {
+            const int x = (t - it.t0) & 1, nk = it.L - t * kRows;
+            const uint32_t st = n % C::VS, c = x ? done[1]++ : done[0]++;
+            // the codes, and room: P V of the group's tile before is done
+            ok = wait_all(smem_u32(&bars->v_full[st]), (n / C::VS) & 1, abort_flag) &&
+                 (c == 0 || wait_all(smem_u32(&bars->pv_done[x][1]), (c - 1) & 1, abort_flag));
+            if (!ok) break;
+            const int ch = lane & 7, up = ch >> 2;       // 16 dims of a row; of which panel
+            const uint8_t *src = smem + C::OFF_V + st * kPanelBytes;
+            uint8_t *dst = smem + C::OFF_VF + (2 * x + up) * kPanelBytes;
+            uint4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int j = 32 * w + 4 * k + (lane >> 3);
+                v[k] = *reinterpret_cast<const uint4 *>(src + j * 128 + ((ch ^ (j & 7)) << 4));
+                if (j >= nk) v[k] = make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int j = 32 * w + 4 * k + (lane >> 3), f = 2 * (ch & 3);
+                // eight dims at a time; the panels' lanes begin with different ones, so that their banks differ
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    const bool high = (o ^ up) != 0;
+                    const uint32_t a = high ? v[k].z : v[k].x, b = high ? v[k].w : v[k].y;
+                    uint4 y;
+                    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+                        : "=r"(y.x), "=r"(y.y) : "r"(a));
+                    asm("{\n.reg .b16 a, b;\nmov.b32 {a, b}, %2;\ncvt.rn.f16x2.e4m3x2 %0, a;\ncvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+                        : "=r"(y.z), "=r"(y.w) : "r"(b));
+                    *reinterpret_cast<uint4 *>(dst + j * 128 + (((f + high) ^ (j & 7)) << 4)) = y;
+                }
+            }
+            proxy_fence();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&bars->v_empty[st]));
+                mbar_arrive(smem_u32(&bars->vf_full[x]));
+            }
+        }
+        if (!ok) break;
+    }
 }
 
 // MMA issuer of group x.  P lies in shared memory, apart from S, so that S of the
@@ -1357,12 +1408,10 @@ __device__ void rows_mma(uint8_t *smem, RowsBarsOf<C::VS> *bars, uint32_t tmem_a
     volatile int *abort_flag = &bars->abort;
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
     const uint32_t s_tm = tmem + x * kRows, o_tm = tmem + 2 * kRows + x * kD;
-    constexpr uint32_t kIdS = mma_idesc(0u, kRows, false), kIdP = mma_idesc(0u, kD, true);
-    constexpr uint32_t kIdP2 = kIdP | (1u << 7);             // A (the weights' third term) e5m2
+    constexpr uint32_t kIdS = mma_idesc(0u, kRows / 2, false), kIdP = mma_idesc(0u, kD, true);
     const uint64_t q = smem_desc(smem_u32(smem), 16, 1024);
-    const uint64_t k = smem_desc(smem_u32(smem + C::k_at(x)), 16, 1024);
-    const uint64_t v0 = smem_desc(smem_u32(smem + C::v_at(x, 0)), kPanelBytes, 1024);
-    const uint64_t p0 = smem_desc(smem_u32(smem + C::OFF_P + x * C::NT * kPanelBytes), 16, 1024);
+    const uint64_t k = smem_desc(smem_u32(smem + C::OFF_K + x * kPanelBytes), 16, 1024);
+    const uint64_t v = smem_desc(smem_u32(smem + C::OFF_VF + 2 * x * kPanelBytes), kPanelBytes, 1024);   // MN-major: LBO = panel stride
     uint32_t m = 0;                      // tiles of this group
     bool ok = true;
     PagedItem it;
@@ -1373,50 +1422,38 @@ __device__ void rows_mma(uint8_t *smem, RowsBarsOf<C::VS> *bars, uint32_t tmem_a
         }
         const int tb = it.t0 + x;
         if (tb >= it.t1) tc_commit(smem_u32(&bars->q_empty));   // an item of one tile is group 0's alone
-        for (int t = tb; ok && tb < it.t1 && t < it.t1 + 2; t += 2) {
-            if (t < it.t1) {             // S of this tile
-                if (!wait_all(smem_u32(&bars->k_full[x][0]), m & 1, abort_flag) ||
-                    (m > 0 && !wait_all(smem_u32(&bars->s_free[x]), (m - 1) & 1, abort_flag))) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
+        // S of half h of tile m, over P of that of tile m - 1; P V of that
+        auto scores = [&](int h) -> bool {
+            if (h == 0 && !wait_all(smem_u32(&bars->k_full[x]), m & 1, abort_flag)) return false;
+            tc_fence_after();
 #pragma unroll
-                for (int term = 0; term < C::NT; ++term)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ss<true>(s_tm, q + ((term * kPanelBytes + kk * 32) >> 4), k + ((kk * 32) >> 4), kIdS,
-                                     term > 0 || kk > 0 ? 1u : 0u);
-                tc_commit(smem_u32(&bars->s_full[x]));
-                tc_commit(smem_u32(&bars->k_empty[x][0]));
+            for (int term = 0; term < C::NT; ++term)     // 32 dims a step: 32 bytes of a row
+                mma4<true, 32, 32>(s_tm + 64 * h, q + ((term * kPanelBytes) >> 4), k + ((h * 64 * 128) >> 4), kIdS, term > 0 ? 1u : 0u);
+            tc_commit(smem_u32(&bars->s_full[x][h]));
+            return true;
+        };
+        auto values = [&](int h, bool first) -> bool {
+            if ((h == 0 && !wait_all(smem_u32(&bars->vf_full[x]), (m - 1) & 1, abort_flag)) ||
+                !wait_all(smem_u32(&bars->p_full[x][h]), (m - 1) & 1, abort_flag))
+                return false;
+            tc_fence_after();
+            // 16 keys a step: 8 columns of P's, 16 rows of V
+            mma4_ts<16 * 128>(o_tm, s_tm + 64 * h, v + ((h * 64 * 128) >> 4), kIdP, first ? 0u : 1u);
+            tc_commit(smem_u32(&bars->pv_done[x][h]));
+            return true;
+        };
+        for (int t = tb; ok && t < it.t1 + 2 && tb < it.t1; t += 2) {
+            const bool more = t < it.t1, before = t > tb;    // a tile here; one before it
+            for (int h = 0; ok && h < 2; ++h) {
+                // in this order, which the tensor cores keep: P is where the next S goes
+                ok = !before || values(h, h == 0 && t == tb + 2);
+                ok = ok && (!more || scores(h));
+            }
+            if (!ok) break;
+            if (more) {
+                tc_commit(smem_u32(&bars->k_empty[x]));
                 if (t + 2 >= it.t1) tc_commit(smem_u32(&bars->q_empty));
                 ++m;
-            }
-            if (t > tb) {             // P V of the tile before, which is tile m - 1, or m - 2 if S of this one was issued
-                const uint32_t mm = m - (t < it.t1 ? 2 : 1), st = mm % C::VS;
-                if (!wait_all(smem_u32(&bars->v_full[x][st]), (mm / C::VS) & 1, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                const int halves = it.L - (t - 2) * kRows > kRows / 2 ? 2 : 1;
-                const uint64_t v = v0 + ((st * kPanelBytes) >> 4);
-                for (int h = 0; h < halves; ++h) {
-                    if (!wait_all(smem_u32(&bars->p_full[x][h]), mm & 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-#pragma unroll
-                    for (int term = 0; term < C::NT; ++term)
-#pragma unroll
-                        for (int kk = 0; kk < 2; ++kk)       // 32 keys: 32 bytes of P's rows, 32 rows of V
-                            mma_ss<true>(o_tm, p0 + ((term * kPanelBytes + (h * 2 + kk) * 32) >> 4),
-                                         v + (((h * 2 + kk) * 32 * 128) >> 4), term == 2 ? kIdP2 : kIdP,
-                                         t - 2 > tb || h > 0 || term > 0 || kk > 0 ? 1u : 0u);
-                }
-                if (!ok) break;
-                tc_commit(smem_u32(&bars->pv_done[x]));
-                tc_commit(smem_u32(&bars->v_empty[x][st]));
             }
         }
     }
@@ -1459,14 +1496,13 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBarsOf<C::
     const int x = warp >> 2, r = (warp & 3) * 32 + lane;   // group, row of the unit
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_tm = lane_base + x * kRows, o_tm = lane_base + 2 * kRows + x * kD;
-    uint8_t *prow = smem + C::OFF_P + x * C::NT * kPanelBytes + r * 128;
     uint32_t c = 0;                                     // tiles of this group
     int parts = 0;                                      // bit s: slot s of this CTA holds a partial
-    PagedItem it;
-    for (uint32_t i = 0; rows_take(bars, i, it, abort_flag, lane); ++i) {
-        const int tok = r / p.G;
+    for (uint32_t i = 0;; ++i) {
+        // read where it lies, and given back at its end: registers are scarce
+        const PagedItem &it = bars->item[i % kPagedItems];
+        if (!wait_all(smem_u32(&bars->item_full[i % kPagedItems]), (i / kPagedItems) & 1, abort_flag) || it.rows == 0) break;
         const bool row_ok = r < it.rows;
-        const int at = row_ok ? (it.row0 + tok) * p.H + it.h0 + r - tok * p.G : -1;
         // the unit's rows of q, 16 a warp, for both groups; the S MMAs of the item before are done
         if (i > 0 && !wait_all(smem_u32(&bars->q_empty), (i - 1) & 1, abort_flag)) break;
         const int k = warp * 16 + (lane & 15), tk = k / p.G;
@@ -1477,176 +1513,139 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBarsOf<C::
         if (lane < 2) mbar_arrive(smem_u32(&bars->q_full[lane]));
         if (!wait_all(smem_u32(&bars->q_full[x]), i & 1, abort_flag)) break;
         const bool work = __any_sync(0xffffffffu, row_ok);   // else the warp only keeps step
-        const int lim = it.base + it.tok0 + tok;        // last key it sees
+        const int lim = it.base + it.tok0 + r / p.G;    // last key it sees
+        const int t1 = it.t1, L = it.L;
         const float fq = p.c * bars->qscale[r];
         float m = -INFINITY, M = -INFINITY;             // reference (log2 units) of P and O, and the highest so far
         float l = 0.f;                                  // row sum
         int since = kRowsTiles;
         bool ok = true;
         const int tb = it.t0 + x;
-        for (int t = tb; t < it.t1; t += 2, ++c) {
-            const int nk = it.L - t * kRows, halves = nk > kRows / 2 ? 2 : 1;
-            // once the P V of the tile before is done, the room for P and O are free; in a
-            // sequence's last tile, V's rows past the keys are zeroed here, so that P = 0 contributes 0
-            auto before_p = [&]() -> bool {
-                if (t > tb && !wait_all(smem_u32(&bars->pv_done[x]), (c - 1) & 1, abort_flag)) return false;
-                if (nk < kRows) {
-                    const uint32_t st = c % C::VS;
-                    if (!wait_all(smem_u32(&bars->v_full[x][st]), (c / C::VS) & 1, abort_flag)) return false;
-                    if (r >= nk) {
-                        proxy_fence();
-                        uint4 *v = reinterpret_cast<uint4 *>(smem + C::v_at(x, st) + r * 128);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = make_uint4(0u, 0u, 0u, 0u);
-                        proxy_fence();
-                    }
-                    __syncwarp();
-                }
-                return true;
-            };
-            // scores, and the scales
-            if (!wait_all(smem_u32(&bars->s_full[x]), c & 1, abort_flag) ||
-                !wait_all(smem_u32(&bars->scale_full[x][c & 1]), c >> 1 & 1, abort_flag)) {
+        // a warp without rows keeps step with those that have some
+        for (int t = tb; !work && ok && t < t1; t += 2, ++c)
+            for (int h = 0; ok && h < 2; ++h) {
+                ok = wait_all(smem_u32(&bars->s_full[x][h]), c & 1, abort_flag) &&
+                     (c == 0 || wait_all(smem_u32(&bars->pv_done[x][h]), (c - 1) & 1, abort_flag));
+                if (ok && lane == 0) mbar_arrive(smem_u32(&bars->p_full[x][h]));
+            }
+        for (int t = tb; work && t < t1; t += 2, ++c) {
+            const int cnt = imin(L, lim + 1) - t * kRows;   // visible keys
+            if (!wait_all(smem_u32(&bars->scale_full[x][c & 1]), c >> 1 & 1, abort_flag)) {
                 ok = false;
                 break;
             }
-            if (!work) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[x]));
-                // S comes ahead of P V: not a tile ahead of the warps that write P
-                if (!before_p()) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&bars->p_full[x][0]));
-                    mbar_arrive(smem_u32(&bars->p_full[x][1]));
-                }
-                continue;
-            }
-            tc_fence_after();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32(s_tm + 32 * q, s[q]);
             // k_scale and log2 of v_scale of 16 columns, a page or a part of one: in lane u those of columns 16 u ...
             const float lane_ks = bars->scale[x][c & 1][0][(16 * (lane & 7)) >> p.shift];
             const float lane_vs = __log2f(fminf(fmaxf(bars->scale[x][c & 1][1][(16 * (lane & 7)) >> p.shift], kLeastScale), kMostScale));
             auto factor = [&](int u) { return fmaxf(fq * __shfl_sync(0xffffffffu, lane_ks, u), FLT_MIN); };   // not 0: -inf stays -inf
             auto summand = [&](int u) { return __shfl_sync(0xffffffffu, lane_vs, u); };
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_wait_ld(s[q]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->s_free[x]));
-            const int cnt = imin(nk, lim - t * kRows + 1);   // visible keys
-            if (__any_sync(0xffffffffu, cnt < kRows)) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (32 * q + k >= cnt) s[q][k] = 0xff800000u;
-            }
-            float tmax = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const uint32_t *su = s[u >> 1] + 16 * (u & 1);
-                float a = -INFINITY, b = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < 16; k += 4) {
-                    a = max3(a, __uint_as_float(su[k]), __uint_as_float(su[k + 1]));
-                    b = max3(b, __uint_as_float(su[k + 2]), __uint_as_float(su[k + 3]));
-                }
-                tmax = fmaxf(tmax, fmaf(fmaxf(a, b), factor(u), summand(u)));
-            }
-            const bool need = tmax > m + kGrown || since == kRowsTiles;
             if (since == kRowsTiles) since = 0;
             ++since;
-            if (!before_p()) {
-                ok = false;
-                break;
-            }
-            if (__any_sync(0xffffffffu, need)) {
-                float alpha = 1.f;
-                if (need) {
-                    const float own = tmax - kRowsBias, ref = fmaxf(fmaxf(own, fminf(M, own + kAbove)), M - kBelow);
-                    alpha = m == -INFINITY ? 0.f : ex2(m - ref);
-                    m = ref;
-                    M = fmaxf(M, ref);
-                    l *= alpha;
-                }
-                if (t > tb) {
-                    tc_fence_after();
 #pragma unroll 1
-                    for (int q = 0; q < 8; ++q) {
-                        uint32_t o[16];
-                        tmem_ld16(o_tm + 16 * q, o);
-                        tmem_wait_ld16(o);
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                        tmem_st16(o_tm + 16 * q, o);
-                    }
-                }
-            }
-            // a row that has seen no key yet: every score is -inf, P = 0
-            const float mr = m == -INFINITY ? 0.f : m;
-#pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (h < halves) {
-#pragma unroll
-                    for (int q = 2 * h; q < 2 * h + 2; ++q) {
-                        uint32_t w[C::NT][8];
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const float fu = factor(2 * q + u), du = summand(2 * q + u);
-                            const uint64_t f2 = pack_f2(fu, fu), d2 = pack_f2(du - mr, du - mr);
-                            uint64_t sum[2] = {0, 0};
-#pragma unroll
-                            for (int k = 0; k < 16; k += 4) {
-                                const uint32_t *sk = s[q] + 16 * u + k;
-                                float e[4];
-                                unpack_f2(fma_f2(pack_f2(__uint_as_float(sk[0]), __uint_as_float(sk[1])), f2, d2), e[0], e[1]);
-                                unpack_f2(fma_f2(pack_f2(__uint_as_float(sk[2]), __uint_as_float(sk[3])), f2, d2), e[2], e[3]);
-#pragma unroll
-                                for (int y = 0; y < 4; ++y) e[y] = ex2(e[y]);
-                                sum[0] = add_f2(sum[0], pack_f2(e[0], e[1]));
-                                sum[1] = add_f2(sum[1], pack_f2(e[2], e[3]));
-                                if constexpr (C::BF) split4<true>(e, w[0][4 * u + k / 4], w[1][4 * u + k / 4]);
-                                else split4_wide_third(e, w[0][4 * u + k / 4], w[1][4 * u + k / 4], w[C::NT - 1][4 * u + k / 4]);
-                            }
-                            float a, b;
-                            unpack_f2(add_f2(sum[0], sum[1]), a, b);
-                            l = fmaf(a + b, ex2(-du), l);
-                        }
-                        // 16-byte chunks 2 q and 2 q + 1 of the row, swizzled
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(prow + (((2 * q + u) ^ (r & 7)) << 4));
-#pragma unroll
-                            for (int y = 0; y < C::NT; ++y)
-                                dst[y * (kPanelBytes / 16)] = make_uint4(w[y][4 * u], w[y][4 * u + 1], w[y][4 * u + 2], w[y][4 * u + 3]);
-                        }
-                    }
-                    proxy_fence();
-                    if (h == 0) {        // O may have been stored to above
-                        tmem_wait_st();
-                        tc_fence_before();
-                    }
-                    __syncwarp();
+                // P V of the half's tile before, done before S, is waited for as well, so that
+                // no phase of its barrier goes unseen
+                if (!wait_all(smem_u32(&bars->s_full[x][h]), c & 1, abort_flag) ||
+                    (c > 0 && !wait_all(smem_u32(&bars->pv_done[x][h]), (c - 1) & 1, abort_flag))) {
+                    ok = false;
+                    break;
                 }
+                uint32_t s[2][32];
+                tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) tmem_ld32(s_tm + 64 * h + 32 * q, s[q]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) tmem_wait_ld(s[q]);
+                if (__any_sync(0xffffffffu, cnt < 64 * h + 64)) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (32 * q + k >= cnt - 64 * h) s[q][k] = 0xff800000u;
+                }
+                float tmax = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t *su = s[u >> 1] + 16 * (u & 1);
+                    float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 16; k += 4) {
+                        a = max3(a, __uint_as_float(su[k]), __uint_as_float(su[k + 1]));
+                        b = max3(b, __uint_as_float(su[k + 2]), __uint_as_float(su[k + 3]));
+                    }
+                    tmax = fmaxf(tmax, fmaf(fmaxf(a, b), factor(4 * h + u), summand(4 * h + u)));
+                }
+                const bool need = tmax > m + kRowsGrown || (since == 1 && h == 0);
+                if (__any_sync(0xffffffffu, need)) {
+                    float alpha = 1.f;
+                    if (need) {
+                        const float own = tmax - kRowsBias, ref = fmaxf(fmaxf(own, fminf(M, own + kAbove)), M - kBelow);
+                        alpha = m == -INFINITY ? 0.f : ex2(m - ref);
+                        m = ref;
+                        M = fmaxf(M, ref);
+                        l *= alpha;
+                    }
+                    if (t > tb || h > 0) {   // O: once the P V of the half before is done
+                        if (!wait_all(smem_u32(&bars->pv_done[x][h ^ 1]), (h ? c : c - 1) & 1, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int q = 0; q < 8; ++q) {
+                            uint32_t o[16];
+                            tmem_ld16(o_tm + 16 * q, o);
+                            tmem_wait_ld16(o);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                            tmem_st16(o_tm + 16 * q, o);
+                        }
+                    }
+                }
+                // a row that has seen no key yet: every score is -inf, P = 0
+                const float mr = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float fu = factor(4 * h + u), du = summand(4 * h + u);
+                    const uint64_t f2 = pack_f2(fu, fu), d2 = pack_f2(du - mr, du - mr);
+                    const uint32_t *su = s[u >> 1] + 16 * (u & 1);
+                    uint64_t sum[2] = {0, 0};
+                    uint32_t w[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        float a, b;
+                        unpack_f2(fma_f2(pack_f2(__uint_as_float(su[2 * k]), __uint_as_float(su[2 * k + 1])), f2, d2), a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        sum[k & 1] = add_f2(sum[k & 1], pack_f2(a, b));
+                        w[k] = pack2<false>(a, b);
+                    }
+                    float a, b;
+                    unpack_f2(add_f2(sum[0], sum[1]), a, b);
+                    l = fmaf(a + b, ex2(-du), l);
+                    tmem_st8(s_tm + 64 * h + 8 * u, w);      // over the scores: 16 keys, eight columns
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[x][h]));
             }
+            if (!ok) break;
         }
         if (!ok) break;
 
         // epilogue: O of a unit that this CTA covers alone, else a partial
-        if (tb < it.t1 && !wait_all(smem_u32(&bars->pv_done[x]), (c - 1) & 1, abort_flag)) break;
-        const bool two = it.t1 - it.t0 > 1;             // group 1 has an O of the same rows
+        if (tb < t1 && !wait_all(smem_u32(&bars->pv_done[x][1]), (c - 1) & 1, abort_flag)) break;
+        const int t0 = it.t0;
+        const bool two = t1 - t0 > 1;                   // group 1 has an O of the same rows
         if (x == 1) {
             bars->stat[r] = make_float2(m, l);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&bars->stat_full));
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&bars->stat_full));
+                mbar_arrive(smem_u32(&bars->item_empty[i % kPagedItems]));
+            }
             // group 0 reads this group's O: not overwritten before it has
             if (!wait_all(smem_u32(&bars->epi_done), i & 1, abort_flag)) break;
             continue;
@@ -1658,11 +1657,12 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBarsOf<C::
         const float f1 = other.x == -INFINITY && other.y == 0.f ? 0.f : ex2(other.x - mm);
         l = l * f0 + other.y * f1;
         m = mm;
-        const bool whole = it.t1 - it.t0 == it.nt;
-        const int part = 2 * blockIdx.x + (it.t0 == 0 ? 1 : 0);
+        const bool whole = t1 - t0 == it.nt;
+        const int part = 2 * blockIdx.x + (t0 == 0 ? 1 : 0), tok = r / p.G;
+        const int at = (it.row0 + tok) * p.H + it.h0 + r - tok * p.G;
         if (threadIdx.x == 0 && !whole) {
-            parts |= it.t0 == 0 ? 2 : 1;
-            p.meta[part] = PagedMeta{it.row0, it.h0, it.rows, it.t1 == it.nt};
+            parts |= t0 == 0 ? 2 : 1;
+            p.meta[part] = PagedMeta{it.row0, it.h0, it.rows, t1 == it.nt};
         }
         if (work) {
             tc_fence_after();
@@ -1704,7 +1704,10 @@ __device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBarsOf<C::
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->epi_done));
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&bars->epi_done));
+            mbar_arrive(smem_u32(&bars->item_empty[i % kPagedItems]));
+        }
     }
     if (threadIdx.x == 0)               // empty slots; one that is missing (a CTA that gave up) also ends its unit
         for (int s = 0; s < 2; ++s)
@@ -1715,31 +1718,36 @@ template <bool BF>
 __global__ void __launch_bounds__(kRowsThreads, 1)
     fmha_paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
     using C = RowsCfg<BF>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];        // no room to align it here
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x < 2) p.meta[2 * blockIdx.x + threadIdx.x] = PagedMeta{0, 0, 0, 1};
+        if (threadIdx.x == 0) atomicCAS(&g_status, FMHA_OK, FMHA_ERR_CUDA);
+        return;
+    }
     RowsBarsOf<C::VS> *bars = reinterpret_cast<RowsBarsOf<C::VS> *>(smem + C::OFF_BARS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&bars->q_full[x]), 8);          // the warps that write its rows
-            mbar_init(smem_u32(&bars->s_full[x]), 1);
-            mbar_init(smem_u32(&bars->p_full[x][0]), 4);
-            mbar_init(smem_u32(&bars->p_full[x][1]), 4);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(smem_u32(&bars->s_full[x][h]), 1);
+                mbar_init(smem_u32(&bars->p_full[x][h]), 4);
+                mbar_init(smem_u32(&bars->pv_done[x][h]), 1);
+            }
             mbar_init(smem_u32(&bars->scale_full[x][0]), 32);  // the producer's lanes
             mbar_init(smem_u32(&bars->scale_full[x][1]), 32);
-            mbar_init(smem_u32(&bars->s_free[x]), 4);
-            mbar_init(smem_u32(&bars->pv_done[x]), 1);
             mbar_init(smem_u32(&bars->drain[x]), 1);
-            mbar_init(smem_u32(&bars->k_full[x][0]), 1);
-            mbar_init(smem_u32(&bars->k_empty[x][0]), 1);
-            for (int s = 0; s < C::VS; ++s) {
-                mbar_init(smem_u32(&bars->v_full[x][s]), 1);
-                mbar_init(smem_u32(&bars->v_empty[x][s]), 1);
-            }
+            mbar_init(smem_u32(&bars->k_full[x]), 1);
+            mbar_init(smem_u32(&bars->k_empty[x]), 1);
+            mbar_init(smem_u32(&bars->vf_full[x]), 4);         // the converters
+        }
+        for (int s = 0; s < C::VS; ++s) {
+            mbar_init(smem_u32(&bars->v_full[s]), 1);
+            mbar_init(smem_u32(&bars->v_empty[s]), 4);
         }
         for (int s = 0; s < kPagedItems; ++s) {
             mbar_init(smem_u32(&bars->item_full[s]), 1);
-            mbar_init(smem_u32(&bars->item_empty[s]), 11);       // the softmax, V and MMA warps
+            mbar_init(smem_u32(&bars->item_empty[s]), 15);       // all warps but K's
         }
         mbar_init(smem_u32(&bars->q_empty), 2);
         mbar_init(smem_u32(&bars->stat_full), 4);
@@ -1747,13 +1755,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
         bars->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) {
+    if (warp == kRowsMma) {
         tmem_alloc(smem_u32(&bars->tmem_base), 512);
         tmem_relinquish();
     }
     PagedCursor cur;
     int gate = 0;
-    if (warp == 8) {
+    if (warp == kRowsK) {
         if (lane == 0) {
             prefetch_tmap(&tmK);
             prefetch_tmap(&tmV);
@@ -1766,14 +1774,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
     tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (warp < 8) rows_softmax<C>(p, smem, bars, tmem, warp, lane);
-    else if (warp == 8) rows_producer<C, false>(p, cur, gate, &tmK, smem, bars, lane);
-    else if (warp == 11) rows_producer<C, true>(p, cur, 0, &tmV, smem, bars, lane);
-    else rows_mma<C>(smem, bars, tmem, warp - 9, lane);
+    if (warp < kRowsConv) rows_softmax<C>(p, smem, bars, tmem, warp, lane);
+    else if (warp < kRowsK) rows_convert<C>(smem, bars, warp - kRowsConv, lane);
+    else if (warp == kRowsK) rows_producer<C, false>(p, cur, gate, &tmK, smem, bars, lane);
+    else if (warp == kRowsV) rows_producer<C, true>(p, cur, 0, &tmV, smem, bars, lane);
+    else rows_mma<C>(smem, bars, tmem, warp - kRowsMma, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) {
+    if (warp == kRowsMma) {
         __syncwarp();
         tmem_dealloc(tmem, 512);
     }
