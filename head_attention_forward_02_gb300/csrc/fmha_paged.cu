@@ -178,8 +178,7 @@ __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint
                  : "memory");
 }
 
-// Four k-steps, whose descriptors lie `as` and `bs` apart, under one election: with
-// one a step, a step took an issuing warp 100 cycles next to the softmax warps.
+// Four k-steps, whose descriptors lie AS and BS bytes apart, under one election
 template <bool FP8, int AS, int BS>
 __device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
 #define FMHA_MMA4(KIND)                                                                                                   \
@@ -334,8 +333,8 @@ __device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&r)[N]) 
 }
 
 // Four weights as two terms each (first weight in the low byte), by way of f16,
-// whose 11 bits hold a rest exactly: p = hi + mid / 16 in e4m3.  In one piece of PTX, since a 16-bit code that passes through
-// C++ costs an instruction to widen it.
+// whose 11 bits hold a rest exactly: p = hi + mid / 16 in e4m3.  In one piece of
+// PTX, since a 16-bit code that passes through C++ costs an instruction to widen it.
 __device__ __forceinline__ void split4(const float (&e)[4], uint32_t &hi, uint32_t &mid) {
     const uint32_t p = pack2<false>(e[0], e[1]), q = pack2<false>(e[2], e[3]);
     asm("{\n.reg .b16 a, b;\n.reg .b32 x, y;\n"
@@ -1187,28 +1186,37 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 // 3400 cycles a tile of 64 rows where the MMAs need 800.  Here S = Q K^T has the
 // rows as M: a thread is a row (TMEM lane), its reference, sum and limit are in
 // registers, nothing is exchanged, and a page's scale is one factor for its
-// columns.  Two groups, each an MMA issuer and four softmax warps with a ring, S, P
-// and O of their own, take every other tile, and their O are added up at the
-// end.  The terms are passes of their own into the same accumulator:
-//   S  = Q_0 K^T + Q_1 K^T (+ Q_2 K^T, f16), without a factor of 16, so that elements
-//        of q below 2^-9 (f16 2^-6) of their row's largest are off by 2^-17 of it;
-//   O += P_0 V + P_1 V (f16: + P_2 V, in e5m2), also without a factor of 16: a weight
-//        is off by 2^-8 (f16 2^-11) of itself, or by 2^-10 (f16 2^-13) where the group's
-//        largest is 2^7 or more; a group has 16 tiles, and loses 2^-6 of its weight
-//        at most.  (P_1 in e5m2 under a largest of 2^2 was 3% faster and twice as far off.)
+// columns.  Two groups, each an MMA issuer and four softmax warps with K, V, S
+// and O of their own, take every other tile, and their O are added up at the end.
+//   S  = Q_0 K^T + Q_1 K^T (+ Q_2 K^T, f16), the terms passes of their own into the same
+//        accumulator, without a factor of 16, so that elements of q below 2^-9
+//        (f16 2^-6) of their row's largest are off by 2^-17 of it;
+//   O += P V with both in f16, which holds every e4m3 number: a weight is off by 2^-11
+//        of itself, or by 2^-25 where the group's largest is 2^7 or more (a reference
+//        serves 16 tiles, so that this is 2^-21 of their weight at most).
+// 128 rows share a tile's V, so that four warps that convert it cost less than
+// splitting every weight into e4m3 terms did (12 instructions for four weights
+// instead of two), and less shared memory traffic, which two terms of P read.
 //
-// The tensor cores do four (f16: six) e4m3 products of 128 x 128 x 128 a tile, the
-// time of the two that bf16 operands would take.  What bounds it is the softmax:
-// of 4 chunks of 512 tokens on 8192 keys (229 us, 813 TFLOP/s; f16 291; flops 97 at the
-// bf16 rate) the tensor pipe is busy 39% of the time, the ALU, which splits the weights,
-// 44%, and a group's tile is a chain of 5300 cycles.  Units of 256 rows, a block a group,
-// were 3% slower; P over S in TMEM, so that S waits for P V, 8%.
+// A tile's scores, and its weights, are halves of 64 keys, each a link of a chain:
+// S of a half, softmax, P over that S in TMEM, P V, and S of the half two tiles on,
+// while the softmax is at the other half.
+//
+// What bounds it is that chain: of 4 chunks of 512 tokens on 8192 keys (206 us, 903
+// TFLOP/s; f16 215; flops 97 at the bf16 rate) a half takes a group 2500 cycles, of
+// which its softmax computes 1600 and waits 700 for S; the tensor pipe is busy 40%
+// of them, issue slots 73%.  Without one of S's passes it takes 1% less, without P V 3%, without
+// the conversion 7%.  Weights as e4m3 terms in shared memory took 229 (f16: three,
+// 291), f16 ones there 232; S and P V a whole tile at a time 232; V converted a tile ahead
+// 213; 16 softmax warps, two threads a row, 231; units of 256 rows, a block a
+// group, 3% more.
 // ---------------------------------------------------------------------------
 
 constexpr int kRowsBars = 3072;          // barrier block
+constexpr int kRowsVs = 2;               // tiles of V as codes, for both groups
 constexpr int kRowsTiles = 16;           // tiles that a reference serves at most
 constexpr float kRowsGrown = 15.f;       // as kGrown: f16 ends at 2^16
-constexpr float kRowsBias = 7.f;         // as kBias: higher, for the second term's sake
+constexpr float kRowsBias = 7.f;         // as kBias
 constexpr int kRowsConv = 8, kRowsK = 12, kRowsMma = 13, kRowsV = 15;   // first warps of the roles behind the softmax's
 constexpr int kRowsThreads = 512;        // two softmax groups and the converters, of four warps; K's and V's producers, an MMA issuer a group
 
@@ -1216,21 +1224,19 @@ template <bool BF_>
 struct RowsCfg {
     static constexpr bool BF = BF_;
     static constexpr int NT = BF ? 2 : 3;                     // terms of q
-    static constexpr int VS = BF ? 2 : 1;                     // tiles of V as codes
     static constexpr int OFF_VF = NT * kPanelBytes;           // after q's terms, by group: V in f16,
     static constexpr int OFF_K = OFF_VF + 4 * kPanelBytes;    // and K (one tile, free once its S is there)
     static constexpr int OFF_V = OFF_K + 2 * kPanelBytes;     // V as it comes, for both
-    static constexpr int OFF_BARS = OFF_V + VS * kPanelBytes;
-    static constexpr int SMEM_BYTES = OFF_BARS + kRowsBars;   // the array is 1 KB aligned
+    static constexpr int OFF_BARS = OFF_V + kRowsVs * kPanelBytes;
+    static constexpr int SMEM_BYTES = OFF_BARS + kRowsBars + 1024;   // 1 KB alignment
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
-template <int VS>
-struct RowsBarsOf {
+struct RowsBars {
     uint64_t q_full[2], q_empty, drain[2];                    // by group,
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];   // and half of a tile
     uint64_t stat_full, epi_done;
-    uint64_t k_full[2], k_empty[2], v_full[VS], v_empty[VS], vf_full[2], scale_full[2][2];
+    uint64_t k_full[2], k_empty[2], v_full[kRowsVs], v_empty[kRowsVs], vf_full[2], scale_full[2][2];
     uint64_t item_full[kPagedItems], item_empty[kPagedItems];
     PagedItem item[kPagedItems];
     uint32_t tmem_base;
@@ -1239,10 +1245,9 @@ struct RowsBarsOf {
     float2 stat[kRows];                  // reference and sum of group 1's rows
     float qscale[kRows];                 // of the rows of q
 };
-static_assert(sizeof(RowsBarsOf<2>) <= kRowsBars, "barrier block");
+static_assert(sizeof(RowsBars) <= kRowsBars, "barrier block");
 
-template <int VS>
-__device__ __forceinline__ bool rows_take(RowsBarsOf<VS> *bars, uint32_t i, PagedItem &it, volatile int *abort_flag, int lane) {
+__device__ __forceinline__ bool rows_take(RowsBars *bars, uint32_t i, PagedItem &it, volatile int *abort_flag, int lane) {
     const uint32_t st = i % kPagedItems;
     if (!wait_all(smem_u32(&bars->item_full[st]), (i / kPagedItems) & 1, abort_flag)) return false;
     it = bars->item[st];
@@ -1253,9 +1258,9 @@ __device__ __forceinline__ bool rows_take(RowsBarsOf<VS> *bars, uint32_t i, Page
 
 // A producer warp: the groups' tiles of K, with the pages' scales, or (V) of V.  One
 // warp for both held a group's K back behind the other's V (230 us for 4 chunks of
-// 512, f16 400).
+// 512, f16 400, with one slot of either).
 template <class C, bool V>
-__device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, const CUtensorMap *tm, uint8_t *smem, RowsBarsOf<C::VS> *bars,
+__device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, const CUtensorMap *tm, uint8_t *smem, RowsBars *bars,
                               int lane) {
     volatile int *abort_flag = &bars->abort;
     bool ok = true;
@@ -1294,7 +1299,7 @@ __device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, 
             const int head = id >= 0 ? id * p.H_k + it.g : p.n_pages * p.H_k;
             const int x = (t - it.t0) & 1;
             // V's tiles share a ring; K's have a slot a group
-            const uint32_t n = V || x == 0 ? fill[0] : fill[1], st = V ? n % C::VS : 0, lap = V ? n / C::VS : n;
+            const uint32_t n = V || x == 0 ? fill[0] : fill[1], st = V ? n % kRowsVs : 0, lap = V ? n / kRowsVs : n;
             const uint32_t full = smem_u32(V ? &bars->v_full[st] : &bars->k_full[x]);
             if (lap > 0 && !wait_all(smem_u32(V ? &bars->v_empty[st] : &bars->k_empty[x]), lap & 1 ^ 1, abort_flag)) {
                 ok = false;
@@ -1333,7 +1338,7 @@ __device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, 
     }
     // no copy may be in flight when the block ends, nor a product that reads one
     ok = *abort_flag == 0;
-    constexpr uint32_t kSlots = V ? C::VS : 1;
+    constexpr uint32_t kSlots = V ? kRowsVs : 1;
 #pragma unroll
     for (int x = 0; x < (V ? 1 : 2); ++x)
         for (uint32_t n = fill[x] > kSlots ? fill[x] - kSlots : 0; n < fill[x]; ++n) {
@@ -1349,7 +1354,7 @@ __device__ void rows_producer(const PagedParams &p, PagedCursor &cur, int gate, 
 // bytes to two panels of 64 dims; in a sequence's last tile the rows past the keys
 // are zeros, so that P = 0 contributes 0.
 template <class C>
-__device__ void rows_convert(uint8_t *smem, RowsBarsOf<C::VS> *bars, int w, int lane) {
+__device__ void rows_convert(uint8_t *smem, RowsBars *bars, int w, int lane) {
     volatile int *abort_flag = &bars->abort;
     uint32_t n = 0, done[2] = {0, 0};    // tiles, and those of either group
     PagedItem it;
@@ -1357,9 +1362,9 @@ __device__ void rows_convert(uint8_t *smem, RowsBarsOf<C::VS> *bars, int w, int 
         bool ok = true;
         for (int t = it.t0; t < it.t1; ++t, ++n) {
             const int x = (t - it.t0) & 1, nk = it.L - t * kRows;
-            const uint32_t st = n % C::VS, c = x ? done[1]++ : done[0]++;
+            const uint32_t st = n % kRowsVs, c = x ? done[1]++ : done[0]++;
             // the codes, and room: P V of the group's tile before is done
-            ok = wait_all(smem_u32(&bars->v_full[st]), (n / C::VS) & 1, abort_flag) &&
+            ok = wait_all(smem_u32(&bars->v_full[st]), (n / kRowsVs) & 1, abort_flag) &&
                  (c == 0 || wait_all(smem_u32(&bars->pv_done[x][1]), (c - 1) & 1, abort_flag));
             if (!ok) break;
             const int ch = lane & 7, up = ch >> 2;       // 16 dims of a row; of which panel
@@ -1399,12 +1404,10 @@ __device__ void rows_convert(uint8_t *smem, RowsBarsOf<C::VS> *bars, int w, int 
     }
 }
 
-// MMA issuer of group x.  P lies in shared memory, apart from S, so that S of the
-// next tile is issued as soon as the softmax has this one's in registers, and
-// P V while it is at the next: with P over S in TMEM a group waited 1700 of 5700
-// cycles a tile for P V and S, one after the other (15% more for 4 chunks of 512).
+// MMA issuer of group x.  The code of both is the same: a copy for each, with constant
+// operands, took 299 us for 4 chunks of 512.
 template <class C>
-__device__ void rows_mma(uint8_t *smem, RowsBarsOf<C::VS> *bars, uint32_t tmem_any, int x, int lane) {
+__device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x, int lane) {
     volatile int *abort_flag = &bars->abort;
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
     const uint32_t s_tm = tmem + x * kRows, o_tm = tmem + 2 * kRows + x * kD;
@@ -1491,7 +1494,7 @@ __device__ __forceinline__ float rows_terms(const PagedParams &p, uint8_t *tile,
 
 // Softmax and epilogue of group x, a row a thread.
 template <class C>
-__device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBarsOf<C::VS> *bars, uint32_t tmem, int warp, int lane) {
+__device__ void rows_softmax(const PagedParams &p, uint8_t *smem, RowsBars *bars, uint32_t tmem, int warp, int lane) {
     volatile int *abort_flag = &bars->abort;
     const int x = warp >> 2, r = (warp & 3) * 32 + lane;   // group, row of the unit
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -1718,13 +1721,9 @@ template <bool BF>
 __global__ void __launch_bounds__(kRowsThreads, 1)
     fmha_paged_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
     using C = RowsCfg<BF>;
-    extern __shared__ __align__(1024) uint8_t smem[];        // no room to align it here
-    if (smem_u32(smem) & 1023u) {
-        if (threadIdx.x < 2) p.meta[2 * blockIdx.x + threadIdx.x] = PagedMeta{0, 0, 0, 1};
-        if (threadIdx.x == 0) atomicCAS(&g_status, FMHA_OK, FMHA_ERR_CUDA);
-        return;
-    }
-    RowsBarsOf<C::VS> *bars = reinterpret_cast<RowsBarsOf<C::VS> *>(smem + C::OFF_BARS);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    RowsBars *bars = reinterpret_cast<RowsBars *>(smem + C::OFF_BARS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int x = 0; x < 2; ++x) {
@@ -1741,7 +1740,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
             mbar_init(smem_u32(&bars->k_empty[x]), 1);
             mbar_init(smem_u32(&bars->vf_full[x]), 4);         // the converters
         }
-        for (int s = 0; s < C::VS; ++s) {
+        for (int s = 0; s < kRowsVs; ++s) {
             mbar_init(smem_u32(&bars->v_full[s]), 1);
             mbar_init(smem_u32(&bars->v_empty[s]), 4);
         }

@@ -137,11 +137,11 @@ def attend(q, kc, ks, vc, vs, see, scale, out_scale, dtype, chunk=False):
     top = q.abs().amax(-1)
     ds = (a * 134 * 2.0 ** -23 + top * 2.0 ** (-17 if chunk else -21) * (keys.abs().sum(-1)[None, None] * seen).amax(-1) * scale +
           lse.abs().nan_to_num(0, 0, 0) * 2.0 ** -21 + 1e-5)
-    # a weight: two terms of four bits (2^-8; f16 a third of four, 2^-12, chunk: of three,
-    # 2^-11) from f16's eleven (2^-11); and where the terms end, 2^-14 where the largest
-    # weight is 2^4 or more (chunk: 2^-10, f16 2^-13, and 2^7)
+    # a weight: two terms of four bits (2^-8; f16 three, 2^-12) from f16's eleven (2^-11;
+    # chunk: these, and 2^-12 for the sums of up to 2^10 products, each off by 2^-23 of
+    # the partial one); and where the terms end, 2^-14 where the largest weight is 2^4 or more
     ab = torch.einsum("tgk,kd->tgd", w, vals.abs()) * abs(out_scale)
     low = (w * vs).amax(-1, keepdim=True) * torch.einsum("tgk,kd->tgd", seen.expand(n, G, L), vc.abs()) * abs(out_scale)
-    tol = ab * (2.0 ** (-8 if dtype != "f16" else -11 if chunk else -12) + 2.0 ** -11 + 2 * ds[..., None]) + low * 2.0 ** (-17 if chunk and dtype != "f16" else -18)
+    tol = ab * (2.0 ** (-12 if chunk or dtype == "f16" else -8) + 2.0 ** -11 + 2 * ds[..., None]) + low * 2.0 ** -18
     tol = tol + (o.abs() + tol) * cu.HALF[dtype] + cu.SUBHALF[dtype]
     return o, lse, tol, ds
