@@ -17,8 +17,8 @@
 // bisection.  What a token's slot needs of pages taken by this call comes from
 // the stack, not from the table that other threads write, so there is nothing
 // else to wait for.  Bound by latency (a launch, two dependent reads, a scan, a
-// bisection): 700 sequences with 30000 tokens took 18.0 us as four lists one
-// after the other, a token a job.
+// bisection): 64 sequences of a token each 6.8 us, 700 sequences with 30000 tokens 15.2
+// (18.0 as four lists one after the other, a token a job).
 //
 // Write: a run of tokens with consecutive slots in one page (some of them
 // perhaps left out, by a negative slot); for each kv head
@@ -37,6 +37,9 @@
 // loads of their slots, and in registers between the maximum and the rounding.
 // A longer run (of pages of 32 and more) is spread over two to eight warps, 16
 // rows each, the next head's rows fetched under the rounding of this one's.
+// 16600 tokens of 8 heads: 21.6 us in pages of 16 tokens, 4.7 TB/s, 70% of the copy
+// rate, 22.5 / 25.0 / 28.9 in pages of 32 / 64 / 128; 64 single tokens 4.8 us, a launch
+// and two dependent reads.
 #include <cooperative_groups.h>
 
 #include "fmha_cache.cuh"

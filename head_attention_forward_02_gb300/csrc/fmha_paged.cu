@@ -1875,10 +1875,9 @@ __global__ void __launch_bounds__(32 * kPagedMergeWarps) fmha_paged_merge_kernel
 // ---------------------------------------------------------------------------
 
 // Query rows of a unit: 16 or 32 where a sequence's rows of a kv head fit them,
-// else 128.  (16 sequences of 28 rows on 6000 keys: 45.6 us in units of 32, 57.1 of
+// else 128.  (16 sequences of 28 rows on 6000 keys: 44.4 us in units of 32, 50.8 of
 // 128; 4 sequences of 8192 keys and 64 / 80 / 128 rows: 35 / 48 / 56 in units of 64,
-// two groups a pipeline, 32 / 34 / 37 of 128; 160 / 256 / 2048 rows: 53 / 59 / 229 in
-// units of 256, a block of rows a group, 45 / 50 / 224 of 128.)
+// two groups a pipeline, 30 / 31 / 34 of 128.)
 int paged_rows(int64_t max_q, int G) { return max_q * G <= 16 ? 16 : max_q * G <= 32 ? 32 : kRows; }
 
 using PagedKernel = void (*)(CUtensorMap, CUtensorMap, PagedParams);
