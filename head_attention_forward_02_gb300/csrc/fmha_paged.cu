@@ -1212,7 +1212,7 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 // group, 3% more.
 // ---------------------------------------------------------------------------
 
-constexpr int kRowsBars = 3072;          // barrier block
+constexpr int kRowsBars = 4096;          // barrier block
 constexpr int kRowsVs = 2;               // tiles of V as codes, for both groups
 constexpr int kRowsTiles = 16;           // tiles that a reference serves at most
 constexpr float kRowsGrown = 15.f;       // as kGrown: f16 ends at 2^16
