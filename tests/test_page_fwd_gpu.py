@@ -289,3 +289,26 @@ def test_random_cases(fm):
         o, lse, status = run(fm, c)
         assert status == 0
         check(c, o, lse)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_chunks(fm, seed):
+    """Sequences of many rows beside those of few, any group size, lengths around the
+    tiles' ends, fewer keys than rows."""
+    rng = random.Random(seed)
+    for k in range(4):
+        H_k = rng.choice([1, 2, 3, 4])
+        G = rng.choice([1, 2, 3, 4, 5, 7, 8, 16, 33, 128 if H_k == 1 else 6])
+        lengths, news = [], []
+        for _ in range(rng.choice([1, 2, 3, 5])):
+            n = min(rng.choice([0, 1, 3, 17, 33, 64, 100, 129, 200]), max(1, 600 // G))
+            L = n + rng.choice([0, 0, 1, 15, 63, 64, 65, 127, 128, 129, 200, 500, 900, 1500])
+            news.append(n)
+            lengths.append(max(0, n - rng.choice([1, 3])) if rng.random() < 0.1 else L)
+        if max(news) * G <= 32:
+            news[0], lengths[0] = 33, 33 + rng.randint(0, 700)
+        c = make(rng.choice(["bf16", "f16"]), H_k * G, H_k, rng.choice([16, 32, 64, 128]), lengths, news, seed=100 * seed + k,
+                 mask=rng.choice(["causal", "causal", "none"]), extra_rows=rng.choice([0, 3]), q_scale=rng.choice([0.5, 2.0, 8.0]))
+        o, lse, status = run(fm, c)
+        assert status == 0
+        check(c, o, lse)
