@@ -178,22 +178,18 @@ __device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint
                  : "memory");
 }
 
-// Four k-steps, whose descriptors lie AS and BS bytes apart, under one election
-template <bool FP8, int AS, int BS>
+// Four k-steps of e4m3, whose descriptors lie AS and BS bytes apart, under one election
+template <int AS, int BS>
 __device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-#define FMHA_MMA4(KIND)                                                                                                   \
-    asm volatile("{\n.reg .pred p, e;\n.reg .b64 a1, a2, a3, b1, b2, b3;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n" \
-                 "add.u64 a1, %1, %5;\nadd.u64 b1, %2, %6;\nadd.u64 a2, a1, %5;\nadd.u64 b2, b1, %6;\n"                  \
-                 "add.u64 a3, a2, %5;\nadd.u64 b3, b2, %6;\n"                                                             \
-                 "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], %1, %2, %3, p;\n"                                       \
-                 "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a1, b1, %3, 1;\n"                                       \
-                 "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a2, b2, %3, 1;\n"                                       \
-                 "@e tcgen05.mma.cta_group::1.kind::" KIND " [%0], a3, b3, %3, 1;\n}\n" ::"r"(d),                         \
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(AS >> 4), "n"(BS >> 4)                                          \
-                 : "memory")
-    if constexpr (FP8) FMHA_MMA4("f8f6f4");
-    else FMHA_MMA4("f16");
-#undef FMHA_MMA4
+    asm volatile("{\n.reg .pred p, e;\n.reg .b64 a1, a2, a3, b1, b2, b3;\nsetp.ne.b32 p, %4, 0;\nelect.sync _|e, 0xffffffff;\n"
+                 "add.u64 a1, %1, %5;\nadd.u64 b1, %2, %6;\nadd.u64 a2, a1, %5;\nadd.u64 b2, b1, %6;\n"
+                 "add.u64 a3, a2, %5;\nadd.u64 b3, b2, %6;\n"
+                 "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+                 "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, 1;\n"
+                 "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, 1;\n"
+                 "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, 1;\n}\n" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(acc), "n"(AS >> 4), "n"(BS >> 4)
+                 : "memory");
 }
 
 __device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
@@ -701,9 +697,9 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
         const uint64_t v = v0 + ((st * C::STAGE) >> 4), pt = p0 + ((b * C::P_BYTES) >> 4);
         const uint32_t o_tm = tmem + 2 * C::COLS;
         // 32 keys a step
-        mma4<true, 32 * 128, 32 * C::P_ROW>(o_tm, v, pt, paged_idesc(32, true), begins ? 0u : 1u);
+        mma4<32 * 128, 32 * C::P_ROW>(o_tm, v, pt, paged_idesc(32, true), begins ? 0u : 1u);
         if constexpr (C::THIRD && !C::INLINE3)
-            mma4<true, 32 * 128, 32 * C::P_ROW>(o_tm + C::COLS, v, pt + (C::P_TILE >> 4), paged_idesc(16, true), begins ? 0u : 1u);
+            mma4<32 * 128, 32 * C::P_ROW>(o_tm + C::COLS, v, pt + (C::P_TILE >> 4), paged_idesc(16, true), begins ? 0u : 1u);
         tc_commit(smem_u32(&bars->pv_done[w][b]));
         tc_commit(smem_u32(&bars->kv_empty[st]));
         return true;
@@ -738,8 +734,8 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
             tc_fence_after();
             const uint64_t k = k0 + ((st * C::STAGE) >> 4);
             const uint32_t s_tm = tmem + b * C::COLS;
-            mma4<true, 32, 32>(s_tm, k, q, paged_idesc(32, false), 0u);      // 32 dims a step: 32 bytes of a row
-            if constexpr (!C::BF) mma4<true, 32, 32>(s_tm + 16, k, q3, paged_idesc(16, false), 1u);
+            mma4<32, 32>(s_tm, k, q, paged_idesc(32, false), 0u);      // 32 dims a step: 32 bytes of a row
+            if constexpr (!C::BF) mma4<32, 32>(s_tm + 16, k, q3, paged_idesc(16, false), 1u);
             tc_commit(smem_u32(&bars->s_full[w][b]));
             if (t + kStep >= it.t1) tc_commit(smem_u32(&bars->q_empty[slot]));
             if (t > tb && !issue_pv(m - 1, st_before, t - kStep == tb)) {
@@ -1431,7 +1427,7 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
             tc_fence_after();
 #pragma unroll
             for (int term = 0; term < C::NT; ++term)     // 32 dims a step: 32 bytes of a row
-                mma4<true, 32, 32>(s_tm + 64 * h, q + ((term * kPanelBytes) >> 4), k + ((h * 64 * 128) >> 4), kIdS, term > 0 ? 1u : 0u);
+                mma4<32, 32>(s_tm + 64 * h, q + ((term * kPanelBytes) >> 4), k + ((h * 64 * 128) >> 4), kIdS, term > 0 ? 1u : 0u);
             tc_commit(smem_u32(&bars->s_full[x][h]));
             return true;
         };
