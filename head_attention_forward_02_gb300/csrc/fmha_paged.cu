@@ -1200,9 +1200,9 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 //
 // What bounds it is that chain: of 4 chunks of 512 tokens on 8192 keys (206 us, 903
 // TFLOP/s; f16 215; flops 97 at the bf16 rate) a half takes a group 2500 cycles, of
-// which its softmax computes 1600 and waits 700 for S; the tensor pipe is busy 40%
-// of them, issue slots 73%.  Without one of S's passes it takes 1% less, without P V 3%, without
-// the conversion 7%.  Weights as e4m3 terms in shared memory took 229 (f16: three,
+// which its softmax computes 1600 and waits 700 for S; the tensor pipe is busy 43%
+// (f16 52%), the ALU 42%, issue slots 54%.  Without one of S's passes it takes 1% less,
+// without P V 3%, without the conversion 7%.  Weights as e4m3 terms in shared memory took 229 (f16: three,
 // 291), f16 ones there 232; S and P V a whole tile at a time 232; V converted a tile ahead
 // 213; 16 softmax warps, two threads a row, 231; units of 256 rows, a block a
 // group, 3% more.
