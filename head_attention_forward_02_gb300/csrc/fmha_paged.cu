@@ -17,8 +17,8 @@
 //   q  = 2^k (q_0 + q_1 / 16), each 4 bits: all 8 bits of a bf16 row's
 //        elements down to 2^-13 of its largest (2^k: a power of two per row); f16
 //        has a third term, added to the second's columns by an MMA of its own;
-//   P' = p_0 + p_1 / 16, off by 2^-8 of a weight at most, 16 times less than
-//        the rounding that made the codes; f16: + p_2 / 256, off by 2^-11.
+//   P' = p_0 + p_1 / 16 + p_2 / 256, off by 2^-11 of a weight (two terms: 2^-8, and
+//        small weights next to a large one lost from 2^-14 of the terms' unit on).
 // A group of 16 query rows is thus 32 columns, [16 first terms | 16 second], and a
 // unit one or two such groups of one kv head: single tokens, drafts, the ends of
 // prompts.  More rows have a kernel of their own, further down.
@@ -30,8 +30,8 @@
 // score that outgrows the reference opens a new group early (a reference up to
 // 2^2 higher, if one was that high before, makes these fewer).
 // So a long context of small weights behind a large one is not rounded to
-// nothing: of a group's weight, what e4m3's smallest steps lose is 2^-6 at most
-// (1024 weights of 2^-14 where the largest is 2^2 or more), or 2^-42 a key of the
+// nothing: of a group's weight, what e4m3's smallest steps lose is 2^-10 at most
+// (1024 weights of 2^-18 where the largest is 2^2 or more), or 2^-46 a key of the
 // largest weight of all (a reference is not more than 2^24 below the highest so
 // far, which keeps fp32 in its range).
 // Row sums are of the unrounded weights, in fp32.
@@ -47,11 +47,11 @@
 // thread is a key, and for O^T a dim.
 //
 // Bound by HBM where there are few rows.  64 sequences of 2100 to 8192 keys, 32/8
-// heads, bf16: 109 us, 6.2 TB/s, 92% of the copy rate (one pipeline, and scales
+// heads, bf16: 110 us, 6.2 TB/s, 91% of the copy rate (one pipeline, and scales
 // loaded by the softmax threads: 149); 8 of 8200 to 32768 in pages of 16, 64/8 heads,
 // f16: 75 us, 71%; one sequence of 1000: 10.7 us, all latency: 2.5 to the first
 // item, 5 to the first S, 7.5 to the last O, the rest the join.  16 sequences of 1500
-// to 6000 with 7 tokens: 45 us where the bytes take 19: a tile's chain of S, vote,
+// to 6000 with 7 tokens: 48 us where the bytes take 19 (weights as two terms: 45): a tile's chain of S, vote,
 // weights and P V takes 1.1 us where its bytes take 0.73.
 #include "fmha_cache.cuh"
 
@@ -85,13 +85,12 @@ struct PagedCfg {
     static constexpr int QW = SW, PROD = SW + 1, MMA = PROD + NP;   // q warp, producers, two MMA issuers
     static constexpr int THREADS = 32 * (MMA + 2);
     static constexpr int COLS = 32;                           // of a pipeline's S^T and O^T: a group's
-    static constexpr bool THIRD = !BF;                        // weights have a third term:
-    static constexpr bool INLINE3 = THIRD && NR <= 8;         // in columns 8 .. 15 of the group, else a tile of its own
+    static constexpr bool INLINE3 = NR <= 8;                  // third terms in columns 8 .. 15 of the group, else in a tile of their own
     static constexpr int PIPE_COLS = 4 * COLS;                // TMEM: two S^T, O^T, and O^T of third terms that are apart
     static constexpr int TMEM_COLS = 2 * PIPE_COLS;
     static constexpr int P_ROW = COLS;                        // bytes of a key's P^T row
     static constexpr int P_TILE = kRows * P_ROW;
-    static constexpr int P_BYTES = P_TILE * (THIRD && !INLINE3 ? 2 : 1);
+    static constexpr int P_BYTES = P_TILE * (INLINE3 ? 1 : 2);
     static constexpr uint64_t P_SWZ = 6;                      // 32-byte swizzle
     static constexpr int Q_BYTES = (BF ? 32 : 48) * NG * 128; // first and second terms, then f16's third
     static constexpr int STAGE = 2 * kPanelBytes;             // K and V of 128 keys
@@ -256,21 +255,6 @@ __device__ __forceinline__ void wait_terms(uint32_t (&r)[2 * NR]) {
     }
 }
 
-// As split4, with a third term: p = hi + mid / 16 + low / 256.
-__device__ __forceinline__ void split4_third(const float (&e)[4], uint32_t &hi, uint32_t &mid, uint32_t &low) {
-    const uint32_t p = pack2<false>(e[0], e[1]), q = pack2<false>(e[2], e[3]);
-    asm("{\n.reg .b16 a, b;\n.reg .b32 x, y, u, v;\n"
-        "cvt.rn.satfinite.e4m3x2.f16x2 a, %3;\ncvt.rn.satfinite.e4m3x2.f16x2 b, %4;\nmov.b32 %0, {a, b};\n"
-        "cvt.rn.f16x2.e4m3x2 x, a;\ncvt.rn.f16x2.e4m3x2 y, b;\nsub.rn.f16x2 x, %3, x;\nsub.rn.f16x2 y, %4, y;\n"
-        "mul.rn.f16x2 x, x, %5;\nmul.rn.f16x2 y, y, %5;\n"
-        "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\ncvt.rn.satfinite.e4m3x2.f16x2 b, y;\nmov.b32 %1, {a, b};\n"
-        "cvt.rn.f16x2.e4m3x2 u, a;\ncvt.rn.f16x2.e4m3x2 v, b;\nsub.rn.f16x2 x, x, u;\nsub.rn.f16x2 y, y, v;\n"
-        "mul.rn.f16x2 x, x, %5;\nmul.rn.f16x2 y, y, %5;\n"
-        "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\ncvt.rn.satfinite.e4m3x2.f16x2 b, y;\nmov.b32 %2, {a, b};\n}\n"
-        : "=&r"(hi), "=&r"(mid), "=&r"(low)
-        : "r"(p), "r"(q), "r"(0x4c004c00u));                 // 16, 16
-}
-
 // Bounded waits as in fmha_cache.cuh, but with a hint that lets the hardware
 // suspend the warp for up to 20 us: most of a CTA's warps wait most of the time,
 // and polling took as many issue slots as the softmax.
@@ -328,18 +312,21 @@ __device__ __forceinline__ void st_cols(uint32_t taddr, const uint32_t (&r)[N]) 
                      : "memory");
 }
 
-// Four weights as two terms each (first weight in the low byte), by way of f16,
-// whose 11 bits hold a rest exactly: p = hi + mid / 16 in e4m3.  In one piece of
+// Four weights as three terms each (first weight in the low byte), by way of f16,
+// whose 11 bits hold a rest exactly: p = hi + mid / 16 + low / 256 in e4m3.  In one piece of
 // PTX, since a 16-bit code that passes through C++ costs an instruction to widen it.
-__device__ __forceinline__ void split4(const float (&e)[4], uint32_t &hi, uint32_t &mid) {
+__device__ __forceinline__ void split4(const float (&e)[4], uint32_t &hi, uint32_t &mid, uint32_t &low) {
     const uint32_t p = pack2<false>(e[0], e[1]), q = pack2<false>(e[2], e[3]);
-    asm("{\n.reg .b16 a, b;\n.reg .b32 x, y;\n"
-        "cvt.rn.satfinite.e4m3x2.f16x2 a, %2;\ncvt.rn.satfinite.e4m3x2.f16x2 b, %3;\nmov.b32 %0, {a, b};\n"
-        "cvt.rn.f16x2.e4m3x2 x, a;\ncvt.rn.f16x2.e4m3x2 y, b;\nsub.rn.f16x2 x, %2, x;\nsub.rn.f16x2 y, %3, y;\n"
-        "mul.rn.f16x2 x, x, %4;\nmul.rn.f16x2 y, y, %4;\n"
-        "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\ncvt.rn.satfinite.e4m3x2.f16x2 b, y;\nmov.b32 %1, {a, b};\n}\n"
-        : "=r"(hi), "=r"(mid)
-        : "r"(p), "r"(q), "r"(0x4c004c00u));             // 16, 16
+    asm("{\n.reg .b16 a, b;\n.reg .b32 x, y, u, v;\n"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, %3;\ncvt.rn.satfinite.e4m3x2.f16x2 b, %4;\nmov.b32 %0, {a, b};\n"
+        "cvt.rn.f16x2.e4m3x2 x, a;\ncvt.rn.f16x2.e4m3x2 y, b;\nsub.rn.f16x2 x, %3, x;\nsub.rn.f16x2 y, %4, y;\n"
+        "mul.rn.f16x2 x, x, %5;\nmul.rn.f16x2 y, y, %5;\n"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\ncvt.rn.satfinite.e4m3x2.f16x2 b, y;\nmov.b32 %1, {a, b};\n"
+        "cvt.rn.f16x2.e4m3x2 u, a;\ncvt.rn.f16x2.e4m3x2 v, b;\nsub.rn.f16x2 x, x, u;\nsub.rn.f16x2 y, y, v;\n"
+        "mul.rn.f16x2 x, x, %5;\nmul.rn.f16x2 y, y, %5;\n"
+        "cvt.rn.satfinite.e4m3x2.f16x2 a, x;\ncvt.rn.satfinite.e4m3x2.f16x2 b, y;\nmov.b32 %2, {a, b};\n}\n"
+        : "=&r"(hi), "=&r"(mid), "=&r"(low)
+        : "r"(p), "r"(q), "r"(0x4c004c00u));                 // 16, 16
 }
 
 // ---------------------------------------------------------------------------
@@ -698,7 +685,7 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
         const uint32_t o_tm = tmem + 2 * C::COLS;
         // 32 keys a step
         mma4<32 * 128, 32 * C::P_ROW>(o_tm, v, pt, paged_idesc(32, true), begins ? 0u : 1u);
-        if constexpr (C::THIRD && !C::INLINE3)
+        if constexpr (!C::INLINE3)
             mma4<32 * 128, 32 * C::P_ROW>(o_tm + C::COLS, v, pt + (C::P_TILE >> 4), paged_idesc(16, true), begins ? 0u : 1u);
         tc_commit(smem_u32(&bars->pv_done[w][b]));
         tc_commit(smem_u32(&bars->kv_empty[st]));
@@ -920,14 +907,12 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                         }
                     }
                     st_terms<NR>(tmem + 2 * C::COLS, s);
-                    if constexpr (C::THIRD) {
-                        uint32_t z[NR];
-                        ld_cols<NR>(tmem + (C::INLINE3 ? 2 * C::COLS + 8 : 3 * C::COLS), z);
+                    uint32_t z[NR];
+                    ld_cols<NR>(tmem + (C::INLINE3 ? 2 * C::COLS + 8 : 3 * C::COLS), z);
 #pragma unroll
-                        for (int k = 0; k < NR; ++k)
-                            z[k] = __float_as_uint(__uint_as_float(z[k]) * bars->am[w][row0 + k]);
-                        st_cols<NR>(tmem + (C::INLINE3 ? 2 * C::COLS + 8 : 3 * C::COLS), z);
-                    }
+                    for (int k = 0; k < NR; ++k)
+                        z[k] = __float_as_uint(__uint_as_float(z[k]) * bars->am[w][row0 + k]);
+                    st_cols<NR>(tmem + (C::INLINE3 ? 2 * C::COLS + 8 : 3 * C::COLS), z);
                 }
 #pragma unroll
                 for (int k = 0; k < NR; k += 4) {
@@ -958,22 +943,21 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                 for (int q = 0; q < 4; ++q) v[q] = ex2(v[q]);
                 l[k / 2] = fma_f2(pack_f2(v[0], v[1]), isv2, l[k / 2]);
                 l[k / 2 + 1] = fma_f2(pack_f2(v[2], v[3]), isv2, l[k / 2 + 1]);
-                if constexpr (C::THIRD) split4_third(v, hi[k / 4], mid[k / 4], low[k / 4]);
-                else split4(v, hi[k / 4], mid[k / 4]);
+                split4(v, hi[k / 4], mid[k / 4], low[k / 4]);
             }
             uint8_t *ph = prow + (swz << 4), *pm = prow + ((1 ^ swz) << 4);
             if constexpr (NR == 16) {
                 *reinterpret_cast<uint4 *>(ph) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4 *>(pm) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                if constexpr (C::THIRD) *reinterpret_cast<uint4 *>(ph + C::P_TILE) = make_uint4(low[0], low[1], low[2], low[3]);
+                *reinterpret_cast<uint4 *>(ph + C::P_TILE) = make_uint4(low[0], low[1], low[2], low[3]);
             } else if constexpr (NR == 8) {
                 *reinterpret_cast<uint2 *>(ph) = make_uint2(hi[0], hi[1]);
                 *reinterpret_cast<uint2 *>(pm) = make_uint2(mid[0], mid[1]);
-                if constexpr (C::THIRD) *reinterpret_cast<uint2 *>(ph + 8) = make_uint2(low[0], low[1]);
+                *reinterpret_cast<uint2 *>(ph + 8) = make_uint2(low[0], low[1]);
             } else {
                 *reinterpret_cast<uint32_t *>(ph) = hi[0];
                 *reinterpret_cast<uint32_t *>(pm) = mid[0];
-                if constexpr (C::THIRD) *reinterpret_cast<uint32_t *>(ph + 8) = low[0];
+                *reinterpret_cast<uint32_t *>(ph + 8) = low[0];
             }
             proxy_fence();
             __syncwarp();
@@ -993,12 +977,10 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
             wait_terms<NR>(s);
 #pragma unroll
             for (int k = 0; k < NR; ++k) o[k] = fmaf(__uint_as_float(s[NR + k]), 0.0625f, __uint_as_float(s[k]));
-            if constexpr (C::THIRD) {
-                uint32_t z[NR];
-                ld_cols<NR>(tmem + (C::INLINE3 ? 2 * C::COLS + 8 : 3 * C::COLS), z);
+            uint32_t z[NR];
+            ld_cols<NR>(tmem + (C::INLINE3 ? 2 * C::COLS + 8 : 3 * C::COLS), z);
 #pragma unroll
-                for (int k = 0; k < NR; ++k) o[k] = fmaf(__uint_as_float(z[k]), 0x1p-8f, o[k]);
-            }
+            for (int k = 0; k < NR; ++k) o[k] = fmaf(__uint_as_float(z[k]), 0x1p-8f, o[k]);
         } else {
 #pragma unroll
             for (int k = 0; k < NR; ++k) o[k] = 0.f;
@@ -1871,7 +1853,7 @@ __global__ void __launch_bounds__(32 * kPagedMergeWarps) fmha_paged_merge_kernel
 // ---------------------------------------------------------------------------
 
 // Query rows of a unit: 16 or 32 where a sequence's rows of a kv head fit them,
-// else 128.  (16 sequences of 28 rows on 6000 keys: 44.4 us in units of 32, 50.8 of
+// else 128.  (16 sequences of 28 rows on 6000 keys: 48.2 us in units of 32, 50.8 of
 // 128; 4 sequences of 8192 keys and 64 / 80 / 128 rows: 35 / 48 / 56 in units of 64,
 // two groups a pipeline, 30 / 31 / 34 of 128.)
 int paged_rows(int64_t max_q, int G) { return max_q * G <= 16 ? 16 : max_q * G <= 32 ? 32 : kRows; }
