@@ -607,6 +607,15 @@ __device__ __forceinline__ uint32_t take_term(uint32_t (&rest)[2]) {
     return code;
 }
 
+// What is left of them, in e5m2.
+__device__ __forceinline__ uint32_t last_term(const uint32_t (&rest)[2]) {
+    uint32_t code;
+    asm("{\n.reg .b16 a, b;\ncvt.rn.satfinite.e5m2x2.f16x2 a, %1;\ncvt.rn.satfinite.e5m2x2.f16x2 b, %2;\nmov.b32 %0, {a, b};\n}\n"
+        : "=r"(code)
+        : "r"(rest[0]), "r"(rest[1]));
+    return code;
+}
+
 // Rows r0 .. r0 + N - 1 of an item's q as e4m3 terms in shared memory, and what
 // the softmax needs to know of each row; by a warp.
 template <class C, int N>
@@ -1166,9 +1175,10 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 // registers, nothing is exchanged, and a page's scale is one factor for its
 // columns.  Two groups, each an MMA issuer and four softmax warps with K, V, S
 // and O of their own, take every other tile, and their O are added up at the end.
-//   S  = Q_0 K^T + Q_1 K^T (+ Q_2 K^T, f16), the terms passes of their own into the same
-//        accumulator, without a factor of 16, so that elements of q below 2^-9
-//        (f16 2^-6) of their row's largest are off by 2^-17 of it;
+//   S  = Q_0 K^T + Q_1 K^T + Q_2 K^T, the terms passes of their own into the same
+//        accumulator, without factors; the third in e5m2, whose steps go on where e4m3's end, so that
+//        as above elements of q below 2^-13 (f16 2^-10) of their row's largest are off by 2^-21 of it
+//        (bf16 with two terms, f16 with three of e4m3: 2^-17; bf16's pass more takes 4%, 206 -> 215 us for 4 chunks of 512 on 8192 keys);
 //   O += P V with both in f16, which holds every e4m3 number: a weight is off by 2^-11
 //        of itself, or by 2^-25 where the group's largest is 2^7 or more (a reference
 //        serves 16 tiles, so that this is 2^-21 of their weight at most).
@@ -1180,10 +1190,10 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 // S of a half, softmax, P over that S in TMEM, P V, and S of the half two tiles on,
 // while the softmax is at the other half.
 //
-// What bounds it is that chain: of 4 chunks of 512 tokens on 8192 keys (206 us, 903
-// TFLOP/s; f16 215; flops 97 at the bf16 rate) a half takes a group 2500 cycles, of
-// which its softmax computes 1600 and waits 700 for S; the tensor pipe is busy 43%
-// (f16 52%), the ALU 42%, issue slots 54%.  Without one of S's passes it takes 1% less,
+// What bounds it is that chain: of 4 chunks of 512 tokens on 8192 keys (215 us, 867
+// TFLOP/s; flops 97 at the bf16 rate) a half takes a group 2500 cycles, of
+// which its softmax computes 1600 and waits 700 for S; the tensor pipe is busy 52%,
+// the ALU 42%, issue slots 54%.  Without one of S's passes it takes 4% less,
 // without P V 3%, without the conversion 7%.  Weights as e4m3 terms in shared memory took 229 (f16: three,
 // 291), f16 ones there 232; S and P V a whole tile at a time 232; V converted a tile ahead
 // 213; 16 softmax warps, two threads a row, 231; units of 256 rows, a block a
@@ -1191,6 +1201,7 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 // ---------------------------------------------------------------------------
 
 constexpr int kRowsBars = 4096;          // barrier block
+constexpr int kRowsTerms = 3;            // of q
 constexpr int kRowsVs = 2;               // tiles of V as codes, for both groups
 constexpr int kRowsTiles = 16;           // tiles that a reference serves at most
 constexpr float kRowsGrown = 15.f;       // as kGrown: f16 ends at 2^16
@@ -1201,8 +1212,7 @@ constexpr int kRowsThreads = 512;        // two softmax groups and the converter
 template <bool BF_>
 struct RowsCfg {
     static constexpr bool BF = BF_;
-    static constexpr int NT = BF ? 2 : 3;                     // terms of q
-    static constexpr int OFF_VF = NT * kPanelBytes;           // after q's terms, by group: V in f16,
+    static constexpr int OFF_VF = kRowsTerms * kPanelBytes;   // after q's terms, by group: V in f16,
     static constexpr int OFF_K = OFF_VF + 4 * kPanelBytes;    // and K (one tile, free once its S is there)
     static constexpr int OFF_V = OFF_K + 2 * kPanelBytes;     // V as it comes, for both
     static constexpr int OFF_BARS = OFF_V + kRowsVs * kPanelBytes;
@@ -1390,6 +1400,7 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
     const uint32_t s_tm = tmem + x * kRows, o_tm = tmem + 2 * kRows + x * kD;
     constexpr uint32_t kIdS = mma_idesc(0u, kRows / 2, false), kIdP = mma_idesc(0u, kD, true);
+    constexpr uint32_t kIdLast = kIdS | (1u << 7);           // A in e5m2
     const uint64_t q = smem_desc(smem_u32(smem), 16, 1024);
     const uint64_t k = smem_desc(smem_u32(smem + C::OFF_K + x * kPanelBytes), 16, 1024);
     const uint64_t v = smem_desc(smem_u32(smem + C::OFF_VF + 2 * x * kPanelBytes), kPanelBytes, 1024);   // MN-major: LBO = panel stride
@@ -1408,8 +1419,9 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
             if (h == 0 && !wait_all(smem_u32(&bars->k_full[x]), m & 1, abort_flag)) return false;
             tc_fence_after();
 #pragma unroll
-            for (int term = 0; term < C::NT; ++term)     // 32 dims a step: 32 bytes of a row
-                mma4<32, 32>(s_tm + 64 * h, q + ((term * kPanelBytes) >> 4), k + ((h * 64 * 128) >> 4), kIdS, term > 0 ? 1u : 0u);
+            for (int term = 0; term < kRowsTerms; ++term)    // 32 dims a step: 32 bytes of a row
+                mma4<32, 32>(s_tm + 64 * h, q + ((term * kPanelBytes) >> 4), k + ((h * 64 * 128) >> 4),
+                             term + 1 < kRowsTerms ? kIdS : kIdLast, term > 0 ? 1u : 0u);
             tc_commit(smem_u32(&bars->s_full[x][h]));
             return true;
         };
@@ -1463,9 +1475,10 @@ __device__ __forceinline__ float rows_terms(const PagedParams &p, uint8_t *tile,
         uint32_t rest[2] = {pack2<false>(y[0], y[1]), pack2<false>(y[2], y[3])};
         const int row = r0 + k;
 #pragma unroll
-        for (int term = 0; term < C::NT; ++term)
+        for (int term = 0; term < kRowsTerms; ++term)
             *reinterpret_cast<uint32_t *>(tile + term * kPanelBytes + row * 128 +
-                                          ((((lane >> 2) ^ (row & 7)) << 4) | ((lane & 3) << 2))) = take_term(rest);
+                                          ((((lane >> 2) ^ (row & 7)) << 4) | ((lane & 3) << 2))) =
+                term + 1 < kRowsTerms ? take_term(rest) : last_term(rest);
     }
     return g;
 }

@@ -549,8 +549,8 @@ int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_t k_head_st
  * page_size below 2^31, max_pages * page_size at most 2^30.  Data pointers
  * 16-byte aligned, the others 4-byte.  o, lse and the workspace are apart from
  * the inputs and from one another.
- * q and the codes enter the products as they are (elements of q below 2^-9,
- * f16 2^-6, of their row's largest are rounded, by 2^-17 of it at most), scores,
+ * q and the codes enter the products as they are (elements of q below 2^-13,
+ * f16 2^-10, of their row's largest are rounded, by 2^-21 of it at most), scores,
  * sums and O are fp32; a weight is rounded by 2^-10 of itself at most, and
  * below that all of them together by 2^-10 of the row's sum.  A q row that holds an
  * infinity or a NaN gives NaN.  v_scale counts as 2^-60 or 2^60 outside these.

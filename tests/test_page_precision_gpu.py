@@ -91,3 +91,22 @@ def test_small_weights_beside_a_key_without_value(fm, H, H_k, n, dtype):  # noqa
     o, lse, status = tf.run(fm, c)
     assert status == 0
     check(c, o, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [1, 5, 40])
+def test_a_dim_of_q_above_the_others(fm, n, dtype):  # noqa: F811
+    """One element of every row 2^9 times the others, on a dim where all keys are zero: the scores are the others'."""
+    c = tf.make(dtype, 8, 2, 32, [300, 200], [n, n], seed=5, q_scale=0.2)
+    g = torch.Generator().manual_seed(6)
+    c["q"][..., 0] = 180.0
+    c["q"][..., 1] = (0.125 + 0.125 * torch.rand(c["q"].shape[:-1], generator=g)).to(c["q"].dtype)
+    k = c["kc"].view(torch.uint8)                        # keys: dim 1 alone, up to e4m3's largest
+    nan = (k & 0x7F) == 0x7F
+    k.copy_(torch.where(nan, k, 0))
+    top = pu.codes(torch.rand(k.shape[:-1], generator=g).double() * 448)
+    k[..., 1] = torch.where(nan[..., 1], k[..., 1], top)
+    c["ks"].copy_(torch.where(c["ks"].isnan(), c["ks"], 1.0))
+    o, lse, status = tf.run(fm, c)
+    assert status == 0
+    check(c, o, lse)
