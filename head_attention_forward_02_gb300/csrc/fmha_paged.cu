@@ -1190,7 +1190,7 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 // S of a half, softmax, P over that S in TMEM, P V, and S of the half two tiles on,
 // while the softmax is at the other half.
 //
-// What bounds it is that chain: of 4 chunks of 512 tokens on 8192 keys (215 us, 867
+// What bounds it is that chain: of 4 chunks of 512 tokens on 8192 keys (220 us, 847
 // TFLOP/s; flops 97 at the bf16 rate) a half takes a group 2500 cycles, of
 // which its softmax computes 1600 and waits 700 for S; the tensor pipe is busy 52%,
 // the ALU 42%, issue slots 54%.  Without one of S's passes it takes 4% less,
@@ -1414,9 +1414,13 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
         }
         const int tb = it.t0 + x;
         if (tb >= it.t1) tc_commit(smem_u32(&bars->q_empty));   // an item of one tile is group 0's alone
-        // S of half h of tile m, over P of that of tile m - 1; P V of that
+        // S of half h of tile m, over P of that of tile m - 1, so once that P V is done: MMAs into one
+        // accumulator keep their order, of others nothing is promised (without the wait 215 us for 4
+        // chunks of 512, with it 220); P V of tile m - 1
         auto scores = [&](int h) -> bool {
-            if (h == 0 && !wait_all(smem_u32(&bars->k_full[x]), m & 1, abort_flag)) return false;
+            if ((h == 0 && !wait_all(smem_u32(&bars->k_full[x]), m & 1, abort_flag)) ||
+                (m > 0 && !wait_all(smem_u32(&bars->pv_done[x][h]), (m - 1) & 1, abort_flag)))
+                return false;
             tc_fence_after();
 #pragma unroll
             for (int term = 0; term < kRowsTerms; ++term)    // 32 dims a step: 32 bytes of a row
@@ -1438,7 +1442,6 @@ __device__ void rows_mma(uint8_t *smem, RowsBars *bars, uint32_t tmem_any, int x
         for (int t = tb; ok && t < it.t1 + 2 && tb < it.t1; t += 2) {
             const bool more = t < it.t1, before = t > tb;    // a tile here; one before it
             for (int h = 0; ok && h < 2; ++h) {
-                // in this order, which the tensor cores keep: P is where the next S goes
                 ok = !before || values(h, h == 0 && t == tb + 2);
                 ok = ok && (!more || scores(h));
             }

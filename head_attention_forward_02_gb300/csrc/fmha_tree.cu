@@ -364,7 +364,8 @@ __device__ void tree_producer(const TreeParams &p, TreeCursor &cur, int gate, co
 }
 
 // MMA issuer of group x (one warp, one elected lane).  MMAs of one warp
-// execute in issue order, so S of the next tile may overwrite the columns of
+// execute in issue order (promised for those into one accumulator, observed for
+// others), so S of the next tile may overwrite the columns of
 // P once P V is issued: the chain is P V, next S, softmax.  Where both groups
 // work on the same tiles their chains would settle in step, with both softmax
 // passes, then both groups' MMAs, at the same time (4200 cycles a tile against
