@@ -16,7 +16,9 @@
 // further term costs columns of N, not another pass over K or V:
 //   q  = 2^k (q_0 + q_1 / 16), each 4 bits: all 8 bits of a bf16 row's
 //        elements down to 2^-13 of its largest (2^k: a power of two per row); f16
-//        has a third term, added to the second's columns by an MMA of its own;
+//        has a third term, in units of the second: in columns of its own where a unit has
+//        up to 8 rows, else added to the second's by an MMA of the first's shape, which
+//        keeps their order;
 //   P' = p_0 + p_1 / 16 + p_2 / 256, off by 2^-11 of a weight (two terms: 2^-8, and
 //        small weights next to a large one lost from 2^-14 of the terms' unit on).
 // A group of 16 query rows is thus 32 columns, [16 first terms | 16 second], and a
@@ -92,7 +94,9 @@ struct PagedCfg {
     static constexpr int P_TILE = kRows * P_ROW;
     static constexpr int P_BYTES = P_TILE * (INLINE3 ? 1 : 2);
     static constexpr uint64_t P_SWZ = 6;                      // 32-byte swizzle
-    static constexpr int Q_BYTES = (BF ? 32 : 48) * NG * 128; // first and second terms, then f16's third
+    static constexpr bool QPASS = !BF && !INLINE3;            // q's third terms have an MMA of their own
+    static constexpr int Q_ROWS = INLINE3 ? 8 : 16;           // rows of a group that have terms
+    static constexpr int Q_BYTES = (QPASS ? 64 : 32) * NG * 128;   // by group 32 rows, and for that MMA 32 more: 16 of zeros, third terms
     static constexpr int STAGE = 2 * kPanelBytes;             // K and V of 128 keys
     static constexpr int OFF_P = 2 * Q_BYTES;                 // two buffers a pipeline
     static constexpr int OFF_KV = OFF_P + 4 * P_BYTES;
@@ -647,7 +651,7 @@ __device__ __forceinline__ void paged_terms(const PagedParams &p, uint8_t *smem,
 #pragma unroll
         for (int j = 0; j < 2; ++j) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(rest[j]) : "r"(0x4c004c00u));   // by 16
         term(row + 16);
-        if constexpr (!C::BF) term(32 * C::NG + r);    // behind the others' rows, in units of the second
+        if constexpr (!C::BF) term(C::INLINE3 ? row + 8 : 32 * C::NG + row + 16);   // in units of the second
         if (lane == 0) bars->qscale[slot][r] = g;
     }
 }
@@ -663,7 +667,7 @@ __device__ void paged_queries(const PagedParams &p, uint8_t *smem, PagedBars *ba
         const int slot = i & 1;
         if (i == 0) continue;
         if (i >= 2 && !wait_all(smem_u32(&bars->q_empty[slot]), ((i >> 1) - 1) & 1, abort_flag)) break;
-        const int rows = (it.rows + 15) & ~15;
+        const int rows = imin((it.rows + 15) & ~15, C::NG * C::Q_ROWS);
         for (int r0 = 0; r0 < rows; r0 += 8) paged_terms<C, 8>(p, smem, bars, it, slot, r0, lane);
         proxy_fence();
         __syncwarp();
@@ -710,7 +714,7 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
         // this pipeline's group in q's tile
         const int grp = C::SPLIT ? 0 : w;
         const uint64_t q = q0 + ((slot * C::Q_BYTES + grp * 32 * 128) >> 4);
-        const uint64_t q3 = q0 + ((slot * C::Q_BYTES + (32 * C::NG + 16 * grp) * 128) >> 4);
+        const uint64_t q3 = q + ((32 * C::NG * 128) >> 4);
         const int tb = it.t0 + (C::SPLIT ? w : 0);
         uint32_t st_before = 0;
         for (int t = tb; t < it.t1; t += kStep, ++c) {
@@ -731,7 +735,7 @@ __device__ void paged_mma(uint8_t *smem, PagedBars *bars, uint32_t tmem_any, int
             const uint64_t k = k0 + ((st * C::STAGE) >> 4);
             const uint32_t s_tm = tmem + b * C::COLS;
             mma4<32, 32>(s_tm, k, q, paged_idesc(32, false), 0u);      // 32 dims a step: 32 bytes of a row
-            if constexpr (!C::BF) mma4<32, 32>(s_tm + 16, k, q3, paged_idesc(16, false), 1u);
+            if constexpr (C::QPASS) mma4<32, 32>(s_tm, k, q3, paged_idesc(32, false), 1u);
             tc_commit(smem_u32(&bars->s_full[w][b]));
             if (t + kStep >= it.t1) tc_commit(smem_u32(&bars->q_empty[slot]));
             if (t > tb && !issue_pv(m - 1, st_before, t - kStep == tb)) {
@@ -784,7 +788,7 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
         const int tb = it.t0 + (C::SPLIT ? w : 0);
         if (i == 0) {
             constexpr int N = C::R / C::SW;
-            if (warp * N < ((it.rows + 15) & ~15)) paged_terms<C, N>(p, smem, bars, it, slot, warp * N, lane);
+            if (warp * N < ((it.rows + 15) & ~15) && (warp * N & 15) < C::Q_ROWS) paged_terms<C, N>(p, smem, bars, it, slot, warp * N, lane);
             proxy_fence();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&bars->q_full[slot]));
@@ -827,7 +831,13 @@ __device__ void paged_softmax(const PagedParams &p, uint8_t *smem, PagedBars *ba
                 float top = -INFINITY;
                 uint32_t s[2 * NR];
                 ld_terms<NR>(tmem + b * C::COLS, s);
+                uint32_t z[NR];
+                if constexpr (!C::BF && C::INLINE3) ld_cols<NR>(tmem + b * C::COLS + 8, z);
                 wait_terms<NR>(s);
+                if constexpr (!C::BF && C::INLINE3) {
+#pragma unroll
+                    for (int k = 0; k < NR; ++k) s[NR + k] = __float_as_uint(__uint_as_float(s[NR + k]) + __uint_as_float(z[k]));
+                }
                 const float4 *g4 = reinterpret_cast<const float4 *>(&bars->qscale[slot][row0]);
                 const float4 *n4 = reinterpret_cast<const float4 *>(fresh ? bars->zero : &bars->nm[w][row0]);
 #pragma unroll
@@ -1127,6 +1137,13 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
         for (int k = 0; k < 16; ++k) bars->zero[k] = 0.f;
         bars->abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if constexpr (C::QPASS) {            // the zeros beside q's third terms: 2 KB a group and slot
+        for (int i = threadIdx.x; i < 2 * C::NG * 128; i += C::THREADS) {
+            const int slot = i / (C::NG * 128), grp = i / 128 % C::NG;
+            reinterpret_cast<uint4 *>(smem + slot * C::Q_BYTES + (32 * C::NG + 32 * grp) * 128)[i % 128] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        proxy_fence();
     }
     if (warp == C::MMA) {                // pipeline 0's issuer
         tmem_alloc(smem_u32(&bars->tmem_base), C::TMEM_COLS);
