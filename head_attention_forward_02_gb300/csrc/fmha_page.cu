@@ -21,7 +21,7 @@
 // (18.0 as four lists one after the other, a token a job).
 //
 // Write: a run of tokens with consecutive slots in one page (some of them
-// perhaps left out, by a negative slot); for each kv head
+// perhaps left out, by a slot outside the cache); for each kv head
 // and of K and V, a = max |x| over it and
 //   s = max(scale before, 2^e), e the least with a <= 448 * 2^e
 // (a run that begins its page: s = 2^e), rows before the run are rounded again
@@ -315,6 +315,10 @@ __device__ __forceinline__ uint32_t again4(uint32_t c, float f) {
     return pack4_e4m3(a.x * f, a.y * f, b.x * f, b.y * f);
 }
 
+// Is a token with this slot written?  A slot outside the cache is as a negative one: were
+// it the end of a run, two warps would have runs of the same page, in no order.
+__device__ __forceinline__ bool written(const WriteParams &p, int slot) { return (unsigned)slot < (unsigned)p.slots_end; }
+
 // A run: tokens [i, i + n) become rows [off, off + n) of a page.
 struct Run {
     uint8_t *rows;                       // the page's head: its first row
@@ -360,9 +364,9 @@ __device__ __forceinline__ void batch_load(Batch &b, const uint8_t *x, int64_t x
     for (int k = 0; k < kBatchRows / 2; ++k)
         if (j0 + 2 * k + half < end) b.v[k] = *reinterpret_cast<const uint4 *>(x + (j0 + 2 * k + half) * x_t);
 }
-__device__ __forceinline__ void batch_live(Batch &b, const int *slots, int j0, int n) {
+__device__ __forceinline__ void batch_live(Batch &b, const WriteParams &p, const int *slots, int j0, int n) {
     const int lane = threadIdx.x & 31;
-    b.live = __ballot_sync(0xffffffffu, lane < kBatchRows && j0 + lane < n && slots[j0 + lane] >= 0) >> (lane >> 4);
+    b.live = __ballot_sync(0xffffffffu, lane < kBatchRows && j0 + lane < n && written(p, slots[j0 + lane])) >> (lane >> 4);
 }
 template <bool BF>
 __device__ __forceinline__ float batch_max(const Batch &b, float a) {
@@ -381,12 +385,12 @@ __device__ __forceinline__ void batch_store(const Batch &b, const Run &r, int j0
 }
 
 // How far the run that begins at slots[0] = s goes, at most `room` tokens.
-__device__ __forceinline__ int run_length(const int *slots, int s, int room) {
+__device__ __forceinline__ int run_length(const WriteParams &p, const int *slots, int s, int room) {
     const int lane = threadIdx.x & 31;
     int n = 1;
     while (n < room) {
-        const int j = n + lane, at = j < room ? slots[j] : 0;
-        const unsigned stop = __ballot_sync(0xffffffffu, j >= room || (at >= 0 && at != s + j));
+        const int j = n + lane, at = j < room ? slots[j] : -1;
+        const unsigned stop = __ballot_sync(0xffffffffu, j >= room || (written(p, at) && at != s + j));
         n += stop ? __ffs(stop) - 1 : 32;
         if (stop) break;
     }
@@ -402,13 +406,12 @@ __global__ void __launch_bounds__(32 * kWriteWarps, 3) fmha_page_write_kernel(co
     const int i = c0 + lane;
     const bool here = lane < kBatchRows && i < p.N;
     const int slot = here ? p.slots[i] : -1, before = here && i > 0 ? p.slots[i - 1] : -1;
-    const bool inside = slot >= 0 && slot < p.slots_end;
     if (warp == 0 && blockIdx.y == 0 && slot >= p.slots_end) atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
-    bool begins = inside;
+    bool begins = written(p, slot);
     for (int j = 1; begins && j <= min(i, slot & (P - 1)); ++j) {
         const int other = j == 1 ? before : p.slots[i - j];
         if (other == slot - j) begins = false;               // of the same run
-        else if (other >= 0) break;
+        else if (written(p, other)) break;
     }
     unsigned starts = __ballot_sync(0xffffffffu, begins);
     if (starts == 0) return;             // the same in every warp
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(32 * kWriteWarps, 3) fmha_page_write_kernel(co
     // the last run is the only one that can have more than 16 rows, which all warps then share
     const int last = 31 - __clz(starts), s_last = __shfl_sync(0xffffffffu, slot, last);
     const int room_last = min(P - (s_last & (P - 1)), p.N - (c0 + last));
-    const int n_last = room_last > kBatchRows ? run_length(p.slots + c0 + last, s_last, room_last) : 0;
+    const int n_last = room_last > kBatchRows ? run_length(p, p.slots + c0 + last, s_last, room_last) : 0;
     const bool longer = n_last > kBatchRows;
     if (longer) starts &= ~(1u << last);
     const int items = __popc(starts) * pairs;
@@ -438,7 +441,7 @@ __global__ void __launch_bounds__(32 * kWriteWarps, 3) fmha_page_write_kernel(co
         const uint8_t *x = rows_of(pair, t, x_t);
         Batch b;
         batch_load(b, x, x_t, 0, room);
-        batch_live(b, slots, 0, run_length(slots, s, room));
+        batch_live(b, p, slots, 0, run_length(p, slots, s, room));
         float old;
         const float sc = run_scale(r, warp_max(batch_max<BF>(b, 0.f)), old);
         if (r.off > 0 && sc > old) rescale_rows(r, old / sc, lane >> 3, 4);
@@ -459,7 +462,7 @@ __global__ void __launch_bounds__(32 * kWriteWarps, 3) fmha_page_write_kernel(co
         batch_load(b, x, x_t, j0, n_last);
     };
     fetch(warp / team);
-    batch_live(b, p.slots + c0 + last, j0, n_last);
+    batch_live(b, p, p.slots + c0 + last, j0, n_last);
     for (int q0 = 0, buf = 0; q0 < pairs; q0 += abreast, buf ^= 1) {
         const int q = q0 + warp / team;
         const bool on = q < pairs;       // the same in every warp of a team

@@ -515,7 +515,7 @@ int fmha_page_plan(const int *seqlen, const int *n_new, const int *batch_idx, in
  * The slots of a page's tokens are consecutive for consecutive i, as
  * fmha_page_plan gives them, where none is negative in between; such a token's
  * row keeps its codes.  No slot comes twice.  (Otherwise that page's contents
- * are undefined.)  A slot at or past n_pages * P is not written, and
+ * are undefined.)  A slot at or past n_pages * P is as a negative one, and
  * fmha_device_status reports FMHA_ERR_INVALID_ARG.
  * No workspace; one launch.  Returns FMHA_OK, FMHA_ERR_INVALID_ARG,
  * FMHA_ERR_UNSUPPORTED (dtype, alignment, device) or FMHA_ERR_CUDA.  N = 0
