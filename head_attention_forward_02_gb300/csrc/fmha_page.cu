@@ -548,8 +548,10 @@ extern "C" int fmha_page_plan(const int *seqlen, const int *n_new, const int *ba
     p.cap = n_pages;
     p.job = N > 8 * kPlanThreads ? 4 : 1;
     const int smem = 6 * B * (int)sizeof(int);
-    if (smem > 47 * 1024 &&
-        cudaFuncSetAttribute(fmha_page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    // always to the same: the kernel's limit is the process's, and a smaller call must not lower
+    // it between another thread's setting and its launch
+    if (smem > 47 * 1024 && cudaFuncSetAttribute(fmha_page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 6 * kPlanSeqs * (int)sizeof(int)) != cudaSuccess)
         return cuda_failed();
     cudaLaunchConfig_t cfg = {};
     // one CTA where every thread has a few jobs at most
