@@ -29,7 +29,8 @@
 // e4m3(x / s).  Scales are powers of two: e4m3 has the same relative step in
 // every binade, so a finer scale would not make values more exact, and x / s and
 // the old rows' factor are exact, which leaves each value one rounding (a row
-// whose scale grows into e4m3's subnormals: two).
+// whose scale grows into e4m3's subnormals: two).  A page that another program filled may have
+// any scale; then they are rounded once all the same, by way of rounding to odd.
 //
 // Bound by memory: 2 bytes in and 1 out an element.  A CTA takes the runs that
 // begin in 16 tokens, for some heads' K or V, and each of its warps a run of
@@ -293,6 +294,30 @@ __device__ __forceinline__ uint2 codes8(uint4 v, float inv) {
     return make_uint2(pack4_e4m3(x[0].x, x[0].y, x[1].x, x[1].y), pack4_e4m3(x[2].x, x[2].y, x[3].x, x[3].y));
 }
 
+// A scale that this call chooses is a power of two; one that a page had before may be any,
+// and its quotients and products have more bits than 32 hold.  To odd: q, the value
+// rounded to nearest, with its last bit set towards what is left, so that rounding it again, to
+// e4m3, is as rounding the value itself (a tie of q alone is none of the value).
+__device__ __forceinline__ bool power_of_two(float s) { return (__float_as_uint(s) & 0x7fffffu) == 0; }
+__device__ __forceinline__ float to_odd(float q, float left) {
+    const uint32_t u = __float_as_uint(q);
+    if ((u & 1u) != 0 || !(left < 0.f || left > 0.f)) return q;      // exact, infinite, NaN
+    return __uint_as_float((left < 0.f) == (u >> 31 != 0) ? u + 1 : u - 1);
+}
+template <bool BF>
+__device__ __forceinline__ uint2 codes8_over(uint4 v, float s) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = wide2<BF>(w[i]);
+        const float a = x.x / s, b = x.y / s;
+        y[2 * i] = to_odd(a, fmaf(-a, s, x.x));
+        y[2 * i + 1] = to_odd(b, fmaf(-b, s, x.y));
+    }
+    return make_uint2(pack4_e4m3(y[0], y[1], y[2], y[3]), pack4_e4m3(y[4], y[5], y[6], y[7]));
+}
+
 // The least power of two that brings a to 448 = 1.75 * 2^8 or below it, within
 // the bounds.
 __device__ __forceinline__ int scale_exponent(float a) {
@@ -307,12 +332,15 @@ __device__ __forceinline__ float warp_max(float a) {
     return a;
 }
 
-// Four codes times a power of two (or any factor), rounded again.
+// Four codes times a factor, rounded again.
+template <bool ANY>
 __device__ __forceinline__ uint32_t again4(uint32_t c, float f) {
     const __half2 lo = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c & 0xffffu), __NV_E4M3));
     const __half2 hi = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c >> 16), __NV_E4M3));
     const float2 a = __half22float2(lo), b = __half22float2(hi);
-    return pack4_e4m3(a.x * f, a.y * f, b.x * f, b.y * f);
+    if constexpr (!ANY) return pack4_e4m3(a.x * f, a.y * f, b.x * f, b.y * f);
+    auto times = [&](float x) { return to_odd(x * f, fmaf(x, f, -(x * f))); };
+    return pack4_e4m3(times(a.x), times(a.y), times(b.x), times(b.y));
 }
 
 // Is a token with this slot written?  A slot outside the cache is as a negative one: were
@@ -340,6 +368,14 @@ __device__ __forceinline__ float run_scale(const Run &r, float a, float &old) {
 // Rows [first, off) of the page by `step` groups of eight lanes, each a row at a time, four in flight.
 __device__ __forceinline__ void rescale_rows(const Run &r, float f, int first, int step) {
     uint4 *rows = reinterpret_cast<uint4 *>(r.rows) + (threadIdx.x & 7);
+    if (!power_of_two(f)) {
+#pragma unroll 1
+        for (int j = first; j < r.off; j += step) {
+            const uint4 v = rows[j * 8];
+            rows[j * 8] = make_uint4(again4<true>(v.x, f), again4<true>(v.y, f), again4<true>(v.z, f), again4<true>(v.w, f));
+        }
+        return;
+    }
     for (int j = first; j < r.off; j += 4 * step) {
         uint4 v[4];
 #pragma unroll
@@ -348,7 +384,7 @@ __device__ __forceinline__ void rescale_rows(const Run &r, float f, int first, i
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (j + k * step < r.off)
-                rows[(j + k * step) * 8] = make_uint4(again4(v[k].x, f), again4(v[k].y, f), again4(v[k].z, f), again4(v[k].w, f));
+                rows[(j + k * step) * 8] = make_uint4(again4<false>(v[k].x, f), again4<false>(v[k].y, f), again4<false>(v[k].z, f), again4<false>(v[k].w, f));
     }
 }
 
@@ -382,6 +418,17 @@ __device__ __forceinline__ void batch_store(const Batch &b, const Run &r, int j0
 #pragma unroll
     for (int k = 0; k < kBatchRows / 2; ++k)
         if (b.live >> (2 * k) & 1) *reinterpret_cast<uint2 *>(dst + 2 * k * 128) = codes8<BF>(b.v[k], inv);
+}
+// The same over a scale that is no power of two: the rows are read again, so that the
+// usual path keeps its registers.
+template <bool BF>
+__device__ __forceinline__ void batch_store_over(const uint8_t *x, int64_t x_t, unsigned live, const Run &r, int j0, float s) {
+    const int half = (threadIdx.x >> 4) & 1;
+    uint8_t *dst = r.rows + (r.off + j0 + half) * 128 + (threadIdx.x & 15) * 8;
+#pragma unroll 1
+    for (int k = 0; k < kBatchRows / 2; ++k)
+        if (live >> (2 * k) & 1)
+            *reinterpret_cast<uint2 *>(dst + 2 * k * 128) = codes8_over<BF>(*reinterpret_cast<const uint4 *>(x + (j0 + 2 * k + half) * x_t), s);
 }
 
 // How far the run that begins at slots[0] = s goes, at most `room` tokens.
@@ -445,7 +492,8 @@ __global__ void __launch_bounds__(32 * kWriteWarps, 3) fmha_page_write_kernel(co
         float old;
         const float sc = run_scale(r, warp_max(batch_max<BF>(b, 0.f)), old);
         if (r.off > 0 && sc > old) rescale_rows(r, old / sc, lane >> 3, 4);
-        batch_store<BF>(b, r, 0, 1.f / sc);
+        if (power_of_two(sc)) batch_store<BF>(b, r, 0, 1.f / sc);
+        else batch_store_over<BF>(x, x_t, b.live, r, 0, sc);
         __syncwarp();
         if (lane == 0) *r.scale = sc;
     }
@@ -474,7 +522,13 @@ __global__ void __launch_bounds__(32 * kWriteWarps, 3) fmha_page_write_kernel(co
         const float sc = run_scale(r, a, old);
         if (on) {
             if (r.off > 0 && sc > old) rescale_rows(r, old / sc, sub * 4 + (lane >> 3), 4 * team);
-            batch_store<BF>(b, r, j0, 1.f / sc);
+            if (power_of_two(sc)) {
+                batch_store<BF>(b, r, j0, 1.f / sc);
+            } else {
+                int64_t x_t;
+                const uint8_t *x = rows_of(pair0 + q, last, x_t);
+                batch_store_over<BF>(x, x_t, b.live, r, j0, sc);
+            }
         }
         fetch(q + abreast);
         __syncthreads();                 // all have read the scale
