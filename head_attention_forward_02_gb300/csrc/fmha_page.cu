@@ -639,10 +639,11 @@ extern "C" int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_
         return FMHA_ERR_UNSUPPORTED;
     for (const void *ptr : {(const void *)k_new.data, (const void *)v_new.data, (const void *)k_pages, (const void *)v_pages})
         if (misaligned(ptr, 16)) return FMHA_ERR_UNSUPPORTED;
-    for (int64_t s : {k_token_stride, k_head_stride, v_token_stride, v_head_stride}) {
+    for (int64_t s : {k_token_stride, k_head_stride, v_token_stride, v_head_stride})
         if (s < 0 || s > (int64_t(1) << 40)) return FMHA_ERR_INVALID_ARG;
-        if (s % 8 != 0) return FMHA_ERR_UNSUPPORTED;
-    }
+    // strides that are never stepped along do not count
+    if ((N > 1 && (k_token_stride % 8 != 0 || v_token_stride % 8 != 0)) || (H_k > 1 && (k_head_stride % 8 != 0 || v_head_stride % 8 != 0)))
+        return FMHA_ERR_UNSUPPORTED;
     if (misaligned(slots, 4) || misaligned(k_scale, 4) || misaligned(v_scale, 4)) return FMHA_ERR_INVALID_ARG;
     const size_t pages = ((size_t)n_pages * H_k << shift) * kD, scales = (size_t)n_pages * H_k * sizeof(float);
     const auto span = [&](int64_t t, int64_t h) { return (size_t)((N - 1) * t + (H_k - 1) * h + kD) * 2; };

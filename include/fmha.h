@@ -508,8 +508,8 @@ int fmha_page_plan(const int *seqlen, const int *n_new, const int *batch_idx, in
  * counts as more than the range of scales holds and is written as 448.
  *
  * Layouts: k_new, v_new FMHA_F16 or FMHA_BF16 [N, H_k, 128] with strides, in
- * elements, of tokens and heads (multiples of 8; pieces of a projection's
- * rows need no copy); slots int32 [N]; the cache as above.  D must be 128.
+ * elements, of tokens and heads (multiples of 8 where there are two; pieces of
+ * a projection's rows need no copy); slots int32 [N]; the cache as above.  D must be 128.
  * Data pointers 16-byte aligned (scales and slots 4-byte).  The cache's arrays
  * are apart from the others and from one another.
  * The slots of a page's tokens are consecutive for consecutive i, as

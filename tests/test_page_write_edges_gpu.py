@@ -155,3 +155,21 @@ def test_rows_before_under_a_scale_that_was_no_power_of_two(fm, P, n):  # noqa: 
         f = Fraction(old[p, 0].item()) / Fraction(s[p, 0].item())
         again = torch.tensor([nearest(Fraction(LEVELS[v]) * f) for v in range(127)], dtype=torch.uint8)
         assert torch.equal(got[p], again[c[p, 0, :off].long()]), f"page {p}"
+
+
+@pytest.mark.gpu
+def test_strides_that_are_never_stepped_along(fm):  # noqa: F811
+    """One token, or one head: its stride may be anything."""
+    x = cu.draw(torch.Generator().manual_seed(8), (4096,), "bf16")
+    one_token, one_head = x.as_strided((1, 3, 128), (1001, 136, 1)), x.as_strided((5, 1, 128), (264, 77, 1))
+    for k, slots in ((one_token, [3]), (one_head, [16, 17, 18, 30, 31])):
+        dev = x.cuda().as_strided(k.shape, k.stride())   # cuda() of the view itself would be packed
+        c, s = pu.draw_pages(torch.Generator().manual_seed(9), 2, k.shape[1], 16)
+        kc, vc, ks, vs = c.cuda(), c.cuda(), s.cuda(), s.cuda()
+        fm.page_write(dev, dev, torch.tensor(slots, dtype=torch.int32, device="cuda"), kc, vc, ks, vs)
+        torch.cuda.synchronize()
+        assert fm.device_status(reset=True) == 0
+        c = c.view(torch.uint8)
+        pu.write(k, slots, c, s)
+        for got, scale in ((kc, ks), (vc, vs)):
+            assert torch.equal(got.cpu().view(torch.uint8), c) and torch.equal(scale.cpu(), s)
