@@ -234,8 +234,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fmha_page_plan_kernel(const P
             const int k = (int)y, b = last_at_most(s_need, p.B, k);
             row(b)[((s_len[b] + mask) >> p.shift) + k - s_need[b]] = page_taken(k);
         } else if (y < (long long)taken + given) {
-            const int j = (int)(y - taken);
-            p.free_list[spare + j] = page_given(j);
+            const int j = (int)(y - taken), page = page_given(j);
+            if (page < 0 || page >= p.cap) atomicCAS(&g_status, FMHA_OK, FMHA_ERR_INVALID_ARG);
+            p.free_list[spare + j] = page;
         } else {
             const int b = (int)(y - taken - given);
             p.cu_new[b] = s_cu[b];

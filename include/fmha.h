@@ -481,7 +481,8 @@ int fmha_cache_evict(fmha_tensor k_cache, fmha_tensor v_cache, const float *acc,
  * that (else the sequence gets no pages); -L <= n; the sum of n > 0 at most N
  * (rows from N on are dropped, and cu_new ends at N); batch_idx in [0, B_table)
  * and no two alike; 0 <= n_free, and with the pages given back at most n_pages;
- * pages in [0, n_pages) (else the slot is -1).  A kernel that meets a violation
+ * pages in [0, n_pages) (else the slot is -1; one that is given back goes onto
+ * the stack as it is).  A kernel that meets a violation
  * clamps, and fmha_device_status then reports FMHA_ERR_INVALID_ARG (not for
  * two equal batch_idx, whose results are undefined).
  * No workspace; one launch, asynchronous on `stream`.  Returns FMHA_OK,
