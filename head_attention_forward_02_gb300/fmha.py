@@ -675,7 +675,8 @@ def page_plan(seqlen: torch.Tensor, n_new: torch.Tensor, table: torch.Tensor, fr
     free_list int32 [n_pages], both changed in place; n_free int32 [1], changed
     in place unless ``n_free_out`` is given.  The step's tensors have
     ``max_tokens`` rows (or as many as ``slots``).  Returns (slots, positions,
-    cu_new [B + 1], new_seqlen [B]), all int32; ``new_seqlen`` may be seqlen."""
+    cu_new [B + 1], new_seqlen [B]), all int32; ``new_seqlen`` may be seqlen.
+    Without sequences (an idle step) every row is told that it has none."""
     index = n_free.get_device()
     if index < 0:
         raise ValueError(f"the tensors are on {n_free.device}, not on a CUDA device")
@@ -711,6 +712,13 @@ def page_plan(seqlen: torch.Tensor, n_new: torch.Tensor, table: torch.Tensor, fr
         _check(index, i32, (1,), n_free=n_free, n_free_out=n_free_out)
         _check(index, i32, table.shape, table=table)
         _check(index, i32, free_list.shape, free_list=free_list)
+    if B == 0:                              # the C function has nothing to do, or refuses rows without sequences
+        cu_new.zero_()
+        slots.fill_(-1)
+        positions.fill_(-1)
+        if n_free_out is not n_free:
+            n_free_out.copy_(n_free)
+        return slots, positions, cu_new, new_seqlen
     _raise(lib().fmha_page_plan(
         seqlen.data_ptr(), n_new.data_ptr(), _ptr(batch_idx), table.data_ptr(), free_list.data_ptr(), n_free.data_ptr(),
         n_free_out.data_ptr(), slots.data_ptr(), positions.data_ptr(), cu_new.data_ptr(), new_seqlen.data_ptr(), B, N,

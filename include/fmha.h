@@ -486,8 +486,9 @@ int fmha_cache_evict(fmha_tensor k_cache, fmha_tensor v_cache, const float *acc,
  * clamps, and fmha_device_status then reports FMHA_ERR_INVALID_ARG (not for
  * two equal batch_idx, whose results are undefined).
  * No workspace; one launch, asynchronous on `stream`.  Returns FMHA_OK,
- * FMHA_ERR_INVALID_ARG, FMHA_ERR_UNSUPPORTED or FMHA_ERR_CUDA.  B = 0 and
- * N = 0 succeed without a launch.
+ * FMHA_ERR_INVALID_ARG, FMHA_ERR_UNSUPPORTED or FMHA_ERR_CUDA.  B = 0 needs
+ * N = 0, and succeeds without a launch: no output is written then, cu_new[0]
+ * and n_free_out neither.  N = 0 with B > 0 (drops alone) is a call as any.
  */
 int fmha_page_plan(const int *seqlen, const int *n_new, const int *batch_idx, int *table, int *free_list,
                    const int *n_free, int *n_free_out, int *slots, int *positions, int *cu_new, int *new_seqlen,

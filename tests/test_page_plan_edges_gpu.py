@@ -18,3 +18,22 @@ def test_a_page_outside_the_cache_that_is_given_back_is_reported(fm, page, n_new
     fm.page_plan(**a, **kw)
     torch.cuda.synchronize()
     assert fm.device_status(reset=True) == fm.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("rows", [0, 5])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_a_step_without_sequences(fm, rows, in_place):  # noqa: F811
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    kept = tp.KEPT
+    given = dict(slots=i32([kept] * rows), positions=i32([kept] * rows), cu_new=i32([kept]), new_seqlen=i32([]))
+    table, free, n_free, n_free_out = i32([[3, 1]]), i32([0, 2]), i32([2]), i32([kept])
+    got = fm.page_plan(i32([]), i32([]), table, free, n_free, page_size=16, **given, **({} if in_place else dict(n_free_out=n_free_out)))
+    fresh = fm.page_plan(i32([]), i32([]), table, free, n_free, page_size=16, max_tokens=rows)
+    for out in (got, fresh):
+        assert [x.tolist() for x in out] == [[-1] * rows, [-1] * rows, [0], []]
+    assert n_free.tolist() == [2] and n_free_out.tolist() == [kept if in_place else 2]
+    assert table.tolist() == [[3, 1]] and free.tolist() == [0, 2] and fm.device_status(reset=True) == 0
+
+
+def test_a_step_of_drops_alone(fm):  # noqa: F811
+    tp.run_and_check(fm, tp.make([40, 20], [-9, -20], 16, 1, rows=0))
