@@ -457,7 +457,12 @@ int fmha_cache_evict(fmha_tensor k_cache, fmha_tensor v_cache, const float *acc,
  *   n < 0: its last -n tokens are dropped (n = -L: it has ended; n = -3: three
  *          drafts were not accepted).  The pages that become empty go onto the
  *          stack of free pages, free_list[0 .. n_free - 1], in the order of
- *          the sequences and of their pages.
+ *          the sequences and of their pages.  They must have one owner: a page
+ *          that another sequence's row lists too (a common prefix) would be
+ *          handed out while that one still reads it, and twice once both have
+ *          dropped it.  The kernel cannot see that.  So of sequences that share
+ *          their first pages (full ones, which none of them writes) all but the last
+ *          drop only the tokens behind these, and their length is then the caller's to set.
  *   n >= 0: its n new tokens need ceil((L + n) / P) - ceil(L / P) pages.  After
  *          all drops, they are taken from the stack's top, the sequences in
  *          order; a sequence for which what is left does not suffice gets none,
@@ -546,7 +551,7 @@ int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_t k_head_st
  * Layouts (contiguous): q, o [N, H, 128], FMHA_F16 or FMHA_BF16; the cache as
  * above; table int32 [B_table, max_pages]; seqlen, batch_idx int32 [B]; cu_q
  * int32 [B + 1], ascending; lse float [N, H] or NULL.  batch_idx may be NULL,
- * and sequences may share a table row or pages.  max_q: the most rows that a
+ * and sequences may share a table row or pages (giving them back: fmha_page_plan).  max_q: the most rows that a
  * sequence has.  D must be 128, H / H_k at most 128, N * H and n_pages *
  * page_size below 2^31, max_pages * page_size at most 2^30.  Data pointers
  * 16-byte aligned, the others 4-byte.  o, lse and the workspace are apart from

@@ -37,3 +37,17 @@ def test_a_step_without_sequences(fm, rows, in_place):  # noqa: F811
 
 def test_a_step_of_drops_alone(fm):  # noqa: F811
     tp.run_and_check(fm, tp.make([40, 20], [-9, -20], 16, 1, rows=0))
+
+
+def test_sequences_that_share_their_first_pages(fm):  # noqa: F811
+    """The first to end drops what lies behind them, the last all: every page comes back once."""
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    table, free, n_free = i32([[4, 2, 5, 0], [4, 2, 1, -1]]), i32([3] + [-1] * 5), i32([1])
+    seqlen = i32([60, 40])
+    step = lambda n: fm.page_plan(seqlen, i32(n), table, free, n_free, page_size=16, max_tokens=4, new_seqlen=seqlen)
+    step([-28, 1])                                       # 32 tokens in the shared pages
+    assert seqlen.tolist() == [32, 41] and n_free.tolist() == [3] and free[:3].tolist() == [3, 5, 0]
+    seqlen[0] = 0                                        # it has ended: the pages are the other's alone
+    step([0, -41])
+    assert seqlen.tolist() == [0, 0] and n_free.tolist() == [6] and sorted(free.tolist()) == list(range(6))
+    assert fm.device_status(reset=True) == 0
