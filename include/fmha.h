@@ -466,9 +466,14 @@ int fmha_cache_evict(fmha_tensor k_cache, fmha_tensor v_cache, const float *acc,
  *   n >= 0: its n new tokens need ceil((L + n) / P) - ceil(L / P) pages.  After
  *          all drops, they are taken from the stack's top, the sequences in
  *          order; a sequence for which what is left does not suffice gets none,
- *          and so do those after it that need any.
+ *          and so do those after it that need any.  Such a sequence waits: its rows
+ *          of this step mean nothing.  fmha_page_write leaves them out (slot -1);
+ *          fmha_page_fwd with this cu_new computes them all the same, on other
+ *          keys than theirs, so a caller with long chunks plans again without it.
  * Outputs
- *   table, free_list   in place; entries behind what is in use stay as they were
+ *   table, free_list   in place; entries behind what is in use stay as they were,
+ *                      in free_list those behind the most pages that the stack held
+ *                      during the call
  *   n_free_out         free pages now (n_free itself, or another)
  *   new_seqlen [B]     L + n, or L where the pages did not suffice (seqlen
  *                      itself, or another)
