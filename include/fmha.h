@@ -563,8 +563,9 @@ int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_t k_head_st
  * the inputs and from one another.
  * q and the codes enter the products as they are (elements of q below 2^-13,
  * f16 2^-10, of their row's largest are rounded, by 2^-21 of it at most), scores,
- * sums and O are fp32; a weight is rounded by 2^-10 of itself at most, and
- * below that all of them together by 2^-10 of the row's sum.  A q row that holds an
+ * sums and O are fp32.  A weight, times its page's v_scale, is rounded by 2^-10 of
+ * itself at most, and below that all of them together by 2^-10 of the row's
+ * sum of these products; LSE is of unrounded weights.  A q row that holds an
  * infinity or a NaN gives NaN.  v_scale counts as 2^-60 or 2^60 outside these.
  * Requirements the host cannot check: 0 <= seqlen[b] <= max_pages * page_size,
  * 0 <= batch_idx[b] < B_table, cu_q ascending within [0, N] and in steps of
