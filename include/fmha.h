@@ -606,7 +606,8 @@ enum fmha_rope_layout {
  * with a, b by `layout`; transpose != 0: by the opposite angle, which makes
  * the gradient of x from that of y.  The other D - rot elements are copied.
  * Computed in fp32 from angles that are exact to 2^-24 of a turn at any
- * position, and rounded once.  Longer contexts are the caller's choice of
+ * position (for |inv_freq| up to 2^11; f times above, f times further off), and
+ * rounded once.  Longer contexts are the caller's choice of
  * inv_freq and magnitude.
  *
  * Layouts: q, q_out [B, S, H, D] and k, k_out [B, S, H_k, D], D contiguous, with
