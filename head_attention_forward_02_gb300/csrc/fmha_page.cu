@@ -16,8 +16,9 @@
 // where there are many) are one list of jobs that the threads share out; a job finds its sequence by
 // bisection.  What a token's slot needs of pages taken by this call comes from
 // the stack, not from the table that other threads write, so there is nothing
-// else to wait for.  Bound by latency (a launch, two dependent reads, a scan, a
-// bisection): 64 sequences of a token each 6.8 us, 700 sequences with 30000 tokens 15.2
+// else to wait for.  Bound by latency: 64 sequences of a token each 6.6 us, a launch, two
+// dependent reads, a scan, a bisection; 700 sequences with 45000 tokens 15.1, where 24500 jobs on
+// 8192 threads are three turns of a bisection, for new pages a second one, and a dependent read
 // (18.0 as four lists one after the other, a token a job).
 //
 // Write: a run of tokens with consecutive slots in one page (some of them
@@ -38,9 +39,10 @@
 // loads of their slots, and in registers between the maximum and the rounding.
 // A longer run (of pages of 32 and more) is spread over two to eight warps, 16
 // rows each, the next head's rows fetched under the rounding of this one's.
-// 16600 tokens of 8 heads: 21.6 us in pages of 16 tokens, 4.7 TB/s, 70% of the copy
-// rate, 22.5 / 25.0 / 28.9 in pages of 32 / 64 / 128; 64 single tokens 4.8 us, a launch
-// and two dependent reads.
+// 16600 tokens of 8 heads: 21.4 us in pages of 16 tokens, 4.8 TB/s, 70% of the copy
+// rate, 22.6 / 24.8 / 28.7 in pages of 32 / 64 / 128 (a long run's pairs follow one another in a
+// CTA, with two barriers each, and in pages of 128 the 540 CTAs that have one are 1.2 waves of
+// 456); 64 single tokens 4.6 us, a launch and two dependent reads.
 #include <cooperative_groups.h>
 
 #include "fmha_cache.cuh"
@@ -609,7 +611,10 @@ extern "C" int fmha_page_plan(const int *seqlen, const int *n_new, const int *ba
                                                  6 * kPlanSeqs * (int)sizeof(int)) != cudaSuccess)
         return cuda_failed();
     cudaLaunchConfig_t cfg = {};
-    // one CTA where every thread has a few jobs at most
+    // One CTA where every thread has a few jobs at most, of those that the host can count: 64 sequences of a
+    // token 6.7 us with one and 6.8 with eight, with 8000 tokens more 18.6 and 8.1.  A cluster would be
+    // faster from some 300 jobs on (300 single tokens 10.4 and 8.6), and where many pages come back (200
+    // sequences, of which 100 end with up to 512 pages each: 25 and 9.8).
     const int ranks = N > 4 * kPlanThreads || B > kPlanThreads ? 8 : 1;
     cfg.gridDim = dim3(ranks);
     cfg.blockDim = dim3(kPlanThreads);
@@ -670,7 +675,11 @@ extern "C" int fmha_page_write(fmha_tensor k_new, int64_t k_token_stride, int64_
     p.shift = shift;
     p.slots_end = n_pages << shift;
     // Few tokens: as many CTAs as there are (head, K or V) pairs for every 16 of
-    // them.  Many: a CTA's warps share out the pairs, or a long run's rows.
+    // them (64 single tokens of 8 heads: 4.7 us, two pairs a CTA 7.5, eight 24).  Many: a CTA's
+    // warps share out the pairs, or a long run's rows (16600 tokens, 1 / 2 / 4 / 8 pairs: in pages
+    // of 16 67 / 40 / 25.1 / 21.0, of 64 48 / 29.0 / 24.7 / 26.5, of 128 41 / 30.4 / 28.6 / 29.4).
+    // Between the two the rule is not always the best: 1600 tokens 5.1 with its two pairs, in
+    // pages of 16 3.6 with four; 3200 in pages of 128 13.3 with its four, 9.5 with two.
     const int64_t chunks = ((int64_t)N + kBatchRows - 1) / kBatchRows;
     p.pairs = chunks >= 2 * 152 ? (shift >= 6 ? 4 : 8) : chunks >= 152 ? 4 : chunks >= 76 ? 2 : 1;
     const dim3 grid((unsigned)chunks, (2 * H_k + p.pairs - 1) / p.pairs);

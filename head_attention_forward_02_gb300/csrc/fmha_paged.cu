@@ -49,9 +49,9 @@
 // thread is a key, and for O^T a dim.
 //
 // Bound by HBM where there are few rows.  64 sequences of 2100 to 8192 keys, 32/8
-// heads, bf16: 110 us, 6.2 TB/s, 91% of the copy rate (one pipeline, and scales
+// heads, bf16: 108 us, 6.3 TB/s, 92% of the copy rate (one pipeline, and scales
 // loaded by the softmax threads: 149); 8 of 8200 to 32768 in pages of 16, 64/8 heads,
-// f16: 75 us, 71%; one sequence of 1000: 10.7 us, all latency: 2.5 to the first
+// f16: 74 us, 72%; one sequence of 1000: 10.7 us, all latency: 2.5 to the first
 // item, 5 to the first S, 7.5 to the last O, the rest the join.  16 sequences of 1500
 // to 6000 with 7 tokens: 48 us where the bytes take 19 (weights as two terms: 45): a tile's chain of S, vote,
 // weights and P V takes 1.1 us where its bytes take 0.73.
@@ -1195,7 +1195,8 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 //   S  = Q_0 K^T + Q_1 K^T + Q_2 K^T, the terms passes of their own into the same
 //        accumulator, without factors; the third in e5m2, whose steps go on where e4m3's end, so that
 //        as above elements of q below 2^-13 (f16 2^-10) of their row's largest are off by 2^-21 of it
-//        (bf16 with two terms, f16 with three of e4m3: 2^-17; bf16's pass more takes 4%, 206 -> 215 us for 4 chunks of 512 on 8192 keys);
+//        (bf16 with two terms, f16 with three of e4m3: 2^-17; bf16's pass more takes 4%,
+//        206 -> 215 us for 4 chunks of 512 on 8192 keys);
 //   O += P V with both in f16, which holds every e4m3 number: a weight is off by 2^-11
 //        of itself, or by 2^-25 where the group's largest is 2^7 or more (a reference
 //        serves 16 tiles, so that this is 2^-21 of their weight at most).
@@ -1208,10 +1209,11 @@ __global__ void __launch_bounds__((PagedCfg<BF, NG, NR>::THREADS), 1)
 // while the softmax is at the other half.
 //
 // What bounds it is that chain: of 4 chunks of 512 tokens on 8192 keys (220 us, 847
-// TFLOP/s; flops 97 at the bf16 rate) a half takes a group 2500 cycles, of
-// which its softmax computes 1600 and waits 700 for S; the tensor pipe is busy 52%,
-// the ALU 42%, issue slots 54%.  Without one of S's passes it takes 4% less,
-// without P V 3%, without the conversion 7%.  Weights as e4m3 terms in shared memory took 229 (f16: three,
+// TFLOP/s; flops 97 at the bf16 rate) a half takes a group 2700 cycles, of
+// which its softmax computes 1600 and waits 900 for S; the tensor pipe is busy 50%,
+// the ALU 40%, issue slots 51%.  Without one of S's passes it takes 4% less, without the
+// wait for P V 2%.  With two passes and no such wait (206): without P V 3% less, without
+// the conversion 7%; weights as e4m3 terms in shared memory took 229 (f16: three,
 // 291), f16 ones there 232; S and P V a whole tile at a time 232; V converted a tile ahead
 // 213; 16 softmax warps, two threads a row, 231; units of 256 rows, a block a
 // group, 3% more.
@@ -1886,9 +1888,9 @@ __global__ void __launch_bounds__(32 * kPagedMergeWarps) fmha_paged_merge_kernel
 // ---------------------------------------------------------------------------
 
 // Query rows of a unit: 16 or 32 where a sequence's rows of a kv head fit them,
-// else 128.  (16 sequences of 28 rows on 6000 keys: 48.2 us in units of 32, 50.8 of
+// else 128.  (16 sequences of 28 rows on 1500 to 6000 keys: 46 us in units of 32, 55 of
 // 128; 4 sequences of 8192 keys and 64 / 80 / 128 rows: 35 / 48 / 56 in units of 64,
-// two groups a pipeline, 30 / 31 / 34 of 128.)
+// two groups a pipeline, 35 / 36 / 40 of 128.)
 int paged_rows(int64_t max_q, int G) { return max_q * G <= 16 ? 16 : max_q * G <= 32 ? 32 : kRows; }
 
 using PagedKernel = void (*)(CUtensorMap, CUtensorMap, PagedParams);

@@ -18,8 +18,10 @@
 // rot / 2 sines and cosines serve all its heads, so a CTA takes TOK tokens with
 // all heads and computes them once, under the loads of its elements, which
 // are all issued first.  4 x 4096 tokens of 32 + 8 heads of 128: 52 us, 6.4 TB/s, 95%
-// of the copy rate; the gradient of 8 x 2047 tokens of 16 + 16 heads of 64, half of each
-// turned, 26 us, 76%; 32 single tokens 2.8 us, a launch.
+// of the copy rate, to e4m3 46 us, 81%; the gradient of 8 x 2047 tokens of 16 + 16 heads of 64, half of each
+// turned, 26 us, 76%; 32 single tokens 2.7 us, a launch.  Heads that cannot be read 16 bytes at a
+// time are read element by element: 4 x 4096 tokens of 40 heads of 96, 24 of which are turned, 269 us
+// where the bytes take 37 (32 turned: 52).
 #include "fmha_cache.cuh"
 
 namespace fmha {
@@ -382,7 +384,9 @@ extern "C" int fmha_rope(fmha_tensor q, int64_t q_b, int64_t q_t, int64_t q_h, f
     const dim3 block(p.chunks, p.chunks >= kRopeThreads ? 1 : kRopeThreads / p.chunks);
     // Many tokens: as many a CTA as its threads take in one batch of loads (a CTA
     // of 4 tokens of 32 heads of 64, 16 bytes a thread and item, 4 items, took 27.9 us
-    // for 16376 tokens).  Few: a CTA each.
+    // for 16376 tokens; 16384 of 40 heads of 128, 4 a CTA by this rule, 52 us, one a CTA 71).  Few: a CTA
+    // each (32 tokens 2.7 us, two a CTA 3.0, eight 6.3), which from some 500 on is not the best any
+    // more (1024 tokens 6.6 us, two a CTA 5.7, four 5.1).
     const int fill = rope_batch(half) * (int)block.y / p.heads;
     p.tok = p.tokens < 4 * 4 * 152 || p.heads > 512 ? 1 : fill < 1 ? 1 : fill > kRopeTok ? kRopeTok : fill;
     p.magic = p.heads > 1 ? (uint32_t)(((uint64_t(1) << 32) + p.heads - 1) / p.heads) : 0;
